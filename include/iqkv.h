@@ -393,6 +393,178 @@ int iq_debug_inject(int flags, unsigned spin_limit, unsigned long long combine_w
  */
 int iq_read_status(void* workspace, iq_stream_t stream, int* device_status);
 
+/* ------------------------------------------------------------------------
+ * The paged 8-bit cache: a pool of pages of IQ_PAGE tokens, codes in e4m3
+ * with one power-of-two scale per (page, kv head), keys and values apart, and
+ * one row of page ids per slot (sequence).  Library services: the source pages
+ * have no counterpart.  Next to iq_cache it holds 8 bits per element without a
+ * rotation (a floating code's error is relative to its own element, so
+ * spreading outliers over neighbouring dims gains nothing), shares pages
+ * between forked sequences, and serves sequences of very different lengths
+ * from one pool.
+ *
+ * Values held.  For the rows an append adds to a page, e_new is the least e in
+ * [-40, 60] with max|x| <= 448 * 2^e (-40 for all-zero rows).  The page's
+ * exponent becomes e_new when the page held no row before, else
+ * max(e_old, e_new); rows already there are then rescaled, code * 2^(e_old - e)
+ * rounded to e4m3 again (exact unless it falls below e4m3's normal range).
+ * code = e4m3(x * 2^-e), to nearest even, saturating at 448; the value held is
+ * code * 2^e, exact in bfloat16.  A trim keeps the exponent of the page that
+ * it cuts.  Codes are always finite: a NaN is held as 0, an infinity as the
+ * largest value, and both, like any |x| above 448 * 2^60, set status bit
+ * IQ_STATUS_RANGE.
+ *
+ * Bookkeeping is the host's: lens, table_host and refs are the authoritative
+ * lengths, page ids and page holder counts; kernels get lengths by value and
+ * page ids from the device copy of the table.  A captured call therefore
+ * replays with the lengths that it was captured with.  The host arrays change
+ * when a call returns, so a page that a call releases may be handed out by the
+ * next one: order a cache's calls on one stream, or by events.
+ */
+#define IQ_PAGE 64
+#define IQ_STATUS_RANGE 0x40000   /* an appended value was not finite or above 448 * 2^60 */
+#define IQ_STATUS_BAD_PAGE 0x80000 /* the device table held an id outside the pool (page 0 was read) */
+
+/*
+ * iq_paged — descriptor of one paged cache.  The caller owns every pointer.
+ *   k_codes, v_codes    device e4m3 [pages][kv_heads][IQ_PAGE][head_dim]
+ *   k_scales, v_scales  device float32 [pages][kv_heads], powers of two
+ *   table       device int32 [slots][max_pages]: page ids, position t of a
+ *               slot in its page t / IQ_PAGE
+ *   status      device, IQ_WORKSPACE_HEAD_BYTES, zero at first: the status
+ *               word of this cache's kernels (iq_read_status takes it)
+ *   lens        HOST int32 [slots]; table_host: HOST int32 [slots][max_pages];
+ *   refs        HOST int32 [pages]: how many slots hold a page (0: free)
+ *   free_pages  how many pages are free; first_free: no free page is below it
+ * Device buffers must be 16-byte aligned.  A page that several slots hold is
+ * never written: an append into one first takes a page of its own.
+ */
+typedef struct {
+  int32_t slots, kv_heads, head_dim, pages, max_pages, free_pages, first_free, reserved;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t* table;
+  uint32_t* status;
+  int32_t* lens;
+  int32_t* table_host;
+  int32_t* refs;
+} iq_paged;
+
+/*
+ * iq_paged_bytes — byte sizes of the six device buffers in descriptor order.
+ * head_dim 256, 1 <= slots <= IQ_MAX_BATCH, 1 <= kv_heads <= 1024,
+ * pages * kv_heads * IQ_PAGE < 2^31, max_pages >= 1.
+ * Errors: INVALID_ARG, UNSUPPORTED.
+ */
+int iq_paged_bytes(int slots, int kv_heads, int head_dim, int pages, int max_pages, size_t out_bytes[6]);
+
+/*
+ * iq_paged_alloc — bind the caller's buffers into the descriptor of an empty
+ * cache; buffers in descriptor order.  The three host arrays are zeroed.
+ * Nothing is copied or launched.  Errors: INVALID_ARG, UNSUPPORTED.
+ */
+int iq_paged_alloc(iq_paged* cache, int slots, int kv_heads, int head_dim, int pages, int max_pages,
+                   void* const buffers[6], int32_t* lens, int32_t* table_host, int32_t* refs);
+
+/* iq_paged_check — validate a descriptor (shapes, pointers, alignment, lens and free_pages in range). */
+int iq_paged_check(const iq_paged* cache);
+
+/*
+ * iq_paged_append — quantise and store new rows.
+ * keys, values: device bf16 [n_slots][kv_heads][n][head_dim], contiguous,
+ *   16-byte aligned, not rotated.
+ * slots: host int32 [n_slots], distinct (NULL: 0 .. n_slots-1).
+ * counts: host int32 [n_slots], 0 <= counts[i] <= n: rows [0, counts[i]) of
+ *   entry i are appended to slots[i], the others are not read (NULL: n).
+ * Free pages are taken lowest id first, in the order of the entries.  A page
+ * whose last rows are shared with other slots is copied first.
+ * Errors: INVALID_ARG; CAPACITY (the pool has too few free pages, or a slot
+ * would pass max_pages); CUDA.  On an error nothing has changed, but on CUDA,
+ * where launches before the failing one stand.
+ */
+int iq_paged_append(iq_paged* cache, const void* keys, const void* values, int n, const int32_t* slots,
+                    const int32_t* counts, int n_slots, iq_stream_t stream);
+
+/*
+ * iq_paged_read — the values held: rows [start[i], start[i] + n) of slot
+ * slots[i], as bfloat16 (exact), into keys_out, values_out
+ * [n_slots][kv_heads][n][head_dim]; rows past the slot's length come back as 0.
+ * slots as above, but a slot may be given twice.  Errors: INVALID_ARG, CUDA.
+ */
+int iq_paged_read(const iq_paged* cache, const int32_t* slots, const int32_t* start, int n_slots, int n,
+                  void* keys_out, void* values_out, iq_stream_t stream);
+
+/*
+ * iq_paged_trim — drop the last n[i] tokens (all, if fewer) of slots[i] and
+ * release the pages that hold none of its tokens any more.  Host bookkeeping
+ * only.  trimmed: host int32 [n_slots] out (may be NULL).
+ * Errors: INVALID_ARG (null, a negative count, a slot out of range or given twice).
+ */
+int iq_paged_trim(iq_paged* cache, const int32_t* slots, const int32_t* n, int n_slots, int32_t* trimmed);
+
+/* iq_paged_free — release every page of these slots: iq_paged_trim of all their tokens. */
+int iq_paged_free(iq_paged* cache, const int32_t* slots, int n_slots);
+
+/*
+ * iq_paged_fork — slot dst[i] becomes a second holder of all pages of slot
+ * src[i]; what dst[i] held is released.  No codes are copied until one of the
+ * holders appends into a page that is partly full.  All forks of a call happen
+ * at once: every source is the slot as it was before the call, also one that
+ * is some other pair's dst, so a permutation of slots is one call.
+ * Errors: INVALID_ARG (a slot out of range, a dst given twice), CUDA.
+ */
+int iq_paged_fork(iq_paged* cache, const int32_t* src, const int32_t* dst, int count, iq_stream_t stream);
+
+/*
+ * iq_paged_compact — make dst a copy of src that holds each live page once, at
+ * ids 0, 1, 2, ... in the order in which the slots' rows name them first; slots
+ * that share pages in src share the copies in dst.  dst's former contents are
+ * dropped.  It grows or shrinks a pool, takes a snapshot and restores one.
+ * src and dst: the same slots, kv_heads and head_dim, no common buffer.
+ * Errors: INVALID_ARG, CAPACITY (dst has too few pages or too short rows), CUDA.
+ */
+int iq_paged_compact(const iq_paged* src, iq_paged* dst, iq_stream_t stream);
+
+/* iq_paged_attend_workspace — device scratch bytes iq_paged_attend needs for these shapes, whatever the lengths. */
+int iq_paged_attend_workspace(const iq_paged* cache, int q_heads, int n_queries, int n_slots, size_t* bytes);
+
+/*
+ * iq_paged_attend — attention of n_queries queries per slot over its pages.
+ * q: device bf16 [n_slots][q_heads][n_queries][head_dim], 16-byte aligned;
+ *   query head h reads kv head h / (q_heads / kv_heads); at most 64 query
+ *   heads per kv head.
+ * slots as in iq_paged_read.  counts: only the first counts[i] queries of
+ *   entry i exist (NULL: n_queries); the rows of out behind them are left as
+ *   they were.
+ * Query j of entry i stands at position p = lens - counts[i] + j and sees key t < lens if
+ *   causal == 0, or t <= p and (window == 0 or t > p - window or t < sinks).
+ *   window and sinks need causal == 1, sinks a window.
+ * out: device [n_slots][q_heads][n_queries][head_dim], bf16 or float32
+ *   (out_f32); softmax(scale * q.k) . v, rounded once; 0 for a query that sees
+ *   no key (an empty slot, a position before the first token).
+ * workspace: at least iq_paged_attend_workspace() bytes, 256-byte aligned; it
+ *   needs no initialisation and holds nothing between calls.  Calls that may
+ *   run at the same time need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA; a kernel-side failure sets
+ * a bit in the cache's status word.
+ */
+int iq_paged_attend(const iq_paged* cache, const void* q, int q_heads, int n_queries, const int32_t* slots,
+                    const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
+                    void* out, int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream);
+
+/*
+ * iq_paged_append_attend — iq_paged_append, then iq_paged_attend of the same
+ * entries, with every argument of both checked before anything is done.
+ * counts, where given, holds for the rows and for the queries, and n must be
+ * n_queries.  slots must be distinct.
+ */
+int iq_paged_append_attend(iq_paged* cache, const void* keys, const void* values, int n, const void* q,
+                           int q_heads, int n_queries, const int32_t* slots, const int32_t* counts,
+                           int n_slots, float scale, int causal, int window, int sinks, void* out,
+                           int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

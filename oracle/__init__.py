@@ -9,6 +9,8 @@ Plain, slow, obviously-correct NumPy restatement of what the pages compute:
 * page "sparkle mlx_streaming/mtp/kv_cache.py": `commit_verified_prefix`
   (trim branch), `_snapshot`/`_restore`, `tile_caches`/`commit_tree_row`.
 
+`paged` is the same for the paged 8-bit cache, which has no page to follow.
+
 Only the tests, the smoke check and the benchmark's CPU-baseline / reference
 arm may import this package.  The product path (the `libiqkv` C-ABI library and
 its Python binding) never imports, calls or links anything here, and nothing
@@ -19,4 +21,4 @@ Every function here has a pin in `tests/test_oracle_*.py` that checks it
 against something other than itself (closed forms, invariants, brute force,
 textbook routines, hand-worked fixtures under `tests/golden/`).
 """
-from . import bf16, rotation, codec, cache, attention  # noqa: F401
+from . import bf16, rotation, codec, cache, attention, paged  # noqa: F401

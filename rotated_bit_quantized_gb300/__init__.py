@@ -6,4 +6,5 @@ load the library; the first call that needs it does, and raises ImportError if
 the library has not been built.
 """
 from .cache import IQCache, Rotation, commit_verified_snapshot  # noqa: F401
+from .paged import IQPagedCache  # noqa: F401
 from ._abi import IQError, LIB_PATH  # noqa: F401

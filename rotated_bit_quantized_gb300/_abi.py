@@ -24,12 +24,18 @@ IQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 IQ_MASK_NONE, IQ_MASK_CAUSAL, IQ_MASK_ADD_F32, IQ_MASK_BOOL_U8 = 0, 1, 2, 3
 IQ_INJECT_COMBINE_WAIT, IQ_INJECT_STAGE_NEVER_FILLED = 1, 2
 IQ_DTYPE_BF16, IQ_DTYPE_F32 = 0, 1
+IQ_PAGE = 64
+IQ_WORKSPACE_HEAD_BYTES = 8448
+IQ_STATUS_RANGE, IQ_STATUS_BAD_PAGE = 0x40000, 0x80000
 
 EXPORTS = ("iq_status_string", "iq_last_error", "iq_build_rotation", "iq_cache_bytes",
            "iq_cache_check", "iq_cache_nbytes", "iq_cache_append", "iq_cache_trim",
            "iq_cache_gather", "iq_attend_workspace", "iq_attend", "iq_read_status",
            "iq_attend_noalloc", "iq_cache_append_attend", "iq_attend_mask", "iq_noalloc_read_status",
-           "iq_debug_inject", "iq_cache_alloc", "iq_cache_grow")
+           "iq_debug_inject", "iq_cache_alloc", "iq_cache_grow", "iq_paged_bytes", "iq_paged_alloc",
+           "iq_paged_check", "iq_paged_append", "iq_paged_read", "iq_paged_trim", "iq_paged_free",
+           "iq_paged_fork", "iq_paged_compact", "iq_paged_attend_workspace", "iq_paged_attend",
+           "iq_paged_append_attend")
 
 
 class IQCacheDesc(ctypes.Structure):
@@ -41,6 +47,18 @@ class IQCacheDesc(ctypes.Structure):
                 ("k_biases", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("v_biases", ctypes.c_void_p),
                 ("lens", ctypes.POINTER(ctypes.c_int32))]
+
+
+class IQPagedDesc(ctypes.Structure):
+    _fields_ = [("slots", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("free_pages", ctypes.c_int32),
+                ("first_free", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("table_host", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
 
 
 class IQError(RuntimeError):
@@ -81,6 +99,20 @@ def lib() -> ctypes.CDLL:
         L.iq_debug_inject.argtypes = [I, ctypes.c_uint, ctypes.c_ulonglong]
         L.iq_cache_alloc.argtypes = [DESC, I, I, I, I, I, I, I, I, ctypes.POINTER(P), I32P]
         L.iq_cache_grow.argtypes = [DESC, DESC, P]
+        PAGED = ctypes.POINTER(IQPagedDesc)
+        F = ctypes.c_float
+        L.iq_paged_bytes.argtypes = [I, I, I, I, I, ctypes.POINTER(S)]
+        L.iq_paged_alloc.argtypes = [PAGED, I, I, I, I, I, ctypes.POINTER(P), P, P, P]
+        L.iq_paged_check.argtypes = [PAGED]
+        L.iq_paged_append.argtypes = [PAGED, P, P, I, P, P, I, P]
+        L.iq_paged_read.argtypes = [PAGED, P, P, I, I, P, P, P]
+        L.iq_paged_trim.argtypes = [PAGED, P, P, I, P]
+        L.iq_paged_free.argtypes = [PAGED, P, I]
+        L.iq_paged_fork.argtypes = [PAGED, P, P, I, P]
+        L.iq_paged_compact.argtypes = [PAGED, PAGED, P]
+        L.iq_paged_attend_workspace.argtypes = [PAGED, I, I, I, ctypes.POINTER(S)]
+        L.iq_paged_attend.argtypes = [PAGED, P, I, I, P, P, I, F, I, I, I, P, I, P, S, P]
+        L.iq_paged_append_attend.argtypes = [PAGED, P, P, I, P, I, I, P, P, I, F, I, I, I, P, I, P, S, P]
         for name in EXPORTS:
             if name not in ("iq_status_string", "iq_last_error", "iq_cache_nbytes"):
                 getattr(L, name).restype = I
