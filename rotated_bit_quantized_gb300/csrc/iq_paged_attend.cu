@@ -1,14 +1,32 @@
 // libiqkv: attention over the paged 8-bit cache.
 //
-// First form: a warp per query row, online softmax over the keys that the row
-// sees (at most two runs of them: the sinks and the window), every key's codes
-// decoded in registers.  float32 throughout.
+// Two kernels.  Calls with at most 64 query rows per kv head (decode, verify)
+// run paged_split_kernel, below: the keys are the matrix products' M dimension,
+// the codes go from HBM through shared memory into tcgen05.mma untouched, and
+// the keys of all (slot, kv head) pairs are split evenly over the GPU.  More
+// rows run a warp per query row (paged_attend_simple).
+//
+// Mathematics of the split kernel.  With a query as two e4m3 parts, x = 2^eq
+// (hi + lo / 16), and key codes K of a page under 2^ek, the scores in log2 units
+// are  s = (K.hi + K.lo / 16) * 2^ek * (2^eq * scale * log2 e): exact products,
+// summed in fp32 by the tensor cores, hi and lo as columns of their own.  With
+// value codes V of a page under 2^ev, the weight of a key is
+// w = 2^(s + ev - ref) = p * 2^ev up to a common factor, so
+// o = sum w V / sum w 2^-ev : the value scales ride in the exponents.  w is held
+// as two e4m3 parts, hi + lo / 128, in columns of their own again (relative
+// error at most 2^-8, at random; 2^-18 of the largest below e4m3's range); the
+// sum w 2^-ev takes w before that rounding, in fp32.  ref moves only when a
+// weight would pass 2^6 (it then becomes the row's maximum), so steady-state
+// tiles need no exchange between the threads, which hold one key each, but a
+// vote.
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstring>
+#include <mutex>
 
-#include "iq_paged.cuh"
+#include "iq_paged_mma.cuh"
 
 namespace iq {
 namespace paged {
@@ -80,6 +98,537 @@ __global__ void __launch_bounds__(256) paged_attend_simple(const __grid_constant
   }
 }
 
+// ------------------------------------------------------------------ decode and verify
+
+constexpr float kTau = 6.0f;    // weights stay below 2^6
+constexpr float kPLo = 128.0f;  // the low parts' scale: half a step at 2^6 is 2, times 128 below 448
+constexpr float kUnset = -1e30f, kDead = 1e30f;  // a row's reference before its first key, and of rows that do not exist
+
+struct SplitParams {
+  CUtensorMap k_map, v_map;
+  const float* k_scales;
+  const float* v_scales;
+  const int* table;
+  unsigned* status;
+  const uint16_t* q;
+  void* out;
+  float* part_o;   // [2 * grid][NR][256] unnormalised partial results
+  float2* part_ml; // [2 * grid][NR] their references and sums
+  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries;
+  float scale;
+  int total;       // tiles of all units
+  // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
+  // its queries; cum: tiles before it (all heads), per: tiles of one of its heads
+  short entry[IQ_MAX_BATCH], slot[IQ_MAX_BATCH];
+  int len[IQ_MAX_BATCH], count[IQ_MAX_BATCH], cum[IQ_MAX_BATCH + 1], per[IQ_MAX_BATCH];
+};
+
+// The key tiles of one entry: those of the sinks, then those of the window.
+struct Tiles {
+  int sinks, skip;  // tiles of the sinks; tiles between them and the window
+  __host__ __device__ int tile(int j) const { return j < sinks ? j : j + skip; }
+};
+__host__ __device__ inline Tiles tiles_of(int first_pos, int window, int sinks) {
+  const int low = window > 0 && first_pos >= window ? first_pos - window + 1 : 0;  // the lowest position's window
+  const int begin = low / kTile, reach = sinks < low ? sinks : low;
+  const int n = (reach + kTile - 1) / kTile;
+  return {n < begin ? n : begin, n < begin ? begin - n : 0};
+}
+
+// The range of a CTA, and the CTA of a tile.
+__host__ __device__ inline int range_begin(int g, int grid, int total) {
+  return static_cast<int>(static_cast<long long>(g) * total / grid);
+}
+__host__ __device__ inline int range_of(int tile, int grid, int total) {
+  return static_cast<int>((static_cast<long long>(tile + 1) * grid - 1) / total);
+}
+
+template <int NR>
+struct SplitShape {
+  static constexpr int kGroups = NR >= 32 ? 2 : 1;    // warpgroups on the softmax, NR / kGroups rows each
+  static constexpr int kRows = NR / kGroups;
+  static constexpr int kCols = 2 * NR;                // high and low parts
+  static constexpr int kSlots = NR == 64 ? 5 : 6;     // tiles of keys or values in flight
+  static constexpr int kQ = kSlots * kSlotBytes;      // [2 halves of the dims][kCols rows][128 bytes]
+  static constexpr int kP = kQ + 2 * kCols * 128;     // [2][kCols rows][128 keys]
+  static constexpr int kMisc = kP + 2 * kCols * 128;
+  static constexpr int kFloats = 2 * NR + 4 * NR;     // factors, references; reductions
+  static constexpr int kBars = 2 * kSlots + 10;
+  static constexpr int kSmem = 1024 + kMisc + kFloats * 4 + NR * 4 + kBars * 8 + 16;
+  static constexpr int kThreads = kGroups * 128 + 64;
+  static constexpr int kTmem = 4 * kCols;             // S twice, O of both halves of the dims
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+// One persistent CTA per SM: warps 0 .. 4 kGroups - 1 hold a key per thread
+// (warp w reaches tensor-memory lanes 32 (w % 4) ..), then one warp streams the
+// pages and one issues the matrix products.
+template <int NR>
+__global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kernel(const __grid_constant__ SplitParams p) {
+  using C = SplitShape<NR>;
+  constexpr int RT = C::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  float* factor = reinterpret_cast<float*>(smem + C::kMisc);  // [NR] 2^eq * scale * log2 e
+  float* ref = factor + NR;                                   // [NR]
+  float* red = ref + NR;                                      // [4 warps][NR]
+  int* pos = reinterpret_cast<int*>(red + 4 * NR);            // [NR]
+  uint64_t* full = reinterpret_cast<uint64_t*>(pos + NR);     // [kSlots]
+  uint64_t* empty = full + C::kSlots;                         // [kSlots]
+  uint64_t* s_full = empty + C::kSlots;                       // [2] scores of a tile in tensor memory
+  uint64_t* s_free = s_full + 2;                              // [2] and read
+  uint64_t* p_ready = s_free + 2;                             // [2] weights of a tile in shared memory
+  uint64_t* o_done = p_ready + 2;                             // [2] and multiplied with its values
+  uint64_t* q_ready = o_done + 2;
+  uint64_t* drained = q_ready + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  static_assert(NR % 2 == 0 && C::kMisc % 8 == 0, "barriers are 8-byte aligned");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kLoader = 4 * C::kGroups, kIssuer = kLoader + 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_free[s], 4 * C::kGroups);
+      mbar_init(&p_ready[s], 4 * C::kGroups);
+      mbar_init(&o_done[s], 1);
+    }
+    mbar_init(q_ready, 4 * C::kGroups);
+    mbar_init(drained, 1);
+    *abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(C::kTmem));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tslot;
+  const uint32_t t_o = tmem + 2 * C::kCols;  // O: [half of the dims][kCols]
+  const Waits wait{abort, p.status};
+
+  const int first = range_begin(blockIdx.x, gridDim.x, p.total), last = range_begin(blockIdx.x + 1, gridDim.x, p.total);
+  // the entry that holds tile `t` of all: every role walks the same segments
+  auto entry_of = [&](int t) {
+    int lo = 0, hi = p.entries - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (p.cum[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+
+  if (warp == kLoader) {
+    // ---------------------------------------------------------------- pages to shared memory
+    const uint64_t pol = policy_evict_first();
+    int issued = 0;
+    bool ok = true;
+    for (int at = first; at < last && ok;) {
+      const int e = entry_of(at), u = at - p.cum[e], h = u / p.per[e], k0 = u % p.per[e];
+      const int n = min(p.per[e] - k0, last - at);
+      const Tiles tiles = tiles_of(p.len[e] - p.count[e], p.window, p.sinks);
+      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
+      const int end_page = (p.len[e] + kPage - 1) / kPage - 1;
+      // lanes fetch the ids of 16 tiles' pages at a time, one such piece ahead
+      auto fetch = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j + (lane >> 1), n - 1)) + (lane & 1), end_page)); };
+      auto load = [&](const CUtensorMap* map, int id0, int id1) {
+        const int s = issued % C::kSlots;
+        if (issued >= C::kSlots) ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], issued / C::kSlots - 1, kLostLoad));
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&full[s], kSlotBytes);
+          uint8_t* to = smem + s * kSlotBytes;
+          const int y0 = (id0 * p.heads + h) * kPage, y1 = (id1 * p.heads + h) * kPage;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            tensor2d_g2s(to + half * kHalfBytes, map, 128 * half, y0, &full[s], pol);
+            tensor2d_g2s(to + half * kHalfBytes + kHalfBytes / 2, map, 128 * half, y1, &full[s], pol);
+          }
+        }
+        if (ok) ++issued;
+        __syncwarp();
+      };
+      int ids = fetch(0), next = fetch(16), v0 = 0, v1 = 0;
+      for (int j = 0; j <= n && ok; ++j) {  // in the order of the products: K0, K1, V0, K2, V1, ...
+        int k0id = 0, k1id = 0;
+        if (j < n) {
+          if (j % 16 == 0) {
+            if (j) {
+              ids = next;
+              next = fetch(j + 16);
+            }
+            ids = page_in_pool(ids, p.pages, p.status);
+          }
+          k0id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16));
+          k1id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16) + 1);
+          load(&p.k_map, k0id, k1id);
+        }
+        if (j > 0 && ok) load(&p.v_map, v0, v1);
+        v0 = k0id;
+        v1 = k1id;
+      }
+      at += n;
+    }
+    if (lane == 0)  // no copy left in flight
+      for (int s = 0; s < C::kSlots && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / C::kSlots);
+  } else if (warp == kIssuer) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t kS = shape(128, C::kCols, false, false), kO = shape(128, C::kCols, true, false);
+      int it = 0, used = 0, segment = 0;
+      bool ok = true;
+      for (int at = first; at < last && ok; ++segment) {
+        const int e = entry_of(at), n = min(p.per[e] - (at - p.cum[e]) % p.per[e], last - at);
+        ok = wait(q_ready, segment, kLostMma);
+        for (int j = 0; j <= n && ok; ++j) {
+          if (j < n) {
+            const int b = (it + j) & 1, s = used % C::kSlots;
+            if (it + j >= 2) ok = wait(&s_free[b], (it + j) / 2 - 1, kLostMma);
+            ok = ok && wait(&full[s], used / C::kSlots, kLostMma);
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_e4m3(tmem + b * C::kCols, operand(sbase + s * kSlotBytes + (k >> 2) * kHalfBytes + (k & 3) * 32),
+                       operand(sbase + C::kQ + (k >> 2) * C::kCols * 128 + (k & 3) * 32), kS, k > 0);
+            mma_commit(&s_full[b]);
+            mma_commit(&empty[s]);
+            ++used;
+          }
+          if (j > 0) {
+            const int b = (it + j - 1) & 1, s = used % C::kSlots;
+            ok = wait(&p_ready[b], (it + j - 1) / 2, kLostMma) && wait(&full[s], used / C::kSlots, kLostMma);
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_e4m3(t_o + half * C::kCols, operand(sbase + s * kSlotBytes + half * kHalfBytes + k * 32 * 128),
+                         operand(sbase + C::kP + b * C::kCols * 128 + k * 32), kO, j > 1 || k > 0);
+            mma_commit(&o_done[b]);
+            mma_commit(&empty[s]);
+            ++used;
+          }
+        }
+        it += n;
+        at += n;
+      }
+      if (!ok) {  // given up: what is in flight ends before the tensor memory goes
+        mma_commit(drained);
+        wait.drain(drained, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax: a key per thread
+    const int group = warp >> 2, key = threadIdx.x & 127, r0 = group * RT;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float l[RT];
+    int it = 0;
+    bool ok = true;
+    auto await = [&](uint64_t* bar, uint32_t phase) {  // a lost wait changes no path: every barrier below is still reached
+      if (ok) ok = wait(bar, phase, kLostRows);
+      __syncwarp();
+    };
+    for (int at = first; at < last;) {
+      const int e = entry_of(at), u = at - p.cum[e], h = u / p.per[e], k0 = u % p.per[e];
+      const int n = min(p.per[e] - k0, last - at), len = p.len[e], count = p.count[e], rows = count * p.rep;
+      const bool whole = n == p.per[e];
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
+      const Tiles tiles = tiles_of(len - count, p.window, p.sinks);
+      const long long q_row = (static_cast<long long>(p.entry[e]) * p.heads + h) * p.rep;  // the kv head's first query head
+      // the query rows, a warp each
+      for (int r = warp; r < NR; r += 4 * C::kGroups) {
+        uint2 hi = make_uint2(0, 0), lo = hi;
+        float f = 0.0f;
+        if (r < rows) {
+          const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(p.q + ((q_row + r % p.rep) * p.nq + r / p.rep) * kHeadDim) + lane);
+          f = clamp_finite(split_query<16>(raw, hi, lo) * (p.scale * kLog2e));
+        }
+        uint8_t* to = smem + C::kQ + (lane >> 4) * C::kCols * 128;
+        *reinterpret_cast<uint2*>(to + swizzled(r, (lane & 15) * 8)) = hi;
+        *reinterpret_cast<uint2*>(to + swizzled(NR + r, (lane & 15) * 8)) = lo;
+        if (lane == 0) {
+          factor[r] = f;
+          ref[r] = r < rows ? kUnset : kDead;
+          pos[r] = r < rows ? len - count + r / p.rep : -1;
+        }
+      }
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+      named_bar(3, 128 * C::kGroups);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) l[r] = 0.0f;
+
+      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
+      const int end_page = (len + kPage - 1) / kPage - 1;
+      // this thread's page of tile j (half of a tile): ids two tiles ahead, scales one
+      auto id_of = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j, n - 1)) + (key >> 6), end_page)); };
+      auto scales_of = [&](int id) {
+        const long long x = static_cast<long long>(page_in_pool(id, p.pages, p.status)) * p.heads + h;
+        return make_float2(__ldcg(p.k_scales + x), __ldcg(p.v_scales + x));
+      };
+      int id = id_of(1);
+      float2 sc = scales_of(id_of(0));
+      for (int j = 0; j < n; ++j, ++it) {
+        const int b = it & 1;
+        const float ks = sc.x;
+        const int ev = exponent_of(sc.y);
+        sc = scales_of(id);
+        id = id_of(j + 2);
+        const int t0 = tiles.tile(k0 + j) * kTile;
+        await(&s_full[b], it / 2);
+        tc_after();
+        float s[RT], w[RT];
+        tmem_ld<RT < 32 ? RT : 32>(tmem + lanes + b * C::kCols + r0, s);
+        tmem_ld<RT < 32 ? RT : 32>(tmem + lanes + b * C::kCols + NR + r0, w);
+        ld_wait();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r] = fmaf(w[r], 1.0f / 16, s[r]) * clamp_finite(factor[r0 + r] * ks) + static_cast<float>(ev);
+        // masks, in tiles that some row does not see whole
+        const int p_lo = len - count, p_hi = len - 1;
+        const bool low_ok = p.window == 0 || t0 > p_hi - p.window || t0 + kTile <= p.sinks;
+        if (!(t0 + kTile <= (p.causal ? p_lo + 1 : len) && low_ok)) {
+          const int t = t0 + key;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int x = pos[r0 + r];
+            const bool see = t < len && (!p.causal || (t <= x && (p.window == 0 || x < p.window || t > x - p.window || t < p.sinks)));
+            if (!see) s[r] = -__builtin_huge_valf();
+          }
+        }
+        int far = 0;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) far |= s[r] - ref[r0 + r] > kTau;
+        asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 128, a;\nselp.s32 %0, 1, 0, b;\n}"
+                     : "+r"(far)
+                     : "r"(1 + group)
+                     : "memory");
+        if (far) {
+          // some row's maximum passed its reference by 2^6: move the references
+          // of such rows to their maxima, and what was summed with them
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            float m = s[r];
+#pragma unroll
+            for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            if (lane == 0) red[(warp & 3) * NR + r0 + r] = m;
+          }
+          named_bar(1 + group, 128);
+          if (j > 0) await(&o_done[b ^ 1], (it - 1) / 2);
+          tc_after();
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int x = r0 + r;
+            const float m = fmaxf(fmaxf(red[x], red[NR + x]), fmaxf(red[2 * NR + x], red[3 * NR + x])), old = ref[x];
+            w[r] = m - old > kTau ? ex2_approx(old - m) : 1.0f;  // the row's change
+            l[r] *= w[r];
+          }
+          if (j > 0) {
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {  // both halves of the dims, high and low parts
+              const uint32_t c = t_o + lanes + (part >> 1) * C::kCols + (part & 1) * NR + r0;
+#pragma unroll
+              for (int x = 0; x < RT; x += 8) {
+                float o[8];
+                tmem_ld<8>(c + x, o);
+                ld_wait();
+#pragma unroll
+                for (int y = 0; y < 8; ++y) o[y] *= w[x + y];
+                tmem_st<8>(c + x, o);
+              }
+            }
+            st_wait();
+          }
+          named_bar(1 + group, 128);
+          if (key < RT) {
+            const int x = r0 + key;
+            const float m = fmaxf(fmaxf(red[x], red[NR + x]), fmaxf(red[2 * NR + x], red[3 * NR + x]));
+            if (m - ref[x] > kTau) ref[x] = m;
+          }
+          named_bar(1 + group, 128);
+        }
+        // weights, their sums, their two parts (the buffer is free once tile it - 2 is multiplied)
+        if (it >= 2) await(&o_done[b], it / 2 - 1);
+        uint8_t* pb = smem + C::kP + b * C::kCols * 128;
+        const float back = power2(-ev);
+#pragma unroll
+        for (int r = 0; r < RT; r += 2) {
+          const float a = ex2_approx(s[r] - ref[r0 + r]), c = ex2_approx(s[r + 1] - ref[r0 + r + 1]);
+          l[r] = fmaf(a, back, l[r]);
+          l[r + 1] = fmaf(c, back, l[r + 1]);
+          const uint32_t hi = e4m3x2(a, c);
+          const float2 f = f16x2_to_f32(e4m3x2_to_f16x2(hi));
+          const uint32_t lo = e4m3x2((a - f.x) * kPLo, (c - f.y) * kPLo);
+          pb[swizzled(r0 + r, key)] = static_cast<uint8_t>(hi);
+          pb[swizzled(r0 + r + 1, key)] = static_cast<uint8_t>(hi >> 8);
+          pb[swizzled(NR + r0 + r, key)] = static_cast<uint8_t>(lo);
+          pb[swizzled(NR + r0 + r + 1, key)] = static_cast<uint8_t>(lo >> 8);
+        }
+        proxy_fence();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[b]);
+      }
+      // ---- the segment's end: sums over the keys, then the results
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float x = l[r];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+        if (lane == 0) red[(warp & 3) * NR + r0 + r] = x;
+      }
+      await(&o_done[(it - 1) & 1], (it - 1) / 2);
+      tc_after();
+      named_bar(3, 128 * C::kGroups);
+      for (int half = group; half < 2; half += C::kGroups) {
+        const int d = half * 128 + key;
+#pragma unroll 1
+        for (int x = 0; x < rows; x += 8) {
+          float o[8], o2[8];
+          tmem_ld<8>(t_o + lanes + half * C::kCols + x, o);
+          tmem_ld<8>(t_o + lanes + half * C::kCols + NR + x, o2);
+          ld_wait();
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = x + y;
+            if (r >= rows) break;
+            const float v = fmaf(o2[y], 1.0f / kPLo, o[y]);
+            const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
+            if (whole) {
+              store_out(p.out, p.out_f32, ((q_row + r % p.rep) * p.nq + r / p.rep) * kHeadDim + d, sum == 0.0f ? 0.0f : v / sum);
+            } else {
+              p.part_o[(static_cast<long long>(slot) * NR + r) * kHeadDim + d] = v;
+              if (d == 0) p.part_ml[slot * NR + r] = make_float2(ref[r], sum);
+            }
+          }
+        }
+      }
+      tc_before();
+      named_bar(3, 128 * C::kGroups);  // red, ref and the query buffer are free again
+      at += n;
+    }
+  }
+  __syncthreads();
+  if (warp == kIssuer) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem));
+  }
+}
+
+// Joins the partial results of units whose tiles more than one CTA took: a
+// thread per dim, in the order of the CTAs.
+template <int NR>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ SplitParams p, int grid) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int e = blockIdx.x / p.heads, h = blockIdx.x % p.heads, r = blockIdx.y;
+  if (r >= p.count[e] * p.rep) return;
+  const int a = p.cum[e] + h * p.per[e], g0 = range_of(a, grid, p.total), g1 = range_of(a + p.per[e] - 1, grid, p.total);
+  if (g0 == g1) return;
+  auto slot = [&](int g) { return 2 * g + (g == g0 && range_begin(g, grid, p.total) < a ? 1 : 0); };
+  float m = kUnset;
+  for (int g = g0; g <= g1; ++g) m = fmaxf(m, __ldcg(&p.part_ml[slot(g) * NR + r]).x);
+  float sum = 0.0f, o = 0.0f;
+#pragma unroll 4
+  for (int g = g0; g <= g1; ++g) {
+    const float2 ml = __ldcg(&p.part_ml[slot(g) * NR + r]);
+    const float f = ex2_approx(ml.x - m);
+    sum = fmaf(f, ml.y, sum);
+    o = fmaf(f, __ldcg(&p.part_o[(static_cast<long long>(slot(g)) * NR + r) * kHeadDim + threadIdx.x]), o);
+  }
+  const long long row = ((static_cast<long long>(p.entry[e]) * p.heads + h) * p.rep + r % p.rep) * p.nq + r / p.rep;
+  store_out(p.out, p.out_f32, row * kHeadDim + threadIdx.x, sum == 0.0f ? 0.0f : o / sum);
+}
+
+// Rows of entries without a key: zeros.
+struct ZeroParams {
+  void* out;
+  int q_heads, nq, out_bytes;
+  short entry[IQ_MAX_BATCH];
+  int count[IQ_MAX_BATCH];
+};
+__global__ void __launch_bounds__(256) paged_zero_kernel(const __grid_constant__ ZeroParams p) {
+  const int pieces = kHeadDim * p.out_bytes / 16;
+  const long long n = static_cast<long long>(p.count[blockIdx.y]) * pieces;
+  for (int h = 0; h < p.q_heads; ++h) {
+    uint4* out = static_cast<uint4*>(p.out) + (static_cast<long long>(p.entry[blockIdx.y]) * p.q_heads + h) * p.nq * pieces;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) out[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+constexpr int kMaxSplitRows = 64;
+int rows_up(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+size_t split_workspace(int rows) {
+  const size_t parts = 2 * static_cast<size_t>(num_sms()) * rows_up(rows);
+  return parts * (kHeadDim * sizeof(float) + sizeof(float2));
+}
+
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int NR>
+cudaError_t launch_split(const SplitParams& p, int grid, bool join, cudaStream_t stream) {
+  using C = SplitShape<NR>;
+  cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e == cudaSuccess) e = launch_after<SplitParams>(paged_split_kernel<NR>, dim3(grid), C::kThreads, C::kSmem, stream, p);
+  if (e == cudaSuccess && join)
+    e = launch_after<SplitParams, int>(paged_join_kernel<NR>, dim3(p.entries * p.heads, p.nq * p.rep), 256, 0, stream, p, grid);
+  return e;
+}
+
+}  // namespace
+
+bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows) {
+  const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(rows)}, strides[1] = {kHeadDim};
+  const cuuint32_t box[2] = {128, kPage}, unit[2] = {1, 1};
+  auto fn = encode_fn();
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots,
                  const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
                  const void* out, int out_f32, const void* workspace, size_t workspace_bytes) {
@@ -124,7 +673,8 @@ int iq_paged_attend_workspace(const iq_paged* c, int q_heads, int n_queries, int
   if (q_heads % c->kv_heads) return fail(IQ_ERR_UNSUPPORTED, "q_heads must be a multiple of kv_heads");
   if (q_heads / c->kv_heads > kMaxRep) return fail(IQ_ERR_UNSUPPORTED, "at most 64 query heads per kv head");
   if (static_cast<long long>(n_queries) * (q_heads / c->kv_heads) >= (1LL << 30)) return fail(IQ_ERR_UNSUPPORTED, "too many query rows");
-  *bytes = 0;
+  const int rows = n_queries * (q_heads / c->kv_heads);
+  *bytes = rows > 0 && rows <= kMaxSplitRows && n_slots > 0 ? split_workspace(rows) : 0;
   return IQ_OK;
 }
 
@@ -134,6 +684,79 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   const int st = check_attend(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32,
                               workspace, workspace_bytes);
   if (st != IQ_OK || n_slots == 0 || n_queries == 0) return st;
+  const int rep = q_heads / c->kv_heads, rows = rep * n_queries;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  {
+    ZeroParams z;
+    z.out = out;
+    z.q_heads = q_heads;
+    z.nq = n_queries;
+    z.out_bytes = out_f32 ? 4 : 2;
+    int n = 0, most = 0;
+    for (int i = 0; i < n_slots; ++i) {
+      const int count = counts ? counts[i] : n_queries;
+      if (count == 0 || c->lens[slot_of(slots, i)] > 0) continue;
+      z.entry[n] = static_cast<short>(i);
+      z.count[n++] = count;
+      most = std::max(most, count);
+    }
+    if (n > 0) {
+      paged_zero_kernel<<<dim3(std::min(64, (most + 7) / 8), n), 256, 0, cs>>>(z);
+      IQ_CUDA(cudaGetLastError());
+    }
+  }
+  if (rows <= kMaxSplitRows) {
+    SplitParams p;
+    std::memset(&p, 0, sizeof(p));
+    long long total = 0;
+    for (int i = 0; i < n_slots; ++i) {
+      const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
+      if (count == 0 || len == 0) continue;
+      const Tiles t = tiles_of(len - count, window, sinks);
+      const int e = p.entries++;
+      p.entry[e] = static_cast<short>(i);
+      p.slot[e] = static_cast<short>(s);
+      p.len[e] = len;
+      p.count[e] = count;
+      p.cum[e] = static_cast<int>(total);
+      p.per[e] = (len + kTile - 1) / kTile - t.skip;
+      total += static_cast<long long>(p.per[e]) * c->kv_heads;
+      if (total >= (1LL << 31)) return fail(IQ_ERR_UNSUPPORTED, "the slots hold too many tokens for one call");
+    }
+    if (p.entries == 0) return IQ_OK;
+    p.cum[p.entries] = p.total = static_cast<int>(total);
+    const long long pool_rows = static_cast<long long>(c->pages) * c->kv_heads * kPage;
+    if (!code_map(&p.k_map, c->k_codes, pool_rows) || !code_map(&p.v_map, c->v_codes, pool_rows))
+      return fail(IQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    p.k_scales = c->k_scales;
+    p.v_scales = c->v_scales;
+    p.table = c->table;
+    p.status = c->status;
+    p.q = static_cast<const uint16_t*>(q);
+    p.out = out;
+    p.out_f32 = out_f32;
+    p.heads = c->kv_heads;
+    p.rep = rep;
+    p.nq = n_queries;
+    p.pages = c->pages;
+    p.max_pages = c->max_pages;
+    p.causal = causal;
+    p.window = window;
+    p.sinks = sinks;
+    p.scale = scale;
+    const int nr = rows_up(rows), grid = static_cast<int>(std::min<long long>(num_sms(), total));
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * grid * nr * kHeadDim);
+    bool join = false;  // some range begins inside a unit
+    for (int g = 1, e = 0; g < grid && !join; ++g) {
+      const int b = range_begin(g, grid, p.total);
+      while (p.cum[e + 1] <= b) ++e;
+      join = (b - p.cum[e]) % p.per[e] != 0;
+    }
+    cudaError_t err = nr == 8 ? launch_split<8>(p, grid, join, cs) : nr == 16 ? launch_split<16>(p, grid, join, cs)
+                      : nr == 32 ? launch_split<32>(p, grid, join, cs) : launch_split<64>(p, grid, join, cs);
+    return err == cudaSuccess ? IQ_OK : cuda_fail(err, "paged attention");
+  }
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.k_codes = c->k_codes;
@@ -146,7 +769,7 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   p.out = out;
   p.out_f32 = out_f32;
   p.heads = c->kv_heads;
-  p.rep = q_heads / c->kv_heads;
+  p.rep = rep;
   p.nq = n_queries;
   p.pages = c->pages;
   p.max_pages = c->max_pages;
@@ -159,7 +782,7 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
     p.len[i] = c->lens[p.slot[i]];
     p.count[i] = counts ? counts[i] : n_queries;
   }
-  paged_attend_simple<<<dim3((n_queries + 7) / 8, q_heads, n_slots), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  paged_attend_simple<<<dim3((n_queries + 7) / 8, q_heads, n_slots), 256, 0, cs>>>(p);
   IQ_CUDA(cudaGetLastError());
   return IQ_OK;
 }

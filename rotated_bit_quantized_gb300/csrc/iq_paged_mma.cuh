@@ -1,0 +1,178 @@
+// tcgen05 pieces shared by the paged cache's attention kernels: e4m3 operands
+// in 128-byte-swizzled shared memory, fp32 accumulators in tensor memory, and
+// waits that end.
+#pragma once
+
+#include <cuda.h>
+
+#include "iq_paged.cuh"
+
+namespace iq {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTile = 128;                    // keys per tile: two pages
+constexpr int kHalfBytes = kTile * 128;       // 128 rows of half a head's dims
+constexpr int kSlotBytes = 2 * kHalfBytes;    // a tile of keys or of values in shared memory
+
+// The tensor map of a code pool: rows of 256 bytes, boxes of one page of one
+// kv head by half of the dims (64 x 128 bytes, 128-byte swizzle).
+bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows);
+
+// Waits end: after a second (no stage takes a thousandth of it) the CTA's
+// abort flag is raised, every later wait of the CTA returns at once, and the
+// kernel runs out with a status bit set.
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+struct Waits {
+  volatile int* abort;  // shared memory
+  unsigned* status;
+  __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity, unsigned bit) const {
+    const unsigned long long t0 = now_ns();
+    for (;;) {
+      if (mbar_try_wait(bar, parity, 20000u)) return true;
+      if (*abort) return false;
+      if (now_ns() - t0 > 1000000000ull) {
+        *abort = 1;
+        atomicOr(status, bit);
+        return false;
+      }
+    }
+  }
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, unsigned bit) const {
+    return mbar_try_wait(bar, parity & 1, 20000u) || slow(bar, parity & 1, bit);
+  }
+  // the same whether or not the CTA has given up: for what is in flight at the end
+  __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
+    const unsigned long long t0 = now_ns();
+    while (!mbar_try_wait(bar, parity & 1, 20000u))
+      if (now_ns() - t0 > 1000000000ull) return;
+  }
+};
+// status bits of the waits that ran out
+constexpr unsigned kLostLoad = 0x1, kLostMma = 0x2, kLostRows = 0x8;
+
+// Shared-memory operand descriptors, 128-byte swizzle.  K-major: rows of 128
+// bytes, groups of 8 rows 1024 bytes apart.  MN-major: the 128 contiguous
+// bytes run along M or N, `wide` bytes to the next 128 of them, and groups of
+// 8 rows of K lie 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t saddr, uint32_t wide = 16) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(wide >> 4) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+// kind::f8f6f4, e4m3 x e4m3 -> fp32; which operands are MN-major
+__host__ __device__ constexpr uint32_t shape(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// n consecutive columns of this thread's lane (volatile, and read only after ld_wait)
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float* v);
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const float* v);
+
+template <>
+__device__ __forceinline__ void tmem_ld<8>(uint32_t addr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_ld<32>(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+        "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]),
+        "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_st<8>(uint32_t addr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st<16>(uint32_t addr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+
+// Byte offset of byte `c` of row `r` in a 128-byte-swizzled block of 128-byte rows.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 15));
+}
+
+// One query row (a warp; lane l holds dims 8l .. 8l+7 as bf16) as two e4m3
+// parts: x * 2^-e = hi + lo / kQLo, with the row's largest element in (224,
+// 448].  A bf16 has 8 significant bits and an e4m3 code 4, so the two parts
+// hold it exactly but for elements 2^14 below the row's largest (kQLo 16).
+// Returns 2^e; a row with a NaN or an infinity becomes all NaN.
+template <int QLO>
+__device__ __forceinline__ float split_query(uint4 raw, uint2& hi, uint2& lo) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (top >= 0x7F80u) {
+    hi = lo = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    return 1.0f;
+  }
+  int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
+  e = min(max(e, -100), 120);
+  const float inv = power2(-e);
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = bf16_to_f32(w[j] & 0xFFFFu) * inv, b = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+    h[j] = e4m3x2(a, b);
+    const float2 f = f16x2_to_f32(e4m3x2_to_f16x2(h[j]));
+    l[j] = e4m3x2((a - f.x) * QLO, (b - f.y) * QLO);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  return power2(e);
+}
+__device__ __forceinline__ float clamp_finite(float x) { return fminf(fmaxf(x, -3e38f), 3e38f); }
+
+__device__ __forceinline__ void store_out(void* out, int out_f32, long long at, float x) {
+  if (out_f32) static_cast<float*>(out)[at] = x;
+  else static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(f32_to_bf16_bits(x));
+}
+
+}  // namespace paged
+}  // namespace iq

@@ -159,8 +159,9 @@ class IQPagedCache:
         need = self._need.get(key)
         if need is None:
             c = ctypes.c_size_t()
-            check(lib().iq_paged_attend_workspace(self._d, q_heads, rows, entries, ctypes.byref(c)),
-                  "iq_paged_attend_workspace")
+            with self._on:
+                check(lib().iq_paged_attend_workspace(self._d, q_heads, rows, entries, ctypes.byref(c)),
+                      "iq_paged_attend_workspace")
             if len(self._need) > 256:
                 self._need.clear()
             need = self._need[key] = c.value
