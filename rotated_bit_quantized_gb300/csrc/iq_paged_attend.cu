@@ -4,7 +4,7 @@
 // run paged_split_kernel, below: the keys are the matrix products' M dimension,
 // the codes go from HBM through shared memory into tcgen05.mma untouched, and
 // the keys of all (slot, kv head) pairs are split evenly over the GPU.  More
-// rows run a warp per query row (paged_attend_simple).
+// rows run paged_prefill_kernel (iq_paged_prefill.cu).
 //
 // Mathematics of the split kernel.  With a query as two e4m3 parts, x = 2^eq
 // (hi + lo / 16), and key codes K of a page under 2^ek, the scores in log2 units
@@ -31,117 +31,11 @@
 namespace iq {
 namespace paged {
 
-struct AttendParams {
-  const uint8_t* k_codes;
-  const uint8_t* v_codes;
-  const float* k_scales;
-  const float* v_scales;
-  const int* table;
-  unsigned* status;
-  const uint16_t* q;
-  void* out;
-  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks;
-  float scale;
-  int slot[IQ_MAX_BATCH], len[IQ_MAX_BATCH], count[IQ_MAX_BATCH];
-};
-
-__device__ __forceinline__ void load8(const uint8_t* codes, float s, float (&x)[8]) {
-  const uint2 c = *reinterpret_cast<const uint2*>(codes);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = f16x2_to_f32(e4m3x2_to_f16x2((j < 2 ? c.x : c.y) >> (16 * (j & 1)) & 0xFFFFu));
-    x[2 * j] = f.x * s;
-    x[2 * j + 1] = f.y * s;
-  }
-}
-
-__global__ void __launch_bounds__(256) paged_attend_simple(const __grid_constant__ AttendParams p) {
-  const int lane = threadIdx.x & 31, i = blockIdx.z, hq = blockIdx.y, h = hq / p.rep;
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (j >= p.count[i]) return;
-  const int len = p.len[i], pos = len - p.count[i] + j;
-  const long long row = ((static_cast<long long>(i) * p.heads * p.rep + hq) * p.nq + j) * kHeadDim + lane * 8;
-  float q[8], o[8] = {};
-  const uint4 raw = *reinterpret_cast<const uint4*>(p.q + row);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int d = 0; d < 8; ++d) q[d] = bf16_to_f32(w[d / 2] >> (16 * (d & 1)) & 0xFFFFu) * p.scale;
-  const int stop = p.causal ? pos + 1 : len;
-  const int low = p.window && pos >= p.window ? pos - p.window + 1 : 0;  // first key of the window
-  float m = -__builtin_huge_valf(), l = 0.0f;
-  for (int t = min(p.sinks, low) > 0 ? 0 : low; t < stop; ++t) {
-    if (t == p.sinks && t < low) t = low;
-    const int page = page_in_pool(p.table[static_cast<long long>(p.slot[i]) * p.max_pages + t / kPage], p.pages, p.status);
-    const long long at = static_cast<long long>(page) * p.heads + h, byte = at * kPageBytes + (t % kPage) * kHeadDim + lane * 8;
-    float x[8], s = 0.0f;
-    load8(p.k_codes + byte, p.k_scales[at], x);
-#pragma unroll
-    for (int d = 0; d < 8; ++d) s = fmaf(q[d], x[d], s);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const float m2 = fmaxf(m, s), f = __expf(m - m2), e = __expf(s - m2);
-    load8(p.v_codes + byte, p.v_scales[at], x);
-#pragma unroll
-    for (int d = 0; d < 8; ++d) o[d] = fmaf(o[d], f, e * x[d]);
-    l = fmaf(l, f, e);
-    m = m2;
-  }
-  const float inv = stop > 0 ? 1.0f / l : 0.0f;
-  if (p.out_f32) {
-    float* out = static_cast<float*>(p.out) + row;
-#pragma unroll
-    for (int d = 0; d < 8; ++d) out[d] = o[d] * inv;
-  } else {
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row);
-#pragma unroll
-    for (int d = 0; d < 4; ++d) out[d] = f32_to_bf16_bits(o[2 * d] * inv) | f32_to_bf16_bits(o[2 * d + 1] * inv) << 16;
-  }
-}
-
 // ------------------------------------------------------------------ decode and verify
 
 constexpr float kTau = 6.0f;    // weights stay below 2^6
 constexpr float kPLo = 128.0f;  // the low parts' scale: half a step at 2^6 is 2, times 128 below 448
 constexpr float kUnset = -1e30f, kDead = 1e30f;  // a row's reference before its first key, and of rows that do not exist
-
-struct SplitParams {
-  CUtensorMap k_map, v_map;
-  const float* k_scales;
-  const float* v_scales;
-  const int* table;
-  unsigned* status;
-  const uint16_t* q;
-  void* out;
-  float* part_o;   // [2 * grid][NR][256] unnormalised partial results
-  float2* part_ml; // [2 * grid][NR] their references and sums
-  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries;
-  float scale;
-  int total;       // tiles of all units
-  // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
-  // its queries; cum: tiles before it (all heads), per: tiles of one of its heads
-  short entry[IQ_MAX_BATCH], slot[IQ_MAX_BATCH];
-  int len[IQ_MAX_BATCH], count[IQ_MAX_BATCH], cum[IQ_MAX_BATCH + 1], per[IQ_MAX_BATCH];
-};
-
-// The key tiles of one entry: those of the sinks, then those of the window.
-struct Tiles {
-  int sinks, skip;  // tiles of the sinks; tiles between them and the window
-  __host__ __device__ int tile(int j) const { return j < sinks ? j : j + skip; }
-};
-__host__ __device__ inline Tiles tiles_of(int first_pos, int window, int sinks) {
-  const int low = window > 0 && first_pos >= window ? first_pos - window + 1 : 0;  // the lowest position's window
-  const int begin = low / kTile, reach = sinks < low ? sinks : low;
-  const int n = (reach + kTile - 1) / kTile;
-  return {n < begin ? n : begin, n < begin ? begin - n : 0};
-}
-
-// The range of a CTA, and the CTA of a tile.
-__host__ __device__ inline int range_begin(int g, int grid, int total) {
-  return static_cast<int>(static_cast<long long>(g) * total / grid);
-}
-__host__ __device__ inline int range_of(int tile, int grid, int total) {
-  return static_cast<int>((static_cast<long long>(tile + 1) * grid - 1) / total);
-}
 
 template <int NR>
 struct SplitShape {
@@ -164,7 +58,7 @@ struct SplitShape {
 // (warp w reaches tensor-memory lanes 32 (w % 4) ..), then one warp streams the
 // pages and one issues the matrix products.
 template <int NR>
-__global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kernel(const __grid_constant__ SplitParams p) {
+__global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kernel(const __grid_constant__ AttendParams p) {
   using C = SplitShape<NR>;
   constexpr int RT = C::kRows;
   extern __shared__ uint8_t smem_raw[];
@@ -218,26 +112,18 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   const Waits wait{abort, p.status};
 
   const int first = range_begin(blockIdx.x, gridDim.x, p.total), last = range_begin(blockIdx.x + 1, gridDim.x, p.total);
-  // the entry that holds tile `t` of all: every role walks the same segments
-  auto entry_of = [&](int t) {
-    int lo = 0, hi = p.entries - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (p.cum[mid] <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  };
+  const Place start = place_of(p, first);  // every role walks the same segments from here
 
   if (warp == kLoader) {
     // ---------------------------------------------------------------- pages to shared memory
     const uint64_t pol = policy_evict_first();
     int issued = 0;
     bool ok = true;
-    for (int at = first; at < last && ok;) {
-      const int e = entry_of(at), u = at - p.cum[e], h = u / p.per[e], k0 = u % p.per[e];
-      const int n = min(p.per[e] - k0, last - at);
-      const Tiles tiles = tiles_of(p.len[e] - p.count[e], p.window, p.sinks);
+    Place w = start;
+    for (int at = first; at < last && ok; next_unit(p, w)) {
+      const int e = w.e, h = w.h, k0 = w.j;
+      const Tiles tiles = tiles_at(p, w);
+      const int n = min(tiles.n - k0, last - at);
       const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
       const int end_page = (p.len[e] + kPage - 1) / kPage - 1;
       // lanes fetch the ids of 16 tiles' pages at a time, one such piece ahead
@@ -287,8 +173,9 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       constexpr uint32_t kS = shape(128, C::kCols, false, false), kO = shape(128, C::kCols, true, false);
       int it = 0, used = 0, segment = 0;
       bool ok = true;
-      for (int at = first; at < last && ok; ++segment) {
-        const int e = entry_of(at), n = min(p.per[e] - (at - p.cum[e]) % p.per[e], last - at);
+      Place w = start;
+      for (int at = first; at < last && ok; ++segment, next_unit(p, w)) {
+        const int n = min(tiles_at(p, w).n - w.j, last - at);
         ok = wait(q_ready, segment, kLostMma);
         for (int j = 0; j <= n && ok; ++j) {
           if (j < n) {
@@ -341,19 +228,19 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       if (ok) ok = wait(bar, phase, kLostRows);
       __syncwarp();
     };
-    for (int at = first; at < last;) {
-      const int e = entry_of(at), u = at - p.cum[e], h = u / p.per[e], k0 = u % p.per[e];
-      const int n = min(p.per[e] - k0, last - at), len = p.len[e], count = p.count[e], rows = count * p.rep;
-      const bool whole = n == p.per[e];
+    Place at_unit = start;
+    for (int at = first; at < last; next_unit(p, at_unit)) {
+      const int e = at_unit.e, h = at_unit.h, k0 = at_unit.j;
+      const Tiles tiles = tiles_at(p, at_unit);
+      const int n = min(tiles.n - k0, last - at), len = p.len[e], count = p.count[e], rows = count * p.rep;
+      const bool whole = n == tiles.n;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
-      const Tiles tiles = tiles_of(len - count, p.window, p.sinks);
-      const long long q_row = (static_cast<long long>(p.entry[e]) * p.heads + h) * p.rep;  // the kv head's first query head
       // the query rows, a warp each
       for (int r = warp; r < NR; r += 4 * C::kGroups) {
         uint2 hi = make_uint2(0, 0), lo = hi;
         float f = 0.0f;
         if (r < rows) {
-          const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(p.q + ((q_row + r % p.rep) * p.nq + r / p.rep) * kHeadDim) + lane);
+          const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, at_unit, r) * kHeadDim) + lane);
           f = clamp_finite(split_query<16>(raw, hi, lo) * (p.scale * kLog2e));
         }
         uint8_t* to = smem + C::kQ + (lane >> 4) * C::kCols * 128;
@@ -401,9 +288,8 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r] = fmaf(w[r], 1.0f / 16, s[r]) * clamp_finite(factor[r0 + r] * ks) + static_cast<float>(ev);
         // masks, in tiles that some row does not see whole
-        const int p_lo = len - count, p_hi = len - 1;
-        const bool low_ok = p.window == 0 || t0 > p_hi - p.window || t0 + kTile <= p.sinks;
-        if (!(t0 + kTile <= (p.causal ? p_lo + 1 : len) && low_ok)) {
+        const bool low_ok = p.window == 0 || t0 > tiles.p_hi - p.window || t0 + kTile <= p.sinks;
+        if (!(t0 + kTile <= (p.causal ? tiles.p_lo + 1 : len) && low_ok)) {
           const int t = t0 + key;
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
@@ -511,7 +397,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
             const float v = fmaf(o2[y], 1.0f / kPLo, o[y]);
             const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
             if (whole) {
-              store_out(p.out, p.out_f32, ((q_row + r % p.rep) * p.nq + r / p.rep) * kHeadDim + d, sum == 0.0f ? 0.0f : v / sum);
+              store_out(p.out, p.out_f32, row_index(p, at_unit, r) * kHeadDim + d, sum == 0.0f ? 0.0f : v / sum);
             } else {
               p.part_o[(static_cast<long long>(slot) * NR + r) * kHeadDim + d] = v;
               if (d == 0) p.part_ml[slot * NR + r] = make_float2(ref[r], sum);
@@ -531,28 +417,39 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   }
 }
 
-// Joins the partial results of units whose tiles more than one CTA took: a
-// thread per dim, in the order of the CTAs.
-template <int NR>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ SplitParams p, int grid) {
+// Joins the partial results of the units that ranges cut: CTA (g, y) takes 8 rows
+// of the unit that range g + 1 begins inside of, where it is the first to do so; a
+// warp per row, a lane per 8 dims, the partials in the order of the ranges.
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ AttendParams p, int grid) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int e = blockIdx.x / p.heads, h = blockIdx.x % p.heads, r = blockIdx.y;
-  if (r >= p.count[e] * p.rep) return;
-  const int a = p.cum[e] + h * p.per[e], g0 = range_of(a, grid, p.total), g1 = range_of(a + p.per[e] - 1, grid, p.total);
-  if (g0 == g1) return;
-  auto slot = [&](int g) { return 2 * g + (g == g0 && range_begin(g, grid, p.total) < a ? 1 : 0); };
-  float m = kUnset;
-  for (int g = g0; g <= g1; ++g) m = fmaxf(m, __ldcg(&p.part_ml[slot(g) * NR + r]).x);
-  float sum = 0.0f, o = 0.0f;
+  const int cut = range_begin(blockIdx.x + 1, grid, p.total);
+  const Place w = place_of(p, cut);
+  const int a = cut - w.j, n = tiles_at(p, w).n;
+  const int g0 = range_of(a, grid, p.total), g1 = range_of(a + n - 1, grid, p.total);
+  if (w.j == 0 || g0 != static_cast<int>(blockIdx.x)) return;
+  const int x = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, r = w.z * p.unit_rows + x;
+  if (x >= p.unit_rows || r >= p.count[w.e] * p.rep) return;
+  auto row = [&](int g) {
+    return static_cast<long long>(2 * g + (g == g0 && range_begin(g, grid, p.total) < a ? 1 : 0)) * p.unit_rows + x;
+  };
+  float m = -1e30f;  // every lane a partial, then the largest reference
+  for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, __ldcg(&p.part_ml[row(g)]).x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  float sum = 0.0f, o[8] = {};
 #pragma unroll 4
   for (int g = g0; g <= g1; ++g) {
-    const float2 ml = __ldcg(&p.part_ml[slot(g) * NR + r]);
+    const long long i = row(g);
+    const float2 ml = __ldcg(&p.part_ml[i]);
+    const float4* v = reinterpret_cast<const float4*>(p.part_o + i * kHeadDim + lane * 8);
+    const float4 v0 = __ldcg(v), v1 = __ldcg(v + 1);
     const float f = ex2_approx(ml.x - m);
     sum = fmaf(f, ml.y, sum);
-    o = fmaf(f, __ldcg(&p.part_o[(static_cast<long long>(slot(g)) * NR + r) * kHeadDim + threadIdx.x]), o);
+    o[0] = fmaf(f, v0.x, o[0]), o[1] = fmaf(f, v0.y, o[1]), o[2] = fmaf(f, v0.z, o[2]), o[3] = fmaf(f, v0.w, o[3]);
+    o[4] = fmaf(f, v1.x, o[4]), o[5] = fmaf(f, v1.y, o[5]), o[6] = fmaf(f, v1.z, o[6]), o[7] = fmaf(f, v1.w, o[7]);
   }
-  const long long row = ((static_cast<long long>(p.entry[e]) * p.heads + h) * p.rep + r % p.rep) * p.nq + r / p.rep;
-  store_out(p.out, p.out_f32, row * kHeadDim + threadIdx.x, sum == 0.0f ? 0.0f : o / sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  store_out8(p.out, p.out_f32, row_index(p, w, r) * kHeadDim + lane * 8, o, inv);
 }
 
 // Rows of entries without a key: zeros.
@@ -587,35 +484,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 constexpr int kMaxSplitRows = 64;
-int rows_up(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-size_t split_workspace(int rows) {
-  const size_t parts = 2 * static_cast<size_t>(num_sms()) * rows_up(rows);
-  return parts * (kHeadDim * sizeof(float) + sizeof(float2));
-}
-
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
+int unit_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kMaxSplitRows ? 64 : 128; }
 
 template <int NR>
-cudaError_t launch_split(const SplitParams& p, int grid, bool join, cudaStream_t stream) {
+cudaError_t launch_split(const AttendParams& p, int grid, cudaStream_t stream) {
   using C = SplitShape<NR>;
-  cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e == cudaSuccess) e = launch_after<SplitParams>(paged_split_kernel<NR>, dim3(grid), C::kThreads, C::kSmem, stream, p);
-  if (e == cudaSuccess && join)
-    e = launch_after<SplitParams, int>(paged_join_kernel<NR>, dim3(p.entries * p.heads, p.nq * p.rep), 256, 0, stream, p, grid);
-  return e;
+  const cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  return e == cudaSuccess ? launch_after<AttendParams>(paged_split_kernel<NR>, dim3(grid), C::kThreads, C::kSmem, stream, p) : e;
 }
 
 }  // namespace
@@ -674,7 +549,8 @@ int iq_paged_attend_workspace(const iq_paged* c, int q_heads, int n_queries, int
   if (q_heads / c->kv_heads > kMaxRep) return fail(IQ_ERR_UNSUPPORTED, "at most 64 query heads per kv head");
   if (static_cast<long long>(n_queries) * (q_heads / c->kv_heads) >= (1LL << 30)) return fail(IQ_ERR_UNSUPPORTED, "too many query rows");
   const int rows = n_queries * (q_heads / c->kv_heads);
-  *bytes = rows > 0 && rows <= kMaxSplitRows && n_slots > 0 ? split_workspace(rows) : 0;
+  const size_t parts = rows > 0 && n_slots > 0 ? 2 * static_cast<size_t>(num_sms()) * unit_rows(rows) : 0;
+  *bytes = parts * (kHeadDim * sizeof(float) + sizeof(float2));
   return IQ_OK;
 }
 
@@ -705,62 +581,31 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
       IQ_CUDA(cudaGetLastError());
     }
   }
-  if (rows <= kMaxSplitRows) {
-    SplitParams p;
-    std::memset(&p, 0, sizeof(p));
-    long long total = 0;
-    for (int i = 0; i < n_slots; ++i) {
-      const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
-      if (count == 0 || len == 0) continue;
-      const Tiles t = tiles_of(len - count, window, sinks);
-      const int e = p.entries++;
-      p.entry[e] = static_cast<short>(i);
-      p.slot[e] = static_cast<short>(s);
-      p.len[e] = len;
-      p.count[e] = count;
-      p.cum[e] = static_cast<int>(total);
-      p.per[e] = (len + kTile - 1) / kTile - t.skip;
-      total += static_cast<long long>(p.per[e]) * c->kv_heads;
-      if (total >= (1LL << 31)) return fail(IQ_ERR_UNSUPPORTED, "the slots hold too many tokens for one call");
-    }
-    if (p.entries == 0) return IQ_OK;
-    p.cum[p.entries] = p.total = static_cast<int>(total);
-    const long long pool_rows = static_cast<long long>(c->pages) * c->kv_heads * kPage;
-    if (!code_map(&p.k_map, c->k_codes, pool_rows) || !code_map(&p.v_map, c->v_codes, pool_rows))
-      return fail(IQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    p.k_scales = c->k_scales;
-    p.v_scales = c->v_scales;
-    p.table = c->table;
-    p.status = c->status;
-    p.q = static_cast<const uint16_t*>(q);
-    p.out = out;
-    p.out_f32 = out_f32;
-    p.heads = c->kv_heads;
-    p.rep = rep;
-    p.nq = n_queries;
-    p.pages = c->pages;
-    p.max_pages = c->max_pages;
-    p.causal = causal;
-    p.window = window;
-    p.sinks = sinks;
-    p.scale = scale;
-    const int nr = rows_up(rows), grid = static_cast<int>(std::min<long long>(num_sms(), total));
-    p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * grid * nr * kHeadDim);
-    bool join = false;  // some range begins inside a unit
-    for (int g = 1, e = 0; g < grid && !join; ++g) {
-      const int b = range_begin(g, grid, p.total);
-      while (p.cum[e + 1] <= b) ++e;
-      join = (b - p.cum[e]) % p.per[e] != 0;
-    }
-    cudaError_t err = nr == 8 ? launch_split<8>(p, grid, join, cs) : nr == 16 ? launch_split<16>(p, grid, join, cs)
-                      : nr == 32 ? launch_split<32>(p, grid, join, cs) : launch_split<64>(p, grid, join, cs);
-    return err == cudaSuccess ? IQ_OK : cuda_fail(err, "paged attention");
-  }
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
-  p.k_codes = c->k_codes;
-  p.v_codes = c->v_codes;
+  p.unit_rows = unit_rows(rows);
+  long long total = 0;
+  for (int i = 0; i < n_slots; ++i) {
+    const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
+    if (count == 0 || len == 0) continue;
+    const int e = p.entries++;
+    p.entry[e] = static_cast<short>(i);
+    p.slot[e] = static_cast<short>(s);
+    p.len[e] = len;
+    p.count[e] = count;
+    p.cum[e] = static_cast<int>(total);
+    long long per = 0;
+    for (int z = 0; static_cast<long long>(z) * p.unit_rows < static_cast<long long>(count) * rep; ++z)
+      per += tiles_of(len, count, rep, p.unit_rows, z, causal, window, sinks).n;
+    total += per * c->kv_heads;
+    if (total >= (1LL << 31)) return fail(IQ_ERR_UNSUPPORTED, "too many queries and keys for one call");
+    p.per[e] = static_cast<int>(per);
+  }
+  if (p.entries == 0) return IQ_OK;
+  p.cum[p.entries] = p.total = static_cast<int>(total);
+  const long long pool_rows = static_cast<long long>(c->pages) * c->kv_heads * kPage;
+  if (!code_map(&p.k_map, c->k_codes, pool_rows) || !code_map(&p.v_map, c->v_codes, pool_rows))
+    return fail(IQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   p.k_scales = c->k_scales;
   p.v_scales = c->v_scales;
   p.table = c->table;
@@ -777,14 +622,17 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   p.window = window;
   p.sinks = sinks;
   p.scale = scale;
-  for (int i = 0; i < n_slots; ++i) {
-    p.slot[i] = slot_of(slots, i);
-    p.len[i] = c->lens[p.slot[i]];
-    p.count[i] = counts ? counts[i] : n_queries;
-  }
-  paged_attend_simple<<<dim3((n_queries + 7) / 8, q_heads, n_slots), 256, 0, cs>>>(p);
-  IQ_CUDA(cudaGetLastError());
-  return IQ_OK;
+  const int grid = static_cast<int>(std::min<long long>(num_sms(), total));
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * grid * p.unit_rows * kHeadDim);
+  cudaError_t err = p.unit_rows == 8    ? launch_split<8>(p, grid, cs)
+                    : p.unit_rows == 16 ? launch_split<16>(p, grid, cs)
+                    : p.unit_rows == 32 ? launch_split<32>(p, grid, cs)
+                    : p.unit_rows == 64 ? launch_split<64>(p, grid, cs)
+                                        : launch_prefill(p, grid, cs);
+  if (err == cudaSuccess && grid > 1)
+    err = launch_after<AttendParams, int>(paged_join_kernel, dim3(grid - 1, std::min(p.unit_rows, rows + 7) / 8), 256, 0, cs, p, grid);
+  return err == cudaSuccess ? IQ_OK : cuda_fail(err, "paged attention");
 }
 
 }  // extern "C"

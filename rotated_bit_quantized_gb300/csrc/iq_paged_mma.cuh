@@ -19,6 +19,138 @@ constexpr int kSlotBytes = 2 * kHalfBytes;    // a tile of keys or of values in 
 // kv head by half of the dims (64 x 128 bytes, 128-byte swizzle).
 bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows);
 
+// ------------------------------------------------------------------ work
+
+// The arguments of an attention launch.  A unit is (entry, kv head, tile of
+// unit_rows query rows); row r of an entry and kv head is query r / rep of head
+// r % rep.  The key tiles of all units, laid end to end, are cut into gridDim
+// ranges of equal length, one for each CTA; a unit that lies in one range is
+// stored at once, the others leave a partial result per range.
+struct AttendParams {
+  CUtensorMap k_map, v_map;
+  const float* k_scales;
+  const float* v_scales;
+  const int* table;
+  unsigned* status;
+  const uint16_t* q;
+  void* out;
+  float* part_o;    // [2 * grid][unit_rows][256] unnormalised partial results: a range's first segment, its last
+  float2* part_ml;  // [2 * grid][unit_rows] their references and sums
+  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, total;
+  float scale;
+  // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
+  // its queries; cum: tiles before it (all heads), per: tiles of one of its heads
+  short entry[IQ_MAX_BATCH], slot[IQ_MAX_BATCH];
+  int len[IQ_MAX_BATCH], count[IQ_MAX_BATCH], cum[IQ_MAX_BATCH + 1], per[IQ_MAX_BATCH];
+};
+
+// The key tiles of a unit: those of the sinks, then those of the window up to
+// its last row's position.  A unit that sees no key keeps one tile, all masked.
+struct Tiles {
+  int sinks, skip, n;  // tiles of the sinks; tiles between them and the window; all
+  int p_lo, p_hi;      // positions of the first and the last row
+  __host__ __device__ int tile(int j) const { return j < sinks ? j : j + skip; }
+};
+__host__ __device__ inline Tiles tiles_of(int len, int count, int rep, int unit_rows, int z, int causal, int window, int sinks) {
+  Tiles t;
+  const int rows = count * rep, r1 = z * unit_rows + unit_rows - 1;
+  t.p_lo = len - count + z * unit_rows / rep;
+  t.p_hi = len - count + (r1 < rows ? r1 : rows - 1) / rep;
+  const int stop = !causal ? len : t.p_hi < 0 ? 1 : t.p_hi + 1;
+  const int low = window > 0 && t.p_lo >= window ? t.p_lo - window + 1 : 0;  // where the first row's window begins
+  const int begin = low / kTile, reach = sinks < low ? sinks : low, n = (reach + kTile - 1) / kTile;
+  t.sinks = n < begin ? n : begin;
+  t.skip = n < begin ? begin - n : 0;
+  t.n = (stop + kTile - 1) / kTile - t.skip;
+  return t;
+}
+
+// The first tile of a range, and the range of a tile.
+__host__ __device__ inline int range_begin(int g, int grid, int total) {
+  return static_cast<int>(static_cast<long long>(g) * total / grid);
+}
+__host__ __device__ inline int range_of(int tile, int grid, int total) {
+  return static_cast<int>((static_cast<long long>(tile + 1) * grid - 1) / total);
+}
+
+// A place in the tiles of all units: entry, head, row tile, tile j of the unit.
+struct Place {
+  int e, h, z, j;
+};
+__device__ __forceinline__ Tiles tiles_at(const AttendParams& p, const Place& w) {
+  return tiles_of(p.len[w.e], p.count[w.e], p.rep, p.unit_rows, w.z, p.causal, p.window, p.sinks);
+}
+// Of tile t (a whole warp calls it together).
+__device__ inline Place place_of(const AttendParams& p, int t) {
+  Place w;
+  int hi = p.entries - 1;
+  w.e = 0;
+  while (w.e < hi) {
+    const int mid = (w.e + hi + 1) / 2;
+    if (p.cum[mid] <= t) w.e = mid;
+    else hi = mid - 1;
+  }
+  t -= p.cum[w.e];
+  w.h = t / p.per[w.e];
+  w.z = 0;
+  w.j = t % p.per[w.e];
+  const int units = (p.count[w.e] * p.rep + p.unit_rows - 1) / p.unit_rows;
+  if (units == 1) return w;
+  const int lane = threadIdx.x & 31;
+  for (int z0 = 0;; z0 += 32) {  // 32 row tiles at a time, their tiles summed up
+    const int z = z0 + lane;
+    int sum = 0;
+    if (z < units) sum = tiles_of(p.len[w.e], p.count[w.e], p.rep, p.unit_rows, z, p.causal, p.window, p.sinks).n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    const unsigned beyond = __ballot_sync(0xFFFFFFFFu, sum > w.j);
+    if (beyond) {
+      const int i = __ffs(beyond) - 1;
+      const int before = __shfl_sync(0xFFFFFFFFu, sum, i ? i - 1 : 0);
+      w.z = z0 + i;
+      w.j -= i ? before : 0;
+      return w;
+    }
+    w.j -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+    if (z0 + 32 >= units) return w;  // not reached: t is a tile of this head
+  }
+}
+// The unit after w's.
+__device__ __forceinline__ void next_unit(const AttendParams& p, Place& w) {
+  w.j = 0;
+  if (++w.z * p.unit_rows < p.count[w.e] * p.rep) return;
+  w.z = 0;
+  if (++w.h < p.heads) return;
+  w.h = 0;
+  ++w.e;
+}
+// The index of a unit's first row among the rows [entry][query head][query] of
+// q and out is (entry * heads + h) * rep * nq; row r of the unit:
+__device__ __forceinline__ long long row_index(const AttendParams& p, const Place& w, int r) {
+  return ((static_cast<long long>(p.entry[w.e]) * p.heads + w.h) * p.rep + r % p.rep) * p.nq + r / p.rep;
+}
+
+cudaError_t launch_prefill(const AttendParams& p, int grid, cudaStream_t stream);
+
+// A launch that may begin while the kernel before it ends (it waits itself).
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Waits end: after a second (no stage takes a thousandth of it) the CTA's
 // abort flag is raised, every later wait of the CTA returns at once, and the
 // kernel runs out with a status bit set.
@@ -172,6 +304,19 @@ __device__ __forceinline__ float clamp_finite(float x) { return fminf(fmaxf(x, -
 __device__ __forceinline__ void store_out(void* out, int out_f32, long long at, float x) {
   if (out_f32) static_cast<float*>(out)[at] = x;
   else static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(f32_to_bf16_bits(x));
+}
+
+__device__ __forceinline__ void store_out8(void* out, int out_f32, long long at, const float (&x)[8], float f) {
+  if (out_f32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    o[0] = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+    o[1] = make_float4(x[4] * f, x[5] * f, x[6] * f, x[7] * f);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_bits(x[2 * j] * f) | f32_to_bf16_bits(x[2 * j + 1] * f) << 16;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 }  // namespace paged
