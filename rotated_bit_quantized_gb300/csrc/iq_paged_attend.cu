@@ -121,9 +121,12 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
     bool ok = true;
     Place w = start;
     for (int at = first; at < last && ok; next_unit(p, w)) {
-      const int e = w.e, h = w.h, k0 = w.j;
+      const int e = w.e, h = w.h;
       const Tiles tiles = tiles_at(p, w);
-      const int n = min(tiles.n - k0, last - at);
+      const Part part = part_of(p, w, tiles.n, last - at);
+      const int k0 = part.begin, n = part.n;
+      at += tiles.n + p.cost - w.j;
+      if (n == 0) break;
       const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
       const int end_page = (p.len[e] + kPage - 1) / kPage - 1;
       // lanes fetch the ids of 16 tiles' pages at a time, one such piece ahead
@@ -163,7 +166,6 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         v0 = k0id;
         v1 = k1id;
       }
-      at += n;
     }
     if (lane == 0)  // no copy left in flight
       for (int s = 0; s < C::kSlots && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / C::kSlots);
@@ -175,7 +177,9 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       bool ok = true;
       Place w = start;
       for (int at = first; at < last && ok; ++segment, next_unit(p, w)) {
-        const int n = min(tiles_at(p, w).n - w.j, last - at);
+        const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
+        at += tiles + p.cost - w.j;
+        if (n == 0) break;
         ok = wait(q_ready, segment, kLostMma);
         for (int j = 0; j <= n && ok; ++j) {
           if (j < n) {
@@ -209,7 +213,6 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
           }
         }
         it += n;
-        at += n;
       }
       if (!ok) {  // given up: what is in flight ends before the tensor memory goes
         mma_commit(drained);
@@ -230,11 +233,14 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
     };
     Place at_unit = start;
     for (int at = first; at < last; next_unit(p, at_unit)) {
-      const int e = at_unit.e, h = at_unit.h, k0 = at_unit.j;
+      const int e = at_unit.e, h = at_unit.h;
       const Tiles tiles = tiles_at(p, at_unit);
-      const int n = min(tiles.n - k0, last - at), len = p.len[e], count = p.count[e], rows = count * p.rep;
+      const Part part = part_of(p, at_unit, tiles.n, last - at);
+      const int k0 = part.begin, n = part.n, len = p.len[e], count = p.count[e], rows = count * p.rep;
       const bool whole = n == tiles.n;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
+      at += tiles.n + p.cost - at_unit.j;
+      if (n == 0) break;
       // the query rows, a warp each
       for (int r = warp; r < NR; r += 4 * C::kGroups) {
         uint2 hi = make_uint2(0, 0), lo = hi;
@@ -353,6 +359,10 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         if (it >= 2) await(&o_done[b], it / 2 - 1);
         uint8_t* pb = smem + C::kP + b * C::kCols * 128;
         const float back = power2(-ev);
+        // where within a step of the low parts' least codes this key's weights are
+        // cut: another place for each key, so that many equal small weights are
+        // not all cut the same way (their sum would be off by up to half of it)
+        const float cut = (static_cast<float>((__brev(key) >> 25) + (it & 15) * 8 & 127) - 63.5f) * (1.0f / 128 / 512);
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
           const float a = ex2_approx(s[r] - ref[r0 + r]), c = ex2_approx(s[r + 1] - ref[r0 + r + 1]);
@@ -360,7 +370,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
           l[r + 1] = fmaf(c, back, l[r + 1]);
           const uint32_t hi = e4m3x2(a, c);
           const float2 f = f16x2_to_f32(e4m3x2_to_f16x2(hi));
-          const uint32_t lo = e4m3x2((a - f.x) * kPLo, (c - f.y) * kPLo);
+          const uint32_t lo = e4m3x2(fmaf(a - f.x, kPLo, cut), fmaf(c - f.y, kPLo, cut));
           pb[swizzled(r0 + r, key)] = static_cast<uint8_t>(hi);
           pb[swizzled(r0 + r + 1, key)] = static_cast<uint8_t>(hi >> 8);
           pb[swizzled(NR + r0 + r, key)] = static_cast<uint8_t>(lo);
@@ -407,7 +417,6 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       }
       tc_before();
       named_bar(3, 128 * C::kGroups);  // red, ref and the query buffer are free again
-      at += n;
     }
   }
   __syncthreads();
@@ -425,8 +434,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const int cut = range_begin(blockIdx.x + 1, grid, p.total);
   const Place w = place_of(p, cut);
   const int a = cut - w.j, n = tiles_at(p, w).n;
-  const int g0 = range_of(a, grid, p.total), g1 = range_of(a + n - 1, grid, p.total);
-  if (w.j == 0 || g0 != static_cast<int>(blockIdx.x)) return;
+  const int g0 = range_of(a + p.cost, grid, p.total), g1 = range_of(a + p.cost + n - 1, grid, p.total);
+  if (w.j <= p.cost || g0 != static_cast<int>(blockIdx.x)) return;
   const int x = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, r = w.z * p.unit_rows + x;
   if (x >= p.unit_rows || r >= p.count[w.e] * p.rep) return;
   auto row = [&](int g) {
@@ -584,6 +593,17 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.unit_rows = unit_rows(rows);
+  long long tiles = 0;
+  for (int i = 0; i < n_slots; ++i) {
+    const int len = c->lens[slot_of(slots, i)], count = counts ? counts[i] : n_queries;
+    if (len > 0)
+      for (int z = 0; static_cast<long long>(z) * p.unit_rows < static_cast<long long>(count) * rep; ++z)
+        tiles += static_cast<long long>(tiles_of(len, count, rep, p.unit_rows, z, causal, window, sinks).n) * c->kv_heads;
+  }
+  const int grid = static_cast<int>(std::min<long long>(num_sms(), tiles));
+  if (grid == 0) return IQ_OK;
+  // short ranges are left at a tile's grain
+  p.cost = tiles >= 8ll * grid ? 1 : 0;
   long long total = 0;
   for (int i = 0; i < n_slots; ++i) {
     const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
@@ -596,12 +616,11 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
     p.cum[e] = static_cast<int>(total);
     long long per = 0;
     for (int z = 0; static_cast<long long>(z) * p.unit_rows < static_cast<long long>(count) * rep; ++z)
-      per += tiles_of(len, count, rep, p.unit_rows, z, causal, window, sinks).n;
+      per += tiles_of(len, count, rep, p.unit_rows, z, causal, window, sinks).n + p.cost;
     total += per * c->kv_heads;
     if (total >= (1LL << 31)) return fail(IQ_ERR_UNSUPPORTED, "too many queries and keys for one call");
     p.per[e] = static_cast<int>(per);
   }
-  if (p.entries == 0) return IQ_OK;
   p.cum[p.entries] = p.total = static_cast<int>(total);
   const long long pool_rows = static_cast<long long>(c->pages) * c->kv_heads * kPage;
   if (!code_map(&p.k_map, c->k_codes, pool_rows) || !code_map(&p.v_map, c->v_codes, pool_rows))
@@ -622,7 +641,6 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   p.window = window;
   p.sinks = sinks;
   p.scale = scale;
-  const int grid = static_cast<int>(std::min<long long>(num_sms(), total));
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * grid * p.unit_rows * kHeadDim);
   cudaError_t err = p.unit_rows == 8    ? launch_split<8>(p, grid, cs)

@@ -36,10 +36,10 @@ struct AttendParams {
   void* out;
   float* part_o;    // [2 * grid][unit_rows][256] unnormalised partial results: a range's first segment, its last
   float2* part_ml;  // [2 * grid][unit_rows] their references and sums
-  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, total;
+  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, cost, total;
   float scale;
   // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
-  // its queries; cum: tiles before it (all heads), per: tiles of one of its heads
+  // its queries; cum: slots before it (all heads), per: slots of one of its heads
   short entry[IQ_MAX_BATCH], slot[IQ_MAX_BATCH];
   int len[IQ_MAX_BATCH], count[IQ_MAX_BATCH], cum[IQ_MAX_BATCH + 1], per[IQ_MAX_BATCH];
 };
@@ -65,7 +65,7 @@ __host__ __device__ inline Tiles tiles_of(int len, int count, int rep, int unit_
   return t;
 }
 
-// The first tile of a range, and the range of a tile.
+// The first slot of a range, and the range of a slot.
 __host__ __device__ inline int range_begin(int g, int grid, int total) {
   return static_cast<int>(static_cast<long long>(g) * total / grid);
 }
@@ -73,14 +73,23 @@ __host__ __device__ inline int range_of(int tile, int grid, int total) {
   return static_cast<int>((static_cast<long long>(tile + 1) * grid - 1) / total);
 }
 
-// A place in the tiles of all units: entry, head, row tile, tile j of the unit.
+// A place in the slots of all units: entry, head, row tile, slot j of the unit.
 struct Place {
   int e, h, z, j;
 };
+// The tiles of a unit that a range takes from slot w.j on, `left` slots of the
+// range being left: [begin, begin + n), none where it ends in the unit's empty slots.
+struct Part {
+  int begin, n;
+};
+__device__ __forceinline__ Part part_of(const AttendParams& p, const Place& w, int tiles, int left) {
+  const int begin = max(w.j - p.cost, 0), end = min(max(w.j + left - p.cost, 0), tiles);
+  return {begin, end - begin};
+}
 __device__ __forceinline__ Tiles tiles_at(const AttendParams& p, const Place& w) {
   return tiles_of(p.len[w.e], p.count[w.e], p.rep, p.unit_rows, w.z, p.causal, p.window, p.sinks);
 }
-// Of tile t (a whole warp calls it together).
+// Of slot t (a whole warp calls it together).
 __device__ inline Place place_of(const AttendParams& p, int t) {
   Place w;
   int hi = p.entries - 1;
@@ -97,10 +106,10 @@ __device__ inline Place place_of(const AttendParams& p, int t) {
   const int units = (p.count[w.e] * p.rep + p.unit_rows - 1) / p.unit_rows;
   if (units == 1) return w;
   const int lane = threadIdx.x & 31;
-  for (int z0 = 0;; z0 += 32) {  // 32 row tiles at a time, their tiles summed up
+  for (int z0 = 0;; z0 += 32) {  // 32 row tiles at a time, their slots summed up
     const int z = z0 + lane;
     int sum = 0;
-    if (z < units) sum = tiles_of(p.len[w.e], p.count[w.e], p.rep, p.unit_rows, z, p.causal, p.window, p.sinks).n;
+    if (z < units) sum = tiles_of(p.len[w.e], p.count[w.e], p.rep, p.unit_rows, z, p.causal, p.window, p.sinks).n + p.cost;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
@@ -115,7 +124,7 @@ __device__ inline Place place_of(const AttendParams& p, int t) {
       return w;
     }
     w.j -= __shfl_sync(0xFFFFFFFFu, sum, 31);
-    if (z0 + 32 >= units) return w;  // not reached: t is a tile of this head
+    if (z0 + 32 >= units) return w;  // not reached: t is a slot of this head
   }
 }
 // The unit after w's.
@@ -162,7 +171,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
 struct Waits {
   volatile int* abort;  // shared memory
   unsigned* status;
-  __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity, unsigned bit) const {
+  __device__ __forceinline__ bool slow(uint64_t* bar, uint32_t parity, unsigned bit) const {
     const unsigned long long t0 = now_ns();
     for (;;) {
       if (mbar_try_wait(bar, parity, 20000u)) return true;
@@ -261,6 +270,12 @@ __device__ __forceinline__ void tmem_st<16>(uint32_t addr, const float* v) {
       "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
       "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
+}
+
+template <>
+__device__ __forceinline__ void tmem_st<32>(uint32_t addr, const float* v) {
+  tmem_st<16>(addr, v);
+  tmem_st<16>(addr + 16, v + 16);
 }
 
 // Byte offset of byte `c` of row `r` in a 128-byte-swizzled block of 128-byte rows.

@@ -10,10 +10,12 @@
 // part) at e4m3's rate, twice bf16's, so the bound is bf16's rate; no code is
 // ever converted.
 //
-// Rounding.  A weight's two parts leave at most 2^-8 of it, and 2^-10 below
-// e4m3's range: a row's reference puts its running maximum at 2^5 and moves
-// when a weight would pass 2^8.75 (448 is the largest code), so that floor is
-// 2^-15 of the largest weight or less.
+// Rounding.  A weight, as fp16 at first (2^-11 of it), leaves at most 2^-8 of it
+// behind its two parts, and a step of the least codes, 2^-9, below e4m3's range:
+// a row's reference puts its running maximum at 2^5 and moves when a weight
+// would pass 2^8.75 (448 is the largest code), so that floor is 2^-14 of the
+// largest weight or less.  Where within such a step a weight is cut differs from
+// key to key, so what many small weights lose does not add up.
 #include <cuda_runtime.h>
 
 #include "iq_paged_mma.cuh"
@@ -26,11 +28,11 @@ constexpr int kRows = 128;
 constexpr int kSlots = 5;                         // tiles of keys or values in flight
 constexpr int kQ = kSlots * kSlotBytes;           // [high, low][2 halves of the dims][128 rows][128 bytes]
 constexpr int kMisc = kQ + 4 * kHalfBytes;
-constexpr int kSmem = 1024 + kMisc + 3 * kRows * 4 + 32 * 8;
-constexpr int kThreads = 320;
-constexpr int kLoader = 8, kIssuer = 9;
-constexpr float kPlace = 5.0f, kTop = 8.75f;      // the running maximum's place, and how far a weight may grow
-constexpr float kUnset = -1e30f, kDead = 1e30f;
+constexpr int kSmem = kMisc + 4 * kRows * 4 + 32 * 8;
+constexpr int kThreads = 512;
+constexpr int kAsker = 8, kLoader = 12, kIssuer = 13;
+constexpr int kRowRegs = 136, kAskRegs = 168, kRestRegs = 72;  // 2 * 136 + 168 + 72 = 4 * 128, what the CTA is launched with
+constexpr float kPlace = 5.0f, kTop = 8.75f;      // the running maximum's place, and how far a weight may grow (448 = 2^8.8)
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
@@ -55,33 +57,78 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// One persistent CTA per SM.  Warps 0-7: two threads per query row (warp w
-// reaches tensor-memory lanes 32 (w % 4) ..), each with the 64 keys of one
-// page of a tile; warps w and w + 4 hold the same rows and settle the rows'
-// references between themselves.  Then one warp streams the pages and one
-// issues the products, S of the next tile but one behind O of this tile.
+// Where within a step of e4m3's least codes (2^-9) the weights of keys c and
+// c + 1 of a page are cut, as an fp16 pair: a place of its own for each key
+// (bits reversed), so that many equal small weights are not all cut the same
+// way; each stays below half a step, so that a weight of 0 stays 0.
+__host__ __device__ constexpr uint32_t half_bits(int x) {  // x * 2^-16 as fp16, 0 < |x| < 128
+  const int m = x < 0 ? -x : x;
+  int top = 0;
+  while ((m >> top) > 1) ++top;
+  // 2^(top - 16) is an fp16 subnormal (units of 2^-24) below 2^-14
+  return (x < 0 ? 0x8000u : 0u) |
+         (top < 2 ? static_cast<uint32_t>(m << 8) : static_cast<uint32_t>(top - 1) << 10 | (static_cast<uint32_t>(m << (10 - top)) & 0x3FFu));
+}
+__host__ __device__ constexpr int reversed6(int c) {
+  return (c & 1) << 5 | (c & 2) << 3 | (c & 4) << 1 | (c & 8) >> 1 | (c & 16) >> 3 | (c & 32) >> 5;
+}
+__host__ __device__ constexpr uint32_t cut_at(int c) {  // (reversed / 64 - 63 / 128) steps
+  return half_bits(2 * reversed6(c) - 63) | half_bits(2 * reversed6(c + 1) - 63) << 16;
+}
+
+// Four 16-byte pieces per lane, transposed among groups of four lanes: piece k
+// of lane i becomes piece i of lane k.
+__device__ __forceinline__ void transpose4(uint32_t (&c)[16], int lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & d) continue;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t mine = lane & d ? c[4 * k + x] : c[4 * (k + d) + x];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, mine, d);
+        if (lane & d) c[4 * k + x] = got;
+        else c[4 * (k + d) + x] = got;
+      }
+    }
+}
+
+// One persistent CTA per SM, four warpgroups.  Warps 0-7: two threads per query
+// row (warp w reaches tensor-memory lanes 32 (w % 4) ..), each with the 64 keys
+// of one page of a tile; warps w and w + 4 hold the same rows and settle the
+// rows' references between themselves.  Warps 8-11 hold the next unit's queries
+// in registers until this unit's last scores are done.  Then one warp streams
+// the pages and one issues the products, S of the next tile but one behind O
+// of this tile.  A unit's results are stored after the next unit's first
+// weights are written, so the products wait for the stores alone.
 __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid_constant__ AttendParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled operands need it; no room to align by hand
   const uint32_t sbase = smem_u32(smem);
-  float* factor = reinterpret_cast<float*>(smem + kMisc);  // [128] 2^eq * scale * log2 e
-  float* xch = factor + kRows;                             // [2][128] what the two threads of a row exchange
+  if (sbase & 1023u) {  // (the kernel has no other shared memory in front)
+    if (threadIdx.x == 0) atomicOr(p.status, kLostMma);
+    return;
+  }
+  float* factor = reinterpret_cast<float*>(smem + kMisc);  // [2][128] 2^eq * scale * log2 e, by the segment's parity
+  float* xch = factor + 2 * kRows;                         // [2][128] what the two threads of a row exchange
   uint64_t* full = reinterpret_cast<uint64_t*>(xch + 2 * kRows);
   uint64_t* empty = full + kSlots;
   uint64_t* s_full = empty + kSlots;   // [2] scores of a tile in tensor memory
   uint64_t* p_ready = s_full + 2;      // [2] weights of a tile in their place
   uint64_t* o_done = p_ready + 2;      // [2] and multiplied with its values
-  uint64_t* q_ready = o_done + 2;
-  uint64_t* drained = q_ready + 1;
+  uint64_t* q_ready = o_done + 2;      // [2] a segment's queries and factors written, by its parity: the
+                                       // issuer may be a segment ahead of the softmax
+  uint64_t* q_free = q_ready + 2;      // a segment's last scores done
+  uint64_t* drained = q_free + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  static_assert(2 * kSlots + 8 < 31, "the barriers and the two words behind them fit");
+  static_assert(2 * kSlots + 10 < 31, "the barriers and the two words behind them fit");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -93,8 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       mbar_init(&s_full[s], 1);
       mbar_init(&p_ready[s], 8);
       mbar_init(&o_done[s], 1);
+      mbar_init(&q_ready[s], 4);
     }
-    mbar_init(q_ready, 8);
+    mbar_init(q_free, 1);
     mbar_init(drained, 1);
     *abort = 0;
     mbar_fence_init();
@@ -114,7 +162,247 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
   const int first = range_begin(blockIdx.x, gridDim.x, p.total), last = range_begin(blockIdx.x + 1, gridDim.x, p.total);
   const Place start = place_of(p, first);
 
-  if (warp == kLoader) {
+  if (warp < kAsker) {
+    // ---------------------------------------------------------------- softmax: half a row per thread
+    setmaxnreg_inc<kRowRegs>();
+    const int group = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    int it = 0, segment = 0;
+    bool ok = true;
+    auto await = [&](uint64_t* bar, uint32_t phase) {  // a lost wait changes no path: every barrier below is still reached
+      if (ok) ok = wait(bar, phase, kLostRows);
+      __syncwarp();
+    };
+    // the unit whose results are still in tensor memory
+    Place done{};
+    bool pending = false, done_whole = false;
+    int done_slot = 0;
+    float done_l = 0.0f, done_ref = 0.0f;
+    auto store_results = [&](int last_tile) {  // the sums of a row's two halves, half of its dims per thread
+      xch[group * kRows + r] = done_l;
+      named_bar(1 + quad, 64);
+      const float sum = done_l + xch[(group ^ 1) * kRows + r];
+      named_bar(1 + quad, 64);
+      const int rows = min(kRows, p.count[done.e] * p.rep - done.z * kRows);
+      const float inv = !done_whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      const bool wide = !done_whole || p.out_f32;
+      uint8_t* base = static_cast<uint8_t*>(done_whole ? p.out : p.part_o) + ((lane & 3) * 16 + group * (wide ? 512 : 256));
+      long long to[4];  // the rows that this lane stores pieces of
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = (r & ~3) + k;
+        to[k] = (done_whole ? row_index(p, done, min(done.z * kRows + x, p.count[done.e] * p.rep - 1))
+                            : static_cast<long long>(done_slot) * kRows + x) *
+                (wide ? 1024 : 512);
+      }
+      await(&o_done[last_tile & 1], last_tile / 2);
+      tc_after();
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        float o[32];
+        tmem_ld<32>(t_o + lanes + group * 128 + c, o);
+        ld_wait();
+        uint32_t x[16];
+        if (wide) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[half * 16 + i] * inv);
+            transpose4(x, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if ((r & ~3) + k < rows)
+                *reinterpret_cast<uint4*>(base + to[k] + (c + half * 16) * 4) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(o[2 * i + 1] * inv), "f"(o[2 * i] * inv));
+          transpose4(x, lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((r & ~3) + k < rows)
+              *reinterpret_cast<uint4*>(base + to[k] + c * 2) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        }
+      }
+      if (!done_whole && r < rows && group == 0) p.part_ml[done_slot * kRows + r] = make_float2(done_ref, sum);
+    };
+    Place w = start;
+    for (int at = first; at < last; ++segment, next_unit(p, w)) {
+      const Tiles tiles = tiles_at(p, w);
+      const Part part = part_of(p, w, tiles.n, last - at);
+      const int e = w.e, k0 = part.begin, n = part.n, len = p.len[e];
+      const bool whole = n == tiles.n, exists = w.z * kRows + r < p.count[e] * p.rep;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
+      at += tiles.n + p.cost - w.j;
+      if (n == 0) break;
+      const int pos = len - p.count[e] + (w.z * kRows + r) / p.rep;
+      const int stop = !exists ? 0 : p.causal ? pos + 1 : len;
+      const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+      // a row that has seen no key yet has no reference (its weights are relative to 2^0)
+      bool unset = exists;
+      float ref = exists ? 0.0f : 1e30f, l = 0.0f;
+
+      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
+      const int end_page = (len + kPage - 1) / kPage - 1;
+      // this thread's page of tile j: ids two tiles ahead, scales one
+      auto id_of = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j, n - 1)) + group, end_page)); };
+      auto scales_of = [&](int id) {
+        const long long i = static_cast<long long>(page_in_pool(id, p.pages, p.status)) * p.heads + w.h;
+        return make_float2(__ldcg(p.k_scales + i), __ldcg(p.v_scales + i));
+      };
+      int id = id_of(1);
+      float2 sc = scales_of(id_of(0));
+      await(&q_ready[segment & 1], segment / 2);
+      const float fq = factor[(segment & 1) * kRows + r];
+      for (int j = 0; j < n; ++j, ++it) {
+        const int b = it & 1;
+        const float f = clamp_finite(fq * sc.x);
+        const int ev = exponent_of(sc.y);
+        sc = scales_of(id);
+        id = id_of(j + 2);
+        const int t0 = tiles.tile(k0 + j) * kTile;
+        // whether some row of the unit does not see the whole tile
+        const bool masked = t0 + kTile > (p.causal ? tiles.p_lo + 1 : len) ||
+                            (p.window > 0 && t0 <= tiles.p_hi - p.window && t0 + kTile > p.sinks);
+        const uint32_t t_s = tmem + lanes + b * 128 + group * 64;
+        await(&s_full[b], it / 2);
+        tc_after();
+        float s[64];
+        tmem_ld<32>(t_s, s);
+        tmem_ld<32>(t_s + 32, s + 32);
+        ld_wait();
+        const float shift = static_cast<float>(ev) - ref;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i] = fmaf(s[i], f, shift);
+        if (masked) {
+          const int tb = t0 + group * 64;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (!(tb + i < stop && (tb + i >= low || tb + i < p.sinks))) s[i] = -__builtin_huge_valf();
+        }
+        float m = s[0];
+#pragma unroll
+        for (int i = 1; i < 63; i += 2) m = fmaxf(fmaxf(m, s[i]), s[i + 1]);
+        m = fmaxf(m, s[63]);
+        int far = m > kTop || (unset && m > -1e38f);
+        asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
+                     : "+r"(far)
+                     : "r"(1 + quad)
+                     : "memory");
+        if (far) {
+          // some row of the quad passed its reference: move such rows' references
+          // so that their maxima land at 2^kPlace, and what was summed with them
+          xch[group * kRows + r] = m;
+          named_bar(1 + quad, 64);
+          m = fmaxf(m, xch[(group ^ 1) * kRows + r]);
+          named_bar(1 + quad, 64);
+          float move = 0.0f;
+          if (m > kTop || (unset && m > -1e38f)) move = m - kPlace;
+          ref += move;
+          unset = unset && !(m > -1e38f);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] -= move;
+          if (j > 0) {  // this thread's half of the row's results
+            const float change = ex2_approx(-move);
+            l *= change;
+            await(&o_done[b ^ 1], (it - 1) / 2);
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              float o[32];
+              tmem_ld<32>(t_o + lanes + group * 128 + c, o);
+              ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= change;
+              tmem_st<32>(t_o + lanes + group * 128 + c, o);
+            }
+            st_wait();
+          }
+        }
+        // the weights; as fp16 pairs (11 bits), cut into two parts of 4 bits, over
+        // the scores that this thread has read
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t ha, hb;
+            {
+              const int c = 32 * x + 4 * i;
+              const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]), w2 = ex2_approx(s[c + 2]), w3 = ex2_approx(s[c + 3]);
+              s0 += w0;
+              s1 += w1;
+              s0 += w2;
+              s1 += w3;
+              ha = f16x2(w0, w1);
+              hb = f16x2(w2, w3);
+            }
+            const uint32_t a = e4m3x2_of_f16x2(ha), d = e4m3x2_of_f16x2(hb);
+            hi[i] = a | d << 16;
+            lo[i] = e4m3x2_of_f16x2(add_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a)), cut_at(32 * x + 4 * i))) |
+                    e4m3x2_of_f16x2(add_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d)), cut_at(32 * x + 4 * i + 2))) << 16;
+          }
+          tmem_st<8>(t_s + 8 * x, reinterpret_cast<const float*>(hi));
+          tmem_st<8>(t_s + 16 + 8 * x, reinterpret_cast<const float*>(lo));
+        }
+        l = fmaf(s0 + s1, power2(-ev), l);
+        st_wait();
+        if (j == 0 && pending) store_results(it - 1);
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[b]);
+      }
+      pending = true;
+      done = w;
+      done_whole = whole;
+      done_slot = slot;
+      done_l = l;
+      done_ref = unset ? -1e30f : ref;
+    }
+    if (pending) store_results(it - 1);
+  } else if (warp < kLoader) {
+    // ---------------------------------------------------------------- queries: 32 rows per warp
+    setmaxnreg_inc<kAskRegs>();
+    int segment = 0;
+    Place w = start;
+    for (int at = first; at < last; ++segment, next_unit(p, w)) {
+      const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
+      at += tiles + p.cost - w.j;
+      if (n == 0) break;
+      const int x0 = (warp - kAsker) * 32, rows = p.count[w.e] * p.rep - w.z * kRows;
+      uint2 hi[32], lo[32];
+      float f = 0.0f;  // of row x0 + lane
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        uint4 raw[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          raw[k] = make_uint4(0, 0, 0, 0);
+          if (x0 + i + k < rows)
+            raw[k] = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, w, w.z * kRows + x0 + i + k) * kHeadDim) + lane);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float g = split_query<1>(raw[k], hi[i + k], lo[i + k]);
+          if (lane == i + k) f = g;
+        }
+      }
+      if (segment > 0 && !__all_sync(0xFFFFFFFFu, wait(q_free, segment - 1, kLostRows))) break;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        uint8_t* to = smem + kQ + (lane >> 4) * kHalfBytes + swizzled(x0 + i, (lane & 15) * 8);
+        *reinterpret_cast<uint2*>(to) = hi[i];
+        *reinterpret_cast<uint2*>(to + 2 * kHalfBytes) = lo[i];
+      }
+      factor[(segment & 1) * kRows + x0 + lane] = clamp_finite(f * (p.scale * kLog2e));
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready[segment & 1]);
+    }
+  } else {
+    setmaxnreg_dec<kRestRegs>();
+    if (warp == kLoader) {
     // ---------------------------------------------------------------- pages to shared memory
     uint64_t pol;  // other row tiles read the same pages
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
@@ -122,9 +410,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
     bool ok = true;
     Place w = start;
     for (int at = first; at < last && ok; next_unit(p, w)) {
-      const int e = w.e, h = w.h, k0 = w.j;
+      const int e = w.e, h = w.h;
       const Tiles tiles = tiles_at(p, w);
-      const int n = min(tiles.n - k0, last - at);
+      const Part part = part_of(p, w, tiles.n, last - at);
+      const int k0 = part.begin, n = part.n;
+      at += tiles.n + p.cost - w.j;
+      if (n == 0) break;
       const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
       const int end_page = (p.len[e] + kPage - 1) / kPage - 1;
       // lanes fetch the ids of 16 tiles' pages at a time, one such piece ahead
@@ -164,11 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
         v0 = k0id;
         v1 = k1id;
       }
-      at += n;
     }
     if (lane == 0)  // no copy left in flight
       for (int s = 0; s < kSlots && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / kSlots);
-  } else if (warp == kIssuer) {
+    } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- products
     if (lane == 0) {
       constexpr uint32_t kS = shape(128, kTile, false, false), kO = shape(128, kHeadDim, false, true);
@@ -189,10 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       };
       Place w = start;
       for (int at = first; at < last && ok; ++segment, next_unit(p, w)) {
-        const int n = min(tiles_at(p, w).n - w.j, last - at);
-        ok = wait(q_ready, segment, kLostMma);
+        const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
+        at += tiles + p.cost - w.j;
+        if (n == 0) break;
+        ok = wait(&q_ready[segment & 1], segment / 2, kLostMma);
         if (ok) scores(0);
         if (ok && n > 1) scores(1);
+        if (ok && n <= 2) mma_commit(q_free);
         for (int j = 0; j < n && ok; ++j) {
           const int b = (it + j) & 1, s = used % kSlots;
           ok = wait(&p_ready[b], (it + j) / 2, kLostMma) && wait(&full[s], used / kSlots, kLostMma);
@@ -205,10 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           mma_commit(&o_done[b]);
           mma_commit(&empty[s]);
           ++used;
-          if (j + 2 < n) scores(j + 2);  // runs behind O of this tile, whose weights it overwrites
+          if (j + 2 < n) {
+            scores(j + 2);  // runs behind O of this tile, whose weights it overwrites
+            if (ok && j + 3 == n) mma_commit(q_free);
+          }
         }
         it += n;
-        at += n;
       }
       if (!ok) {  // given up: what is in flight ends before the tensor memory goes
         mma_commit(drained);
@@ -216,215 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       }
     }
     __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- softmax: half a row per thread
-    const int group = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    int it = 0;
-    bool ok = true;
-    auto await = [&](uint64_t* bar, uint32_t phase) {  // a lost wait changes no path: every barrier below is still reached
-      if (ok) ok = wait(bar, phase, kLostRows);
-      __syncwarp();
-    };
-    // a unit's queries into the operand buffer, 16 of the quad's 32 rows per warp
-    auto put_queries = [&](const Place& w) {
-      const int rows = min(kRows, p.count[w.e] * p.rep - w.z * kRows);
-#pragma unroll 1
-      for (int i = 0; i < 16; i += 8) {
-        uint4 raw[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int x = quad * 32 + group * 16 + i + k;
-          raw[k] = make_uint4(0, 0, 0, 0);
-          if (x < rows) raw[k] = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, w, w.z * kRows + x) * kHeadDim) + lane);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int x = quad * 32 + group * 16 + i + k;
-          uint2 hi, lo;
-          const float f = split_query<1>(raw[k], hi, lo);
-          uint8_t* to = smem + kQ + (lane >> 4) * kHalfBytes + swizzled(x, (lane & 15) * 8);
-          *reinterpret_cast<uint2*>(to) = hi;
-          *reinterpret_cast<uint2*>(to + 2 * kHalfBytes) = lo;
-          if (lane == 0) factor[x] = clamp_finite(f * (p.scale * kLog2e));
-        }
-      }
-      proxy_fence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
-      named_bar(1 + quad, 64);  // the quad's factors
-    };
-    Place w = start;
-    put_queries(w);
-    for (int at = first; at < last;) {
-      const Tiles tiles = tiles_at(p, w);
-      const int e = w.e, k0 = w.j, n = min(tiles.n - k0, last - at), len = p.len[e];
-      const bool whole = n == tiles.n, exists = w.z * kRows + r < p.count[e] * p.rep;
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
-      const float fq = factor[r];
-      const int x = len - p.count[e] + (w.z * kRows + r) / p.rep;  // the row's position
-      const int stop = !exists ? 0 : p.causal ? x + 1 : len;
-      const int low = p.window > 0 && x >= p.window ? x - p.window + 1 : 0;
-      float ref = exists ? kUnset : kDead, l = 0.0f;
-
-      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
-      const int end_page = (len + kPage - 1) / kPage - 1;
-      // this thread's page of tile j: ids two tiles ahead, scales one
-      auto id_of = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j, n - 1)) + group, end_page)); };
-      auto scales_of = [&](int id) {
-        const long long i = static_cast<long long>(page_in_pool(id, p.pages, p.status)) * p.heads + w.h;
-        return make_float2(__ldcg(p.k_scales + i), __ldcg(p.v_scales + i));
-      };
-      int id = id_of(1);
-      float2 sc = scales_of(id_of(0));
-      for (int j = 0; j < n; ++j, ++it) {
-        const int b = it & 1;
-        const float f = clamp_finite(fq * sc.x);
-        const int ev = exponent_of(sc.y);
-        sc = scales_of(id);
-        id = id_of(j + 2);
-        const int t0 = tiles.tile(k0 + j) * kTile, tb = t0 + group * 64;  // the tile's, this thread's first key
-        // whether some row of the unit does not see the whole tile
-        const bool masked = t0 + kTile > (p.causal ? tiles.p_lo + 1 : len) ||
-                            (p.window > 0 && t0 <= tiles.p_hi - p.window && t0 + kTile > p.sinks);
-        const uint32_t t_s = tmem + lanes + b * 128 + group * 64;
-        await(&s_full[b], it / 2);
-        tc_after();
-        uint32_t h[32];  // the weights as fp16 pairs: 11 bits, to be cut into two parts of 4
-        float sum;
-        auto weights = [&]() {  // returns the largest exponent, for the references, only where asked: see below
-          const float shift = static_cast<float>(ev) - ref;
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            float s[32];
-            tmem_ld<32>(t_s + c, s);
-            ld_wait();
-            if (masked) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int t = tb + c + i;
-                if (!(t < stop && (t >= low || t < p.sinks))) s[i] = -__builtin_huge_valf();
-                else s[i] = fmaf(s[i], f, shift);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = fmaf(s[i], f, shift);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float a = ex2_approx(s[i]), d = ex2_approx(s[i + 1]);
-              s0 += a;
-              s1 += d;
-              h[(c + i) / 2] = f16x2(a, d);
-            }
-          }
-          sum = s0 + s1;
-          uint32_t m = h[0];
-#pragma unroll
-          for (int i = 1; i < 32; ++i) m = max_f16x2(m, h[i]);
-          const float2 mm = f16x2_to_f32(m);
-          return fmaxf(mm.x, mm.y);
-        };
-        int far = weights() > 430.0f;  // 2^8.75: e4m3 ends at 448
-        asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
-                     : "+r"(far)
-                     : "r"(1 + quad)
-                     : "memory");
-        if (far) {
-          // some row of the quad passed its reference: the rows' maxima in log2
-          // units, the references moved so that they land at 2^kPlace, and what
-          // was summed with the old ones
-          float m = -__builtin_huge_valf();
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            float s[32];
-            tmem_ld<32>(t_s + c, s);
-            ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int t = tb + c + i;
-              if (t < stop && (t >= low || t < p.sinks)) m = fmaxf(m, fmaf(s[i], f, static_cast<float>(ev)));
-            }
-          }
-          xch[group * kRows + r] = m;
-          named_bar(1 + quad, 64);
-          m = fmaxf(m, xch[(group ^ 1) * kRows + r]);
-          named_bar(1 + quad, 64);
-          float change = 1.0f;
-          if (m - ref > kTop - 0.01f) {
-            change = ex2_approx(ref - (m - kPlace));
-            ref = m - kPlace;
-            l *= change;
-          }
-          if (j > 0) {  // this thread's half of the row's results
-            await(&o_done[b ^ 1], (it - 1) / 2);
-            tc_after();
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-              float o[16];
-              tmem_ld<16>(t_o + lanes + group * 128 + c, o);
-              ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= change;
-              tmem_st<16>(t_o + lanes + group * 128 + c, o);
-            }
-            st_wait();
-          }
-          weights();
-        }
-        l = fmaf(sum, power2(-ev), l);
-        // the two parts, over the scores that this thread has read
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t a = e4m3x2_of_f16x2(h[2 * i]), d = e4m3x2_of_f16x2(h[2 * i + 1]);
-          hi[i] = a | d << 16;
-          lo[i] = e4m3x2_of_f16x2(sub_f16x2(h[2 * i], e4m3x2_to_f16x2(a))) |
-                  e4m3x2_of_f16x2(sub_f16x2(h[2 * i + 1], e4m3x2_to_f16x2(d))) << 16;
-        }
-        tmem_st<16>(t_s, reinterpret_cast<const float*>(hi));
-        tmem_st<16>(t_s + 16, reinterpret_cast<const float*>(lo));
-        st_wait();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[b]);
-      }
-      at += n;
-      // the next unit's queries, while the last product runs (its scores are done with these)
-      Place next = w;
-      next_unit(p, next);
-      if (at < last) put_queries(next);
-      // ---- the results: the sums of a row's two halves, half of its dims per thread
-      xch[group * kRows + r] = l;
-      named_bar(1 + quad, 64);
-      const float total = l + xch[(group ^ 1) * kRows + r];
-      named_bar(1 + quad, 64);
-      await(&o_done[(it - 1) & 1], (it - 1) / 2);
-      tc_after();
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-      const long long to = whole ? row_index(p, w, w.z * kRows + r) * kHeadDim + group * 128
-                                 : (static_cast<long long>(slot) * kRows + r) * kHeadDim + group * 128;
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 16) {
-        float o[16];
-        tmem_ld<16>(t_o + lanes + group * 128 + c, o);
-        ld_wait();
-        if (exists) {
-          const float(&o0)[8] = *reinterpret_cast<const float(*)[8]>(o);
-          const float(&o1)[8] = *reinterpret_cast<const float(*)[8]>(o + 8);
-          if (whole) {
-            store_out8(p.out, p.out_f32, to + c, o0, inv);
-            store_out8(p.out, p.out_f32, to + c + 8, o1, inv);
-          } else {
-            store_out8(p.part_o, 1, to + c, o0, 1.0f);
-            store_out8(p.part_o, 1, to + c + 8, o1, 1.0f);
-          }
-        }
-      }
-      if (!whole && exists && group == 0) p.part_ml[slot * kRows + r] = make_float2(ref, total);
-      tc_before();
-      w = next;
     }
   }
   __syncthreads();

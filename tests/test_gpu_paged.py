@@ -53,11 +53,13 @@ def put(c, o, k, v, slots=None, counts=None):
 
 
 def bounds(res, out_f32):
-    """How far a result may be off: every weight p 2^e is held in two e4m3 parts (half a step twice: 2^-8 of it,
-    and at the least code 2^-15 of the largest); a query element in two parts too (exact, but 2^-17 of the row's
-    largest at the least code); sums of 256 products in fp32 (2^-16 of the sum of magnitudes); exp and the rest 2^-13."""
+    """How far a result may be off: every weight p 2^e is held in two e4m3 parts (half a step twice: 2^-8 of it),
+    cut from its fp16 form (half a step: 2^-11); a query element in two parts too (exact, but 2^-17 of the row's
+    largest at the least code); sums of 256 products in fp32 (2^-16 of the sum of magnitudes); exp and the rest 2^-13.
+    At the least codes a weight is off by half a step, and by half a step for the place where it is cut: 2^-9 in all,
+    and the row's largest weight is at 2^5 or above then, so 2^-14 of that one."""
     out, weight, floor, slack = res
-    tol = (2.0**-8 + 2 * (2.0**-17 + 2.0**-16) * slack + 2.0**-13) * weight + 2.0**-15 * floor + 1e-30
+    tol = (2.0**-8 + 2.0**-11 + 2 * (2.0**-17 + 2.0**-16) * slack + 2.0**-13) * weight + 2.0**-14 * floor + 1e-30
     return tol if out_f32 else tol + 2.0**-8 * (np.abs(out) + tol)
 
 
@@ -357,6 +359,31 @@ def test_rising_scores_move_the_reference(n):
         q = (u + 0.1 * rows(3, 1, 4, n).float()).bfloat16()
         check_attend(c, o, q)
         check_attend(c, o, q, causal=False)
+
+
+@pytest.mark.parametrize("n", [1, 4, 140])
+@pytest.mark.parametrize("spread", [0.0, 0.05, 1.0])
+def test_one_heavy_key_and_a_long_flat_tail(n, spread):
+    """Half of the weight on the first key, half on 16384 others, whose values have a common part: each small weight
+    lies near or below e4m3's least codes, but what they lose must not add up.  2^-8 and 2^-11 for the parts of the
+    heavy key.  The tail: 64 weights of a page are cut at 64 evenly spaced places of a step of 2^-9, so their sum is
+    off by half a step at most where they are equal: 2^-16 each, 16384 of them, against a sum of 2 * 2^5: 2^-8.
+    Not equal ones are off by 2^-9 / sqrt(3) each at random: 128 * 2^-9.8 / 2^6 = 2^-8.8; the bound takes three of it."""
+    N = 16384
+    c, o = pair(1, 1, 260)
+    g = torch.Generator().manual_seed(7)
+    u = torch.randn(256, generator=g).sign() * 0.25  # |u|^2 = 16
+    k = torch.zeros(1, 1, N + 1, 256)
+    k[0, 0, 1:] = torch.randn(N, 1, generator=g) * spread * u
+    k[0, 0, 0] = 8 * u  # score 8 * 16 * scale
+    k, v = k.bfloat16(), (1 + 0.25 * torch.randn(1, 1, N + 1, 256, generator=g)).bfloat16()
+    v[0, 0, 0] *= -1  # the two halves nearly cancel: an error of either shows
+    put(c, o, k, v)
+    q = (u * (1 + 0 * torch.arange(4 * n).view(1, 4, n, 1))).bfloat16()
+    scale = np.log(N) / 128  # the heavy key's weight is that of all others together
+    out, weight = paged.attend(o, f64(q), scale, causal=False)[:2]
+    got = f64(c.attend(q.cuda(), scale=scale, causal=False, out_dtype=torch.float32))
+    assert (np.abs(got - out) <= (2.0**-8 + 2.0**-11 + 3 * 2.0**-8.8 + 2.0**-13) * weight).all()
 
 
 def test_append_attend_is_both_calls():
