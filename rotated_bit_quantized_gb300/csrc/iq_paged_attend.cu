@@ -173,6 +173,8 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
     // ---------------------------------------------------------------- products
     if (lane == 0) {
       constexpr uint32_t kS = shape(128, C::kCols, false, false), kO = shape(128, C::kCols, true, false);
+      // descriptors count in 16 bytes: those of other pieces are sums
+      const uint64_t queries = operand(sbase + C::kQ), weights = operand(sbase + C::kP), at_slot = operand(sbase);
       int it = 0, used = 0, segment = 0;
       bool ok = true;
       Place w = start;
@@ -190,8 +192,8 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
             tc_after();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_e4m3(tmem + b * C::kCols, operand(sbase + s * kSlotBytes + (k >> 2) * kHalfBytes + (k & 3) * 32),
-                       operand(sbase + C::kQ + (k >> 2) * C::kCols * 128 + (k & 3) * 32), kS, k > 0);
+              mma_e4m3(tmem + b * C::kCols, at_slot + ((s * kSlotBytes + (k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+                       queries + (((k >> 2) * C::kCols * 128 + (k & 3) * 32) >> 4), kS, k > 0);
             mma_commit(&s_full[b]);
             mma_commit(&empty[s]);
             ++used;
@@ -205,8 +207,8 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
             for (int half = 0; half < 2; ++half)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_e4m3(t_o + half * C::kCols, operand(sbase + s * kSlotBytes + half * kHalfBytes + k * 32 * 128),
-                         operand(sbase + C::kP + b * C::kCols * 128 + k * 32), kO, j > 1 || k > 0);
+                mma_e4m3(t_o + half * C::kCols, at_slot + ((s * kSlotBytes + half * kHalfBytes + k * 32 * 128) >> 4),
+                         weights + ((b * C::kCols * 128 + k * 32) >> 4), kO, j > 1 || k > 0);
             mma_commit(&o_done[b]);
             mma_commit(&empty[s]);
             ++used;
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         if (lane == 0) {
           factor[r] = f;
           ref[r] = r < rows ? kUnset : kDead;
-          pos[r] = r < rows ? len - count + r / p.rep : -1;
+          pos[r] = r < rows ? len - count + query_of(p, r) : -1;
         }
       }
       proxy_fence();
@@ -593,17 +595,27 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.unit_rows = unit_rows(rows);
-  long long tiles = 0;
+  // the tiles of one head of an entry
+  auto tiles_of_entry = [&](int len, int count, int* units) {
+    long long n = 0;
+    const int all = count * rep;
+    *units = 0;
+    for (long long r = 0; r < all; r += p.unit_rows, ++*units)
+      n += tiles_of(len, len - count + static_cast<int>(r) / rep, len - count + (static_cast<int>(std::min<long long>(r + p.unit_rows, all)) - 1) / rep,
+                    causal, window, sinks).n;
+    return n;
+  };
+  long long tiles = 0, per[IQ_MAX_BATCH];
+  int units[IQ_MAX_BATCH];
   for (int i = 0; i < n_slots; ++i) {
     const int len = c->lens[slot_of(slots, i)], count = counts ? counts[i] : n_queries;
-    if (len > 0)
-      for (int z = 0; static_cast<long long>(z) * p.unit_rows < static_cast<long long>(count) * rep; ++z)
-        tiles += static_cast<long long>(tiles_of(len, count, rep, p.unit_rows, z, causal, window, sinks).n) * c->kv_heads;
+    per[i] = units[i] = 0;
+    if (len > 0 && count > 0) tiles += (per[i] = tiles_of_entry(len, count, &units[i])) * c->kv_heads;
   }
   const int grid = static_cast<int>(std::min<long long>(num_sms(), tiles));
   if (grid == 0) return IQ_OK;
   // short ranges are left at a tile's grain
-  p.cost = tiles >= 8ll * grid ? 1 : 0;
+  p.cost = tiles >= 8ll * grid ? (p.unit_rows == 128 ? 3 : 1) : 0;
   long long total = 0;
   for (int i = 0; i < n_slots; ++i) {
     const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
@@ -614,12 +626,10 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
     p.len[e] = len;
     p.count[e] = count;
     p.cum[e] = static_cast<int>(total);
-    long long per = 0;
-    for (int z = 0; static_cast<long long>(z) * p.unit_rows < static_cast<long long>(count) * rep; ++z)
-      per += tiles_of(len, count, rep, p.unit_rows, z, causal, window, sinks).n + p.cost;
-    total += per * c->kv_heads;
+    per[i] += static_cast<long long>(units[i]) * p.cost;
+    total += per[i] * c->kv_heads;
     if (total >= (1LL << 31)) return fail(IQ_ERR_UNSUPPORTED, "too many queries and keys for one call");
-    p.per[e] = static_cast<int>(per);
+    p.per[e] = static_cast<int>(per[i]);
   }
   p.cum[p.entries] = p.total = static_cast<int>(total);
   const long long pool_rows = static_cast<long long>(c->pages) * c->kv_heads * kPage;
@@ -634,6 +644,8 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   p.out_f32 = out_f32;
   p.heads = c->kv_heads;
   p.rep = rep;
+  while ((2 << p.rep_shift) <= rep) ++p.rep_shift;
+  if (rep & (rep - 1)) p.rep_mul = static_cast<unsigned>(((1ull << (32 + p.rep_shift)) + rep - 1) / rep);
   p.nq = n_queries;
   p.pages = c->pages;
   p.max_pages = c->max_pages;

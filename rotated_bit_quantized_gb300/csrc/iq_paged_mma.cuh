@@ -37,6 +37,7 @@ struct AttendParams {
   float* part_o;    // [2 * grid][unit_rows][256] unnormalised partial results: a range's first segment, its last
   float2* part_ml;  // [2 * grid][unit_rows] their references and sums
   int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, cost, total;
+  unsigned rep_mul, rep_shift;  // division by rep, see query_of
   float scale;
   // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
   // its queries; cum: slots before it (all heads), per: slots of one of its heads
@@ -51,11 +52,10 @@ struct Tiles {
   int p_lo, p_hi;      // positions of the first and the last row
   __host__ __device__ int tile(int j) const { return j < sinks ? j : j + skip; }
 };
-__host__ __device__ inline Tiles tiles_of(int len, int count, int rep, int unit_rows, int z, int causal, int window, int sinks) {
+__host__ __device__ inline Tiles tiles_of(int len, int first_pos, int last_pos, int causal, int window, int sinks) {
   Tiles t;
-  const int rows = count * rep, r1 = z * unit_rows + unit_rows - 1;
-  t.p_lo = len - count + z * unit_rows / rep;
-  t.p_hi = len - count + (r1 < rows ? r1 : rows - 1) / rep;
+  t.p_lo = first_pos;
+  t.p_hi = last_pos;
   const int stop = !causal ? len : t.p_hi < 0 ? 1 : t.p_hi + 1;
   const int low = window > 0 && t.p_lo >= window ? t.p_lo - window + 1 : 0;  // where the first row's window begins
   const int begin = low / kTile, reach = sinks < low ? sinks : low, n = (reach + kTile - 1) / kTile;
@@ -86,8 +86,16 @@ __device__ __forceinline__ Part part_of(const AttendParams& p, const Place& w, i
   const int begin = max(w.j - p.cost, 0), end = min(max(w.j + left - p.cost, 0), tiles);
   return {begin, end - begin};
 }
+// floor(r / rep) for r < 2^31: a shift where rep is a power of two; else, with s =
+// floor(log2 rep) and mul = ceil(2^(32+s) / rep) < 2^32, umulhi(r, mul) >> s (its
+// error is below r / 2^(32+s) < 1 / rep).
+__device__ __forceinline__ int query_of(const AttendParams& p, int r) {
+  return static_cast<int>((p.rep_mul ? __umulhi(static_cast<unsigned>(r), p.rep_mul) : static_cast<unsigned>(r)) >> p.rep_shift);
+}
 __device__ __forceinline__ Tiles tiles_at(const AttendParams& p, const Place& w) {
-  return tiles_of(p.len[w.e], p.count[w.e], p.rep, p.unit_rows, w.z, p.causal, p.window, p.sinks);
+  const int rows = p.count[w.e] * p.rep, r0 = w.z * p.unit_rows, before = p.len[w.e] - p.count[w.e];
+  return tiles_of(p.len[w.e], before + query_of(p, r0), before + query_of(p, min(r0 + p.unit_rows, rows) - 1), p.causal, p.window,
+                  p.sinks);
 }
 // Of slot t (a whole warp calls it together).
 __device__ inline Place place_of(const AttendParams& p, int t) {
@@ -109,7 +117,7 @@ __device__ inline Place place_of(const AttendParams& p, int t) {
   for (int z0 = 0;; z0 += 32) {  // 32 row tiles at a time, their slots summed up
     const int z = z0 + lane;
     int sum = 0;
-    if (z < units) sum = tiles_of(p.len[w.e], p.count[w.e], p.rep, p.unit_rows, z, p.causal, p.window, p.sinks).n + p.cost;
+    if (z < units) sum = tiles_at(p, {w.e, w.h, z, 0}).n + p.cost;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
@@ -136,10 +144,10 @@ __device__ __forceinline__ void next_unit(const AttendParams& p, Place& w) {
   w.h = 0;
   ++w.e;
 }
-// The index of a unit's first row among the rows [entry][query head][query] of
-// q and out is (entry * heads + h) * rep * nq; row r of the unit:
+// The index of row r of an entry and kv head among the rows [entry][query head][query] of q and out.
 __device__ __forceinline__ long long row_index(const AttendParams& p, const Place& w, int r) {
-  return ((static_cast<long long>(p.entry[w.e]) * p.heads + w.h) * p.rep + r % p.rep) * p.nq + r / p.rep;
+  const int j = query_of(p, r);
+  return static_cast<long long>((p.entry[w.e] * p.heads + w.h) * p.rep + r - j * p.rep) * p.nq + j;
 }
 
 cudaError_t launch_prefill(const AttendParams& p, int grid, cudaStream_t stream);
@@ -283,35 +291,53 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
   return static_cast<uint32_t>(r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 15));
 }
 
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h2) {
+  unsigned short d;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(h2));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // One query row (a warp; lane l holds dims 8l .. 8l+7 as bf16) as two e4m3
 // parts: x * 2^-e = hi + lo / kQLo, with the row's largest element in (224,
 // 448].  A bf16 has 8 significant bits and an e4m3 code 4, so the two parts
 // hold it exactly but for elements 2^14 below the row's largest (kQLo 16).
 // Returns 2^e; a row with a NaN or an infinity becomes all NaN.
-template <int QLO>
+template <int QLO>  // 1 or 16
 __device__ __forceinline__ float split_query(uint4 raw, uint2& hi, uint2& lo) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if (top >= 0x7F80u) {
-    hi = lo = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    return 1.0f;
-  }
+  uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));  // bf16 magnitudes order as integers
+  const uint32_t bad = top >= 0x7F80u ? 0x7F7F7F7Fu : 0u;  // no branch, so that several rows interleave
   int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
   e = min(max(e, -100), 120);
   const float inv = power2(-e);
   uint32_t h[4], l[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float a = bf16_to_f32(w[j] & 0xFFFFu) * inv, b = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
-    h[j] = e4m3x2(a, b);
-    const float2 f = f16x2_to_f32(e4m3x2_to_f16x2(h[j]));
-    l[j] = e4m3x2((a - f.x) * QLO, (b - f.y) * QLO);
+    // as fp16, exact (8 significant bits, at most 448) but for elements 2^23 below the row's largest
+    const uint32_t x = f16x2(bf16_to_f32(w[j] & 0xFFFFu) * inv, __uint_as_float(w[j] & 0xFFFF0000u) * inv);
+    h[j] = e4m3x2_of_f16x2(x);
+    uint32_t rest = sub_f16x2(x, e4m3x2_to_f16x2(h[j]));
+    if constexpr (QLO > 1) rest = mul_f16x2(rest, 0x4C004C00u);  // 16
+    l[j] = e4m3x2_of_f16x2(rest);
   }
-  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  hi = make_uint2(h[0] | h[1] << 16 | bad, h[2] | h[3] << 16 | bad);
+  lo = make_uint2(l[0] | l[1] << 16 | bad, l[2] | l[3] << 16 | bad);
   return power2(e);
 }
 __device__ __forceinline__ float clamp_finite(float x) { return fminf(fmaxf(x, -3e38f), 3e38f); }

@@ -42,21 +42,6 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
       : "memory");
 }
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h2) {
-  unsigned short d;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(h2));
-  return d;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -188,54 +173,60 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const bool wide = !done_whole || p.out_f32;
       uint8_t* base = static_cast<uint8_t*>(done_whole ? p.out : p.part_o) + ((lane & 3) * 16 + group * (wide ? 512 : 256));
       long long to[4];  // the rows that this lane stores pieces of
+      const long long mine = done_whole ? row_index(p, done, done.z * kRows + min(r, rows - 1)) : static_cast<long long>(done_slot) * kRows + r;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int x = (r & ~3) + k;
-        to[k] = (done_whole ? row_index(p, done, min(done.z * kRows + x, p.count[done.e] * p.rep - 1))
-                            : static_cast<long long>(done_slot) * kRows + x) *
-                (wide ? 1024 : 512);
-      }
+      for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) + k) * (wide ? 1024 : 512);
       await(&o_done[last_tile & 1], last_tile / 2);
       tc_after();
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        float o[32];
+      for (int c = 0; c < 128; c += 64) {
+        float o[64];
         tmem_ld<32>(t_o + lanes + group * 128 + c, o);
+        tmem_ld<32>(t_o + lanes + group * 128 + c + 32, o + 32);
         ld_wait();
         uint32_t x[16];
-        if (wide) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[half * 16 + i] * inv);
-            transpose4(x, lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if ((r & ~3) + k < rows)
-                *reinterpret_cast<uint4*>(base + to[k] + (c + half * 16) * 4) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(o[2 * i + 1] * inv), "f"(o[2 * i] * inv));
+        auto store = [&](int byte) {  // 16 words of this lane's row become 16 bytes of each of four rows, next to its neighbours'
           transpose4(x, lane);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if ((r & ~3) + k < rows)
-              *reinterpret_cast<uint4*>(base + to[k] + c * 2) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+              *reinterpret_cast<uint4*>(base + to[k] + byte) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        };
+        if (wide) {
+#pragma unroll
+          for (int part = 0; part < 4; ++part) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[part * 16 + i] * inv);
+            store((c + part * 16) * 4);
+          }
+        } else {
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(o[part * 32 + 2 * i + 1] * inv), "f"(o[part * 32 + 2 * i] * inv));
+            store((c + part * 32) * 2);
+          }
         }
       }
       if (!done_whole && r < rows && group == 0) p.part_ml[done_slot * kRows + r] = make_float2(done_ref, sum);
     };
     Place w = start;
-    for (int at = first; at < last; ++segment, next_unit(p, w)) {
-      const Tiles tiles = tiles_at(p, w);
-      const Part part = part_of(p, w, tiles.n, last - at);
-      const int e = w.e, k0 = part.begin, n = part.n, len = p.len[e];
+    for (int at = first;; ++segment, next_unit(p, w)) {
+      Tiles tiles{};
+      Part part{0, 0};
+      if (at < last) {
+        tiles = tiles_at(p, w);
+        part = part_of(p, w, tiles.n, last - at);
+      }
+      const int n = part.n;
+      if (n == 0 && !pending) break;
+      if (n == 0) w = start;  // no unit follows: one turn more, for the last one's results alone
+      const int e = w.e, k0 = part.begin, len = p.len[e];
       const bool whole = n == tiles.n, exists = w.z * kRows + r < p.count[e] * p.rep;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
       at += tiles.n + p.cost - w.j;
-      if (n == 0) break;
-      const int pos = len - p.count[e] + (w.z * kRows + r) / p.rep;
+      const int pos = len - p.count[e] + query_of(p, w.z * kRows + r);
       const int stop = !exists ? 0 : p.causal ? pos + 1 : len;
       const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
       // a row that has seen no key yet has no reference (its weights are relative to 2^0)
@@ -245,114 +236,128 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
       const int end_page = (len + kPage - 1) / kPage - 1;
       // this thread's page of tile j: ids two tiles ahead, scales one
-      auto id_of = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j, n - 1)) + group, end_page)); };
+      auto id_of = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + max(min(j, n - 1), 0)) + group, end_page)); };
       auto scales_of = [&](int id) {
         const long long i = static_cast<long long>(page_in_pool(id, p.pages, p.status)) * p.heads + w.h;
         return make_float2(__ldcg(p.k_scales + i), __ldcg(p.v_scales + i));
       };
       int id = id_of(1);
       float2 sc = scales_of(id_of(0));
-      await(&q_ready[segment & 1], segment / 2);
+      if (n > 0) await(&q_ready[segment & 1], segment / 2);
       const float fq = factor[(segment & 1) * kRows + r];
-      for (int j = 0; j < n; ++j, ++it) {
+      int j = 0;
+      do {
         const int b = it & 1;
-        const float f = clamp_finite(fq * sc.x);
-        const int ev = exponent_of(sc.y);
-        sc = scales_of(id);
-        id = id_of(j + 2);
-        const int t0 = tiles.tile(k0 + j) * kTile;
-        // whether some row of the unit does not see the whole tile
-        const bool masked = t0 + kTile > (p.causal ? tiles.p_lo + 1 : len) ||
-                            (p.window > 0 && t0 <= tiles.p_hi - p.window && t0 + kTile > p.sinks);
-        const uint32_t t_s = tmem + lanes + b * 128 + group * 64;
-        await(&s_full[b], it / 2);
-        tc_after();
-        float s[64];
-        tmem_ld<32>(t_s, s);
-        tmem_ld<32>(t_s + 32, s + 32);
-        ld_wait();
-        const float shift = static_cast<float>(ev) - ref;
+        if (n > 0) {
+          const float f = clamp_finite(fq * sc.x);
+          const int ev = exponent_of(sc.y);
+          sc = scales_of(id);
+          id = id_of(j + 2);
+          const int t0 = tiles.tile(k0 + j) * kTile;
+          // whether some row of the unit does not see the whole tile
+          const bool masked = t0 + kTile > (p.causal ? tiles.p_lo + 1 : len) ||
+                              (p.window > 0 && t0 <= tiles.p_hi - p.window && t0 + kTile > p.sinks);
+          const uint32_t t_s = tmem + lanes + b * 128 + group * 64;
+          await(&s_full[b], it / 2);
+          tc_after();
+          float s[64];
+          tmem_ld<32>(t_s, s);
+          tmem_ld<32>(t_s + 32, s + 32);
+          ld_wait();
+          const float shift = static_cast<float>(ev) - ref;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) s[i] = fmaf(s[i], f, shift);
-        if (masked) {
-          const int tb = t0 + group * 64;
+          for (int i = 0; i < 64; ++i) s[i] = fmaf(s[i], f, shift);
+          if (masked) {
+            const int tb = t0 + group * 64;
+            auto below = [&](int x) { return x <= tb ? 0ull : x - tb >= 64 ? ~0ull : (1ull << (x - tb)) - 1; };  // keys before x
+            const unsigned long long see = below(stop) & (~below(low) | below(p.sinks));
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!(tb + i < stop && (tb + i >= low || tb + i < p.sinks))) s[i] = -__builtin_huge_valf();
-        }
-        float m = s[0];
+            for (int i = 0; i < 64; ++i)
+              if (!(static_cast<uint32_t>(see >> (i & 32)) & 1u << (i & 31))) s[i] = -__builtin_huge_valf();
+          }
+          float m = s[0];
 #pragma unroll
-        for (int i = 1; i < 63; i += 2) m = fmaxf(fmaxf(m, s[i]), s[i + 1]);
-        m = fmaxf(m, s[63]);
-        int far = m > kTop || (unset && m > -1e38f);
-        asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
-                     : "+r"(far)
-                     : "r"(1 + quad)
-                     : "memory");
-        if (far) {
-          // some row of the quad passed its reference: move such rows' references
-          // so that their maxima land at 2^kPlace, and what was summed with them
-          xch[group * kRows + r] = m;
-          named_bar(1 + quad, 64);
-          m = fmaxf(m, xch[(group ^ 1) * kRows + r]);
-          named_bar(1 + quad, 64);
-          float move = 0.0f;
-          if (m > kTop || (unset && m > -1e38f)) move = m - kPlace;
-          ref += move;
-          unset = unset && !(m > -1e38f);
+          for (int i = 1; i < 63; i += 2) m = fmaxf(fmaxf(m, s[i]), s[i + 1]);
+          m = fmaxf(m, s[63]);
+          int far = m > kTop || (unset && m > -1e38f);
+          asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
+                       : "+r"(far)
+                       : "r"(1 + quad)
+                       : "memory");
+          float change = 1.0f;
+          if (far) {
+            // some row of the quad passed its reference: move such rows' references
+            // so that their maxima land at 2^kPlace
+            xch[group * kRows + r] = m;
+            named_bar(1 + quad, 64);
+            m = fmaxf(m, xch[(group ^ 1) * kRows + r]);
+            named_bar(1 + quad, 64);
+            float move = 0.0f;
+            if (m > kTop || (unset && m > -1e38f)) move = m - kPlace;
+            ref += move;
+            if (!unset) change = ex2_approx(-move);  // (else there is nothing yet, and move may be far below 0)
+            unset = unset && !(m > -1e38f);
 #pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] -= move;
-          if (j > 0) {  // this thread's half of the row's results
-            const float change = ex2_approx(-move);
+            for (int i = 0; i < 64; ++i) s[i] -= move;
             l *= change;
+          }
+          // the weights; as fp16 pairs (11 bits), cut into two parts of 4 bits, over
+          // the scores that this thread has read
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t ha, hb;
+              {
+                const int c = 32 * x + 4 * i;
+                const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]), w2 = ex2_approx(s[c + 2]), w3 = ex2_approx(s[c + 3]);
+                s0 += w0;
+                s1 += w1;
+                s0 += w2;
+                s1 += w3;
+                ha = f16x2(w0, w1);
+                hb = f16x2(w2, w3);
+              }
+              const uint32_t a = e4m3x2_of_f16x2(ha), d = e4m3x2_of_f16x2(hb);
+              hi[i] = a | d << 16;
+              lo[i] = e4m3x2_of_f16x2(add_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a)), cut_at(32 * x + 4 * i))) |
+                      e4m3x2_of_f16x2(add_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d)), cut_at(32 * x + 4 * i + 2))) << 16;
+            }
+            tmem_st<8>(t_s + 8 * x, reinterpret_cast<const float*>(hi));
+            tmem_st<8>(t_s + 16 + 8 * x, reinterpret_cast<const float*>(lo));
+          }
+          l = fmaf(s0 + s1, power2(-ev), l);
+          if (far && j > 0) {
+            // what was summed with the old references, this thread's half of the
+            // row; last, so that the product with the tile before, which has to end
+            // first, ran under the work on the weights
             await(&o_done[b ^ 1], (it - 1) / 2);
             tc_after();
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              float o[32];
+            for (int c = 0; c < 128; c += 64) {
+              float o[64];
               tmem_ld<32>(t_o + lanes + group * 128 + c, o);
+              tmem_ld<32>(t_o + lanes + group * 128 + c + 32, o + 32);
               ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= change;
+              for (int i = 0; i < 64; ++i) o[i] *= change;
               tmem_st<32>(t_o + lanes + group * 128 + c, o);
+              tmem_st<32>(t_o + lanes + group * 128 + c + 32, o + 32);
             }
-            st_wait();
           }
+          st_wait();
         }
-        // the weights; as fp16 pairs (11 bits), cut into two parts of 4 bits, over
-        // the scores that this thread has read
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t ha, hb;
-            {
-              const int c = 32 * x + 4 * i;
-              const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]), w2 = ex2_approx(s[c + 2]), w3 = ex2_approx(s[c + 3]);
-              s0 += w0;
-              s1 += w1;
-              s0 += w2;
-              s1 += w3;
-              ha = f16x2(w0, w1);
-              hb = f16x2(w2, w3);
-            }
-            const uint32_t a = e4m3x2_of_f16x2(ha), d = e4m3x2_of_f16x2(hb);
-            hi[i] = a | d << 16;
-            lo[i] = e4m3x2_of_f16x2(add_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a)), cut_at(32 * x + 4 * i))) |
-                    e4m3x2_of_f16x2(add_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d)), cut_at(32 * x + 4 * i + 2))) << 16;
-          }
-          tmem_st<8>(t_s + 8 * x, reinterpret_cast<const float*>(hi));
-          tmem_st<8>(t_s + 16 + 8 * x, reinterpret_cast<const float*>(lo));
-        }
-        l = fmaf(s0 + s1, power2(-ev), l);
-        st_wait();
         if (j == 0 && pending) store_results(it - 1);
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[b]);
-      }
+        if (n > 0) {
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[b]);
+          ++it;
+        }
+      } while (++j < n);
+      if (n == 0) break;
       pending = true;
       done = w;
       done_whole = whole;
@@ -360,40 +365,67 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       done_l = l;
       done_ref = unset ? -1e30f : ref;
     }
-    if (pending) store_results(it - 1);
   } else if (warp < kLoader) {
     // ---------------------------------------------------------------- queries: 32 rows per warp
     setmaxnreg_inc<kAskRegs>();
-    int segment = 0;
+        int segment = 0;
     Place w = start;
     for (int at = first; at < last; ++segment, next_unit(p, w)) {
       const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
       at += tiles + p.cost - w.j;
       if (n == 0) break;
       const int x0 = (warp - kAsker) * 32, rows = p.count[w.e] * p.rep - w.z * kRows;
-      uint2 hi[32], lo[32];
-      float f = 0.0f;  // of row x0 + lane
+      const long long mine = row_index(p, w, w.z * kRows + min(x0 + lane, rows - 1));  // of row x0 + lane
+      float f = 0.0f;  // of the same row
+      auto load = [&](int i) {
+        const long long at_row = __shfl_sync(0xFFFFFFFFu, mine, i);
+        return x0 + i < rows ? __ldcg(reinterpret_cast<const uint4*>(p.q + at_row * kHeadDim) + lane) : make_uint4(0, 0, 0, 0);
+      };
+      auto cut = [&](int i, uint4& v) {  // a row's dims 8 lane .. + 7 become its two parts
+        uint2 hi, lo;
+        const float g = split_query<1>(v, hi, lo);
+        if (lane == i) f = g;
+        v = make_uint4(hi.x, hi.y, lo.x, lo.y);
+      };
+      auto store = [&](int i, const uint4& v) {
+        uint8_t* to = smem + kQ + (lane >> 4) * kHalfBytes + swizzled(x0 + i, (lane & 15) * 8);
+        *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
+        *reinterpret_cast<uint2*>(to + 2 * kHalfBytes) = make_uint2(v.z, v.w);
+      };
+      if (at < last) {  // the next unit's rows towards L2
+        Place after = w;
+        next_unit(p, after);
+        if (after.z * kRows + x0 + lane < p.count[after.e] * p.rep) {
+          const char* to = reinterpret_cast<const char*>(p.q + row_index(p, after, after.z * kRows + x0 + lane) * kHeadDim);
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        uint4 raw[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          raw[k] = make_uint4(0, 0, 0, 0);
-          if (x0 + i + k < rows)
-            raw[k] = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, w, w.z * kRows + x0 + i + k) * kHeadDim) + lane);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float g = split_query<1>(raw[k], hi[i + k], lo[i + k]);
-          if (lane == i + k) f = g;
+          for (int k = 0; k < 4; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(to + 128 * k));
         }
       }
-      if (segment > 0 && !__all_sync(0xFFFFFFFFu, wait(q_free, segment - 1, kLostRows))) break;
+      if (segment == 0) {  // by a short loop: its code is fetched anew by every launch, and the products wait for it
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 16) {
+          uint4 v[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        uint8_t* to = smem + kQ + (lane >> 4) * kHalfBytes + swizzled(x0 + i, (lane & 15) * 8);
-        *reinterpret_cast<uint2*>(to) = hi[i];
-        *reinterpret_cast<uint2*>(to + 2 * kHalfBytes) = lo[i];
+          for (int k = 0; k < 16; ++k) v[k] = load(i + k);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            cut(i + k, v[k]);
+            store(i + k, v[k]);
+          }
+        }
+      } else {  // held in registers until the last unit's scores are done
+        uint4 v[32];
+#pragma unroll
+        for (int half = 0; half < 32; half += 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[half + i] = load(half + i);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) cut(half + i, v[half + i]);
+          asm volatile("" ::: "memory");  // the other half's loads stay behind: registers
+        }
+        if (!__all_sync(0xFFFFFFFFu, wait(q_free, segment - 1, kLostRows))) break;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) store(i, v[i]);
       }
       factor[(segment & 1) * kRows + x0 + lane] = clamp_finite(f * (p.scale * kLog2e));
       proxy_fence();
@@ -464,15 +496,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       constexpr uint32_t kS = shape(128, kTile, false, false), kO = shape(128, kHeadDim, false, true);
       int it = 0, used = 0, segment = 0;
       bool ok = true;
+      // descriptors count in 16 bytes: those of other pieces are sums
+      const uint64_t queries = operand(sbase + kQ), at_slot = operand(sbase), at_values = operand(sbase, kHalfBytes);
       auto scores = [&](int j) {  // S of the segment's tile j
         const int b = (it + j) & 1, s = used % kSlots;
         ok = wait(&full[s], used / kSlots, kLostMma);
         if (!ok) return;
         tc_after();
+        const uint64_t keys = at_slot + s * (kSlotBytes >> 4);
 #pragma unroll
         for (int k = 0; k < 16; ++k)  // high parts, low parts; halves of the dims; 32 dims at a time
-          mma_e4m3(tmem + b * 128, operand(sbase + kQ + (k >> 2) * kHalfBytes + (k & 3) * 32),
-                   operand(sbase + s * kSlotBytes + ((k >> 2) & 1) * kHalfBytes + (k & 3) * 32), kS, k > 0);
+          mma_e4m3(tmem + b * 128, queries + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+                   keys + ((((k >> 2) & 1) * kHalfBytes + (k & 3) * 32) >> 4), kS, k > 0);
         mma_commit(&s_full[b]);
         mma_commit(&empty[s]);
         ++used;
@@ -494,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // high and low parts in turn, 32 keys at a time (so that one read of V may serve both)
             mma_tmem_a(t_o, tmem + b * 128 + (k >> 2) * 64 + ((k >> 1) & 1) * 8 + (k & 1) * 16,
-                       operand(sbase + s * kSlotBytes + (k >> 1) * 32 * 128, kHalfBytes), kO, j > 0 || k > 0);
+                       at_values + ((s * kSlotBytes + (k >> 1) * 32 * 128) >> 4), kO, j > 0 || k > 0);
           mma_commit(&o_done[b]);
           mma_commit(&empty[s]);
           ++used;
