@@ -46,9 +46,10 @@ struct SplitShape {
   static constexpr int kQ = kSlots * kSlotBytes;      // [2 halves of the dims][kCols rows][128 bytes]
   static constexpr int kP = kQ + 2 * kCols * 128;     // [2][kCols rows][128 keys]
   static constexpr int kMisc = kP + 2 * kCols * 128;
+  static constexpr int kRing = Loader<kSlots>::kRing;
   static constexpr int kFloats = 2 * NR + 4 * NR;     // factors, references; reductions
-  static constexpr int kBars = 2 * kSlots + 10;
-  static constexpr int kSmem = 1024 + kMisc + kFloats * 4 + NR * 4 + kBars * 8 + 16;
+  static constexpr int kBars = 2 * kSlots + kRing + 10;
+  static constexpr int kSmem = 1024 + kMisc + kFloats * 4 + kRing * 16 + kBars * 8 + 8;
   static constexpr int kThreads = kGroups * 128 + 64;
   static constexpr int kTmem = 4 * kCols;             // S twice, O of both halves of the dims
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -67,10 +68,11 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   float* factor = reinterpret_cast<float*>(smem + C::kMisc);  // [NR] 2^eq * scale * log2 e
   float* ref = factor + NR;                                   // [NR]
   float* red = ref + NR;                                      // [4 warps][NR]
-  int* pos = reinterpret_cast<int*>(red + 4 * NR);            // [NR]
-  uint64_t* full = reinterpret_cast<uint64_t*>(pos + NR);     // [kSlots]
+  float4* scales = reinterpret_cast<float4*>(red + 4 * NR);   // [kRing] of a tile's two pages: keys', values'
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kRing);  // [kSlots]
   uint64_t* empty = full + C::kSlots;                         // [kSlots]
-  uint64_t* s_full = empty + C::kSlots;                       // [2] scores of a tile in tensor memory
+  uint64_t* scales_in = empty + C::kSlots;                    // [kRing]
+  uint64_t* s_full = scales_in + C::kRing;                    // [2] scores of a tile in tensor memory
   uint64_t* s_free = s_full + 2;                              // [2] and read
   uint64_t* p_ready = s_free + 2;                             // [2] weights of a tile in shared memory
   uint64_t* o_done = p_ready + 2;                             // [2] and multiplied with its values
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   uint64_t* drained = q_ready + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  static_assert(NR % 2 == 0 && C::kMisc % 8 == 0, "barriers are 8-byte aligned");
+  static_assert(NR % 8 == 0 && C::kMisc % 16 == 0, "scales and barriers are aligned");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kLoader = 4 * C::kGroups, kIssuer = kLoader + 1;
@@ -87,6 +89,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    for (int s = 0; s < C::kRing; ++s) mbar_init(&scales_in[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&s_free[s], 4 * C::kGroups);
@@ -115,60 +118,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   const Place start = place_of(p, first);  // every role walks the same segments from here
 
   if (warp == kLoader) {
-    // ---------------------------------------------------------------- pages to shared memory
-    const uint64_t pol = policy_evict_first();
-    int issued = 0;
-    bool ok = true;
-    Place w = start;
-    for (int at = first; at < last && ok; next_unit(p, w)) {
-      const int e = w.e, h = w.h;
-      const Tiles tiles = tiles_at(p, w);
-      const Part part = part_of(p, w, tiles.n, last - at);
-      const int k0 = part.begin, n = part.n;
-      at += tiles.n + p.cost - w.j;
-      if (n == 0) break;
-      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
-      const int end_page = (p.len[e] + kPage - 1) / kPage - 1;
-      // lanes fetch the ids of 16 tiles' pages at a time, one such piece ahead
-      auto fetch = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j + (lane >> 1), n - 1)) + (lane & 1), end_page)); };
-      auto load = [&](const CUtensorMap* map, int id0, int id1) {
-        const int s = issued % C::kSlots;
-        if (issued >= C::kSlots) ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], issued / C::kSlots - 1, kLostLoad));
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&full[s], kSlotBytes);
-          uint8_t* to = smem + s * kSlotBytes;
-          const int y0 = (id0 * p.heads + h) * kPage, y1 = (id1 * p.heads + h) * kPage;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tensor2d_g2s(to + half * kHalfBytes, map, 128 * half, y0, &full[s], pol);
-            tensor2d_g2s(to + half * kHalfBytes + kHalfBytes / 2, map, 128 * half, y1, &full[s], pol);
-          }
-        }
-        if (ok) ++issued;
-        __syncwarp();
-      };
-      int ids = fetch(0), next = fetch(16), v0 = 0, v1 = 0;
-      for (int j = 0; j <= n && ok; ++j) {  // in the order of the products: K0, K1, V0, K2, V1, ...
-        int k0id = 0, k1id = 0;
-        if (j < n) {
-          if (j % 16 == 0) {
-            if (j) {
-              ids = next;
-              next = fetch(j + 16);
-            }
-            ids = page_in_pool(ids, p.pages, p.status);
-          }
-          k0id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16));
-          k1id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16) + 1);
-          load(&p.k_map, k0id, k1id);
-        }
-        if (j > 0 && ok) load(&p.v_map, v0, v1);
-        v0 = k0id;
-        v1 = k1id;
-      }
-    }
-    if (lane == 0)  // no copy left in flight
-      for (int s = 0; s < C::kSlots && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / C::kSlots);
+    Loader<C::kSlots>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy_evict_first());
   } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- products
     if (lane == 0) {
@@ -235,7 +185,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
     };
     Place at_unit = start;
     for (int at = first; at < last; next_unit(p, at_unit)) {
-      const int e = at_unit.e, h = at_unit.h;
+      const int e = at_unit.e;
       const Tiles tiles = tiles_at(p, at_unit);
       const Part part = part_of(p, at_unit, tiles.n, last - at);
       const int k0 = part.begin, n = part.n, len = p.len[e], count = p.count[e], rows = count * p.rep;
@@ -244,20 +194,25 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       at += tiles.n + p.cost - at_unit.j;
       if (n == 0) break;
       // the query rows, a warp each
-      for (int r = warp; r < NR; r += 4 * C::kGroups) {
-        uint2 hi = make_uint2(0, 0), lo = hi;
-        float f = 0.0f;
-        if (r < rows) {
-          const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, at_unit, r) * kHeadDim) + lane);
-          f = clamp_finite(split_query<16>(raw, hi, lo) * (p.scale * kLog2e));
-        }
+      constexpr int kEach = NR / (4 * C::kGroups);
+      uint4 raw[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = warp + i * 4 * C::kGroups;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows) raw[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, at_unit, r) * kHeadDim) + lane);
+      }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = warp + i * 4 * C::kGroups;
+        uint2 hi, lo;
+        const float f = clamp_finite(split_query<16>(raw[i], hi, lo) * (p.scale * kLog2e));
         uint8_t* to = smem + C::kQ + (lane >> 4) * C::kCols * 128;
         *reinterpret_cast<uint2*>(to + swizzled(r, (lane & 15) * 8)) = hi;
         *reinterpret_cast<uint2*>(to + swizzled(NR + r, (lane & 15) * 8)) = lo;
         if (lane == 0) {
           factor[r] = f;
           ref[r] = r < rows ? kUnset : kDead;
-          pos[r] = r < rows ? len - count + query_of(p, r) : -1;
         }
       }
       proxy_fence();
@@ -267,22 +222,12 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = 0.0f;
 
-      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
-      const int end_page = (len + kPage - 1) / kPage - 1;
-      // this thread's page of tile j (half of a tile): ids two tiles ahead, scales one
-      auto id_of = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j, n - 1)) + (key >> 6), end_page)); };
-      auto scales_of = [&](int id) {
-        const long long x = static_cast<long long>(page_in_pool(id, p.pages, p.status)) * p.heads + h;
-        return make_float2(__ldcg(p.k_scales + x), __ldcg(p.v_scales + x));
-      };
-      int id = id_of(1);
-      float2 sc = scales_of(id_of(0));
       for (int j = 0; j < n; ++j, ++it) {
         const int b = it & 1;
-        const float ks = sc.x;
-        const int ev = exponent_of(sc.y);
-        sc = scales_of(id);
-        id = id_of(j + 2);
+        await(&scales_in[it % C::kRing], it / C::kRing);
+        const float* sc = reinterpret_cast<const float*>(&scales[it % C::kRing]) + (key >> 6);  // this key's page
+        const float ks = sc[0];
+        const int ev = exponent_of(sc[2]);
         const int t0 = tiles.tile(k0 + j) * kTile;
         await(&s_full[b], it / 2);
         tc_after();
@@ -301,7 +246,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
           const int t = t0 + key;
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            const int x = pos[r0 + r];
+            const int x = r0 + r < rows ? tiles.p_lo + query_of(p, r0 + r) : -1;
             const bool see = t < len && (!p.causal || (t <= x && (p.window == 0 || x < p.window || t > x - p.window || t < p.sinks)));
             if (!see) s[r] = -__builtin_huge_valf();
           }
@@ -407,12 +352,12 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
             const int r = x + y;
             if (r >= rows) break;
             const float v = fmaf(o2[y], 1.0f / kPLo, o[y]);
-            const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
             if (whole) {
+              const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
               store_out(p.out, p.out_f32, row_index(p, at_unit, r) * kHeadDim + d, sum == 0.0f ? 0.0f : v / sum);
             } else {
               p.part_o[(static_cast<long long>(slot) * NR + r) * kHeadDim + d] = v;
-              if (d == 0) p.part_ml[slot * NR + r] = make_float2(ref[r], sum);
+              if (d == 0) p.part_ml[slot * NR + r] = make_float2(ref[r], red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r]);
             }
           }
         }

@@ -234,6 +234,132 @@ __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The loading warp of an attention kernel (a whole warp): streams the key and
+// value tiles of a range's segments through a ring of SLOTS shared-memory slots,
+// in the order of the products, K0, K1, V0, K2, V1, ... per segment, and hands
+// the tiles' page scales to the row threads through a ring of their own, so
+// that those touch no global memory between a segment's begin and its end (a
+// load under a saturated HBM takes a tile's time and more).  A lane holds the
+// id and the scales of one page of 16 tiles.  Ids are fetched 16 tiles or two
+// segments ahead, scales half of that.
+template <int SLOTS>
+struct Loader {
+  // a tile's scales live until its weights are written: with 5 slots K(j + 4) waits for the values of
+  // tile j, with 6 K(j + 8) for the scores of tile j + 5, which wait for the weights of tile j + 3
+  static constexpr int kRing = SLOTS == 5 ? 4 : 8;
+  static_assert(SLOTS == 5 || SLOTS == 6, "the ring's length is reasoned above");
+
+  struct Segment {
+    const int* row;
+    Tiles tiles;
+    int begin, n, end_page, h;
+  };
+  const AttendParams& p;
+  uint8_t* smem;
+  uint64_t *full, *empty;
+  float4* scales;      // [kRing] keys' scales of the tile's two pages, values'
+  uint64_t* scales_in; // [kRing]
+  const Waits& wait;
+
+  // the segment at slot `at` of the range, which moves behind it; none (n == 0) at the range's end
+  __device__ __forceinline__ Segment take(Place& w, int& at, int last) const {
+    Segment g{};
+    if (at >= last) return g;
+    g.tiles = tiles_at(p, w);
+    const Part part = part_of(p, w, g.tiles.n, last - at);
+    g.begin = part.begin;
+    g.n = part.n;
+    g.row = p.table + static_cast<long long>(p.slot[w.e]) * p.max_pages;
+    g.end_page = (p.len[w.e] + kPage - 1) / kPage - 1;
+    g.h = w.h;
+    at += g.tiles.n + p.cost - w.j;
+    next_unit(p, w);
+    return g;
+  }
+  __device__ __forceinline__ int fetch(const Segment& g, int j) const {  // this lane's page of tiles j .. j + 15
+    const int lane = threadIdx.x & 31;
+    return __ldcg(g.row + min(2 * g.tiles.tile(g.begin + min(j + (lane >> 1), g.n - 1)) + (lane & 1), g.end_page));
+  }
+  __device__ __forceinline__ float2 scales_of(const Segment& g, int id) const {
+    const long long x = static_cast<long long>(id) * p.heads + g.h;
+    return make_float2(__ldcg(p.k_scales + x), __ldcg(p.v_scales + x));
+  }
+
+  __device__ __forceinline__ void run(Place w, int first, int last, uint64_t policy) const {
+    const int lane = threadIdx.x & 31;
+    int issued = 0, it = 0;
+    bool ok = true;
+    auto load = [&](const CUtensorMap* map, int id0, int id1, int h) {
+      const int s = issued % SLOTS;
+      if (issued >= SLOTS) ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], issued / SLOTS - 1, kLostLoad));
+      if (!ok) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[s], kSlotBytes);
+        uint8_t* to = smem + s * kSlotBytes;
+        const int y0 = (id0 * p.heads + h) * kPage, y1 = (id1 * p.heads + h) * kPage;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          tensor2d_g2s(to + half * kHalfBytes, map, 128 * half, y0, &full[s], policy);
+          tensor2d_g2s(to + half * kHalfBytes + kHalfBytes / 2, map, 128 * half, y1, &full[s], policy);
+        }
+      }
+      ++issued;
+      __syncwarp();
+    };
+    int at = first;
+    Segment g = take(w, at, last), g1 = take(w, at, last);
+    int ids = g.n > 0 ? page_in_pool(fetch(g, 0), p.pages, p.status) : 0, ids1 = g1.n > 0 ? fetch(g1, 0) : 0;
+    float2 sc = g.n > 0 ? scales_of(g, ids) : make_float2(1.0f, 1.0f);
+    while (ok && g.n > 0) {
+      int next = g.n > 16 ? fetch(g, 16) : 0, v0 = 0, v1 = 0;
+      float2 next_sc = sc, sc1 = sc;
+      if (g1.n > 0) {
+        ids1 = page_in_pool(ids1, p.pages, p.status);
+        sc1 = scales_of(g1, ids1);
+      }
+      const Segment g2 = take(w, at, last);
+      const int ids2 = g2.n > 0 ? fetch(g2, 0) : 0;
+      for (int j = 0; j <= g.n && ok; ++j) {
+        int k0 = 0, k1 = 0;
+        if (j < g.n) {
+          if (j % 16 == 0 && j > 0) {
+            ids = next;
+            sc = next_sc;
+            if (j + 16 < g.n) next = fetch(g, j + 16);
+          }
+          if (j % 16 == 8 && j + 8 < g.n) {
+            next = page_in_pool(next, p.pages, p.status);
+            next_sc = scales_of(g, next);
+          }
+          k0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16));
+          k1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16) + 1);
+          load(&p.k_map, k0, k1, g.h);
+          if (!ok) break;
+          const int x = lane - 2 * (j % 16);
+          if (x == 0 || x == 1) {
+            float* to = reinterpret_cast<float*>(&scales[it % kRing]);
+            to[x] = sc.x;
+            to[2 + x] = sc.y;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scales_in[it % kRing]);
+          ++it;
+        }
+        if (j > 0) load(&p.v_map, v0, v1, g.h);
+        v0 = k0;
+        v1 = k1;
+      }
+      g = g1;
+      ids = ids1;
+      sc = sc1;
+      g1 = g2;
+      ids1 = ids2;
+    }
+    if (lane == 0)  // no copy left in flight
+      for (int s = 0; s < SLOTS && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / SLOTS);
+  }
+};
+
 // n consecutive columns of this thread's lane (volatile, and read only after ld_wait)
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float* v);

@@ -28,7 +28,8 @@ constexpr int kRows = 128;
 constexpr int kSlots = 5;                         // tiles of keys or values in flight
 constexpr int kQ = kSlots * kSlotBytes;           // [high, low][2 halves of the dims][128 rows][128 bytes]
 constexpr int kMisc = kQ + 4 * kHalfBytes;
-constexpr int kSmem = kMisc + 4 * kRows * 4 + 32 * 8;
+constexpr int kRing = Loader<kSlots>::kRing;
+constexpr int kSmem = kMisc + 4 * kRows * 4 + kRing * 16 + 32 * 8;
 constexpr int kThreads = 512;
 constexpr int kAsker = 8, kLoader = 12, kIssuer = 13;
 constexpr int kRowRegs = 136, kAskRegs = 168, kRestRegs = 72;  // 2 * 136 + 168 + 72 = 4 * 128, what the CTA is launched with
@@ -102,9 +103,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
   }
   float* factor = reinterpret_cast<float*>(smem + kMisc);  // [2][128] 2^eq * scale * log2 e, by the segment's parity
   float* xch = factor + 2 * kRows;                         // [2][128] what the two threads of a row exchange
-  uint64_t* full = reinterpret_cast<uint64_t*>(xch + 2 * kRows);
+  float4* scales = reinterpret_cast<float4*>(xch + 2 * kRows);  // [kRing] of a tile's two pages: keys', values'
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kRing);
   uint64_t* empty = full + kSlots;
-  uint64_t* s_full = empty + kSlots;   // [2] scores of a tile in tensor memory
+  uint64_t* scales_in = empty + kSlots;
+  uint64_t* s_full = scales_in + kRing;  // [2] scores of a tile in tensor memory
   uint64_t* p_ready = s_full + 2;      // [2] weights of a tile in their place
   uint64_t* o_done = p_ready + 2;      // [2] and multiplied with its values
   uint64_t* q_ready = o_done + 2;      // [2] a segment's queries and factors written, by its parity: the
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
   uint64_t* drained = q_free + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  static_assert(2 * kSlots + 10 < 31, "the barriers and the two words behind them fit");
+  static_assert(2 * kSlots + kRing + 10 < 31, "the barriers and the two words behind them fit");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -121,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    for (int s = 0; s < kRing; ++s) mbar_init(&scales_in[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_ready[s], 8);
@@ -233,26 +237,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       bool unset = exists;
       float ref = exists ? 0.0f : 1e30f, l = 0.0f;
 
-      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
-      const int end_page = (len + kPage - 1) / kPage - 1;
-      // this thread's page of tile j: ids two tiles ahead, scales one
-      auto id_of = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + max(min(j, n - 1), 0)) + group, end_page)); };
-      auto scales_of = [&](int id) {
-        const long long i = static_cast<long long>(page_in_pool(id, p.pages, p.status)) * p.heads + w.h;
-        return make_float2(__ldcg(p.k_scales + i), __ldcg(p.v_scales + i));
-      };
-      int id = id_of(1);
-      float2 sc = scales_of(id_of(0));
       if (n > 0) await(&q_ready[segment & 1], segment / 2);
       const float fq = factor[(segment & 1) * kRows + r];
       int j = 0;
       do {
         const int b = it & 1;
         if (n > 0) {
-          const float f = clamp_finite(fq * sc.x);
-          const int ev = exponent_of(sc.y);
-          sc = scales_of(id);
-          id = id_of(j + 2);
+          await(&scales_in[it % kRing], it / kRing);
+          const float* sc = reinterpret_cast<const float*>(&scales[it % kRing]) + group;  // this thread's page
+          const float f = clamp_finite(fq * sc[0]);
+          const int ev = exponent_of(sc[2]);
           const int t0 = tiles.tile(k0 + j) * kTile;
           // whether some row of the unit does not see the whole tile
           const bool masked = t0 + kTile > (p.causal ? tiles.p_lo + 1 : len) ||
@@ -435,61 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
   } else {
     setmaxnreg_dec<kRestRegs>();
     if (warp == kLoader) {
-    // ---------------------------------------------------------------- pages to shared memory
-    uint64_t pol;  // other row tiles read the same pages
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    int issued = 0;
-    bool ok = true;
-    Place w = start;
-    for (int at = first; at < last && ok; next_unit(p, w)) {
-      const int e = w.e, h = w.h;
-      const Tiles tiles = tiles_at(p, w);
-      const Part part = part_of(p, w, tiles.n, last - at);
-      const int k0 = part.begin, n = part.n;
-      at += tiles.n + p.cost - w.j;
-      if (n == 0) break;
-      const int* row = p.table + static_cast<long long>(p.slot[e]) * p.max_pages;
-      const int end_page = (p.len[e] + kPage - 1) / kPage - 1;
-      // lanes fetch the ids of 16 tiles' pages at a time, one such piece ahead
-      auto fetch = [&](int j) { return __ldcg(row + min(2 * tiles.tile(k0 + min(j + (lane >> 1), n - 1)) + (lane & 1), end_page)); };
-      auto load = [&](const CUtensorMap* map, int id0, int id1) {
-        const int s = issued % kSlots;
-        if (issued >= kSlots) ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], issued / kSlots - 1, kLostLoad));
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&full[s], kSlotBytes);
-          uint8_t* to = smem + s * kSlotBytes;
-          const int y0 = (id0 * p.heads + h) * kPage, y1 = (id1 * p.heads + h) * kPage;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tensor2d_g2s(to + half * kHalfBytes, map, 128 * half, y0, &full[s], pol);
-            tensor2d_g2s(to + half * kHalfBytes + kHalfBytes / 2, map, 128 * half, y1, &full[s], pol);
-          }
-        }
-        if (ok) ++issued;
-        __syncwarp();
-      };
-      int ids = fetch(0), next = fetch(16), v0 = 0, v1 = 0;
-      for (int j = 0; j <= n && ok; ++j) {  // in the order of the products: K0, K1, V0, K2, V1, ...
-        int k0id = 0, k1id = 0;
-        if (j < n) {
-          if (j % 16 == 0) {
-            if (j) {
-              ids = next;
-              next = fetch(j + 16);
-            }
-            ids = page_in_pool(ids, p.pages, p.status);
-          }
-          k0id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16));
-          k1id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16) + 1);
-          load(&p.k_map, k0id, k1id);
-        }
-        if (j > 0 && ok) load(&p.v_map, v0, v1);
-        v0 = k0id;
-        v1 = k1id;
-      }
-    }
-    if (lane == 0)  // no copy left in flight
-      for (int s = 0; s < kSlots && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / kSlots);
+      uint64_t policy;  // other row tiles read the same pages
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+      Loader<kSlots>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy);
     } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- products
     if (lane == 0) {

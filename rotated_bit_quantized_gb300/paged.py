@@ -14,25 +14,40 @@ import torch
 
 from . import _abi
 from ._abi import IQ_PAGE, IQPagedDesc, check, lib
-from .cache import _OnDevice, _ptr, _stream
+from .cache import _OnDevice, _raw_stream, _stream
+
+
+_INT32 = np.dtype(np.int32)
 
 
 def _ints(x, n: int | None, name: str):
     """A contiguous int32 array of `n` whole numbers (any number of them where n is None)."""
-    a = np.asarray(x if isinstance(x, (np.ndarray, int)) else list(x))
-    if a.size and a.dtype.kind not in "iu":
-        raise ValueError(f"{name} must be whole numbers")
-    if a.size and (a.min() < -2**31 or a.max() >= 2**31):
-        raise ValueError(f"{name} must fit in 32 bits")
+    if type(x) is np.ndarray:
+        a = x
+        if a.dtype is _INT32 and a.ndim == 1 and a.flags.c_contiguous and (n is None or a.shape[0] == n):
+            return a
+    elif type(x) is range:
+        a = np.arange(x.start, x.stop, x.step)
+    else:
+        a = np.asarray(x if isinstance(x, (int, np.integer)) else list(x))
+    if a.dtype is not _INT32:
+        if a.size and a.dtype.kind not in "iu":
+            raise ValueError(f"{name} must be whole numbers")
+        wide, a = a, a.astype(np.int32)
+        if (a != wide).any():
+            raise ValueError(f"{name} must fit in 32 bits")
     if n is not None and a.ndim == 0:
-        a = np.broadcast_to(a, (n,))
+        a = np.full(n, a)
     if a.ndim != 1 or (n is not None and a.shape[0] != n):
         raise ValueError(f"{name} must be one whole number or {'a list of them' if n is None else n}")
-    return np.ascontiguousarray(a, dtype=np.int32)
+    return np.ascontiguousarray(a)
 
 
 def _at(a):
-    return None if a is None else a.ctypes.data
+    return None if a is None else a.__array_interface__["data"][0]
+
+
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 class IQPagedCache:
@@ -67,7 +82,7 @@ class IQPagedCache:
         self.device = torch.device(device or "cuda")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self._on = _OnDevice(self.device.index)
+        self._index, self._on, self._lib = self.device.index, _OnDevice(self.device.index), lib()
         dev = self.device
         self.k_codes = torch.empty((pages, kv_heads, IQ_PAGE, head_dim), dtype=torch.uint8, device=dev)
         self.v_codes = torch.empty_like(self.k_codes)
@@ -80,12 +95,26 @@ class IQPagedCache:
         self._lens = np.zeros(slots, dtype=np.int32)
         self._table = np.zeros((slots, self.max_pages), dtype=np.int32)
         self._refs = np.zeros(pages, dtype=np.int32)
-        self._need = {}
+        self._need, self._scale = {}, 1.0 / math.sqrt(head_dim)
         self._desc = IQPagedDesc()
         self._d = ctypes.byref(self._desc)
         check(lib().iq_paged_alloc(self._d, slots, kv_heads, head_dim, pages, self.max_pages,
                                    (ctypes.c_void_p * 6)(*[t.data_ptr() for t in bufs]),
                                    _at(self._lens), _at(self._table), _at(self._refs)), "iq_paged_alloc")
+
+    def _run(self, f, *args) -> None:
+        """Call a library function with the cache's device current."""
+        if _device() == self._index:
+            code = f(*args)
+        else:
+            with self._on:
+                code = f(*args)
+        if code:
+            check(code, f.__name__)
+
+    def _queue(self):
+        """The current stream of the cache's device."""
+        return _raw_stream(self._index) if _raw_stream is not None else _stream(self._index)
 
     # ---------------------------------------------------------------- state
     @property
@@ -115,16 +144,16 @@ class IQPagedCache:
         """Synchronise, return the kernels' status word (0: all normal) and clear it."""
         st = ctypes.c_int()
         with self._on:
-            code = lib().iq_read_status(_ptr(self._status), _stream(self.device.index), ctypes.byref(st))
+            code = lib().iq_read_status(self._status.data_ptr(), _stream(self._index), ctypes.byref(st))
         if code not in (_abi.IQ_OK, _abi.IQ_ERR_DEVICE):
             check(code, "iq_read_status")
         return st.value
 
     # ---------------------------------------------------------------- arguments
     def _tensor(self, t: torch.Tensor, name: str) -> torch.Tensor:
-        if not t.is_cuda or t.device.index != self.device.index:
+        if not t.is_cuda or t.get_device() != self._index:
             raise ValueError(f"{name} must be a CUDA tensor on {self.device}")
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise ValueError(f"{name} must be torch.bfloat16")
         if t.dim() != 4 or t.shape[3] != self.head_dim:
             raise ValueError(f"{name} must be [entries, heads, rows, {self.head_dim}]")
@@ -145,27 +174,28 @@ class IQPagedCache:
 
     def _outputs(self, q, counts, out, out_dtype):
         if out is None:  # rows that do not exist are left as they are: zeros
-            out = (torch.empty if counts is None else torch.zeros)(q.shape, dtype=out_dtype or torch.bfloat16, device=q.device)
+            dtype = out_dtype or torch.bfloat16
+            if dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+            return torch.empty_like(q, dtype=dtype) if counts is None else torch.zeros_like(q, dtype=dtype)
         if out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous():
             raise ValueError("out must be a contiguous bf16 or f32 tensor")
         if out.shape != q.shape or out.device != q.device or (out_dtype or out.dtype) != out.dtype:
             raise ValueError("out must have q's shape and device, and out_dtype")
         return out
 
-    def _workspace(self, q_heads: int, rows: int, entries: int) -> torch.Tensor | None:
+    def _workspace(self, q_heads: int, rows: int, entries: int):
         """Scratch for one call, from PyTorch's allocator: its own for every call, so
         that calls on different streams, or in two captured graphs, do not share it."""
         key = (q_heads, rows, entries)
         need = self._need.get(key)
         if need is None:
             c = ctypes.c_size_t()
-            with self._on:
-                check(lib().iq_paged_attend_workspace(self._d, q_heads, rows, entries, ctypes.byref(c)),
-                      "iq_paged_attend_workspace")
+            self._run(self._lib.iq_paged_attend_workspace, self._d, q_heads, rows, entries, ctypes.byref(c))
             if len(self._need) > 256:
                 self._need.clear()
             need = self._need[key] = c.value
-        return torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        return torch.empty(need, dtype=torch.uint8, device=self.device), need
 
     # ---------------------------------------------------------------- rows
     def append(self, keys: torch.Tensor, values: torch.Tensor, slots=None, counts=None) -> None:
@@ -175,10 +205,9 @@ class IQPagedCache:
         (capacity) when the pool or a slot is too small; nothing has changed then.
         """
         keys, values = self._rows(keys, values)
-        slots, counts = self._entries(keys.shape[0], slots, counts)
-        with self._on:
-            check(lib().iq_paged_append(self._d, _ptr(keys), _ptr(values), keys.shape[2], _at(slots), _at(counts),
-                                        keys.shape[0], _stream(self.device.index)), "iq_paged_append")
+        E, _, n, _ = keys.shape
+        slots, counts = self._entries(E, slots, counts)
+        self._run(self._lib.iq_paged_append, self._d, keys.data_ptr(), values.data_ptr(), n, _at(slots), _at(counts), E, self._queue())
 
     def read(self, start, n: int, slots=None) -> tuple[torch.Tensor, torch.Tensor]:
         """The values held in rows [start, start + n) of the slots (default: all), as bf16
@@ -191,9 +220,7 @@ class IQPagedCache:
             raise ValueError("n must not be negative")
         keys = torch.empty((entries, self.kv_heads, n, self.head_dim), dtype=torch.bfloat16, device=self.device)
         values = torch.empty_like(keys)
-        with self._on:
-            check(lib().iq_paged_read(self._d, _at(slots), _at(start), entries, n, _ptr(keys), _ptr(values),
-                                      _stream(self.device.index)), "iq_paged_read")
+        self._run(self._lib.iq_paged_read, self._d, _at(slots), _at(start), entries, n, keys.data_ptr(), values.data_ptr(), self._queue())
         return keys, values
 
     def trim(self, n, slots=None) -> np.ndarray:
@@ -203,22 +230,21 @@ class IQPagedCache:
         slots, _ = self._entries(entries, slots, None)
         n = _ints(n, entries, "n")
         out = np.zeros(entries, dtype=np.int32)
-        check(lib().iq_paged_trim(self._d, _at(slots), _at(n), entries, _at(out)), "iq_paged_trim")
+        self._run(self._lib.iq_paged_trim, self._d, _at(slots), _at(n), entries, _at(out))
         return out
 
     # ---------------------------------------------------------------- pages
     def free(self, slots) -> None:
         """Release every page of these slots."""
         slots = _ints(slots, None, "slots")
-        check(lib().iq_paged_free(self._d, _at(slots), len(slots)), "iq_paged_free")
+        self._run(self._lib.iq_paged_free, self._d, _at(slots), len(slots))
 
     def fork(self, src, dst) -> None:
         """Make each slot dst[i] a second holder of slot src[i]'s pages; what dst[i] held is released.
         No codes are copied.  All at once: a source is what it was before the call."""
         dst = _ints(dst, None, "dst")
         src = _ints(src, len(dst), "src")
-        with self._on:
-            check(lib().iq_paged_fork(self._d, _at(src), _at(dst), len(dst), _stream(self.device.index)), "iq_paged_fork")
+        self._run(self._lib.iq_paged_fork, self._d, _at(src), _at(dst), len(dst), self._queue())
 
     def compact(self, out: "IQPagedCache | None" = None) -> "IQPagedCache":
         """A copy of this cache that holds each live page once, lowest ids first; sharing is kept.
@@ -229,8 +255,7 @@ class IQPagedCache:
                                self.head_dim, self.device)
         elif out.device != self.device:
             raise ValueError("out must be on the cache's device")
-        with self._on:
-            check(lib().iq_paged_compact(self._d, out._d, _stream(self.device.index)), "iq_paged_compact")
+        self._run(self._lib.iq_paged_compact, self._d, out._d, self._queue())
         return out
 
     # ---------------------------------------------------------------- attention
@@ -248,13 +273,10 @@ class IQPagedCache:
         E, Hq, L, D = q.shape
         slots, counts = self._entries(E, slots, counts)
         out = self._outputs(q, counts, out, out_dtype)
-        ws = self._workspace(Hq, L, E)
-        with self._on:
-            check(lib().iq_paged_attend(self._d, _ptr(q), Hq, L, _at(slots), _at(counts), E,
-                                        1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0,
-                                        window, sinks, _ptr(out), 1 if out.dtype == torch.float32 else 0,
-                                        None if ws is None else _ptr(ws), 0 if ws is None else ws.numel(),
-                                        _stream(self.device.index)), "iq_paged_attend")
+        ws, need = self._workspace(Hq, L, E)
+        self._run(self._lib.iq_paged_attend, self._d, q.data_ptr(), Hq, L, _at(slots), _at(counts), E,
+                  self._scale if scale is None else scale, 1 if causal else 0, window, sinks, out.data_ptr(),
+                  1 if out.dtype is torch.float32 else 0, ws.data_ptr(), need, self._queue())
         return out
 
     def append_attend(self, keys: torch.Tensor, values: torch.Tensor, q: torch.Tensor, causal: bool = True,
@@ -269,13 +291,8 @@ class IQPagedCache:
             raise ValueError("keys/values and q must have the same entries")
         slots, counts = self._entries(E, slots, counts)
         out = self._outputs(q, counts, out, out_dtype)
-        ws = self._workspace(Hq, L, E)
-        with self._on:
-            check(lib().iq_paged_append_attend(self._d, _ptr(keys), _ptr(values), keys.shape[2], _ptr(q), Hq, L,
-                                               _at(slots), _at(counts), E,
-                                               1.0 / math.sqrt(D) if scale is None else float(scale),
-                                               1 if causal else 0, window, sinks, _ptr(out),
-                                               1 if out.dtype == torch.float32 else 0,
-                                               None if ws is None else _ptr(ws), 0 if ws is None else ws.numel(),
-                                               _stream(self.device.index)), "iq_paged_append_attend")
+        ws, need = self._workspace(Hq, L, E)
+        self._run(self._lib.iq_paged_append_attend, self._d, keys.data_ptr(), values.data_ptr(), keys.shape[2], q.data_ptr(), Hq, L,
+                  _at(slots), _at(counts), E, self._scale if scale is None else scale, 1 if causal else 0, window, sinks,
+                  out.data_ptr(), 1 if out.dtype is torch.float32 else 0, ws.data_ptr(), need, self._queue())
         return out
