@@ -32,7 +32,7 @@ constexpr int kRing = Loader<kSlots>::kRing;
 constexpr int kSmem = kMisc + 4 * kRows * 4 + kRing * 16 + 32 * 8;
 constexpr int kThreads = 512;
 constexpr int kAsker = 8, kLoader = 12, kIssuer = 13;
-constexpr int kRowRegs = 136, kAskRegs = 168, kRestRegs = 72;  // 2 * 136 + 168 + 72 = 4 * 128, what the CTA is launched with
+constexpr int kRowRegs = 144, kRestRegs = 96;  // 2 * 144 + 128 + 96 = 4 * 128, what the CTA is launched with
 constexpr float kPlace = 5.0f, kTop = 8.75f;      // the running maximum's place, and how far a weight may grow (448 = 2^8.8)
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
@@ -89,8 +89,8 @@ __device__ __forceinline__ void transpose4(uint32_t (&c)[16], int lane) {
 // One persistent CTA per SM, four warpgroups.  Warps 0-7: two threads per query
 // row (warp w reaches tensor-memory lanes 32 (w % 4) ..), each with the 64 keys
 // of one page of a tile; warps w and w + 4 hold the same rows and settle the
-// rows' references between themselves.  Warps 8-11 hold the next unit's queries
-// in registers until this unit's last scores are done.  Then one warp streams
+// rows' references between themselves.  Warps 8-11 write the next unit's queries as
+// soon as this unit's last scores are done.  Then one warp streams
 // the pages and one issues the products, S of the next tile but one behind O
 // of this tile.  A unit's results are stored after the next unit's first
 // weights are written, so the products wait for the stores alone.
@@ -361,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
     }
   } else if (warp < kLoader) {
     // ---------------------------------------------------------------- queries: 32 rows per warp
-    setmaxnreg_inc<kAskRegs>();
         int segment = 0;
     Place w = start;
     for (int at = first; at < last; ++segment, next_unit(p, w)) {
@@ -371,21 +370,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int x0 = (warp - kAsker) * 32, rows = p.count[w.e] * p.rep - w.z * kRows;
       const long long mine = row_index(p, w, w.z * kRows + min(x0 + lane, rows - 1));  // of row x0 + lane
       float f = 0.0f;  // of the same row
-      auto load = [&](int i) {
-        const long long at_row = __shfl_sync(0xFFFFFFFFu, mine, i);
-        return x0 + i < rows ? __ldcg(reinterpret_cast<const uint4*>(p.q + at_row * kHeadDim) + lane) : make_uint4(0, 0, 0, 0);
+      auto load = [&](int i, uint4 (&v)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const long long at_row = __shfl_sync(0xFFFFFFFFu, mine, i + k);
+          v[k] = x0 + i + k < rows ? __ldcg(reinterpret_cast<const uint4*>(p.q + at_row * kHeadDim) + lane) : make_uint4(0, 0, 0, 0);
+        }
       };
-      auto cut = [&](int i, uint4& v) {  // a row's dims 8 lane .. + 7 become its two parts
-        uint2 hi, lo;
-        const float g = split_query<1>(v, hi, lo);
-        if (lane == i) f = g;
-        v = make_uint4(hi.x, hi.y, lo.x, lo.y);
+      auto cut = [&](int i, const uint4 (&v)[8]) {  // into their two parts
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint2 hi, lo;
+          const float g = split_query<1>(v[k], hi, lo);
+          if (lane == i + k) f = g;
+          uint8_t* to = smem + kQ + (lane >> 4) * kHalfBytes + swizzled(x0 + i + k, (lane & 15) * 8);
+          *reinterpret_cast<uint2*>(to) = hi;
+          *reinterpret_cast<uint2*>(to + 2 * kHalfBytes) = lo;
+        }
       };
-      auto store = [&](int i, const uint4& v) {
-        uint8_t* to = smem + kQ + (lane >> 4) * kHalfBytes + swizzled(x0 + i, (lane & 15) * 8);
-        *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
-        *reinterpret_cast<uint2*>(to + 2 * kHalfBytes) = make_uint2(v.z, v.w);
-      };
+      uint4 v[8], u[8];
+      load(0, v);
+      load(8, u);
       if (at < last) {  // the next unit's rows towards L2
         Place after = w;
         next_unit(p, after);
@@ -395,31 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           for (int k = 0; k < 4; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(to + 128 * k));
         }
       }
-      if (segment == 0) {  // by a short loop: its code is fetched anew by every launch, and the products wait for it
+      if (segment > 0 && !__all_sync(0xFFFFFFFFu, wait(q_free, segment - 1, kLostRows))) break;
 #pragma unroll 1
-        for (int i = 0; i < 32; i += 16) {
-          uint4 v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = load(i + k);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            cut(i + k, v[k]);
-            store(i + k, v[k]);
-          }
-        }
-      } else {  // held in registers until the last unit's scores are done
-        uint4 v[32];
-#pragma unroll
-        for (int half = 0; half < 32; half += 16) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[half + i] = load(half + i);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) cut(half + i, v[half + i]);
-          asm volatile("" ::: "memory");  // the other half's loads stay behind: registers
-        }
-        if (!__all_sync(0xFFFFFFFFu, wait(q_free, segment - 1, kLostRows))) break;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) store(i, v[i]);
+      for (int i = 0; i < 32; i += 16) {  // a short loop: code for all rows at once would drive the others' out of the caches
+        cut(i, v);
+        if (i == 0) load(16, v);
+        cut(i + 8, u);
+        if (i == 0) load(24, u);
       }
       factor[(segment & 1) * kRows + x0 + lane] = clamp_finite(f * (p.scale * kLog2e));
       proxy_fence();
