@@ -451,9 +451,9 @@ cudaError_t launch_split(const AttendParams& p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows) {
+bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows, int box_rows) {
   const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(rows)}, strides[1] = {kHeadDim};
-  const cuuint32_t box[2] = {128, kPage}, unit[2] = {1, 1};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, unit[2] = {1, 1};
   auto fn = encode_fn();
   return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, unit,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -507,6 +507,11 @@ int iq_paged_attend_workspace(const iq_paged* c, int q_heads, int n_queries, int
   const int rows = n_queries * (q_heads / c->kv_heads);
   const size_t parts = rows > 0 && n_slots > 0 ? 2 * static_cast<size_t>(num_sms()) * unit_rows(rows) : 0;
   *bytes = parts * (kHeadDim * sizeof(float) + sizeof(float2));
+  if (rows > kMaxSplitRows) {  // the queries' two parts and factors
+    const size_t all = static_cast<size_t>(n_slots) * q_heads * n_queries;
+    if (all >= (1u << 30)) return fail(IQ_ERR_UNSUPPORTED, "too many query rows");
+    *bytes += all * (2 * kHeadDim + sizeof(float));
+  }
   return IQ_OK;
 }
 
@@ -599,12 +604,21 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   p.sinks = sinks;
   p.scale = scale;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * grid * p.unit_rows * kHeadDim);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * num_sms() * p.unit_rows * kHeadDim);
+  int all_counts[IQ_MAX_BATCH];
+  if (p.unit_rows == 128) {
+    const long long all = static_cast<long long>(n_slots) * q_heads * n_queries;
+    p.cut = reinterpret_cast<uint8_t*>(p.part_ml + 2ll * num_sms() * p.unit_rows);  // 16-byte aligned
+    p.factors = reinterpret_cast<float*>(p.cut + all * 2 * kHeadDim);
+    p.slots_n = n_slots;
+    for (int i = 0; i < n_slots; ++i) all_counts[i] = counts ? counts[i] : n_queries;
+    if (!code_map(&p.q_map, p.cut, 2 * all, 128)) return fail(IQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  }
   cudaError_t err = p.unit_rows == 8    ? launch_split<8>(p, grid, cs)
                     : p.unit_rows == 16 ? launch_split<16>(p, grid, cs)
                     : p.unit_rows == 32 ? launch_split<32>(p, grid, cs)
                     : p.unit_rows == 64 ? launch_split<64>(p, grid, cs)
-                                        : launch_prefill(p, grid, cs);
+                                        : launch_prefill(p, all_counts, grid, cs);
   if (err == cudaSuccess && grid > 1)
     err = launch_after<AttendParams, int>(paged_join_kernel, dim3(grid - 1, std::min(p.unit_rows, rows + 7) / 8), 256, 0, cs, p, grid);
   return err == cudaSuccess ? IQ_OK : cuda_fail(err, "paged attention");

@@ -17,7 +17,7 @@ constexpr int kSlotBytes = 2 * kHalfBytes;    // a tile of keys or of values in 
 
 // The tensor map of a code pool: rows of 256 bytes, boxes of one page of one
 // kv head by half of the dims (64 x 128 bytes, 128-byte swizzle).
-bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows);
+bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows, int box_rows = kPage);
 
 // ------------------------------------------------------------------ work
 
@@ -27,7 +27,7 @@ bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows);
 // ranges of equal length, one for each CTA; a unit that lies in one range is
 // stored at once, the others leave a partial result per range.
 struct AttendParams {
-  CUtensorMap k_map, v_map;
+  CUtensorMap k_map, v_map, q_map;  // (q_map: the prefill kernel's queries, cut beforehand)
   const float* k_scales;
   const float* v_scales;
   const int* table;
@@ -36,7 +36,9 @@ struct AttendParams {
   void* out;
   float* part_o;    // [2 * grid][unit_rows][256] unnormalised partial results: a range's first segment, its last
   float2* part_ml;  // [2 * grid][unit_rows] their references and sums
-  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, cost, total;
+  uint8_t* cut;     // prefill: [high, low parts][entry][kv head][row][256] e4m3
+  float* factors;   // prefill: [entry][kv head][row] 2^e * scale * log2 e
+  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, cost, total, slots_n;
   unsigned rep_mul, rep_shift;  // division by rep, see query_of
   float scale;
   // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
@@ -150,7 +152,8 @@ __device__ __forceinline__ long long row_index(const AttendParams& p, const Plac
   return static_cast<long long>((p.entry[w.e] * p.heads + w.h) * p.rep + r - j * p.rep) * p.nq + j;
 }
 
-cudaError_t launch_prefill(const AttendParams& p, int grid, cudaStream_t stream);
+// counts: of every entry of the call, also those without keys
+cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream);
 
 // A launch that may begin while the kernel before it ends (it waits itself).
 template <typename... Args>

@@ -29,10 +29,10 @@ constexpr int kSlots = 5;                         // tiles of keys or values in 
 constexpr int kQ = kSlots * kSlotBytes;           // [high, low][2 halves of the dims][128 rows][128 bytes]
 constexpr int kMisc = kQ + 4 * kHalfBytes;
 constexpr int kRing = Loader<kSlots>::kRing;
-constexpr int kSmem = kMisc + 4 * kRows * 4 + kRing * 16 + 32 * 8;
-constexpr int kThreads = 512;
-constexpr int kAsker = 8, kLoader = 12, kIssuer = 13;
-constexpr int kRowRegs = 144, kRestRegs = 96;  // 2 * 144 + 128 + 96 = 4 * 128, what the CTA is launched with
+constexpr int kSmem = kMisc + 2 * kRows * 4 + kRing * 16 + 32 * 8;
+constexpr int kThreads = 384;
+constexpr int kLoader = 8, kIssuer = 9, kAsker = 10;
+constexpr int kRowRegs = 208, kRestRegs = 88;     // 2 * 208 + 88 = 3 * 168, what the CTA is launched with
 constexpr float kPlace = 5.0f, kTop = 8.75f;      // the running maximum's place, and how far a weight may grow (448 = 2^8.8)
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
@@ -86,13 +86,49 @@ __device__ __forceinline__ void transpose4(uint32_t (&c)[16], int lane) {
     }
 }
 
-// One persistent CTA per SM, four warpgroups.  Warps 0-7: two threads per query
+// The queries' two parts and factors, a warp per four rows, before the kernel
+// below: cut inside it, by warps of its own, they slowed the row threads by a
+// third around every unit's begin (the conversions share a pipe), 260 against
+// 214 us for 8191 queries under a window of 1023.
+struct CutParams {
+  const uint16_t* q;
+  uint8_t* cut;
+  float* factors;
+  int heads, rep, nq, total;
+  float scale;
+  int count[IQ_MAX_BATCH];
+};
+__global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ CutParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, w0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4, rows = p.nq * p.rep;
+  uint4 raw[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int w = min(w0 + k, p.total - 1), eh = w / rows, r = w - eh * rows, j = r / p.rep, e = eh / p.heads;
+    raw[k] = make_uint4(0, 0, 0, 0);
+    if (j < p.count[e])  // row r of (entry, kv head): query j of query head eh * rep + r % rep
+      raw[k] = __ldcs(reinterpret_cast<const uint4*>(p.q + ((static_cast<long long>(eh) * p.rep + r - j * p.rep) * p.nq + j) * kHeadDim) + lane);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint2 hi, lo;
+    const float f = split_query<1>(raw[k], hi, lo);
+    const long long w = w0 + k;
+    if (w >= p.total) break;
+    reinterpret_cast<uint2*>(p.cut + w * kHeadDim)[lane] = hi;
+    reinterpret_cast<uint2*>(p.cut + (p.total + w) * kHeadDim)[lane] = lo;
+    if (lane == 0) p.factors[w] = clamp_finite(f * (p.scale * kLog2e));
+  }
+}
+
+// One persistent CTA per SM, three warpgroups.  Warps 0-7: two threads per query
 // row (warp w reaches tensor-memory lanes 32 (w % 4) ..), each with the 64 keys
 // of one page of a tile; warps w and w + 4 hold the same rows and settle the
-// rows' references between themselves.  Warps 8-11 write the next unit's queries as
-// soon as this unit's last scores are done.  Then one warp streams
-// the pages and one issues the products, S of the next tile but one behind O
-// of this tile.  A unit's results are stored after the next unit's first
+// rows' references between themselves.  Then one warp streams
+// the pages, one issues the products, S of the next tile but one behind O of
+// this tile, and one fetches a unit's queries once the last unit's scores are
+// done. A unit's results are stored after the next unit's first
 // weights are written, so the products wait for the stores alone.
 __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled operands need it; no room to align by hand
@@ -101,8 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
     if (threadIdx.x == 0) atomicOr(p.status, kLostMma);
     return;
   }
-  float* factor = reinterpret_cast<float*>(smem + kMisc);  // [2][128] 2^eq * scale * log2 e, by the segment's parity
-  float* xch = factor + 2 * kRows;                         // [2][128] what the two threads of a row exchange
+  float* xch = reinterpret_cast<float*>(smem + kMisc);          // [2][128] what the two threads of a row exchange
   float4* scales = reinterpret_cast<float4*>(xch + 2 * kRows);  // [kRing] of a tile's two pages: keys', values'
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + kRing);
   uint64_t* empty = full + kSlots;
@@ -110,9 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
   uint64_t* s_full = scales_in + kRing;  // [2] scores of a tile in tensor memory
   uint64_t* p_ready = s_full + 2;      // [2] weights of a tile in their place
   uint64_t* o_done = p_ready + 2;      // [2] and multiplied with its values
-  uint64_t* q_ready = o_done + 2;      // [2] a segment's queries and factors written, by its parity: the
-                                       // issuer may be a segment ahead of the softmax
-  uint64_t* q_free = q_ready + 2;      // a segment's last scores done
+  uint64_t* q_ready = o_done + 2;      // a segment's queries in shared memory
+  uint64_t* q_free = q_ready + 1;      // a segment's last scores done
   uint64_t* drained = q_free + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
@@ -129,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       mbar_init(&s_full[s], 1);
       mbar_init(&p_ready[s], 8);
       mbar_init(&o_done[s], 1);
-      mbar_init(&q_ready[s], 4);
     }
+    mbar_init(q_ready, 1);
     mbar_init(q_free, 1);
     mbar_init(drained, 1);
     *abort = 0;
@@ -150,13 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
 
   const int first = range_begin(blockIdx.x, gridDim.x, p.total), last = range_begin(blockIdx.x + 1, gridDim.x, p.total);
   const Place start = place_of(p, first);
+  const int q_rows = p.slots_n * p.heads * p.rep * p.nq;  // high parts, then as many rows of low parts
 
-  if (warp < kAsker) {
+  if (warp < kLoader) {
     // ---------------------------------------------------------------- softmax: half a row per thread
     setmaxnreg_inc<kRowRegs>();
     const int group = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    int it = 0, segment = 0;
+    int it = 0;
     bool ok = true;
     auto await = [&](uint64_t* bar, uint32_t phase) {  // a lost wait changes no path: every barrier below is still reached
       if (ok) ok = wait(bar, phase, kLostRows);
@@ -215,8 +250,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       }
       if (!done_whole && r < rows && group == 0) p.part_ml[done_slot * kRows + r] = make_float2(done_ref, sum);
     };
+    // the factor of this thread's row, fetched a unit ahead
+    auto factor_of = [&](const Place& u) {
+      const int x = u.z * kRows + r;
+      return x < p.count[u.e] * p.rep ? __ldcg(p.factors + (p.entry[u.e] * p.heads + u.h) * p.nq * p.rep + x) : 0.0f;
+    };
     Place w = start;
-    for (int at = first;; ++segment, next_unit(p, w)) {
+    float next_factor = first < last ? factor_of(w) : 0.0f;
+    for (int at = first;; next_unit(p, w)) {
       Tiles tiles{};
       Part part{0, 0};
       if (at < last) {
@@ -237,8 +278,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       bool unset = exists;
       float ref = exists ? 0.0f : 1e30f, l = 0.0f;
 
-      if (n > 0) await(&q_ready[segment & 1], segment / 2);
-      const float fq = factor[(segment & 1) * kRows + r];
+      const float fq = next_factor;
+      if (n > 0 && at < last) {
+        Place after = w;
+        next_unit(p, after);
+        next_factor = factor_of(after);
+      }
       int j = 0;
       do {
         const int b = it & 1;
@@ -359,60 +404,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       done_l = l;
       done_ref = unset ? -1e30f : ref;
     }
-  } else if (warp < kLoader) {
-    // ---------------------------------------------------------------- queries: 32 rows per warp
-        int segment = 0;
-    Place w = start;
-    for (int at = first; at < last; ++segment, next_unit(p, w)) {
-      const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
-      at += tiles + p.cost - w.j;
-      if (n == 0) break;
-      const int x0 = (warp - kAsker) * 32, rows = p.count[w.e] * p.rep - w.z * kRows;
-      const long long mine = row_index(p, w, w.z * kRows + min(x0 + lane, rows - 1));  // of row x0 + lane
-      float f = 0.0f;  // of the same row
-      auto load = [&](int i, uint4 (&v)[8]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const long long at_row = __shfl_sync(0xFFFFFFFFu, mine, i + k);
-          v[k] = x0 + i + k < rows ? __ldcg(reinterpret_cast<const uint4*>(p.q + at_row * kHeadDim) + lane) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      auto cut = [&](int i, const uint4 (&v)[8]) {  // into their two parts
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint2 hi, lo;
-          const float g = split_query<1>(v[k], hi, lo);
-          if (lane == i + k) f = g;
-          uint8_t* to = smem + kQ + (lane >> 4) * kHalfBytes + swizzled(x0 + i + k, (lane & 15) * 8);
-          *reinterpret_cast<uint2*>(to) = hi;
-          *reinterpret_cast<uint2*>(to + 2 * kHalfBytes) = lo;
-        }
-      };
-      uint4 v[8], u[8];
-      load(0, v);
-      load(8, u);
-      if (at < last) {  // the next unit's rows towards L2
-        Place after = w;
-        next_unit(p, after);
-        if (after.z * kRows + x0 + lane < p.count[after.e] * p.rep) {
-          const char* to = reinterpret_cast<const char*>(p.q + row_index(p, after, after.z * kRows + x0 + lane) * kHeadDim);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(to + 128 * k));
-        }
-      }
-      if (segment > 0 && !__all_sync(0xFFFFFFFFu, wait(q_free, segment - 1, kLostRows))) break;
-#pragma unroll 1
-      for (int i = 0; i < 32; i += 16) {  // a short loop: code for all rows at once would drive the others' out of the caches
-        cut(i, v);
-        if (i == 0) load(16, v);
-        cut(i + 8, u);
-        if (i == 0) load(24, u);
-      }
-      factor[(segment & 1) * kRows + x0 + lane] = clamp_finite(f * (p.scale * kLog2e));
-      proxy_fence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_ready[segment & 1]);
-    }
   } else {
     setmaxnreg_dec<kRestRegs>();
     if (warp == kLoader) {
@@ -446,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
         const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
         at += tiles + p.cost - w.j;
         if (n == 0) break;
-        ok = wait(&q_ready[segment & 1], segment / 2, kLostMma);
+        ok = wait(q_ready, segment, kLostMma);
         if (ok) scores(0);
         if (ok && n > 1) scores(1);
         if (ok && n <= 2) mma_commit(q_free);
@@ -475,6 +466,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       }
     }
     __syncwarp();
+    } else if (warp == kAsker && lane == 0) {
+      // ---------------------------------------------------------------- queries to shared memory
+      int segment = 0;
+      Place w = start;
+      for (int at = first; at < last; ++segment, next_unit(p, w)) {
+        const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
+        at += tiles + p.cost - w.j;
+        if (n == 0 || (segment > 0 && !wait(q_free, segment - 1, kLostLoad))) break;
+        mbar_arrive_expect_tx(q_ready, 4 * kHalfBytes);
+        const int y = (p.entry[w.e] * p.heads + w.h) * p.nq * p.rep + w.z * kRows;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // high parts, low parts; halves of the dims (rows behind the unit's are others', or zeros)
+          tensor2d_g2s(smem + kQ + k * kHalfBytes, &p.q_map, 128 * (k & 1), y + (k >> 1) * q_rows, q_ready, policy_evict_first());
+      }
+      if (segment > 0) wait.drain(q_ready, segment - 1);  // no copy left in flight
     }
   }
   __syncthreads();
@@ -486,9 +492,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
 
 }  // namespace
 
-cudaError_t launch_prefill(const AttendParams& p, int grid, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(paged_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  return e == cudaSuccess ? launch_after<AttendParams>(paged_prefill_kernel, dim3(grid), kThreads, kSmem, stream, p) : e;
+cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(paged_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  CutParams c;
+  c.q = p.q;
+  c.cut = p.cut;
+  c.factors = p.factors;
+  c.heads = p.heads;
+  c.rep = p.rep;
+  c.nq = p.nq;
+  c.total = p.slots_n * p.heads * p.rep * p.nq;
+  c.scale = p.scale;
+  for (int i = 0; i < p.slots_n; ++i) c.count[i] = counts[i];
+  if (e == cudaSuccess) e = launch_after<CutParams>(paged_cut_kernel, dim3((c.total + 31) / 32), 256, 0, stream, c);
+  if (e == cudaSuccess) e = launch_after<AttendParams>(paged_prefill_kernel, dim3(grid), kThreads, kSmem, stream, p);
+  return e;
 }
 
 }  // namespace paged
