@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
     // ---------------------------------------------------------------- softmax: a key per thread
     const int group = warp >> 2, key = threadIdx.x & 127, r0 = group * RT;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    if (threadIdx.x == 0) p.cuts[blockIdx.x].last = -1;
     float l[RT];
     int it = 0;
     bool ok = true;
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       const int k0 = part.begin, n = part.n, len = p.len[e], count = p.count[e], rows = count * p.rep;
       const bool whole = n == tiles.n;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
+      if (n > 0 && n < tiles.n && k0 == 0 && threadIdx.x == 0) tell_cut(p, at_unit, at, tiles.n, slot);
       at += tiles.n + p.cost - at_unit.j;
       if (n == 0) break;
       // the query rows, a warp each
@@ -373,39 +375,52 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   }
 }
 
-// Joins the partial results of the units that ranges cut: CTA (g, y) takes 8 rows
-// of the unit that range g + 1 begins inside of, where it is the first to do so; a
-// warp per row, a lane per 8 dims, the partials in the order of the ranges.
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ AttendParams p, int grid) {
+// Joins the partial results of the units that ranges cut, in the order of the
+// ranges.  CTA (g, y) takes `rows` rows of the unit that range g's end cuts, 8 /
+// rows warps each, a lane per 8 dims: one row where the partials are many
+// (eight warps share them, then add up through shared memory), eight where the
+// rows are.
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ AttendParams p, int rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int cut = range_begin(blockIdx.x + 1, grid, p.total);
-  const Place w = place_of(p, cut);
-  const int a = cut - w.j, n = tiles_at(p, w).n;
-  const int g0 = range_of(a + p.cost, grid, p.total), g1 = range_of(a + p.cost + n - 1, grid, p.total);
-  if (w.j <= p.cost || g0 != static_cast<int>(blockIdx.x)) return;
-  const int x = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, r = w.z * p.unit_rows + x;
-  if (x >= p.unit_rows || r >= p.count[w.e] * p.rep) return;
-  auto row = [&](int g) {
-    return static_cast<long long>(2 * g + (g == g0 && range_begin(g, grid, p.total) < a ? 1 : 0)) * p.unit_rows + x;
-  };
-  float m = -1e30f;  // every lane a partial, then the largest reference
-  for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, __ldcg(&p.part_ml[row(g)]).x);
+  const Cut cut = p.cuts[blockIdx.x];
+  if (cut.last < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = 8 / rows;
+  const int x = blockIdx.y * rows + warp / share, r = cut.z * p.unit_rows + x;
+  const bool live = x < p.unit_rows && r < p.count[cut.e] * p.rep;
+  auto row = [&](int g) { return static_cast<long long>(g == static_cast<int>(blockIdx.x) ? cut.slot : 2 * g) * p.unit_rows + x; };
+  __shared__ float part[8][kHeadDim + 2];
+  float m = -1e30f, sum = 0.0f, o[8] = {};
+  if (live) {
+    for (int g = blockIdx.x + lane; g <= cut.last; g += 32) m = fmaxf(m, __ldcg(&p.part_ml[row(g)]).x);  // every lane a partial
 #pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-  float sum = 0.0f, o[8] = {};
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
 #pragma unroll 4
-  for (int g = g0; g <= g1; ++g) {
-    const long long i = row(g);
-    const float2 ml = __ldcg(&p.part_ml[i]);
-    const float4* v = reinterpret_cast<const float4*>(p.part_o + i * kHeadDim + lane * 8);
-    const float4 v0 = __ldcg(v), v1 = __ldcg(v + 1);
-    const float f = ex2_approx(ml.x - m);
-    sum = fmaf(f, ml.y, sum);
-    o[0] = fmaf(f, v0.x, o[0]), o[1] = fmaf(f, v0.y, o[1]), o[2] = fmaf(f, v0.z, o[2]), o[3] = fmaf(f, v0.w, o[3]);
-    o[4] = fmaf(f, v1.x, o[4]), o[5] = fmaf(f, v1.y, o[5]), o[6] = fmaf(f, v1.z, o[6]), o[7] = fmaf(f, v1.w, o[7]);
+    for (int g = blockIdx.x + warp % share; g <= cut.last; g += share) {
+      const long long i = row(g);
+      const float2 ml = __ldcg(&p.part_ml[i]);
+      const float4* v = reinterpret_cast<const float4*>(p.part_o + i * kHeadDim + lane * 8);
+      const float4 v0 = __ldcg(v), v1 = __ldcg(v + 1);
+      const float f = ex2_approx(ml.x - m);
+      sum = fmaf(f, ml.y, sum);
+      o[0] = fmaf(f, v0.x, o[0]), o[1] = fmaf(f, v0.y, o[1]), o[2] = fmaf(f, v0.z, o[2]), o[3] = fmaf(f, v0.w, o[3]);
+      o[4] = fmaf(f, v1.x, o[4]), o[5] = fmaf(f, v1.y, o[5]), o[6] = fmaf(f, v1.z, o[6]), o[7] = fmaf(f, v1.w, o[7]);
+    }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  store_out8(p.out, p.out_f32, row_index(p, w, r) * kHeadDim + lane * 8, o, inv);
+  if (share > 1) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) part[warp][d * 32 + lane] = o[d];
+    if (lane == 0) part[warp][kHeadDim] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < 8; ++w) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] += part[w][d * 32 + lane];
+      sum += part[w][kHeadDim];
+    }
+  }
+  if (!live) return;
+  const Place w{cut.e, cut.h, cut.z, 0};
+  store_out8(p.out, p.out_f32, row_index(p, w, r) * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
 }
 
 // Rows of entries without a key: zeros.
@@ -506,7 +521,7 @@ int iq_paged_attend_workspace(const iq_paged* c, int q_heads, int n_queries, int
   if (static_cast<long long>(n_queries) * (q_heads / c->kv_heads) >= (1LL << 30)) return fail(IQ_ERR_UNSUPPORTED, "too many query rows");
   const int rows = n_queries * (q_heads / c->kv_heads);
   const size_t parts = rows > 0 && n_slots > 0 ? 2 * static_cast<size_t>(num_sms()) * unit_rows(rows) : 0;
-  *bytes = parts * (kHeadDim * sizeof(float) + sizeof(float2));
+  *bytes = parts ? parts * (kHeadDim * sizeof(float) + sizeof(float2)) + num_sms() * sizeof(Cut) : 0;
   if (rows > kMaxSplitRows) {  // the queries' two parts and factors
     const size_t all = static_cast<size_t>(n_slots) * q_heads * n_queries;
     if (all >= (1u << 30)) return fail(IQ_ERR_UNSUPPORTED, "too many query rows");
@@ -565,7 +580,7 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   const int grid = static_cast<int>(std::min<long long>(num_sms(), tiles));
   if (grid == 0) return IQ_OK;
   // short ranges are left at a tile's grain
-  p.cost = tiles >= 8ll * grid ? (p.unit_rows == 128 ? 3 : 1) : 0;
+  p.cost = tiles >= 8ll * grid ? (p.unit_rows == 128 ? 2 : 4) : 0;
   long long total = 0;
   for (int i = 0; i < n_slots; ++i) {
     const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
@@ -605,10 +620,11 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   p.scale = scale;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * num_sms() * p.unit_rows * kHeadDim);
+  p.cuts = reinterpret_cast<Cut*>(p.part_ml + 2ll * num_sms() * p.unit_rows);
   int all_counts[IQ_MAX_BATCH];
   if (p.unit_rows == 128) {
     const long long all = static_cast<long long>(n_slots) * q_heads * n_queries;
-    p.cut = reinterpret_cast<uint8_t*>(p.part_ml + 2ll * num_sms() * p.unit_rows);  // 16-byte aligned
+    p.cut = reinterpret_cast<uint8_t*>(p.cuts + num_sms());  // 16-byte aligned
     p.factors = reinterpret_cast<float*>(p.cut + all * 2 * kHeadDim);
     p.slots_n = n_slots;
     for (int i = 0; i < n_slots; ++i) all_counts[i] = counts ? counts[i] : n_queries;
@@ -619,8 +635,10 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
                     : p.unit_rows == 32 ? launch_split<32>(p, grid, cs)
                     : p.unit_rows == 64 ? launch_split<64>(p, grid, cs)
                                         : launch_prefill(p, all_counts, grid, cs);
-  if (err == cudaSuccess && grid > 1)
-    err = launch_after<AttendParams, int>(paged_join_kernel, dim3(grid - 1, std::min(p.unit_rows, rows + 7) / 8), 256, 0, cs, p, grid);
+  if (err == cudaSuccess && grid > 1) {
+    const int each = p.unit_rows == 128 ? 8 : 1, most = std::min(p.unit_rows, rows);
+    err = launch_after<AttendParams, int>(paged_join_kernel, dim3(grid - 1, (most + each - 1) / each), 256, 0, cs, p, each);
+  }
   return err == cudaSuccess ? IQ_OK : cuda_fail(err, "paged attention");
 }
 

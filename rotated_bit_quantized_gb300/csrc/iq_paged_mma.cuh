@@ -26,6 +26,12 @@ bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows, int box_ro
 // r % rep.  The key tiles of all units, laid end to end, are cut into gridDim
 // ranges of equal length, one for each CTA; a unit that lies in one range is
 // stored at once, the others leave a partial result per range.
+// A unit that lies in several ranges, told by the range that holds its first
+// tile: the slots of the partial results are `slot` and, for the ranges behind,
+// 2 g.  last < 0: the range's end cuts no unit that begins in it.
+struct Cut {
+  int last, slot, e, h, z, pad[3];
+};
 struct AttendParams {
   CUtensorMap k_map, v_map, q_map;  // (q_map: the prefill kernel's queries, cut beforehand)
   const float* k_scales;
@@ -36,6 +42,7 @@ struct AttendParams {
   void* out;
   float* part_o;    // [2 * grid][unit_rows][256] unnormalised partial results: a range's first segment, its last
   float2* part_ml;  // [2 * grid][unit_rows] their references and sums
+  Cut* cuts;        // [grid] the unit that a range's end cuts
   uint8_t* cut;     // prefill: [high, low parts][entry][kv head][row][256] e4m3
   float* factors;   // prefill: [entry][kv head][row] 2^e * scale * log2 e
   int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, cost, total, slots_n;
@@ -98,6 +105,12 @@ __device__ __forceinline__ Tiles tiles_at(const AttendParams& p, const Place& w)
   const int rows = p.count[w.e] * p.rep, r0 = w.z * p.unit_rows, before = p.len[w.e] - p.count[w.e];
   return tiles_of(p.len[w.e], before + query_of(p, r0), before + query_of(p, min(r0 + p.unit_rows, rows) - 1), p.causal, p.window,
                   p.sinks);
+}
+// For the joining kernel: the unit at w, whose first slot in the range is `at`,
+// of which the range takes all tiles from the first on, but not all.
+__device__ __forceinline__ void tell_cut(const AttendParams& p, const Place& w, int at, int tiles, int slot) {
+  const int end = at - w.j + p.cost + tiles - 1;  // the unit's last slot
+  p.cuts[blockIdx.x] = {range_of(end, gridDim.x, p.total), slot, w.e, w.h, w.z, {0, 0, 0}};
 }
 // Of slot t (a whole warp calls it together).
 __device__ inline Place place_of(const AttendParams& p, int t) {

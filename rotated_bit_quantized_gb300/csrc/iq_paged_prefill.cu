@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       if (ok) ok = wait(bar, phase, kLostRows);
       __syncwarp();
     };
+    if (threadIdx.x == 0) p.cuts[blockIdx.x].last = -1;
     // the unit whose results are still in tensor memory
     Place done{};
     bool pending = false, done_whole = false;
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int e = w.e, k0 = part.begin, len = p.len[e];
       const bool whole = n == tiles.n, exists = w.z * kRows + r < p.count[e] * p.rep;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
+      if (n > 0 && n < tiles.n && k0 == 0 && threadIdx.x == 0) tell_cut(p, w, at, tiles.n, slot);
       at += tiles.n + p.cost - w.j;
       const int pos = len - p.count[e] + query_of(p, w.z * kRows + r);
       const int stop = !exists ? 0 : p.causal ? pos + 1 : len;

@@ -41,16 +41,20 @@ struct AppendParams {
   Segment seg[kSegments];
 };
 
-__device__ __forceinline__ uint32_t drop_non_finite(uint32_t w, bool& odd) {
+// NaN: 0; infinity: the largest value of its sign.
+__device__ __forceinline__ uint32_t drop_non_finite(uint32_t w) {
 #pragma unroll
   for (int s = 0; s < 32; s += 16) {
     const uint32_t h = (w >> s) & 0x7FFFu;
-    if (h >= 0x7F80u) {  // NaN: 0; infinity: the largest value of its sign
-      odd = true;
-      w = (w & ~(0x7FFFu << s)) | ((h == 0x7F80u ? 0x7F7Fu : 0u) << s);
-    }
+    if (h >= 0x7F80u) w = (w & ~(0x7FFFu << s)) | ((h == 0x7F80u ? 0x7F7Fu : 0u) << s);
   }
   return w;
+}
+// The larger magnitude of both halves of eight bf16 values (they order as integers).
+__device__ __forceinline__ uint32_t magnitude(const uint4& x) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t t = __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
+  return max(t & 0xFFFFu, t >> 16);
 }
 
 // One CTA per (page of a segment, kv head, keys or values): 8 warps, a warp per
@@ -75,7 +79,6 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
 
   uint4 x[8];
   uint32_t top = 0;
-  bool odd = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = warp + 8 * i;
@@ -83,12 +86,14 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
     if (r >= begin && r < end) x[i] = __ldcs(reinterpret_cast<const uint4*>(in + static_cast<long long>(r) * kHeadDim));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+  for (int i = 0; i < 8; ++i) top = max(top, magnitude(x[i]));
+  bool odd = top >= 0x7F80u;
+  if (odd) {  // rare: make this thread's values finite, and find their maximum again
+    top = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = drop_non_finite(w[j], odd);
-      top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));  // bf16 magnitudes order as integers
+    for (int i = 0; i < 8; ++i) {
+      x[i] = make_uint4(drop_non_finite(x[i].x), drop_non_finite(x[i].y), drop_non_finite(x[i].z), drop_non_finite(x[i].w));
+      top = max(top, magnitude(x[i]));
     }
   }
   __shared__ uint32_t tops[8];
