@@ -24,6 +24,15 @@ int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, c
                  const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
                  const void* out, int out_f32, const void* workspace, size_t workspace_bytes);
 
+// A launch that may begin while the kernel before it ends; every kernel of the
+// paged cache waits for that one itself, before it touches memory.  args: one
+// pointer per parameter.
+cudaError_t launch_after(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args);
+__device__ __forceinline__ void wait_for_last_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Two floats to e4m3, to nearest even, saturating at +-448: `lo` in bits 0..7.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   unsigned short d;

@@ -105,8 +105,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(C::kTmem));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_last_kernel();
   tc_before();
   __syncthreads();
   tc_after();
@@ -341,27 +340,31 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
       await(&o_done[(it - 1) & 1], (it - 1) / 2);
       tc_after();
       named_bar(3, 128 * C::kGroups);
-      for (int half = group; half < 2; half += C::kGroups) {
-        const int d = half * 128 + key;
 #pragma unroll 1
-        for (int x = 0; x < rows; x += 8) {
-          float o[8], o2[8];
-          tmem_ld<8>(t_o + lanes + half * C::kCols + x, o);
-          tmem_ld<8>(t_o + lanes + half * C::kCols + NR + x, o2);
-          ld_wait();
+      for (int x = 0; x < rows; x += 8) {
+        float o[2][16];  // both halves of the dims, or this group's: high parts, low parts
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const int r = x + y;
-            if (r >= rows) break;
-            const float v = fmaf(o2[y], 1.0f / kPLo, o[y]);
-            if (whole) {
-              const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
-              store_out(p.out, p.out_f32, row_index(p, at_unit, r) * kHeadDim + d, sum == 0.0f ? 0.0f : v / sum);
-            } else {
-              p.part_o[(static_cast<long long>(slot) * NR + r) * kHeadDim + d] = v;
-              if (d == 0) p.part_ml[slot * NR + r] = make_float2(ref[r], red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r]);
-            }
+        for (int i = 0; i < 2 / C::kGroups; ++i) {
+          const uint32_t c = t_o + lanes + (C::kGroups == 2 ? group : i) * C::kCols + x;
+          tmem_ld<8>(c, o[i]);
+          tmem_ld<8>(c + NR, o[i] + 8);
+        }
+        ld_wait();
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int r = x + y;
+          if (r >= rows) break;
+          const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const long long to = whole ? row_index(p, at_unit, r) * kHeadDim : (static_cast<long long>(slot) * NR + r) * kHeadDim;
+#pragma unroll
+          for (int i = 0; i < 2 / C::kGroups; ++i) {
+            const int d = (C::kGroups == 2 ? group : i) * 128 + key;
+            const float v = fmaf(o[i][8 + y], 1.0f / kPLo, o[i][y]);
+            if (whole) store_out(p.out, p.out_f32, to + d, v * inv);
+            else p.part_o[to + d] = v;
           }
+          if (!whole && threadIdx.x == 0) p.part_ml[slot * NR + r] = make_float2(ref[r], sum);
         }
       }
       tc_before();
@@ -380,12 +383,21 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
 // rows warps each, a lane per 8 dims: one row where the partials are many
 // (eight warps share them, then add up through shared memory), eight where the
 // rows are.
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ AttendParams p, int rows) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+struct JoinParams {
+  const float* part_o;
+  const float2* part_ml;
+  const Cut* cuts;
+  void* out;
+  int out_f32, heads, rep, nq, unit_rows, rows;
+  short entry[IQ_MAX_BATCH];
+  int count[IQ_MAX_BATCH];
+};
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ JoinParams p) {
+  wait_for_last_kernel();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.last < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = 8 / rows;
-  const int x = blockIdx.y * rows + warp / share, r = cut.z * p.unit_rows + x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = 8 / p.rows;
+  const int x = blockIdx.y * p.rows + warp / share, r = cut.z * p.unit_rows + x, j = r / p.rep;
   const bool live = x < p.unit_rows && r < p.count[cut.e] * p.rep;
   auto row = [&](int g) { return static_cast<long long>(g == static_cast<int>(blockIdx.x) ? cut.slot : 2 * g) * p.unit_rows + x; };
   __shared__ float part[8][kHeadDim + 2];
@@ -419,8 +431,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     }
   }
   if (!live) return;
-  const Place w{cut.e, cut.h, cut.z, 0};
-  store_out8(p.out, p.out_f32, row_index(p, w, r) * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
+  const long long to = static_cast<long long>((p.entry[cut.e] * p.heads + cut.h) * p.rep + r - j * p.rep) * p.nq + j;
+  store_out8(p.out, p.out_f32, to * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
 }
 
 // Rows of entries without a key: zeros.
@@ -431,6 +443,7 @@ struct ZeroParams {
   int count[IQ_MAX_BATCH];
 };
 __global__ void __launch_bounds__(256) paged_zero_kernel(const __grid_constant__ ZeroParams p) {
+  wait_for_last_kernel();
   const int pieces = kHeadDim * p.out_bytes / 16;
   const long long n = static_cast<long long>(p.count[blockIdx.y]) * pieces;
   for (int h = 0; h < p.q_heads; ++h) {
@@ -460,11 +473,37 @@ int unit_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 
 template <int NR>
 cudaError_t launch_split(const AttendParams& p, int grid, cudaStream_t stream) {
   using C = SplitShape<NR>;
-  const cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  return e == cudaSuccess ? launch_after<AttendParams>(paged_split_kernel<NR>, dim3(grid), C::kThreads, C::kSmem, stream, p) : e;
+  static std::atomic<uint64_t> seen{0};
+  const void* kernel = reinterpret_cast<const void*>(&paged_split_kernel<NR>);
+  const cudaError_t e = allow_smem(kernel, C::kSmem, seen);
+  void* args[] = {const_cast<AttendParams*>(&p)};
+  return e == cudaSuccess ? launch_after(kernel, dim3(grid), C::kThreads, C::kSmem, stream, args) : e;
 }
 
 }  // namespace
+
+cudaError_t launch_after(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& seen) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && seen.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) seen.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows, int box_rows) {
   const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(rows)}, strides[1] = {kHeadDim};
@@ -553,8 +592,8 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
       most = std::max(most, count);
     }
     if (n > 0) {
-      paged_zero_kernel<<<dim3(std::min(64, (most + 7) / 8), n), 256, 0, cs>>>(z);
-      IQ_CUDA(cudaGetLastError());
+      void* args[] = {&z};
+      IQ_CUDA(launch_after(reinterpret_cast<const void*>(&paged_zero_kernel), dim3(std::min(64, (most + 7) / 8), n), 256, 0, cs, args));
     }
   }
   AttendParams p;
@@ -637,7 +676,21 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
                                         : launch_prefill(p, all_counts, grid, cs);
   if (err == cudaSuccess && grid > 1) {
     const int each = p.unit_rows == 128 ? 8 : 1, most = std::min(p.unit_rows, rows);
-    err = launch_after<AttendParams, int>(paged_join_kernel, dim3(grid - 1, (most + each - 1) / each), 256, 0, cs, p, each);
+    JoinParams j;
+    j.part_o = p.part_o;
+    j.part_ml = p.part_ml;
+    j.cuts = p.cuts;
+    j.out = p.out;
+    j.out_f32 = p.out_f32;
+    j.heads = p.heads;
+    j.rep = p.rep;
+    j.nq = p.nq;
+    j.unit_rows = p.unit_rows;
+    j.rows = each;
+    std::memcpy(j.entry, p.entry, sizeof(j.entry));
+    std::memcpy(j.count, p.count, sizeof(j.count));
+    void* args[] = {&j};
+    err = launch_after(reinterpret_cast<const void*>(&paged_join_kernel), dim3(grid - 1, (most + each - 1) / each), 256, 0, cs, args);
   }
   return err == cudaSuccess ? IQ_OK : cuda_fail(err, "paged attention");
 }

@@ -5,6 +5,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "iq_paged.cuh"
 
 namespace iq {
@@ -168,21 +170,8 @@ __device__ __forceinline__ long long row_index(const AttendParams& p, const Plac
 // counts: of every entry of the call, also those without keys
 cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream);
 
-// A launch that may begin while the kernel before it ends (it waits itself).
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
+// Shared memory above 48 KB, allowed once per kernel and device (`seen`: the kernel's own).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& seen);
 
 // Waits end: after a second (no stage takes a thousandth of it) the CTA's
 // abort flag is raised, every later wait of the CTA returns at once, and the

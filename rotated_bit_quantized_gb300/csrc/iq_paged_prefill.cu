@@ -99,8 +99,7 @@ struct CutParams {
   int count[IQ_MAX_BATCH];
 };
 __global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ CutParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_last_kernel();
   const int lane = threadIdx.x & 31, w0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4, rows = p.nq * p.rep;
   uint4 raw[4];
 #pragma unroll
@@ -174,8 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_last_kernel();
   tc_before();
   __syncthreads();
   tc_after();
@@ -495,7 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(paged_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> seen{0};
+  const void* kernel = reinterpret_cast<const void*>(&paged_prefill_kernel);
+  cudaError_t e = allow_smem(kernel, kSmem, seen);
   CutParams c;
   c.q = p.q;
   c.cut = p.cut;
@@ -506,8 +506,10 @@ cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, c
   c.total = p.slots_n * p.heads * p.rep * p.nq;
   c.scale = p.scale;
   for (int i = 0; i < p.slots_n; ++i) c.count[i] = counts[i];
-  if (e == cudaSuccess) e = launch_after<CutParams>(paged_cut_kernel, dim3((c.total + 31) / 32), 256, 0, stream, c);
-  if (e == cudaSuccess) e = launch_after<AttendParams>(paged_prefill_kernel, dim3(grid), kThreads, kSmem, stream, p);
+  void* cut_args[] = {&c};
+  void* args[] = {const_cast<AttendParams*>(&p)};
+  if (e == cudaSuccess) e = launch_after(reinterpret_cast<const void*>(&paged_cut_kernel), dim3((c.total + 31) / 32), 256, 0, stream, cut_args);
+  if (e == cudaSuccess) e = launch_after(kernel, dim3(grid), kThreads, kSmem, stream, args);
   return e;
 }
 

@@ -61,6 +61,7 @@ __device__ __forceinline__ uint32_t magnitude(const uint4& x) {
 // row, a lane per 8 dims, the page's new rows (32 KB at most) held in registers
 // between the maximum and the rounding, so every row is read once.
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ AppendParams p) {
+  wait_for_last_kernel();
   const Segment sg = p.seg[blockIdx.z];
   const int k = blockIdx.x, h = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
@@ -168,6 +169,7 @@ struct ReadParams {
 
 // A warp per row of (entry, kv head), keys and values; a lane per 8 dims.
 __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ ReadParams p) {
+  wait_for_last_kernel();
   const int lane = threadIdx.x & 31, h = blockIdx.y, i = blockIdx.z;
   const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= p.n) return;
@@ -205,6 +207,7 @@ struct ForkParams {
 // A CTA takes 32 columns of the table for every pair: all sources are read
 // before any row is written, so a permutation of slots needs no second table.
 __global__ void __launch_bounds__(256) paged_fork_kernel(const __grid_constant__ ForkParams p) {
+  wait_for_last_kernel();
   __shared__ int rows[IQ_MAX_BATCH][32];
   const int lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane;
   for (int i = threadIdx.x >> 5; i < p.count; i += 8)
@@ -239,6 +242,7 @@ struct CompactParams {
 // Blocks [0, pages * 2 * heads): 16 KB each, a page of one kv head, keys or
 // values, and its scale.  The blocks behind them: a run of table entries each.
 __global__ void __launch_bounds__(256) paged_compact_kernel(const __grid_constant__ CompactParams p) {
+  wait_for_last_kernel();
   const long long copies = static_cast<long long>(p.pages) * 2 * p.heads;
   if (blockIdx.x >= copies) {
     const int r = static_cast<int>(blockIdx.x - copies);
@@ -351,8 +355,9 @@ int do_append(iq_paged* c, const void* keys, const void* values, int n, const in
   cudaError_t err = cudaSuccess;
   auto launch = [&]() {
     if (segs && err == cudaSuccess) {
-      paged_append_kernel<<<dim3(widest, 2 * c->kv_heads, segs), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-      err = cudaGetLastError();
+      void* args[] = {&p};
+      err = launch_after(reinterpret_cast<const void*>(&paged_append_kernel), dim3(widest, 2 * c->kv_heads, segs), 256, 0,
+                         static_cast<cudaStream_t>(stream), args);
     }
     segs = widest = 0;
   };
@@ -537,8 +542,9 @@ int iq_paged_read(const iq_paged* c, const int32_t* slots, const int32_t* start,
     p.start[i] = start[i];
     p.len[i] = c->lens[p.slot[i]];
   }
-  paged_read_kernel<<<dim3((n + 7) / 8, c->kv_heads, n_slots), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  IQ_CUDA(cudaGetLastError());
+  void* args[] = {&p};
+  IQ_CUDA(launch_after(reinterpret_cast<const void*>(&paged_read_kernel), dim3((n + 7) / 8, c->kv_heads, n_slots), 256, 0,
+                       static_cast<cudaStream_t>(stream), args));
   return IQ_OK;
 }
 
@@ -591,8 +597,9 @@ int iq_paged_fork(iq_paged* c, const int32_t* src, const int32_t* dst, int count
   int32_t* rows = new (std::nothrow) int32_t[total + 1];
   if (!rows) return fail(IQ_ERR_CAPACITY, "no host memory for the forked rows");
   if (widest > 0) {
-    paged_fork_kernel<<<(widest + 31) / 32, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t err = cudaGetLastError();
+    void* args[] = {&p};
+    const cudaError_t err =
+        launch_after(reinterpret_cast<const void*>(&paged_fork_kernel), dim3((widest + 31) / 32), 256, 0, static_cast<cudaStream_t>(stream), args);
     if (err != cudaSuccess) {
       delete[] rows;
       return cuda_fail(err, "paged fork");
@@ -651,8 +658,9 @@ int iq_paged_compact(const iq_paged* src, iq_paged* dst, iq_stream_t stream) {
   auto launch = [&]() {
     const long long blocks = static_cast<long long>(p.pages) * 2 * p.heads + p.table_runs;
     if (blocks && err == cudaSuccess) {
-      paged_compact_kernel<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-      err = cudaGetLastError();
+      void* args[] = {&p};
+      err = launch_after(reinterpret_cast<const void*>(&paged_compact_kernel), dim3(static_cast<unsigned>(blocks)), 256, 0,
+                         static_cast<cudaStream_t>(stream), args);
     }
     p.pages = p.page_runs = p.table_runs = run_len = 0;
   };

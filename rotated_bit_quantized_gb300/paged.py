@@ -95,7 +95,7 @@ class IQPagedCache:
         self._lens = np.zeros(slots, dtype=np.int32)
         self._table = np.zeros((slots, self.max_pages), dtype=np.int32)
         self._refs = np.zeros(pages, dtype=np.int32)
-        self._need, self._scale = {}, 1.0 / math.sqrt(head_dim)
+        self._need, self._scratch, self._scale = {}, {}, 1.0 / math.sqrt(head_dim)
         self._desc = IQPagedDesc()
         self._d = ctypes.byref(self._desc)
         check(lib().iq_paged_alloc(self._d, slots, kv_heads, head_dim, pages, self.max_pages,
@@ -184,9 +184,9 @@ class IQPagedCache:
             raise ValueError("out must have q's shape and device, and out_dtype")
         return out
 
-    def _workspace(self, q_heads: int, rows: int, entries: int):
-        """Scratch for one call, from PyTorch's allocator: its own for every call, so
-        that calls on different streams, or in two captured graphs, do not share it."""
+    def _workspace(self, q_heads: int, rows: int, entries: int, stream):
+        """Scratch for a call on `stream`: one per stream, kept, as work on one stream is in order;
+        for a captured call its own, as graphs captured on one stream may run at once."""
         key = (q_heads, rows, entries)
         need = self._need.get(key)
         if need is None:
@@ -195,7 +195,14 @@ class IQPagedCache:
             if len(self._need) > 256:
                 self._need.clear()
             need = self._need[key] = c.value
-        return torch.empty(need, dtype=torch.uint8, device=self.device), need
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        ws = self._scratch.get(stream)
+        if ws is None or ws.numel() < need:
+            if len(self._scratch) > 16:
+                self._scratch.clear()
+            ws = self._scratch[stream] = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=self.device)
+        return ws
 
     # ---------------------------------------------------------------- rows
     def append(self, keys: torch.Tensor, values: torch.Tensor, slots=None, counts=None) -> None:
@@ -273,10 +280,11 @@ class IQPagedCache:
         E, Hq, L, D = q.shape
         slots, counts = self._entries(E, slots, counts)
         out = self._outputs(q, counts, out, out_dtype)
-        ws, need = self._workspace(Hq, L, E)
+        stream = self._queue()
+        ws = self._workspace(Hq, L, E, stream)
         self._run(self._lib.iq_paged_attend, self._d, q.data_ptr(), Hq, L, _at(slots), _at(counts), E,
                   self._scale if scale is None else scale, 1 if causal else 0, window, sinks, out.data_ptr(),
-                  1 if out.dtype is torch.float32 else 0, ws.data_ptr(), need, self._queue())
+                  1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
         return out
 
     def append_attend(self, keys: torch.Tensor, values: torch.Tensor, q: torch.Tensor, causal: bool = True,
@@ -291,8 +299,9 @@ class IQPagedCache:
             raise ValueError("keys/values and q must have the same entries")
         slots, counts = self._entries(E, slots, counts)
         out = self._outputs(q, counts, out, out_dtype)
-        ws, need = self._workspace(Hq, L, E)
+        stream = self._queue()
+        ws = self._workspace(Hq, L, E, stream)
         self._run(self._lib.iq_paged_append_attend, self._d, keys.data_ptr(), values.data_ptr(), keys.shape[2], q.data_ptr(), Hq, L,
                   _at(slots), _at(counts), E, self._scale if scale is None else scale, 1 if causal else 0, window, sinks,
-                  out.data_ptr(), 1 if out.dtype is torch.float32 else 0, ws.data_ptr(), need, self._queue())
+                  out.data_ptr(), 1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
         return out
