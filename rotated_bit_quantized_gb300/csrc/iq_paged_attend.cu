@@ -46,7 +46,7 @@ struct SplitShape {
   static constexpr int kQ = kSlots * kSlotBytes;      // [2 halves of the dims][kCols rows][128 bytes]
   static constexpr int kP = kQ + 2 * kCols * 128;     // [2][kCols rows][128 keys]
   static constexpr int kMisc = kP + 2 * kCols * 128;
-  static constexpr int kRing = Loader<kSlots>::kRing;
+  static constexpr int kRing = Loader<kSlots, false>::kRing;
   static constexpr int kFloats = 2 * NR + 4 * NR;     // factors, references; reductions
   static constexpr int kBars = 2 * kSlots + kRing + 10;
   static constexpr int kSmem = 1024 + kMisc + kFloats * 4 + kRing * 16 + kBars * 8 + 8;
@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   const Place start = place_of(p, first);  // every role walks the same segments from here
 
   if (warp == kLoader) {
-    Loader<C::kSlots>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy_evict_first());
+    Loader<C::kSlots, false>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy_evict_first());
   } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
+    {
       constexpr uint32_t kS = shape(128, C::kCols, false, false), kO = shape(128, C::kCols, true, false);
       // descriptors count in 16 bytes: those of other pieces are sums
       const uint64_t queries = operand(sbase + C::kQ), weights = operand(sbase + C::kP), at_slot = operand(sbase);
@@ -131,12 +131,12 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
         at += tiles + p.cost - w.j;
         if (n == 0) break;
-        ok = wait(q_ready, segment, kLostMma);
+        ok = wait.together(q_ready, segment, kLostMma);
         for (int j = 0; j <= n && ok; ++j) {
           if (j < n) {
             const int b = (it + j) & 1, s = used % C::kSlots;
-            if (it + j >= 2) ok = wait(&s_free[b], (it + j) / 2 - 1, kLostMma);
-            ok = ok && wait(&full[s], used / C::kSlots, kLostMma);
+            if (it + j >= 2) ok = wait.together(&s_free[b], (it + j) / 2 - 1, kLostMma);
+            ok = ok && wait.together(&full[s], used / C::kSlots, kLostMma);
             if (!ok) break;
             tc_after();
 #pragma unroll
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
           }
           if (j > 0) {
             const int b = (it + j - 1) & 1, s = used % C::kSlots;
-            ok = wait(&p_ready[b], (it + j - 1) / 2, kLostMma) && wait(&full[s], used / C::kSlots, kLostMma);
+            ok = wait.together(&p_ready[b], (it + j - 1) / 2, kLostMma) && wait.together(&full[s], used / C::kSlots, kLostMma);
             if (!ok) break;
             tc_after();
 #pragma unroll
@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         wait.drain(drained, 0);
       }
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax: a key per thread
     const int group = warp >> 2, key = threadIdx.x & 127, r0 = group * RT;

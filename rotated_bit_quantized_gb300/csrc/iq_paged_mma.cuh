@@ -199,6 +199,10 @@ struct Waits {
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, unsigned bit) const {
     return mbar_try_wait(bar, parity & 1, 20000u) || slow(bar, parity & 1, bit);
   }
+  // for a warp that runs as one: the same answer to every lane
+  __device__ __forceinline__ bool together(uint64_t* bar, uint32_t parity, unsigned bit) const {
+    return __all_sync(0xFFFFFFFFu, (*this)(bar, parity, bit));
+  }
   // the same whether or not the CTA has given up: for what is in flight at the end
   __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
     const unsigned long long t0 = now_ns();
@@ -222,16 +226,29 @@ __host__ __device__ constexpr uint32_t shape(int m, int n, bool a_mn, bool b_mn)
   return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
+// The products are issued by a whole warp that runs as one, an elected lane (always
+// the same) executing them: their operands then live in uniform registers.  From
+// a lane that runs alone each operand is moved there first, and next to the row
+// threads' work the issue, not the tensor cores, sets the pace.
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
       : "memory");
 }
+__device__ __forceinline__ void mma_e4m3_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {  // A in tensor memory
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -241,13 +258,14 @@ __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.
 
 // The loading warp of an attention kernel (a whole warp): streams the key and
 // value tiles of a range's segments through a ring of SLOTS shared-memory slots,
-// in the order of the products, K0, K1, V0, K2, V1, ... per segment, and hands
+// in the order of the products, K0, K1, V0, K2, V1, ... (each segment to its
+// end, or ACROSS segments as one stream), and hands
 // the tiles' page scales to the row threads through a ring of their own, so
 // that those touch no global memory between a segment's begin and its end (a
 // load under a saturated HBM takes a tile's time and more).  A lane holds the
 // id and the scales of one page of 16 tiles.  Ids are fetched 16 tiles or two
 // segments ahead, scales half of that.
-template <int SLOTS>
+template <int SLOTS, bool ACROSS>
 struct Loader {
   // a tile's scales live until its weights are written: with 5 slots K(j + 4) waits for the values of
   // tile j, with 6 K(j + 8) for the scores of tile j + 5, which wait for the weights of tile j + 3
@@ -292,7 +310,7 @@ struct Loader {
 
   __device__ __forceinline__ void run(Place w, int first, int last, uint64_t policy) const {
     const int lane = threadIdx.x & 31;
-    int issued = 0, it = 0;
+    int issued = 0, it = 0, v0 = 0, v1 = 0, v_head = -1;  // (the tile whose values come next)
     bool ok = true;
     auto load = [&](const CUtensorMap* map, int id0, int id1, int h) {
       const int s = issued % SLOTS;
@@ -316,7 +334,7 @@ struct Loader {
     int ids = g.n > 0 ? page_in_pool(fetch(g, 0), p.pages, p.status) : 0, ids1 = g1.n > 0 ? fetch(g1, 0) : 0;
     float2 sc = g.n > 0 ? scales_of(g, ids) : make_float2(1.0f, 1.0f);
     while (ok && g.n > 0) {
-      int next = g.n > 16 ? fetch(g, 16) : 0, v0 = 0, v1 = 0;
+      int next = g.n > 16 ? fetch(g, 16) : 0;
       float2 next_sc = sc, sc1 = sc;
       if (g1.n > 0) {
         ids1 = page_in_pool(ids1, p.pages, p.status);
@@ -324,35 +342,36 @@ struct Loader {
       }
       const Segment g2 = take(w, at, last);
       const int ids2 = g2.n > 0 ? fetch(g2, 0) : 0;
-      for (int j = 0; j <= g.n && ok; ++j) {
-        int k0 = 0, k1 = 0;
-        if (j < g.n) {
-          if (j % 16 == 0 && j > 0) {
-            ids = next;
-            sc = next_sc;
-            if (j + 16 < g.n) next = fetch(g, j + 16);
-          }
-          if (j % 16 == 8 && j + 8 < g.n) {
-            next = page_in_pool(next, p.pages, p.status);
-            next_sc = scales_of(g, next);
-          }
-          k0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16));
-          k1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16) + 1);
-          load(&p.k_map, k0, k1, g.h);
-          if (!ok) break;
-          const int x = lane - 2 * (j % 16);
-          if (x == 0 || x == 1) {
-            float* to = reinterpret_cast<float*>(&scales[it % kRing]);
-            to[x] = sc.x;
-            to[2 + x] = sc.y;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&scales_in[it % kRing]);
-          ++it;
+      for (int j = 0; j < g.n && ok; ++j) {
+        if (j % 16 == 0 && j > 0) {
+          ids = next;
+          sc = next_sc;
+          if (j + 16 < g.n) next = fetch(g, j + 16);
         }
-        if (j > 0) load(&p.v_map, v0, v1, g.h);
-        v0 = k0;
-        v1 = k1;
+        if (j % 16 == 8 && j + 8 < g.n) {
+          next = page_in_pool(next, p.pages, p.status);
+          next_sc = scales_of(g, next);
+        }
+        const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16) + 1);
+        load(&p.k_map, id0, id1, g.h);
+        if (!ok) break;
+        const int x = lane - 2 * (j % 16);
+        if (x == 0 || x == 1) {
+          float* to = reinterpret_cast<float*>(&scales[it % kRing]);
+          to[x] = sc.x;
+          to[2 + x] = sc.y;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scales_in[it % kRing]);
+        ++it;
+        if (v_head >= 0) load(&p.v_map, v0, v1, v_head);
+        v0 = id0;
+        v1 = id1;
+        v_head = g.h;
+      }
+      if (!ACROSS && ok) {
+        load(&p.v_map, v0, v1, v_head);
+        v_head = -1;
       }
       g = g1;
       ids = ids1;
@@ -360,6 +379,7 @@ struct Loader {
       g1 = g2;
       ids1 = ids2;
     }
+    if (ACROSS && ok && v_head >= 0) load(&p.v_map, v0, v1, v_head);
     if (lane == 0)  // no copy left in flight
       for (int s = 0; s < SLOTS && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / SLOTS);
   }

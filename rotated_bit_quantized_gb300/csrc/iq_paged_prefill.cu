@@ -28,7 +28,7 @@ constexpr int kRows = 128;
 constexpr int kSlots = 5;                         // tiles of keys or values in flight
 constexpr int kQ = kSlots * kSlotBytes;           // [high, low][2 halves of the dims][128 rows][128 bytes]
 constexpr int kMisc = kQ + 4 * kHalfBytes;
-constexpr int kRing = Loader<kSlots>::kRing;
+constexpr int kRing = Loader<kSlots, true>::kRing;
 constexpr int kSmem = kMisc + 2 * kRows * 4 + kRing * 16 + 32 * 8;
 constexpr int kThreads = 384;
 constexpr int kLoader = 8, kIssuer = 9, kAsker = 10;
@@ -36,13 +36,6 @@ constexpr int kRowRegs = 208, kRestRegs = 88;     // 2 * 208 + 88 = 3 * 168, wha
 constexpr float kPlace = 5.0f, kTop = 8.75f;      // the running maximum's place, and how far a weight may grow (448 = 2^8.8)
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
-__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
-      : "memory");
-}
 __device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -66,24 +59,6 @@ __host__ __device__ constexpr int reversed6(int c) {
 }
 __host__ __device__ constexpr uint32_t cut_at(int c) {  // (reversed / 64 - 63 / 128) steps
   return half_bits(2 * reversed6(c) - 63) | half_bits(2 * reversed6(c + 1) - 63) << 16;
-}
-
-// Four 16-byte pieces per lane, transposed among groups of four lanes: piece k
-// of lane i becomes piece i of lane k.
-__device__ __forceinline__ void transpose4(uint32_t (&c)[16], int lane) {
-#pragma unroll
-  for (int d = 1; d <= 2; d <<= 1)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k & d) continue;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t mine = lane & d ? c[4 * k + x] : c[4 * (k + d) + x];
-        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, mine, d);
-        if (lane & d) c[4 * k + x] = got;
-        else c[4 * (k + d) + x] = got;
-      }
-    }
 }
 
 // The queries' two parts and factors, a warp per four rows, before the kernel
@@ -209,41 +184,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int rows = min(kRows, p.count[done.e] * p.rep - done.z * kRows);
       const float inv = !done_whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
       const bool wide = !done_whole || p.out_f32;
-      uint8_t* base = static_cast<uint8_t*>(done_whole ? p.out : p.part_o) + ((lane & 3) * 16 + group * (wide ? 512 : 256));
-      long long to[4];  // the rows that this lane stores pieces of
-      const long long mine = done_whole ? row_index(p, done, done.z * kRows + min(r, rows - 1)) : static_cast<long long>(done_slot) * kRows + r;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) + k) * (wide ? 1024 : 512);
+      const long long to = done_whole ? row_index(p, done, done.z * kRows + min(r, rows - 1)) : static_cast<long long>(done_slot) * kRows + r;
+      uint8_t* out = static_cast<uint8_t*>(done_whole ? p.out : p.part_o) + (to * kHeadDim + group * 128) * (wide ? 4 : 2);
       await(&o_done[last_tile & 1], last_tile / 2);
       tc_after();
+      // a thread stores whole 32-byte pieces of its row: rows 16 bytes at a time
+      // through shuffles, for wider pieces of a line per instruction, were slower
 #pragma unroll 1
       for (int c = 0; c < 128; c += 64) {
         float o[64];
         tmem_ld<32>(t_o + lanes + group * 128 + c, o);
         tmem_ld<32>(t_o + lanes + group * 128 + c + 32, o + 32);
         ld_wait();
-        uint32_t x[16];
-        auto store = [&](int byte) {  // 16 words of this lane's row become 16 bytes of each of four rows, next to its neighbours'
-          transpose4(x, lane);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if ((r & ~3) + k < rows)
-              *reinterpret_cast<uint4*>(base + to[k] + byte) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-        };
+        if (r >= rows) continue;
         if (wide) {
 #pragma unroll
-          for (int part = 0; part < 4; ++part) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[part * 16 + i] * inv);
-            store((c + part * 16) * 4);
-          }
+          for (int i = 0; i < 64; i += 4)
+            *reinterpret_cast<float4*>(out + (c + i) * 4) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
         } else {
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
+          for (int i = 0; i < 64; i += 8) {
+            uint32_t x[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(o[part * 32 + 2 * i + 1] * inv), "f"(o[part * 32 + 2 * i] * inv));
-            store((c + part * 32) * 2);
+            for (int k = 0; k < 4; ++k)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[k]) : "f"(o[i + 2 * k + 1] * inv), "f"(o[i + 2 * k] * inv));
+            *reinterpret_cast<uint4*>(out + (c + i) * 2) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
       }
@@ -409,18 +374,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
     if (warp == kLoader) {
       uint64_t policy;  // other row tiles read the same pages
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-      Loader<kSlots>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy);
+      Loader<kSlots, true>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy);
     } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
       constexpr uint32_t kS = shape(128, kTile, false, false), kO = shape(128, kHeadDim, false, true);
-      int it = 0, used = 0, segment = 0;
+      int used = 0;
       bool ok = true;
       // descriptors count in 16 bytes: those of other pieces are sums
       const uint64_t queries = operand(sbase + kQ), at_slot = operand(sbase), at_values = operand(sbase, kHalfBytes);
-      auto scores = [&](int j) {  // S of the segment's tile j
-        const int b = (it + j) & 1, s = used % kSlots;
-        ok = wait(&full[s], used / kSlots, kLostMma);
+      // the scores run two tiles ahead, over the segments' ends
+      Place ws = start;
+      int at_s = first, left = 0, tile = 0, segment = 0;
+      auto scores = [&]() {  // S of the next tile, if there is one
+        if (left == 0) {
+          if (at_s >= last) return;
+          const int tiles = tiles_at(p, ws).n;
+          left = part_of(p, ws, tiles, last - at_s).n;
+          at_s += tiles + p.cost - ws.j;
+          next_unit(p, ws);
+          if (left == 0) return;
+          ok = wait.together(q_ready, segment++, kLostMma);
+        }
+        const int b = tile++ & 1, s = used % kSlots;
+        ok = ok && wait.together(&full[s], used / kSlots, kLostMma);
         if (!ok) return;
         tc_after();
         const uint64_t keys = at_slot + s * (kSlotBytes >> 4);
@@ -430,42 +406,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
                    keys + ((((k >> 2) & 1) * kHalfBytes + (k & 3) * 32) >> 4), kS, k > 0);
         mma_commit(&s_full[b]);
         mma_commit(&empty[s]);
+        if (--left == 0) mma_commit(q_free);
         ++used;
       };
       Place w = start;
-      for (int at = first; at < last && ok; ++segment, next_unit(p, w)) {
-        const int tiles = tiles_at(p, w).n, n = part_of(p, w, tiles, last - at).n;
-        at += tiles + p.cost - w.j;
-        if (n == 0) break;
-        ok = wait(q_ready, segment, kLostMma);
-        if (ok) scores(0);
-        if (ok && n > 1) scores(1);
-        if (ok && n <= 2) mma_commit(q_free);
-        for (int j = 0; j < n && ok; ++j) {
-          const int b = (it + j) & 1, s = used % kSlots;
-          ok = wait(&p_ready[b], (it + j) / 2, kLostMma) && wait(&full[s], used / kSlots, kLostMma);
+      int at = first, n = 0, j = 0;
+      for (int it = -2; ok; ++it) {
+        if (it >= 0) {
+          if (j == n) {  // the next segment
+            if (at >= last) break;
+            const int tiles = tiles_at(p, w).n;
+            n = part_of(p, w, tiles, last - at).n;
+            at += tiles + p.cost - w.j;
+            next_unit(p, w);
+            if (n == 0) break;
+            j = 0;
+          }
+          const int b = it & 1, s = used % kSlots;
+          ok = wait.together(&p_ready[b], it / 2, kLostMma) && wait.together(&full[s], used / kSlots, kLostMma);
           if (!ok) break;
           tc_after();
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // high and low parts in turn, 32 keys at a time (so that one read of V may serve both)
-            mma_tmem_a(t_o, tmem + b * 128 + (k >> 2) * 64 + ((k >> 1) & 1) * 8 + (k & 1) * 16,
+          for (int k = 0; k < 8; ++k)  // 32 keys at a time, their high and low parts in turn
+            mma_e4m3_tmem(t_o, tmem + b * 128 + (k >> 2) * 64 + ((k >> 1) & 1) * 8 + (k & 1) * 16,
                        at_values + ((s * kSlotBytes + (k >> 1) * 32 * 128) >> 4), kO, j > 0 || k > 0);
           mma_commit(&o_done[b]);
           mma_commit(&empty[s]);
           ++used;
-          if (j + 2 < n) {
-            scores(j + 2);  // runs behind O of this tile, whose weights it overwrites
-            if (ok && j + 3 == n) mma_commit(q_free);
-          }
+          ++j;
         }
-        it += n;
+        scores();  // runs behind O of this tile, whose weights it overwrites
       }
       if (!ok) {  // given up: what is in flight ends before the tensor memory goes
         mma_commit(drained);
         wait.drain(drained, 0);
       }
-    }
-    __syncwarp();
     } else if (warp == kAsker && lane == 0) {
       // ---------------------------------------------------------------- queries to shared memory
       int segment = 0;
