@@ -25,7 +25,7 @@ namespace paged {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kSlots = 5;                         // tiles of keys or values in flight
+constexpr int kSlots = 4;                         // tiles of keys or values in flight, from L2 mostly (3: no slower, 5: 1.5% slower)
 constexpr int kQ = kSlots * kSlotBytes;           // [high, low][2 halves of the dims][128 rows][128 bytes]
 constexpr int kMisc = kQ + 4 * kHalfBytes;
 constexpr int kRing = Loader<kSlots, true>::kRing;
@@ -191,19 +191,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       // a thread stores whole 32-byte pieces of its row: rows 16 bytes at a time
       // through shuffles, for wider pieces of a line per instruction, were slower
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 64) {
-        float o[64];
+      for (int c = 0; c < 128; c += 32) {
+        float o[32];
         tmem_ld<32>(t_o + lanes + group * 128 + c, o);
-        tmem_ld<32>(t_o + lanes + group * 128 + c + 32, o + 32);
         ld_wait();
         if (r >= rows) continue;
         if (wide) {
 #pragma unroll
-          for (int i = 0; i < 64; i += 4)
+          for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(out + (c + i) * 4) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
         } else {
 #pragma unroll
-          for (int i = 0; i < 64; i += 8) {
+          for (int i = 0; i < 32; i += 8) {
             uint32_t x[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
