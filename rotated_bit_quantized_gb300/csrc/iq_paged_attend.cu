@@ -35,7 +35,6 @@ namespace paged {
 
 constexpr float kTau = 6.0f;    // weights stay below 2^6
 constexpr float kPLo = 128.0f;  // the low parts' scale: half a step at 2^6 is 2, times 128 below 448
-constexpr float kUnset = -1e30f, kDead = 1e30f;  // a row's reference before its first key, and of rows that do not exist
 
 template <int NR>
 struct SplitShape {
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
           for (int r = 0; r < RT; ++r) {
             const int x = r0 + r < rows ? tiles.p_lo + query_of(p, r0 + r) : -1;
             const bool see = t < len && (!p.causal || (t <= x && (p.window == 0 || x < p.window || t > x - p.window || t < p.sinks)));
-            if (!see) s[r] = -__builtin_huge_valf();
+            if (!see) s[r] = kNothing;
           }
         }
         int far = 0;
@@ -400,7 +399,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const bool live = x < p.unit_rows && r < p.count[cut.e] * p.rep;
   auto row = [&](int g) { return static_cast<long long>(g == static_cast<int>(blockIdx.x) ? cut.slot : 2 * g) * p.unit_rows + x; };
   __shared__ float part[8][kHeadDim + 2];
-  float m = -1e30f, sum = 0.0f, o[8] = {};
+  float m = kUnset, sum = 0.0f, o[8] = {};
   if (live) {
     for (int g = blockIdx.x + lane; g <= cut.last; g += 32) m = fmaxf(m, __ldcg(&p.part_ml[row(g)]).x);  // every lane a partial
 #pragma unroll

@@ -13,6 +13,8 @@ namespace iq {
 namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNothing = -__builtin_huge_valf();      // the score of a key that a row does not see
+constexpr float kUnset = -3e38f, kDead = 3e38f;         // a row's reference before its first key, and of rows that do not exist
 constexpr int kTile = 128;                    // keys per tile: two pages
 constexpr int kHalfBytes = kTile * 128;       // 128 rows of half a head's dims
 constexpr int kSlotBytes = 2 * kHalfBytes;    // a tile of keys or of values in shared memory

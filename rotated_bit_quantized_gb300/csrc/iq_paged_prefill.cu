@@ -99,15 +99,16 @@ __global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ 
 // One persistent CTA per SM, three warpgroups.  Warps 0-7: two threads per query
 // row (warp w reaches tensor-memory lanes 32 (w % 4) ..), each with the 64 keys
 // of one page of a tile; warps w and w + 4 hold the same rows and settle the
-// rows' references between themselves.  Then one warp streams
-// the pages, one issues the products, S of the next tile but one behind O of
-// this tile, and one fetches a unit's queries once the last unit's scores are
-// done. A unit's results are stored after the next unit's first
-// weights are written, so the products wait for the stores alone.
+// rows' references between themselves.  Then one warp streams the pages, one
+// issues the products, S of the next tile but one behind O of this tile, and one
+// fetches a unit's queries once the last unit's scores are done.  A unit's
+// results are stored after the next unit's first weights are written, so the
+// products wait for the stores alone.
 __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled operands need it; no room to align by hand
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // (the kernel has no other shared memory in front)
+    wait_for_last_kernel();
     if (threadIdx.x == 0) atomicOr(p.status, kLostMma);
     return;
   }
@@ -188,8 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       uint8_t* out = static_cast<uint8_t*>(done_whole ? p.out : p.part_o) + (to * kHeadDim + group * 128) * (wide ? 4 : 2);
       await(&o_done[last_tile & 1], last_tile / 2);
       tc_after();
-      // a thread stores whole 32-byte pieces of its row: rows 16 bytes at a time
-      // through shuffles, for wider pieces of a line per instruction, were slower
+      // A thread stores its row in 32-byte pieces.  Slower, for 8191 queries under
+      // a window of 1023 in 190 us: four lanes' pieces side by side through shuffles
+      // (201), through shared memory and a warp that stores whole rows (213), kept as
+      // bf16 and stored an eighth per tile (224, spills).
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float o[32];
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
       // a row that has seen no key yet has no reference (its weights are relative to 2^0)
       bool unset = exists;
-      float ref = exists ? 0.0f : 1e30f, l = 0.0f;
+      float ref = exists ? 0.0f : kDead, l = 0.0f;
 
       const float fq = next_factor;
       if (n > 0 && at < last) {
@@ -276,13 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
             const unsigned long long see = below(stop) & (~below(low) | below(p.sinks));
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (!(static_cast<uint32_t>(see >> (i & 32)) & 1u << (i & 31))) s[i] = -__builtin_huge_valf();
+              if (!(static_cast<uint32_t>(see >> (i & 32)) & 1u << (i & 31))) s[i] = kNothing;
           }
           float m = s[0];
 #pragma unroll
           for (int i = 1; i < 63; i += 2) m = fmaxf(fmaxf(m, s[i]), s[i + 1]);
           m = fmaxf(m, s[63]);
-          int far = m > kTop || (unset && m > -1e38f);
+          int far = m > kTop || (unset && m > kNothing);
           asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
                        : "+r"(far)
                        : "r"(1 + quad)
@@ -296,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
             m = fmaxf(m, xch[(group ^ 1) * kRows + r]);
             named_bar(1 + quad, 64);
             float move = 0.0f;
-            if (m > kTop || (unset && m > -1e38f)) move = m - kPlace;
+            if (m > kTop || (unset && m > kNothing)) move = m - kPlace;
             ref += move;
             if (!unset) change = ex2_approx(-move);  // (else there is nothing yet, and move may be far below 0)
-            unset = unset && !(m > -1e38f);
+            unset = unset && !(m > kNothing);
 #pragma unroll
             for (int i = 0; i < 64; ++i) s[i] -= move;
             l *= change;
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       done_whole = whole;
       done_slot = slot;
       done_l = l;
-      done_ref = unset ? -1e30f : ref;
+      done_ref = unset ? kUnset : ref;
     }
   } else {
     setmaxnreg_dec<kRestRegs>();
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
       Loader<kSlots, true>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy);
     } else if (warp == kIssuer) {
-    // ---------------------------------------------------------------- products
+      // ---------------------------------------------------------------- products
       constexpr uint32_t kS = shape(128, kTile, false, false), kO = shape(128, kHeadDim, false, true);
       int used = 0;
       bool ok = true;
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 32 keys at a time, their high and low parts in turn
             mma_e4m3_tmem(t_o, tmem + b * 128 + (k >> 2) * 64 + ((k >> 1) & 1) * 8 + (k & 1) * 16,
-                       at_values + ((s * kSlotBytes + (k >> 1) * 32 * 128) >> 4), kO, j > 0 || k > 0);
+                          at_values + ((s * kSlotBytes + (k >> 1) * 32 * 128) >> 4), kO, j > 0 || k > 0);
           mma_commit(&o_done[b]);
           mma_commit(&empty[s]);
           ++used;

@@ -337,6 +337,22 @@ def test_ranges(qs, ks, vs, n):
     check_attend(c, o, rows(3, 1, 4, n) * qs)
 
 
+@pytest.mark.parametrize("n", [1, 4, 130])
+@pytest.mark.parametrize("signs", [(1, -1), (-1, -2), (2, 1)])
+def test_scores_of_any_size(n, signs):
+    """Scores of 1e34 and their like, of either sign: the largest takes all the weight, also over several ranges of keys."""
+    c, o = pair(1, 1, 60)
+    u = torch.randn(256, generator=torch.Generator().manual_seed(4)).sign()
+    k = (signs[1] * 1e14 * u).expand(1, 1, 3000, 256).clone()
+    k[0, 0, 1234] = signs[0] * 1e14 * u
+    v = rows(2, 1, 1, 3000)
+    put(c, o, k.bfloat16(), v)
+    q = (1e18 * u).expand(1, 4, n, 256).bfloat16()
+    out = c.attend(q.cuda(), causal=False, out_dtype=torch.float32)
+    want = o.values(0)[1][0, 1234]  # held exactly: one key, one weight
+    assert np.allclose(f64(out), want, rtol=2.0**-8, atol=0) and c.device_status() == 0
+
+
 @pytest.mark.parametrize("n", [1, 130])
 def test_value_pages_of_very_different_sizes(n):
     c, o = pair(1, 1, 12)
