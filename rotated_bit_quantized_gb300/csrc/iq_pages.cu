@@ -59,7 +59,13 @@ __device__ __forceinline__ uint32_t magnitude(const uint4& x) {
 
 // One CTA per (page of a segment, kv head, keys or values): 8 warps, a warp per
 // row, a lane per 8 dims, the page's new rows (32 KB at most) held in registers
-// between the maximum and the rounding, so every row is read once.
+// between the maximum and the rounding, so every row is read once and written
+// once.  Bound by HBM: 32 x 2 x 4096 rows and their read-back take 115 us, 805 MB
+// at 7.0 TB/s (a copy's measured rate is 6.8); one row for each of 32 slots and
+// its read-back 4.3 us.  Looking at every element for NaN and infinity before the
+// maximum cost 143 us instead of 54; the maximum of the magnitudes tells both.
+// The page ids of a segment come by value, so that no launch for table entries,
+// and no read of the table, precedes it.
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ AppendParams p) {
   wait_for_last_kernel();
   const Segment sg = p.seg[blockIdx.z];
@@ -167,7 +173,8 @@ struct ReadParams {
   int slot[IQ_MAX_BATCH], start[IQ_MAX_BATCH], len[IQ_MAX_BATCH];
 };
 
-// A warp per row of (entry, kv head), keys and values; a lane per 8 dims.
+// A warp per row of (entry, kv head), keys and values; a lane per 8 dims.  Bound
+// by HBM (32 x 2 x 4096 rows: 61 us, 403 MB at 6.6 TB/s).
 __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ ReadParams p) {
   wait_for_last_kernel();
   const int lane = threadIdx.x & 31, h = blockIdx.y, i = blockIdx.z;
@@ -241,6 +248,7 @@ struct CompactParams {
 
 // Blocks [0, pages * 2 * heads): 16 KB each, a page of one kv head, keys or
 // values, and its scale.  The blocks behind them: a run of table entries each.
+// Bound by HBM: 7640 pages of two kv heads in 73 us, 501 MB at 6.8 TB/s.
 __global__ void __launch_bounds__(256) paged_compact_kernel(const __grid_constant__ CompactParams p) {
   wait_for_last_kernel();
   const long long copies = static_cast<long long>(p.pages) * 2 * p.heads;
