@@ -424,6 +424,8 @@ int iq_read_status(void* workspace, iq_stream_t stream, int* device_status);
 #define IQ_PAGE 64
 #define IQ_STATUS_RANGE 0x40000   /* an appended value was not finite or above 448 * 2^60 */
 #define IQ_STATUS_BAD_PAGE 0x80000 /* the device table held an id outside the pool (page 0 was read) */
+/* (Bits 1, 2 and 8: a wait of an attention kernel for pages, for products or for
+ * rows ran out after a second; its results are not meaningful.) */
 
 /*
  * iq_paged — descriptor of one paged cache.  The caller owns every pointer.

@@ -615,9 +615,13 @@ int iq_paged_fork(iq_paged* c, const int32_t* src, const int32_t* dst, int count
   }
   int32_t lens[IQ_MAX_BATCH];
   int32_t* at = rows;
-  for (int i = 0; i < count; ++i) {  // the new holders first, so that no page is free in between
+  for (int i = 0, same = 0; i < count; ++i) {  // the new holders first, so that no page is free in between
     std::memcpy(at, row_of(c, src[i]), sizeof(int32_t) * p.n[i]);
-    for (int j = 0; j < p.n[i]; ++j) ++c->refs[at[j]];
+    ++same;
+    if (i + 1 == count || src[i + 1] != src[i]) {  // a run of pairs with one source
+      for (int j = 0; j < p.n[i]; ++j) c->refs[at[j]] += same;
+      same = 0;
+    }
     lens[i] = c->lens[src[i]];
     at += p.n[i];
   }

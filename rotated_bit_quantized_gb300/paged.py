@@ -47,7 +47,8 @@ def _at(a):
     return None if a is None else a.__array_interface__["data"][0]
 
 
-_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 class IQPagedCache:
@@ -174,6 +175,8 @@ class IQPagedCache:
 
     def _outputs(self, q, counts, out, out_dtype):
         if out is None:  # rows that do not exist are left as they are: zeros
+            if out_dtype is None and counts is None:
+                return torch.empty_like(q)
             dtype = out_dtype or torch.bfloat16
             if dtype not in (torch.float32, torch.bfloat16):
                 raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
@@ -195,7 +198,12 @@ class IQPagedCache:
             if len(self._need) > 256:
                 self._need.clear()
             need = self._need[key] = c.value
-        if torch.cuda.is_current_stream_capturing():
+        if _device() == self._index:
+            captured = _capturing()
+        else:
+            with self._on:
+                captured = _capturing()
+        if captured:
             return torch.empty(need, dtype=torch.uint8, device=self.device)
         ws = self._scratch.get(stream)
         if ws is None or ws.numel() < need:
