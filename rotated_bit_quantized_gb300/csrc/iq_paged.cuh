@@ -18,10 +18,10 @@ inline int slot_of(const int32_t* slots, int i) { return slots ? slots[i] : i; }
 inline int pages_for(long long tokens) { return static_cast<int>((tokens + kPage - 1) / kPage); }
 inline bool misaligned(const void* p, uintptr_t to = 16) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
-// The arguments of an attention call, checked (lens_after: what each entry's
-// slot will hold when the attention runs, NULL: what it holds).
+// The arguments of an attention call, checked.  added: the rows that the call
+// appends to every entry first (counts[i] of them, where counts are given).
 int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots,
-                 const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
+                 const int32_t* counts, int n_slots, int added, float scale, int causal, int window, int sinks,
                  const void* out, int out_f32, const void* workspace, size_t workspace_bytes);
 
 // A launch that may begin while the kernel before it ends; every kernel of the

@@ -482,6 +482,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 constexpr int kMaxSplitRows = 64;
 int unit_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kMaxSplitRows ? 64 : 128; }
 
+// The tiles of one head of an entry whose units hold `each` rows, and how many units those are.
+long long tiles_of_entry(int len, int count, int rep, int each, int causal, int window, int sinks, int* units) {
+  long long n = 0;
+  const int all = count * rep;
+  *units = 0;
+  for (long long r = 0; r < all; r += each, ++*units)
+    n += tiles_of(len, len - count + static_cast<int>(r) / rep, len - count + (static_cast<int>(std::min<long long>(r + each, all)) - 1) / rep,
+                  causal, window, sinks).n;
+  return n;
+}
+// What a unit's beginning and end take, in tiles, where a range has 8 tiles or
+// more (shorter ones are left at a tile's grain).  Measured, 0 / 1 / 2 / 4 / 6:
+// 4 x 1531 prompts - / 137 / 131 / 138 / 145 us; batched decode under a window
+// of 4096 - / 34.5 / 33.9 / 32.9 / - us.
+constexpr int unit_cost(int each) { return each == 128 ? 2 : 4; }
+
 template <int NR>
 cudaError_t launch_split(const AttendParams& p, int grid, cudaStream_t stream) {
   using C = SplitShape<NR>;
@@ -527,7 +543,7 @@ bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows, int box_ro
 }
 
 int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots,
-                 const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
+                 const int32_t* counts, int n_slots, int added, float scale, int causal, int window, int sinks,
                  const void* out, int out_f32, const void* workspace, size_t workspace_bytes) {
   size_t need = 0;
   int st = iq_paged_attend_workspace(c, q_heads, n_queries, n_slots, &need);
@@ -550,7 +566,21 @@ int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, c
     if (!workspace || workspace_bytes < need) return fail(IQ_ERR_WORKSPACE, "workspace missing or too small");
     if (misaligned(workspace, 256)) return fail(IQ_ERR_WORKSPACE, "workspace not 256-byte aligned");
   }
-  return IQ_OK;
+  // the slots of all units stay below 2^31: told by a bound, counted where that passes it
+  const int rep = q_heads / c->kv_heads, each = unit_rows(n_queries * rep);
+  for (int exact = 0; exact < 2; ++exact) {
+    long long total = 0;
+    for (int i = 0; i < n_slots; ++i) {
+      const int count = counts ? counts[i] : n_queries, len = c->lens[slot_of(slots, i)] + (counts && added ? counts[i] : added);
+      if (len <= 0 || count <= 0) continue;
+      int units = (count * rep + each - 1) / each;
+      const long long tiles = exact ? tiles_of_entry(len, count, rep, each, causal, window, sinks, &units)
+                                    : static_cast<long long>(units) * (len / kTile + 1);
+      total += (tiles + static_cast<long long>(units) * unit_cost(each)) * c->kv_heads;
+    }
+    if (total < (1LL << 31)) return IQ_OK;
+  }
+  return fail(IQ_ERR_UNSUPPORTED, "too many queries and keys for one call");
 }
 
 }  // namespace paged
@@ -584,7 +614,7 @@ int iq_paged_attend_workspace(const iq_paged* c, int q_heads, int n_queries, int
 int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots,
                     const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks, void* out,
                     int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream) {
-  const int st = check_attend(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32,
+  const int st = check_attend(c, q, q_heads, n_queries, slots, counts, n_slots, 0, scale, causal, window, sinks, out, out_f32,
                               workspace, workspace_bytes);
   if (st != IQ_OK || n_slots == 0 || n_queries == 0) return st;
   const int rep = q_heads / c->kv_heads, rows = rep * n_queries;
@@ -611,30 +641,16 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.unit_rows = unit_rows(rows);
-  // the tiles of one head of an entry
-  auto tiles_of_entry = [&](int len, int count, int* units) {
-    long long n = 0;
-    const int all = count * rep;
-    *units = 0;
-    for (long long r = 0; r < all; r += p.unit_rows, ++*units)
-      n += tiles_of(len, len - count + static_cast<int>(r) / rep, len - count + (static_cast<int>(std::min<long long>(r + p.unit_rows, all)) - 1) / rep,
-                    causal, window, sinks).n;
-    return n;
-  };
   long long tiles = 0, per[IQ_MAX_BATCH];
   int units[IQ_MAX_BATCH];
   for (int i = 0; i < n_slots; ++i) {
     const int len = c->lens[slot_of(slots, i)], count = counts ? counts[i] : n_queries;
     per[i] = units[i] = 0;
-    if (len > 0 && count > 0) tiles += (per[i] = tiles_of_entry(len, count, &units[i])) * c->kv_heads;
+    if (len > 0 && count > 0) tiles += (per[i] = tiles_of_entry(len, count, rep, p.unit_rows, causal, window, sinks, &units[i])) * c->kv_heads;
   }
   const int grid = static_cast<int>(std::min<long long>(num_sms(), tiles));
   if (grid == 0) return IQ_OK;
-  // What a unit's beginning and end take, in tiles, where a range has 8 tiles or
-  // more (shorter ones are left at a tile's grain).  Measured, 0 / 1 / 2 / 4 / 6:
-  // 4 x 1531 prompts - / 137 / 131 / 138 / 145 us; batched decode under a window
-  // of 4096 - / 34.5 / 33.9 / 32.9 / - us.
-  p.cost = tiles >= 8ll * grid ? (p.unit_rows == 128 ? 2 : 4) : 0;
+  p.cost = tiles >= 8ll * grid ? unit_cost(p.unit_rows) : 0;
   long long total = 0;
   for (int i = 0; i < n_slots; ++i) {
     const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
@@ -647,7 +663,6 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
     p.cum[e] = static_cast<int>(total);
     per[i] += static_cast<long long>(units[i]) * p.cost;
     total += per[i] * c->kv_heads;
-    if (total >= (1LL << 31)) return fail(IQ_ERR_UNSUPPORTED, "too many queries and keys for one call");
     p.per[e] = static_cast<int>(per[i]);
   }
   p.cum[p.entries] = p.total = static_cast<int>(total);

@@ -511,7 +511,7 @@ int iq_paged_append_attend(iq_paged* c, const void* keys, const void* values, in
   int st = check_append(c, keys, values, n, slots, counts, n_slots);
   if (st != IQ_OK) return st;
   if (counts && n != n_queries) return fail(IQ_ERR_INVALID_ARG, "counts need as many rows as queries");
-  st = check_attend(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32, workspace,
+  st = check_attend(c, q, q_heads, n_queries, slots, counts, n_slots, n, scale, causal, window, sinks, out, out_f32, workspace,
                     workspace_bytes);
   if (st != IQ_OK) return st;
   st = do_append(c, keys, values, n, slots, counts, n_slots, stream);

@@ -210,6 +210,20 @@ def test_append_attend_checks_both_first(L):
     assert f.state() == was
 
 
+def test_calls_with_too_many_tiles_are_refused_before_the_append(L):
+    """2^29 query rows, 2^22 units of 128, over 512 tiles of keys: 2^31 tiles."""
+    def call(f, nq, causal, n=64, k=1):
+        return L.iq_paged_append_attend(f.p, P, P, n, P, 1, nq, None, None, k, 0.1, causal, 0, 0, P, 0,
+                                        ctypes.c_void_p(0x40000000), 1 << 40, None)
+    f = Fake(L, slots=1, heads=1, pages=1024, max_pages=1024)
+    f.hold(0, list(range(1023)), 1023 * 64)
+    was = f.state()
+    assert call(f, 1 << 29, 0) == UNSUPPORTED and f.state() == was
+    assert f.attend(Hq=1, n=1 << 29, k=1, causal=0, ws=ctypes.c_void_p(0x40000000)) == UNSUPPORTED
+    if not torch.cuda.is_available():  # a bound passes 2^31, the tiles do not: causal rows before the first key see one tile each
+        assert call(f, 1 << 29, 1) == CUDA and f.state() == was
+
+
 def test_read_refusals(L):
     f = Fake(L)
     f.hold(0, [0], 10)
