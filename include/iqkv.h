@@ -545,7 +545,8 @@ int iq_paged_attend_workspace(const iq_paged* cache, int q_heads, int n_queries,
  *   window and sinks need causal == 1, sinks a window.
  * out: device [n_slots][q_heads][n_queries][head_dim], bf16 or float32
  *   (out_f32); softmax(scale * q.k) . v, rounded once; 0 for a query that sees
- *   no key (an empty slot, a position before the first token).
+ *   no key (an empty slot, a position before the first token).  It must not
+ *   overlap q, which some CTAs still read when others store.
  * workspace: at least iq_paged_attend_workspace() bytes, 256-byte aligned; it
  *   needs no initialisation and holds nothing between calls.  Calls that may
  *   run at the same time need one each.

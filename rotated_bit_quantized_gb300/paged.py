@@ -185,6 +185,9 @@ class IQPagedCache:
             raise ValueError("out must be a contiguous bf16 or f32 tensor")
         if out.shape != q.shape or out.device != q.device or (out_dtype or out.dtype) != out.dtype:
             raise ValueError("out must have q's shape and device, and out_dtype")
+        at, to = q.data_ptr(), out.data_ptr()
+        if to < at + q.numel() * 2 and at < to + out.numel() * out.element_size():
+            raise ValueError("out must not overlap q")
         return out
 
     def _workspace(self, q_heads: int, rows: int, entries: int, stream):
@@ -280,8 +283,8 @@ class IQPagedCache:
 
         The L queries stand at each slot's last L positions (its last counts[i],
         where counts are given: the queries behind them do not exist, and their
-        rows of `out` are left as they were).  causal: a query sees the keys up
-        to its own position; `window` > 0: only the last `window` of them, and
+        rows of `out` are left as they were).  `out` must not overlap q.  causal: a query sees the keys
+        up to its own position; `window` > 0: only the last `window` of them, and
         the slot's first `sinks` tokens.  A query that sees nothing gets 0.
         """
         q = self._tensor(q, "q")

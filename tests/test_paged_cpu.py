@@ -194,6 +194,20 @@ def test_attend_refusals(L):
     assert f.attend(n=0) == 0 and f.attend(k=0) == 0                     # nothing to do
 
 
+def test_outputs_over_the_queries_are_refused():
+    from rotated_bit_quantized_gb300.paged import IQPagedCache
+
+    def given(q, out):
+        return IQPagedCache._outputs(None, q, None, out, None)
+    x = torch.zeros(6, 2, 3, 256, dtype=torch.bfloat16)
+    wide = x.view(torch.float32).view(3, 2, 3, 256)                       # the same memory as fp32 rows
+    for q, out in [(x[:2], x[2:4]), (x[2:4], x[:2]), (x[4:5], wide[:1]), (x[:1], wide[1:2])]:   # side by side, apart
+        assert given(q, out) is out
+    for q, out in [(x, x), (x[:2], x[1:3]), (x[1:3], x[:2]), (x[1:2], wide[:1]), (x[:1], wide[:1])]:
+        with pytest.raises(ValueError, match="overlap"):
+            given(q, out)
+
+
 def test_append_attend_checks_both_first(L):
     f = Fake(L)
     f.hold(0, [0], 10)
@@ -213,13 +227,13 @@ def test_append_attend_checks_both_first(L):
 def test_calls_with_too_many_tiles_are_refused_before_the_append(L):
     """2^29 query rows, 2^22 units of 128, over 512 tiles of keys: 2^31 tiles."""
     def call(f, nq, causal, n=64, k=1):
-        return L.iq_paged_append_attend(f.p, P, P, n, P, 1, nq, None, None, k, 0.1, causal, 0, 0, P, 0,
-                                        ctypes.c_void_p(0x40000000), 1 << 40, None)
+        return L.iq_paged_append_attend(f.p, P, P, n, P, 1, nq, None, None, k, 0.1, causal, 0, 0,
+                                        ctypes.c_void_p(1 << 44), 0, ctypes.c_void_p(0x40000000), 1 << 40, None)
     f = Fake(L, slots=1, heads=1, pages=1024, max_pages=1024)
     f.hold(0, list(range(1023)), 1023 * 64)
     was = f.state()
     assert call(f, 1 << 29, 0) == UNSUPPORTED and f.state() == was
-    assert f.attend(Hq=1, n=1 << 29, k=1, causal=0, ws=ctypes.c_void_p(0x40000000)) == UNSUPPORTED
+    assert f.attend(Hq=1, n=1 << 29, k=1, causal=0, out=ctypes.c_void_p(1 << 44), ws=ctypes.c_void_p(0x40000000)) == UNSUPPORTED
     if not torch.cuda.is_available():  # a bound passes 2^31, the tiles do not: causal rows before the first key see one tile each
         assert call(f, 1 << 29, 1) == CUDA and f.state() == was
 
