@@ -619,6 +619,9 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   if (st != IQ_OK || n_slots == 0 || n_queries == 0) return st;
   const int rep = q_heads / c->kv_heads, rows = rep * n_queries;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int longest = 0;
+  for (int i = 0; i < n_slots; ++i) longest = std::max(longest, c->lens[slot_of(slots, i)]);
+  if (window >= longest) window = sinks = 0;  // nothing is out of it, and positions less a window stay in 32 bits
   {
     ZeroParams z;
     z.out = out;

@@ -43,6 +43,13 @@ def _ints(x, n: int | None, name: str):
     return np.ascontiguousarray(a)
 
 
+def _span(window, sinks):
+    """Window and sinks as the library takes them: whole numbers of 32 bits (ctypes would cut longer ones)."""
+    if not (-1 << 31 <= window < 1 << 31 and -1 << 31 <= sinks < 1 << 31):
+        raise ValueError("window and sinks must fit in 32 bits")
+    return window, sinks
+
+
 def _at(a):
     return None if a is None else a.__array_interface__["data"][0]
 
@@ -291,6 +298,7 @@ class IQPagedCache:
         E, Hq, L, D = q.shape
         slots, counts = self._entries(E, slots, counts)
         out = self._outputs(q, counts, out, out_dtype)
+        window, sinks = _span(window, sinks)
         stream = self._queue()
         ws = self._workspace(Hq, L, E, stream)
         self._run(self._lib.iq_paged_attend, self._d, q.data_ptr(), Hq, L, _at(slots), _at(counts), E,
@@ -310,6 +318,7 @@ class IQPagedCache:
             raise ValueError("keys/values and q must have the same entries")
         slots, counts = self._entries(E, slots, counts)
         out = self._outputs(q, counts, out, out_dtype)
+        window, sinks = _span(window, sinks)
         stream = self._queue()
         ws = self._workspace(Hq, L, E, stream)
         self._run(self._lib.iq_paged_append_attend, self._d, keys.data_ptr(), values.data_ptr(), keys.shape[2], q.data_ptr(), Hq, L,

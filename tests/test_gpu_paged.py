@@ -284,6 +284,24 @@ def test_a_window_over_everything_is_causal_attention():
         assert torch.equal(c.attend(q), c.attend(q, window=900 + 5, sinks=0))
 
 
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_the_largest_window_and_sinks(n):
+    """Also for queries before the first token, whose positions are negative."""
+    c, o = pair(3, 2, 30, 500)
+    put(c, o, rows(1, 3, 2, 450), rows(2, 3, 2, 450), None, [450, 2, 129])
+    q = rows(3, 3, 8, n)
+    for kw in (dict(window=2**31 - 1), dict(window=2**31 - 1, sinks=2**31 - 1), dict(window=449, sinks=2**31 - 1), dict(window=450)):
+        assert (check_attend(c, o, q, **kw) == check_attend(c, o, q)).all()
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30])
+def test_scales_that_turn_or_level_the_scores(n, scale):
+    c, o = pair(2, 2, 30, 500)
+    put(c, o, rows(1, 2, 2, 450), rows(2, 2, 2, 450), None, [450, 131])
+    check_attend(c, o, rows(3, 2, 8, n), scale=scale)
+
+
 def test_counts_and_slots():
     c, o = pair(7, 2, 60)
     put(c, o, rows(1, 7, 2, 400, True), rows(2, 7, 2, 400), None, [400, 1, 64, 0, 333, 128, 200])

@@ -259,3 +259,11 @@ def test_integer_arguments():
     for bad, n in [([1, 2], 3), ([1.5], 1), ([[1]], None), ([2**31], 1), ([-2**31 - 1], 1), (3, None)]:
         with pytest.raises(ValueError):
             _ints(bad, n, "x")
+
+
+def test_window_and_sinks_fit_in_32_bits():
+    from rotated_bit_quantized_gb300.paged import _span
+    assert _span(2**31 - 1, 2**31 - 1) == (2**31 - 1, 2**31 - 1) and _span(-1, 0) == (-1, 0)
+    for bad in [(2**31, 0), (2**32 + 5, 0), (5, 2**32), (-2**31 - 1, 0)]:
+        with pytest.raises(ValueError):
+            _span(*bad)
