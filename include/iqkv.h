@@ -24,6 +24,10 @@
  *  - Functions return an `iq_status`; nothing is thrown across the ABI.  On an
  *    error nothing is enqueued and nothing the caller owns is modified, and
  *    `iq_last_error()` holds a one-line explanation (per host thread).
+ *  - Kernels are launched as programmatic dependents of what is in front of them
+ *    on the stream.  What one call of this library hands out may be the next
+ *    one's input.  A kernel of someone else's directly in front that releases its
+ *    dependents before it has stored such an input is not waited for.
  *  - Supported shapes: head_dim 256; k_bits and v_bits 2, 3, 4, 5, 6 or 8 (the
  *    widths the page's `_packed_words` lists); group_size 32, 64 or 128;
  *    1 <= batch <= IQ_MAX_BATCH, kv heads >= 1, query heads a multiple of kv

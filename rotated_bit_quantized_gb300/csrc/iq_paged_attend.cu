@@ -619,6 +619,7 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   if (st != IQ_OK || n_slots == 0 || n_queries == 0) return st;
   const int rep = q_heads / c->kv_heads, rows = rep * n_queries;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const Range written{out, static_cast<size_t>(n_slots) * q_heads * n_queries * kHeadDim * (out_f32 ? 4 : 2)};
   int longest = 0;
   for (int i = 0; i < n_slots; ++i) longest = std::max(longest, c->lens[slot_of(slots, i)]);
   if (window >= longest) window = sinks = 0;  // nothing is out of it, and positions less a window stay in 32 bits
@@ -639,6 +640,7 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
     if (n > 0) {
       void* args[] = {&z};
       IQ_CUDA(launch_after(reinterpret_cast<const void*>(&paged_zero_kernel), dim3(std::min(64, (most + 7) / 8), n), 256, 0, cs, args));
+      launched_outputs(stream, written);
     }
   }
   AttendParams p;
@@ -725,7 +727,9 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
     void* args[] = {&j};
     err = launch_after(reinterpret_cast<const void*>(&paged_join_kernel), dim3(grid - 1, (most + each - 1) / each), 256, 0, cs, args);
   }
-  return err == cudaSuccess ? IQ_OK : cuda_fail(err, "paged attention");
+  if (err != cudaSuccess) return cuda_fail(err, "paged attention");
+  launched_outputs(stream, written);
+  return IQ_OK;
 }
 
 }  // extern "C"

@@ -553,6 +553,8 @@ int iq_paged_read(const iq_paged* c, const int32_t* slots, const int32_t* start,
   void* args[] = {&p};
   IQ_CUDA(launch_after(reinterpret_cast<const void*>(&paged_read_kernel), dim3((n + 7) / 8, c->kv_heads, n_slots), 256, 0,
                        static_cast<cudaStream_t>(stream), args));
+  const size_t bytes = static_cast<size_t>(n_slots) * c->kv_heads * n * kHeadDim * 2;
+  launched_outputs(stream, {keys_out, bytes}, {values_out, bytes});
   return IQ_OK;
 }
 
