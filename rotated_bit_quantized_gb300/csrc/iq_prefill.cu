@@ -297,7 +297,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   const long long row0 = static_cast<long long>(bh) * p.cap;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // With new rows to store, no early release: a split-KV attention behind this
+  // grid streams cache tiles before its own wait, and expects unfinished rows
+  // among a sequence's last ones only, not anywhere in a chunk.
+  if constexpr (!FUSED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- fused append.  The new rows (B x Hkv x n_new of them, in (sequence,
   // kv head, row) order) are encoded in chunks of ENC_CHUNK rows that every CTA

@@ -106,3 +106,21 @@ def test_a_mask_made_by_the_call_before():
         mask = out.view(-1)[: 2 * 2 * 2048].view(2, 2, 2048)
         return out, c.attend(q, rot, mask=mask)
     both_ways(chain)
+
+
+@pytest.mark.parametrize("slots,H", [(1, 1), (1, 2), (3, 2)])
+def test_an_appended_chunk_is_attended_at_once(slots, H):
+    """A chunk whose attention encodes its own rows, then a step that reads all of them."""
+    c, rot = rotated(slots, H, 256, 3)
+    k, v, big = rows(7, slots, H, 1024), rows(8, slots, H, 1024), rows(9, slots, 8 * H, 1024)
+    k1, v1, q1 = rows(10, slots, H, 1), rows(11, slots, H, 1), rows(12, slots, 8 * H, 1)
+
+    def chain(wait):
+        a = c.append_attend(k, v, big, rot)
+        wait()
+        b = c.append_attend(k1, v1, q1, rot)
+        wait()
+        d = c.attend(q1, rot)
+        c.trim(1025)
+        return a, b, d
+    both_ways(chain)
