@@ -487,8 +487,8 @@ int iq_paged_check(const iq_paged* cache);
  * Free pages are taken lowest id first, in the order of the entries.  A page
  * whose last rows are shared with other slots is copied first.
  * Errors: INVALID_ARG; CAPACITY (the pool has too few free pages, or a slot
- * would pass max_pages); CUDA.  On an error nothing has changed, but on CUDA,
- * where launches before the failing one stand.
+ * would pass max_pages); CUDA (a launch failed).  On an error nothing that a slot
+ * holds has changed.
  */
 int iq_paged_append(iq_paged* cache, const void* keys, const void* values, int n, const int32_t* slots,
                     const int32_t* counts, int n_slots, iq_stream_t stream);
@@ -532,6 +532,14 @@ int iq_paged_fork(iq_paged* cache, const int32_t* src, const int32_t* dst, int c
  * Errors: INVALID_ARG, CAPACITY (dst has too few pages or too short rows), CUDA.
  */
 int iq_paged_compact(const iq_paged* src, iq_paged* dst, iq_stream_t stream);
+
+/*
+ * iq_paged_debug_fail — a fault-injection hook for tests: of the launches that
+ * this host thread's iq_paged_* calls make from now on, number `launch` (from 0)
+ * is not made and reported as failed (CUDA).  It holds for one failure; a
+ * negative number takes it back.
+ */
+int iq_paged_debug_fail(int launch);
 
 /* iq_paged_attend_workspace — device scratch bytes iq_paged_attend needs for these shapes, whatever the lengths. */
 int iq_paged_attend_workspace(const iq_paged* cache, int q_heads, int n_queries, int n_slots, size_t* bytes);

@@ -510,7 +510,10 @@ cudaError_t launch_split(const AttendParams& p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
+thread_local int launch_to_fail = -1;
+
 cudaError_t launch_after(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args) {
+  if (launch_to_fail >= 0 && launch_to_fail-- == 0) return cudaErrorLaunchFailure;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -343,7 +343,11 @@ int check_append(iq_paged* c, const void* keys, const void* values, int n, const
   return need <= c->free_pages ? IQ_OK : fail(IQ_ERR_CAPACITY, "the pool has too few free pages");
 }
 
-// The checked append: takes pages, launches, and puts everything back if a launch fails.
+// The checked append: takes pages, launches, and puts everything back if a launch
+// fails.  What changes a page or a table entry that a slot lives on (a run that
+// begins in a partly full page: it rescales the rows there, or moves them to a copy
+// and names that one) goes with the last launch; the launches before it write
+// pages that are still free to anyone who looks at the host's arrays.
 int do_append(iq_paged* c, const void* keys, const void* values, int n, const int32_t* slots, const int32_t* counts,
               int n_slots, iq_stream_t stream) {
   AppendParams p;
@@ -358,7 +362,9 @@ int do_append(iq_paged* c, const void* keys, const void* values, int n, const in
   p.heads = c->kv_heads;
   p.n = n;
   p.max_pages = c->max_pages;
-  int segs = 0, widest = 0, done = 0;
+  int segs = 0, widest = 0, done = 0, begun = 0;
+  Segment last_ones[IQ_MAX_BATCH];  // one per entry at most
+  static_assert(IQ_MAX_BATCH <= kSegments, "they fit one launch");
   int was[IQ_MAX_BATCH];  // the shared page that entry i's own copy replaced
   cudaError_t err = cudaSuccess;
   auto launch = [&]() {
@@ -368,6 +374,10 @@ int do_append(iq_paged* c, const void* keys, const void* values, int n, const in
                          static_cast<cudaStream_t>(stream), args);
     }
     segs = widest = 0;
+  };
+  auto add = [&](const Segment& sg) {
+    p.seg[segs++] = sg;
+    widest = std::max(widest, (sg.pos % kPage + sg.rows + kPage - 1) / kPage);
   };
   for (; done < n_slots && err == cudaSuccess; ++done) {
     const int s = slot_of(slots, done), len = c->lens[s], cnt = counts ? counts[done] : n;
@@ -389,14 +399,20 @@ int do_append(iq_paged* c, const void* keys, const void* values, int n, const in
       int m = 1;
       while (j + m < last && row[j + m] == row[j] + m) ++m;
       const int stop = std::min((j + m) * static_cast<long long>(kPage), static_cast<long long>(len) + cnt);
-      if (segs == kSegments) launch();
-      p.seg[segs++] = {done, s, pos - len, stop - pos, pos, row[j], from >= 0 ? from : row[j]};
-      widest = std::max(widest, m);
+      const Segment sg{done, s, pos - len, stop - pos, pos, row[j], from >= 0 ? from : row[j]};
+      if (from >= 0) {
+        last_ones[begun++] = sg;
+      } else {
+        if (segs == kSegments) launch();
+        add(sg);
+      }
       pos = stop;
       j += m;
       from = -1;
     }
   }
+  if (segs + begun > kSegments) launch();
+  for (int i = 0; i < begun; ++i) add(last_ones[i]);
   launch();
   if (err != cudaSuccess) {
     for (int i = 0; i < done; ++i) {
@@ -426,6 +442,12 @@ using namespace iq;
 using namespace iq::paged;
 
 extern "C" {
+
+int iq_paged_debug_fail(int launch) {
+  clear_error();
+  launch_to_fail = launch < 0 ? -1 : launch;
+  return IQ_OK;
+}
 
 int iq_paged_bytes(int slots, int kv_heads, int head_dim, int pages, int max_pages, size_t out_bytes[6]) {
   clear_error();

@@ -229,6 +229,41 @@ def test_compact_into_a_given_cache_and_back():
     same(c.compact(), o.compact(700))
 
 
+def fragmented():
+    """Slot 2 and its fork 3 share a partly full page, slot 4 has one of its own, and the free pages lie one by one
+    between slot 0's: a long append takes more runs of pages than one launch describes (256)."""
+    c, o = pair(6, 1, 700, 320 * 64)
+    for i in range(300):
+        put(c, o, rows(i, 2, 1, 64), rows(i + 1, 2, 1, 64), [0, 1])
+    put(c, o, rows(400, 2, 1, 70), rows(401, 2, 1, 70), [2, 4])
+    c.fork([2], [3]), o.fork([2], [3])
+    c.free([1]), o.free([1])
+    k, v = rows(402, 3, 1, 150 * 64) * 40, rows(403, 3, 1, 150 * 64) * 40  # the exponents grow
+    return c, o, k, v, dict(slots=[3, 4, 5], counts=[140 * 64 + 5, 3, 150 * 64 - 1])
+
+
+def test_an_append_of_many_runs():
+    c, o, k, v, kw = fragmented()
+    put(c, o, k, v, **kw)
+    same(c, o)
+    put(c, o, k[:, :, :9], v[:, :, :9], slots=[2, 4, 5])  # the shared page went on in a copy
+    same(c, o)
+
+
+@pytest.mark.parametrize("launch", [0, 1])
+def test_an_append_that_fails_at_a_launch_leaves_what_was_held(launch):
+    from rotated_bit_quantized_gb300 import IQError
+    c, o, k, v, kw = fragmented()
+    c._lib.iq_paged_debug_fail(launch)  # on the host: that launch is not made
+    with pytest.raises(IQError, match="CUDA"):
+        c.append(k.cuda(), v.cuda(), **kw)
+    same(c, o)
+    put(c, o, k[:, :, :200], v[:, :, :200], [0, 1, 5])  # the pages it had taken go to others
+    same(c, o)
+    put(c, o, k, v, [3, 4, 1], kw["counts"])
+    same(c, o)
+
+
 # ------------------------------------------------------------------ attention
 
 LENS = [[1], [64, 1, 65, 63, 2], [128, 127, 129, 0], [300, 0, 1025], [2000]]
