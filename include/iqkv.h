@@ -529,7 +529,8 @@ int iq_paged_fork(iq_paged* cache, const int32_t* src, const int32_t* dst, int c
  * that share pages in src share the copies in dst.  dst's former contents are
  * dropped.  It grows or shrinks a pool, takes a snapshot and restores one.
  * src and dst: the same slots, kv_heads and head_dim, no common buffer.
- * Errors: INVALID_ARG, CAPACITY (dst has too few pages or too short rows), CUDA.
+ * Errors: INVALID_ARG, CAPACITY (dst has too few pages or too short rows), CUDA
+ * (dst is then what it was, or empty).
  */
 int iq_paged_compact(const iq_paged* src, iq_paged* dst, iq_stream_t stream);
 

@@ -691,12 +691,14 @@ int iq_paged_compact(const iq_paged* src, iq_paged* dst, iq_stream_t stream) {
   p.pages = p.page_runs = p.table_runs = 0;
   int run_page = 0, run_len = 0;  // the last page run: its first source page, its length
   cudaError_t err = cudaSuccess;
+  bool begun = false;  // a launch has written dst's pages
   auto launch = [&]() {
     const long long blocks = static_cast<long long>(p.pages) * 2 * p.heads + p.table_runs;
     if (blocks && err == cudaSuccess) {
       void* args[] = {&p};
       err = launch_after(reinterpret_cast<const void*>(&paged_compact_kernel), dim3(static_cast<unsigned>(blocks)), 256, 0,
                          static_cast<cudaStream_t>(stream), args);
+      begun |= err == cudaSuccess;
     }
     p.pages = p.page_runs = p.table_runs = run_len = 0;
   };
@@ -734,6 +736,12 @@ int iq_paged_compact(const iq_paged* src, iq_paged* dst, iq_stream_t stream) {
   launch();
   if (err != cudaSuccess) {
     delete[] to;
+    if (begun) {  // what dst held is lost
+      std::memset(dst->lens, 0, sizeof(int32_t) * dst->slots);
+      std::memset(dst->refs, 0, sizeof(int32_t) * dst->pages);
+      dst->free_pages = dst->pages;
+      dst->first_free = 0;
+    }
     return cuda_fail(err, "paged compact");
   }
   std::memset(dst->refs, 0, sizeof(int32_t) * dst->pages);

@@ -251,6 +251,23 @@ def test_an_append_of_many_runs():
 
 
 @pytest.mark.parametrize("launch", [0, 1])
+def test_a_compaction_that_fails_at_a_launch(launch):
+    """Into a cache that holds something: what it held, or, once its pages have been written over, nothing."""
+    from rotated_bit_quantized_gb300 import IQError
+    c, o, *_ = fragmented()
+    put(c, o, rows(9, 1, 1, 200 * 64), rows(8, 1, 1, 200 * 64), [5])  # 300 runs of one page, and 200 more
+    to, held = pair(6, 1, 700, 320 * 64)
+    put(to, held, rows(1, 2, 1, 500), rows(2, 2, 1, 500), [1, 4])
+    c._lib.iq_paged_debug_fail(launch)
+    with pytest.raises(IQError, match="CUDA"):
+        c.compact(out=to)
+    same(c, o)
+    same(to, held if launch == 0 else paged.OraclePaged(6, 1, 700, 320))
+    assert c.compact(out=to) is to
+    same(to, o.compact(700))
+
+
+@pytest.mark.parametrize("launch", [0, 1])
 def test_an_append_that_fails_at_a_launch_leaves_what_was_held(launch):
     from rotated_bit_quantized_gb300 import IQError
     c, o, k, v, kw = fragmented()
