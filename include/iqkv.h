@@ -423,7 +423,8 @@ int iq_read_status(void* workspace, iq_stream_t stream, int* device_status);
  * page ids from the device copy of the table.  A captured call therefore
  * replays with the lengths that it was captured with.  The host arrays change
  * when a call returns, so a page that a call releases may be handed out by the
- * next one: order a cache's calls on one stream, or by events.
+ * next one: order a cache's calls on one stream, or by events.  Host threads
+ * that call one cache need a lock around each call.
  */
 #define IQ_PAGE 64
 #define IQ_STATUS_RANGE 0x40000   /* an appended value was not finite or above 448 * 2^60 */

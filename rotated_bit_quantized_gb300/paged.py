@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 import numpy as np
 import torch
@@ -75,8 +76,8 @@ class IQPagedCache:
 
     Lengths and page ids are the host's.  Calls on one cache have to be ordered
     on one stream or by events: a page that a call releases may be handed out
-    by the next one.  A call captured into a CUDA graph replays with the lengths
-    that it was captured with.
+    by the next one.  Host threads that call one cache are taken in turn.  A call
+    captured into a CUDA graph replays with the lengths that it was captured with.
     """
 
     PAGE = IQ_PAGE
@@ -90,7 +91,7 @@ class IQPagedCache:
         self.device = torch.device(device or "cuda")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self._index, self._on, self._lib = self.device.index, _OnDevice(self.device.index), lib()
+        self._index, self._lib = self.device.index, lib()
         dev = self.device
         self.k_codes = torch.empty((pages, kv_heads, IQ_PAGE, head_dim), dtype=torch.uint8, device=dev)
         self.v_codes = torch.empty_like(self.k_codes)
@@ -103,6 +104,7 @@ class IQPagedCache:
         self._lens = np.zeros(slots, dtype=np.int32)
         self._table = np.zeros((slots, self.max_pages), dtype=np.int32)
         self._refs = np.zeros(pages, dtype=np.int32)
+        self._lock = threading.RLock()  # the library's calls run without the interpreter's
         self._need, self._scratch, self._scale = {}, {}, 1.0 / math.sqrt(head_dim)
         self._desc = IQPagedDesc()
         self._d = ctypes.byref(self._desc)
@@ -111,14 +113,15 @@ class IQPagedCache:
                                    _at(self._lens), _at(self._table), _at(self._refs)), "iq_paged_alloc")
 
     def _run(self, f, *args) -> None:
-        """Call a library function with the cache's device current."""
-        if _device() == self._index:
-            code = f(*args)
-        else:
-            with self._on:
+        """Call a library function with the cache's device current, one thread at a time."""
+        with self._lock:
+            if _device() == self._index:
                 code = f(*args)
-        if code:
-            check(code, f.__name__)
+            else:
+                with _OnDevice(self._index):
+                    code = f(*args)
+            if code:
+                check(code, f.__name__)
 
     def _queue(self):
         """The current stream of the cache's device."""
@@ -128,7 +131,8 @@ class IQPagedCache:
     @property
     def lens(self) -> np.ndarray:
         """The slots' lengths, int32 [slots] (a copy)."""
-        return self._lens.copy()
+        with self._lock:
+            return self._lens.copy()
 
     @property
     def pages_free(self) -> int:
@@ -146,12 +150,13 @@ class IQPagedCache:
 
     def page_ids(self, slot: int) -> np.ndarray:
         """The page ids of a slot, in order (a copy)."""
-        return self._table[slot, : -(-int(self._lens[slot]) // IQ_PAGE)].copy()
+        with self._lock:
+            return self._table[slot, : -(-int(self._lens[slot]) // IQ_PAGE)].copy()
 
     def device_status(self) -> int:
         """Synchronise, return the kernels' status word (0: all normal) and clear it."""
         st = ctypes.c_int()
-        with self._on:
+        with _OnDevice(self._index):
             code = lib().iq_read_status(self._status.data_ptr(), _stream(self._index), ctypes.byref(st))
         if code not in (_abi.IQ_OK, _abi.IQ_ERR_DEVICE):
             check(code, "iq_read_status")
@@ -198,8 +203,9 @@ class IQPagedCache:
         return out
 
     def _workspace(self, q_heads: int, rows: int, entries: int, stream):
-        """Scratch for a call on `stream`: one per stream, kept, as work on one stream is in order;
-        for a captured call its own, as graphs captured on one stream may run at once."""
+        """Scratch for a call on `stream`: one per stream, kept, as work on one stream is in order
+        (so the lock is held from here until the call has made its launches); for a captured
+        call its own, as graphs captured on one stream may run at once."""
         key = (q_heads, rows, entries)
         need = self._need.get(key)
         if need is None:
@@ -211,7 +217,7 @@ class IQPagedCache:
         if _device() == self._index:
             captured = _capturing()
         else:
-            with self._on:
+            with _OnDevice(self._index):
                 captured = _capturing()
         if captured:
             return torch.empty(need, dtype=torch.uint8, device=self.device)
@@ -280,7 +286,9 @@ class IQPagedCache:
                                self.head_dim, self.device)
         elif out.device != self.device:
             raise ValueError("out must be on the cache's device")
-        self._run(self._lib.iq_paged_compact, self._d, out._d, self._queue())
+        first, second = sorted((self, out), key=id)  # the same order in every thread
+        with first._lock, second._lock:
+            self._run(self._lib.iq_paged_compact, self._d, out._d, self._queue())
         return out
 
     # ---------------------------------------------------------------- attention
@@ -300,10 +308,11 @@ class IQPagedCache:
         out = self._outputs(q, counts, out, out_dtype)
         window, sinks = _span(window, sinks)
         stream = self._queue()
-        ws = self._workspace(Hq, L, E, stream)
-        self._run(self._lib.iq_paged_attend, self._d, q.data_ptr(), Hq, L, _at(slots), _at(counts), E,
-                  self._scale if scale is None else scale, 1 if causal else 0, window, sinks, out.data_ptr(),
-                  1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
+        with self._lock:
+            ws = self._workspace(Hq, L, E, stream)
+            self._run(self._lib.iq_paged_attend, self._d, q.data_ptr(), Hq, L, _at(slots), _at(counts), E,
+                      self._scale if scale is None else scale, 1 if causal else 0, window, sinks, out.data_ptr(),
+                      1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
         return out
 
     def append_attend(self, keys: torch.Tensor, values: torch.Tensor, q: torch.Tensor, causal: bool = True,
@@ -320,8 +329,9 @@ class IQPagedCache:
         out = self._outputs(q, counts, out, out_dtype)
         window, sinks = _span(window, sinks)
         stream = self._queue()
-        ws = self._workspace(Hq, L, E, stream)
-        self._run(self._lib.iq_paged_append_attend, self._d, keys.data_ptr(), values.data_ptr(), keys.shape[2], q.data_ptr(), Hq, L,
-                  _at(slots), _at(counts), E, self._scale if scale is None else scale, 1 if causal else 0, window, sinks,
-                  out.data_ptr(), 1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
+        with self._lock:
+            ws = self._workspace(Hq, L, E, stream)
+            self._run(self._lib.iq_paged_append_attend, self._d, keys.data_ptr(), values.data_ptr(), keys.shape[2], q.data_ptr(), Hq, L,
+                      _at(slots), _at(counts), E, self._scale if scale is None else scale, 1 if causal else 0, window, sinks,
+                      out.data_ptr(), 1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
         return out

@@ -517,6 +517,27 @@ def test_calls_on_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_host_threads_on_one_stream():
+    import threading
+    c, o = pair(2, 2, 300)
+    put(c, o, rows(1, 2, 2, 8000), rows(2, 2, 2, 8000))
+    qs = [rows(3 + i, 2, 16, n).cuda() for i, n in enumerate((1, 4, 1, 200))]
+    want = [c.attend(q) for q in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+
+    def work(i):
+        for _ in range(30):
+            got[i].append(c.attend(qs[i]))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(qs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(len(g) == 30 and all(torch.equal(x, w) for x in g) for g, w in zip(got, want))
+
+
 def test_captured_calls_replay_with_their_lengths():
     c, o = pair(3, 2, 60)
     put(c, o, rows(1, 2, 2, 500), rows(2, 2, 2, 500), [0, 1], [500, 130])

@@ -267,3 +267,41 @@ def test_window_and_sinks_fit_in_32_bits():
     for bad in [(2**31, 0), (2**32 + 5, 0), (5, 2**32), (-2**31 - 1, 0)]:
         with pytest.raises(ValueError):
             _span(*bad)
+
+
+def test_host_threads_take_turns(monkeypatch):
+    """Library calls drop the interpreter's lock; a call and its choice of scratch must not be torn apart."""
+    import threading
+    import time
+
+    from rotated_bit_quantized_gb300 import paged
+    c = paged.IQPagedCache.__new__(paged.IQPagedCache)
+    c.device, c._index, c.slots, c.kv_heads, c.head_dim, c._d, c._scale = torch.device("cuda", 0), 0, 4, 2, 256, None, 1 / 16
+    c._lock, c._scratch, c._need = threading.RLock(), {}, {}
+    c._lens = np.zeros(4, dtype=np.int32)
+    inside, seen = [], []
+
+    class Lib:
+        def busy(self, *args):
+            inside.append(1)
+            seen.append(len(inside))
+            time.sleep(0.002)
+            inside.pop()
+            return 0
+        iq_paged_append = iq_paged_attend = iq_paged_append_attend = iq_paged_trim = iq_paged_read = busy
+    c._lib = Lib()
+    monkeypatch.setattr(paged, "_device", lambda: 0)
+    monkeypatch.setattr(c.__class__, "_tensor", lambda self, t, name: t)
+    monkeypatch.setattr(c.__class__, "_queue", lambda self: 0)
+    monkeypatch.setattr(c.__class__, "_workspace", lambda self, *a: inside.append(1) or time.sleep(0.001) or inside.pop() and torch.empty(1))
+    x, q = torch.zeros(4, 2, 1, 256, dtype=torch.bfloat16), torch.zeros(4, 8, 1, 256, dtype=torch.bfloat16)
+
+    def work():
+        for _ in range(5):
+            c.append(x, x), c.attend(q), c.append_attend(x, x, q), c.trim(1), c.lens
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert seen == [1] * (4 * 5 * 4)
