@@ -35,6 +35,12 @@ def _stream(device_index: int | None = None) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device_index).cuda_stream)
 
 
+def _device_of(device) -> torch.device:
+    """The device of an argument: a name, an index (0 is one), a torch.device, or None for the current one."""
+    d = torch.device("cuda") if device is None else torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
 class _OnDevice:
     """Make `index` the current device for a call, switching only when it is not."""
 
@@ -78,7 +84,7 @@ class Rotation:
     """
 
     def __init__(self, seed: int = 0, head_dim: int = 256, device=None):
-        device = torch.device(device or "cuda")
+        device = _device_of(device)
         nb = head_dim // 4
         self.seed, self.head_dim = seed, head_dim
         self.blocks_f32 = torch.empty((nb, 4, 4), dtype=torch.float32, device=device)
@@ -115,9 +121,7 @@ class IQCache:
         self.batch, self.kv_heads, self.head_dim = batch, kv_heads, head_dim
         self.group_size, self.k_bits, self.v_bits = group_size, k_bits, v_bits
         self.dtype = dtype
-        self.device = torch.device(device or "cuda")
-        if self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device = _device_of(device)
         self._on = _OnDevice(self.device.index)
         self.lens = np.zeros(batch, dtype=np.int32)
         self._workspace = None

@@ -15,7 +15,7 @@ import torch
 
 from . import _abi
 from ._abi import IQ_PAGE, IQPagedDesc, check, lib
-from .cache import _OnDevice, _raw_stream, _stream
+from .cache import _OnDevice, _device_of, _raw_stream, _stream
 
 
 _INT32 = np.dtype(np.int32)
@@ -88,9 +88,9 @@ class IQPagedCache:
         self.max_pages = pages if max_tokens is None else max(1, -(-max_tokens // IQ_PAGE))
         sizes = (ctypes.c_size_t * 6)()
         check(lib().iq_paged_bytes(slots, kv_heads, head_dim, pages, self.max_pages, sizes), "iq_paged_bytes")
-        self.device = torch.device(device or "cuda")
-        if self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
+        if device is not None and not isinstance(device, int) and torch.device(device).type != "cuda":
+            raise ValueError("device must be a CUDA device")
+        self.device = _device_of(device)
         self._index, self._lib = self.device.index, lib()
         dev = self.device
         self.k_codes = torch.empty((pages, kv_heads, IQ_PAGE, head_dim), dtype=torch.uint8, device=dev)

@@ -305,3 +305,14 @@ def test_host_threads_take_turns(monkeypatch):
     for t in threads:
         t.join()
     assert seen == [1] * (4 * 5 * 4)
+
+
+def test_device_arguments(L, monkeypatch):
+    from rotated_bit_quantized_gb300 import IQPagedCache
+    from rotated_bit_quantized_gb300.cache import _device_of
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert _device_of(None) == _device_of("cuda") == torch.device("cuda", 1)
+    assert _device_of(0) == _device_of("cuda:0") == torch.device("cuda", 0)
+    assert _device_of(2) == _device_of(torch.device("cuda", 2)) == torch.device("cuda", 2)
+    with pytest.raises(ValueError, match="CUDA device"):
+        IQPagedCache(1, 1, 1, device="cpu")
