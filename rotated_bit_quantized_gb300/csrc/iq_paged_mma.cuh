@@ -14,6 +14,7 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNothing = -__builtin_huge_valf();      // the score of a key that a row does not see
+constexpr float kAhead = 40.0f;  // how far, in binades, a row's weights may pass its reference before that moves
 constexpr float kUnset = -3e38f, kDead = 3e38f;         // a row's reference before its first key, and of rows that do not exist
 constexpr int kTile = 128;                    // keys per tile: two pages
 constexpr int kHalfBytes = kTile * 128;       // 128 rows of half a head's dims
@@ -239,11 +240,33 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       "l"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
       : "memory");
 }
-__device__ __forceinline__ void mma_e4m3_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {  // A in tensor memory
+// kind::mxf8f6f4: the same product with a power-of-two scale (an exponent + 127 in a
+// byte) for every row of A or B and 32 elements of K.  A scale is byte `id` of the
+// 32-bit word in lane r % 32, column r / 32 of its operand's place in tensor memory,
+// the same in all four groups of 32 lanes.
+constexpr int kScaleBytes = 512;  // of 128 rows and four ids in shared memory: [r % 32][r / 32][id]
+__device__ __forceinline__ int scale_at(int r, int id) { return (r & 31) * 16 + (r >> 5) * 4 + id; }
+__host__ __device__ constexpr uint32_t shape_scaled(int m, int n, bool a_mn, bool b_mn, int a_id, int b_id) {
+  return (static_cast<uint32_t>(b_id) << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24) |
+         (static_cast<uint32_t>(a_id) << 29);
+}
+// the scales of 128 rows from shared memory to four columns; runs in order with the products behind it
+__device__ __forceinline__ void copy_scales(uint32_t to, uint32_t saddr) {
+  const uint64_t from = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1) << 16 |
+                        static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;  // rows of 16 bytes, not swizzled
   asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
-      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u)
+      "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(to),
+      "l"(from)
+      : "memory");
+}
+__device__ __forceinline__ void mma_scaled_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t a_scales, uint32_t b_scales,
+                                                bool add) {  // A in tensor memory
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], [%1], %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(a_scales), "r"(b_scales), "r"(add ? 1u : 0u)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {

@@ -4,18 +4,21 @@
 // The same mathematics as the split kernel (iq_paged_attend.cu) with the query
 // rows as the products' M dimension: S = Q.K^T with Q as two e4m3 parts summed
 // into one accumulator, S (128 rows x 128 keys) twice in tensor memory, and
-// O += W.V with the weights W = 2^(s + ev - ref) as two e4m3 parts that the
-// row threads write over the scores they came from.  Keys and values are the
-// pages' codes as they lie in HBM.  Each product runs twice (high and low
-// part) at e4m3's rate, twice bf16's, so the bound is bf16's rate; no code is
-// ever converted.
+// O += W.V with the weights W as two e4m3 parts that the row threads write over
+// the scores they came from.  Keys and values are the pages' codes as they lie
+// in HBM.  Each product runs twice (high and low part) at e4m3's rate, twice
+// bf16's, so the bound is bf16's rate; no code is ever converted.
 //
-// Rounding.  A weight, as fp16 at first (2^-11 of it), leaves at most 2^-8 of it
-// behind its two parts, and a step of the least codes, 2^-9, below e4m3's range:
-// a row's reference puts its running maximum at 2^5 and moves when a weight
-// would pass 2^8.75 (448 is the largest code), so that floor is 2^-14 of the
-// largest weight or less.  Where within such a step a weight is cut differs from
-// key to key, so what many small weights lose does not add up.
+// Rounding.  The second product is block-scaled: with e the largest score of a
+// row's 32 keys, rounded up, their weights are 2^(s - e + 8), and 2^(e + ev - ref - 8)
+// is their scale.  A weight, as fp16 at first (2^-11 of it), leaves at most 2^-8
+// of it behind its two parts, and half a step of the least codes, 2^-10, where it
+// lies below their range: 2^-17 of the largest weight among its 32 keys, whatever
+// the row's other keys weigh.  (One reference for a row's whole tile, its running
+// maximum at 2^5, left a floor of 2^-15 of the row's largest weight: next to one
+// key with half of it, 32768 others were off by 12% in norm, 131072 by 32%.)
+// The scales also carry what a row's reference does not: that one only keeps the
+// sums in fp32's range, and moves when the scores pass it by 2^kAhead.
 #include <cuda_runtime.h>
 
 #include "iq_paged_mma.cuh"
@@ -27,39 +30,16 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kSlots = 4;                         // tiles of keys or values in flight, from L2 mostly (3: no slower, 5: 1.5% slower)
 constexpr int kQ = kSlots * kSlotBytes;           // [high, low][2 halves of the dims][128 rows][128 bytes]
-constexpr int kMisc = kQ + 4 * kHalfBytes;
+constexpr int kScales = kQ + 4 * kHalfBytes;      // of the weights of a tile, twice; ones, the values'
+constexpr int kMisc = kScales + 3 * kScaleBytes;
 constexpr int kRing = Loader<kSlots, true>::kRing;
 constexpr int kSmem = kMisc + 2 * kRows * 4 + kRing * 16 + 32 * 8;
 constexpr int kThreads = 384;
 constexpr int kLoader = 8, kIssuer = 9, kAsker = 10;
 constexpr int kRowRegs = 208, kRestRegs = 88;     // 2 * 208 + 88 = 3 * 168, what the CTA is launched with
-constexpr float kPlace = 5.0f, kTop = 8.75f;      // the running maximum's place, and how far a weight may grow (448 = 2^8.8)
+constexpr float kPlace = 8.0f;                    // the place of a block's largest weight (2^8.8 = 448 is the largest code)
+constexpr int kWeightScales = 32, kOnes = 96;     // their columns among a tile's 128, where its scores were
 static_assert(kSmem <= 232448, "shared memory of one CTA");
-
-__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Where within a step of e4m3's least codes (2^-9) the weights of keys c and
-// c + 1 of a page are cut, as an fp16 pair: a place of its own for each key
-// (bits reversed), so that many equal small weights are not all cut the same
-// way; each stays below half a step, so that a weight of 0 stays 0.
-__host__ __device__ constexpr uint32_t half_bits(int x) {  // x * 2^-16 as fp16, 0 < |x| < 128
-  const int m = x < 0 ? -x : x;
-  int top = 0;
-  while ((m >> top) > 1) ++top;
-  // 2^(top - 16) is an fp16 subnormal (units of 2^-24) below 2^-14
-  return (x < 0 ? 0x8000u : 0u) |
-         (top < 2 ? static_cast<uint32_t>(m << 8) : static_cast<uint32_t>(top - 1) << 10 | (static_cast<uint32_t>(m << (10 - top)) & 0x3FFu));
-}
-__host__ __device__ constexpr int reversed6(int c) {
-  return (c & 1) << 5 | (c & 2) << 3 | (c & 4) << 1 | (c & 8) >> 1 | (c & 16) >> 3 | (c & 32) >> 5;
-}
-__host__ __device__ constexpr uint32_t cut_at(int c) {  // (reversed / 64 - 63 / 128) steps
-  return half_bits(2 * reversed6(c) - 63) | half_bits(2 * reversed6(c + 1) - 63) << 16;
-}
 
 // The queries' two parts and factors, a warp per four rows, before the kernel
 // below: cut inside it, by warps of its own, they slowed the row threads by a
@@ -84,6 +64,11 @@ __global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ 
     if (j < p.count[e])  // row r of (entry, kv head): query j of query head eh * rep + r % rep
       raw[k] = __ldcs(reinterpret_cast<const uint4*>(p.q + ((static_cast<long long>(eh) * p.rep + r - j * p.rep) * p.nq + j) * kHeadDim) + lane);
   }
+  if (p.scale < 0.0f) {  // the factors are positive, so that the largest product is the largest score
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      raw[k] = make_uint4(raw[k].x ^ 0x80008000u, raw[k].y ^ 0x80008000u, raw[k].z ^ 0x80008000u, raw[k].w ^ 0x80008000u);
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint2 hi, lo;
@@ -92,7 +77,7 @@ __global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ 
     if (w >= p.total) break;
     reinterpret_cast<uint2*>(p.cut + w * kHeadDim)[lane] = hi;
     reinterpret_cast<uint2*>(p.cut + (p.total + w) * kHeadDim)[lane] = lo;
-    if (lane == 0) p.factors[w] = clamp_finite(f * (p.scale * kLog2e));
+    if (lane == 0) p.factors[w] = fminf(f * (fabsf(p.scale) * kLog2e), 3e38f);
   }
 }
 
@@ -107,9 +92,11 @@ __global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ 
 // Bound by the row threads' chain (scores out of tensor memory, maximum, vote,
 // exponentials, two parts, back), 2.6 K cycles a tile, next to the products' 2.1 K
 // (measured alone, of 2.05 K at the nominal rate).  2048 queries of 16 / 2 heads
-// over 32768 keys: 664 us, 1605 TFLOP/s, 84% of a measured bf16 matrix product; a
-// unit's beginning and end cost 4 to 5 tiles' time, which shows where units are
-// short: 4 x 1531 tokens 118 us, 8191 under a window of 1023 188 us.  What counted
+// over 32768 keys: 741 us, 1440 TFLOP/s, 75% of a measured bf16 matrix product
+// (710 with weights that are not block-scaled, whose second product reads no
+// scales); a unit's beginning and end cost 4 to 5 tiles' time, which shows where
+// units are short: 4 x 1531 tokens 114 us, 8191 under a window of 1023 177 us
+// (118 and 188 without: references had to follow the maxima).  What counted
 // on the way: the queries cut beforehand (260 to 214 us on the last), products
 // issued by a whole warp (745 to 673 us on the first), the references' rescaling
 // behind the weights, scores issued over a unit's end.
@@ -154,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
     *abort = 0;
     mbar_fence_init();
   }
+  if (threadIdx.x < kScaleBytes / 4) reinterpret_cast<uint32_t*>(smem + kScales + 2 * kScaleBytes)[threadIdx.x] = 0x7F7F7F7Fu;
+  proxy_fence();
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -250,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int pos = len - p.count[e] + query_of(p, w.z * kRows + r);
       const int stop = !exists ? 0 : p.causal ? pos + 1 : len;
       const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-      // a row that has seen no key yet has no reference (its weights are relative to 2^0)
+      // a row that has seen no key yet has no reference (its weights are all 0)
       bool unset = exists;
       float ref = exists ? 0.0f : kDead, l = 0.0f;
 
@@ -266,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
         if (n > 0) {
           await(&scales_in[it % kRing], it / kRing);
           const float* sc = reinterpret_cast<const float*>(&scales[it % kRing]) + group;  // this thread's page
-          const float f = clamp_finite(fq * sc[0]);
-          const int ev = exponent_of(sc[2]);
+          float f = fminf(fmaxf(fq * sc[0], 2e-38f), 3e38f);  // (above 0: a hidden key's score stays below all)
+          const float ev = static_cast<float>(exponent_of(sc[2]));
           const int t0 = tiles.tile(k0 + j) * kTile;
           // whether some row of the unit does not see the whole tile
           const bool masked = t0 + kTile > (p.causal ? tiles.p_lo + 1 : len) ||
@@ -279,9 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           tmem_ld<32>(t_s, s);
           tmem_ld<32>(t_s + 32, s + 32);
           ld_wait();
-          const float shift = static_cast<float>(ev) - ref;
-#pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = fmaf(s[i], f, shift);
           if (masked) {
             const int tb = t0 + group * 64;
             auto below = [&](int x) { return x <= tb ? 0ull : x - tb >= 64 ? ~0ull : (1ull << (x - tb)) - 1; };  // keys before x
@@ -290,11 +276,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
             for (int i = 0; i < 64; ++i)
               if (!(static_cast<uint32_t>(see >> (i & 32)) & 1u << (i & 31))) s[i] = kNothing;
           }
-          float m = s[0];
+          float m0 = s[0], m1 = s[32];
 #pragma unroll
-          for (int i = 1; i < 63; i += 2) m = fmaxf(fmaxf(m, s[i]), s[i + 1]);
-          m = fmaxf(m, s[63]);
-          int far = m > kTop || (unset && m > kNothing);
+          for (int i = 1; i < 31; i += 2) {
+            m0 = fmaxf(fmaxf(m0, s[i]), s[i + 1]);
+            m1 = fmaxf(fmaxf(m1, s[32 + i]), s[33 + i]);
+          }
+          m0 = __fmul_rn(fmaxf(m0, s[31]), f);
+          m1 = __fmul_rn(fmaxf(m1, s[63]), f);
+          const float e0 = fmaxf(ceilf(m0), kUnset), e1 = fmaxf(ceilf(m1), kUnset);  // kUnset: no key is seen
+          float shift0 = kPlace - e0, shift1 = kPlace - e1;
+          if (fmaxf(e0 > kUnset ? fabsf(e0) : 0.0f, e1 > kUnset ? fabsf(e1) : 0.0f) >= 4194304.0f) {
+            // scores whose own rounding counts: the same one for the maximum and
+            // for every key, so that no weight passes 2^kPlace
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i] = __fsub_rn(__fmul_rn(s[i], f), i < 32 ? e0 : e1);
+            f = 1.0f;
+            shift0 = shift1 = kPlace;
+          }
+          __syncwarp();
+          float top = fmaxf(e0, e1) + ev;
+          int far = top - ref > kAhead || (unset && top > kUnset);
           asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
                        : "+r"(far)
                        : "r"(1 + quad)
@@ -302,32 +304,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           float change = 1.0f;
           if (far) {
             // some row of the quad passed its reference: move such rows' references
-            // so that their maxima land at 2^kPlace
-            xch[group * kRows + r] = m;
+            // to their maxima
+            xch[group * kRows + r] = top;
             named_bar(1 + quad, 64);
-            m = fmaxf(m, xch[(group ^ 1) * kRows + r]);
+            top = fmaxf(top, xch[(group ^ 1) * kRows + r]);
             named_bar(1 + quad, 64);
-            float move = 0.0f;
-            if (m > kTop || (unset && m > kNothing)) move = m - kPlace;
-            ref += move;
-            if (!unset) change = ex2_approx(-move);  // (else there is nothing yet, and move may be far below 0)
-            unset = unset && !(m > kNothing);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] -= move;
+            if (top - ref > kAhead || (unset && top > kUnset)) {
+              if (!unset) change = ex2_approx(ref - top);  // (else there is nothing yet)
+              ref = top;
+              unset = false;
+            }
             l *= change;
           }
+          // the blocks' scales, 2^(above - kPlace), down to the least that a byte holds
+          const float above0 = (e0 + ev) - ref, above1 = (e1 + ev) - ref;
+          const int least = 127 - static_cast<int>(kPlace);
+          const int scale0 = static_cast<int>(fminf(fmaxf(above0, static_cast<float>(-least)), kAhead)) + least;
+          const int scale1 = static_cast<int>(fminf(fmaxf(above1, static_cast<float>(-least)), kAhead)) + least;
+          *reinterpret_cast<uint16_t*>(smem + kScales + b * kScaleBytes + scale_at(r, 2 * group)) = static_cast<uint16_t>(scale0 | scale1 << 8);
           // the weights; as fp16 pairs (11 bits), cut into two parts of 4 bits, over
           // the scores that this thread has read
-          float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
+            const float shift = x ? shift1 : shift0;
+            float s0 = 0.0f, s1 = 0.0f;
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint32_t ha, hb;
               {
                 const int c = 32 * x + 4 * i;
-                const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]), w2 = ex2_approx(s[c + 2]), w3 = ex2_approx(s[c + 3]);
+                const float w0 = ex2_approx(fmaf(s[c], f, shift)), w1 = ex2_approx(fmaf(s[c + 1], f, shift));
+                const float w2 = ex2_approx(fmaf(s[c + 2], f, shift)), w3 = ex2_approx(fmaf(s[c + 3], f, shift));
                 s0 += w0;
                 s1 += w1;
                 s0 += w2;
@@ -337,13 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
               }
               const uint32_t a = e4m3x2_of_f16x2(ha), d = e4m3x2_of_f16x2(hb);
               hi[i] = a | d << 16;
-              lo[i] = e4m3x2_of_f16x2(add_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a)), cut_at(32 * x + 4 * i))) |
-                      e4m3x2_of_f16x2(add_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d)), cut_at(32 * x + 4 * i + 2))) << 16;
+              lo[i] = e4m3x2_of_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a))) | e4m3x2_of_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d))) << 16;
             }
             tmem_st<8>(t_s + 8 * x, reinterpret_cast<const float*>(hi));
             tmem_st<8>(t_s + 16 + 8 * x, reinterpret_cast<const float*>(lo));
+            l = fmaf(s0 + s1, ex2_approx((x ? above1 : above0) - ev - kPlace), l);
           }
-          l = fmaf(s0 + s1, power2(-ev), l);
           if (far && j > 0) {
             // what was summed with the old references, this thread's half of the
             // row; last, so that the product with the tile before, which has to end
@@ -363,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
             }
           }
           st_wait();
+          proxy_fence();
         }
         if (j == 0 && pending) store_results(it - 1);
         if (n > 0) {
@@ -388,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       Loader<kSlots, true>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy);
     } else if (warp == kIssuer) {
       // ---------------------------------------------------------------- products
-      constexpr uint32_t kS = shape(128, kTile, false, false), kO = shape(128, kHeadDim, false, true);
+      constexpr uint32_t kS = shape(128, kTile, false, false);
       int used = 0;
       bool ok = true;
       // descriptors count in 16 bytes: those of other pieces are sums
@@ -437,10 +445,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           ok = wait.together(&p_ready[b], it / 2, kLostMma) && wait.together(&full[s], used / kSlots, kLostMma);
           if (!ok) break;
           tc_after();
+          // The weights' scales (a copy of 75 cycles, which the products wait for) and
+          // the values'.  Told to this warp by a barrier of their own and copied before
+          // the weights are there: 756 against 741 us for the chunk below, as the row
+          // threads then stop once more; before the scores ahead: 790.
+          const uint32_t weights = tmem + b * 128;
+          copy_scales(weights + kWeightScales, sbase + kScales + b * kScaleBytes);
+          copy_scales(weights + kOnes, sbase + kScales + 2 * kScaleBytes);
+          copy_scales(weights + kOnes + 4, sbase + kScales + 2 * kScaleBytes);
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 32 keys at a time, their high and low parts in turn
-            mma_e4m3_tmem(t_o, tmem + b * 128 + (k >> 2) * 64 + ((k >> 1) & 1) * 8 + (k & 1) * 16,
-                          at_values + ((s * kSlotBytes + (k >> 1) * 32 * 128) >> 4), kO, j > 0 || k > 0);
+            mma_scaled_tmem(t_o, weights + (k >> 2) * 64 + ((k >> 1) & 1) * 8 + (k & 1) * 16,
+                            at_values + ((s * kSlotBytes + (k >> 1) * 32 * 128) >> 4),
+                            shape_scaled(128, kHeadDim, false, true, k >> 1, 0), weights + kWeightScales, weights + kOnes, j > 0 || k > 0);
           mma_commit(&o_done[b]);
           mma_commit(&empty[s]);
           ++used;

@@ -472,6 +472,32 @@ def test_one_heavy_key_and_a_long_flat_tail(n, spread):
     assert (np.abs(got - out) <= (2.0**-8 + 2.0**-11 + 3 * 2.0**-8.8 + 2.0**-13) * weight).all()
 
 
+@pytest.mark.parametrize("n", [140])
+@pytest.mark.parametrize("N", [4096, 32768, 131072])
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+def test_small_weights_beside_a_heavy_key(n, N, spread):
+    """Half of the weight on one key whose value is 0, as on a first token that only draws attention: what comes out is
+    what N small weights leave, on values without a common part.  Every weight is held in two e4m3 parts to 2^-8 of it
+    (and 2^-11 for its fp16 form), and, where it lies below 2^-8 of the largest among its 32 keys, to 2^-9 or worse of
+    what then hardly counts; the errors go with the values' signs, so the result is off by as much, in norm, at most;
+    then exp and the scores' own error (slack, see check_attend), which moves all small weights alike."""
+    H = 2
+    c, o = pair(1, 1, N // 64 + 2)
+    g = torch.Generator().manual_seed(N + n)
+    u = torch.randn(256, generator=g).sign() * 0.25  # |u|^2 = 16
+    k = torch.randn(1, 1, N + 1, 1, generator=g) * spread / np.log(N) * 8 * u
+    k[0, 0, 777] = 8 * u
+    v = torch.randn(1, 1, N + 1, 256, generator=g)
+    v[0, 0, 777] = 0
+    put(c, o, k.bfloat16(), v.bfloat16())
+    q = u.expand(1, H, n, 256).bfloat16()
+    scale = np.log(N) / 128
+    out, weight, floor, slack = paged.attend(o, f64(q), scale, causal=False)
+    got = f64(c.attend(q.cuda(), scale=scale, causal=False, out_dtype=torch.float32))
+    off = np.linalg.norm(got - out) / np.linalg.norm(out)
+    assert off <= 2.0**-8 + 2.0**-9 + 2.0**-11 + 2.0**-13 + 2 * (2.0**-17 + 2.0**-16) * slack.max(), off
+
+
 def test_append_attend_is_both_calls():
     for lens, n, nq in [([100, 0, 64, 63], 1, 1), ([500, 3, 1, 0], 4, 4), ([130, 700, 0, 64], 150, 150), ([70, 5, 9, 200], 3, 1)]:
         a, o = pair(5, 2, 60)
