@@ -10,16 +10,18 @@
 // (hi + lo / 16), and key codes K of a page under 2^ek, the scores in log2 units
 // are  s = (K.hi + K.lo / 16) * 2^ek * (2^eq * scale * log2 e): exact products,
 // summed in fp32 by the tensor cores, hi and lo as columns of their own.  With
-// value codes V of a page under 2^ev, the weight of a key is
-// w = 2^(s + ev - ref) = p * 2^ev up to a common factor, so
-// o = sum w V / sum w 2^-ev : the value scales ride in the exponents.  w is held
-// as two e4m3 parts, hi + lo / 128, in columns of their own again (off by at most
-// 2^-8 of it, at random, and below e4m3's range by a step of the least codes, 2^-16
-// of the largest weight, cut at another place for each key); the sum w 2^-ev takes
-// w before that rounding, in fp32.  ref moves only when a
-// weight would pass 2^6 (it then becomes the row's maximum), so steady-state
-// tiles need no exchange between the threads, which hold one key each, but a
-// vote.
+// value codes V of a page under 2^ev, a key weighs 2^(s + ev - ref) = p * 2^ev up
+// to a common factor, so o = sum p 2^ev V / sum p : the value scales ride in the
+// exponents.  The second product is block-scaled: with e the largest score of a
+// row's 32 keys (a warp's), rounded up, their weights are w = 2^(s - e + 6) and
+// 2^(e + ev - ref - 6) is their scale.  w is held as two e4m3 parts, hi + lo / 128,
+// in columns of their own again: off by at most 2^-8 of it, at random, and below
+// e4m3's range by half a step of the least codes, 2^-22 of the largest weight among
+// its 32 keys.  (One reference for the whole row left 2^-17 of the row's largest:
+// next to one key with half of it, 131072 others were off by 8% in norm.)  The sum
+// of p takes w before that rounding, in fp32.  ref only keeps the sums in fp32's
+// range: it moves when the scores pass it by 2^kAhead, so steady-state tiles need
+// no exchange between warps but a vote.
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -34,7 +36,7 @@ namespace paged {
 
 // ------------------------------------------------------------------ decode and verify
 
-constexpr float kTau = 6.0f;    // weights stay below 2^6
+constexpr float kPlace = 6.0f;  // the place of a block's largest weight
 constexpr float kPLo = 128.0f;  // the low parts' scale: half a step at 2^6 is 2, times 128 below 448
 
 template <int NR>
@@ -45,11 +47,12 @@ struct SplitShape {
   static constexpr int kSlots = NR == 64 ? 5 : 6;     // tiles of keys or values in flight
   static constexpr int kQ = kSlots * kSlotBytes;      // [2 halves of the dims][kCols rows][128 bytes]
   static constexpr int kP = kQ + 2 * kCols * 128;     // [2][kCols rows][128 keys]
-  static constexpr int kMisc = kP + 2 * kCols * 128;
+  static constexpr int kScales = kP + 2 * kCols * 128;  // [2] the weights'
+  static constexpr int kMisc = kScales + 2 * kScaleBytes;
   static constexpr int kRing = Loader<kSlots, false>::kRing;
   static constexpr int kFloats = 2 * NR + 4 * NR;     // factors, references; reductions
   static constexpr int kBars = 2 * kSlots + kRing + 10;
-  static constexpr int kSmem = 1024 + kMisc + kFloats * 4 + kRing * 16 + kBars * 8 + 8;
+  static constexpr int kSmem = kMisc + kFloats * 4 + kRing * 16 + kBars * 8 + 8;
   static constexpr int kThreads = kGroups * 128 + 64;
   static constexpr int kTmem = 4 * kCols;             // S twice, O of both halves of the dims
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -64,19 +67,24 @@ struct SplitShape {
 // its 64 KB take from HBM.  Five or six tiles of keys or values in flight (192 KB
 // per SM) cover HBM's latency.  Up to 64 rows: at 32 the row work is still
 // shorter than the stream, beyond 64 the columns of tensor memory end.
-// Bound by HBM.  32 slots x 32768 tokens, 16 / 2 heads, one query: 165 us, 1.07 GB
-// at 6.5 TB/s (96% of a measured copy), DRAM traffic within 0.1% of the keys and
-// values.  8 x 131072 tokens, four queries: 179 us.  One slot of 4096 tokens: 10.6
-// us with the join, a launch's and a pipeline's latency.  A thread's own loads of
+// Bound by HBM.  32 slots x 32768 tokens, 16 / 2 heads, one query: 168 us, 1.07 GB
+// at 6.4 TB/s (94% of a measured copy), DRAM traffic within 0.1% of the keys and
+// values.  8 x 131072 tokens, four queries: 183 us.  One slot of 4096 tokens: 10.7
+// us with the join, a launch's and a pipeline's latency.  The weights' block scales
+// cost 1 us of the first.  A thread's own loads of
 // its page's scale, one tile ahead, cost 5%: under a full HBM they take longer
 // than a tile; the loading warp hands them over instead.
 template <int NR>
 __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kernel(const __grid_constant__ AttendParams p) {
   using C = SplitShape<NR>;
   constexpr int RT = C::kRows;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled operands need it; no room to align by hand
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // (the kernel has no other shared memory in front)
+    wait_for_last_kernel();
+    if (threadIdx.x == 0) atomicOr(p.status, kLostMma);
+    return;
+  }
   float* factor = reinterpret_cast<float*>(smem + C::kMisc);  // [NR] 2^eq * scale * log2 e
   float* ref = factor + NR;                                   // [NR]
   float* red = ref + NR;                                      // [4 warps][NR]
@@ -133,7 +141,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
   } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- products
     {
-      constexpr uint32_t kS = shape(128, C::kCols, false, false), kO = shape(128, C::kCols, true, false);
+      constexpr uint32_t kS = shape(128, C::kCols, false, false);
       // descriptors count in 16 bytes: those of other pieces are sums
       const uint64_t queries = operand(sbase + C::kQ), weights = operand(sbase + C::kP), at_slot = operand(sbase);
       int it = 0, used = 0, segment = 0;
@@ -164,12 +172,15 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
             ok = wait.together(&p_ready[b], (it + j - 1) / 2, kLostMma) && wait.together(&full[s], used / C::kSlots, kLostMma);
             if (!ok) break;
             tc_after();
+            const uint32_t place = tmem + b * C::kCols;  // of the scales, where the scores were; the values' behind them
+            copy_scales(place, sbase + C::kScales + b * kScaleBytes);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_e4m3(t_o + half * C::kCols, at_slot + ((s * kSlotBytes + half * kHalfBytes + k * 32 * 128) >> 4),
-                         weights + ((b * C::kCols * 128 + k * 32) >> 4), kO, j > 1 || k > 0);
+                mma_scaled(t_o + half * C::kCols, at_slot + ((s * kSlotBytes + half * kHalfBytes + k * 32 * 128) >> 4),
+                           weights + ((b * C::kCols * 128 + k * 32) >> 4), shape_scaled(128, C::kCols, true, false, 0, k), place + 4, place,
+                           j > 1 || k > 0);
             mma_commit(&o_done[b]);
             mma_commit(&empty[s]);
             ++used;
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         await(&scales_in[it % C::kRing], it / C::kRing);
         const float* sc = reinterpret_cast<const float*>(&scales[it % C::kRing]) + (key >> 6);  // this key's page
         const float ks = sc[0];
-        const int ev = exponent_of(sc[2]);
+        const float ev = static_cast<float>(exponent_of(sc[2]));
         const int t0 = tiles.tile(k0 + j) * kTile;
         await(&s_full[b], it / 2);
         tc_after();
@@ -251,7 +262,7 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[b]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r] = fmaf(w[r], 1.0f / 16, s[r]) * clamp_finite(factor[r0 + r] * ks) + static_cast<float>(ev);
+        for (int r = 0; r < RT; ++r) s[r] = fmaf(w[r], 1.0f / 16, s[r]) * clamp_finite(factor[r0 + r] * ks);
         // masks, in tiles that some row does not see whole
         const bool low_ok = p.window == 0 || t0 > tiles.p_hi - p.window || t0 + kTile <= p.sinks;
         if (!(t0 + kTile <= (p.causal ? tiles.p_lo + 1 : len) && low_ok)) {
@@ -263,77 +274,89 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
             if (!see) s[r] = kNothing;
           }
         }
-        int far = 0;
+        // lane r: the exponent of row r's largest weight here (kUnset: no key is seen)
+        float top = kUnset;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) far |= s[r] - ref[r0 + r] > kTau;
+        for (int r = 0; r < RT; ++r) {
+          const float m = warp_max(s[r]);
+          if (lane == r) top = m;
+        }
+        top = fmaxf(ceilf(top), kUnset);
+        const int own = r0 + lane % RT;
+        int far = lane < RT && top + ev - ref[own] > kAhead;
         asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 128, a;\nselp.s32 %0, 1, 0, b;\n}"
                      : "+r"(far)
                      : "r"(1 + group)
                      : "memory");
         if (far) {
-          // some row's maximum passed its reference by 2^6: move the references
-          // of such rows to their maxima, and what was summed with them
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            float m = s[r];
-#pragma unroll
-            for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            if (lane == 0) red[(warp & 3) * NR + r0 + r] = m;
-          }
+          // some row's scores passed its reference by 2^kAhead, or are its first: move
+          // the references of such rows to their maxima, and what was summed with them
+          if (lane < RT) red[(warp & 3) * NR + own] = top + ev;
           named_bar(1 + group, 128);
           if (j > 0) await(&o_done[b ^ 1], (it - 1) / 2);
           tc_after();
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const int x = r0 + r;
-            const float m = fmaxf(fmaxf(red[x], red[NR + x]), fmaxf(red[2 * NR + x], red[3 * NR + x])), old = ref[x];
-            w[r] = m - old > kTau ? ex2_approx(old - m) : 1.0f;  // the row's change
-            l[r] *= w[r];
-          }
-          if (j > 0) {
+          for (int r = 0; r < RT; r += 8) {
+            float change[8];
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {  // both halves of the dims, high and low parts
-              const uint32_t c = t_o + lanes + (part >> 1) * C::kCols + (part & 1) * NR + r0;
+            for (int y = 0; y < 8; ++y) {
+              const int x = r0 + r + y;
+              const float m = fmaxf(fmaxf(red[x], red[NR + x]), fmaxf(red[2 * NR + x], red[3 * NR + x])), old = ref[x];
+              change[y] = m - old > kAhead ? ex2_approx(old - m) : 1.0f;
+              l[r + y] *= change[y];
+            }
+            if (j > 0) {
 #pragma unroll
-              for (int x = 0; x < RT; x += 8) {
+              for (int part = 0; part < 4; ++part) {  // both halves of the dims, high and low parts
+                const uint32_t c = t_o + lanes + (part >> 1) * C::kCols + (part & 1) * NR + r0 + r;
                 float o[8];
-                tmem_ld<8>(c + x, o);
+                tmem_ld<8>(c, o);
                 ld_wait();
 #pragma unroll
-                for (int y = 0; y < 8; ++y) o[y] *= w[x + y];
-                tmem_st<8>(c + x, o);
+                for (int y = 0; y < 8; ++y) o[y] *= change[y];
+                tmem_st<8>(c, o);
               }
             }
-            st_wait();
           }
+          if (j > 0) st_wait();
           named_bar(1 + group, 128);
           if (key < RT) {
             const int x = r0 + key;
             const float m = fmaxf(fmaxf(red[x], red[NR + x]), fmaxf(red[2 * NR + x], red[3 * NR + x]));
-            if (m - ref[x] > kTau) ref[x] = m;
+            if (m - ref[x] > kAhead) ref[x] = m;
           }
           named_bar(1 + group, 128);
         }
         // weights, their sums, their two parts (the buffer is free once tile it - 2 is multiplied)
         if (it >= 2) await(&o_done[b], it / 2 - 1);
         uint8_t* pb = smem + C::kP + b * C::kCols * 128;
-        const float back = power2(-ev);
-        // where within a step of the low parts' least codes this key's weights are
-        // cut: another place for each key, so that many equal small weights are
-        // not all cut the same way (their sum would be off by up to half of it)
-        const float cut = (static_cast<float>((__brev(key) >> 25) + (it & 15) * 8 & 127) - 63.5f) * (1.0f / 128 / 512);
+        const float above = top + ev - ref[own], back = ex2_approx(above - ev - kPlace);
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
-          const float a = ex2_approx(s[r] - ref[r0 + r]), c = ex2_approx(s[r + 1] - ref[r0 + r + 1]);
-          l[r] = fmaf(a, back, l[r]);
-          l[r + 1] = fmaf(c, back, l[r + 1]);
+          const float e0 = __shfl_sync(0xFFFFFFFFu, top, r), e1 = __shfl_sync(0xFFFFFFFFu, top, r + 1);
+          // (the difference first: it is exact near the maximum however large the scores are)
+          const float a = ex2_approx(s[r] - e0 + kPlace), c = ex2_approx(s[r + 1] - e1 + kPlace);
+          l[r] = fmaf(a, __shfl_sync(0xFFFFFFFFu, back, r), l[r]);
+          l[r + 1] = fmaf(c, __shfl_sync(0xFFFFFFFFu, back, r + 1), l[r + 1]);
           const uint32_t hi = e4m3x2(a, c);
           const float2 f = f16x2_to_f32(e4m3x2_to_f16x2(hi));
-          const uint32_t lo = e4m3x2(fmaf(a - f.x, kPLo, cut), fmaf(c - f.y, kPLo, cut));
+          const uint32_t lo = e4m3x2((a - f.x) * kPLo, (c - f.y) * kPLo);
           pb[swizzled(r0 + r, key)] = static_cast<uint8_t>(hi);
           pb[swizzled(r0 + r + 1, key)] = static_cast<uint8_t>(hi >> 8);
           pb[swizzled(NR + r0 + r, key)] = static_cast<uint8_t>(lo);
           pb[swizzled(NR + r0 + r + 1, key)] = static_cast<uint8_t>(lo >> 8);
+        }
+        if (lane < RT) {  // down to the least that a byte holds
+          constexpr float kLeast = 127.0f - kPlace;
+          const uint8_t x = static_cast<uint8_t>(static_cast<int>(fminf(fmaxf(above, -kLeast), kAhead) + kLeast));
+          uint8_t* to = smem + C::kScales + b * kScaleBytes;
+          to[scale_at(r0 + lane, warp & 3)] = x;
+          to[scale_at(NR + r0 + lane, warp & 3)] = x;
+        }
+        if (group == 0) {  // the values' scales, 1; the scores' place is free until this tile is multiplied
+          const float one = __uint_as_float(0x7F7F7F7Fu), ones[4] = {one, one, one, one};
+          tmem_st<4>(tmem + lanes + b * C::kCols + 4, ones);
+          st_wait();
         }
         proxy_fence();
         tc_before();

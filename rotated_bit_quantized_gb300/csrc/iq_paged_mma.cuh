@@ -269,6 +269,13 @@ __device__ __forceinline__ void mma_scaled_tmem(uint32_t d, uint32_t a, uint64_t
       "r"(a), "l"(b), "r"(id), "r"(a_scales), "r"(b_scales), "r"(add ? 1u : 0u)
       : "memory");
 }
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t a_scales, uint32_t b_scales, bool add) {
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(a_scales), "r"(b_scales), "r"(add ? 1u : 0u)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
       "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
@@ -444,6 +451,11 @@ __device__ __forceinline__ void tmem_ld<32>(uint32_t addr, float* v) {
       : "r"(addr));
 }
 template <>
+__device__ __forceinline__ void tmem_st<4>(uint32_t addr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+               : "memory");
+}
+template <>
 __device__ __forceinline__ void tmem_st<8>(uint32_t addr, const float* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(v[0]), "f"(v[1]),
                "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
@@ -517,6 +529,12 @@ __device__ __forceinline__ float split_query(uint4 raw, uint2& hi, uint2& lo) {
   hi = make_uint2(h[0] | h[1] << 16 | bad, h[2] | h[3] << 16 | bad);
   lo = make_uint2(l[0] | l[1] << 16 | bad, l[2] | l[3] << 16 | bad);
   return power2(e);
+}
+// the largest of a whole warp's values (of those that are numbers)
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(x));
+  return m;
 }
 __device__ __forceinline__ float clamp_finite(float x) { return fminf(fmaxf(x, -3e38f), 3e38f); }
 

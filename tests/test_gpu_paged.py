@@ -472,7 +472,7 @@ def test_one_heavy_key_and_a_long_flat_tail(n, spread):
     assert (np.abs(got - out) <= (2.0**-8 + 2.0**-11 + 3 * 2.0**-8.8 + 2.0**-13) * weight).all()
 
 
-@pytest.mark.parametrize("n", [140])
+@pytest.mark.parametrize("n", [1, 4, 8, 12, 24, 140])
 @pytest.mark.parametrize("N", [4096, 32768, 131072])
 @pytest.mark.parametrize("spread", [0.0, 1.0])
 def test_small_weights_beside_a_heavy_key(n, N, spread):
