@@ -33,6 +33,11 @@ __device__ __forceinline__ void wait_for_last_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// For a kernel that takes tensor memory: it takes it between these two.  A kernel
+// that holds some while it waits for another, which may still have to take its own
+// on the same multiprocessor, could wait forever.
+__device__ __forceinline__ void wait_only() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void release_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Two floats to e4m3, to nearest even, saturating at +-448: `lo` in bits 0..7.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

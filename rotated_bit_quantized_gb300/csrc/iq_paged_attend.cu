@@ -121,14 +121,15 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
     *abort = 0;
     mbar_fence_init();
   }
+  wait_only();
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(C::kTmem));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  wait_for_last_kernel();
   tc_before();
   __syncthreads();
   tc_after();
+  release_dependents();
   const uint32_t tmem = *tslot;
   const uint32_t t_o = tmem + 2 * C::kCols;  // O: [half of the dims][kCols]
   const Waits wait{abort, p.status};

@@ -143,14 +143,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
   }
   if (threadIdx.x < kScaleBytes / 4) reinterpret_cast<uint32_t*>(smem + kScales + 2 * kScaleBytes)[threadIdx.x] = 0x7F7F7F7Fu;
   proxy_fence();
+  wait_only();
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  wait_for_last_kernel();
   tc_before();
   __syncthreads();
   tc_after();
+  release_dependents();
   const uint32_t tmem = *tslot, t_o = tmem + 256;  // S or W: 0..127, 128..255; O: 256..511
   const Waits wait{abort, p.status};
 
