@@ -12,16 +12,18 @@
 // summed in fp32 by the tensor cores, hi and lo as columns of their own.  With
 // value codes V of a page under 2^ev, a key weighs 2^(s + ev - ref) = p * 2^ev up
 // to a common factor, so o = sum p 2^ev V / sum p : the value scales ride in the
-// exponents.  The second product is block-scaled: with e the largest score of a
-// row's 32 keys (a warp's), rounded up, their weights are w = 2^(s - e + 6) and
-// 2^(e + ev - ref - 6) is their scale.  w is held as two e4m3 parts, hi + lo / 128,
-// in columns of their own again: off by at most 2^-8 of it, at random, and below
-// e4m3's range by half a step of the least codes, 2^-22 of the largest weight among
-// its 32 keys.  (One reference for the whole row left 2^-17 of the row's largest:
-// next to one key with half of it, 131072 others were off by 8% in norm.)  The sum
-// of p takes w before that rounding, in fp32.  ref only keeps the sums in fp32's
-// range: it moves when the scores pass it by 2^kAhead, so steady-state tiles need
-// no exchange between warps but a vote.
+// exponents.  The second product is block-scaled: with e the exponent s + ev - ref
+// of the largest weight of a row's 32 keys (a warp's), rounded up, they are held as
+// w = 2^(s + ev - ref - e + 6) under the scale 2^(e - 6).  w has two e4m3 parts, hi +
+// lo / 128, in columns of their own again: off by at most 2^-8 of it, at random, and
+// below e4m3's range by half a step of the least codes, 2^-22 of the largest weight
+// among its 32 keys.  (One reference for the whole row left 2^-17 of the row's
+// largest: next to one key with half of it, 131072 others were off by 8% in norm.)
+// The sum of p, in fp32, takes w as the parts hold it: where one key dominates, its
+// rounding then cancels (0.00035 off in norm for 32 x 32768 tokens, 0.0006 with w
+// itself; no slower).  ref only keeps the sums in fp32's range: it moves, to the row's
+// maximum, when the weights pass it by 2^kAhead, so steady-state tiles need no
+// exchange between warps but a vote.
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -69,7 +71,7 @@ struct SplitShape {
 // shorter than the stream, beyond 64 the columns of tensor memory end.
 // Bound by HBM.  32 slots x 32768 tokens, 16 / 2 heads, one query: 168 us, 1.07 GB
 // at 6.4 TB/s (94% of a measured copy), DRAM traffic within 0.1% of the keys and
-// values.  8 x 131072 tokens, four queries: 183 us.  One slot of 4096 tokens: 10.7
+// values.  8 x 131072 tokens, four queries: 175 us.  One slot of 4096 tokens: 10.7
 // us with the join, a launch's and a pipeline's latency.  The weights' block scales
 // cost 1 us of the first.  A thread's own loads of
 // its page's scale, one tile ahead, cost 5%: under a full HBM they take longer
@@ -275,14 +277,13 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
             if (!see) s[r] = kNothing;
           }
         }
-        // lane r: the exponent of row r's largest weight here (kUnset: no key is seen)
-        float top = kUnset;
+        // lane r: the largest score of row r among the warp's keys
+        float top = kNothing;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           const float m = warp_max(s[r]);
           if (lane == r) top = m;
         }
-        top = fmaxf(ceilf(top), kUnset);
         const int own = r0 + lane % RT;
         int far = lane < RT && top + ev - ref[own] > kAhead;
         asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 128, a;\nselp.s32 %0, 1, 0, b;\n}"
@@ -331,17 +332,20 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         // weights, their sums, their two parts (the buffer is free once tile it - 2 is multiplied)
         if (it >= 2) await(&o_done[b], it / 2 - 1);
         uint8_t* pb = smem + C::kP + b * C::kCols * 128;
-        const float above = top + ev - ref[own], back = ex2_approx(above - ev - kPlace);
+        const float real = top + ev - ref[own], above = fmaxf(ceilf(real), kUnset), back = ex2_approx(above - ev - kPlace);
+        const float below = real - above + kPlace;  // the exponent of the row's largest weight here
+        top = fmaxf(top, kUnset);                   // (kUnset: no key is seen)
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
-          const float e0 = __shfl_sync(0xFFFFFFFFu, top, r), e1 = __shfl_sync(0xFFFFFFFFu, top, r + 1);
           // (the difference first: it is exact near the maximum however large the scores are)
-          const float a = ex2_approx(s[r] - e0 + kPlace), c = ex2_approx(s[r + 1] - e1 + kPlace);
-          l[r] = fmaf(a, __shfl_sync(0xFFFFFFFFu, back, r), l[r]);
-          l[r + 1] = fmaf(c, __shfl_sync(0xFFFFFFFFu, back, r + 1), l[r + 1]);
+          const float a = ex2_approx(s[r] - __shfl_sync(0xFFFFFFFFu, top, r) + __shfl_sync(0xFFFFFFFFu, below, r));
+          const float c = ex2_approx(s[r + 1] - __shfl_sync(0xFFFFFFFFu, top, r + 1) + __shfl_sync(0xFFFFFFFFu, below, r + 1));
           const uint32_t hi = e4m3x2(a, c);
           const float2 f = f16x2_to_f32(e4m3x2_to_f16x2(hi));
           const uint32_t lo = e4m3x2((a - f.x) * kPLo, (c - f.y) * kPLo);
+          const float2 g = f16x2_to_f32(e4m3x2_to_f16x2(lo));
+          l[r] = fmaf(fmaf(g.x, 1.0f / kPLo, f.x), __shfl_sync(0xFFFFFFFFu, back, r), l[r]);
+          l[r + 1] = fmaf(fmaf(g.y, 1.0f / kPLo, f.y), __shfl_sync(0xFFFFFFFFu, back, r + 1), l[r + 1]);
           pb[swizzled(r0 + r, key)] = static_cast<uint8_t>(hi);
           pb[swizzled(r0 + r + 1, key)] = static_cast<uint8_t>(hi >> 8);
           pb[swizzled(NR + r0 + r, key)] = static_cast<uint8_t>(lo);

@@ -503,10 +503,10 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 
 // One query row (a warp; lane l holds dims 8l .. 8l+7 as bf16) as two e4m3
-// parts: x * 2^-e = hi + lo / kQLo, with the row's largest element in (224,
+// parts: x * 2^-e = hi + lo / QLO, with the row's largest element in (224,
 // 448].  A bf16 has 8 significant bits and an e4m3 code 4, so the two parts
-// hold it exactly but for elements 2^14 below the row's largest (kQLo 16).
-// Returns 2^e; a row with a NaN or an infinity becomes all NaN.
+// hold it exactly but for elements 2^14 (QLO 16) or 2^10 (QLO 1) below the row's
+// largest.  Returns 2^e; a row with a NaN or an infinity becomes all NaN.
 template <int QLO>  // 1 or 16
 __device__ __forceinline__ float split_query(uint4 raw, uint2& hi, uint2& lo) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};

@@ -9,16 +9,21 @@
 // in HBM.  Each product runs twice (high and low part) at e4m3's rate, twice
 // bf16's, so the bound is bf16's rate; no code is ever converted.
 //
-// Rounding.  The second product is block-scaled: with e the largest score of a
-// row's 32 keys, rounded up, their weights are 2^(s - e + 8), and 2^(e + ev - ref - 8)
-// is their scale.  A weight, as fp16 at first (2^-11 of it), leaves at most 2^-8
+// Rounding.  The second product is block-scaled: with 2^(a + ev - ref) the largest
+// weight of a row's 32 keys, and e that exponent rounded up, they are held as
+// 2^(s + ev - ref - e + 8) under the scale 2^(e - 8).  A weight, as fp16 at first (2^-11 of it), leaves at most 2^-8
 // of it behind its two parts, and half a step of the least codes, 2^-10, where it
 // lies below their range: 2^-17 of the largest weight among its 32 keys, whatever
 // the row's other keys weigh.  (One reference for a row's whole tile, its running
 // maximum at 2^5, left a floor of 2^-15 of the row's largest weight: next to one
 // key with half of it, 32768 others were off by 12% in norm, 131072 by 32%.)
 // The scales also carry what a row's reference does not: that one only keeps the
-// sums in fp32's range, and moves when the scores pass it by 2^kAhead.
+// sums in fp32's range, and moves when the weights pass it by 2^kAhead.  It is the
+// row's maximum as it was then, not rounded, so that this key's weight is exact.
+// In norm, on random rows with outliers, the weights leave 0.0006 to 0.0007 of the
+// result (bfloat16 weights 0.0016); with references that move at 2^6, so that the
+// heaviest key is exact more often, 0.0005, but 5 to 8% slower where units are
+// short; with sums of the weights as they are held, 0.0004, but 4% slower.
 #include <cuda_runtime.h>
 
 #include "iq_paged_mma.cuh"
@@ -38,6 +43,7 @@ constexpr int kThreads = 384;
 constexpr int kLoader = 8, kIssuer = 9, kAsker = 10;
 constexpr int kRowRegs = 208, kRestRegs = 88;     // 2 * 208 + 88 = 3 * 168, what the CTA is launched with
 constexpr float kPlace = 8.0f;                    // the place of a block's largest weight (2^8.8 = 448 is the largest code)
+constexpr float kFar = 16384.0f;
 constexpr int kWeightScales = 32, kOnes = 96;     // their columns among a tile's 128, where its scores were
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
@@ -92,10 +98,10 @@ __global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ 
 // Bound by the row threads' chain (scores out of tensor memory, maximum, vote,
 // exponentials, two parts, back), 2.6 K cycles a tile, next to the products' 2.1 K
 // (measured alone, of 2.05 K at the nominal rate).  2048 queries of 16 / 2 heads
-// over 32768 keys: 741 us, 1440 TFLOP/s, 75% of a measured bf16 matrix product
+// over 32768 keys: 736 us, 1450 TFLOP/s, 76% of a measured bf16 matrix product
 // (710 with weights that are not block-scaled, whose second product reads no
 // scales); a unit's beginning and end cost 4 to 5 tiles' time, which shows where
-// units are short: 4 x 1531 tokens 114 us, 8191 under a window of 1023 177 us
+// units are short: 4 x 1531 tokens 116 us, 8191 under a window of 1023 182 us
 // (118 and 188 without: references had to follow the maxima).  What counted
 // on the way: the queries cut beforehand (260 to 214 us on the last), products
 // issued by a whole warp (745 to 673 us on the first), the references' rescaling
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
       // a row that has seen no key yet has no reference (its weights are all 0)
       bool unset = exists;
-      float ref = exists ? 0.0f : kDead, l = 0.0f;
+      float ref = exists ? 0.0f : 0.5f * kFar, l = 0.0f;  // (rows that do not exist weigh next to nothing)
 
       const float fq = next_factor;
       if (n > 0 && at < last) {
@@ -285,18 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           }
           m0 = __fmul_rn(fmaxf(m0, s[31]), f);
           m1 = __fmul_rn(fmaxf(m1, s[63]), f);
-          const float e0 = fmaxf(ceilf(m0), kUnset), e1 = fmaxf(ceilf(m1), kUnset);  // kUnset: no key is seen
-          float shift0 = kPlace - e0, shift1 = kPlace - e1;
-          if (fmaxf(e0 > kUnset ? fabsf(e0) : 0.0f, e1 > kUnset ? fabsf(e1) : 0.0f) >= 4194304.0f) {
-            // scores whose own rounding counts: the same one for the maximum and
-            // for every key, so that no weight passes 2^kPlace
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = __fsub_rn(__fmul_rn(s[i], f), i < 32 ? e0 : e1);
-            f = 1.0f;
-            shift0 = shift1 = kPlace;
-          }
-          __syncwarp();
-          float top = fmaxf(e0, e1) + ev;
+          float top = fmaxf(m0, m1) + ev;
           int far = top - ref > kAhead || (unset && top > kUnset);
           asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
                        : "+r"(far)
@@ -318,7 +313,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
             l *= change;
           }
           // the blocks' scales, 2^(above - kPlace), down to the least that a byte holds
-          const float above0 = (e0 + ev) - ref, above1 = (e1 + ev) - ref;
+          const float real0 = m0 + ev - ref, real1 = m1 + ev - ref;
+          const float above0 = fmaxf(ceilf(real0), kUnset), above1 = fmaxf(ceilf(real1), kUnset);  // (kUnset: no key is seen)
+          float shift0 = kPlace - above0 + (ev - ref), shift1 = kPlace - above1 + (ev - ref);
+          if (fmaxf(fmaxf(m0 > kNothing ? fabsf(m0) : 0.0f, m1 > kNothing ? fabsf(m1) : 0.0f), fabsf(ref)) >= kFar) {
+            // sums with scores this large are off by 2^-9 and more: differences from
+            // the block's maximum first, which are exact near it
+            m0 = fmaxf(m0, kUnset);
+            m1 = fmaxf(m1, kUnset);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i] = __fsub_rn(__fmul_rn(s[i], f), i < 32 ? m0 : m1);
+            f = 1.0f;
+            shift0 = kPlace + (real0 - above0);
+            shift1 = kPlace + (real1 - above1);
+          }
+          __syncwarp();
           const int least = 127 - static_cast<int>(kPlace);
           const int scale0 = static_cast<int>(fminf(fmaxf(above0, static_cast<float>(-least)), kAhead)) + least;
           const int scale1 = static_cast<int>(fminf(fmaxf(above1, static_cast<float>(-least)), kAhead)) + least;

@@ -498,6 +498,25 @@ def test_small_weights_beside_a_heavy_key(n, N, spread):
     assert off <= 2.0**-8 + 2.0**-9 + 2.0**-11 + 2.0**-13 + 2 * (2.0**-17 + 2.0**-16) * slack.max(), off
 
 
+@pytest.mark.parametrize("n", [1, 4, 8, 24])
+def test_a_key_that_dominates_gives_its_values(n):
+    """The last of 3001 keys weighs 1 - 2^-10.  Its weight enters numerator and sum as it is held, so its rounding
+    cancels: what is left is 2^-8 of the others' share, twice, and the fp32 score's error times that share."""
+    c, o = pair(1, 1, 60)
+    g = torch.Generator().manual_seed(11)
+    u = torch.randn(256, generator=g).sign() * 0.25
+    k = torch.randn(1, 1, 3001, 1, generator=g) * 0.01 * u
+    k[0, 0, 3000] = 7.3 * u
+    put(c, o, k.bfloat16(), rows(2, 1, 1, 3001))
+    q = u.expand(1, 2, n, 256).bfloat16()
+    scale = np.log(3000 * 2.0**10) / (7.3 * 16)
+    out, weight, _, slack = paged.attend(o, f64(q), scale, causal=False)
+    got = f64(c.attend(q.cuda(), scale=scale, causal=False, out_dtype=torch.float32))
+    largest = np.abs(o.values(0)[1]).max()
+    share = 2.0**-9  # of the others, and their effect on the sum
+    assert (np.abs(got - out) <= share * (2 * 2.0**-8 + 2.0**-13 + 2 * (2.0**-17 + 2.0**-16) * slack) * largest + 2.0**-22 * np.abs(out)).all()
+
+
 def test_append_attend_is_both_calls():
     for lens, n, nq in [([100, 0, 64, 63], 1, 1), ([500, 3, 1, 0], 4, 4), ([130, 700, 0, 64], 150, 150), ([70, 5, 9, 200], 3, 1)]:
         a, o = pair(5, 2, 60)
