@@ -1,6 +1,6 @@
 // libiqkv: attention over the paged 8-bit cache.
 //
-// Two kernels.  Calls with at most 64 query rows per kv head (decode, verify)
+// Two kernels.  Calls with at most 32 query rows per kv head (decode, verify)
 // run paged_split_kernel, below: the keys are the matrix products' M dimension,
 // the codes go from HBM through shared memory into tcgen05.mma untouched, and
 // the keys of all (slot, kv head) pairs are split evenly over the GPU.  More
@@ -46,7 +46,7 @@ struct SplitShape {
   static constexpr int kGroups = NR >= 32 ? 2 : 1;    // warpgroups on the softmax, NR / kGroups rows each
   static constexpr int kRows = NR / kGroups;
   static constexpr int kCols = 2 * NR;                // high and low parts
-  static constexpr int kSlots = NR == 64 ? 5 : 6;     // tiles of keys or values in flight
+  static constexpr int kSlots = 6;                    // tiles of keys or values in flight
   static constexpr int kQ = kSlots * kSlotBytes;      // [2 halves of the dims][kCols rows][128 bytes]
   static constexpr int kP = kQ + 2 * kCols * 128;     // [2][kCols rows][128 keys]
   static constexpr int kScales = kP + 2 * kCols * 128;  // [2] the weights'
@@ -66,9 +66,9 @@ struct SplitShape {
 // Why keys as M: M is 128 whatever it holds, so 8 query rows as M would leave 15
 // of 16 lanes idle; as N they fill 16 columns (two parts each), a product takes
 // its least time (65 cycles) and a tile's 16 products a third of the time that
-// its 64 KB take from HBM.  Five or six tiles of keys or values in flight (192 KB
-// per SM) cover HBM's latency.  Up to 64 rows: at 32 the row work is still
-// shorter than the stream, beyond 64 the columns of tensor memory end.
+// its 64 KB take from HBM.  Six tiles of keys or values in flight (192 KB per SM)
+// cover HBM's latency.  Up to 32 rows, where the row work is still shorter than the
+// stream (see kMaxSplitRows).
 // Bound by HBM.  32 slots x 32768 tokens, 16 / 2 heads, one query: 168 us, 1.07 GB
 // at 6.4 TB/s (94% of a measured copy), DRAM traffic within 0.1% of the keys and
 // values.  8 x 131072 tokens, four queries: 175 us.  One slot of 4096 tokens: 10.7
@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(SplitShape<NR>::kThreads, 1) paged_split_kerne
         await(&s_full[b], it / 2);
         tc_after();
         float s[RT], w[RT];
-        tmem_ld<RT < 32 ? RT : 32>(tmem + lanes + b * C::kCols + r0, s);
-        tmem_ld<RT < 32 ? RT : 32>(tmem + lanes + b * C::kCols + NR + r0, w);
+        tmem_ld<RT>(tmem + lanes + b * C::kCols + r0, s);
+        tmem_ld<RT>(tmem + lanes + b * C::kCols + NR + r0, w);
         ld_wait();
         tc_before();
         __syncwarp();
@@ -507,8 +507,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-constexpr int kMaxSplitRows = 64;
-int unit_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kMaxSplitRows ? 64 : 128; }
+// Up to 32 query rows per kv head the split kernel, beyond the prefill kernel.
+// Measured over 8 x 131072 tokens (and 4 x 16384, 1 x 4096 with 8 kv heads): 32 rows
+// 173.5 us split (28.3, 20.3); 33 rows 194.6 prefill (29.4, 21.0); a split kernel of
+// 64 rows, which spills and stores its weights byte by byte, took 255.5 us at 33
+// rows (37.7, 24.7) and 265.6 at 64 (45.9, 33.0), the prefill kernel 197.0 (31.2, 22.7).
+constexpr int kMaxSplitRows = 32;
+int unit_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kMaxSplitRows ? 32 : 128; }
 
 // The tiles of one head of an entry whose units hold `each` rows, and how many units those are.
 long long tiles_of_entry(int len, int count, int rep, int each, int causal, int window, int sinks, int* units) {
@@ -738,7 +743,6 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   cudaError_t err = p.unit_rows == 8    ? launch_split<8>(p, grid, cs)
                     : p.unit_rows == 16 ? launch_split<16>(p, grid, cs)
                     : p.unit_rows == 32 ? launch_split<32>(p, grid, cs)
-                    : p.unit_rows == 64 ? launch_split<64>(p, grid, cs)
                                         : launch_prefill(p, all_counts, grid, cs);
   if (err == cudaSuccess && grid > 1) {
     const int each = p.unit_rows == 128 ? 8 : 1, most = std::min(p.unit_rows, rows);

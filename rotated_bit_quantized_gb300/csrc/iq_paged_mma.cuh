@@ -299,12 +299,11 @@ __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.
 // segments ahead, scales half of that.
 template <int SLOTS, bool ACROSS>
 struct Loader {
-  // a tile's scales live until its weights are written: K(j + 4) takes, of 5 slots, that of V(j), free
-  // once tile j is through, and, of 4, that of K(j + 2), free once its scores are done, which the prefill
-  // kernel issues behind tile j's last product; K(j + 8) takes, of 6 slots, that of K(j + 5), whose scores
-  // wait for the weights of tile j + 3
-  static constexpr int kRing = SLOTS <= 5 ? 4 : 8;
-  static_assert(SLOTS == 4 || SLOTS == 5 || SLOTS == 6, "the ring's length is reasoned above");
+  // a tile's scales live until its weights are written: K(j + 4) takes, of 4 slots, that of K(j + 2), free
+  // once its scores are done, which the prefill kernel issues behind tile j's last product; K(j + 8) takes,
+  // of 6 slots, that of K(j + 5), whose scores wait for the weights of tile j + 3
+  static constexpr int kRing = SLOTS == 4 ? 4 : 8;
+  static_assert(SLOTS == 4 || SLOTS == 6, "the ring's length is reasoned above");
 
   struct Segment {
     const int* row;
