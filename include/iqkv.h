@@ -310,7 +310,8 @@ int iq_attend_mask(const iq_cache* cache, const void* q, int q_heads, int n_quer
  * grows by n on success (the causal mask and the scanned length use the
  * grown lengths).  Errors: as both (nothing is launched on an error).
  * Overlap: an attention grid starts streaming cache tiles while the previous
- * call's grids finish (only its stores wait for them).  The library remembers,
+ * call's grids finish (only its stores wait for them, and its reads of what the
+ * last call on the stream hands out).  The library remembers,
  * per key-code buffer, the rows the latest attention on it reads; when a trim
  * since then puts the new rows below that mark, the fused encode also waits.
  * Writing the cache by other means (outside this library's calls) while a call
@@ -561,6 +562,9 @@ int iq_paged_attend_workspace(const iq_paged* cache, int q_heads, int n_queries,
  *   (out_f32); softmax(scale * q.k) . v, rounded once; 0 for a query that sees
  *   no key (an empty slot, a position before the first token).  It must not
  *   overlap q, which some CTAs still read when others store.
+ *   For either output type every softmax weight is held to 2^-8 of it (two e4m3
+ *   parts; sums in float32), however small it is next to the row's others: as in
+ *   an attention whose weights are bfloat16.
  * workspace: at least iq_paged_attend_workspace() bytes, 256-byte aligned; it
  *   needs no initialisation and holds nothing between calls.  Calls that may
  *   run at the same time need one each.
@@ -573,7 +577,8 @@ int iq_paged_attend(const iq_paged* cache, const void* q, int q_heads, int n_que
 
 /*
  * iq_paged_append_attend — iq_paged_append, then iq_paged_attend of the same
- * entries, with every argument of both checked before anything is done.
+ * entries, with every argument of both checked before anything is done.  Where a
+ * launch of the attention fails (CUDA), the append stands.
  * counts, where given, holds for the rows and for the queries, and n must be
  * n_queries.  slots must be distinct.
  */

@@ -69,9 +69,9 @@ struct SplitShape {
 // its 64 KB take from HBM.  Six tiles of keys or values in flight (192 KB per SM)
 // cover HBM's latency.  Up to 32 rows, where the row work is still shorter than the
 // stream (see kMaxSplitRows).
-// Bound by HBM.  32 slots x 32768 tokens, 16 / 2 heads, one query: 168 us, 1.07 GB
-// at 6.4 TB/s (94% of a measured copy), DRAM traffic within 0.1% of the keys and
-// values.  8 x 131072 tokens, four queries: 175 us.  One slot of 4096 tokens: 10.7
+// Bound by HBM.  32 slots x 32768 tokens, 16 / 2 heads, one query: 170 us, 1.07 GB
+// at 6.3 TB/s (93% of a measured copy), DRAM traffic within 0.1% of the keys and
+// values.  8 x 131072 tokens, four queries: 175 us.  One slot of 4096 tokens: 10.9
 // us with the join, a launch's and a pipeline's latency.  The weights' block scales
 // cost 1 us of the first.  A thread's own loads of
 // its page's scale, one tile ahead, cost 5%: under a full HBM they take longer

@@ -248,7 +248,7 @@ struct CompactParams {
 
 // Blocks [0, pages * 2 * heads): 16 KB each, a page of one kv head, keys or
 // values, and its scale.  The blocks behind them: a run of table entries each.
-// Bound by HBM: 7640 pages of two kv heads in 73 us, 501 MB at 6.8 TB/s.
+// Bound by HBM: 3818 pages of two kv heads in 73 us, 501 MB at 6.8 TB/s.
 __global__ void __launch_bounds__(256) paged_compact_kernel(const __grid_constant__ CompactParams p) {
   wait_for_last_kernel();
   const long long copies = static_cast<long long>(p.pages) * 2 * p.heads;

@@ -301,6 +301,7 @@ class IQPagedCache:
         rows of `out` are left as they were).  `out` must not overlap q.  causal: a query sees the keys
         up to its own position; `window` > 0: only the last `window` of them, and
         the slot's first `sinks` tokens.  A query that sees nothing gets 0.
+        Softmax weights are held to 2^-8 of each, sums in float32, whatever out_dtype is.
         """
         q = self._tensor(q, "q")
         E, Hq, L, D = q.shape
