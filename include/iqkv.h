@@ -544,6 +544,14 @@ int iq_paged_compact(const iq_paged* src, iq_paged* dst, iq_stream_t stream);
  */
 int iq_paged_debug_fail(int launch);
 
+/*
+ * iq_paged_debug_stall — another: the next iq_paged_attend of this host thread
+ * loads no pages, so its kernel's waits for them run out after a second.  The
+ * kernels return normally, with some of the bits 1, 2 and 8 in the status word
+ * and nothing meaningful in the call's output.
+ */
+int iq_paged_debug_stall(void);
+
 /* iq_paged_attend_workspace — device scratch bytes iq_paged_attend needs for these shapes, whatever the lengths. */
 int iq_paged_attend_workspace(const iq_paged* cache, int q_heads, int n_queries, int n_slots, size_t* bytes);
 

@@ -35,7 +35,7 @@ EXPORTS = ("iq_status_string", "iq_last_error", "iq_build_rotation", "iq_cache_b
            "iq_debug_inject", "iq_cache_alloc", "iq_cache_grow", "iq_paged_bytes", "iq_paged_alloc",
            "iq_paged_check", "iq_paged_append", "iq_paged_read", "iq_paged_trim", "iq_paged_free",
            "iq_paged_fork", "iq_paged_compact", "iq_paged_attend_workspace", "iq_paged_attend",
-           "iq_paged_append_attend", "iq_paged_debug_fail")
+           "iq_paged_append_attend", "iq_paged_debug_fail", "iq_paged_debug_stall")
 
 
 class IQCacheDesc(ctypes.Structure):
@@ -114,6 +114,7 @@ def lib() -> ctypes.CDLL:
         L.iq_paged_attend.argtypes = [PAGED, P, I, I, P, P, I, F, I, I, I, P, I, P, S, P]
         L.iq_paged_append_attend.argtypes = [PAGED, P, P, I, P, I, I, P, P, I, F, I, I, I, P, I, P, S, P]
         L.iq_paged_debug_fail.argtypes = [I]
+        L.iq_paged_debug_stall.argtypes = []
         for name in EXPORTS:
             if name not in ("iq_status_string", "iq_last_error", "iq_cache_nbytes"):
                 getattr(L, name).restype = I

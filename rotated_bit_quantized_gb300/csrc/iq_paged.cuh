@@ -29,6 +29,7 @@ int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, c
 // pointer per parameter.
 cudaError_t launch_after(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args);
 extern thread_local int launch_to_fail;  // test hook (iq_paged_debug_fail): how many launches from now, < 0: none
+extern thread_local bool stall_next;     // test hook (iq_paged_debug_stall)
 __device__ __forceinline__ void wait_for_last_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

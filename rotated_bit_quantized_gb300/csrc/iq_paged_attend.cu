@@ -544,6 +544,7 @@ cudaError_t launch_split(const AttendParams& p, int grid, cudaStream_t stream) {
 }  // namespace
 
 thread_local int launch_to_fail = -1;
+thread_local bool stall_next = false;
 
 cudaError_t launch_after(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args) {
   if (launch_to_fail >= 0 && launch_to_fail-- == 0) return cudaErrorLaunchFailure;
@@ -728,6 +729,8 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   p.window = window;
   p.sinks = sinks;
   p.scale = scale;
+  p.stall = stall_next ? 1 : 0;
+  stall_next = false;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * num_sms() * p.unit_rows * kHeadDim);
   p.cuts = reinterpret_cast<Cut*>(p.part_ml + 2ll * num_sms() * p.unit_rows);

@@ -52,6 +52,7 @@ struct AttendParams {
   float* factors;   // prefill: [entry][kv head][row] 2^e * scale * log2 e
   int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, cost, total, slots_n;
   unsigned rep_mul, rep_shift;  // division by rep, see query_of
+  int stall;                    // test hook (iq_paged_debug_stall): no page is loaded, so the waits for them run out
   float scale;
   // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
   // its queries; cum: slots before it (all heads), per: slots of one of its heads
@@ -342,6 +343,7 @@ struct Loader {
   }
 
   __device__ __forceinline__ void run(Place w, int first, int last, uint64_t policy) const {
+    if (p.stall) return;
     const int lane = threadIdx.x & 31;
     int issued = 0, it = 0, v0 = 0, v1 = 0, v_head = -1;  // (the tile whose values come next)
     bool ok = true;

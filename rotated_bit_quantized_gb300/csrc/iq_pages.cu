@@ -449,6 +449,12 @@ int iq_paged_debug_fail(int launch) {
   return IQ_OK;
 }
 
+int iq_paged_debug_stall(void) {
+  clear_error();
+  stall_next = true;
+  return IQ_OK;
+}
+
 int iq_paged_bytes(int slots, int kv_heads, int head_dim, int pages, int max_pages, size_t out_bytes[6]) {
   clear_error();
   if (!out_bytes) return fail(IQ_ERR_INVALID_ARG, "null out_bytes");

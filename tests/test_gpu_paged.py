@@ -668,6 +668,22 @@ def test_a_bad_page_id_sets_a_status_bit(n):
     check_attend(c, o, rows(3, 1, 8, n))
 
 
+@pytest.mark.parametrize("Hq,n", [(4, 1), (16, 1), (16, 4), (16, 140)])
+def test_waits_that_run_out_are_told(Hq, n):
+    """No page is loaded, through a hook on the host: every wait for one ends after a second, the call returns, the
+    status word tells, and the calls behind it are right."""
+    c, o = pair(3, 2, 60)
+    put(c, o, rows(1, 3, 2, 900), rows(2, 3, 2, 900), None, [900, 1, 129])
+    q = rows(3, 3, Hq, n)
+    check_attend(c, o, q)
+    c._lib.iq_paged_debug_stall()
+    c.attend(q.cuda())
+    status = c.device_status()  # (of the roles that wait, each tells or sees that another one has given up)
+    assert status & 0xB and not status & ~0xB
+    check_attend(c, o, q)
+    same(c, o)
+
+
 def test_python_refusals():
     c, _ = pair(2, 2, 4)
     k, q = rows(1, 2, 2, 3).cuda(), rows(2, 2, 4, 3).cuda()
