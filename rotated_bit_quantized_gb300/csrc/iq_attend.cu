@@ -44,7 +44,9 @@
 #include <algorithm>
 #include <array>
 #include <cstring>
+#include <map>
 #include <mutex>
+#include <tuple>
 #include <type_traits>
 #include <unordered_map>
 #include <vector>
@@ -1837,9 +1839,32 @@ ReadMarks& read_marks() {
 }
 
 // What the last call on a stream hands out, and who asks for it; see launched_outputs.
+// A stream is told by its device and handle; the default stream of a thread by the
+// thread too.  What is captured has a record per capture: it does not run in between.
 class LastOutputs {
  public:
-  void record(const void* stream, const Range& a, const Range& b) {
+  struct Key {
+    int device = 0;
+    uintptr_t stream = 0, thread = 0;
+    unsigned long long capture = 0;
+    explicit Key(iq_stream_t s) {
+      const cudaStream_t cs = static_cast<cudaStream_t>(s);
+      cudaGetDevice(&device);
+      stream = cs == cudaStreamLegacy ? 0 : reinterpret_cast<uintptr_t>(cs);
+      static thread_local char here;
+      if (cs == cudaStreamPerThread) thread = reinterpret_cast<uintptr_t>(&here);
+      cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+      if (cudaStreamGetCaptureInfo(cs, &st, &capture) != cudaSuccess) {
+        cudaGetLastError();
+        st = cudaStreamCaptureStatusNone;
+      }
+      if (st != cudaStreamCaptureStatusActive) capture = 0;
+    }
+    bool operator<(const Key& o) const {
+      return std::tie(device, stream, thread, capture) < std::tie(o.device, o.stream, o.thread, o.capture);
+    }
+  };
+  void record(const Key& stream, const Range& a, const Range& b) {
     std::lock_guard<std::mutex> lk(mu_);
     if (last_.size() >= 256 && !last_.count(stream)) {
       last_.clear();  // bounded: from here on a stream without a record counts as unknown
@@ -1851,7 +1876,7 @@ class LastOutputs {
       lost_ = true;
     }
   }
-  bool overlaps(const void* stream, const Range& x) {
+  bool overlaps(const Key& stream, const Range& x) {
     if (!x.at || !x.bytes) return false;
     std::lock_guard<std::mutex> lk(mu_);
     auto it = last_.find(stream);
@@ -1867,7 +1892,7 @@ class LastOutputs {
  private:
   std::mutex mu_;
   bool lost_ = false;
-  std::unordered_map<const void*, std::array<Range, 2>> last_;
+  std::map<Key, std::array<Range, 2>> last_;
 };
 LastOutputs& last_outputs() {
   static LastOutputs o;
@@ -1987,8 +2012,10 @@ int attend_impl(const iq_cache* c, const void* q_in, int q_heads, int n_queries,
   const size_t q_bytes = static_cast<size_t>(c->batch) * q_heads * n_queries * kHeadDim * 2;
   const size_t new_bytes = static_cast<size_t>(c->batch) * c->kv_heads * n_new * kHeadDim * 2;
   const size_t mask_bytes = static_cast<size_t>(c->batch) * n_queries * mask_stride * (mask_kind == IQ_MASK_ADD_F32 ? 4 : 1);
-  prm.input_wait = launched_outputs_overlap(stream, {q, q_bytes}) || launched_outputs_overlap(stream, {k_new, new_bytes}) ||
-                   launched_outputs_overlap(stream, {v_new, new_bytes}) || launched_outputs_overlap(stream, {mask, mask_bytes});
+  prm.input_wait = 0;
+  const LastOutputs::Key on(stream);
+  for (const Range& x : {Range{q, q_bytes}, Range{k_new, new_bytes}, Range{v_new, new_bytes}, Range{mask, mask_bytes}})
+    if (last_outputs().overlaps(on, x)) prm.input_wait = 1;
   prm.spin_limit = t_inject.spin_limit ? t_inject.spin_limit : kSpinLimit;
   prm.combine_wait_ns = t_inject.wait_ns;
   prm.inject = t_inject.flags;
@@ -2034,8 +2061,9 @@ int attend_impl(const iq_cache* c, const void* q_in, int q_heads, int n_queries,
 
 }  // namespace attn
 
-void launched_outputs(iq_stream_t stream, Range a, Range b) { attn::last_outputs().record(stream, a, b); }
-bool launched_outputs_overlap(iq_stream_t stream, Range x) { return attn::last_outputs().overlaps(stream, x); }
+void launched_outputs(iq_stream_t stream, Range a, Range b) {
+  attn::last_outputs().record(attn::LastOutputs::Key(stream), a, b);
+}
 
 }  // namespace iq
 

@@ -30,14 +30,14 @@ int num_sms();  // multiprocessor count of the current device (cached per device
 // may start while the last call on a stream still writes what it hands out (and
 // only that call: each of its kernels, or the one behind it, has waited for the
 // calls before).  A call whose last kernels may leave such outputs unfinished
-// tells where they are; a kernel that reads its inputs before it waits asks
-// whether they are among them.  Work of others in between has completed by then.
+// tells where they are; the split-KV attention, whose kernel reads its inputs before
+// it waits, looks whether they are among them.  Work of others in between has
+// completed by then.
 struct Range {
   const void* at;
   size_t bytes;
 };
 void launched_outputs(iq_stream_t stream, Range a, Range b = {nullptr, 0});
-bool launched_outputs_overlap(iq_stream_t stream, Range x);  // (true where the record was lost)
 
 // Cache formats (iq_generic.cu): the tuned one (k 4 bits, v 3 bits, 64-dim
 // groups, bfloat16) runs the tuned kernels, every other supported one (any

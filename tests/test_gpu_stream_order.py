@@ -124,3 +124,25 @@ def test_an_appended_chunk_is_attended_at_once(slots, H):
         c.trim(1025)
         return a, b, d
     both_ways(chain)
+
+
+def test_a_capture_in_between_does_not_count():
+    """Calls captured between a call and the one that takes its result do not run there."""
+    p = paged(4, 2, 9000, 1)
+    c, rot = rotated(4, 2, 2000, 3)
+    q, other = rows(5, 4, 16, 1), rows(6, 4, 16, 1)
+    stream = torch.cuda.Stream()
+    graphs = []
+
+    def chain(wait):
+        with torch.cuda.stream(stream):
+            a = p.attend(q)
+            wait()
+            g = torch.cuda.CUDAGraph()
+            g.capture_begin()
+            p.attend(other)
+            g.capture_end()
+            graphs.append(g)
+            return a, c.attend(a, rot)
+    torch.cuda.synchronize()
+    both_ways(chain, times=5)
