@@ -9,12 +9,12 @@
 // in HBM.  Each product runs twice (high and low part) at e4m3's rate, twice
 // bf16's, so the bound is bf16's rate; no code is ever converted.
 //
-// Rounding.  The second product is block-scaled: with 2^(a + ev - ref) the largest
-// weight of a row's 32 keys, and e that exponent rounded up, they are held as
-// 2^(s + ev - ref - e + 8) under the scale 2^(e - 8).  A weight, as fp16 at first (2^-11 of it), leaves at most 2^-8
-// of it behind its two parts, and half a step of the least codes, 2^-10, where it
-// lies below their range: 2^-17 of the largest weight among its 32 keys, whatever
-// the row's other keys weigh.  (One reference for a row's whole tile, its running
+// Rounding.  The second product is block-scaled: with e the exponent s + ev - ref of
+// the largest weight of a row's 32 keys, rounded up, they are held as 2^(s + ev - ref
+// - e + 8) under the scale 2^(e - 8).  A weight, as fp16 at first (2^-11 of it), leaves
+// at most 2^-8 of it behind its two parts, and half a step of the least codes, 2^-10,
+// where it lies below their range: 2^-17 of the largest weight among its 32 keys,
+// whatever the row's other keys weigh.  (One reference for a row's whole tile, its running
 // maximum at 2^5, left a floor of 2^-15 of the row's largest weight: next to one
 // key with half of it, 32768 others were off by 12% in norm, 131072 by 32%.)
 // The scales also carry what a row's reference does not: that one only keeps the
@@ -43,7 +43,7 @@ constexpr int kThreads = 384;
 constexpr int kLoader = 8, kIssuer = 9, kAsker = 10;
 constexpr int kRowRegs = 208, kRestRegs = 88;     // 2 * 208 + 88 = 3 * 168, what the CTA is launched with
 constexpr float kPlace = 8.0f;                    // the place of a block's largest weight (2^8.8 = 448 is the largest code)
-constexpr float kFar = 16384.0f;
+constexpr float kFar = 16384.0f;                  // scores from here on take differences first
 constexpr int kWeightScales = 32, kOnes = 96;     // their columns among a tile's 128, where its scores were
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
