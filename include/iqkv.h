@@ -595,6 +595,84 @@ int iq_paged_append_attend(iq_paged* cache, const void* keys, const void* values
                            int n_slots, float scale, int causal, int window, int sinks, void* out,
                            int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions: what a model does to its queries and keys before either cache
+ * takes them.  Library services: the source pages have no counterpart (their
+ * callers hand over keys that are normed and turned already).
+ *
+ * For a vector x of a head at position t:  y = x * (mean(x^2) + eps)^-1/2 * weight
+ * where a weight is given, else y = x; then each of the rotary_dim / 2 pairs (a, b) of
+ * the leading rotary_dim elements becomes amplitude * (a cos - b sin, a sin + b cos) of
+ * the angle t * frequency.  In float32, rounded once to the output's type.  Angles are
+ * reduced in 64-bit fixed point: a position is any 32-bit integer, and however far it
+ * is, the angle is off by no more than the frequency itself times it (2^-53).
+ */
+typedef struct {
+  int32_t rotary_dim;     /* 0 (nothing turns) or a multiple of 16 up to 256 */
+  int32_t interleaved;    /* 1: pairs are elements (2i, 2i+1); 0: (i, i + rotary_dim/2) */
+  float amplitude, eps;   /* eps: 1e-30 or more, where a weight is given */
+  const uint64_t* turns;  /* device [rotary_dim/2], from iq_rotary_turns (NULL where rotary_dim is 0) */
+  const float* q_weight;  /* device float32 [256], 16-byte aligned; NULL: queries are not normed */
+  const float* k_weight;  /* the same for keys */
+} iq_rotary;
+
+/* Rows of 256 elements [entries][heads][n] anywhere: the first one's address and the
+ * strides, in elements, all rows 16-byte aligned (a view of a projection's output). */
+typedef struct {
+  const void* at;
+  int64_t entry, head, row;
+} iq_rows;
+
+#define IQ_SCALING_NONE 0   /* frequency i of n: base^(-i/n) */
+#define IQ_SCALING_LINEAR 1 /* divided by factor */
+#define IQ_SCALING_NTK 2    /* of a base that grows by factor^(rotary_dim/(rotary_dim-2)) */
+#define IQ_SCALING_YARN 3   /* YaRN: pairs that turn over `high` times within `original` positions stay, those under `low` are
+                             * divided by factor, a ramp over the pairs between; amplitude 0.1 ln factor + 1 */
+#define IQ_SCALING_BANDED 4 /* the same limits with a ramp over the turns, and amplitude 1 */
+
+/*
+ * iq_rotary_frequencies — the angles per position, in radians, of the rotary_dim / 2 pairs
+ * (host only).  factor >= 1 where scaling is not NONE; original >= 1 and 0 < low < high for
+ * YARN and BANDED.  frequencies: host double [rotary_dim/2] out; amplitude: host out.
+ * Errors: INVALID_ARG, UNSUPPORTED (rotary_dim).
+ */
+int iq_rotary_frequencies(int rotary_dim, double base, int scaling, double factor, double original, double low,
+                          double high, double* frequencies, double* amplitude);
+
+/*
+ * iq_rotary_turns — frequencies (host double [pairs], radians per position, any finite ones)
+ * as the kernels take them, into turns (device [pairs]).  The host array may be reused at
+ * once.  Errors: INVALID_ARG, CUDA.
+ */
+int iq_rotary_turns(const double* frequencies, int pairs, uint64_t* turns, iq_stream_t stream);
+
+/*
+ * iq_rotary_apply — queries and keys normed and turned.
+ * q, k: rows [entries][q_heads or k_heads][n] of dtype; q_out, k_out: the same, contiguous,
+ *   16-byte aligned, apart from the inputs and each other.  q_heads or k_heads may be 0.
+ * Row j of entry i is at position start[i] + j (start: host int32 [entries], NULL: zeros),
+ *   or at positions[i][j] (device int32 [entries][n]); not both.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_heads, const iq_rows* k, int k_heads,
+                    int entries, int n, const int32_t* start, const int32_t* positions, void* q_out, void* k_out,
+                    iq_stream_t stream);
+
+/*
+ * iq_paged_append_rotary — iq_paged_append of a projection's rows in one launch: queries and
+ * keys normed and turned at the positions where the rows come to stand in their slots (or at
+ * positions[i][j], device int32 [n_slots][n]), keys and values quantised into the pages.
+ * q, k, v: bf16 rows [n_slots][q_heads or kv_heads][n]; q_heads may be 0.
+ * q_out: device bf16 [n_slots][q_heads][n][256], apart from the inputs; rows behind counts[i]
+ *   are not read, and left as they were.
+ * Codes are rounded once, from the turned keys in float32: iq_rotary_apply and then
+ * iq_paged_append round twice, to bfloat16 in between.
+ * Everything else as iq_paged_append.
+ */
+int iq_paged_append_rotary(iq_paged* cache, const iq_rotary* rotary, const iq_rows* q, int q_heads, const iq_rows* k,
+                           const iq_rows* v, int n, const int32_t* slots, const int32_t* counts, int n_slots,
+                           const int32_t* positions, void* q_out, iq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

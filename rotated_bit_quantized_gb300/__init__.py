@@ -7,4 +7,5 @@ the library has not been built.
 """
 from .cache import IQCache, Rotation, commit_verified_snapshot  # noqa: F401
 from .paged import IQPagedCache  # noqa: F401
+from .rotary import IQRotary, rotary_frequencies  # noqa: F401
 from ._abi import IQError, LIB_PATH  # noqa: F401

@@ -27,6 +27,7 @@ IQ_DTYPE_BF16, IQ_DTYPE_F32 = 0, 1
 IQ_PAGE = 64
 IQ_WORKSPACE_HEAD_BYTES = 8448
 IQ_STATUS_RANGE, IQ_STATUS_BAD_PAGE = 0x40000, 0x80000
+IQ_SCALING_NONE, IQ_SCALING_LINEAR, IQ_SCALING_NTK, IQ_SCALING_YARN, IQ_SCALING_BANDED = range(5)
 
 EXPORTS = ("iq_status_string", "iq_last_error", "iq_build_rotation", "iq_cache_bytes",
            "iq_cache_check", "iq_cache_nbytes", "iq_cache_append", "iq_cache_trim",
@@ -35,7 +36,8 @@ EXPORTS = ("iq_status_string", "iq_last_error", "iq_build_rotation", "iq_cache_b
            "iq_debug_inject", "iq_cache_alloc", "iq_cache_grow", "iq_paged_bytes", "iq_paged_alloc",
            "iq_paged_check", "iq_paged_append", "iq_paged_read", "iq_paged_trim", "iq_paged_free",
            "iq_paged_fork", "iq_paged_compact", "iq_paged_attend_workspace", "iq_paged_attend",
-           "iq_paged_append_attend", "iq_paged_debug_fail", "iq_paged_debug_stall")
+           "iq_paged_append_attend", "iq_paged_debug_fail", "iq_paged_debug_stall", "iq_rotary_frequencies",
+           "iq_rotary_turns", "iq_rotary_apply", "iq_paged_append_rotary")
 
 
 class IQCacheDesc(ctypes.Structure):
@@ -59,6 +61,16 @@ class IQPagedDesc(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("status", ctypes.c_void_p),
                 ("lens", ctypes.c_void_p), ("table_host", ctypes.c_void_p),
                 ("refs", ctypes.c_void_p)]
+
+
+class IQRotaryDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
+class IQRows(ctypes.Structure):
+    _fields_ = [("at", ctypes.c_void_p), ("entry", ctypes.c_int64), ("head", ctypes.c_int64), ("row", ctypes.c_int64)]
 
 
 class IQError(RuntimeError):
@@ -113,6 +125,11 @@ def lib() -> ctypes.CDLL:
         L.iq_paged_attend_workspace.argtypes = [PAGED, I, I, I, ctypes.POINTER(S)]
         L.iq_paged_attend.argtypes = [PAGED, P, I, I, P, P, I, F, I, I, I, P, I, P, S, P]
         L.iq_paged_append_attend.argtypes = [PAGED, P, P, I, P, I, I, P, P, I, F, I, I, I, P, I, P, S, P]
+        ROTARY, ROWS, D = ctypes.POINTER(IQRotaryDesc), ctypes.POINTER(IQRows), ctypes.c_double
+        L.iq_rotary_frequencies.argtypes = [I, D, I, D, D, D, D, P, ctypes.POINTER(D)]
+        L.iq_rotary_turns.argtypes = [P, I, P, P]
+        L.iq_rotary_apply.argtypes = [ROTARY, I, ROWS, I, ROWS, I, I, I, P, P, P, P, P]
+        L.iq_paged_append_rotary.argtypes = [PAGED, ROTARY, ROWS, I, ROWS, ROWS, I, P, P, I, P, P, P]
         L.iq_paged_debug_fail.argtypes = [I]
         L.iq_paged_debug_stall.argtypes = []
         for name in EXPORTS:

@@ -2,6 +2,8 @@
 // checks, e4m3 conversions and the page exponent.
 #pragma once
 
+#include <atomic>
+
 #include "iq_common.cuh"
 
 namespace iq {
@@ -28,6 +30,8 @@ int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, c
 // paged cache waits for that one itself, before it touches memory.  args: one
 // pointer per parameter.
 cudaError_t launch_after(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args);
+// Shared memory above 48 KB, allowed once per kernel and device (`seen`: the kernel's own).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& seen);
 extern thread_local int launch_to_fail;  // test hook (iq_paged_debug_fail): how many launches from now, < 0: none
 extern thread_local bool stall_next;     // test hook (iq_paged_debug_stall)
 __device__ __forceinline__ void wait_for_last_kernel() {

@@ -5,8 +5,6 @@
 
 #include <cuda.h>
 
-#include <atomic>
-
 #include "iq_paged.cuh"
 
 namespace iq {
@@ -173,9 +171,6 @@ __device__ __forceinline__ long long row_index(const AttendParams& p, const Plac
 
 // counts: of every entry of the call, also those without keys
 cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream);
-
-// Shared memory above 48 KB, allowed once per kernel and device (`seen`: the kernel's own).
-cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& seen);
 
 // Waits end: after a second (no stage takes a thousandth of it) the CTA's
 // abort flag is raised, every later wait of the CTA returns at once, and the

@@ -12,50 +12,12 @@
 #include <cstring>
 #include <new>
 
-#include "iq_paged.cuh"
+#include "iq_pages.cuh"
 
 namespace iq {
 namespace paged {
 
 // ------------------------------------------------------------------ append
-
-// One contiguous run of pages of one entry: `rows` rows of the call, from row
-// `row0`, go to positions pos .. pos + rows - 1 of the slot, which lie in pages
-// page, page + 1, ...; the rows that the first page already holds come from
-// page `from` (another one when the page was shared and is being copied).
-struct Segment {
-  int entry, slot, row0, rows, pos, page, from;
-};
-constexpr int kSegments = 256;  // per launch, by value
-
-struct AppendParams {
-  const uint16_t* keys;
-  const uint16_t* values;
-  uint8_t* k_codes;
-  uint8_t* v_codes;
-  float* k_scales;
-  float* v_scales;
-  int* table;
-  unsigned* status;
-  int heads, n, max_pages;
-  Segment seg[kSegments];
-};
-
-// NaN: 0; infinity: the largest value of its sign.
-__device__ __forceinline__ uint32_t drop_non_finite(uint32_t w) {
-#pragma unroll
-  for (int s = 0; s < 32; s += 16) {
-    const uint32_t h = (w >> s) & 0x7FFFu;
-    if (h >= 0x7F80u) w = (w & ~(0x7FFFu << s)) | ((h == 0x7F80u ? 0x7F7Fu : 0u) << s);
-  }
-  return w;
-}
-// The larger magnitude of both halves of eight bf16 values (they order as integers).
-__device__ __forceinline__ uint32_t magnitude(const uint4& x) {
-  const uint32_t m = 0x7FFF7FFFu;
-  const uint32_t t = __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
-  return max(t & 0xFFFFu, t >> 16);
-}
 
 // One CTA per (page of a segment, kv head, keys or values): 8 warps, a warp per
 // row, a lane per 8 dims, the page's new rows (32 KB at most) held in registers
@@ -110,11 +72,9 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, tops[i]);
 
-  // top = 1.m * 2^x:  448 * 2^e = 1.75 * 2^(8+e) is reached from e = x - 8 on, or x - 7 where 1.m is above 1.75
-  int e = kEMin;
-  if (top >= 0x80u) e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
+  int e = least_exponent(top << 16);
   odd |= e > kEMax;
-  e = min(max(e, kEMin), kEMax);
+  e = min(e, kEMax);
   const int old = begin > 0 ? exponent_of(scales[at_from]) : e;
   e = max(e, old);
   const float inv = power2(-e);
@@ -128,28 +88,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
     for (int j = 0; j < 4; ++j) c[j] = e4m3x2(bf16_to_f32(w[j] & 0xFFFFu) * inv, __uint_as_float(w[j] & 0xFFFF0000u) * inv);
     *reinterpret_cast<uint2*>(codes + r * kHeadDim) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
   }
-  // rows that were there: moved to this page, rescaled to the grown exponent
-  if (begin > 0 && (from != page || e > old)) {
-    const uint8_t* src = (is_v ? p.v_codes : p.k_codes) + at_from * kPageBytes + lane * 8;
-    const float f = power2(max(old - e, -126));
-    for (int r = warp; r < begin; r += 8) {
-      uint2 c = *reinterpret_cast<const uint2*>(src + r * kHeadDim);
-      if (e > old) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&c);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 lo = f16x2_to_f32(e4m3x2_to_f16x2(w[j] & 0xFFFFu)), hi = f16x2_to_f32(e4m3x2_to_f16x2(w[j] >> 16));
-          w[j] = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
-        }
-      }
-      *reinterpret_cast<uint2*>(codes + r * kHeadDim) = c;
-    }
-  }
-  // a page that is new to its slot: the rows behind are zero, so that whole
-  // pages can enter matrix products before they are full
-  if (begin == 0 || from != page)
-    for (int r = warp; r < kPage; r += 8)
-      if (r >= end) *reinterpret_cast<uint2*>(codes + r * kHeadDim) = make_uint2(0, 0);
+  upkeep((is_v ? p.v_codes : p.k_codes) + at_from * kPageBytes, codes - lane * 8, begin, end, from != page, old, e);
   if (odd) atomicOr(p.status, IQ_STATUS_RANGE);
   __syncthreads();  // the old scale has been read by every thread
   if (threadIdx.x == 0) {
@@ -314,7 +253,8 @@ void drop_from(iq_paged* c, int slot, int keep) {  // the slot's pages from inde
   for (int j = pages_for(c->lens[slot]) - 1; j >= keep; --j) drop_page(c, row[j]);
 }
 
-// What an append of the entries needs, checked without a change.
+}  // namespace
+
 int check_append(iq_paged* c, const void* keys, const void* values, int n, const int32_t* slots, const int32_t* counts,
                  int n_slots) {
   int st = iq_paged_check(c);
@@ -349,7 +289,7 @@ int check_append(iq_paged* c, const void* keys, const void* values, int n, const
 // and names that one) goes with the last launch; the launches before it write
 // pages that are still free to anyone who looks at the host's arrays.
 int do_append(iq_paged* c, const void* keys, const void* values, int n, const int32_t* slots, const int32_t* counts,
-              int n_slots, iq_stream_t stream) {
+              int n_slots, iq_stream_t stream, AppendLaunch enqueue, const void* more) {
   AppendParams p;
   p.keys = static_cast<const uint16_t*>(keys);
   p.values = static_cast<const uint16_t*>(values);
@@ -368,11 +308,7 @@ int do_append(iq_paged* c, const void* keys, const void* values, int n, const in
   int was[IQ_MAX_BATCH];  // the shared page that entry i's own copy replaced
   cudaError_t err = cudaSuccess;
   auto launch = [&]() {
-    if (segs && err == cudaSuccess) {
-      void* args[] = {&p};
-      err = launch_after(reinterpret_cast<const void*>(&paged_append_kernel), dim3(widest, 2 * c->kv_heads, segs), 256, 0,
-                         static_cast<cudaStream_t>(stream), args);
-    }
+    if (segs && err == cudaSuccess) err = enqueue(p, widest, segs, static_cast<cudaStream_t>(stream), more);
     segs = widest = 0;
   };
   auto add = [&](const Segment& sg) {
@@ -434,7 +370,11 @@ int do_append(iq_paged* c, const void* keys, const void* values, int n, const in
   return IQ_OK;
 }
 
-}  // namespace
+static cudaError_t launch_append(const AppendParams& p, int widest, int segs, cudaStream_t stream, const void*) {
+  void* args[] = {const_cast<AppendParams*>(&p)};
+  return launch_after(reinterpret_cast<const void*>(&paged_append_kernel), dim3(widest, 2 * p.heads, segs), 256, 0, stream, args);
+}
+
 }  // namespace paged
 }  // namespace iq
 
@@ -529,7 +469,7 @@ int iq_paged_alloc(iq_paged* c, int slots, int kv_heads, int head_dim, int pages
 int iq_paged_append(iq_paged* c, const void* keys, const void* values, int n, const int32_t* slots,
                     const int32_t* counts, int n_slots, iq_stream_t stream) {
   const int st = check_append(c, keys, values, n, slots, counts, n_slots);
-  return st != IQ_OK ? st : do_append(c, keys, values, n, slots, counts, n_slots, stream);
+  return st != IQ_OK ? st : do_append(c, keys, values, n, slots, counts, n_slots, stream, launch_append, nullptr);
 }
 
 int iq_paged_append_attend(iq_paged* c, const void* keys, const void* values, int n, const void* q, int q_heads,
@@ -542,7 +482,7 @@ int iq_paged_append_attend(iq_paged* c, const void* keys, const void* values, in
   st = check_attend(c, q, q_heads, n_queries, slots, counts, n_slots, n, scale, causal, window, sinks, out, out_f32, workspace,
                     workspace_bytes);
   if (st != IQ_OK) return st;
-  st = do_append(c, keys, values, n, slots, counts, n_slots, stream);
+  st = do_append(c, keys, values, n, slots, counts, n_slots, stream, launch_append, nullptr);
   if (st != IQ_OK) return st;
   return iq_paged_attend(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32,
                          workspace, workspace_bytes, stream);

@@ -16,6 +16,7 @@ import torch
 from . import _abi
 from ._abi import IQ_PAGE, IQPagedDesc, check, lib
 from .cache import _OnDevice, _device_of, _raw_stream, _stream
+from .rotary import IQRotary, _positions, _rows
 
 
 _INT32 = np.dtype(np.int32)
@@ -239,6 +240,40 @@ class IQPagedCache:
         E, _, n, _ = keys.shape
         slots, counts = self._entries(E, slots, counts)
         self._run(self._lib.iq_paged_append, self._d, keys.data_ptr(), values.data_ptr(), n, _at(slots), _at(counts), E, self._queue())
+
+    def append_rotary(self, q: torch.Tensor | None, keys: torch.Tensor, values: torch.Tensor, rotary: IQRotary, slots=None, counts=None,
+                      positions: torch.Tensor | None = None) -> torch.Tensor | None:
+        """`append` of a projection's rows as they are, in one launch: queries and keys normed and turned by `rotary`
+        at the positions where the rows come to stand (or at positions, an int32 CUDA tensor [entries, n]), keys and values quantised into
+        the pages.  Returns the queries for `attend`, [entries, Hq, n, D] (None where q is None).
+
+        q [entries, Hq, n, D], keys, values [entries, Hkv, n, D]: bf16 CUDA tensors, views with any strides (see
+        `IQRotary.apply`).  Rows behind counts[i] are not read; their queries come back as zeros.  Keys
+        are rounded to their codes once, from float32.
+        """
+        if rotary._index != self._index:
+            raise ValueError("the rotary plan must be on the cache's device")
+        keys, k_rows = _rows(keys, torch.bfloat16, self._index, "keys")
+        values, v_rows = _rows(values, torch.bfloat16, self._index, "values")
+        if keys.shape != values.shape or keys.shape[1] != self.kv_heads:
+            raise ValueError("keys/values must be [entries, Hkv, n, D]")
+        E, _, n, D = keys.shape
+        q_rows, Hq, out = None, 0, None
+        if q is not None:
+            q, q_rows = _rows(q, torch.bfloat16, self._index, "q")
+            if q.shape[0] != E or q.shape[2] != n:
+                raise ValueError("keys/values and q must have the same entries and rows")
+            Hq = q.shape[1]
+        slots, counts = self._entries(E, slots, counts)
+        at = None
+        if positions is not None:
+            positions = _positions(positions, E, n, self._index)
+            at = positions.data_ptr()
+        if q is not None:
+            out = (torch.empty if counts is None else torch.zeros)((E, Hq, n, D), dtype=torch.bfloat16, device=self.device)
+        self._run(self._lib.iq_paged_append_rotary, self._d, rotary._d, None if q is None else ctypes.byref(q_rows), Hq, ctypes.byref(k_rows),
+                  ctypes.byref(v_rows), n, _at(slots), _at(counts), E, at, None if q is None else out.data_ptr(), self._queue())
+        return out
 
     def read(self, start, n: int, slots=None) -> tuple[torch.Tensor, torch.Tensor]:
         """The values held in rows [start, start + n) of the slots (default: all), as bf16

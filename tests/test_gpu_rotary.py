@@ -1,0 +1,354 @@
+"""Rotary positions on the GPU against the oracle in 64 bits: rows to rows, and into the pages of the 8-bit cache."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged, rotary
+from test_gpu_paged import f64, pair, rows
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0**-24  # half a step of float32 at 1
+
+
+def plan(rd=64, interleaved=False, norm=True, scaling="none", seed=9, **kw):
+    """A plan and what the oracle needs of it."""
+    from rotated_bit_quantized_gb300 import IQRotary
+    g = torch.Generator().manual_seed(seed)
+    w = [0.3 * torch.randn(256, generator=g) for _ in range(2)] if norm else [None, None]
+    kw = dict(scaling=scaling, factor=8.0, original=4096) | kw
+    rot = IQRotary(rd, interleaved=interleaved, q_norm=w[0], k_norm=w[1], eps=1e-6, norm_offset=1.0, **kw)
+    lo, hi = {"yarn": (1, 32), "banded": (1, 4)}.get(scaling, (0, 0))
+    f = [rotary.frequency(i, rd, 10000.0, scaling, 8.0, 4096, lo, hi) for i in range(rd // 2)]
+    return rot, (w, f, interleaved, rot.amplitude)
+
+
+def exact(x, at, ref, which):
+    """x [entries, heads, n, 256] (a tensor) at positions [entries, n], in 64 bits, and a bound of its fp32 form's error:
+    the sum of 256 squares (a chain of 4, then 6 levels of a tree: 10 roundings, halved by the root), the root, two products:
+    9 U of a normed element at most.  A cosine or sine: the angle's last conversion (U of pi/4), sincospif's 2 units of the
+    last place and the amplitude's product, below 8 U of the amplitude; a product and a sum: 2 U more.  The frequency's own 2^-53 and
+    its turns' 2^-53, both relative, times the angle's size."""
+    w, f, interleaved, amplitude = ref
+    x = f64(x)
+    if w[which] is not None:
+        x = rotary.norm(x, 1.0 + w[which].double().numpy(), 1e-6)
+    y = rotary.turn(x, at[:, None, :], f, interleaved, amplitude)
+    n = len(f)
+    size = np.abs(x)
+    if n:
+        a, b = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+        both = (size[..., a] + size[..., b]) * amplitude
+        size[..., a] = size[..., b] = both
+    return y, size * (20 * U + 2.0**-51 * (1 + np.abs(at).max()))
+
+
+def check(out, y, tol):
+    got = f64(out)
+    if out.dtype == torch.bfloat16:
+        tol = tol + 2.0**-8 * (np.abs(y) + tol)
+    assert (np.abs(got - y) <= tol).all(), (np.abs(got - y) / tol).max()
+
+
+@pytest.mark.parametrize("rd,interleaved", [(0, False), (16, False), (64, False), (96, False), (128, False), (144, False), (192, False), (240, False), (256, False),
+                                            (16, True), (80, True), (128, True), (144, True), (256, True)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("norm", [False, True])
+def test_layouts(rd, interleaved, dtype, norm):
+    rot, ref = plan(rd, interleaved, norm)
+    q, k = rows(1, 3, 5, 37, True, dtype).cuda(), rows(2, 3, 2, 37, True, dtype).cuda()
+    start = [0, 1000, 77]
+    a, b = rot.apply(q, k, positions=start)
+    assert a.shape == q.shape and b.shape == k.shape and a.dtype == dtype and a.is_contiguous()
+    at = np.array(start)[:, None] + np.arange(37)
+    check(a, *exact(q, at, ref, 0))
+    check(b, *exact(k, at, ref, 1))
+
+
+@pytest.mark.parametrize("E,H,n", [(1, 1, 1), (1, 17, 1), (7, 3, 1), (32, 16, 1), (256, 1, 1), (2, 40, 3), (1, 1, 513), (3, 18, 97), (2, 2, 2049)])
+def test_sizes(E, H, n):
+    rot, ref = plan()
+    q = rows(3, E, H, n).cuda()
+    out = rot.apply(q, positions=5)
+    check(out, *exact(q, np.broadcast_to(5 + np.arange(n), (E, n)), ref, 0))
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "yarn", "banded"])
+def test_far_positions_and_scalings(scaling):
+    rot, ref = plan(128, True, False, scaling)
+    q = rows(4, 6, 2, 20, dtype=torch.float32).cuda()
+    start = [0, 1 << 20, 10**6 + 7, (1 << 31) - 20, -5, -(1 << 31)]
+    out = rot.apply(q, positions=start)
+    at = np.array(start, dtype=np.int64)[:, None] + np.arange(20)
+    check(out, *exact(q, at, ref, 0))
+
+
+def test_positions_of_every_row():
+    rot, ref = plan(96)
+    q, k = rows(5, 4, 6, 50).cuda(), rows(6, 4, 2, 50).cuda()
+    at = torch.randint(-100, 1 << 30, (4, 50), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    a, b = rot.apply(q, k, positions=at.cuda())
+    check(a, *exact(q, at.numpy().astype(np.int64), ref, 0))
+    check(b, *exact(k, at.numpy().astype(np.int64), ref, 1))
+    c = rot.apply(q, positions=at.cuda().t().contiguous().t())  # strided positions
+    assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_views_of_a_projection(dtype):
+    rot, ref = plan(256)
+    x = rows(7, 1, 2, 33 * 8, dtype=dtype).view(2, 33, 8, 256).cuda()  # [entries, rows, heads, 256]
+    q, k, v = x.transpose(1, 2).split([4, 2, 2], 1)
+    a, b = rot.apply(q, k, positions=3)
+    c, d = rot.apply(q.contiguous(), k.contiguous(), positions=3)
+    assert torch.equal(a, c) and torch.equal(b, d)
+    check(a, *exact(q, np.broadcast_to(3 + np.arange(33), (2, 33)), ref, 0))
+    # rows that no kernel can read where they lie (an odd offset, dims apart): copied
+    flat = torch.zeros(2 * 4 * 33 * 256 + 3, dtype=dtype, device="cuda")
+    odd = flat[3:].view(2, 4, 33, 256)
+    odd.copy_(q)
+    assert torch.equal(rot.apply(odd, positions=3), a)
+    assert torch.equal(rot.apply(q.transpose(2, 3).contiguous().transpose(2, 3), positions=3), a)
+    # the same rows for every entry and head
+    one = q[:1, :1].expand(3, 5, -1, -1)
+    assert torch.equal(rot.apply(one, positions=3), a[:1, :1].expand(3, 5, -1, -1))
+
+
+def test_extreme_rows():
+    rot, (w, f, il, amp) = plan(32)
+    x = torch.zeros(1, 1, 6, 256, dtype=torch.float32)
+    x[0, 0, 1] = 1e30                      # squares beyond fp32
+    x[0, 0, 2] = 1e-25                     # squares of nothing next to eps
+    x[0, 0, 3, 5] = float("nan")
+    x[0, 0, 4, 200] = float("inf")
+    x[0, 0, 5] = 3e38
+    out = f64(rot.apply(x.cuda()))
+    assert (out[0, 0, 0] == 0).all() and np.isnan(out[0, 0, 3]).all()
+    for r in (1, 2, 5):
+        y, tol = exact(x[:, :, r:r + 1], np.array([[r]]), (w, f, il, amp), 0)
+        assert (np.abs(out[0, 0, r] - y[0, 0, 0]) <= tol[0, 0, 0] + 1e-38).all()
+    assert np.isnan(out[0, 0, 4, 200]) and (out[0, 0, 4, 32:200] == 0).all()
+    for dtype in (torch.bfloat16, torch.float32):  # without a norm only the pairs of such elements are touched
+        plain, _ = plan(32, norm=False)
+        y = plain.apply(x.to(dtype).cuda())[0, 0]
+        assert torch.isnan(y[3, 5]) and torch.isnan(y[3, 21]) and torch.isfinite(torch.cat([y[3, :5], y[3, 6:21], y[3, 22:]])).all()
+        assert torch.isinf(y[4, 200]) and torch.isfinite(y[4, :200]).all()
+
+
+def test_nothing_to_turn_and_no_rows():
+    rot, _ = plan(0, norm=False)
+    q = rows(8, 2, 3, 9).cuda()
+    assert torch.equal(rot.apply(q, positions=12), q)
+    a, b = rot.apply(q[:, :, :0], q[:, :1, :0])
+    assert a.shape == (2, 3, 0, 256) and b.shape == (2, 1, 0, 256)
+    assert rot.apply(q[:0]).shape == (0, 3, 9, 256)
+
+
+def test_refusals():
+    from rotated_bit_quantized_gb300 import IQPagedCache
+    rot, _ = plan()
+    q = rows(1, 2, 4, 8).cuda()
+    at = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    for args, kw in [((q.half(),), {}), ((q.cpu(),), {}), ((q[..., :128],), {}), ((q[0],), {}), ((q, q.float()), {}), ((q, q[:1]), {}), ((q, q[:, :, :7]), {}),
+                     ((q,), dict(positions=1.5)), ((q,), dict(positions=[1, 2, 3])), ((q,), dict(positions=1 << 31)), ((q,), dict(positions=at[:1])),
+                     ((q,), dict(positions=at.long())), ((q,), dict(positions=at.cpu())), ((q.expand(2, 4, 8, 256).repeat(129, 1, 1, 1),), {})]:
+        with pytest.raises(ValueError):
+            rot.apply(*args, **kw)
+    c = IQPagedCache(4, 2, 10)
+    k, v = rows(2, 2, 2, 8).cuda(), rows(3, 2, 2, 8).cuda()
+    for args, kw in [((q, k.float(), v), {}), ((q, k, v[:, :1]), {}), ((q[:1], k, v), {}), ((q[:, :, :3], k, v), {}), ((q, k, v), dict(positions=at[:, :3])),
+                     ((q, k, v), dict(slots=[0, 0])), ((q, k, v), dict(counts=[9, 1])), ((q, rows(2, 2, 3, 8).cuda(), rows(3, 2, 3, 8).cuda()), {})]:
+        with pytest.raises((ValueError, RuntimeError)):
+            c.append_rotary(*args[:3], rot, **kw)
+    assert c.lens.tolist() == [0] * 4 and c.pages_free == 10
+
+
+# ------------------------------------------------------------------ into pages
+
+def check_append(c, o, rot, ref, q, k, v, slots=None, counts=None, positions=None):
+    """Append to both; every key held is its page's code nearest to the exact one, or, where that lies as near to the
+    border of two codes as fp32 can err, a neighbour; values and the pages' other rows are the oracle's."""
+    E, H, n, _ = k.shape
+    ids = list(range(E)) if slots is None else list(slots)
+    cnt = [n] * E if counts is None else list(counts)
+    before = [o.lens[s] for s in ids]
+    at = np.array(before)[:, None] + np.arange(n) if positions is None else positions.numpy().astype(np.int64)
+    y, tol = exact(k, at, ref, 1)
+    out = c.append_rotary(None if q is None else q.cuda(), k.cuda(), v.cuda(), rot, slots=slots, counts=counts,
+                          positions=None if positions is None else positions.cuda())
+    o.append(y, f64(v), slots, counts)
+    assert c.lens.tolist() == o.lens and c._refs.tolist() == o.refs
+    table = c.table.cpu().numpy()
+    kk, vv = (f64(t) for t in c.read(0, max(o.lens) + 1))
+    scales = f64(c.k_scales)
+    for i, s in enumerate(ids):
+        assert table[s, : len(o.rows[s])].tolist() == o.rows[s]
+        ok, ov, _ = o.values(s)
+        assert (vv[s][:, : o.lens[s]] == ov).all() and (kk[s][:, o.lens[s]:] == 0).all()
+        assert (kk[s][:, : before[i]] == ok[:, : before[i]]).all()
+        new, want = kk[s][:, before[i]: o.lens[s]], y[i, :, : cnt[i]]
+        unit = np.repeat(scales[o.rows[s]].T, 64, 1)[:, before[i]: o.lens[s], None]  # the pages' scales
+        step = np.ldexp(unit, np.frexp(np.maximum(np.abs(want) / unit, 2.0**-6))[1] - 4)
+        assert (np.abs(new - want) <= step / 2 + tol[i, :, : cnt[i]]).all()
+        same = new == ok[:, before[i]:]
+        assert (~same).sum() <= 0.001 * same.size  # (of a border's neighbourhood, 2^-18 of a step, 1e-5 is expected)
+        for t in range(before[i], o.lens[s]):  # a neighbour stays one: the oracle goes on from the codes held
+            for h in range(H):
+                o.held[o.rows[s][t // 64]][0][h].codes[t % 64] = kk[s][h, t] / scales[o.rows[s][t // 64], h]
+    if q is not None:
+        yq, tq = exact(q, at, ref, 0)
+        for i in range(E):
+            check(out[i, :, : cnt[i]], yq[i, :, : cnt[i]], tq[i, :, : cnt[i]])
+            assert (out[i, :, cnt[i]:] == 0).all()
+    else:
+        assert out is None
+    return out
+
+
+@pytest.mark.parametrize("rd,interleaved", [(0, False), (64, False), (160, False), (256, False), (64, True), (256, True)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_append_layouts(rd, interleaved, norm):
+    rot, ref = plan(rd, interleaved, norm)
+    c, o = pair(3, 2, 40, 800)
+    for i, n in enumerate((70, 1, 64, 133)):
+        check_append(c, o, rot, ref, rows(i, 3, 6, n, True), rows(10 + i, 3, 2, n, True) * (1 + i), rows(20 + i, 3, 2, n) * (1 + i))
+    assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("H,Hq", [(1, 1), (1, 8), (3, 33), (8, 8)])
+def test_append_heads_and_padded_batches(H, Hq):
+    rot, ref = plan(64)
+    c, o = pair(5, H, 60, 900)
+    check_append(c, o, rot, ref, rows(1, 4, Hq, 200), rows(2, 4, H, 200), rows(3, 4, H, 200), [4, 0, 1, 2], [200, 0, 1, 127])
+    check_append(c, o, rot, ref, rows(4, 5, Hq, 1), rows(5, 5, H, 1), rows(6, 5, H, 1))
+    check_append(c, o, rot, ref, None, rows(7, 2, H, 65), rows(8, 2, H, 65), [3, 2])
+    at = torch.randint(0, 1 << 22, (2, 30), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    check_append(c, o, rot, ref, rows(9, 2, Hq, 30), rows(10, 2, H, 30), rows(11, 2, H, 30), [1, 0], [30, 7], positions=at)
+    assert c.device_status() == 0
+
+
+def test_append_copies_shared_pages():
+    rot, ref = plan(64)
+    c, o = pair(4, 2, 30, 400)
+    check_append(c, o, rot, ref, None, rows(1, 1, 2, 100), rows(2, 1, 2, 100), [0])
+    c.fork([0, 0, 0], [1, 2, 3])
+    o.fork([0, 0, 0], [1, 2, 3])
+    check_append(c, o, rot, ref, rows(3, 4, 4, 3), rows(4, 4, 2, 3) * 50, rows(5, 4, 2, 3) * 50, None, [3, 2, 0, 1])
+    assert c.device_status() == 0
+
+
+def test_append_of_what_is_not_finite():
+    from rotated_bit_quantized_gb300 import _abi
+    rot, _ = plan(64, norm=False)
+    k, v = rows(1, 1, 2, 3), rows(2, 1, 2, 3)
+    for bad, status in ((float("nan"), _abi.IQ_STATUS_RANGE), (float("inf"), _abi.IQ_STATUS_RANGE), (3e38, _abi.IQ_STATUS_RANGE), (1e20, 0)):
+        for which in (0, 1):
+            c, _ = pair(1, 2, 2)
+            x = [k.clone(), v.clone()]
+            x[which][0, 1, 1, 200] = bad
+            c.append_rotary(None, x[0].cuda(), x[1].cuda(), rot)
+            held = [f64(t) for t in c.read(0, 3)]
+            assert all(np.isfinite(t).all() for t in held)
+            assert c.device_status() == status
+            if bad != bad:
+                assert held[which][0, 1, 1, 200] == 0 and np.abs(held[which]).max() < 10
+            elif status:
+                assert held[which][0, 1, 1, 200] == 448.0 * 2.0**60
+
+
+def test_a_large_append_equals_small_ones():
+    """More pages and entries than one launch's list of runs holds, past 2^16 rows."""
+    rot, _ = plan(128)
+    from rotated_bit_quantized_gb300 import IQPagedCache
+    a, b = IQPagedCache(3, 1, 3400), IQPagedCache(3, 1, 3400)
+    a.append(*(rows(s, 3, 1, 64).cuda() for s in (1, 2)), counts=[64, 0, 64])
+    a.free([0])  # pages no longer in a row
+    b.append(*(rows(s, 3, 1, 64).cuda() for s in (1, 2)), counts=[0, 0, 64])
+    q, k, v = (rows(5 + i, 2, h, 1, ).expand(2, h, 66000, 256) for i, h in enumerate((2, 1, 1)))
+    x = [t.clone().cuda() for t in (q, k, v)]
+    out = a.append_rotary(*x, rot, slots=[0, 1])
+    parts = [b.append_rotary(*(t[:, :, i:i + 22000] for t in x), rot, slots=[0, 1]) for i in range(0, 66000, 22000)]
+    assert torch.equal(out, torch.cat(parts, 2))
+    for s in (0, 65000, 21990):
+        assert all(torch.equal(i, j) for i, j in zip(a.read(s, 900, slots=[0, 1]), b.read(s, 900, slots=[0, 1])))
+    assert a.device_status() == 0 and b.device_status() == 0
+
+
+# ------------------------------------------------------------------ streams, graphs, chains
+
+def test_replays_in_a_graph_on_another_stream():
+    rot, _ = plan(64)
+    from rotated_bit_quantized_gb300 import IQPagedCache
+    q, k, v = rows(1, 4, 8, 1).cuda(), rows(2, 4, 2, 1).cuda(), rows(3, 4, 2, 1).cuda()
+    a, b = IQPagedCache(4, 2, 16), IQPagedCache(4, 2, 16)
+    for c in (a, b):
+        c.append(*(rows(s, 4, 2, 100).cuda() for s in (4, 5)))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            turned = rot.apply(q, k, positions=100)
+            out = a.append_rotary(q, k, v, rot)
+            att = a.attend(out)
+        for i in range(3):
+            q.copy_(rows(50 + i, 4, 8, 1)), k.copy_(rows(60 + i, 4, 2, 1)), v.copy_(rows(70 + i, 4, 2, 1))
+            g.replay()
+    torch.cuda.current_stream().wait_stream(s)
+    want = b.append_rotary(q, k, v, rot)
+    x, y = rot.apply(q, k, positions=100)
+    assert torch.equal(out, want) and torch.equal(turned[0], x) and torch.equal(turned[1], y)
+    assert torch.equal(att, b.attend(want))
+    assert a.device_status() == 0 and b.device_status() == 0
+
+
+def test_chains_of_calls_without_waits():
+    """Each call reads what the one before hands out; the rotated cache's attention reads its queries early."""
+    from rotated_bit_quantized_gb300 import IQCache, IQPagedCache, Rotation
+    rot, _ = plan(64)
+    so4 = Rotation(0)
+    q = rows(1, 8, 8, 1).cuda()
+    k, v = rows(2, 8, 2, 1).cuda(), rows(3, 8, 2, 1).cuda()
+    past = [rows(s, 8, 2, 2000).cuda() for s in (4, 5)]
+
+    def chain(wait):
+        c, p = IQCache(8, 2, capacity=2304), IQPagedCache(8, 2, 8 * 34)
+        c.append(*past, so4)
+        p.append(*past)
+        x, res = q, []
+        for i in range(6):
+            a, b = rot.apply(x, k, positions=2000 + i)
+            wait()
+            x = c.append_attend(b, v, a, so4)
+            wait()
+            x = p.append_rotary(x, k, v, rot)
+            wait()
+            x = c.attend(x, so4)
+            wait()
+            x = p.attend(x)
+            wait()
+            res.append(x)
+        return res
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        got = chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_float32_cache_takes_turned_rows():
+    from rotated_bit_quantized_gb300 import IQCache, Rotation
+    rot, ref = plan(128, True, scaling="yarn")
+    so4 = Rotation(0)
+    q, k, v = (rows(i, 2, h, 40, dtype=torch.float32).cuda() for i, h in ((1, 4), (2, 2), (3, 2)))
+    a, b = rot.apply(q, k)
+    c = IQCache(2, 2, k_bits=8, v_bits=8, dtype=torch.float32)
+    c.append(b, v, so4)
+    out = f64(c.attend(a[:, :, -1:].contiguous(), so4))
+    at = np.broadcast_to(np.arange(40), (2, 40))
+    yq, yk = exact(q, at, ref, 0)[0], exact(k, at, ref, 1)[0]
+    s = np.einsum("ehd,ehtd->eht", yq[:, :, -1].reshape(2, 4, 256), np.repeat(yk, 2, 1)) / 16
+    p = np.exp(s - s.max(-1, keepdims=True))
+    want = np.einsum("eht,ehtd->ehd", p / p.sum(-1, keepdims=True), np.repeat(f64(v), 2, 1))
+    # 8 bits of groups whose elements span some 8: half a step of 8 / 255 in a value; a score of 256 such products
+    # of keys off by as much at random moves by 0.02 * |q| / 16, some 0.03 of the weights
+    assert np.abs(out[:, :, 0] - want).max() < 0.1
