@@ -595,6 +595,26 @@ int iq_paged_append_attend(iq_paged* cache, const void* keys, const void* values
                            int n_slots, float scale, int causal, int window, int sinks, void* out,
                            int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream);
 
+/*
+ * iq_paged_attend_shared — iq_paged_attend where slots share pages (forked paths, a common
+ * prompt): pages that several of the call's slots hold are read and multiplied once for all
+ * of them.  The same arguments, results (other sums' orders: within the same bounds) and errors,
+ * and its own size of workspace.  What is shared is taken from table_host, up to four levels of
+ * sharing; a call with nothing to gain (more than 128 query rows per kv head and slot, or little
+ * in common) runs as iq_paged_attend.  A captured call replays with the sharing that it was captured with: the
+ * slots that shared pages then still have to.
+ */
+int iq_paged_attend_shared_workspace(const iq_paged* cache, int q_heads, int n_queries, int n_slots, size_t* bytes);
+int iq_paged_attend_shared(const iq_paged* cache, const void* q, int q_heads, int n_queries, const int32_t* slots,
+                           const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
+                           void* out, int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream);
+
+/* iq_paged_append_attend_shared — iq_paged_append_attend with iq_paged_attend_shared in the second place. */
+int iq_paged_append_attend_shared(iq_paged* cache, const void* keys, const void* values, int n, const void* q,
+                                  int q_heads, int n_queries, const int32_t* slots, const int32_t* counts,
+                                  int n_slots, float scale, int causal, int window, int sinks, void* out,
+                                  int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Rotary positions: what a model does to its queries and keys before either cache
  * takes them.  Library services: the source pages have no counterpart (their

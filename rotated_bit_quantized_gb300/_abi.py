@@ -37,7 +37,8 @@ EXPORTS = ("iq_status_string", "iq_last_error", "iq_build_rotation", "iq_cache_b
            "iq_paged_check", "iq_paged_append", "iq_paged_read", "iq_paged_trim", "iq_paged_free",
            "iq_paged_fork", "iq_paged_compact", "iq_paged_attend_workspace", "iq_paged_attend",
            "iq_paged_append_attend", "iq_paged_debug_fail", "iq_paged_debug_stall", "iq_rotary_frequencies",
-           "iq_rotary_turns", "iq_rotary_apply", "iq_paged_append_rotary")
+           "iq_rotary_turns", "iq_rotary_apply", "iq_paged_append_rotary", "iq_paged_attend_shared_workspace",
+           "iq_paged_attend_shared", "iq_paged_append_attend_shared")
 
 
 class IQCacheDesc(ctypes.Structure):
@@ -130,6 +131,9 @@ def lib() -> ctypes.CDLL:
         L.iq_rotary_turns.argtypes = [P, I, P, P]
         L.iq_rotary_apply.argtypes = [ROTARY, I, ROWS, I, ROWS, I, I, I, P, P, P, P, P]
         L.iq_paged_append_rotary.argtypes = [PAGED, ROTARY, ROWS, I, ROWS, ROWS, I, P, P, I, P, P, P]
+        L.iq_paged_attend_shared_workspace.argtypes = L.iq_paged_attend_workspace.argtypes
+        L.iq_paged_attend_shared.argtypes = L.iq_paged_attend.argtypes
+        L.iq_paged_append_attend_shared.argtypes = L.iq_paged_append_attend.argtypes
         L.iq_paged_debug_fail.argtypes = [I]
         L.iq_paged_debug_stall.argtypes = []
         for name in EXPORTS:

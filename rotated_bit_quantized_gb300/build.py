@@ -16,7 +16,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libiqkv.so")
 SOURCES = ["iq_cache.cu", "iq_attend.cu", "iq_noalloc.cu", "iq_generic.cu", "iq_prefill.cu",
-           "iq_pages.cu", "iq_paged_attend.cu", "iq_paged_prefill.cu", "iq_rotary.cu"]
+           "iq_pages.cu", "iq_paged_attend.cu", "iq_paged_prefill.cu", "iq_paged_shared.cu",
+           "iq_rotary.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE]

@@ -579,6 +579,29 @@ bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows, int box_ro
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int store_zeros(const iq_paged* c, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots, void* out,
+                int out_f32, iq_stream_t stream) {
+  ZeroParams z;
+  z.out = out;
+  z.q_heads = q_heads;
+  z.nq = n_queries;
+  z.out_bytes = out_f32 ? 4 : 2;
+  int n = 0, most = 0;
+  for (int i = 0; i < n_slots; ++i) {
+    const int count = counts ? counts[i] : n_queries;
+    if (count == 0 || c->lens[slot_of(slots, i)] > 0) continue;
+    z.entry[n] = static_cast<short>(i);
+    z.count[n++] = count;
+    most = std::max(most, count);
+  }
+  if (n == 0) return IQ_OK;
+  void* args[] = {&z};
+  IQ_CUDA(launch_after(reinterpret_cast<const void*>(&paged_zero_kernel), dim3(std::min(64, (most + 7) / 8), n), 256, 0,
+                       static_cast<cudaStream_t>(stream), args));
+  launched_outputs(stream, {out, static_cast<size_t>(n_slots) * q_heads * n_queries * kHeadDim * (out_f32 ? 4 : 2)});
+  return IQ_OK;
+}
+
 int check_attend(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots,
                  const int32_t* counts, int n_slots, int added, float scale, int causal, int window, int sinks,
                  const void* out, int out_f32, const void* workspace, size_t workspace_bytes) {
@@ -660,26 +683,8 @@ int iq_paged_attend(const iq_paged* c, const void* q, int q_heads, int n_queries
   int longest = 0;
   for (int i = 0; i < n_slots; ++i) longest = std::max(longest, c->lens[slot_of(slots, i)]);
   if (window >= longest) window = sinks = 0;  // nothing is out of it, and positions less a window stay in 32 bits
-  {
-    ZeroParams z;
-    z.out = out;
-    z.q_heads = q_heads;
-    z.nq = n_queries;
-    z.out_bytes = out_f32 ? 4 : 2;
-    int n = 0, most = 0;
-    for (int i = 0; i < n_slots; ++i) {
-      const int count = counts ? counts[i] : n_queries;
-      if (count == 0 || c->lens[slot_of(slots, i)] > 0) continue;
-      z.entry[n] = static_cast<short>(i);
-      z.count[n++] = count;
-      most = std::max(most, count);
-    }
-    if (n > 0) {
-      void* args[] = {&z};
-      IQ_CUDA(launch_after(reinterpret_cast<const void*>(&paged_zero_kernel), dim3(std::min(64, (most + 7) / 8), n), 256, 0, cs, args));
-      launched_outputs(stream, written);
-    }
-  }
+  const int zeroed = store_zeros(c, q_heads, n_queries, slots, counts, n_slots, out, out_f32, stream);
+  if (zeroed != IQ_OK) return zeroed;
   AttendParams p;
   std::memset(&p, 0, sizeof(p));
   p.unit_rows = unit_rows(rows);

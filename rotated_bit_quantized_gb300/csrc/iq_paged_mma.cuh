@@ -35,7 +35,7 @@ bool code_map(CUtensorMap* map, const uint8_t* codes, long long rows, int box_ro
 struct Cut {
   int last, slot, e, h, z, pad[3];
 };
-struct AttendParams {
+struct AttendBase {
   CUtensorMap k_map, v_map, q_map;  // (q_map: the prefill kernel's queries, cut beforehand)
   const float* k_scales;
   const float* v_scales;
@@ -43,15 +43,20 @@ struct AttendParams {
   unsigned* status;
   const uint16_t* q;
   void* out;
-  float* part_o;    // [2 * grid][unit_rows][256] unnormalised partial results: a range's first segment, its last
-  float2* part_ml;  // [2 * grid][unit_rows] their references and sums
-  Cut* cuts;        // [grid] the unit that a range's end cuts
+  float* part_o;    // rows of 256 unnormalised partial results
+  float2* part_ml;  // their references and sums
   uint8_t* cut;     // prefill: [high, low parts][entry][kv head][row][256] e4m3
   float* factors;   // prefill: [entry][kv head][row] 2^e * scale * log2 e
-  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, unit_rows, cost, total, slots_n;
-  unsigned rep_mul, rep_shift;  // division by rep, see query_of
+  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, cost, total, slots_n;
   int stall;                    // test hook (iq_paged_debug_stall): no page is loaded, so the waits for them run out
   float scale;
+};
+struct AttendParams : AttendBase {
+  static constexpr bool kTree = false;
+  // part_o, part_ml: [2 * grid][unit_rows], a range's first segment, its last
+  Cut* cuts;        // [grid] the unit that a range's end cuts
+  int unit_rows;
+  unsigned rep_mul, rep_shift;  // division by rep, see query_of
   // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
   // its queries; cum: slots before it (all heads), per: slots of one of its heads
   short entry[IQ_MAX_BATCH], slot[IQ_MAX_BATCH];
@@ -62,8 +67,9 @@ struct AttendParams {
 // its last row's position.  A unit that sees no key keeps one tile, all masked.
 struct Tiles {
   int sinks, skip, n;  // tiles of the sinks; tiles between them and the window; all
-  int p_lo, p_hi;      // positions of the first and the last row
-  __host__ __device__ int tile(int j) const { return j < sinks ? j : j + skip; }
+  int p_lo, p_hi;      // the least and the largest position of a row
+  int base;            // the tile before which nothing is of the unit's
+  __host__ __device__ int tile(int j) const { return base + (j < sinks ? j : j + skip); }
 };
 __host__ __device__ inline Tiles tiles_of(int len, int first_pos, int last_pos, int causal, int window, int sinks) {
   Tiles t;
@@ -75,6 +81,7 @@ __host__ __device__ inline Tiles tiles_of(int len, int first_pos, int last_pos, 
   t.sinks = n < begin ? n : begin;
   t.skip = n < begin ? begin - n : 0;
   t.n = (stop + kTile - 1) / kTile - t.skip;
+  t.base = 0;
   return t;
 }
 
@@ -90,12 +97,32 @@ __host__ __device__ inline int range_of(int tile, int grid, int total) {
 struct Place {
   int e, h, z, j;
 };
+// The attention of slots that share pages.  The pages that a group of slots has in
+// common, and others have not, are a node of a tree; its leaves are what a slot holds
+// alone.  A node's rows are those of all its slots, which lie side by side in the cut
+// queries, and its units are (node, kv head, 128 of these rows).  Every unit leaves
+// partial results, at its rows' place, and in ranges behind its first in these ranges';
+// those of the nodes that a slot is under are joined.
+constexpr int kInner = 64, kNodes = IQ_MAX_BATCH + kInner, kDepth = 4;  // inner nodes of a call, all; nodes above one another
+constexpr int kUnitRows = 128;
+struct TreeParams : AttendBase {
+  static constexpr bool kTree = true;
+  const int4* place;     // [rows] the lowest node that a row is under (< 0: none), its position, its place in q and out
+  int rows, cont;        // rows of one kv head; where the ranges' partial results begin
+  short slot[kNodes];    // that holds the node's pages
+  short parent[kNodes];  // < 0: none
+  int end_page[kNodes];  // the slot's last page
+  int row0[kNodes], n[kNodes], part0[kNodes];  // its first row, how many, their place in the partial results
+  int cum[kNodes + 1];   // slots before it
+  int tiles[kNodes], base[kNodes], sink_tiles[kNodes], skip[kNodes], p_lo[kNodes], p_hi[kNodes];  // of its units, see Tiles
+};
+
 // The tiles of a unit that a range takes from slot w.j on, `left` slots of the
 // range being left: [begin, begin + n), none where it ends in the unit's empty slots.
 struct Part {
   int begin, n;
 };
-__device__ __forceinline__ Part part_of(const AttendParams& p, const Place& w, int tiles, int left) {
+__device__ __forceinline__ Part part_of(const AttendBase& p, const Place& w, int tiles, int left) {
   const int begin = max(w.j - p.cost, 0), end = min(max(w.j + left - p.cost, 0), tiles);
   return {begin, end - begin};
 }
@@ -110,6 +137,18 @@ __device__ __forceinline__ Tiles tiles_at(const AttendParams& p, const Place& w)
   return tiles_of(p.len[w.e], before + query_of(p, r0), before + query_of(p, min(r0 + p.unit_rows, rows) - 1), p.causal, p.window,
                   p.sinks);
 }
+__device__ __forceinline__ Tiles tiles_at(const TreeParams& p, const Place& w) {
+  return {p.sink_tiles[w.e], p.skip[w.e], p.tiles[w.e], p.p_lo[w.e], p.p_hi[w.e], p.base[w.e]};
+}
+__device__ __forceinline__ int rows_at(const AttendParams& p, const Place& w) { return p.count[w.e] * p.rep - w.z * p.unit_rows; }
+__device__ __forceinline__ int rows_at(const TreeParams& p, const Place& w) { return p.n[w.e] - w.z * kUnitRows; }
+__device__ __forceinline__ int last_page(const AttendParams& p, int e) { return (p.len[e] + kPage - 1) / kPage - 1; }
+__device__ __forceinline__ int last_page(const TreeParams& p, int e) { return p.end_page[e]; }
+// the cut queries' row of a unit's first
+__device__ __forceinline__ int cut_row(const AttendParams& p, const Place& w) {
+  return (p.entry[w.e] * p.heads + w.h) * p.nq * p.rep + w.z * p.unit_rows;
+}
+__device__ __forceinline__ int cut_row(const TreeParams& p, const Place& w) { return w.h * p.rows + p.row0[w.e] + w.z * kUnitRows; }
 // For the joining kernel: the unit at w, whose first slot in the range is `at`,
 // of which the range takes all tiles from the first on, but not all.
 __device__ __forceinline__ void tell_cut(const AttendParams& p, const Place& w, int at, int tiles, int slot) {
@@ -154,10 +193,34 @@ __device__ inline Place place_of(const AttendParams& p, int t) {
     if (z0 + 32 >= units) return w;  // not reached: t is a slot of this head
   }
 }
+__device__ inline Place place_of(const TreeParams& p, int t) {
+  Place w;
+  int hi = p.entries - 1;
+  w.e = 0;
+  while (w.e < hi) {
+    const int mid = (w.e + hi + 1) / 2;
+    if (p.cum[mid] <= t) w.e = mid;
+    else hi = mid - 1;
+  }
+  t -= p.cum[w.e];
+  const int per = p.tiles[w.e] + p.cost, units = (p.n[w.e] + kUnitRows - 1) / kUnitRows, u = t / per;
+  w.j = t - u * per;
+  w.h = u / units;
+  w.z = u - w.h * units;
+  return w;
+}
 // The unit after w's.
 __device__ __forceinline__ void next_unit(const AttendParams& p, Place& w) {
   w.j = 0;
   if (++w.z * p.unit_rows < p.count[w.e] * p.rep) return;
+  w.z = 0;
+  if (++w.h < p.heads) return;
+  w.h = 0;
+  ++w.e;
+}
+__device__ __forceinline__ void next_unit(const TreeParams& p, Place& w) {
+  w.j = 0;
+  if (++w.z * kUnitRows < p.n[w.e]) return;
   w.z = 0;
   if (++w.h < p.heads) return;
   w.h = 0;
@@ -171,6 +234,10 @@ __device__ __forceinline__ long long row_index(const AttendParams& p, const Plac
 
 // counts: of every entry of the call, also those without keys
 cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream);
+cudaError_t launch_tree(const TreeParams& p, int grid, cudaStream_t stream);  // (its queries are cut already)
+// zeros for the queries of empty slots
+int store_zeros(const iq_paged* c, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots, void* out,
+                int out_f32, iq_stream_t stream);
 
 // Waits end: after a second (no stage takes a thousandth of it) the CTA's
 // abort flag is raised, every later wait of the CTA returns at once, and the
@@ -293,7 +360,7 @@ __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.
 // load under a saturated HBM takes a tile's time and more).  A lane holds the
 // id and the scales of one page of 16 tiles.  Ids are fetched 16 tiles or two
 // segments ahead, scales half of that.
-template <int SLOTS, bool ACROSS>
+template <int SLOTS, bool ACROSS, class P = AttendParams>
 struct Loader {
   // a tile's scales live until its weights are written: K(j + 4) takes, of 4 slots, that of K(j + 2), free
   // once its scores are done, which the prefill kernel issues behind tile j's last product; K(j + 8) takes,
@@ -306,7 +373,7 @@ struct Loader {
     Tiles tiles;
     int begin, n, end_page, h;
   };
-  const AttendParams& p;
+  const P& p;
   uint8_t* smem;
   uint64_t *full, *empty;
   float4* scales;      // [kRing] keys' scales of the tile's two pages, values'
@@ -322,7 +389,7 @@ struct Loader {
     g.begin = part.begin;
     g.n = part.n;
     g.row = p.table + static_cast<long long>(p.slot[w.e]) * p.max_pages;
-    g.end_page = (p.len[w.e] + kPage - 1) / kPage - 1;
+    g.end_page = last_page(p, w.e);
     g.h = w.h;
     at += g.tiles.n + p.cost - w.j;
     next_unit(p, w);

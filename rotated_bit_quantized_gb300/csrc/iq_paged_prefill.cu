@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(256) paged_cut_kernel(const __grid_constant__ 
 // on the way: the queries cut beforehand (260 to 214 us on the last), products
 // issued by a whole warp (745 to 673 us on the first), the references' rescaling
 // behind the weights, scores issued over a unit's end.
-__global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid_constant__ AttendParams p) {
+template <class P>  // AttendParams, or TreeParams: units of slots that share pages, all of whose results are partial
+__global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid_constant__ P p) {
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled operands need it; no room to align by hand
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // (the kernel has no other shared memory in front)
@@ -163,7 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
 
   const int first = range_begin(blockIdx.x, gridDim.x, p.total), last = range_begin(blockIdx.x + 1, gridDim.x, p.total);
   const Place start = place_of(p, first);
-  const int q_rows = p.slots_n * p.heads * p.rep * p.nq;  // high parts, then as many rows of low parts
+  int q_rows;  // high parts, then as many rows of low parts
+  if constexpr (P::kTree) q_rows = p.heads * p.rows;
+  else q_rows = p.slots_n * p.heads * p.rep * p.nq;
 
   if (warp < kLoader) {
     // ---------------------------------------------------------------- softmax: half a row per thread
@@ -176,21 +179,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       if (ok) ok = wait(bar, phase, kLostRows);
       __syncwarp();
     };
-    if (threadIdx.x == 0) p.cuts[blockIdx.x].last = -1;
+    if constexpr (!P::kTree) {
+      if (threadIdx.x == 0) p.cuts[blockIdx.x].last = -1;
+    }
     // the unit whose results are still in tensor memory
     Place done{};
     bool pending = false, done_whole = false;
-    int done_slot = 0;
+    int done_row = 0;  // of partial results: its first row's place
     float done_l = 0.0f, done_ref = 0.0f;
     auto store_results = [&](int last_tile) {  // the sums of a row's two halves, half of its dims per thread
       xch[group * kRows + r] = done_l;
       named_bar(1 + quad, 64);
       const float sum = done_l + xch[(group ^ 1) * kRows + r];
       named_bar(1 + quad, 64);
-      const int rows = min(kRows, p.count[done.e] * p.rep - done.z * kRows);
+      const int rows = min(kRows, rows_at(p, done));
       const float inv = !done_whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
       const bool wide = !done_whole || p.out_f32;
-      const long long to = done_whole ? row_index(p, done, done.z * kRows + min(r, rows - 1)) : static_cast<long long>(done_slot) * kRows + r;
+      long long to = done_row + r;
+      if constexpr (!P::kTree) {
+        if (done_whole) to = row_index(p, done, done.z * kRows + min(r, rows - 1));
+      }
       uint8_t* out = static_cast<uint8_t*>(done_whole ? p.out : p.part_o) + (to * kHeadDim + group * 128) * (wide ? 4 : 2);
       await(&o_done[last_tile & 1], last_tile / 2);
       tc_after();
@@ -219,12 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           }
         }
       }
-      if (!done_whole && r < rows && group == 0) p.part_ml[done_slot * kRows + r] = make_float2(done_ref, sum);
+      if (!done_whole && r < rows && group == 0) p.part_ml[done_row + r] = make_float2(done_ref, sum);
     };
-    // the factor of this thread's row, fetched a unit ahead
+    // the factor of this thread's row, and in a tree its position, fetched a unit ahead
+    int next_pos = 0;
     auto factor_of = [&](const Place& u) {
-      const int x = u.z * kRows + r;
-      return x < p.count[u.e] * p.rep ? __ldcg(p.factors + (p.entry[u.e] * p.heads + u.h) * p.nq * p.rep + x) : 0.0f;
+      if (r >= rows_at(p, u)) return 0.0f;
+      if constexpr (P::kTree) next_pos = __ldcg(&p.place[p.row0[u.e] + u.z * kRows + r].y);
+      return __ldcg(p.factors + cut_row(p, u) + r);
     };
     Place w = start;
     float next_factor = first < last ? factor_of(w) : 0.0f;
@@ -238,13 +248,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       const int n = part.n;
       if (n == 0 && !pending) break;
       if (n == 0) w = start;  // no unit follows: one turn more, for the last one's results alone
-      const int e = w.e, k0 = part.begin, len = p.len[e];
-      const bool whole = n == tiles.n, exists = w.z * kRows + r < p.count[e] * p.rep;
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
-      if (n > 0 && n < tiles.n && k0 == 0 && threadIdx.x == 0) tell_cut(p, w, at, tiles.n, slot);
+      const int k0 = part.begin;
+      const bool whole = !P::kTree && n == tiles.n, exists = r < rows_at(p, w);
+      int row, pos, len = 0;
+      if constexpr (P::kTree) {
+        row = k0 == 0 ? p.part0[w.e] + w.h * p.n[w.e] + w.z * kRows : p.cont + static_cast<int>(blockIdx.x) * kRows;
+        pos = next_pos;
+      } else {
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (at == first ? 0 : 1);
+        if (n > 0 && n < tiles.n && k0 == 0 && threadIdx.x == 0) tell_cut(p, w, at, tiles.n, slot);
+        row = slot * kRows;
+        len = p.len[w.e];
+        pos = len - p.count[w.e] + query_of(p, w.z * kRows + r);
+      }
       at += tiles.n + p.cost - w.j;
-      const int pos = len - p.count[e] + query_of(p, w.z * kRows + r);
-      const int stop = !exists ? 0 : p.causal ? pos + 1 : len;
+      const bool causal = P::kTree || p.causal;  // (in a tree a query that sees all has the last position)
+      const int stop = !exists ? 0 : causal ? pos + 1 : len;
       const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
       // a row that has seen no key yet has no reference (its weights are all 0)
       bool unset = exists;
@@ -266,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
           const float ev = static_cast<float>(exponent_of(sc[2]));
           const int t0 = tiles.tile(k0 + j) * kTile;
           // whether some row of the unit does not see the whole tile
-          const bool masked = t0 + kTile > (p.causal ? tiles.p_lo + 1 : len) ||
+          const bool masked = t0 + kTile > (causal ? tiles.p_lo + 1 : len) ||
                               (p.window > 0 && t0 <= tiles.p_hi - p.window && t0 + kTile > p.sinks);
           const uint32_t t_s = tmem + lanes + b * 128 + group * 64;
           await(&s_full[b], it / 2);
@@ -394,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
       pending = true;
       done = w;
       done_whole = whole;
-      done_slot = slot;
+      done_row = row;
       done_l = l;
       done_ref = unset ? kUnset : ref;
     }
@@ -403,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
     if (warp == kLoader) {
       uint64_t policy;  // other row tiles read the same pages
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-      Loader<kSlots, true>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy);
+      Loader<kSlots, true, P>{p, smem, full, empty, scales, scales_in, wait}.run(start, first, last, policy);
     } else if (warp == kIssuer) {
       // ---------------------------------------------------------------- products
       constexpr uint32_t kS = shape(128, kTile, false, false);
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
         at += tiles + p.cost - w.j;
         if (n == 0 || (segment > 0 && !wait(q_free, segment - 1, kLostLoad))) break;
         mbar_arrive_expect_tx(q_ready, 4 * kHalfBytes);
-        const int y = (p.entry[w.e] * p.heads + w.h) * p.nq * p.rep + w.z * kRows;
+        const int y = cut_row(p, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // high parts, low parts; halves of the dims (rows behind the unit's are others', or zeros)
           tensor2d_g2s(smem + kQ + k * kHalfBytes, &p.q_map, 128 * (k & 1), y + (k >> 1) * q_rows, q_ready, policy_evict_first());
@@ -507,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(const __grid
 
 cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> seen{0};
-  const void* kernel = reinterpret_cast<const void*>(&paged_prefill_kernel);
+  const void* kernel = reinterpret_cast<const void*>(&paged_prefill_kernel<AttendParams>);
   cudaError_t e = allow_smem(kernel, kSmem, seen);
   CutParams c;
   c.q = p.q;
@@ -524,6 +543,14 @@ cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, c
   if (e == cudaSuccess) e = launch_after(reinterpret_cast<const void*>(&paged_cut_kernel), dim3((c.total + 31) / 32), 256, 0, stream, cut_args);
   if (e == cudaSuccess) e = launch_after(kernel, dim3(grid), kThreads, kSmem, stream, args);
   return e;
+}
+
+cudaError_t launch_tree(const TreeParams& p, int grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> seen{0};
+  const void* kernel = reinterpret_cast<const void*>(&paged_prefill_kernel<TreeParams>);
+  const cudaError_t e = allow_smem(kernel, kSmem, seen);
+  void* args[] = {const_cast<TreeParams*>(&p)};
+  return e == cudaSuccess ? launch_after(kernel, dim3(grid), kThreads, kSmem, stream, args) : e;
 }
 
 }  // namespace paged

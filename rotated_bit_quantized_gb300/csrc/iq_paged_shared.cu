@@ -1,0 +1,408 @@
+// libiqkv: attention of slots that share pages of the paged 8-bit cache.
+//
+// softmax(s) . v over a union of key sets is the weighted mean of the sets' own
+// results, weights 2^(their maximum) * their sum; so the pages that several slots
+// hold are multiplied once, with the rows of all of them side by side, and each slot's
+// own pages apart, and the partial results are joined.  What is shared is found on the
+// host, from the page ids of the table: a tree whose nodes are runs of pages that a
+// group of slots holds and others do not.  The products run in the prefill kernel
+// (iq_paged_prefill.cu), whose M dimension the rows of many slots fill.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "iq_paged_mma.cuh"
+#include "iq_pages.cuh"
+
+namespace iq {
+namespace paged {
+namespace {
+
+// ------------------------------------------------------------------ queries
+
+struct TreeCutParams {
+  const uint16_t* q;
+  uint8_t* cut;
+  float* factors;
+  int4* place;
+  int heads, rep, nq, rows, entries, causal;
+  float scale;
+  short entry[IQ_MAX_BATCH], lowest[IQ_MAX_BATCH];  // place in the call, lowest node
+  int row0[IQ_MAX_BATCH + 1], pos0[IQ_MAX_BATCH];   // first row, first query's position
+};
+
+// Every row of (entry, kv head): two e4m3 parts, the factor of its scores, and where it
+// stands; a warp takes four.
+__global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_constant__ TreeCutParams p) {
+  wait_for_last_kernel();
+  const int lane = threadIdx.x & 31, w0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4, h = blockIdx.y;
+  uint4 raw[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = min(w0 + k, p.rows - 1);
+    int s = 0, hi = p.entries - 1;
+    while (s < hi) {
+      const int mid = (s + hi + 1) / 2;
+      if (p.row0[mid] <= row) s = mid;
+      else hi = mid - 1;
+    }
+    const int x = row - p.row0[s], j = x / p.rep;
+    const int at = (p.entry[s] * p.heads * p.rep + x - j * p.rep) * p.nq + j;  // of kv head 0
+    raw[k] = __ldcs(reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(h) * p.rep * p.nq + at) * kHeadDim) + lane);
+    if (h == 0 && lane == 0 && w0 + k < p.rows) p.place[row] = make_int4(p.lowest[s], p.pos0[s] + (p.causal ? j : 0), at, 0);
+  }
+  if (p.scale < 0.0f) {  // the factors are positive, so that the largest product is the largest score
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      raw[k] = make_uint4(raw[k].x ^ 0x80008000u, raw[k].y ^ 0x80008000u, raw[k].z ^ 0x80008000u, raw[k].w ^ 0x80008000u);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint2 hi, lo;
+    const float f = split_query<1>(raw[k], hi, lo);
+    if (w0 + k >= p.rows) break;
+    const long long w = static_cast<long long>(h) * p.rows + w0 + k;
+    reinterpret_cast<uint2*>(p.cut + w * kHeadDim)[lane] = hi;
+    reinterpret_cast<uint2*>(p.cut + (static_cast<long long>(p.heads) * p.rows + w) * kHeadDim)[lane] = lo;
+    if (lane == 0) p.factors[w] = fminf(f * (fabsf(p.scale) * kLog2e), 3e38f);
+  }
+}
+
+// ------------------------------------------------------------------ join
+
+// The partial results of row `row` of kv head h at node e: the first, and those of the
+// ranges behind.
+struct Partials {
+  int first, next, n;
+  __device__ __forceinline__ Partials(const TreeParams& p, int grid, int e, int h, int row) {
+    const int x = row - p.row0[e], z = x / kUnitRows, units = (p.n[e] + kUnitRows - 1) / kUnitRows, per = p.tiles[e] + p.cost;
+    const int begin = p.cum[e] + (h * units + z) * per;
+    const int g0 = range_of(begin + p.cost, grid, p.total), g1 = range_of(begin + per - 1, grid, p.total);
+    first = p.part0[e] + h * p.n[e] + x;
+    next = p.cont + g0 * kUnitRows + x - z * kUnitRows;
+    n = 1 + g1 - g0;
+  }
+  __device__ __forceinline__ int row(int k) const { return k == 0 ? first : next + k * kUnitRows; }
+};
+
+// CTA (x, h) joins `each` rows of kv head h, 8 / each warps a row, a lane per 8 dims,
+// in the order of nodes and ranges.
+__global__ void __launch_bounds__(256) paged_tree_join_kernel(const __grid_constant__ TreeParams p, int grid, int each) {
+  wait_for_last_kernel();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = 8 / each, h = blockIdx.y;
+  const int row = blockIdx.x * each + warp / share;
+  const bool live = row < p.rows;
+  __shared__ float part[8][kHeadDim + 2];
+  float m = kUnset, sum = 0.0f, o[8] = {};
+  int4 at = make_int4(-1, 0, 0, 0);
+  if (live) {
+    at = __ldcg(p.place + row);
+    for (int e = at.x; e >= 0; e = p.parent[e]) {
+      const Partials parts(p, grid, e, h, row);
+      for (int k = lane; k < parts.n; k += 32) m = fmaxf(m, __ldcg(&p.part_ml[parts.row(k)]).x);  // every lane a partial
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    int turn = warp % share;  // of this warp's next partial
+    for (int e = at.x; e >= 0; e = p.parent[e]) {
+      const Partials parts(p, grid, e, h, row);
+#pragma unroll 4
+      for (int k = turn; k < parts.n; k += share) {
+        const long long i = parts.row(k);
+        const float2 ml = __ldcg(&p.part_ml[i]);
+        const float4* v = reinterpret_cast<const float4*>(p.part_o + i * kHeadDim + lane * 8);
+        const float4 v0 = __ldcg(v), v1 = __ldcg(v + 1);
+        const float f = ex2_approx(ml.x - m);
+        sum = fmaf(f, ml.y, sum);
+        o[0] = fmaf(f, v0.x, o[0]), o[1] = fmaf(f, v0.y, o[1]), o[2] = fmaf(f, v0.z, o[2]), o[3] = fmaf(f, v0.w, o[3]);
+        o[4] = fmaf(f, v1.x, o[4]), o[5] = fmaf(f, v1.y, o[5]), o[6] = fmaf(f, v1.z, o[6]), o[7] = fmaf(f, v1.w, o[7]);
+      }
+      turn = (turn + share - parts.n % share) % share;
+    }
+  }
+  if (share > 1) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) part[warp][d * 32 + lane] = o[d];
+    if (lane == 0) part[warp][kHeadDim] = sum;
+    __syncthreads();
+    if (warp % share) return;
+    for (int w = warp + 1; w < warp + share; ++w) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] += part[w][d * 32 + lane];
+      sum += part[w][kHeadDim];
+    }
+  }
+  if (!live) return;
+  const long long to = static_cast<long long>(h) * p.rep * p.nq + at.z;
+  store_out8(p.out, p.out_f32, to * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
+}
+
+// ------------------------------------------------------------------ what is shared
+
+// A unit's beginning and end take about as long as so many tiles.
+constexpr int kUnitCost = 4;
+constexpr int kRangeCost = 2;  // and so many where the ranges are cut, see unit_cost
+
+struct Planner {
+  int rep, window, sinks, inner = 0;
+  // per entry, in the tree's order once it is built
+  int n = 0;
+  struct Entry {
+    const int32_t* row;  // its page ids
+    int pages, len, count, p_lo, p_hi, place, slot, lowest;
+  } e[IQ_MAX_BATCH];
+  // a node before the order of the entries, and with it of the rows, is known
+  struct Node {
+    int first, last, start, stop, parent;  // entries [first, last), tiles [start, stop)
+    Tiles tiles;
+  } node[kNodes];
+  int nodes = 0;
+
+  // The tiles of [start, stop) that some row of entries [a, b) sees.
+  Tiles seen(int a, int b, int start, int stop) const {
+    int lo = e[a].p_lo, hi = e[a].p_hi, len = e[a].len;
+    for (int i = a + 1; i < b; ++i) {
+      lo = std::min(lo, e[i].p_lo);
+      hi = std::max(hi, e[i].p_hi);
+      len = std::max(len, e[i].len);
+    }
+    Tiles t = tiles_of(len, lo, hi, 1, window, sinks);
+    const int end = std::min(t.n + t.skip, stop);
+    const int a1 = std::min(t.sinks, stop), b0 = std::max(t.sinks + t.skip, start);  // sinks' tiles [start, a1), others [b0, end)
+    const int near = std::max(a1 - start, 0), far = std::max(end - b0, 0);
+    t.sinks = near;
+    t.n = near + far;
+    t.base = near ? start : b0;
+    t.skip = near ? b0 - a1 : 0;
+    return t;
+  }
+  int row_units(int a, int b) const {
+    long long rows = 0;
+    for (int i = a; i < b; ++i) rows += static_cast<long long>(e[i].count) * rep;
+    return static_cast<int>((rows + kUnitRows - 1) / kUnitRows);
+  }
+  int add(int a, int b, int start, int stop, int parent, const Tiles& t) {
+    node[nodes] = {a, b, start, stop, parent, t};
+    return nodes++;
+  }
+  // Entries [a, b) hold the same first `page` pages; tiles before `start` are those of `parent` and above.
+  void split(int a, int b, int page, int start, int parent, int depth) {
+    std::sort(e + a, e + b, [&](const Entry& x, const Entry& y) {
+      const int i = x.pages > page ? x.row[page] : -1, j = y.pages > page ? y.row[page] : -1;
+      return i != j ? i < j : x.place < y.place;
+    });
+    for (int x = a, y; x < b; x = y) {
+      y = x + 1;
+      if (e[x].pages > page)
+        while (y < b && e[y].pages > page && e[y].row[page] == e[x].row[page]) ++y;
+      if (y - x == 1) {  // a leaf
+        const Tiles t = seen(x, y, start, (e[x].pages + 1) / 2);
+        e[x].lowest = t.n > 0 ? add(x, y, start, 0, parent, t) : parent;
+        continue;
+      }
+      int common = e[x].pages, most = e[x].pages;
+      for (int i = x + 1; i < y; ++i) {
+        const int32_t *u = e[x].row, *v = e[i].row;
+        const int32_t* end = std::mismatch(u + page, u + std::min(common, e[i].pages), v + page).first;
+        common = static_cast<int>(end - u);
+        most = std::max(most, e[i].pages);
+      }
+      const int stop = common == most ? (common + 1) / 2 : common / 2;
+      const Tiles t = seen(x, y, start, stop);
+      const bool once = depth < kDepth - 1 && inner < kInner &&
+                        static_cast<long long>(row_units(x, y)) * (t.n + kUnitCost) < static_cast<long long>(y - x) * t.n;
+      int under = parent;
+      if (once) {
+        ++inner;
+        under = add(x, y, start, stop, parent, t);
+      }
+      split(x, y, common, once ? stop : start, under, depth + (once ? 1 : 0));
+    }
+  }
+};
+
+// The rows of all nodes of one kv head are at most kDepth times the call's.
+size_t tree_bytes(size_t rows, size_t heads) {
+  const size_t parts = kDepth * heads * rows + static_cast<size_t>(num_sms()) * kUnitRows;
+  return parts * (kHeadDim * sizeof(float) + sizeof(float2)) + rows * sizeof(int4) + heads * rows * (2 * kHeadDim + sizeof(float));
+}
+// Where pages are shared among slots of more rows, their own products fill the tensor cores already.
+bool tree_rows(const iq_paged* c, int q_heads, int n_queries, int n_slots) {
+  const long long rows = static_cast<long long>(q_heads / c->kv_heads) * n_queries;
+  return rows > 0 && rows <= kUnitRows && n_slots > 1 && kDepth * rows * n_slots * c->kv_heads < (1LL << 30);
+}
+
+int check_shared(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots,
+                 int added, float scale, int causal, int window, int sinks, const void* out, int out_f32, const void* workspace,
+                 size_t workspace_bytes) {
+  const int st = check_attend(c, q, q_heads, n_queries, slots, counts, n_slots, added, scale, causal, window, sinks, out, out_f32, workspace,
+                              workspace_bytes);
+  if (st != IQ_OK || !tree_rows(c, q_heads, n_queries, n_slots)) return st;
+  if (workspace_bytes < tree_bytes(static_cast<size_t>(q_heads / c->kv_heads) * n_queries * n_slots, c->kv_heads))
+    return fail(IQ_ERR_WORKSPACE, "workspace missing or too small");
+  return IQ_OK;
+}
+
+// The attention by the tree of shared pages, where there is one; *done says whether.
+int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots,
+                float scale, int causal, int window, int sinks, void* out, int out_f32, void* workspace, iq_stream_t stream, bool* done) {
+  *done = false;
+  const int heads = c->kv_heads;
+  Planner t;
+  t.rep = q_heads / heads;
+  int longest = 0;
+  for (int i = 0; i < n_slots; ++i) longest = std::max(longest, c->lens[slot_of(slots, i)]);
+  if (window >= longest) window = sinks = 0;  // nothing is out of it, and positions less a window stay in 32 bits
+  t.window = window;
+  t.sinks = sinks;
+  for (int i = 0; i < n_slots; ++i) {
+    const int s = slot_of(slots, i), len = c->lens[s], count = counts ? counts[i] : n_queries;
+    if (len == 0 || count == 0) continue;
+    const int first = causal ? len - count : len - 1;
+    t.e[t.n++] = {c->table_host + static_cast<long long>(s) * c->max_pages, pages_for(len), len, count, first, len - 1, i, s, -1};
+  }
+  if (t.n < 2) return IQ_OK;
+  t.split(0, t.n, 0, 0, -1, 0);
+  if (t.inner == 0) return IQ_OK;
+
+  TreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  TreeCutParams cut;
+  std::memset(&cut, 0, sizeof(cut));
+  for (int i = 0; i < t.n; ++i) {
+    cut.entry[i] = static_cast<short>(t.e[i].place);
+    cut.lowest[i] = static_cast<short>(t.e[i].lowest);
+    cut.pos0[i] = t.e[i].p_lo;
+    cut.row0[i + 1] = cut.row0[i] + t.e[i].count * t.rep;
+  }
+  p.rows = cut.row0[t.n];
+  long long tiles = 0, parts = 0;
+  for (int k = 0; k < t.nodes; ++k) {
+    const Planner::Node& a = t.node[k];
+    const Planner::Entry& holder = t.e[a.first];
+    p.slot[k] = static_cast<short>(holder.slot);
+    p.parent[k] = static_cast<short>(a.parent);
+    p.end_page[k] = holder.pages - 1;
+    p.row0[k] = cut.row0[a.first];
+    p.n[k] = cut.row0[a.last] - p.row0[k];
+    p.part0[k] = static_cast<int>(parts);
+    p.tiles[k] = a.tiles.n;
+    p.base[k] = a.tiles.base;
+    p.sink_tiles[k] = a.tiles.sinks;
+    p.skip[k] = a.tiles.skip;
+    p.p_lo[k] = a.tiles.p_lo;
+    p.p_hi[k] = a.tiles.p_hi;
+    parts += static_cast<long long>(heads) * p.n[k];
+    tiles += static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows) * a.tiles.n;
+  }
+  const int grid = static_cast<int>(std::min<long long>(num_sms(), tiles));
+  p.entries = t.nodes;
+  p.cost = tiles >= 8ll * grid ? kRangeCost : 0;
+  long long total = 0;
+  for (int k = 0; k < t.nodes; ++k) {
+    p.cum[k] = static_cast<int>(total);
+    total += static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows) * (p.tiles[k] + p.cost);
+    if (total >= (1LL << 31)) return IQ_OK;
+  }
+  p.cum[t.nodes] = p.total = static_cast<int>(total);
+  p.cont = static_cast<int>(parts);
+  parts += static_cast<long long>(grid) * kUnitRows;
+
+  const long long pool_rows = static_cast<long long>(c->pages) * heads * kPage, cut_rows = static_cast<long long>(heads) * p.rows;
+  p.part_o = static_cast<float*>(workspace);
+  p.cut = reinterpret_cast<uint8_t*>(p.part_o + parts * kHeadDim);
+  cut.place = reinterpret_cast<int4*>(p.cut + cut_rows * 2 * kHeadDim);
+  p.place = cut.place;
+  p.part_ml = reinterpret_cast<float2*>(cut.place + p.rows);
+  p.factors = reinterpret_cast<float*>(p.part_ml + parts);
+  if (!code_map(&p.k_map, c->k_codes, pool_rows) || !code_map(&p.v_map, c->v_codes, pool_rows) ||
+      !code_map(&p.q_map, p.cut, 2 * cut_rows, kUnitRows))
+    return fail(IQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  p.k_scales = c->k_scales;
+  p.v_scales = c->v_scales;
+  p.table = c->table;
+  p.status = c->status;
+  p.out = out;
+  p.out_f32 = out_f32;
+  p.heads = cut.heads = heads;
+  p.rep = cut.rep = t.rep;
+  p.nq = cut.nq = n_queries;
+  p.pages = c->pages;
+  p.max_pages = c->max_pages;
+  p.window = window;
+  p.sinks = sinks;
+  p.stall = stall_next ? 1 : 0;
+  stall_next = false;
+  cut.q = static_cast<const uint16_t*>(q);
+  cut.cut = p.cut;
+  cut.factors = p.factors;
+  cut.rows = p.rows;
+  cut.entries = t.n;
+  cut.causal = causal;
+  cut.scale = scale;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int st = store_zeros(c, q_heads, n_queries, slots, counts, n_slots, out, out_f32, stream);
+  if (st != IQ_OK) return st;
+  void* cut_args[] = {&cut};
+  cudaError_t err = launch_after(reinterpret_cast<const void*>(&paged_tree_cut_kernel), dim3((p.rows + 31) / 32, heads), 256, 0, cs, cut_args);
+  if (err == cudaSuccess) err = launch_tree(p, grid, cs);
+  if (err == cudaSuccess) {
+    int ranges = grid, each = cut_rows >= 4096 ? 8 : 1;
+    void* args[] = {&p, &ranges, &each};
+    err = launch_after(reinterpret_cast<const void*>(&paged_tree_join_kernel), dim3((p.rows + each - 1) / each, heads), 256, 0, cs, args);
+  }
+  if (err != cudaSuccess) return cuda_fail(err, "paged attention of shared pages");
+  launched_outputs(stream, {out, static_cast<size_t>(n_slots) * q_heads * n_queries * kHeadDim * (out_f32 ? 4 : 2)});
+  *done = true;
+  return IQ_OK;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace iq
+
+using namespace iq;
+using namespace iq::paged;
+
+extern "C" {
+
+int iq_paged_attend_shared_workspace(const iq_paged* c, int q_heads, int n_queries, int n_slots, size_t* bytes) {
+  const int st = iq_paged_attend_workspace(c, q_heads, n_queries, n_slots, bytes);
+  if (st == IQ_OK && tree_rows(c, q_heads, n_queries, n_slots))
+    *bytes = std::max(*bytes, tree_bytes(static_cast<size_t>(q_heads / c->kv_heads) * n_queries * n_slots, c->kv_heads));
+  return st;
+}
+
+int iq_paged_attend_shared(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts,
+                           int n_slots, float scale, int causal, int window, int sinks, void* out, int out_f32, void* workspace,
+                           size_t workspace_bytes, iq_stream_t stream) {
+  const int st = check_shared(c, q, q_heads, n_queries, slots, counts, n_slots, 0, scale, causal, window, sinks, out, out_f32, workspace,
+                              workspace_bytes);
+  if (st != IQ_OK || n_slots == 0 || n_queries == 0) return st;
+  if (tree_rows(c, q_heads, n_queries, n_slots)) {
+    bool done = false;
+    const int tree = attend_tree(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32, workspace,
+                                 stream, &done);
+    if (tree != IQ_OK || done) return tree;
+  }
+  return iq_paged_attend(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32, workspace,
+                         workspace_bytes, stream);
+}
+
+int iq_paged_append_attend_shared(iq_paged* c, const void* keys, const void* values, int n, const void* q, int q_heads, int n_queries,
+                                  const int32_t* slots, const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
+                                  void* out, int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream) {
+  int st = check_append(c, keys, values, n, slots, counts, n_slots);
+  if (st != IQ_OK) return st;
+  if (counts && n != n_queries) return fail(IQ_ERR_INVALID_ARG, "counts need as many rows as queries");
+  st = check_shared(c, q, q_heads, n_queries, slots, counts, n_slots, n, scale, causal, window, sinks, out, out_f32, workspace,
+                    workspace_bytes);
+  if (st != IQ_OK) return st;
+  st = iq_paged_append(c, keys, values, n, slots, counts, n_slots, stream);
+  if (st != IQ_OK) return st;
+  return iq_paged_attend_shared(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32, workspace,
+                                workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -203,15 +203,15 @@ class IQPagedCache:
             raise ValueError("out must not overlap q")
         return out
 
-    def _workspace(self, q_heads: int, rows: int, entries: int, stream):
+    def _workspace(self, q_heads: int, rows: int, entries: int, stream, shared: bool):
         """Scratch for a call on `stream`: one per stream, kept, as work on one stream is in order
         (so the lock is held from here until the call has made its launches); for a captured
         call its own, as graphs captured on one stream may run at once."""
-        key = (q_heads, rows, entries)
+        key = (q_heads, rows, entries, shared)
         need = self._need.get(key)
         if need is None:
             c = ctypes.c_size_t()
-            self._run(self._lib.iq_paged_attend_workspace, self._d, q_heads, rows, entries, ctypes.byref(c))
+            self._run(self._lib.iq_paged_attend_shared_workspace if shared else self._lib.iq_paged_attend_workspace, self._d, q_heads, rows, entries, ctypes.byref(c))
             if len(self._need) > 256:
                 self._need.clear()
             need = self._need[key] = c.value
@@ -328,7 +328,8 @@ class IQPagedCache:
 
     # ---------------------------------------------------------------- attention
     def attend(self, q: torch.Tensor, causal: bool = True, scale: float | None = None, window: int = 0,
-               sinks: int = 0, slots=None, counts=None, out: torch.Tensor | None = None, out_dtype=None) -> torch.Tensor:
+               sinks: int = 0, slots=None, counts=None, out: torch.Tensor | None = None, out_dtype=None,
+               shared: bool = False) -> torch.Tensor:
         """Attention of q [entries, Hq, L, D] (bf16) over the slots' pages; returns [entries, Hq, L, D].
 
         The L queries stand at each slot's last L positions (its last counts[i],
@@ -337,6 +338,8 @@ class IQPagedCache:
         up to its own position; `window` > 0: only the last `window` of them, and
         the slot's first `sinks` tokens.  A query that sees nothing gets 0.
         Softmax weights are held to 2^-8 of each, sums in float32, whatever out_dtype is.
+        shared: read pages that several of the slots hold (forked paths, a common prompt) once for all of
+        them; a call captured so replays with the sharing it was captured with.
         """
         q = self._tensor(q, "q")
         E, Hq, L, D = q.shape
@@ -345,15 +348,15 @@ class IQPagedCache:
         window, sinks = _span(window, sinks)
         stream = self._queue()
         with self._lock:
-            ws = self._workspace(Hq, L, E, stream)
-            self._run(self._lib.iq_paged_attend, self._d, q.data_ptr(), Hq, L, _at(slots), _at(counts), E,
+            ws = self._workspace(Hq, L, E, stream, shared)
+            self._run(self._lib.iq_paged_attend_shared if shared else self._lib.iq_paged_attend, self._d, q.data_ptr(), Hq, L, _at(slots), _at(counts), E,
                       self._scale if scale is None else scale, 1 if causal else 0, window, sinks, out.data_ptr(),
                       1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
         return out
 
     def append_attend(self, keys: torch.Tensor, values: torch.Tensor, q: torch.Tensor, causal: bool = True,
                       scale: float | None = None, window: int = 0, sinks: int = 0, slots=None, counts=None,
-                      out: torch.Tensor | None = None, out_dtype=None) -> torch.Tensor:
+                      out: torch.Tensor | None = None, out_dtype=None, shared: bool = False) -> torch.Tensor:
         """`append(keys, values)` then `attend(q)` of the same entries in one library call: the step of
         a decode loop or one chunk of a prompt."""
         keys, values = self._rows(keys, values)
@@ -366,8 +369,8 @@ class IQPagedCache:
         window, sinks = _span(window, sinks)
         stream = self._queue()
         with self._lock:
-            ws = self._workspace(Hq, L, E, stream)
-            self._run(self._lib.iq_paged_append_attend, self._d, keys.data_ptr(), values.data_ptr(), keys.shape[2], q.data_ptr(), Hq, L,
+            ws = self._workspace(Hq, L, E, stream, shared)
+            self._run(self._lib.iq_paged_append_attend_shared if shared else self._lib.iq_paged_append_attend, self._d, keys.data_ptr(), values.data_ptr(), keys.shape[2], q.data_ptr(), Hq, L,
                       _at(slots), _at(counts), E, self._scale if scale is None else scale, 1 if causal else 0, window, sinks,
                       out.data_ptr(), 1 if out.dtype is torch.float32 else 0, ws.data_ptr(), ws.numel(), stream)
         return out

@@ -1,0 +1,266 @@
+"""Attention of slots that share pages, each shared page multiplied once: against the oracle, within the bounds of the
+attention that reads every slot's pages apart."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged
+from test_gpu_paged import bounds, f64, pair, put, rows
+
+pytestmark = pytest.mark.gpu
+
+
+def check(c, o, q, out_dtype=torch.float32, slots=None, counts=None, scale=1 / 16, **kw):
+    out = c.attend(q.cuda(), scale=scale, slots=slots, counts=counts, out_dtype=out_dtype, shared=True, **kw)
+    assert out.dtype == out_dtype and out.shape == q.shape
+    res = paged.attend(o, f64(q), scale, slots, counts, **kw)
+    got, live = f64(out), ~np.isnan(res[0])
+    tol, d = bounds(res, out_dtype == torch.float32), np.abs(got - res[0])
+    assert np.isfinite(got).all()
+    assert (d[live] <= tol[live]).all(), (d[live] / tol[live]).max()
+    if counts is not None:
+        assert (got[~live] == 0).all()
+    score = np.linalg.norm((2 * (2.0**-17 + 2.0**-16) * res[3] * res[1])[live])
+    assert np.linalg.norm(d[live]) <= 2.0**-8 * np.linalg.norm(res[0][live]) + score + 1e-30
+    assert c.device_status() == 0
+    return out
+
+
+def tree(H, common, branch, tails, groups=1, seed=1, outliers=True):
+    """`groups` branches of one prompt, and len(tails) paths of each (the tails' lengths)."""
+    paths = len(tails) // groups
+    slots = len(tails)
+    c, o = pair(slots, H, (common + 63) // 64 + 1 + groups * ((branch + 127) // 64) + sum(2 + t // 64 for t in tails), common + branch + max(tails) + 1)
+    put(c, o, rows(seed, 1, H, common, outliers), rows(seed + 1, 1, H, common), [0])
+    leaders = list(range(0, slots, paths))
+    for x in (c, o):
+        x.fork([0] * (groups - 1), leaders[1:])
+    if branch:
+        put(c, o, rows(seed + 2, groups, H, branch, outliers), rows(seed + 3, groups, H, branch), leaders)
+    others = [s for s in range(slots) if s not in leaders]
+    for x in (c, o):
+        x.fork([s - s % paths for s in others], others)
+    if max(tails):
+        put(c, o, rows(seed + 4, slots, H, max(tails), outliers), rows(seed + 5, slots, H, max(tails)), list(range(slots)), list(tails))
+    return c, o
+
+
+@pytest.mark.parametrize("H,Hq,n", [(1, 1, 1), (2, 16, 1), (2, 6, 3), (4, 4, 1), (1, 64, 2), (1, 5, 25), (3, 24, 4)])
+@pytest.mark.parametrize("paths,common", [(2, 1024), (4, 513), (33, 320), (17, 2000)])
+def test_paths_of_one_prompt(H, Hq, n, paths, common):
+    c, o = tree(H, common, 0, [1 + (37 * b) % 150 + n for b in range(paths)])
+    check(c, o, rows(9, paths, Hq, n))
+
+
+@pytest.mark.parametrize("common,branch,tail,groups,paths", [(640, 300, 70, 3, 5), (64, 1000, 1, 2, 9), (1, 800, 130, 4, 3), (129, 127, 129, 5, 4), (2049, 65, 63, 2, 20)])
+@pytest.mark.parametrize("n", [1, 4])
+def test_branches_of_a_prompt(common, branch, tail, groups, paths, n):
+    c, o = tree(2, common, branch, [tail + (11 * b) % 9 + n for b in range(groups * paths)], groups)
+    check(c, o, rows(9, groups * paths, 12, n), torch.bfloat16)
+    check(c, o, rows(10, groups * paths, 12, n))
+
+
+@pytest.mark.parametrize("common", [1, 63, 64, 127, 128, 191, 700, 1000])
+@pytest.mark.parametrize("n", [1, 5])
+def test_forks_that_nobody_has_appended_to(common, n):
+    """The last, partly full page is shared too; of several queries only the last see all of it, some of one token's none."""
+    c, o = tree(2, common, 0, [0] * 6)
+    check(c, o, rows(9, 6, 4, n))
+
+
+def test_slots_trimmed_inside_a_shared_page():
+    c, o = tree(2, 1000, 0, [0] * 9)
+    for x in (c, o):
+        x.trim([0, 1, 30, 41, 100, 500, 999, 1000, 3], list(range(9)))
+    q = rows(9, 9, 8, 2)
+    check(c, o, q)
+    put(c, o, rows(5, 9, 2, 2), rows(6, 9, 2, 2))
+    check(c, o, q)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 0), (100, 7), (128, 128), (700, 1), (900, 300), (5000, 3)])
+@pytest.mark.parametrize("n", [1, 4])
+def test_windows(window, sinks, n):
+    c, o = tree(2, 1100, 500, [n + (53 * b) % 400 for b in range(12)], 2)
+    check(c, o, rows(9, 12, 8, n), window=window, sinks=sinks)
+
+
+def test_queries_that_see_every_key():
+    c, o = tree(2, 700, 200, [1 + (53 * b) % 400 for b in range(12)], 2)
+    check(c, o, rows(9, 12, 8, 3), causal=False)
+
+
+def test_lists_of_slots_counts_and_empty_slots():
+    c, o = tree(2, 600, 100, [3 + (53 * b) % 200 for b in range(12)], 2)
+    for x in (c, o):
+        x.free([4, 7])
+        x.trim([10**6], [5])
+    put(c, o, rows(5, 1, 2, 2), rows(6, 1, 2, 2), [5])  # a short slot of its own: two tokens, more queries than these
+    slots = [11, 4, 0, 5, 3, 3, 7, 8, 2, 0, 9]
+    q = rows(9, len(slots), 8, 5)
+    check(c, o, q, slots=slots)
+    counts = [5, 5, 0, 4, 1, 5, 0, 2, 3, 5, 1]
+    check(c, o, q, slots=slots, counts=counts)
+    out = torch.full((len(slots), 8, 5, 256), 7.0, device="cuda")
+    c.attend(q.cuda(), slots=slots, counts=counts, out=out, shared=True)
+    for i, n in enumerate(counts):
+        assert (out[i, :, n:] == 7).all() and not (out[i, :, :n] == 7).any()
+
+
+def test_deep_and_wide_trees():
+    """More levels than are told apart, and more branches than there is room for."""
+    c, o = pair(40, 1, 700, 3000)
+    put(c, o, rows(1, 1, 1, 300), rows(2, 1, 1, 300), [0])
+    live = 1
+    for level in range(5):  # every slot is forked, then goes on by itself
+        for x in (c, o):
+            x.fork(list(range(live)), list(range(live, 2 * live)))
+        live *= 2
+        put(c, o, rows(3 + level, live, 1, 270), rows(20 + level, live, 1, 270), list(range(live)))
+    check(c, o, rows(9, 32, 4, 1))
+    check(c, o, rows(9, 40, 4, 2))
+    c, o = pair(240, 1, 1200, 700)
+    firsts = list(range(0, 240, 3))
+    put(c, o, rows(1, 80, 1, 640), rows(2, 80, 1, 640), firsts)
+    for x in (c, o):
+        x.fork([s for s in firsts for _ in (0, 1)], [s + i for s in firsts for i in (1, 2)])
+    put(c, o, rows(3, 240, 1, 3), rows(4, 240, 1, 3))
+    check(c, o, rows(9, 240, 8, 1))
+
+
+def test_many_slots_and_rows():
+    c, o = tree(2, 200, 0, [1 + b % 3 for b in range(256)], outliers=False)
+    check(c, o, rows(9, 256, 16, 1))
+    check(c, o, rows(9, 256, 2, 3), torch.bfloat16)
+
+
+@pytest.mark.parametrize("scale", [-1 / 16, 0.0, 2.0, 1e-6])
+def test_scales(scale):
+    c, o = tree(2, 700, 0, [1 + (53 * b) % 200 for b in range(8)])
+    check(c, o, rows(9, 8, 8, 1), scale=scale)
+
+
+def test_one_heavy_key_among_many():
+    """What many small weights leave next to a heavy key of the shared part, and of a path's own."""
+    for heavy in (5, 1290):
+        c, o = pair(6, 1, 140, 1400)
+        k, v = rows(1, 1, 1, 1280), rows(2, 1, 1, 1280)
+        k2, v2 = rows(3, 6, 1, 40), rows(4, 6, 1, 40)
+        k[..., 0] = k2[..., 0] = 0
+        (k if heavy < 1280 else k2)[:, :, heavy % 1280, 0] = 90
+        (v if heavy < 1280 else v2)[:, :, heavy % 1280] = 0
+        put(c, o, k, v, [0])
+        for x in (c, o):
+            x.fork([0] * 5, [1, 2, 3, 4, 5])
+        put(c, o, k2, v2)
+        q = 0.05 * rows(9, 6, 4, 1)
+        q[..., 0] = 1.3
+        check(c, o, q)
+
+
+def test_same_results_every_time_and_on_every_path():
+    c, _ = tree(2, 3000, 700, [1 + (53 * b) % 200 for b in range(20)], 4)
+    q = rows(9, 20, 16, 1).cuda()
+    first = c.attend(q, shared=True)
+    for _ in range(10):
+        assert torch.equal(c.attend(q, shared=True), first)
+    many = rows(9, 20, 16, 17).cuda()  # 136 rows of a slot: the ordinary kernels
+    assert torch.equal(c.attend(many, shared=True), c.attend(many))
+    alone = rows(9, 1, 16, 1).cuda()
+    assert torch.equal(c.attend(alone, slots=[3], shared=True), c.attend(alone, slots=[3]))
+    small = c.compact()
+    assert torch.equal(small.attend(q, shared=True), first)
+
+
+def test_append_attend_as_two_calls():
+    from rotated_bit_quantized_gb300 import _abi
+    a, _ = tree(2, 900, 0, [5 + b for b in range(7)])
+    b, _ = tree(2, 900, 0, [5 + b for b in range(7)])
+    k, v, q = rows(5, 7, 2, 3).cuda(), rows(6, 7, 2, 3).cuda(), rows(9, 7, 8, 3).cuda()
+    counts = [3, 0, 1, 2, 3, 3, 1]
+    x = a.append_attend(k, v, q, counts=counts, shared=True, window=600, sinks=2)
+    b.append(k, v, counts=counts)
+    assert torch.equal(x, b.attend(q, counts=counts, shared=True, window=600, sinks=2))
+    before = a.lens.tolist()
+    with pytest.raises(_abi.IQError):
+        a.append_attend(k, v, q, shared=True, sinks=1)
+    assert a.lens.tolist() == before
+
+
+def test_streams_and_graphs():
+    c, o = tree(2, 1500, 0, [9 + b for b in range(9)])
+    q = rows(9, 9, 8, 1).cuda()
+    want = c.attend(q, shared=True)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs += [c.attend(q, shared=True) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in outs)
+    graphs = []
+    for s in streams[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            graphs.append((g, c.attend(q, shared=True)))
+    q2 = rows(19, 9, 8, 1).cuda()
+    want2 = c.attend(q2, shared=True)
+    torch.cuda.synchronize()
+    q.copy_(q2)
+    torch.cuda.synchronize()
+    for s, (g, _) in zip(streams, graphs):  # two at once
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want2) for _, x in graphs)
+
+
+def test_waits_run_out():
+    from rotated_bit_quantized_gb300 import _abi
+    c, o = tree(1, 1000, 0, [5] * 4)
+    q = rows(9, 4, 4, 1)
+    assert _abi.lib().iq_paged_debug_stall() == 0
+    c.attend(q.cuda(), shared=True)
+    assert c.device_status() & 0xB
+    check(c, o, q)
+
+
+def test_a_bad_page_is_told_and_read_as_another():
+    from rotated_bit_quantized_gb300 import _abi
+    c, o = tree(1, 1000, 0, [5] * 4)
+    q = rows(9, 4, 4, 1).cuda()
+    c.attend(q, shared=True)
+    torch.cuda.synchronize()
+    keep = c.table.clone()
+    c.table[:, 3] = 10**6
+    c.attend(q, shared=True)
+    assert c.device_status() == _abi.IQ_STATUS_BAD_PAGE
+    c.table.copy_(keep)
+    check(c, o, rows(9, 4, 4, 1))
+
+
+def test_a_decode_step_of_all_of_it():
+    """Projections of forked paths: normed, turned and appended, then attended with the shared pages read once."""
+    from rotated_bit_quantized_gb300 import IQPagedCache, IQRotary
+    g = torch.Generator().manual_seed(1)
+    rot = IQRotary(64, base=1e6, q_norm=0.1 * torch.randn(256, generator=g), k_norm=0.1 * torch.randn(256, generator=g), norm_offset=1.0)
+    a, b = IQPagedCache(9, 2, 60), IQPagedCache(9, 2, 60)
+    for c in (a, b):
+        x = rows(1, 1, 1, 700 * 12).view(1, 700, 12, 256).transpose(1, 2).cuda()
+        c.append_rotary(None, x[:, 8:10], x[:, 10:], rot, slots=[0])
+        c.fork([0] * 8, range(1, 9))
+    for step in range(4):
+        x = rows(10 + step, 1, 1, 8 * 12).view(8, 1, 12, 256).transpose(1, 2).cuda()
+        q = a.append_rotary(x[:, :8], x[:, 8:10], x[:, 10:], rot, slots=range(1, 9))
+        one = a.attend(q, slots=range(1, 9), shared=True, out_dtype=torch.float32)
+        q2, k2 = rot.apply(x[:, :8], x[:, 8:10], positions=700 + step)
+        assert torch.equal(q, q2)
+        b.append(k2, x[:, 10:].contiguous(), slots=range(1, 9))
+        two = b.attend(q2, slots=range(1, 9), out_dtype=torch.float32)
+        # keys rounded once and twice differ by a code's step (2^-3) here and there, weights by 2^-8 twice
+        assert (one - two).norm() <= 0.02 * two.norm()
+        for i, p in enumerate(a.page_ids(1)[: 700 // 64]):
+            assert (b.page_ids(1)[i] == p)
+    assert a.device_status() == 0 and b.device_status() == 0
