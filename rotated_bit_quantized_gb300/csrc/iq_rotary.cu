@@ -9,9 +9,12 @@
 // tell (at 2^20, 2^-4 of a radian is lost), so a frequency is held as its turns per
 // position modulo 1 in 64 bits of fixed point: the product with a position, modulo
 // 2^64, is the angle modulo a turn, off by at most position * 2^-64 and what the
-// frequency itself was off.  One integer product; no table in memory, no fp64.  The
-// eighth of a turn around the nearest quarter goes to sincospif, the quarter swaps
-// and negates.
+// frequency itself was off.  One integer product; no table in memory, no fp64.
+//
+// Rows.  Eight lanes hold a row, 32 elements each in pieces of 16 bytes, 128 bytes apart:
+// what a row costs besides its elements (its address, the norm's sum over lanes and root)
+// a warp then does for four rows at once.  With a row per warp that was most of 210
+// instructions a row, and 16 x 2048 rows of 18 heads took 202 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,17 +26,6 @@
 namespace iq {
 namespace paged {
 namespace {
-
-// Where the pairs of a lane's dims are.  Lane l of a row's warp holds dims 4l .. 4l+3
-// and 128 + 4l .. 128 + 4l+3: then halves that are 128 apart meet in one lane, and a
-// row's cosines are read from shared memory without conflicts.
-enum Layout {
-  kNone,    // nothing turns
-  kPairs,   // dims 2i and 2i + 1
-  kNear,    // dims i and i + pairs, pairs <= 64: all among the first 128 dims
-  kAcross,  // pairs == 128
-  kFar      // between
-};
 
 struct Turn {
   const unsigned long long* turns;
@@ -47,59 +39,75 @@ struct Rows {
   long long entry, head, row;  // strides in bytes
 };
 
+// Lane l of eight holds V elements of each of C pieces: c * 8V + V * l + i.
 template <bool F32>
-struct Raw;
-template <>
-struct Raw<false> {
-  static constexpr int kBytes = 2;
-  uint2 x[2];
-  __device__ __forceinline__ void load(const uint8_t* row, int lane) {
-    x[0] = __ldcs(reinterpret_cast<const uint2*>(row + lane * 8));
-    x[1] = __ldcs(reinterpret_cast<const uint2*>(row + 256 + lane * 8));
-  }
-  __device__ __forceinline__ void get(float (&y)[8]) const {
+struct Raw {
+  static constexpr int V = F32 ? 4 : 8, C = 32 / V, kRowBytes = kHeadDim * (F32 ? 4 : 2);
+  uint4 x[C];
+  __device__ __forceinline__ void load(const uint8_t* row, int l) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      y[4 * g] = __uint_as_float(x[g].x << 16);
-      y[4 * g + 1] = __uint_as_float(x[g].x & 0xFFFF0000u);
-      y[4 * g + 2] = __uint_as_float(x[g].y << 16);
-      y[4 * g + 3] = __uint_as_float(x[g].y & 0xFFFF0000u);
+    for (int c = 0; c < C; ++c) x[c] = __ldcs(reinterpret_cast<const uint4*>(row + c * 128 + l * 16));
+  }
+  __device__ __forceinline__ void get(float (&y)[32]) const {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) {
+          y[4 * c + i] = __uint_as_float(w[i]);
+        } else {
+          y[8 * c + 2 * i] = __uint_as_float(w[i] << 16);
+          y[8 * c + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
     }
   }
-  static __device__ __forceinline__ void store(uint8_t* row, int lane, const float (&y)[8]) {
+  static __device__ __forceinline__ void store(uint8_t* row, int l, const float (&y)[32]) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      uint2 o;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(y[4 * g + 1]), "f"(y[4 * g]));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(y[4 * g + 3]), "f"(y[4 * g + 2]));
-      *reinterpret_cast<uint2*>(row + 256 * g + lane * 8) = o;
+    for (int c = 0; c < C; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) w[i] = __float_as_uint(y[4 * c + i]);
+        else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(y[8 * c + 2 * i + 1]), "f"(y[8 * c + 2 * i]));
+      }
+      *reinterpret_cast<uint4*>(row + c * 128 + l * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  }
-};
-template <>
-struct Raw<true> {
-  static constexpr int kBytes = 4;
-  float4 x[2];
-  __device__ __forceinline__ void load(const uint8_t* row, int lane) {
-    x[0] = __ldcs(reinterpret_cast<const float4*>(row + lane * 16));
-    x[1] = __ldcs(reinterpret_cast<const float4*>(row + 512 + lane * 16));
-  }
-  __device__ __forceinline__ void get(float (&y)[8]) const {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) y[4 * g] = x[g].x, y[4 * g + 1] = x[g].y, y[4 * g + 2] = x[g].z, y[4 * g + 3] = x[g].w;
-  }
-  static __device__ __forceinline__ void store(uint8_t* row, int lane, const float (&y)[8]) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) *reinterpret_cast<float4*>(row + 512 * g + lane * 16) = make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]);
   }
 };
 
-// Cosine and sine of an angle of `a` / 2^32 turns.
+// Where the pairs of a lane's elements are.  With pairs = 8V * K + V * shift:
+enum Layout {
+  kNone,   // nothing turns
+  kPairs,  // elements 2i and 2i + 1
+  kHere,   // halves, shift 0: K pieces on, in the same lane
+  kSwap,   // halves, K = 0, shift 4: the same piece of the lane four on
+  kShift   // halves, any other: K pieces on, or one more, of the lane `shift` on
+};
+
+// Cosine and sine, times the amplitude, of an angle of a / 2^32 turns.  The nearest
+// quarter is taken off, and of what is left, t = h + l with |t| <= pi / 4 and l below half
+// a step of h, Taylor's series: what follows their first terms is below 2^-3 of them,
+// so the results are a half and some hundredths of a step off at most (codes are rounded
+// from what they turn: the nearer, the fewer land on the wrong side of a border).
 __device__ __forceinline__ float2 unit_at(unsigned a, float amplitude) {
   const unsigned quarter = (a + 0x20000000u) >> 30;
-  const int rest = static_cast<int>(a - (quarter << 30));  // an eighth of a turn at most
-  float s, c;
-  sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c);
+  const int rest = static_cast<int>(a - (quarter << 30));
+  constexpr float kHi = 0x1.921fb6p-30f, kLo = -0x1.777a5cp-55f;  // 2 pi / 2^32
+  const float u = static_cast<float>(rest), v = static_cast<float>(rest - static_cast<int>(u));
+  const float h = u * kHi, l = fmaf(u, kHi, -h) + fmaf(u, kLo, v * kHi);
+  const float h2 = h * h, rounded = fmaf(h, h, -h2);  // h^2 = h2 + rounded
+  float p = fmaf(h2, 1.0f / 362880, -1.0f / 5040);
+  p = fmaf(h2, p, 1.0f / 120);
+  p = fmaf(h2, p, -1.0f / 6);
+  const float s1 = fmaf(h * h2, p, l * fmaf(h2, -0.5f, 1.0f));  // sin t - h
+  float q = fmaf(h2, -1.0f / 3628800, 1.0f / 40320);
+  q = fmaf(h2, q, -1.0f / 720);
+  q = fmaf(h2, q, 1.0f / 24);
+  const float c0 = fmaf(h2, -0.5f, 1.0f), c1 = fmaf(h2, -0.5f, 1.0f - c0);  // 1 - h2 / 2 = c0 + c1
+  const float c2 = c1 + fmaf(h2 * h2, q, -fmaf(0.5f, rounded, l * h));      // cos t - c0
+  float s = fmaf(amplitude, h, amplitude * s1), c = fmaf(amplitude, c0, amplitude * c2);
   if (quarter & 1) {
     const float t = c;
     c = -s;
@@ -109,7 +117,7 @@ __device__ __forceinline__ float2 unit_at(unsigned a, float amplitude) {
     c = -c;
     s = -s;
   }
-  return make_float2(c * amplitude, s * amplitude);
+  return make_float2(c, s);
 }
 // Row r of the table: the cosines of its pairs, then their sines.
 template <typename Position>
@@ -130,103 +138,131 @@ __device__ __forceinline__ void fill_table(const Turn& t, float* table, int rows
   }
 }
 
-// (a c - b s, a s + b c)
-__device__ __forceinline__ void spin(float& a, float& b, float c, float s) {
-  const float x = fmaf(a, c, -(b * s));
-  b = fmaf(a, s, b * c);
-  a = x;
+// a c - b s, or a c + b s.  EXACT: off by its own rounding alone, the first product's
+// is made good (for float32 results and codes, see unit_at).
+template <bool EXACT>
+__device__ __forceinline__ float less(float a, float c, float b, float s) {
+  const float t = b * s, x = fmaf(a, c, -t);
+  if constexpr (EXACT) return x - fmaf(b, s, -t);
+  return x;
 }
-// a c + b s, with the sine's sign given by the half that `a` is in
-__device__ __forceinline__ float spun(float a, float b, float c, float s, bool upper) { return fmaf(a, c, upper ? b * s : -(b * s)); }
 
-// A row's vector, turned.  row: its cosines, then its sines.
-template <int LAYOUT>
-__device__ __forceinline__ void turn_row(float (&x)[8], const float* row, int pairs, int lane) {
+// A row's vector, turned (a whole warp, four rows).  row: its cosines, then its sines.
+template <int LAYOUT, int K, bool F32, bool EXACT>
+__device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int pairs, int l) {
+  constexpr int V = Raw<F32>::V, C = Raw<F32>::C;
   if constexpr (LAYOUT == kPairs) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int j = 64 * g + 2 * lane;
+    for (int c = 0; c < C; ++c) {
+      const int j = (c * 8 * V + V * l) / 2;
       if (j >= pairs) continue;
-      const float2 c = *reinterpret_cast<const float2*>(row + j), s = *reinterpret_cast<const float2*>(row + pairs + j);
-      spin(x[4 * g], x[4 * g + 1], c.x, s.x);
-      spin(x[4 * g + 2], x[4 * g + 3], c.y, s.y);
+      float co[V / 2], si[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; i += 2) {
+        *reinterpret_cast<float2*>(co + i) = *reinterpret_cast<const float2*>(row + j + i);
+        *reinterpret_cast<float2*>(si + i) = *reinterpret_cast<const float2*>(row + pairs + j + i);
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float a = x[V * c + 2 * i], b = x[V * c + 2 * i + 1];
+        x[V * c + 2 * i] = less<EXACT>(a, co[i], b, si[i]);
+        x[V * c + 2 * i + 1] = less<EXACT>(a, si[i], -b, co[i]);
+      }
     }
-  } else if constexpr (LAYOUT == kAcross) {
-    const float4 c = *reinterpret_cast<const float4*>(row + 4 * lane), s = *reinterpret_cast<const float4*>(row + 128 + 4 * lane);
-    spin(x[0], x[4], c.x, s.x);
-    spin(x[1], x[5], c.y, s.y);
-    spin(x[2], x[6], c.z, s.z);
-    spin(x[3], x[7], c.w, s.w);
-  } else if constexpr (LAYOUT == kNear || LAYOUT == kFar) {
-    constexpr int kParts = LAYOUT == kNear ? 1 : 2;  // of 128 dims
-    float y[8];
+  } else if constexpr (LAYOUT == kHere) {
 #pragma unroll
-    for (int g = 0; g < kParts; ++g) {
-      const int d = 128 * g + 4 * lane;
-      const bool upper = d >= pairs;
-      const int other = upper ? d - pairs : d + pairs;  // (beyond 2 pairs: unused)
-      float b[4];
+    for (int c = 0; c < K; ++c) {
+      const float* at = row + c * 8 * V + V * l;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        b[i] = __shfl_sync(0xFFFFFFFFu, x[i], other >> 2);
-        if constexpr (LAYOUT == kFar) {
-          const float far = __shfl_sync(0xFFFFFFFFu, x[4 + i], other >> 2);
-          if (other >= 128) b[i] = far;
+      for (int i = 0; i < V; i += 4) {
+        const float4 co = *reinterpret_cast<const float4*>(at + i), si = *reinterpret_cast<const float4*>(at + pairs + i);
+        const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = x[V * c + i + k], b = x[V * (c + K) + i + k];
+          x[V * c + i + k] = less<EXACT>(a, cs[k], b, ss[k]);
+          x[V * (c + K) + i + k] = less<EXACT>(a, ss[k], -b, cs[k]);
         }
       }
+    }
+  } else if constexpr (LAYOUT == kSwap || LAYOUT == kShift) {
+    const int shift = pairs / V - 8 * K, lane = threadIdx.x & 31;
+    const int up = (lane & 24) + ((l + shift) & 7), down = (lane & 24) + ((l - shift) & 7);
+    const int carry = l + shift >= 8, borrow = l < shift;
+    constexpr int kPieces = LAYOUT == kSwap ? 1 : 2 * K + 2 < C ? 2 * K + 2 : C;  // that turn
+    float from_up[kPieces * V], from_down[kPieces * V];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[4 * g + i] = x[4 * g + i];
-      if (d < 2 * pairs) {
-        const float* at = row + (upper ? d - pairs : d);
-        const float4 c = *reinterpret_cast<const float4*>(at), s = *reinterpret_cast<const float4*>(at + pairs);
-        y[4 * g] = spun(x[4 * g], b[0], c.x, s.x, upper);
-        y[4 * g + 1] = spun(x[4 * g + 1], b[1], c.y, s.y, upper);
-        y[4 * g + 2] = spun(x[4 * g + 2], b[2], c.z, s.z, upper);
-        y[4 * g + 3] = spun(x[4 * g + 3], b[3], c.w, s.w, upper);
-      }
+    for (int i = 0; i < kPieces * V; ++i) {
+      from_up[i] = __shfl_sync(0xFFFFFFFFu, x[i], up);
+      if constexpr (LAYOUT == kShift) from_down[i] = __shfl_sync(0xFFFFFFFFu, x[i], down);
     }
 #pragma unroll
-    for (int i = 0; i < 4 * kParts; ++i) x[i] = y[i];
+    for (int c = 0; c < kPieces; ++c) {
+      const int unit = c * 8 + l, half = pairs / V;
+      if (unit >= 2 * half) continue;
+      const bool upper = unit >= half;
+      const float* at = row + (upper ? unit - half : unit) * V;
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 co = *reinterpret_cast<const float4*>(at + i), si = *reinterpret_cast<const float4*>(at + pairs + i);
+        const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float b;
+          if constexpr (LAYOUT == kSwap) {
+            b = from_up[i + k];
+          } else {
+            // (pieces that are not there belong to units beyond the pairs)
+            constexpr int kLast = kPieces - 1;
+            const int e = i + k;
+            const float on = carry ? from_up[V * (c + K + 1 < kLast ? c + K + 1 : kLast) + e] : from_up[V * (c + K < kLast ? c + K : kLast) + e];
+            const float back = borrow ? from_down[V * (c - K - 1 > 0 ? c - K - 1 : 0) + e] : from_down[V * (c - K > 0 ? c - K : 0) + e];
+            b = upper ? back : on;
+          }
+          x[V * c + i + k] = less<EXACT>(x[V * c + i + k], cs[k], upper ? -b : b, ss[k]);
+        }
+      }
+    }
   }
 }
 
-__device__ __forceinline__ float square_sum(const float (&x)[8]) {
-  float a = x[0] * x[0], b = x[4] * x[4];
+__device__ __forceinline__ float square_sum(const float (&x)[32], float unit) {
+  float a[4];
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    a = fmaf(x[i], x[i], a);
-    b = fmaf(x[4 + i], x[4 + i], b);
-  }
-  a += b;
+  for (int i = 0; i < 4; ++i) a[i] = (x[i] * unit) * (x[i] * unit);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, d);
-  return a;
+  for (int i = 4; i < 32; ++i) a[i & 3] = fmaf(x[i] * unit, x[i] * unit, a[i & 3]);
+  float sum = (a[0] + a[1]) + (a[2] + a[3]);
+#pragma unroll
+  for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  return sum;
 }
-// 1 / sqrt(mean of squares + eps) of a warp's row
-__device__ __forceinline__ float inverse_norm(const float (&x)[8], float eps) {
-  float sum = square_sum(x);
-  float unit = 1.0f;
-  if (sum == __int_as_float(0x7F800000)) {  // above 2^63 or so the squares pass fp32's range, not their root
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i] * 0x1p-80f;
-    sum = square_sum(y);
-    unit = 0x1p-80f;
-    eps = 0.0f;
+// 1 / sqrt(mean of squares + eps) of each of a warp's four rows
+__device__ __forceinline__ float inverse_norm(const float (&x)[32], float eps) {
+  const float sum = square_sum(x, 1.0f);
+  float inv = __frsqrt_rn(fmaf(sum, 1.0f / kHeadDim, eps));
+  if (__any_sync(0xFFFFFFFFu, sum == __int_as_float(0x7F800000))) {  // above 2^63 or so the squares pass fp32's range, not their root
+    const float small = square_sum(x, 0x1p-80f);
+    if (sum == __int_as_float(0x7F800000)) inv = __frsqrt_rn(small * (1.0f / kHeadDim)) * 0x1p-80f;
   }
-  return __frsqrt_rn(fmaf(sum, 1.0f / kHeadDim, eps)) * unit;
+  return inv;
 }
 
 // A lane's weights of the norm.
+template <bool F32>
 struct Weights {
-  float w[8];
-  __device__ __forceinline__ void load(const float* at, int lane) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(at) + lane), b = __ldg(reinterpret_cast<const float4*>(at) + 32 + lane);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-  }
-  __device__ __forceinline__ void apply(float (&x)[8], float inv) const {
+  float w[32];
+  __device__ __forceinline__ void load(const float* at, int l) {
+    constexpr int V = Raw<F32>::V;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+    for (int i = 0; i < 32; i += 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(at + i / V * 8 * V + V * l + i % V));
+      w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
+    }
+  }
+  __device__ __forceinline__ void apply(float (&x)[32], float inv) const {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = x[i] * inv * w[i];
   }
 };
 
@@ -256,13 +292,12 @@ __device__ __forceinline__ int divided(unsigned r, unsigned mul, unsigned shift)
 }
 
 // A CTA takes a block of 2^block_shift token rows of (entries x rows) and a group of
-// heads; a warp takes one row of one head at a time, eight (fp32: four) in flight.
-template <int LAYOUT, bool F32>
-__global__ void __launch_bounds__(256) rotate_kernel(const __grid_constant__ RotateParams p) {
+// heads: items, 32 at a time, the next ones' loads in flight.
+template <int LAYOUT, int K, bool F32>
+__global__ void __launch_bounds__(256, 2) rotate_kernel(const __grid_constant__ RotateParams p) {
   extern __shared__ __align__(16) float table[];
-  constexpr int kInFlight = F32 ? 4 : 8;
   wait_for_last_kernel();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int octet = threadIdx.x >> 3, l = threadIdx.x & 7;
   const int r0 = blockIdx.x << p.block_shift, rows = min(1 << p.block_shift, p.rows - r0), mask = (1 << p.block_shift) - 1;
   const bool is_k = static_cast<int>(blockIdx.y) >= p.q_groups;
   const int head0 = (static_cast<int>(blockIdx.y) - (is_k ? p.q_groups : 0)) * p.group, all = is_k ? p.k_heads : p.q_heads;
@@ -271,18 +306,17 @@ __global__ void __launch_bounds__(256) rotate_kernel(const __grid_constant__ Rot
   uint8_t* out = is_k ? p.k_out : p.q_out;
   const float* weight = is_k ? p.turn.k_weight : p.turn.q_weight;
 
-  Raw<F32> raw[kInFlight];
-  auto load = [&](int item0) {
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) {
-      const int item = item0 + 8 * i, r = item & mask, e = divided(r0 + r, p.n_mul, p.n_shift);
-      if (item >= items || r >= rows) continue;
-      raw[i].load(in.at + e * in.entry + (head0 + (item >> p.block_shift)) * in.head + (r0 + r - e * p.n) * in.row, lane);
-    }
+  Raw<F32> raw;
+  auto load = [&](int item) {
+    const int r = item & mask, e = divided(r0 + r, p.n_mul, p.n_shift);
+    if (item < items && r < rows)
+      raw.load(in.at + e * in.entry + (head0 + (item >> p.block_shift)) * in.head + (r0 + r - e * p.n) * in.row, l);
   };
-  load(warp);
-  Weights w;
-  if (weight) w.load(weight, lane);
+#pragma unroll
+  for (int c = 0; c < Raw<F32>::C; ++c) raw.x[c] = make_uint4(0, 0, 0, 0);
+  load(octet);
+  Weights<F32> w;
+  if (weight) w.load(weight, l);
   if constexpr (LAYOUT != kNone) {
     fill_table(p.turn, table, rows, [&](int r) {
       const int e = divided(r0 + r, p.n_mul, p.n_shift);
@@ -290,22 +324,17 @@ __global__ void __launch_bounds__(256) rotate_kernel(const __grid_constant__ Rot
     });
     __syncthreads();
   }
-  for (int item0 = warp;; ) {
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) {
-      const int item = item0 + 8 * i, r = item & mask;
-      if (item >= items || r >= rows) continue;
-      float x[8];
-      raw[i].get(x);
-      if (weight) w.apply(x, inverse_norm(x, p.turn.eps));
-      turn_row<LAYOUT>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, lane);
-      const int e = divided(r0 + r, p.n_mul, p.n_shift);
-      const long long to = (static_cast<long long>(e) * all + head0 + (item >> p.block_shift)) * p.n + (r0 + r - e * p.n);
-      Raw<F32>::store(out + to * kHeadDim * Raw<F32>::kBytes, lane, x);
-    }
-    item0 += 8 * kInFlight;
-    if (item0 >= items) break;
-    load(item0);
+  for (int item0 = 0; item0 < items; item0 += 32) {  // the same turns for every lane: rows are exchanged among them
+    const int item = item0 + octet, r = item & mask;
+    float x[32];
+    raw.get(x);
+    load(item + 32);
+    if (weight) w.apply(x, inverse_norm(x, p.turn.eps));
+    turn_row<LAYOUT, K, F32, F32>(x, table + 2 * min(r, rows - 1) * p.turn.pairs, p.turn.pairs, l);
+    if (item >= items || r >= rows) continue;
+    const int e = divided(r0 + r, p.n_mul, p.n_shift);
+    const long long to = (static_cast<long long>(e) * all + head0 + (item >> p.block_shift)) * p.n + (r0 + r - e * p.n);
+    Raw<F32>::store(out + to * Raw<F32>::kRowBytes, l, x);
   }
 }
 
@@ -322,11 +351,11 @@ struct RotaryAppendParams {
 
 // CTA (page of a segment, y, segment): the keys of kv head y, the values of kv head y -
 // heads, or the queries of a group of heads at the page's new rows.  A page's rows
-// stay in registers as they came, eight to a warp; keys are turned twice, for the page's
-// largest element and for the codes, which takes fewer registers than keeping them in
-// fp32.  Codes are rounded from fp32, once.
-template <int LAYOUT>
-__global__ void __launch_bounds__(256, 3) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
+// stay in registers as they came, two to eight lanes; keys are turned twice, for the
+// page's largest element and for the codes, which takes fewer registers than keeping
+// them in fp32.  Codes are rounded from fp32, once.
+template <int LAYOUT, int K>
+__global__ void __launch_bounds__(256, 2) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
   extern __shared__ __align__(16) float table[];  // of the page's new rows
   __shared__ uint32_t tops[8];
   wait_for_last_kernel();
@@ -336,10 +365,8 @@ __global__ void __launch_bounds__(256, 3) paged_append_rotary_kernel(const __gri
   const int begin = k == 0 ? off : 0;             // this page's new rows: [begin, end)
   const int end = min(kPage, off + sg.rows - k * kPage);
   if (end <= begin) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int octet = threadIdx.x >> 3, l = threadIdx.x & 7;
   const int row0 = sg.row0 + k * kPage - off;     // the call's row of this page's row 0
-  const bool is_v = y >= heads && y < 2 * heads;
-  Raw<false> raw[8];
   auto fill = [&]() {
     if constexpr (LAYOUT != kNone) {
       fill_table(p.turn, table, end - begin, [&](int r) {
@@ -349,99 +376,95 @@ __global__ void __launch_bounds__(256, 3) paged_append_rotary_kernel(const __gri
       __syncthreads();
     }
   };
-  auto turned = [&](const Raw<false>& from, int r, const float* weight, const Weights& w, float inv, float (&x)[8]) {  // r: of the new rows
-    from.get(x);
-    if (weight) w.apply(x, inv);
-    turn_row<LAYOUT>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, lane);
-  };
+  Raw<false> raw[2];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) raw[0].x[c] = raw[1].x[c] = make_uint4(0, 0, 0, 0);
 
   if (y >= 2 * heads) {
     // ---------------------------------------------------------------- queries
     const int head0 = (y - 2 * heads) * p.group, rows = end - begin, items = min(p.group, p.q_heads - head0) * rows;
     const unsigned mul = 0xFFFFFFFFu / rows + 1;  // item / rows = umulhi(item, mul): item < 2^16, rows <= 64 (rows 1: mul 0)
     auto head_of = [&](int item) { return rows == 1 ? item : static_cast<int>(__umulhi(item, mul)); };
-    auto load = [&](int item0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int item = item0 + 8 * i, h = head_of(item), r = item - h * rows;
-        if (item < items) raw[i].load(p.q.at + sg.entry * p.q.entry + (head0 + h) * p.q.head + (row0 + begin + r) * p.q.row, lane);
-      }
+    auto load = [&](int item) {
+      const int h = head_of(item), r = item - h * rows;
+      if (item < items) raw[0].load(p.q.at + sg.entry * p.q.entry + (head0 + h) * p.q.head + (row0 + begin + r) * p.q.row, l);
     };
-    load(warp);
-    Weights w;
-    if (p.turn.q_weight) w.load(p.turn.q_weight, lane);
+    load(octet);
+    Weights<false> w;
+    if (p.turn.q_weight) w.load(p.turn.q_weight, l);
     fill();
-    for (int item0 = warp;;) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int item = item0 + 8 * i, h = head_of(item), r = item - h * rows;
-        if (item >= items) break;
-        float x[8];
-        raw[i].get(x);
-        if (p.turn.q_weight) w.apply(x, inverse_norm(x, p.turn.eps));
-        turn_row<LAYOUT>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, lane);
-        const long long to = (static_cast<long long>(sg.entry) * p.q_heads + head0 + h) * p.a.n + row0 + begin + r;
-        Raw<false>::store(p.q_out + to * kHeadDim * 2, lane, x);
-      }
-      item0 += 64;
-      if (item0 >= items) break;
-      load(item0);
+    for (int item0 = 0; item0 < items; item0 += 32) {  // the same turns for every lane: rows are exchanged among them
+      const int item = item0 + octet, h = head_of(item), r = item - h * rows;
+      float x[32];
+      raw[0].get(x);
+      load(item + 32);
+      if (p.turn.q_weight) w.apply(x, inverse_norm(x, p.turn.eps));
+      turn_row<LAYOUT, K, false, false>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
+      if (item >= items) continue;
+      const long long to = (static_cast<long long>(sg.entry) * p.q_heads + head0 + h) * p.a.n + row0 + begin + r;
+      Raw<false>::store(p.q_out + to * Raw<false>::kRowBytes, l, x);
     }
     return;
   }
   // ---------------------------------------------------------------- keys, values
+  const bool is_v = y >= heads;
   const int h = is_v ? y - heads : y;
   const int page = sg.page + k, from = k == 0 ? sg.from : page;
   const long long at = static_cast<long long>(page) * heads + h, at_from = static_cast<long long>(from) * heads + h;
   uint8_t* codes = (is_v ? p.a.v_codes : p.a.k_codes) + at * kPageBytes;
   float* scales = is_v ? p.a.v_scales : p.a.k_scales;
+  const float* weight = p.turn.k_weight;
   {
     const Rows& in = is_v ? p.v : p.k;
     const uint8_t* rows = in.at + sg.entry * in.entry + h * in.head;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = warp + 8 * i;
-      raw[i].x[0] = raw[i].x[1] = make_uint2(0, 0);
-      if (r >= begin && r < end) raw[i].load(rows + (row0 + r) * in.row, lane);
+    for (int i = 0; i < 2; ++i) {
+      const int r = octet + 32 * i;
+      if (r >= begin && r < end) raw[i].load(rows + (row0 + r) * in.row, l);
     }
   }
-  Weights w;
-  float inv[8] = {};
+  Weights<false> w;
+  float inv[2] = {};
+  auto turned = [&](int i, float (&x)[32]) {  // (rows that are not new are all zeros)
+    raw[i].get(x);
+    if (weight) w.apply(x, inv[i]);
+    const int r = min(max(octet + 32 * i, begin), end - 1) - begin;
+    turn_row<LAYOUT, K, false, true>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
+  };
   uint32_t top = 0;
   bool odd;  // not a number, held as 0, or infinite, held as the largest value
   if (is_v) {
     auto largest = [&]() {
       top = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, magnitude(make_uint4(raw[i].x[0].x, raw[i].x[0].y, raw[i].x[1].x, raw[i].x[1].y)));
+      for (int c = 0; c < 8; ++c) top = max(top, magnitude(raw[c >> 2].x[c & 3]));
     };
     largest();
     odd = top >= 0x7F80u;
     if (odd) {  // rare
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int g = 0; g < 2; ++g) raw[i].x[g] = make_uint2(drop_non_finite(raw[i].x[g].x), drop_non_finite(raw[i].x[g].y));
+      for (int c = 0; c < 8; ++c) {
+        uint4& x = raw[c >> 2].x[c & 3];
+        x = make_uint4(drop_non_finite(x.x), drop_non_finite(x.y), drop_non_finite(x.z), drop_non_finite(x.w));
+      }
       largest();
     }
     top <<= 16;
   } else {
-    if (p.turn.k_weight) w.load(p.turn.k_weight, lane);
+    if (weight) w.load(weight, l);
     fill();
     uint32_t bits = 0;
     float most = 0.0f;  // (a maximum leaves out what is not a number)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = warp + 8 * i;
-      if (r < begin || r >= end) continue;
-      float x[8];
-      if (p.turn.k_weight) {
+    for (int i = 0; i < 2; ++i) {
+      float x[32];
+      if (weight) {
         raw[i].get(x);
         inv[i] = inverse_norm(x, p.turn.eps);
       }
-      turned(raw[i], r - begin, p.turn.k_weight, w, inv[i], x);
+      turned(i, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 32; ++j) {
         most = fmaxf(most, fabsf(x[j]));
         bits = max(bits, __float_as_uint(x[j]) & 0x7FFFFFFFu);
       }
@@ -450,7 +473,7 @@ __global__ void __launch_bounds__(256, 3) paged_append_rotary_kernel(const __gri
     top = min(__float_as_uint(most), 0x7F7FFFFFu);
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if (lane == 0) tops[warp] = top;
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, tops[i]);
@@ -461,19 +484,22 @@ __global__ void __launch_bounds__(256, 3) paged_append_rotary_kernel(const __gri
   e = max(e, old);
   const float unit = power2(-e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = warp + 8 * i;
-    if (r < begin || r >= end) continue;
-    float x[8];
+  for (int i = 0; i < 2; ++i) {
+    const int r = octet + 32 * i;
+    float x[32];
     if (is_v) raw[i].get(x);
-    else turned(raw[i], r - begin, p.turn.k_weight, w, inv[i], x);
+    else turned(i, x);
+    if (r < begin || r >= end) continue;
     if (odd)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] != x[j] ? 0.0f : x[j];
+      for (int j = 0; j < 32; ++j) x[j] = x[j] != x[j] ? 0.0f : x[j];
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-      *reinterpret_cast<uint32_t*>(codes + r * kHeadDim + 128 * g + 4 * lane) =
-          e4m3x2(x[4 * g] * unit, x[4 * g + 1] * unit) | e4m3x2(x[4 * g + 2] * unit, x[4 * g + 3] * unit) << 16;
+    for (int c = 0; c < 4; ++c) {
+      const float* z = x + 8 * c;
+      *reinterpret_cast<uint2*>(codes + r * kHeadDim + 64 * c + 8 * l) =
+          make_uint2(e4m3x2(z[0] * unit, z[1] * unit) | e4m3x2(z[2] * unit, z[3] * unit) << 16,
+                     e4m3x2(z[4] * unit, z[5] * unit) | e4m3x2(z[6] * unit, z[7] * unit) << 16);
+    }
   }
   upkeep((is_v ? p.a.v_codes : p.a.k_codes) + at_from * kPageBytes, codes, begin, end, from != page, old, e);
   if (odd || beyond) atomicOr(p.a.status, IQ_STATUS_RANGE);
@@ -483,7 +509,6 @@ __global__ void __launch_bounds__(256, 3) paged_append_rotary_kernel(const __gri
     if (y == 0) p.a.table[static_cast<long long>(sg.slot) * p.a.max_pages + sg.pos / kPage + k] = page;
   }
 }
-
 
 // The turns per position of a frequency, modulo 1, times 2^64.
 struct TurnsParams {
@@ -497,9 +522,16 @@ __global__ void turns_kernel(const __grid_constant__ TurnsParams p, unsigned lon
 
 // ------------------------------------------------------------------ host
 
-Layout layout_of(const iq_rotary* r) {
-  const int pairs = r->rotary_dim / 2;
-  return pairs == 0 ? kNone : r->interleaved ? kPairs : pairs == 128 ? kAcross : pairs <= 64 ? kNear : kFar;
+struct Kind {
+  Layout layout;
+  int k;
+};
+Kind kind_of(const iq_rotary* r, bool f32) {
+  const int pairs = r->rotary_dim / 2, piece = f32 ? 32 : 64;  // 8V elements
+  if (pairs == 0) return {kNone, 0};
+  if (r->interleaved) return {kPairs, 0};
+  if (pairs % piece == 0) return {kHere, pairs / piece};
+  return {!f32 && pairs == 32 ? kSwap : kShift, pairs / piece};
 }
 Turn turn_of(const iq_rotary* r) {
   return {reinterpret_cast<const unsigned long long*>(r->turns), r->q_weight, r->k_weight, r->amplitude, r->eps, r->rotary_dim / 2};
@@ -551,29 +583,38 @@ bool overlap(Range a, Range b) {
   return x < y + b.bytes && y < x + a.bytes;
 }
 
-template <bool F32>
-const void* rotate_kernel_of(Layout l) {
-  switch (l) {
-    case kPairs: return reinterpret_cast<const void*>(&rotate_kernel<kPairs, F32>);
-    case kNear: return reinterpret_cast<const void*>(&rotate_kernel<kNear, F32>);
-    case kAcross: return reinterpret_cast<const void*>(&rotate_kernel<kAcross, F32>);
-    case kFar: return reinterpret_cast<const void*>(&rotate_kernel<kFar, F32>);
-    default: return reinterpret_cast<const void*>(&rotate_kernel<kNone, F32>);
+template <int LAYOUT, int K = 0>
+const void* rotate_of(bool f32) {
+  return f32 ? reinterpret_cast<const void*>(&rotate_kernel<LAYOUT, K, true>) : reinterpret_cast<const void*>(&rotate_kernel<LAYOUT, K, false>);
+}
+const void* rotate_kernel_of(Kind kind, bool f32) {
+  switch (kind.layout) {
+    case kPairs: return rotate_of<kPairs>(f32);
+    case kSwap: return reinterpret_cast<const void*>(&rotate_kernel<kSwap, 0, false>);
+    case kHere:
+      if (kind.k == 3) return reinterpret_cast<const void*>(&rotate_kernel<kHere, 3, true>);
+      if (kind.k == 4) return reinterpret_cast<const void*>(&rotate_kernel<kHere, 4, true>);
+      return kind.k == 1 ? rotate_of<kHere, 1>(f32) : rotate_of<kHere, 2>(f32);
+    case kShift:
+      if (kind.k == 2) return reinterpret_cast<const void*>(&rotate_kernel<kShift, 2, true>);
+      if (kind.k == 3) return reinterpret_cast<const void*>(&rotate_kernel<kShift, 3, true>);
+      return kind.k == 0 ? rotate_of<kShift, 0>(f32) : rotate_of<kShift, 1>(f32);
+    default: return rotate_of<kNone>(f32);
   }
 }
-const void* append_kernel_of(Layout l) {
-  switch (l) {
-    case kPairs: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kPairs>);
-    case kNear: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kNear>);
-    case kAcross: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kAcross>);
-    case kFar: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kFar>);
-    default: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kNone>);
+const void* append_kernel_of(Kind kind) {
+  switch (kind.layout) {
+    case kPairs: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kPairs, 0>);
+    case kSwap: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kSwap, 0>);
+    case kHere: return kind.k == 1 ? reinterpret_cast<const void*>(&paged_append_rotary_kernel<kHere, 1>) : reinterpret_cast<const void*>(&paged_append_rotary_kernel<kHere, 2>);
+    case kShift: return kind.k == 0 ? reinterpret_cast<const void*>(&paged_append_rotary_kernel<kShift, 0>) : reinterpret_cast<const void*>(&paged_append_rotary_kernel<kShift, 1>);
+    default: return reinterpret_cast<const void*>(&paged_append_rotary_kernel<kNone, 0>);
   }
 }
 
 struct RotaryAppend {
   Turn turn;
-  Layout layout;
+  Kind kind;
   Rows q, k, v;
   uint8_t* q_out;
   const int* positions;
@@ -594,9 +635,9 @@ cudaError_t launch_append_rotary(const AppendParams& a, int widest, int segs, cu
   int rows = 0;  // the most new rows of a page
   for (int i = 0; i < segs; ++i) rows = std::max(rows, std::min(kPage, a.seg[i].rows));
   const int smem = rows * 2 * m.turn.pairs * static_cast<int>(sizeof(float));
-  const void* kernel = append_kernel_of(m.layout);
-  static std::atomic<uint64_t> seen[kFar + 1] = {};
-  const cudaError_t e = smem > 48 * 1024 ? allow_smem(kernel, 64 * 1024, seen[m.layout]) : cudaSuccess;
+  const void* kernel = append_kernel_of(m.kind);
+  static std::atomic<uint64_t> seen[kShift + 1][3] = {};
+  const cudaError_t e = smem > 48 * 1024 ? allow_smem(kernel, 64 * 1024, seen[m.kind.layout][m.kind.k]) : cudaSuccess;
   void* args[] = {&p};
   return e == cudaSuccess ? launch_after(kernel, dim3(widest, 2 * a.heads + (m.q_heads + p.group - 1) / p.group, segs), 256, smem, stream, args) : e;
 }
@@ -709,9 +750,8 @@ int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_
   while (p.block_shift > 0 && static_cast<long long>(blocks()) * (groups(q_heads) + groups(k_heads)) < 4ll * num_sms()) --p.block_shift;
   if (p.block_shift == 0) p.group = 8;
   p.q_groups = groups(q_heads);
-  const Layout layout = layout_of(rotary);
   void* args[] = {&p};
-  IQ_CUDA(launch_after(dtype == IQ_DTYPE_F32 ? rotate_kernel_of<true>(layout) : rotate_kernel_of<false>(layout),
+  IQ_CUDA(launch_after(rotate_kernel_of(kind_of(rotary, size == 4), size == 4),
                        dim3(blocks(), p.q_groups + groups(k_heads)), 256, static_cast<int>(sizeof(float)) * (2 * p.turn.pairs << p.block_shift),
                        static_cast<cudaStream_t>(stream), args));
   launched_outputs(stream, out[0], out[1]);
@@ -730,7 +770,7 @@ int iq_paged_append_rotary(iq_paged* c, const iq_rotary* rotary, const iq_rows* 
   if (n_slots == 0 || n == 0) return IQ_OK;
   RotaryAppend m;
   m.turn = turn_of(rotary);
-  m.layout = layout_of(rotary);
+  m.kind = kind_of(rotary, false);
   Range in[3] = {};
   m.q = {nullptr, 0, 0, 0};
   if (q_heads > 0 && (st = check_rows(q, n_slots, q_heads, n, 2, "q", &m.q, &in[0])) != IQ_OK) return st;

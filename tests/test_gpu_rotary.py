@@ -25,9 +25,9 @@ def plan(rd=64, interleaved=False, norm=True, scaling="none", seed=9, **kw):
 
 def exact(x, at, ref, which):
     """x [entries, heads, n, 256] (a tensor) at positions [entries, n], in 64 bits, and a bound of its fp32 form's error:
-    the sum of 256 squares (a chain of 4, then 6 levels of a tree: 10 roundings, halved by the root), the root, two products:
-    9 U of a normed element at most.  A cosine or sine: the angle's last conversion (U of pi/4), sincospif's 2 units of the
-    last place and the amplitude's product, below 8 U of the amplitude; a product and a sum: 2 U more.  The frequency's own 2^-53 and
+    the sum of 256 squares (chains of 8, then 5 levels of a tree: 13 roundings, halved by the root), the root, two products:
+    10 U of a normed element at most.  A cosine or sine: 2 units of the last place and the amplitude's product, below 8 U of
+    the amplitude; a product and a sum: 2 U more.  The frequency's own 2^-53 and
     its turns' 2^-53, both relative, times the angle's size."""
     w, f, interleaved, amplitude = ref
     x = f64(x)
