@@ -119,16 +119,23 @@ __device__ __forceinline__ float2 unit_at(unsigned a, float amplitude) {
   }
   return make_float2(c, s);
 }
-// Row r of the table: the cosines of its pairs, then their sines.
-template <typename Position>
+// Row r of the table: the cosines of its pairs, then their sines.  In halves' layouts a
+// lane reads V of them, four at a time: the first fours of all lanes stand side by side,
+// then the second fours, so that eight lanes read 128 bytes in a row.
+template <int V>
+__device__ __forceinline__ int table_place(int j, int pairs) {
+  return V == 8 ? (j & 4) * (pairs / 8) + (j >> 3) * 4 + (j & 3) : j;
+}
+template <int V, typename Position>
 __device__ __forceinline__ void fill_table(const Turn& t, float* table, int rows, Position position) {
   int r = threadIdx.x / t.pairs, j = threadIdx.x - r * t.pairs;
   const int down = blockDim.x / t.pairs, across = blockDim.x - down * t.pairs;
   while (r < rows) {
     const long long p = position(r);
     const float2 u = unit_at(static_cast<unsigned>((static_cast<unsigned long long>(p) * __ldg(t.turns + j)) >> 32), t.amplitude);
-    table[(2 * r) * t.pairs + j] = u.x;
-    table[(2 * r + 1) * t.pairs + j] = u.y;
+    const int to = 2 * r * t.pairs + table_place<V>(j, t.pairs);
+    table[to] = u.x;
+    table[to + t.pairs] = u.y;
     r += down;
     j += across;
     if (j >= t.pairs) {
@@ -137,6 +144,8 @@ __device__ __forceinline__ void fill_table(const Turn& t, float* table, int rows
     }
   }
 }
+template <int LAYOUT, bool F32>
+constexpr int kTableOrder = LAYOUT == kPairs ? 1 : Raw<F32>::V;
 
 // a c - b s, or a c + b s.  EXACT: off by its own rounding alone, the first product's
 // is made good (for float32 results and codes, see unit_at).
@@ -156,11 +165,13 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
     for (int c = 0; c < C; ++c) {
       const int j = (c * 8 * V + V * l) / 2;
       if (j >= pairs) continue;
-      float co[V / 2], si[V / 2];
-#pragma unroll
-      for (int i = 0; i < V / 2; i += 2) {
-        *reinterpret_cast<float2*>(co + i) = *reinterpret_cast<const float2*>(row + j + i);
-        *reinterpret_cast<float2*>(si + i) = *reinterpret_cast<const float2*>(row + pairs + j + i);
+      float co[4], si[4];
+      if constexpr (F32) {
+        const float2 a = *reinterpret_cast<const float2*>(row + j), b = *reinterpret_cast<const float2*>(row + pairs + j);
+        co[0] = a.x, co[1] = a.y, si[0] = b.x, si[1] = b.y;
+      } else {
+        const float4 a = *reinterpret_cast<const float4*>(row + j), b = *reinterpret_cast<const float4*>(row + pairs + j);
+        co[0] = a.x, co[1] = a.y, co[2] = a.z, co[3] = a.w, si[0] = b.x, si[1] = b.y, si[2] = b.z, si[3] = b.w;
       }
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) {
@@ -172,10 +183,10 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
   } else if constexpr (LAYOUT == kHere) {
 #pragma unroll
     for (int c = 0; c < K; ++c) {
-      const float* at = row + c * 8 * V + V * l;
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
-        const float4 co = *reinterpret_cast<const float4*>(at + i), si = *reinterpret_cast<const float4*>(at + pairs + i);
+        const float* at = row + i * (pairs / V) + (c * 8 + l) * 4;
+        const float4 co = *reinterpret_cast<const float4*>(at), si = *reinterpret_cast<const float4*>(at + pairs);
         const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -201,10 +212,10 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
       const int unit = c * 8 + l, half = pairs / V;
       if (unit >= 2 * half) continue;
       const bool upper = unit >= half;
-      const float* at = row + (upper ? unit - half : unit) * V;
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
-        const float4 co = *reinterpret_cast<const float4*>(at + i), si = *reinterpret_cast<const float4*>(at + pairs + i);
+        const float* at = row + i * half + (upper ? unit - half : unit) * 4;
+        const float4 co = *reinterpret_cast<const float4*>(at), si = *reinterpret_cast<const float4*>(at + pairs);
         const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -248,23 +259,24 @@ __device__ __forceinline__ float inverse_norm(const float (&x)[32], float eps) {
   return inv;
 }
 
-// A lane's weights of the norm.
+// A row times the norm's weights, which are in shared memory (in registers they would
+// leave room for two CTAs instead of three), in an order like the table's.
 template <bool F32>
-struct Weights {
-  float w[32];
-  __device__ __forceinline__ void load(const float* at, int l) {
-    constexpr int V = Raw<F32>::V;
+__device__ __forceinline__ void put_weight(float* weights, const float* from) {
+  const int d = threadIdx.x;
+  weights[F32 ? d : (d & ~63) + (d & 4) * 8 + ((d & 63) >> 3) * 4 + (d & 3)] = __ldg(from + d);
+}
+template <bool F32>
+__device__ __forceinline__ void weigh(float (&x)[32], float inv, const float* weights, int l) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(at + i / V * 8 * V + V * l + i % V));
-      w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
-    }
+  for (int i = 0; i < 32; i += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(weights + 8 * i + 4 * l);
+    x[i] = x[i] * inv * w.x;
+    x[i + 1] = x[i + 1] * inv * w.y;
+    x[i + 2] = x[i + 2] * inv * w.z;
+    x[i + 3] = x[i + 3] * inv * w.w;
   }
-  __device__ __forceinline__ void apply(float (&x)[32], float inv) const {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = x[i] * inv * w[i];
-  }
-};
+}
 
 // ------------------------------------------------------------------ rows to rows
 
@@ -274,7 +286,7 @@ struct RotateParams {
   uint8_t* q_out;
   uint8_t* k_out;
   const int* positions;
-  int n, rows, q_heads, k_heads, group, q_groups, block_shift;
+  int n, rows, q_heads, k_heads, block, group;  // rows of a CTA, heads of a CTA (queries', then keys')
   unsigned n_mul, n_shift;  // division by n of row numbers, see Quotient
   int start[IQ_MAX_BATCH];
 };
@@ -291,50 +303,59 @@ __device__ __forceinline__ int divided(unsigned r, unsigned mul, unsigned shift)
   return static_cast<int>((mul ? __umulhi(r, mul) : r) >> shift);
 }
 
-// A CTA takes a block of 2^block_shift token rows of (entries x rows) and a group of
-// heads: items, 32 at a time, the next ones' loads in flight.
+// item / n = umulhi(item, mul) for item < 2^16, n <= 64; 0 stands for n == 1.
+struct Split {
+  unsigned mul;
+  int n;
+  __device__ __forceinline__ explicit Split(int n) : mul(0xFFFFFFFFu / n + 1), n(n) {}
+  __device__ __forceinline__ int operator()(int item) const { return n == 1 ? item : static_cast<int>(__umulhi(item, mul)); }
+};
+
+// A CTA takes a block of token rows of (entries x rows) and a group of heads: their
+// items, 32 at a time.
 template <int LAYOUT, int K, bool F32>
-__global__ void __launch_bounds__(256, 2) rotate_kernel(const __grid_constant__ RotateParams p) {
+__global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(const __grid_constant__ RotateParams p) {
   extern __shared__ __align__(16) float table[];
+  __shared__ __align__(16) float weights[2][kHeadDim];
   wait_for_last_kernel();
   const int octet = threadIdx.x >> 3, l = threadIdx.x & 7;
-  const int r0 = blockIdx.x << p.block_shift, rows = min(1 << p.block_shift, p.rows - r0), mask = (1 << p.block_shift) - 1;
-  const bool is_k = static_cast<int>(blockIdx.y) >= p.q_groups;
-  const int head0 = (static_cast<int>(blockIdx.y) - (is_k ? p.q_groups : 0)) * p.group, all = is_k ? p.k_heads : p.q_heads;
-  const int items = min(p.group, all - head0) << p.block_shift;
-  const Rows in = is_k ? p.k : p.q;
-  uint8_t* out = is_k ? p.k_out : p.q_out;
-  const float* weight = is_k ? p.turn.k_weight : p.turn.q_weight;
+  const int r0 = blockIdx.x * p.block, rows = min(p.block, p.rows - r0);
+  const int head0 = blockIdx.y * p.group, items = min(p.group, p.q_heads + p.k_heads - head0) * rows;
+  const Split by_rows(rows);
 
   Raw<F32> raw;
   auto load = [&](int item) {
-    const int r = item & mask, e = divided(r0 + r, p.n_mul, p.n_shift);
-    if (item < items && r < rows)
-      raw.load(in.at + e * in.entry + (head0 + (item >> p.block_shift)) * in.head + (r0 + r - e * p.n) * in.row, l);
+    const int h = by_rows(item), head = head0 + h, row = r0 + item - h * rows, e = divided(row, p.n_mul, p.n_shift);
+    const bool is_k = head >= p.q_heads;
+    const Rows& in = is_k ? p.k : p.q;
+    if (item < items) raw.load(in.at + e * in.entry + (is_k ? head - p.q_heads : head) * in.head + (row - e * p.n) * in.row, l);
   };
 #pragma unroll
   for (int c = 0; c < Raw<F32>::C; ++c) raw.x[c] = make_uint4(0, 0, 0, 0);
   load(octet);
-  Weights<F32> w;
-  if (weight) w.load(weight, l);
-  if constexpr (LAYOUT != kNone) {
-    fill_table(p.turn, table, rows, [&](int r) {
+  if (p.turn.q_weight) put_weight<F32>(weights[0], p.turn.q_weight);
+  if (p.turn.k_weight) put_weight<F32>(weights[1], p.turn.k_weight);
+  if constexpr (LAYOUT != kNone)
+    fill_table<kTableOrder<LAYOUT, F32>>(p.turn, table, rows, [&](int r) {
       const int e = divided(r0 + r, p.n_mul, p.n_shift);
       return static_cast<long long>(p.positions ? __ldg(p.positions + r0 + r) : p.start[e]) + (p.positions ? 0 : r0 + r - e * p.n);
     });
-    __syncthreads();
-  }
+  __syncthreads();
   for (int item0 = 0; item0 < items; item0 += 32) {  // the same turns for every lane: rows are exchanged among them
-    const int item = item0 + octet, r = item & mask;
+    const int item = item0 + octet, h = by_rows(item), head = head0 + h, r = item - h * rows;
+    const bool is_k = head >= p.q_heads;
     float x[32];
     raw.get(x);
     load(item + 32);
-    if (weight) w.apply(x, inverse_norm(x, p.turn.eps));
-    turn_row<LAYOUT, K, F32, F32>(x, table + 2 * min(r, rows - 1) * p.turn.pairs, p.turn.pairs, l);
-    if (item >= items || r >= rows) continue;
-    const int e = divided(r0 + r, p.n_mul, p.n_shift);
-    const long long to = (static_cast<long long>(e) * all + head0 + (item >> p.block_shift)) * p.n + (r0 + r - e * p.n);
-    Raw<F32>::store(out + to * Raw<F32>::kRowBytes, l, x);
+    if (p.turn.q_weight || p.turn.k_weight) {
+      const float inv = inverse_norm(x, p.turn.eps);
+      if (is_k ? p.turn.k_weight : p.turn.q_weight) weigh<F32>(x, inv, weights[is_k], l);
+    }
+    turn_row<LAYOUT, K, F32, F32>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
+    if (item >= items) continue;
+    const int e = divided(r0 + r, p.n_mul, p.n_shift), all = is_k ? p.k_heads : p.q_heads;
+    const long long to = (static_cast<long long>(e) * all + (is_k ? head - p.q_heads : head)) * p.n + (r0 + r - e * p.n);
+    Raw<F32>::store((is_k ? p.k_out : p.q_out) + to * Raw<F32>::kRowBytes, l, x);
   }
 }
 
@@ -346,7 +367,7 @@ struct RotaryAppendParams {
   Rows q, k, v;
   uint8_t* q_out;
   const int* positions;
-  int q_heads, group;
+  int q_heads, group, groups, part_rows;  // queries: of `groups` groups of heads, so many rows of a page
 };
 
 // CTA (page of a segment, y, segment): the keys of kv head y, the values of kv head y -
@@ -355,8 +376,9 @@ struct RotaryAppendParams {
 // page's largest element and for the codes, which takes fewer registers than keeping
 // them in fp32.  Codes are rounded from fp32, once.
 template <int LAYOUT, int K>
-__global__ void __launch_bounds__(256, 2) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
+__global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
   extern __shared__ __align__(16) float table[];  // of the page's new rows
+  __shared__ __align__(16) float weights[kHeadDim];
   __shared__ uint32_t tops[8];
   wait_for_last_kernel();
   const Segment sg = p.a.seg[blockIdx.z];
@@ -367,14 +389,15 @@ __global__ void __launch_bounds__(256, 2) paged_append_rotary_kernel(const __gri
   if (end <= begin) return;
   const int octet = threadIdx.x >> 3, l = threadIdx.x & 7;
   const int row0 = sg.row0 + k * kPage - off;     // the call's row of this page's row 0
-  auto fill = [&]() {
-    if constexpr (LAYOUT != kNone) {
-      fill_table(p.turn, table, end - begin, [&](int r) {
-        return static_cast<long long>(p.positions ? __ldg(p.positions + static_cast<long long>(sg.entry) * p.a.n + row0 + begin + r)
-                                                  : sg.pos - off + k * kPage + begin + r);
+  // the weights, and the table of rows [first, last) of the page
+  auto fill = [&](const float* weight, int first, int last) {
+    if (weight) put_weight<false>(weights, weight);
+    if constexpr (LAYOUT != kNone)
+      fill_table<kTableOrder<LAYOUT, false>>(p.turn, table, last - first, [&](int r) {
+        return static_cast<long long>(p.positions ? __ldg(p.positions + static_cast<long long>(sg.entry) * p.a.n + row0 + first + r)
+                                                  : sg.pos - off + k * kPage + first + r);
       });
-      __syncthreads();
-    }
+    __syncthreads();
   };
   Raw<false> raw[2];
 #pragma unroll
@@ -382,26 +405,26 @@ __global__ void __launch_bounds__(256, 2) paged_append_rotary_kernel(const __gri
 
   if (y >= 2 * heads) {
     // ---------------------------------------------------------------- queries
-    const int head0 = (y - 2 * heads) * p.group, rows = end - begin, items = min(p.group, p.q_heads - head0) * rows;
-    const unsigned mul = 0xFFFFFFFFu / rows + 1;  // item / rows = umulhi(item, mul): item < 2^16, rows <= 64 (rows 1: mul 0)
-    auto head_of = [&](int item) { return rows == 1 ? item : static_cast<int>(__umulhi(item, mul)); };
+    const int part = (y - 2 * heads) / p.groups, head0 = (y - 2 * heads - part * p.groups) * p.group;
+    const int first = max(begin, part * p.part_rows), rows = min(end, (part + 1) * p.part_rows) - first;
+    if (rows <= 0) return;
+    const int items = min(p.group, p.q_heads - head0) * rows;
+    const Split head_of(rows);
     auto load = [&](int item) {
       const int h = head_of(item), r = item - h * rows;
-      if (item < items) raw[0].load(p.q.at + sg.entry * p.q.entry + (head0 + h) * p.q.head + (row0 + begin + r) * p.q.row, l);
+      if (item < items) raw[0].load(p.q.at + sg.entry * p.q.entry + (head0 + h) * p.q.head + (row0 + first + r) * p.q.row, l);
     };
     load(octet);
-    Weights<false> w;
-    if (p.turn.q_weight) w.load(p.turn.q_weight, l);
-    fill();
+    fill(p.turn.q_weight, first, first + rows);
     for (int item0 = 0; item0 < items; item0 += 32) {  // the same turns for every lane: rows are exchanged among them
       const int item = item0 + octet, h = head_of(item), r = item - h * rows;
       float x[32];
       raw[0].get(x);
       load(item + 32);
-      if (p.turn.q_weight) w.apply(x, inverse_norm(x, p.turn.eps));
+      if (p.turn.q_weight) weigh<false>(x, inverse_norm(x, p.turn.eps), weights, l);
       turn_row<LAYOUT, K, false, false>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
       if (item >= items) continue;
-      const long long to = (static_cast<long long>(sg.entry) * p.q_heads + head0 + h) * p.a.n + row0 + begin + r;
+      const long long to = (static_cast<long long>(sg.entry) * p.q_heads + head0 + h) * p.a.n + row0 + first + r;
       Raw<false>::store(p.q_out + to * Raw<false>::kRowBytes, l, x);
     }
     return;
@@ -423,11 +446,12 @@ __global__ void __launch_bounds__(256, 2) paged_append_rotary_kernel(const __gri
       if (r >= begin && r < end) raw[i].load(rows + (row0 + r) * in.row, l);
     }
   }
-  Weights<false> w;
+  const int octet0 = octet & ~3;
+  auto idle = [&](int i) { return octet0 + 32 * i + 4 <= begin || octet0 + 32 * i >= end; };  // no new row in this warp
   float inv[2] = {};
   auto turned = [&](int i, float (&x)[32]) {  // (rows that are not new are all zeros)
     raw[i].get(x);
-    if (weight) w.apply(x, inv[i]);
+    if (weight) weigh<false>(x, inv[i], weights, l);
     const int r = min(max(octet + 32 * i, begin), end - 1) - begin;
     turn_row<LAYOUT, K, false, true>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
   };
@@ -451,12 +475,12 @@ __global__ void __launch_bounds__(256, 2) paged_append_rotary_kernel(const __gri
     }
     top <<= 16;
   } else {
-    if (weight) w.load(weight, l);
-    fill();
+    fill(weight, begin, end);
     uint32_t bits = 0;
     float most = 0.0f;  // (a maximum leaves out what is not a number)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (idle(i)) continue;
       float x[32];
       if (weight) {
         raw[i].get(x);
@@ -485,6 +509,7 @@ __global__ void __launch_bounds__(256, 2) paged_append_rotary_kernel(const __gri
   const float unit = power2(-e);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    if (idle(i)) continue;
     const int r = octet + 32 * i;
     float x[32];
     if (is_v) raw[i].get(x);
@@ -631,15 +656,19 @@ cudaError_t launch_append_rotary(const AppendParams& a, int widest, int segs, cu
   p.q_out = m.q_out;
   p.positions = m.positions;
   p.q_heads = m.q_heads;
-  p.group = 8;
   int rows = 0;  // the most new rows of a page
   for (int i = 0; i < segs; ++i) rows = std::max(rows, std::min(kPage, a.seg[i].rows));
+  p.group = rows == 1 ? 8 : 16;
+  p.groups = (m.q_heads + p.group - 1) / p.group;
+  p.part_rows = kPage;
+  while (p.part_rows > 8 && static_cast<long long>(widest) * segs * p.groups * (kPage / p.part_rows) < 4ll * num_sms()) p.part_rows /= 2;
+  if (rows == 1) p.part_rows = kPage;
   const int smem = rows * 2 * m.turn.pairs * static_cast<int>(sizeof(float));
   const void* kernel = append_kernel_of(m.kind);
   static std::atomic<uint64_t> seen[kShift + 1][3] = {};
   const cudaError_t e = smem > 48 * 1024 ? allow_smem(kernel, 64 * 1024, seen[m.kind.layout][m.kind.k]) : cudaSuccess;
   void* args[] = {&p};
-  return e == cudaSuccess ? launch_after(kernel, dim3(widest, 2 * a.heads + (m.q_heads + p.group - 1) / p.group, segs), 256, smem, stream, args) : e;
+  return e == cudaSuccess ? launch_after(kernel, dim3(widest, 2 * a.heads + p.groups * (kPage / p.part_rows), segs), 256, smem, stream, args) : e;
 }
 
 }  // namespace
@@ -743,16 +772,19 @@ int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_
   p.n_mul = by_n.mul;
   p.n_shift = by_n.shift;
   for (int i = 0; i < entries; ++i) p.start[i] = start ? start[i] : 0;
-  p.group = 16;
-  p.block_shift = 5;
-  auto groups = [&](int heads) { return (heads + p.group - 1) / p.group; };
-  auto blocks = [&]() { return (p.rows + (1 << p.block_shift) - 1) >> p.block_shift; };
-  while (p.block_shift > 0 && static_cast<long long>(blocks()) * (groups(q_heads) + groups(k_heads)) < 4ll * num_sms()) --p.block_shift;
-  if (p.block_shift == 0) p.group = 8;
-  p.q_groups = groups(q_heads);
+  // A CTA holds all heads of its rows (24 at most), so that angles are worked out once, and as many rows as make
+  // whole waves of CTAs, three to an SM; where there are fewer rows than that, fewer heads, down to 8.
+  const int heads = q_heads + k_heads, room = 3 * num_sms();
+  int groups = (heads + 23) / 24;
+  while (static_cast<long long>(p.rows) * groups * 2 <= room && (heads + 2 * groups - 1) / (2 * groups) >= 8) groups *= 2;
+  p.group = (heads + groups - 1) / groups;
+  groups = (heads + p.group - 1) / p.group;
+  const long long abreast = std::max(room / groups, 1);
+  const long long waves = (p.rows + 32 * abreast - 1) / (32 * abreast);
+  p.block = static_cast<int>((p.rows + waves * abreast - 1) / (waves * abreast));
   void* args[] = {&p};
   IQ_CUDA(launch_after(rotate_kernel_of(kind_of(rotary, size == 4), size == 4),
-                       dim3(blocks(), p.q_groups + groups(k_heads)), 256, static_cast<int>(sizeof(float)) * (2 * p.turn.pairs << p.block_shift),
+                       dim3((p.rows + p.block - 1) / p.block, groups), 256, static_cast<int>(sizeof(float)) * 2 * p.turn.pairs * p.block,
                        static_cast<cudaStream_t>(stream), args));
   launched_outputs(stream, out[0], out[1]);
   return IQ_OK;
