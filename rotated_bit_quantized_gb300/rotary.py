@@ -135,10 +135,13 @@ class IQRotary:
         if E > IQ_MAX_BATCH:
             raise ValueError(f"at most {IQ_MAX_BATCH} entries")
         start = at = None
-        if isinstance(positions, torch.Tensor):
+        if type(positions) is int and -1 << 31 <= positions < 1 << 31:
+            if positions:
+                start = np.full(E, positions, dtype=np.int32)
+        elif isinstance(positions, torch.Tensor):
             positions = _positions(positions, E, n, self._index)
             at = positions.data_ptr()
-        elif not (type(positions) is int and positions == 0):
+        else:
             start = np.asarray(positions)
             if start.dtype.kind not in "iu" or start.ndim > 1 or (start.ndim == 1 and start.shape[0] != E):
                 raise ValueError("positions must be one whole number, one for each entry, or an int32 CUDA tensor")
