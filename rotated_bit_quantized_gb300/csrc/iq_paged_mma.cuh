@@ -47,7 +47,7 @@ struct AttendBase {
   float2* part_ml;  // their references and sums
   uint8_t* cut;     // prefill: [high, low parts][entry][kv head][row][256] e4m3
   float* factors;   // prefill: [entry][kv head][row] 2^e * scale * log2 e
-  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks, entries, cost, total, slots_n;
+  int out_f32, heads, rep, nq, pages, max_pages, causal, window, sinks;
   int stall;                    // test hook (iq_paged_debug_stall): no page is loaded, so the waits for them run out
   float scale;
 };
@@ -55,7 +55,7 @@ struct AttendParams : AttendBase {
   static constexpr bool kTree = false;
   // part_o, part_ml: [2 * grid][unit_rows], a range's first segment, its last
   Cut* cuts;        // [grid] the unit that a range's end cuts
-  int unit_rows;
+  int unit_rows, entries, cost, total, slots_n;
   unsigned rep_mul, rep_shift;  // division by rep, see query_of
   // per entry that has queries and keys: its place in the call, its slot, what the slot holds,
   // its queries; cum: slots before it (all heads), per: slots of one of its heads
@@ -93,6 +93,12 @@ __host__ __device__ inline int range_of(int tile, int grid, int total) {
   return static_cast<int>((static_cast<long long>(tile + 1) * grid - 1) / total);
 }
 
+// What the CTAs of a launch, or some of them, share: `count` entries from `first` on,
+// whose slots are cut into `grid` ranges; this CTA's is number `block`.
+struct Work {
+  int first, count, cost, total, block, grid;
+};
+
 // A place in the slots of all units: entry, head, row tile, slot j of the unit.
 struct Place {
   int e, h, z, j;
@@ -103,17 +109,23 @@ struct Place {
 // queries, and its units are (node, kv head, 128 of these rows).  Every unit leaves
 // partial results, at its rows' place, and in ranges behind its first in these ranges';
 // those of the nodes that a slot is under are joined.
+// Leaves of few rows are units of the split kernel's shape: one launch holds CTAs of
+// both kinds, `wide` ranges of the nodes before `leaves`, and `narrow` of those from there on.
 constexpr int kInner = 64, kNodes = IQ_MAX_BATCH + kInner, kDepth = 4;  // inner nodes of a call, all; nodes above one another
 constexpr int kUnitRows = 128;
 struct TreeParams : AttendBase {
   static constexpr bool kTree = true;
-  const int4* place;     // [rows] the lowest node that a row is under (< 0: none), its position, its place in q and out
-  int rows, cont;        // rows of one kv head; where the ranges' partial results begin
-  short slot[kNodes];    // that holds the node's pages
-  short parent[kNodes];  // < 0: none
-  int end_page[kNodes];  // the slot's last page
+  int rows;                       // of one kv head
+  int nodes, leaves, wide, narrow, wide_cost, narrow_cost, wide_total, narrow_total;
+  int wide_cont, narrow_cont, narrow_rows;  // where the ranges' partial results begin; rows of a narrow range's
+  unsigned rep_mul, rep_shift;    // division by rep, see query_of
+  const int* pos;                 // [rows] the position of a row
+  short slot[kNodes];             // that holds the node's pages
+  short parent[kNodes];           // < 0: none
+  short entry[kNodes];            // of a leaf: its place in the call
+  int end_page[kNodes];           // the slot's last page
   int row0[kNodes], n[kNodes], part0[kNodes];  // its first row, how many, their place in the partial results
-  int cum[kNodes + 1];   // slots before it
+  int cum[kNodes];                // slots before it, of its kind
   int tiles[kNodes], base[kNodes], sink_tiles[kNodes], skip[kNodes], p_lo[kNodes], p_hi[kNodes];  // of its units, see Tiles
 };
 
@@ -122,14 +134,15 @@ struct TreeParams : AttendBase {
 struct Part {
   int begin, n;
 };
-__device__ __forceinline__ Part part_of(const AttendBase& p, const Place& w, int tiles, int left) {
-  const int begin = max(w.j - p.cost, 0), end = min(max(w.j + left - p.cost, 0), tiles);
+__device__ __forceinline__ Part part_of(const Work& work, const Place& w, int tiles, int left) {
+  const int begin = max(w.j - work.cost, 0), end = min(max(w.j + left - work.cost, 0), tiles);
   return {begin, end - begin};
 }
 // floor(r / rep) for r < 2^31: a shift where rep is a power of two; else, with s =
 // floor(log2 rep) and mul = ceil(2^(32+s) / rep) < 2^32, umulhi(r, mul) >> s (its
 // error is below r / 2^(32+s) < 1 / rep).
-__device__ __forceinline__ int query_of(const AttendParams& p, int r) {
+template <class P>
+__device__ __forceinline__ int query_of(const P& p, int r) {
   return static_cast<int>((p.rep_mul ? __umulhi(static_cast<unsigned>(r), p.rep_mul) : static_cast<unsigned>(r)) >> p.rep_shift);
 }
 __device__ __forceinline__ Tiles tiles_at(const AttendParams& p, const Place& w) {
@@ -151,14 +164,14 @@ __device__ __forceinline__ int cut_row(const AttendParams& p, const Place& w) {
 __device__ __forceinline__ int cut_row(const TreeParams& p, const Place& w) { return w.h * p.rows + p.row0[w.e] + w.z * kUnitRows; }
 // For the joining kernel: the unit at w, whose first slot in the range is `at`,
 // of which the range takes all tiles from the first on, but not all.
-__device__ __forceinline__ void tell_cut(const AttendParams& p, const Place& w, int at, int tiles, int slot) {
-  const int end = at - w.j + p.cost + tiles - 1;  // the unit's last slot
-  p.cuts[blockIdx.x] = {range_of(end, gridDim.x, p.total), slot, w.e, w.h, w.z, {0, 0, 0}};
+__device__ __forceinline__ void tell_cut(const AttendParams& p, const Work& work, const Place& w, int at, int tiles, int slot) {
+  const int end = at - w.j + work.cost + tiles - 1;  // the unit's last slot
+  p.cuts[work.block] = {range_of(end, work.grid, work.total), slot, w.e, w.h, w.z, {0, 0, 0}};
 }
 // Of slot t (a whole warp calls it together).
-__device__ inline Place place_of(const AttendParams& p, int t) {
+__device__ inline Place place_of(const AttendParams& p, const Work& work, int t) {
   Place w;
-  int hi = p.entries - 1;
+  int hi = work.count - 1;
   w.e = 0;
   while (w.e < hi) {
     const int mid = (w.e + hi + 1) / 2;
@@ -175,7 +188,7 @@ __device__ inline Place place_of(const AttendParams& p, int t) {
   for (int z0 = 0;; z0 += 32) {  // 32 row tiles at a time, their slots summed up
     const int z = z0 + lane;
     int sum = 0;
-    if (z < units) sum = tiles_at(p, {w.e, w.h, z, 0}).n + p.cost;
+    if (z < units) sum = tiles_at(p, {w.e, w.h, z, 0}).n + work.cost;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
@@ -193,17 +206,17 @@ __device__ inline Place place_of(const AttendParams& p, int t) {
     if (z0 + 32 >= units) return w;  // not reached: t is a slot of this head
   }
 }
-__device__ inline Place place_of(const TreeParams& p, int t) {
+__device__ inline Place place_of(const TreeParams& p, const Work& work, int t) {
   Place w;
-  int hi = p.entries - 1;
-  w.e = 0;
+  int hi = work.first + work.count - 1;
+  w.e = work.first;
   while (w.e < hi) {
     const int mid = (w.e + hi + 1) / 2;
     if (p.cum[mid] <= t) w.e = mid;
     else hi = mid - 1;
   }
   t -= p.cum[w.e];
-  const int per = p.tiles[w.e] + p.cost, units = (p.n[w.e] + kUnitRows - 1) / kUnitRows, u = t / per;
+  const int per = p.tiles[w.e] + work.cost, units = (p.n[w.e] + kUnitRows - 1) / kUnitRows, u = t / per;
   w.j = t - u * per;
   w.h = u / units;
   w.z = u - w.h * units;
@@ -226,15 +239,15 @@ __device__ __forceinline__ void next_unit(const TreeParams& p, Place& w) {
   w.h = 0;
   ++w.e;
 }
-// The index of row r of an entry and kv head among the rows [entry][query head][query] of q and out.
-__device__ __forceinline__ long long row_index(const AttendParams& p, const Place& w, int r) {
+// The index of row r of an entry (a leaf) and kv head among the rows [entry][query head][query] of q and out.
+template <class P>
+__device__ __forceinline__ long long row_index(const P& p, const Place& w, int r) {
   const int j = query_of(p, r);
   return static_cast<long long>((p.entry[w.e] * p.heads + w.h) * p.rep + r - j * p.rep) * p.nq + j;
 }
 
 // counts: of every entry of the call, also those without keys
 cudaError_t launch_prefill(const AttendParams& p, const int* counts, int grid, cudaStream_t stream);
-cudaError_t launch_tree(const TreeParams& p, int grid, cudaStream_t stream);  // (its queries are cut already)
 // zeros for the queries of empty slots
 int store_zeros(const iq_paged* c, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots, void* out,
                 int out_f32, iq_stream_t stream);
@@ -374,6 +387,7 @@ struct Loader {
     int begin, n, end_page, h;
   };
   const P& p;
+  const Work& work;
   uint8_t* smem;
   uint64_t *full, *empty;
   float4* scales;      // [kRing] keys' scales of the tile's two pages, values'
@@ -385,13 +399,13 @@ struct Loader {
     Segment g{};
     if (at >= last) return g;
     g.tiles = tiles_at(p, w);
-    const Part part = part_of(p, w, g.tiles.n, last - at);
+    const Part part = part_of(work, w, g.tiles.n, last - at);
     g.begin = part.begin;
     g.n = part.n;
     g.row = p.table + static_cast<long long>(p.slot[w.e]) * p.max_pages;
     g.end_page = last_page(p, w.e);
     g.h = w.h;
-    at += g.tiles.n + p.cost - w.j;
+    at += g.tiles.n + work.cost - w.j;
     next_unit(p, w);
     return g;
   }

@@ -5,14 +5,16 @@
 // hold are multiplied once, with the rows of all of them side by side, and each slot's
 // own pages apart, and the partial results are joined.  What is shared is found on the
 // host, from the page ids of the table: a tree whose nodes are runs of pages that a
-// group of slots holds and others do not.  The products run in the prefill kernel
-// (iq_paged_prefill.cu), whose M dimension the rows of many slots fill.
+// group of slots holds and others do not.  One launch has CTAs of two kinds: nodes of many
+// rows as in the prefill kernel (iq_paged_rows.cuh), whose M dimension the rows of many
+// slots fill; what a slot holds alone as in the split kernel (iq_paged_split.cuh).
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstring>
 
-#include "iq_paged_mma.cuh"
+#include "iq_paged_rows.cuh"
+#include "iq_paged_split.cuh"
 #include "iq_pages.cuh"
 
 namespace iq {
@@ -25,12 +27,22 @@ struct TreeCutParams {
   const uint16_t* q;
   uint8_t* cut;
   float* factors;
-  int4* place;
+  int* pos;
   int heads, rep, nq, rows, entries, causal;
   float scale;
-  short entry[IQ_MAX_BATCH], lowest[IQ_MAX_BATCH];  // place in the call, lowest node
-  int row0[IQ_MAX_BATCH + 1], pos0[IQ_MAX_BATCH];   // first row, first query's position
+  short entry[IQ_MAX_BATCH];                       // place in the call
+  int row0[IQ_MAX_BATCH + 1], pos0[IQ_MAX_BATCH];  // first row, first query's position
 };
+// Which of n entries a row is of.
+__device__ __forceinline__ int entry_of(const int* row0, int n, int row) {
+  int s = 0, hi = n - 1;
+  while (s < hi) {
+    const int mid = (s + hi + 1) / 2;
+    if (row0[mid] <= row) s = mid;
+    else hi = mid - 1;
+  }
+  return s;
+}
 
 // Every row of (entry, kv head): two e4m3 parts, the factor of its scores, and where it
 // stands; a warp takes four.
@@ -41,16 +53,10 @@ __global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_consta
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int row = min(w0 + k, p.rows - 1);
-    int s = 0, hi = p.entries - 1;
-    while (s < hi) {
-      const int mid = (s + hi + 1) / 2;
-      if (p.row0[mid] <= row) s = mid;
-      else hi = mid - 1;
-    }
-    const int x = row - p.row0[s], j = x / p.rep;
+    const int s = entry_of(p.row0, p.entries, row), x = row - p.row0[s], j = x / p.rep;
     const int at = (p.entry[s] * p.heads * p.rep + x - j * p.rep) * p.nq + j;  // of kv head 0
     raw[k] = __ldcs(reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(h) * p.rep * p.nq + at) * kHeadDim) + lane);
-    if (h == 0 && lane == 0 && w0 + k < p.rows) p.place[row] = make_int4(p.lowest[s], p.pos0[s] + (p.causal ? j : 0), at, 0);
+    if (h == 0 && lane == 0 && w0 + k < p.rows) p.pos[row] = p.pos0[s] + (p.causal ? j : 0);
   }
   if (p.scale < 0.0f) {  // the factors are positive, so that the largest product is the largest score
 #pragma unroll
@@ -69,54 +75,94 @@ __global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_consta
   }
 }
 
+// ------------------------------------------------------------------ products
+
+// CTAs of both kinds, so that neither waits for the other's end.
+template <int NR>
+__global__ void __launch_bounds__(rows::kThreads, 1) paged_tree_kernel(const __grid_constant__ TreeParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled operands need it; no room to align by hand
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < p.wide) rows::run(p, {0, p.leaves, p.wide_cost, p.wide_total, block, p.wide}, smem);
+  else split::run<NR>(p, {p.leaves, p.nodes - p.leaves, p.narrow_cost, p.narrow_total, block - p.wide, p.narrow}, smem);
+}
+template <int NR>
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
+  constexpr int kSmem = rows::kTreeSmem > split::Shape<NR>::kSmem ? rows::kTreeSmem : split::Shape<NR>::kSmem;
+  static_assert(split::Shape<NR>::kThreads <= rows::kThreads, "threads of one CTA");
+  static std::atomic<uint64_t> seen{0};
+  const void* kernel = reinterpret_cast<const void*>(&paged_tree_kernel<NR>);
+  const cudaError_t e = allow_smem(kernel, kSmem, seen);
+  void* args[] = {const_cast<TreeParams*>(&p)};
+  return e == cudaSuccess ? launch_after(kernel, dim3(p.wide + p.narrow), rows::kThreads, kSmem, stream, args) : e;
+}
+
 // ------------------------------------------------------------------ join
 
 // The partial results of row `row` of kv head h at node e: the first, and those of the
 // ranges behind.
 struct Partials {
-  int first, next, n;
-  __device__ __forceinline__ Partials(const TreeParams& p, int grid, int e, int h, int row) {
-    const int x = row - p.row0[e], z = x / kUnitRows, units = (p.n[e] + kUnitRows - 1) / kUnitRows, per = p.tiles[e] + p.cost;
-    const int begin = p.cum[e] + (h * units + z) * per;
-    const int g0 = range_of(begin + p.cost, grid, p.total), g1 = range_of(begin + per - 1, grid, p.total);
+  int first, next, step, n;
+  __device__ __forceinline__ Partials(const TreeParams& p, int e, int h, int row) {
+    const bool narrow = e >= p.leaves;
+    const int x = row - p.row0[e], z = x / kUnitRows, units = (p.n[e] + kUnitRows - 1) / kUnitRows;  // (a leaf's: one)
+    const int cost = narrow ? p.narrow_cost : p.wide_cost, grid = narrow ? p.narrow : p.wide, total = narrow ? p.narrow_total : p.wide_total;
+    const int per = p.tiles[e] + cost, begin = p.cum[e] + (h * units + z) * per;
+    const int g0 = range_of(begin + cost, grid, total), g1 = range_of(begin + per - 1, grid, total);
     first = p.part0[e] + h * p.n[e] + x;
-    next = p.cont + g0 * kUnitRows + x - z * kUnitRows;
+    step = narrow ? p.narrow_rows : kUnitRows;
+    next = (narrow ? p.narrow_cont : p.wide_cont) + g0 * step + x - z * kUnitRows;
     n = 1 + g1 - g0;
   }
-  __device__ __forceinline__ int row(int k) const { return k == 0 ? first : next + k * kUnitRows; }
+  __device__ __forceinline__ int row(int k) const { return k == 0 ? first : next + k * step; }
+};
+
+struct JoinPlan {
+  int entries, each;  // rows of a CTA
+  short entry[IQ_MAX_BATCH], lowest[IQ_MAX_BATCH];  // place in the call, lowest node
+  int row0[IQ_MAX_BATCH];
 };
 
 // CTA (x, h) joins `each` rows of kv head h, 8 / each warps a row, a lane per 8 dims,
-// in the order of nodes and ranges.
-__global__ void __launch_bounds__(256) paged_tree_join_kernel(const __grid_constant__ TreeParams p, int grid, int each) {
+// in the order of nodes and ranges: four partial results at a time, their references
+// and sums with them, so that a row takes one trip to memory or few.
+__global__ void __launch_bounds__(256) paged_tree_join_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ JoinPlan plan) {
   wait_for_last_kernel();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = 8 / each, h = blockIdx.y;
-  const int row = blockIdx.x * each + warp / share;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = 8 / plan.each, h = blockIdx.y;
+  const int row = blockIdx.x * plan.each + warp / share;
   const bool live = row < p.rows;
   __shared__ float part[8][kHeadDim + 2];
   float m = kUnset, sum = 0.0f, o[8] = {};
-  int4 at = make_int4(-1, 0, 0, 0);
+  const int s = entry_of(plan.row0, plan.entries, row);
   if (live) {
-    at = __ldcg(p.place + row);
-    for (int e = at.x; e >= 0; e = p.parent[e]) {
-      const Partials parts(p, grid, e, h, row);
-      for (int k = lane; k < parts.n; k += 32) m = fmaxf(m, __ldcg(&p.part_ml[parts.row(k)]).x);  // every lane a partial
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     int turn = warp % share;  // of this warp's next partial
-    for (int e = at.x; e >= 0; e = p.parent[e]) {
-      const Partials parts(p, grid, e, h, row);
-#pragma unroll 4
-      for (int k = turn; k < parts.n; k += share) {
-        const long long i = parts.row(k);
-        const float2 ml = __ldcg(&p.part_ml[i]);
-        const float4* v = reinterpret_cast<const float4*>(p.part_o + i * kHeadDim + lane * 8);
-        const float4 v0 = __ldcg(v), v1 = __ldcg(v + 1);
-        const float f = ex2_approx(ml.x - m);
-        sum = fmaf(f, ml.y, sum);
-        o[0] = fmaf(f, v0.x, o[0]), o[1] = fmaf(f, v0.y, o[1]), o[2] = fmaf(f, v0.z, o[2]), o[3] = fmaf(f, v0.w, o[3]);
-        o[4] = fmaf(f, v1.x, o[4]), o[5] = fmaf(f, v1.y, o[5]), o[6] = fmaf(f, v1.z, o[6]), o[7] = fmaf(f, v1.w, o[7]);
+    for (int e = plan.lowest[s]; e >= 0; e = p.parent[e]) {
+      const Partials parts(p, e, h, row);
+      for (int k = turn; k < parts.n; k += 4 * share) {
+        float2 ml[4];
+        float4 v[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ml[i] = make_float2(kUnset, 0.0f);
+          v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k + i * share >= parts.n) continue;
+          const long long at = parts.row(k + i * share);
+          const float4* from = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 8);
+          ml[i] = __ldcg(&p.part_ml[at]);
+          v[i][0] = __ldcg(from);
+          v[i][1] = __ldcg(from + 1);
+        }
+        const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m), old = ex2_approx(m - top);
+        m = top;
+        sum *= old;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[d] *= old;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = ex2_approx(ml[i].x - m);
+          sum = fmaf(f, ml[i].y, sum);
+          o[0] = fmaf(f, v[i][0].x, o[0]), o[1] = fmaf(f, v[i][0].y, o[1]), o[2] = fmaf(f, v[i][0].z, o[2]), o[3] = fmaf(f, v[i][0].w, o[3]);
+          o[4] = fmaf(f, v[i][1].x, o[4]), o[5] = fmaf(f, v[i][1].y, o[5]), o[6] = fmaf(f, v[i][1].z, o[6]), o[7] = fmaf(f, v[i][1].w, o[7]);
+        }
       }
       turn = (turn + share - parts.n % share) % share;
     }
@@ -124,25 +170,45 @@ __global__ void __launch_bounds__(256) paged_tree_join_kernel(const __grid_const
   if (share > 1) {
 #pragma unroll
     for (int d = 0; d < 8; ++d) part[warp][d * 32 + lane] = o[d];
-    if (lane == 0) part[warp][kHeadDim] = sum;
+    if (lane == 0) {
+      part[warp][kHeadDim] = sum;
+      part[warp][kHeadDim + 1] = m;
+    }
     __syncthreads();
     if (warp % share) return;
-    for (int w = warp + 1; w < warp + share; ++w) {
+    for (int w = warp + 1; w < warp + share; ++w) m = fmaxf(m, part[w][kHeadDim + 1]);
+    const float own = ex2_approx(part[warp][kHeadDim + 1] - m);
+    sum *= own;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) o[d] += part[w][d * 32 + lane];
-      sum += part[w][kHeadDim];
+    for (int d = 0; d < 8; ++d) o[d] *= own;
+    for (int w = warp + 1; w < warp + share; ++w) {
+      const float f = ex2_approx(part[w][kHeadDim + 1] - m);
+      sum = fmaf(f, part[w][kHeadDim], sum);
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] = fmaf(f, part[w][d * 32 + lane], o[d]);
     }
   }
   if (!live) return;
-  const long long to = static_cast<long long>(h) * p.rep * p.nq + at.z;
+  const int x = row - plan.row0[s], j = x / p.rep;
+  const long long to = (static_cast<long long>(plan.entry[s]) * p.heads * p.rep + h * p.rep + x - j * p.rep) * p.nq + j;
   store_out8(p.out, p.out_f32, to * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
 }
 
 // ------------------------------------------------------------------ what is shared
 
 // A unit's beginning and end take about as long as so many tiles.
+#ifndef XCA
+#define XCA 4
+#endif
+#ifndef XCB
+#define XCB 4
+#endif
+#ifndef XTB
+#define XTB 1.0
+#endif
 constexpr int kUnitCost = 4;
-constexpr int kRangeCost = 2;  // and so many where the ranges are cut, see unit_cost
+constexpr int kWideCost = XCA, kNarrowCost = XCB;
+constexpr double kNarrowTile = XTB;  // a tile's time there, of a tile's of many rows
 
 struct Planner {
   int rep, window, sinks, inner = 0;
@@ -154,7 +220,8 @@ struct Planner {
   } e[IQ_MAX_BATCH];
   // a node before the order of the entries, and with it of the rows, is known
   struct Node {
-    int first, last, start, stop, parent;  // entries [first, last), tiles [start, stop)
+    int first, last, parent;  // entries [first, last)
+    bool leaf;
     Tiles tiles;
   } node[kNodes];
   int nodes = 0;
@@ -182,8 +249,8 @@ struct Planner {
     for (int i = a; i < b; ++i) rows += static_cast<long long>(e[i].count) * rep;
     return static_cast<int>((rows + kUnitRows - 1) / kUnitRows);
   }
-  int add(int a, int b, int start, int stop, int parent, const Tiles& t) {
-    node[nodes] = {a, b, start, stop, parent, t};
+  int add(int a, int b, int parent, bool leaf, const Tiles& t) {
+    node[nodes] = {a, b, parent, leaf, t};
     return nodes++;
   }
   // Entries [a, b) hold the same first `page` pages; tiles before `start` are those of `parent` and above.
@@ -198,7 +265,7 @@ struct Planner {
         while (y < b && e[y].pages > page && e[y].row[page] == e[x].row[page]) ++y;
       if (y - x == 1) {  // a leaf
         const Tiles t = seen(x, y, start, (e[x].pages + 1) / 2);
-        e[x].lowest = t.n > 0 ? add(x, y, start, 0, parent, t) : parent;
+        e[x].lowest = t.n > 0 ? add(x, y, parent, true, t) : parent;
         continue;
       }
       int common = e[x].pages, most = e[x].pages;
@@ -215,7 +282,7 @@ struct Planner {
       int under = parent;
       if (once) {
         ++inner;
-        under = add(x, y, start, stop, parent, t);
+        under = add(x, y, parent, false, t);
       }
       split(x, y, common, once ? stop : start, under, depth + (once ? 1 : 0));
     }
@@ -225,7 +292,7 @@ struct Planner {
 // The rows of all nodes of one kv head are at most kDepth times the call's.
 size_t tree_bytes(size_t rows, size_t heads) {
   const size_t parts = kDepth * heads * rows + static_cast<size_t>(num_sms()) * kUnitRows;
-  return parts * (kHeadDim * sizeof(float) + sizeof(float2)) + rows * sizeof(int4) + heads * rows * (2 * kHeadDim + sizeof(float));
+  return parts * (kHeadDim * sizeof(float) + sizeof(float2)) + rows * sizeof(int) + heads * rows * (2 * kHeadDim + sizeof(float));
 }
 // Where pages are shared among slots of more rows, their own products fill the tensor cores already.
 bool tree_rows(const iq_paged* c, int q_heads, int n_queries, int n_slots) {
@@ -270,19 +337,34 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   std::memset(&p, 0, sizeof(p));
   TreeCutParams cut;
   std::memset(&cut, 0, sizeof(cut));
+  JoinPlan join;
+  std::memset(&join, 0, sizeof(join));
+  // leaves of at most 32 rows, as the split kernel's calls, behind the other nodes
+  const int leaf_rows = t.rep * n_queries;
+  const bool apart = leaf_rows <= 32;
+  short number[kNodes];
+  for (int wanted = 0; wanted < 2; ++wanted)
+    for (int k = 0; k < t.nodes; ++k) {
+      if ((t.node[k].leaf && apart) != (wanted == 1)) continue;
+      number[k] = static_cast<short>(p.nodes++);
+      p.leaves += wanted == 0;
+    }
   for (int i = 0; i < t.n; ++i) {
-    cut.entry[i] = static_cast<short>(t.e[i].place);
-    cut.lowest[i] = static_cast<short>(t.e[i].lowest);
+    cut.entry[i] = join.entry[i] = static_cast<short>(t.e[i].place);
+    join.lowest[i] = static_cast<short>(t.e[i].lowest < 0 ? -1 : number[t.e[i].lowest]);
     cut.pos0[i] = t.e[i].p_lo;
+    join.row0[i] = cut.row0[i];
     cut.row0[i + 1] = cut.row0[i] + t.e[i].count * t.rep;
   }
   p.rows = cut.row0[t.n];
-  long long tiles = 0, parts = 0;
-  for (int k = 0; k < t.nodes; ++k) {
-    const Planner::Node& a = t.node[k];
+  long long tiles[2] = {}, units[2] = {}, parts = 0;  // of many rows, of few
+  for (int i = 0; i < t.nodes; ++i) {
+    const Planner::Node& a = t.node[i];
     const Planner::Entry& holder = t.e[a.first];
+    const int k = number[i], kind = k >= p.leaves;
     p.slot[k] = static_cast<short>(holder.slot);
-    p.parent[k] = static_cast<short>(a.parent);
+    p.entry[k] = static_cast<short>(holder.place);
+    p.parent[k] = static_cast<short>(a.parent < 0 ? -1 : number[a.parent]);
     p.end_page[k] = holder.pages - 1;
     p.row0[k] = cut.row0[a.first];
     p.n[k] = cut.row0[a.last] - p.row0[k];
@@ -294,28 +376,41 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
     p.p_lo[k] = a.tiles.p_lo;
     p.p_hi[k] = a.tiles.p_hi;
     parts += static_cast<long long>(heads) * p.n[k];
-    tiles += static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows) * a.tiles.n;
+    const long long u = static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows);
+    units[kind] += u;
+    tiles[kind] += u * a.tiles.n;
   }
-  const int grid = static_cast<int>(std::min<long long>(num_sms(), tiles));
-  p.entries = t.nodes;
-  p.cost = tiles >= 8ll * grid ? kRangeCost : 0;
-  long long total = 0;
-  for (int k = 0; k < t.nodes; ++k) {
-    p.cum[k] = static_cast<int>(total);
-    total += static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows) * (p.tiles[k] + p.cost);
-    if (total >= (1LL << 31)) return IQ_OK;
+  // the SMs go to the two kinds by what each has to do
+  const double wide = static_cast<double>(tiles[0] + units[0] * kWideCost), narrow = kNarrowTile * (tiles[1] + units[1] * kNarrowCost);
+  const int sms = num_sms();
+  p.narrow = tiles[1] == 0 ? 0 : std::min(std::max(static_cast<int>(sms * narrow / (wide + narrow) + 0.5), 1), sms - 1);
+  p.wide = static_cast<int>(std::min<long long>(sms - p.narrow, tiles[0]));
+  p.narrow = static_cast<int>(std::min<long long>(p.narrow, tiles[1]));
+  // where ranges are shorter than units, these are cut at a tile's grain
+  p.wide_cost = tiles[0] >= 8ll * p.wide || units[0] >= p.wide ? kWideCost : 0;
+  p.narrow_cost = tiles[1] >= 8ll * p.narrow || units[1] >= p.narrow ? kNarrowCost : 0;
+  long long total[2] = {};
+  for (int k = 0; k < p.nodes; ++k) {
+    const int kind = k >= p.leaves;
+    p.cum[k] = static_cast<int>(total[kind]);
+    total[kind] += static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows) * (p.tiles[k] + (kind ? p.narrow_cost : p.wide_cost));
+    if (total[kind] >= (1LL << 31)) return IQ_OK;
   }
-  p.cum[t.nodes] = p.total = static_cast<int>(total);
-  p.cont = static_cast<int>(parts);
-  parts += static_cast<long long>(grid) * kUnitRows;
+  p.wide_total = static_cast<int>(total[0]);
+  p.narrow_total = static_cast<int>(total[1]);
+  p.narrow_rows = leaf_rows <= 8 ? 8 : leaf_rows <= 16 ? 16 : 32;
+  p.wide_cont = static_cast<int>(parts);
+  parts += static_cast<long long>(p.wide) * kUnitRows;
+  p.narrow_cont = static_cast<int>(parts);
+  parts += static_cast<long long>(p.narrow) * p.narrow_rows;
 
   const long long pool_rows = static_cast<long long>(c->pages) * heads * kPage, cut_rows = static_cast<long long>(heads) * p.rows;
   p.part_o = static_cast<float*>(workspace);
   p.cut = reinterpret_cast<uint8_t*>(p.part_o + parts * kHeadDim);
-  cut.place = reinterpret_cast<int4*>(p.cut + cut_rows * 2 * kHeadDim);
-  p.place = cut.place;
-  p.part_ml = reinterpret_cast<float2*>(cut.place + p.rows);
+  p.part_ml = reinterpret_cast<float2*>(p.cut + cut_rows * 2 * kHeadDim);
   p.factors = reinterpret_cast<float*>(p.part_ml + parts);
+  cut.pos = reinterpret_cast<int*>(p.factors + cut_rows);
+  p.pos = cut.pos;
   if (!code_map(&p.k_map, c->k_codes, pool_rows) || !code_map(&p.v_map, c->v_codes, pool_rows) ||
       !code_map(&p.q_map, p.cut, 2 * cut_rows, kUnitRows))
     return fail(IQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -323,11 +418,16 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   p.v_scales = c->v_scales;
   p.table = c->table;
   p.status = c->status;
+  p.q = static_cast<const uint16_t*>(q);
   p.out = out;
   p.out_f32 = out_f32;
+  p.causal = causal;
+  p.scale = scale;
   p.heads = cut.heads = heads;
   p.rep = cut.rep = t.rep;
   p.nq = cut.nq = n_queries;
+  while ((2 << p.rep_shift) <= t.rep) ++p.rep_shift;
+  if (t.rep & (t.rep - 1)) p.rep_mul = static_cast<unsigned>(((1ull << (32 + p.rep_shift)) + t.rep - 1) / t.rep);
   p.pages = c->pages;
   p.max_pages = c->max_pages;
   p.window = window;
@@ -346,11 +446,12 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   if (st != IQ_OK) return st;
   void* cut_args[] = {&cut};
   cudaError_t err = launch_after(reinterpret_cast<const void*>(&paged_tree_cut_kernel), dim3((p.rows + 31) / 32, heads), 256, 0, cs, cut_args);
-  if (err == cudaSuccess) err = launch_tree(p, grid, cs);
+  if (err == cudaSuccess) err = p.narrow_rows == 8 ? launch_tree<8>(p, cs) : p.narrow_rows == 16 ? launch_tree<16>(p, cs) : launch_tree<32>(p, cs);
   if (err == cudaSuccess) {
-    int ranges = grid, each = cut_rows >= 4096 ? 8 : 1;
-    void* args[] = {&p, &ranges, &each};
-    err = launch_after(reinterpret_cast<const void*>(&paged_tree_join_kernel), dim3((p.rows + each - 1) / each, heads), 256, 0, cs, args);
+    join.entries = t.n;
+    join.each = cut_rows >= 4096 ? 8 : 1;
+    void* args[] = {&p, &join};
+    err = launch_after(reinterpret_cast<const void*>(&paged_tree_join_kernel), dim3((p.rows + join.each - 1) / join.each, heads), 256, 0, cs, args);
   }
   if (err != cudaSuccess) return cuda_fail(err, "paged attention of shared pages");
   launched_outputs(stream, {out, static_cast<size_t>(n_slots) * q_heads * n_queries * kHeadDim * (out_f32 ? 4 : 2)});
