@@ -189,31 +189,30 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
             __syncwarp();
           }
         }
-        if (r < rows && group == 0) p.part_ml[done_row + r] = make_float2(done_ref, sum);
-        return;
-      }
-      // A thread stores its row in 32-byte pieces.  Slower, for 8191 queries under
-      // a window of 1023 in 190 us: four lanes' pieces side by side through shuffles
-      // (201), through shared memory and a warp that stores whole rows (213), kept as
-      // bf16 and stored an eighth per tile (224, spills).
+      } else {
+        // A thread stores its row in 32-byte pieces.  Slower, for 8191 queries under
+        // a window of 1023 in 190 us: four lanes' pieces side by side through shuffles
+        // (201), through shared memory and a warp that stores whole rows (213), kept as
+        // bf16 and stored an eighth per tile (224, spills).
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        float o[32];
-        tmem_ld<32>(t_o + lanes + group * 128 + c, o);
-        ld_wait();
-        if (r >= rows) continue;
-        if (wide) {
+        for (int c = 0; c < 128; c += 32) {
+          float o[32];
+          tmem_ld<32>(t_o + lanes + group * 128 + c, o);
+          ld_wait();
+          if (r >= rows) continue;
+          if (wide) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(out + (c + i) * 4) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-        } else {
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(out + (c + i) * 4) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t x[4];
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[k]) : "f"(o[i + 2 * k + 1] * inv), "f"(o[i + 2 * k] * inv));
-            *reinterpret_cast<uint4*>(out + (c + i) * 2) = make_uint4(x[0], x[1], x[2], x[3]);
+              for (int k = 0; k < 4; ++k)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[k]) : "f"(o[i + 2 * k + 1] * inv), "f"(o[i + 2 * k] * inv));
+              *reinterpret_cast<uint4*>(out + (c + i) * 2) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
           }
         }
       }
@@ -227,6 +226,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
       return __ldcg(p.factors + cut_row(p, u) + r);
     };
     if constexpr (P::kTree) wait_only();
+    bool at_first = true;
     Place w = start;
     float next_factor = first < last ? factor_of(w) : 0.0f;
     for (int at = first;; next_unit(p, w)) {
@@ -266,11 +266,16 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         next_unit(p, after);
         next_factor = factor_of(after);
       }
+      // A tree's units are short, and its first tile's instructions, some 40 KB, come from a
+      // cache level that all of the GPU's first loads keep busy: one turn without
+      // effect, while those are under way, fetches them.
+      bool rehearsal = P::kTree && at_first;
+      at_first = false;
       int j = 0;
       do {
         const int b = it & 1;
         if (n > 0) {
-          await(&scales_in[it % kRing], it / kRing);
+          if (!rehearsal) await(&scales_in[it % kRing], it / kRing);
           const float* sc = reinterpret_cast<const float*>(&scales[it % kRing]) + group;  // this thread's page
           float f = fminf(fmaxf(fq * sc[0], 2e-38f), 3e38f);  // (above 0: a hidden key's score stays below all)
           const float ev = static_cast<float>(exponent_of(sc[2]));
@@ -279,30 +284,51 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
           const bool masked = t0 + kTile > (causal ? tiles.p_lo + 1 : len) ||
                               (p.window > 0 && t0 <= tiles.p_hi - p.window && t0 + kTile > p.sinks);
           const uint32_t t_s = tmem + lanes + b * 128 + group * 64;
-          await(&s_full[b], it / 2);
+          if (!rehearsal) await(&s_full[b], it / 2);
           tc_after();
-          float s[64];
-          tmem_ld<32>(t_s, s);
-          tmem_ld<32>(t_s + 32, s + 32);
-          ld_wait();
+          // keys that this thread's row sees, of its 64
+          unsigned long long see = ~0ull;
           if (masked) {
             const int tb = t0 + group * 64;
             auto below = [&](int x) { return x <= tb ? 0ull : x - tb >= 64 ? ~0ull : (1ull << (x - tb)) - 1; };  // keys before x
-            const unsigned long long see = below(stop) & (~below(low) | below(p.sinks));
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (!(static_cast<uint32_t>(see >> (i & 32)) & 1u << (i & 31))) s[i] = kNothing;
+            see = below(stop) & (~below(low) | below(p.sinks));
           }
-          float m0 = s[0], m1 = s[32];
+          float s[P::kTree ? 32 : 64], m0, m1;
+          if constexpr (P::kTree) {
+            m0 = m1 = kNothing;
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              float part[16], m = kNothing;
+              tmem_ld<16>(t_s + 16 * x, part);
+              ld_wait();
+              const uint32_t bits = static_cast<uint32_t>(see >> (16 * x));
 #pragma unroll
-          for (int i = 1; i < 31; i += 2) {
-            m0 = fmaxf(fmaxf(m0, s[i]), s[i + 1]);
-            m1 = fmaxf(fmaxf(m1, s[32 + i]), s[33 + i]);
+              for (int i = 0; i < 16; ++i) m = fmaxf(m, bits >> i & 1 ? part[i] : kNothing);
+              if (x < 2) m0 = fmaxf(m0, m);
+              else m1 = fmaxf(m1, m);
+            }
+            m0 = __fmul_rn(m0, f);
+            m1 = __fmul_rn(m1, f);
+          } else {
+            tmem_ld<32>(t_s, s);
+            tmem_ld<32>(t_s + 32, s + 32);
+            ld_wait();
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (!(static_cast<uint32_t>(see >> (i & 32)) & 1u << (i & 31))) s[i] = kNothing;
+            }
+            m0 = s[0], m1 = s[32];
+#pragma unroll
+            for (int i = 1; i < 31; i += 2) {
+              m0 = fmaxf(fmaxf(m0, s[i]), s[i + 1]);
+              m1 = fmaxf(fmaxf(m1, s[32 + i]), s[33 + i]);
+            }
+            m0 = __fmul_rn(fmaxf(m0, s[31]), f);
+            m1 = __fmul_rn(fmaxf(m1, s[63]), f);
           }
-          m0 = __fmul_rn(fmaxf(m0, s[31]), f);
-          m1 = __fmul_rn(fmaxf(m1, s[63]), f);
           float top = fmaxf(m0, m1) + ev;
-          int far = top - ref > kAhead || (unset && top > kUnset);
+          int far = top - ref > kAhead || (unset && top > kUnset) || rehearsal;
           asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 64, a;\nselp.s32 %0, 1, 0, b;\n}"
                        : "+r"(far)
                        : "r"(1 + quad)
@@ -326,36 +352,51 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
           const float real0 = m0 + ev - ref, real1 = m1 + ev - ref;
           const float above0 = fmaxf(ceilf(real0), kUnset), above1 = fmaxf(ceilf(real1), kUnset);  // (kUnset: no key is seen)
           float shift0 = kPlace - above0 + (ev - ref), shift1 = kPlace - above1 + (ev - ref);
-          if (fmaxf(fmaxf(m0 > kNothing ? fabsf(m0) : 0.0f, m1 > kNothing ? fabsf(m1) : 0.0f), fabsf(ref)) >= kFar) {
-            // sums with scores this large are off by 2^-9 and more: differences from
-            // the block's maximum first, which are exact near it
+          if constexpr (P::kTree) {  // (differences from the block's maximum, always: see below)
             m0 = fmaxf(m0, kUnset);
             m1 = fmaxf(m1, kUnset);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = __fsub_rn(__fmul_rn(s[i], f), i < 32 ? m0 : m1);
-            f = 1.0f;
             shift0 = kPlace + (real0 - above0);
             shift1 = kPlace + (real1 - above1);
+          } else {
+            if (fmaxf(fmaxf(m0 > kNothing ? fabsf(m0) : 0.0f, m1 > kNothing ? fabsf(m1) : 0.0f), fabsf(ref)) >= kFar) {
+              // sums with scores this large are off by 2^-9 and more: differences from
+              // the block's maximum first, which are exact near it
+              m0 = fmaxf(m0, kUnset);
+              m1 = fmaxf(m1, kUnset);
+#pragma unroll
+              for (int i = 0; i < 64; ++i) s[i] = __fsub_rn(__fmul_rn(s[i], f), i < 32 ? m0 : m1);
+              f = 1.0f;
+              shift0 = kPlace + (real0 - above0);
+              shift1 = kPlace + (real1 - above1);
+            }
           }
           __syncwarp();
           const int least = 127 - static_cast<int>(kPlace);
           const int scale0 = static_cast<int>(fminf(fmaxf(above0, static_cast<float>(-least)), kAhead)) + least;
           const int scale1 = static_cast<int>(fminf(fmaxf(above1, static_cast<float>(-least)), kAhead)) + least;
-          *reinterpret_cast<uint16_t*>(smem + kScales + b * kScaleBytes + scale_at(r, 2 * group)) = static_cast<uint16_t>(scale0 | scale1 << 8);
+          if (!rehearsal) *reinterpret_cast<uint16_t*>(smem + kScales + b * kScaleBytes + scale_at(r, 2 * group)) = static_cast<uint16_t>(scale0 | scale1 << 8);
           // the weights; as fp16 pairs (11 bits), cut into two parts of 4 bits, over
           // the scores that this thread has read
-#pragma unroll
+#pragma unroll P::kTree ? 1 : 2
           for (int x = 0; x < 2; ++x) {
             const float shift = x ? shift1 : shift0;
             float s0 = 0.0f, s1 = 0.0f;
+            if constexpr (P::kTree) {  // (the first half's weights lie over its scores alone)
+              tmem_ld<32>(t_s + 32 * x, s);
+              ld_wait();
+              const uint32_t bits = static_cast<uint32_t>(see >> (32 * x));
+              const float m = x ? m1 : m0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1 ? __fsub_rn(__fmul_rn(s[i], f), m) : kNothing;
+            }
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint32_t ha, hb;
               {
-                const int c = 32 * x + 4 * i;
-                const float w0 = ex2_approx(fmaf(s[c], f, shift)), w1 = ex2_approx(fmaf(s[c + 1], f, shift));
-                const float w2 = ex2_approx(fmaf(s[c + 2], f, shift)), w3 = ex2_approx(fmaf(s[c + 3], f, shift));
+                const int c = P::kTree ? 4 * i : 32 * x + 4 * i;
+                auto weight = [&](float score) { return ex2_approx(P::kTree ? score + shift : fmaf(score, f, shift)); };
+                const float w0 = weight(s[c]), w1 = weight(s[c + 1]), w2 = weight(s[c + 2]), w3 = weight(s[c + 3]);
                 s0 += w0;
                 s1 += w1;
                 s0 += w2;
@@ -367,9 +408,19 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
               hi[i] = a | d << 16;
               lo[i] = e4m3x2_of_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a))) | e4m3x2_of_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d))) << 16;
             }
-            tmem_st<8>(t_s + 8 * x, reinterpret_cast<const float*>(hi));
-            tmem_st<8>(t_s + 16 + 8 * x, reinterpret_cast<const float*>(lo));
+            if (!rehearsal) {
+              tmem_st<8>(t_s + 8 * x, reinterpret_cast<const float*>(hi));
+              tmem_st<8>(t_s + 16 + 8 * x, reinterpret_cast<const float*>(lo));
+            }
             l = fmaf(s0 + s1, ex2_approx((x ? above1 : above0) - ev - kPlace), l);
+          }
+          if (P::kTree && rehearsal) {
+            rehearsal = false;
+            unset = exists;
+            ref = exists ? 0.0f : 0.5f * kFar;
+            l = 0.0f;
+            j = -1;
+            continue;
           }
           if (far && j > 0) {
             // what was summed with the old references, this thread's half of the
@@ -377,16 +428,17 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
             // first, ran under the work on the weights
             await(&o_done[b ^ 1], (it - 1) / 2);
             tc_after();
+            constexpr int kStep = P::kTree ? 16 : 64;
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 64) {
-              float o[64];
-              tmem_ld<32>(t_o + lanes + group * 128 + c, o);
-              tmem_ld<32>(t_o + lanes + group * 128 + c + 32, o + 32);
+            for (int c = 0; c < 128; c += kStep) {
+              float o[kStep];
+#pragma unroll
+              for (int i = 0; i < kStep; i += 16) tmem_ld<16>(t_o + lanes + group * 128 + c + i, o + i);
               ld_wait();
 #pragma unroll
-              for (int i = 0; i < 64; ++i) o[i] *= change;
-              tmem_st<32>(t_o + lanes + group * 128 + c, o);
-              tmem_st<32>(t_o + lanes + group * 128 + c + 32, o + 32);
+              for (int i = 0; i < kStep; ++i) o[i] *= change;
+#pragma unroll
+              for (int i = 0; i < kStep; i += 16) tmem_st<16>(t_o + lanes + group * 128 + c + i, o + i);
             }
           }
           st_wait();

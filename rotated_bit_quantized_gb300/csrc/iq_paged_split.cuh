@@ -202,6 +202,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
       if (ok) ok = wait(bar, phase, kLostRows);
       __syncwarp();
     };
+    bool at_first = true;
     Place at_unit = start;
     for (int at = first; at < last; next_unit(p, at_unit)) {
       const Tiles tiles = tiles_at(p, at_unit);
@@ -249,14 +250,16 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = 0.0f;
 
-      for (int j = 0; j < n; ++j, ++it) {
+      // (a tree's first turn is a rehearsal: it fetches the instructions, see the rows' kernel)
+      for (int j = P::kTree && at_first ? -1 : 0; j < n; ++j) {
         const int b = it & 1;
-        await(&scales_in[it % C::kRing], it / C::kRing);
+        const bool rehearsal = P::kTree && j < 0;
+        if (!rehearsal) await(&scales_in[it % C::kRing], it / C::kRing);
         const float* sc = reinterpret_cast<const float*>(&scales[it % C::kRing]) + (key >> 6);  // this key's page
         const float ks = sc[0];
         const float ev = static_cast<float>(exponent_of(sc[2]));
         const int t0 = tiles.tile(k0 + j) * kTile;
-        await(&s_full[b], it / 2);
+        if (!rehearsal) await(&s_full[b], it / 2);
         tc_after();
         float s[RT], w[RT];
         tmem_ld<RT>(tmem + lanes + b * C::kCols + r0, s);
@@ -264,7 +267,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         ld_wait();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[b]);
+        if (lane == 0 && !rehearsal) mbar_arrive(&s_free[b]);
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r] = fmaf(w[r], 1.0f / 16, s[r]) * clamp_finite(factor[r0 + r] * ks);
         // masks, in tiles that some row does not see whole
@@ -286,7 +289,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
           if (lane == r) top = m;
         }
         const int own = r0 + lane % RT;
-        int far = lane < RT && top + ev - ref[own] > kAhead;
+        int far = (lane < RT && top + ev - ref[own] > kAhead) || rehearsal;
         asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 128, a;\nselp.s32 %0, 1, 0, b;\n}"
                      : "+r"(far)
                      : "r"(1 + group)
@@ -359,6 +362,14 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
           to[scale_at(r0 + lane, warp & 3)] = x;
           to[scale_at(NR + r0 + lane, warp & 3)] = x;
         }
+        if (P::kTree && rehearsal) {
+          named_bar(1 + group, 128);
+          if (key < RT) ref[r0 + key] = r0 + key < rows ? kUnset : kDead;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) l[r] = 0.0f;
+          named_bar(1 + group, 128);
+          continue;
+        }
         if (group == 0) {  // the values' scales, 1; the scores' place is free until this tile is multiplied
           const float one = __uint_as_float(0x7F7F7F7Fu), ones[4] = {one, one, one, one};
           tmem_st<4>(tmem + lanes + b * C::kCols + 4, ones);
@@ -368,7 +379,9 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[b]);
+        ++it;
       }
+      at_first = false;
       // ---- the segment's end: sums over the keys, then the results
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
