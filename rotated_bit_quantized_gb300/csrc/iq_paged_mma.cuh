@@ -381,10 +381,11 @@ struct Loader {
   static constexpr int kRing = SLOTS == 4 ? 4 : 8;
   static_assert(SLOTS == 4 || SLOTS == 6, "the ring's length is reasoned above");
 
-  struct Segment {
-    const int* row;
-    Tiles tiles;
-    int begin, n, end_page, h;
+  // up to 16 tiles of a segment, a lane's page of them and its scales
+  struct Block {
+    int n, h, id;
+    bool last;  // of its segment
+    float2 scales;
   };
   const P& p;
   const Work& work;
@@ -394,103 +395,90 @@ struct Loader {
   uint64_t* scales_in; // [kRing]
   const Waits& wait;
 
-  // the segment at slot `at` of the range, which moves behind it; none (n == 0) at the range's end
-  __device__ __forceinline__ Segment take(Place& w, int& at, int last) const {
-    Segment g{};
-    if (at >= last) return g;
-    g.tiles = tiles_at(p, w);
-    const Part part = part_of(work, w, g.tiles.n, last - at);
-    g.begin = part.begin;
-    g.n = part.n;
-    g.row = p.table + static_cast<long long>(p.slot[w.e]) * p.max_pages;
-    g.end_page = last_page(p, w.e);
-    g.h = w.h;
-    at += g.tiles.n + work.cost - w.j;
-    next_unit(p, w);
-    return g;
-  }
-  __device__ __forceinline__ int fetch(const Segment& g, int j) const {  // this lane's page of tiles j .. j + 15
-    const int lane = threadIdx.x & 31;
-    return __ldcg(g.row + min(2 * g.tiles.tile(g.begin + min(j + (lane >> 1), g.n - 1)) + (lane & 1), g.end_page));
-  }
-  __device__ __forceinline__ float2 scales_of(const Segment& g, int id) const {
-    const long long x = static_cast<long long>(id) * p.heads + g.h;
-    return make_float2(__ldcg(p.k_scales + x), __ldcg(p.v_scales + x));
-  }
-
+  // One place in the code for every kind of step: the first pass through it is fetched while
+  // all of the GPU fetches its own (see the rows' kernel).
   __device__ __forceinline__ void run(Place w, int first, int last, uint64_t policy) const {
     if (p.stall) return;
     const int lane = threadIdx.x & 31;
-    int issued = 0, it = 0, v0 = 0, v1 = 0, v_head = -1;  // (the tile whose values come next)
-    bool ok = true;
-    auto load = [&](const CUtensorMap* map, int id0, int id1, int h) {
-      const int s = issued % SLOTS;
-      if (issued >= SLOTS) ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], issued / SLOTS - 1, kLostLoad));
-      if (!ok) return;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[s], kSlotBytes);
-        uint8_t* to = smem + s * kSlotBytes;
-        const int y0 = (id0 * p.heads + h) * kPage, y1 = (id1 * p.heads + h) * kPage;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          tensor2d_g2s(to + half * kHalfBytes, map, 128 * half, y0, &full[s], policy);
-          tensor2d_g2s(to + half * kHalfBytes + kHalfBytes / 2, map, 128 * half, y1, &full[s], policy);
+    // the segment whose blocks are being taken
+    Tiles tiles{};
+    const int* row = nullptr;
+    int at = first, begin = 0, left = 0, end_page = 0, h = 0;
+    // the block being loaded, the next (its ids are there), the one behind it (asked for)
+    Block a{}, b{}, c{};
+    int ahead = 0, j = 0, issued = 0, it = 0;
+    int v0 = 0, v1 = 0, v_head = -1;  // the tile whose values come next
+    for (bool ok = true; ok;) {
+      while (j == a.n && ahead < 4) {
+        if (left == 0 && at < last) {
+          tiles = tiles_at(p, w);
+          const Part part = part_of(work, w, tiles.n, last - at);
+          begin = part.begin;
+          left = part.n;
+          row = p.table + static_cast<long long>(p.slot[w.e]) * p.max_pages;
+          end_page = last_page(p, w.e);
+          h = w.h;
+          at += tiles.n + work.cost - w.j;
+          next_unit(p, w);
         }
+        a = b;
+        b = c;
+        c.n = min(left, 16);
+        c.h = h;
+        if (c.n > 0) c.id = __ldcg(row + min(2 * tiles.tile(begin + min(lane >> 1, c.n - 1)) + (lane & 1), end_page));
+        begin += c.n;
+        left -= c.n;
+        c.last = left == 0;
+        if (b.n > 0) {
+          b.id = page_in_pool(b.id, p.pages, p.status);
+          const long long x = static_cast<long long>(b.id) * p.heads + b.h;
+          b.scales = make_float2(__ldcg(p.k_scales + x), __ldcg(p.v_scales + x));
+        }
+        j = 0;
+        ahead = ahead < 2 ? ahead + 1 : a.n == 0 ? 4 : 3;
+        if (ahead == 4) break;
+        if (ahead == 3 && a.n > 0) break;
       }
-      ++issued;
-      __syncwarp();
-    };
-    int at = first;
-    Segment g = take(w, at, last), g1 = take(w, at, last);
-    int ids = g.n > 0 ? page_in_pool(fetch(g, 0), p.pages, p.status) : 0, ids1 = g1.n > 0 ? fetch(g1, 0) : 0;
-    float2 sc = g.n > 0 ? scales_of(g, ids) : make_float2(1.0f, 1.0f);
-    while (ok && g.n > 0) {
-      int next = g.n > 16 ? fetch(g, 16) : 0;
-      float2 next_sc = sc, sc1 = sc;
-      if (g1.n > 0) {
-        ids1 = page_in_pool(ids1, p.pages, p.status);
-        sc1 = scales_of(g1, ids1);
-      }
-      const Segment g2 = take(w, at, last);
-      const int ids2 = g2.n > 0 ? fetch(g2, 0) : 0;
-      for (int j = 0; j < g.n && ok; ++j) {
-        if (j % 16 == 0 && j > 0) {
-          ids = next;
-          sc = next_sc;
-          if (j + 16 < g.n) next = fetch(g, j + 16);
-        }
-        if (j % 16 == 8 && j + 8 < g.n) {
-          next = page_in_pool(next, p.pages, p.status);
-          next_sc = scales_of(g, next);
-        }
-        const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j % 16) + 1);
-        load(&p.k_map, id0, id1, g.h);
+      const bool more = j < a.n;
+      if (!more && v_head < 0) break;
+      const int id0 = __shfl_sync(0xFFFFFFFFu, a.id, 2 * j & 31), id1 = __shfl_sync(0xFFFFFFFFu, a.id, (2 * j + 1) & 31);
+      const bool closes = !ACROSS && more && a.last && j == a.n - 1;  // its own values too
+#pragma unroll 1
+      for (int kind = 0; kind < 3 && ok; ++kind) {  // the tile's keys, the values of the one before, its own
+        if (kind == 0 ? !more : kind == 1 ? v_head < 0 : !closes) continue;
+        const int s = issued % SLOTS;
+        if (issued >= SLOTS) ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], issued / SLOTS - 1, kLostLoad));
         if (!ok) break;
-        const int x = lane - 2 * (j % 16);
+        if (lane == 0) {
+          const CUtensorMap* map = kind == 0 ? &p.k_map : &p.v_map;
+          const int y0 = ((kind == 1 ? v0 : id0) * p.heads + (kind == 1 ? v_head : a.h)) * kPage;
+          const int y1 = ((kind == 1 ? v1 : id1) * p.heads + (kind == 1 ? v_head : a.h)) * kPage;
+          mbar_arrive_expect_tx(&full[s], kSlotBytes);
+          uint8_t* to = smem + s * kSlotBytes;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            tensor2d_g2s(to + half * kHalfBytes, map, 128 * half, y0, &full[s], policy);
+            tensor2d_g2s(to + half * kHalfBytes + kHalfBytes / 2, map, 128 * half, y1, &full[s], policy);
+          }
+        }
+        ++issued;
+        __syncwarp();
+        if (kind > 0) continue;
+        const int x = lane - 2 * j;
         if (x == 0 || x == 1) {
           float* to = reinterpret_cast<float*>(&scales[it % kRing]);
-          to[x] = sc.x;
-          to[2 + x] = sc.y;
+          to[x] = a.scales.x;
+          to[2 + x] = a.scales.y;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&scales_in[it % kRing]);
         ++it;
-        if (v_head >= 0) load(&p.v_map, v0, v1, v_head);
-        v0 = id0;
-        v1 = id1;
-        v_head = g.h;
       }
-      if (!ACROSS && ok) {
-        load(&p.v_map, v0, v1, v_head);
-        v_head = -1;
-      }
-      g = g1;
-      ids = ids1;
-      sc = sc1;
-      g1 = g2;
-      ids1 = ids2;
+      v0 = id0;
+      v1 = id1;
+      v_head = more && !closes ? a.h : -1;
+      j += more;
     }
-    if (ACROSS && ok && v_head >= 0) load(&p.v_map, v0, v1, v_head);
     if (lane == 0)  // no copy left in flight
       for (int s = 0; s < SLOTS && s < issued; ++s) wait.drain(&full[s], (issued - 1 - s) / SLOTS);
   }

@@ -98,98 +98,97 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ join
 
-// The partial results of row `row` of kv head h at node e: the first, and those of the
-// ranges behind.
-struct Partials {
-  int first, next, step, n;
-  __device__ __forceinline__ Partials(const TreeParams& p, int e, int h, int row) {
-    const bool narrow = e >= p.leaves;
-    const int x = row - p.row0[e], z = x / kUnitRows, units = (p.n[e] + kUnitRows - 1) / kUnitRows;  // (a leaf's: one)
-    const int cost = narrow ? p.narrow_cost : p.wide_cost, grid = narrow ? p.narrow : p.wide, total = narrow ? p.narrow_total : p.wide_total;
-    const int per = p.tiles[e] + cost, begin = p.cum[e] + (h * units + z) * per;
-    const int g0 = range_of(begin + cost, grid, total), g1 = range_of(begin + per - 1, grid, total);
-    first = p.part0[e] + h * p.n[e] + x;
-    step = narrow ? p.narrow_rows : kUnitRows;
-    next = (narrow ? p.narrow_cont : p.wide_cont) + g0 * step + x - z * kUnitRows;
-    n = 1 + g1 - g0;
-  }
-  __device__ __forceinline__ int row(int k) const { return k == 0 ? first : next + k * step; }
-};
+// The range that holds slot t of `total` in `grid`: the last g with g * total / grid <= t,
+// that is, g * total < (t + 1) * grid.
+__device__ __forceinline__ int range_with(int t, int grid, int total) {
+  const unsigned long long x = static_cast<unsigned long long>(t + 1u) * grid;
+  int g = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(total)));  // off by one at most
+  if (static_cast<unsigned long long>(g) * total >= x) --g;
+  else if (static_cast<unsigned long long>(g + 1) * total < x) ++g;
+  return g;
+}
 
 struct JoinPlan {
-  int entries, each;  // rows of a CTA
+  int entries, shift;  // 2^shift warps to a row
   short entry[IQ_MAX_BATCH], lowest[IQ_MAX_BATCH];  // place in the call, lowest node
   int row0[IQ_MAX_BATCH];
 };
 
-// CTA (x, h) joins `each` rows of kv head h, 8 / each warps a row, a lane per 8 dims,
-// in the order of nodes and ranges: four partial results at a time, their references
-// and sums with them, so that a row takes one trip to memory or few.
-__global__ void __launch_bounds__(256) paged_tree_join_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ JoinPlan plan) {
+// CTA (x, h) joins rows of kv head h, 2^shift warps a row, a lane per 8 dims, in the
+// order of nodes and ranges.  A row's partial results at a node: the first, and those of
+// the ranges behind.  A warp asks for four at a time, references and sums with
+// them, so that it takes one trip to memory mostly.  Bound by that trip and by L2, which
+// the results of all CTAs pass at once (20 MB for 152 ranges of 128 rows, there and back).
+__global__ void __launch_bounds__(256, 4) paged_tree_join_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ JoinPlan plan) {
   wait_for_last_kernel();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = 8 / plan.each, h = blockIdx.y;
-  const int row = blockIdx.x * plan.each + warp / share;
-  const bool live = row < p.rows;
+  constexpr int kAtOnce = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, shift = plan.shift, share = 1 << shift, h = blockIdx.y;
+  const int row = min(static_cast<int>(blockIdx.x) * (8 >> shift) + (warp >> shift), p.rows - 1);
   __shared__ float part[8][kHeadDim + 2];
   float m = kUnset, sum = 0.0f, o[8] = {};
   const int s = entry_of(plan.row0, plan.entries, row);
-  if (live) {
-    int turn = warp % share;  // of this warp's next partial
-    for (int e = plan.lowest[s]; e >= 0; e = p.parent[e]) {
-      const Partials parts(p, e, h, row);
-      for (int k = turn; k < parts.n; k += 4 * share) {
-        float2 ml[4];
-        float4 v[4][2];
+  int before = 0;  // partial results of the nodes before
+  for (int e = plan.lowest[s]; e >= 0; e = p.parent[e]) {
+    const bool narrow = e >= p.leaves;
+    const int cost = narrow ? p.narrow_cost : p.wide_cost, grid = narrow ? p.narrow : p.wide, total = narrow ? p.narrow_total : p.wide_total;
+    const int step = narrow ? p.narrow_rows : kUnitRows, per = p.tiles[e] + cost;
+    const int x = row - p.row0[e], z = x / kUnitRows, units = (p.n[e] + kUnitRows - 1) / kUnitRows;  // (a leaf's: one)
+    const int begin = p.cum[e] + (h * units + z) * per;
+    const int g0 = range_with(begin + cost, grid, total), count = 1 + range_with(begin + per - 1, grid, total) - g0;
+    const int first = p.part0[e] + h * p.n[e] + x, behind = (narrow ? p.narrow_cont : p.wide_cont) + g0 * step + x - z * kUnitRows;
+#pragma unroll 1
+    for (int turn = (warp - before) & (share - 1); turn < count; turn += kAtOnce * share) {
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ml[i] = make_float2(kUnset, 0.0f);
-          v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (k + i * share >= parts.n) continue;
-          const long long at = parts.row(k + i * share);
-          const float4* from = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 8);
-          ml[i] = __ldcg(&p.part_ml[at]);
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int k = turn + i * share;
+        const long long at = k == 0 ? first : behind + min(k, count - 1) * step;  // (those behind the last count for nothing)
+        const float4* from = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 8);
+        ml[i] = __ldcg(&p.part_ml[k < count ? at : first]);
+        if (k >= count) ml[i] = make_float2(-__builtin_huge_valf(), 0.0f);
+        if (k < count) {
           v[i][0] = __ldcg(from);
           v[i][1] = __ldcg(from + 1);
-        }
-        const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m), old = ex2_approx(m - top);
-        m = top;
-        sum *= old;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) o[d] *= old;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = ex2_approx(ml[i].x - m);
-          sum = fmaf(f, ml[i].y, sum);
-          o[0] = fmaf(f, v[i][0].x, o[0]), o[1] = fmaf(f, v[i][0].y, o[1]), o[2] = fmaf(f, v[i][0].z, o[2]), o[3] = fmaf(f, v[i][0].w, o[3]);
-          o[4] = fmaf(f, v[i][1].x, o[4]), o[5] = fmaf(f, v[i][1].y, o[5]), o[6] = fmaf(f, v[i][1].z, o[6]), o[7] = fmaf(f, v[i][1].w, o[7]);
+        } else {
+          v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
       }
-      turn = (turn + share - parts.n % share) % share;
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, ml[i].x);
+      const float old = ex2_approx(m - top);
+      m = top;
+      sum *= old;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] *= old;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const float f = ex2_approx(ml[i].x - m);
+        sum = fmaf(f, ml[i].y, sum);
+        o[0] = fmaf(f, v[i][0].x, o[0]), o[1] = fmaf(f, v[i][0].y, o[1]), o[2] = fmaf(f, v[i][0].z, o[2]), o[3] = fmaf(f, v[i][0].w, o[3]);
+        o[4] = fmaf(f, v[i][1].x, o[4]), o[5] = fmaf(f, v[i][1].y, o[5]), o[6] = fmaf(f, v[i][1].z, o[6]), o[7] = fmaf(f, v[i][1].w, o[7]);
+      }
     }
+    before += count;
   }
   if (share > 1) {
 #pragma unroll
     for (int d = 0; d < 8; ++d) part[warp][d * 32 + lane] = o[d];
-    if (lane == 0) {
-      part[warp][kHeadDim] = sum;
-      part[warp][kHeadDim + 1] = m;
-    }
+    part[warp][kHeadDim + (lane & 1)] = lane & 1 ? m : sum;
     __syncthreads();
-    if (warp % share) return;
-    for (int w = warp + 1; w < warp + share; ++w) m = fmaxf(m, part[w][kHeadDim + 1]);
-    const float own = ex2_approx(part[warp][kHeadDim + 1] - m);
-    sum *= own;
-#pragma unroll
-    for (int d = 0; d < 8; ++d) o[d] *= own;
+    if (warp & (share - 1)) return;
+#pragma unroll 1
     for (int w = warp + 1; w < warp + share; ++w) {
-      const float f = ex2_approx(part[w][kHeadDim + 1] - m);
-      sum = fmaf(f, part[w][kHeadDim], sum);
+      const float other = part[w][kHeadDim + 1], top = fmaxf(m, other), f = ex2_approx(other - top), old = ex2_approx(m - top);
+      m = top;
+      sum = fmaf(f, part[w][kHeadDim], sum * old);
 #pragma unroll
-      for (int d = 0; d < 8; ++d) o[d] = fmaf(f, part[w][d * 32 + lane], o[d]);
+      for (int d = 0; d < 8; ++d) o[d] = fmaf(f, part[w][d * 32 + lane], o[d] * old);
     }
   }
-  if (!live) return;
-  const int x = row - plan.row0[s], j = x / p.rep;
+  if (static_cast<int>(blockIdx.x) * (8 >> shift) + (warp >> shift) >= p.rows) return;
+  const int x = row - plan.row0[s], j = query_of(p, x);
   const long long to = (static_cast<long long>(plan.entry[s]) * p.heads * p.rep + h * p.rep + x - j * p.rep) * p.nq + j;
   store_out8(p.out, p.out_f32, to * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
 }
@@ -197,18 +196,10 @@ __global__ void __launch_bounds__(256) paged_tree_join_kernel(const __grid_const
 // ------------------------------------------------------------------ what is shared
 
 // A unit's beginning and end take about as long as so many tiles.
-#ifndef XCA
-#define XCA 4
-#endif
-#ifndef XCB
-#define XCB 4
-#endif
-#ifndef XTB
-#define XTB 1.0
-#endif
 constexpr int kUnitCost = 4;
-constexpr int kWideCost = XCA, kNarrowCost = XCB;
-constexpr double kNarrowTile = XTB;  // a tile's time there, of a tile's of many rows
+constexpr int kWideCost = 3, kNarrowCost = 3;
+// The time of a tile of few rows, of that of one of 128 (1.45 us).
+constexpr double narrow_tile(int rows) { return rows == 8 ? 0.7 : rows == 16 ? 1.0 : 1.2; }
 
 struct Planner {
   int rep, window, sinks, inner = 0;
@@ -380,8 +371,9 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
     units[kind] += u;
     tiles[kind] += u * a.tiles.n;
   }
+  p.narrow_rows = leaf_rows <= 8 ? 8 : leaf_rows <= 16 ? 16 : 32;
   // the SMs go to the two kinds by what each has to do
-  const double wide = static_cast<double>(tiles[0] + units[0] * kWideCost), narrow = kNarrowTile * (tiles[1] + units[1] * kNarrowCost);
+  const double wide = static_cast<double>(tiles[0] + units[0] * kWideCost), narrow = narrow_tile(p.narrow_rows) * (tiles[1] + units[1] * kNarrowCost);
   const int sms = num_sms();
   p.narrow = tiles[1] == 0 ? 0 : std::min(std::max(static_cast<int>(sms * narrow / (wide + narrow) + 0.5), 1), sms - 1);
   p.wide = static_cast<int>(std::min<long long>(sms - p.narrow, tiles[0]));
@@ -398,7 +390,6 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   }
   p.wide_total = static_cast<int>(total[0]);
   p.narrow_total = static_cast<int>(total[1]);
-  p.narrow_rows = leaf_rows <= 8 ? 8 : leaf_rows <= 16 ? 16 : 32;
   p.wide_cont = static_cast<int>(parts);
   parts += static_cast<long long>(p.wide) * kUnitRows;
   p.narrow_cont = static_cast<int>(parts);
@@ -449,9 +440,13 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   if (err == cudaSuccess) err = p.narrow_rows == 8 ? launch_tree<8>(p, cs) : p.narrow_rows == 16 ? launch_tree<16>(p, cs) : launch_tree<32>(p, cs);
   if (err == cudaSuccess) {
     join.entries = t.n;
-    join.each = cut_rows >= 4096 ? 8 : 1;
+    // warps to a row, so that each has some six partial results
+    const long long of_row = parts / cut_rows;
+    join.shift = of_row <= 6 ? 0 : of_row <= 12 ? 1 : of_row <= 24 ? 2 : 3;
+    while (join.shift > 0 && (cut_rows << join.shift) / 8 > 4ll * sms) --join.shift;  // all CTAs at once
+    const int each = 8 >> join.shift;
     void* args[] = {&p, &join};
-    err = launch_after(reinterpret_cast<const void*>(&paged_tree_join_kernel), dim3((p.rows + join.each - 1) / join.each, heads), 256, 0, cs, args);
+    err = launch_after(reinterpret_cast<const void*>(&paged_tree_join_kernel), dim3((p.rows + each - 1) / each, heads), 256, 0, cs, args);
   }
   if (err != cudaSuccess) return cuda_fail(err, "paged attention of shared pages");
   launched_outputs(stream, {out, static_cast<size_t>(n_slots) * q_heads * n_queries * kHeadDim * (out_f32 ? 4 : 2)});

@@ -26,6 +26,7 @@ namespace iq {
 namespace paged {
 namespace split {
 
+constexpr int kMu = 4, kHu = 1;  // products unrolled in a tree
 constexpr float kPlace = 6.0f;  // the place of a block's largest weight
 constexpr float kPLo = 128.0f;  // the low parts' scale: half a step at 2^6 is 2, times 128 below 448
 
@@ -154,7 +155,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
             ok = ok && wait.together(&full[s], used / C::kSlots, kLostMma);
             if (!ok) break;
             tc_after();
-#pragma unroll
+#pragma unroll P::kTree ? kMu : 8
             for (int k = 0; k < 8; ++k)
               mma_e4m3(tmem + b * C::kCols, at_slot + ((s * kSlotBytes + (k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
                        queries + (((k >> 2) * C::kCols * 128 + (k & 3) * 32) >> 4), kS, k > 0);
@@ -169,9 +170,9 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
             tc_after();
             const uint32_t place = tmem + b * C::kCols;  // of the scales, where the scores were; the values' behind them
             copy_scales(place, sbase + C::kScales + b * kScaleBytes);
-#pragma unroll
+#pragma unroll P::kTree ? kHu : 2
             for (int half = 0; half < 2; ++half)
-#pragma unroll
+#pragma unroll P::kTree ? kMu : 4
               for (int k = 0; k < 4; ++k)
                 mma_scaled(t_o + half * C::kCols, at_slot + ((s * kSlotBytes + half * kHalfBytes + k * 32 * 128) >> 4),
                            weights + ((b * C::kCols * 128 + k * 32) >> 4), shape_scaled(128, C::kCols, true, false, 0, k), place + 4, place,
