@@ -609,6 +609,13 @@ int iq_paged_attend_shared(const iq_paged* cache, const void* q, int q_heads, in
                            const int32_t* counts, int n_slots, float scale, int causal, int window, int sinks,
                            void* out, int out_f32, void* workspace, size_t workspace_bytes, iq_stream_t stream);
 
+/*
+ * iq_paged_debug_share — a hook for tests: the next iq_paged_attend_shared of this host thread multiplies
+ * shared pages once wherever there are any, also where little is shared and
+ * iq_paged_attend would be faster.
+ */
+int iq_paged_debug_share(void);
+
 /* iq_paged_append_attend_shared — iq_paged_append_attend with iq_paged_attend_shared in the second place. */
 int iq_paged_append_attend_shared(iq_paged* cache, const void* keys, const void* values, int n, const void* q,
                                   int q_heads, int n_queries, const int32_t* slots, const int32_t* counts,

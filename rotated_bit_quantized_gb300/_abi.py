@@ -38,7 +38,7 @@ EXPORTS = ("iq_status_string", "iq_last_error", "iq_build_rotation", "iq_cache_b
            "iq_paged_fork", "iq_paged_compact", "iq_paged_attend_workspace", "iq_paged_attend",
            "iq_paged_append_attend", "iq_paged_debug_fail", "iq_paged_debug_stall", "iq_rotary_frequencies",
            "iq_rotary_turns", "iq_rotary_apply", "iq_paged_append_rotary", "iq_paged_attend_shared_workspace",
-           "iq_paged_attend_shared", "iq_paged_append_attend_shared")
+           "iq_paged_attend_shared", "iq_paged_append_attend_shared", "iq_paged_debug_share")
 
 
 class IQCacheDesc(ctypes.Structure):
@@ -136,6 +136,7 @@ def lib() -> ctypes.CDLL:
         L.iq_paged_append_attend_shared.argtypes = L.iq_paged_append_attend.argtypes
         L.iq_paged_debug_fail.argtypes = [I]
         L.iq_paged_debug_stall.argtypes = []
+        L.iq_paged_debug_share.argtypes = []
         for name in EXPORTS:
             if name not in ("iq_status_string", "iq_last_error", "iq_cache_nbytes"):
                 getattr(L, name).restype = I

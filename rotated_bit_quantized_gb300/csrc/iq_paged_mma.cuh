@@ -119,7 +119,7 @@ struct TreeParams : AttendBase {
   int nodes, leaves, wide, narrow, wide_cost, narrow_cost, wide_total, narrow_total;
   int wide_cont, narrow_cont, narrow_rows;  // where the ranges' partial results begin; rows of a narrow range's
   unsigned rep_mul, rep_shift;    // division by rep, see query_of
-  const int* pos;                 // [rows] the position of a row
+  const int2* place;              // [rows] a row's position, its place in q and out for kv head 0
   short slot[kNodes];             // that holds the node's pages
   short parent[kNodes];           // < 0: none
   short entry[kNodes];            // of a leaf: its place in the call

@@ -223,7 +223,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
     int next_pos = 0;
     auto factor_of = [&](const Place& u) {
       if (r >= rows_at(p, u)) return 0.0f;
-      if constexpr (P::kTree) next_pos = __ldcg(p.pos + p.row0[u.e] + u.z * kRows + r);
+      if constexpr (P::kTree) next_pos = __ldcg(&p.place[p.row0[u.e] + u.z * kRows + r].x);
       return __ldcg(p.factors + cut_row(p, u) + r);
     };
     if constexpr (P::kTree) wait_only();

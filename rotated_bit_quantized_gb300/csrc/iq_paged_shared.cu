@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "iq_paged_rows.cuh"
@@ -27,38 +28,72 @@ struct TreeCutParams {
   const uint16_t* q;
   uint8_t* cut;
   float* factors;
-  int* pos;
-  int heads, rep, nq, rows, entries, causal;
+  int2* place;
+  int4* results;
+  int rows, entries, causal;
   float scale;
-  short entry[IQ_MAX_BATCH];                       // place in the call
-  int row0[IQ_MAX_BATCH + 1], pos0[IQ_MAX_BATCH];  // first row, first query's position
+  short entry[IQ_MAX_BATCH], lowest[IQ_MAX_BATCH];  // place in the call, lowest node
+  int row0[IQ_MAX_BATCH + 1], pos0[IQ_MAX_BATCH];   // first row, first query's position
 };
-// Which of n entries a row is of.
-__device__ __forceinline__ int entry_of(const int* row0, int n, int row) {
-  int s = 0, hi = n - 1;
-  while (s < hi) {
-    const int mid = (s + hi + 1) / 2;
-    if (row0[mid] <= row) s = mid;
-    else hi = mid - 1;
-  }
-  return s;
+
+// The range that holds slot t of `total` in `grid`: the last g with g * total / grid <= t,
+// that is, g * total < (t + 1) * grid.
+__device__ __forceinline__ int range_with(int t, int grid, int total) {
+  const unsigned long long x = static_cast<unsigned long long>(t + 1u) * grid;
+  int g = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(total)));  // off by one at most
+  if (static_cast<unsigned long long>(g) * total >= x) --g;
+  else if (static_cast<unsigned long long>(g + 1) * total < x) ++g;
+  return g;
 }
 
-// Every row of (entry, kv head): two e4m3 parts, the factor of its scores, and where it
-// stands; a warp takes four.
-__global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_constant__ TreeCutParams p) {
+// Where the partial results of a row at a node are: `first`, and from `behind` on those of the
+// ranges behind, `step` rows apart; `count` in all.
+struct Results {
+  int first, behind, step, count;
+};
+__device__ inline Results results_of(const TreeParams& p, int e, int h, int row) {
+  const bool narrow = e >= p.leaves;
+  const int cost = narrow ? p.narrow_cost : p.wide_cost, grid = narrow ? p.narrow : p.wide, total = narrow ? p.narrow_total : p.wide_total;
+  const int step = narrow ? p.narrow_rows : kUnitRows, per = p.tiles[e] + cost;
+  const int x = row - p.row0[e], z = x / kUnitRows, units = (p.n[e] + kUnitRows - 1) / kUnitRows;  // (a leaf's: one)
+  const int begin = p.cum[e] + (h * units + z) * per;
+  const int g0 = range_with(begin + cost, grid, total), g1 = range_with(begin + per - 1, grid, total);
+  return {p.part0[e] + h * p.n[e] + x, (narrow ? p.narrow_cont : p.wide_cont) + (g0 + 1) * step + x - z * kUnitRows, step, 1 + g1 - g0};
+}
+
+// Every row of (entry, kv head): two e4m3 parts, the factor of its scores, where it
+// stands, and where its partial results will be (a lane for each node that it is under: the
+// joining kernel, of eight warps to a row, spent most of its time on that); a warp takes
+// four rows.
+__global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_constant__ TreeCutParams c, const __grid_constant__ TreeParams p) {
   wait_for_last_kernel();
   const int lane = threadIdx.x & 31, w0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4, h = blockIdx.y;
   uint4 raw[4];
+  int entry[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int row = min(w0 + k, p.rows - 1);
-    const int s = entry_of(p.row0, p.entries, row), x = row - p.row0[s], j = x / p.rep;
-    const int at = (p.entry[s] * p.heads * p.rep + x - j * p.rep) * p.nq + j;  // of kv head 0
-    raw[k] = __ldcs(reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(h) * p.rep * p.nq + at) * kHeadDim) + lane);
-    if (h == 0 && lane == 0 && w0 + k < p.rows) p.pos[row] = p.pos0[s] + (p.causal ? j : 0);
+    const int row = min(w0 + k, c.rows - 1);
+    int s = 0, hi = c.entries - 1;  // the last entry that begins at or before the row
+    while (s < hi) {
+      const int mid = (s + hi + 1) / 2;
+      if (c.row0[mid] <= row) s = mid;
+      else hi = mid - 1;
+    }
+    const int x = row - c.row0[s], j = query_of(p, x);
+    const int at = (c.entry[s] * p.heads * p.rep + x - j * p.rep) * p.nq + j;
+    raw[k] = __ldcs(reinterpret_cast<const uint4*>(c.q + (static_cast<long long>(h) * p.rep * p.nq + at) * kHeadDim) + lane);
+    entry[k] = s;
+    if (h == 0 && lane == 0 && w0 + k < c.rows) c.place[row] = make_int2(c.pos0[s] + (c.causal ? j : 0), at);
   }
-  if (p.scale < 0.0f) {  // the factors are positive, so that the largest product is the largest score
+  // lane (k, level): row k's results at its node of that level, the lowest first (while the
+  // queries are on their way)
+  if (const int k = lane / kDepth, level = lane % kDepth, row = w0 + k; k < 4 && row < c.rows) {
+    int e = c.lowest[k == 0 ? entry[0] : k == 1 ? entry[1] : k == 2 ? entry[2] : entry[3]];
+    for (int i = 0; i < level && e >= 0; ++i) e = p.parent[e];
+    const Results r = e >= 0 ? results_of(p, e, h, row) : Results{0, 0, 0, 0};
+    c.results[(static_cast<long long>(h) * c.rows + row) * kDepth + level] = make_int4(r.first, r.behind, r.step, r.count);
+  }
+  if (c.scale < 0.0f) {  // the factors are positive, so that the largest product is the largest score
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       raw[k] = make_uint4(raw[k].x ^ 0x80008000u, raw[k].y ^ 0x80008000u, raw[k].z ^ 0x80008000u, raw[k].w ^ 0x80008000u);
@@ -67,11 +102,11 @@ __global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_consta
   for (int k = 0; k < 4; ++k) {
     uint2 hi, lo;
     const float f = split_query<1>(raw[k], hi, lo);
-    if (w0 + k >= p.rows) break;
-    const long long w = static_cast<long long>(h) * p.rows + w0 + k;
-    reinterpret_cast<uint2*>(p.cut + w * kHeadDim)[lane] = hi;
-    reinterpret_cast<uint2*>(p.cut + (static_cast<long long>(p.heads) * p.rows + w) * kHeadDim)[lane] = lo;
-    if (lane == 0) p.factors[w] = fminf(f * (fabsf(p.scale) * kLog2e), 3e38f);
+    if (w0 + k >= c.rows) break;
+    const long long w = static_cast<long long>(h) * c.rows + w0 + k;
+    reinterpret_cast<uint2*>(c.cut + w * kHeadDim)[lane] = hi;
+    reinterpret_cast<uint2*>(c.cut + (static_cast<long long>(p.heads) * c.rows + w) * kHeadDim)[lane] = lo;
+    if (lane == 0) c.factors[w] = fminf(f * (fabsf(c.scale) * kLog2e), 3e38f);
   }
 }
 
@@ -98,61 +133,48 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ join
 
-// The range that holds slot t of `total` in `grid`: the last g with g * total / grid <= t,
-// that is, g * total < (t + 1) * grid.
-__device__ __forceinline__ int range_with(int t, int grid, int total) {
-  const unsigned long long x = static_cast<unsigned long long>(t + 1u) * grid;
-  int g = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(total)));  // off by one at most
-  if (static_cast<unsigned long long>(g) * total >= x) --g;
-  else if (static_cast<unsigned long long>(g + 1) * total < x) ++g;
-  return g;
-}
-
-struct JoinPlan {
-  int entries, shift;  // 2^shift warps to a row
-  short entry[IQ_MAX_BATCH], lowest[IQ_MAX_BATCH];  // place in the call, lowest node
-  int row0[IQ_MAX_BATCH];
-};
-
 // CTA (x, h) joins rows of kv head h, 2^shift warps a row, a lane per 8 dims, in the
-// order of nodes and ranges.  A row's partial results at a node: the first, and those of
-// the ranges behind.  A warp asks for four at a time, references and sums with
-// them, so that it takes one trip to memory mostly.  Bound by that trip and by L2, which
-// the results of all CTAs pass at once (20 MB for 152 ranges of 128 rows, there and back).
-__global__ void __launch_bounds__(256, 4) paged_tree_join_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ JoinPlan plan) {
+// order of nodes and ranges.  A warp asks for four partial results at a time, references
+// and sums with them, so that it takes a trip to memory or two.  Bound by these, and by
+// L2, which the results of all CTAs pass at once (20 MB for 152 ranges of 128 rows).
+struct TreeJoinParams {
+  const float* part_o;
+  const float2* part_ml;
+  const int2* place;
+  const int4* results;
+  void* out;
+  int out_f32, rows, stride, shift;  // stride: from a kv head's rows to the next one's in out
+};
+__global__ void __launch_bounds__(256, 4) paged_tree_join_kernel(const __grid_constant__ TreeJoinParams p) {
   wait_for_last_kernel();
   constexpr int kAtOnce = 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, shift = plan.shift, share = 1 << shift, h = blockIdx.y;
-  const int row = min(static_cast<int>(blockIdx.x) * (8 >> shift) + (warp >> shift), p.rows - 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, shift = p.shift, share = 1 << shift, h = blockIdx.y;
+  const int wanted = static_cast<int>(blockIdx.x) * (8 >> shift) + (warp >> shift), row = min(wanted, p.rows - 1);
+  const int4* results = p.results + (static_cast<long long>(h) * p.rows + row) * kDepth;
   __shared__ float part[8][kHeadDim + 2];
   float m = kUnset, sum = 0.0f, o[8] = {};
-  const int s = entry_of(plan.row0, plan.entries, row);
+  int4 next = __ldcg(results);
+  const int at = __ldcg(&p.place[row].y);
   int before = 0;  // partial results of the nodes before
-  for (int e = plan.lowest[s]; e >= 0; e = p.parent[e]) {
-    const bool narrow = e >= p.leaves;
-    const int cost = narrow ? p.narrow_cost : p.wide_cost, grid = narrow ? p.narrow : p.wide, total = narrow ? p.narrow_total : p.wide_total;
-    const int step = narrow ? p.narrow_rows : kUnitRows, per = p.tiles[e] + cost;
-    const int x = row - p.row0[e], z = x / kUnitRows, units = (p.n[e] + kUnitRows - 1) / kUnitRows;  // (a leaf's: one)
-    const int begin = p.cum[e] + (h * units + z) * per;
-    const int g0 = range_with(begin + cost, grid, total), count = 1 + range_with(begin + per - 1, grid, total) - g0;
-    const int first = p.part0[e] + h * p.n[e] + x, behind = (narrow ? p.narrow_cont : p.wide_cont) + g0 * step + x - z * kUnitRows;
 #pragma unroll 1
-    for (int turn = (warp - before) & (share - 1); turn < count; turn += kAtOnce * share) {
+  for (int level = 1; next.w > 0; ++level) {
+    const int4 r = next;
+    next = level < kDepth ? __ldcg(results + level) : make_int4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int turn = (warp - before) & (share - 1); turn < r.w; turn += kAtOnce * share) {
       float2 ml[kAtOnce];
       float4 v[kAtOnce][2];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int k = turn + i * share;
-        const long long at = k == 0 ? first : behind + min(k, count - 1) * step;  // (those behind the last count for nothing)
-        const float4* from = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 8);
-        ml[i] = __ldcg(&p.part_ml[k < count ? at : first]);
-        if (k >= count) ml[i] = make_float2(-__builtin_huge_valf(), 0.0f);
-        if (k < count) {
-          v[i][0] = __ldcg(from);
-          v[i][1] = __ldcg(from + 1);
-        } else {
-          v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
+        ml[i] = make_float2(-__builtin_huge_valf(), 0.0f);
+        v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k >= r.w) continue;
+        const long long x = k == 0 ? r.x : r.y + (k - 1) * r.z;
+        const float4* from = reinterpret_cast<const float4*>(p.part_o + x * kHeadDim + lane * 8);
+        ml[i] = __ldcg(&p.part_ml[x]);
+        v[i][0] = __ldcg(from);
+        v[i][1] = __ldcg(from + 1);
       }
       float top = m;
 #pragma unroll
@@ -170,12 +192,12 @@ __global__ void __launch_bounds__(256, 4) paged_tree_join_kernel(const __grid_co
         o[4] = fmaf(f, v[i][1].x, o[4]), o[5] = fmaf(f, v[i][1].y, o[5]), o[6] = fmaf(f, v[i][1].z, o[6]), o[7] = fmaf(f, v[i][1].w, o[7]);
       }
     }
-    before += count;
+    before += r.w;
   }
   if (share > 1) {
 #pragma unroll
     for (int d = 0; d < 8; ++d) part[warp][d * 32 + lane] = o[d];
-    part[warp][kHeadDim + (lane & 1)] = lane & 1 ? m : sum;
+    if (lane < 2) part[warp][kHeadDim + lane] = lane ? m : sum;
     __syncthreads();
     if (warp & (share - 1)) return;
 #pragma unroll 1
@@ -187,22 +209,27 @@ __global__ void __launch_bounds__(256, 4) paged_tree_join_kernel(const __grid_co
       for (int d = 0; d < 8; ++d) o[d] = fmaf(f, part[w][d * 32 + lane], o[d] * old);
     }
   }
-  if (static_cast<int>(blockIdx.x) * (8 >> shift) + (warp >> shift) >= p.rows) return;
-  const int x = row - plan.row0[s], j = query_of(p, x);
-  const long long to = (static_cast<long long>(plan.entry[s]) * p.heads * p.rep + h * p.rep + x - j * p.rep) * p.nq + j;
-  store_out8(p.out, p.out_f32, to * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
+  if (wanted < p.rows)
+    store_out8(p.out, p.out_f32, (static_cast<long long>(h) * p.stride + at) * kHeadDim + lane * 8, o, sum == 0.0f ? 0.0f : 1.0f / sum);
 }
 
 // ------------------------------------------------------------------ what is shared
 
-// A unit's beginning and end take about as long as so many tiles.
-constexpr int kUnitCost = 4;
-constexpr int kWideCost = 3, kNarrowCost = 3;
-// The time of a tile of few rows, of that of one of 128 (1.45 us).
-constexpr double narrow_tile(int rows) { return rows == 8 ? 0.7 : rows == 16 ? 1.0 : 1.2; }
+// Microseconds, measured over 2 to 40 paths of 256 to 32768 common tokens, 2 and 8 kv heads, 1
+// to 8 queries.  A launch's CTAs all fetch the same code at once, some 50 KB each, which the
+// GPU hands out at a rate: kFetch for each.  A tile of 128 rows (near the tensor cores' rate); of at most 8,
+// 16, 32 (HBM's, or the row threads' chain); a unit's beginning and end take as long as kUnitCost tiles.
+// The three launches of this file, without these; the attention of every slot apart: two launches
+// (more rows: three), a tile of at most 8, 16, 32 rows, and of more, over the SMs, part of them from L2.
+// 2 x 8 kv heads' paths of 2048: 14 us here, 11 apart; 32: 25 and 45; 8 paths of 8192, 2 kv heads: 16 and 20.
+constexpr double kFetch = 0.05, kTile = 1.45, kFewTile[4] = {1.0, 1.45, 1.75, 0.0}, kLaunches = 9.25;
+constexpr double kOrdinary = 8.5, kOrdinaryTile[4] = {1.2, 1.8, 3.2, 2.2};
+constexpr int kUnitCost = 3;
+constexpr int narrow_kind(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3; }
 
 struct Planner {
   int rep, window, sinks, inner = 0;
+  bool forced;  // test hook (iq_paged_debug_share): shared wherever pages are
   // per entry, in the tree's order once it is built
   int n = 0;
   struct Entry {
@@ -269,7 +296,7 @@ struct Planner {
       const int stop = common == most ? (common + 1) / 2 : common / 2;
       const Tiles t = seen(x, y, start, stop);
       const bool once = depth < kDepth - 1 && inner < kInner &&
-                        static_cast<long long>(row_units(x, y)) * (t.n + kUnitCost) < static_cast<long long>(y - x) * t.n;
+                        (forced ? t.n > 0 : static_cast<long long>(row_units(x, y)) * (t.n + kUnitCost) < static_cast<long long>(y - x) * t.n);
       int under = parent;
       if (once) {
         ++inner;
@@ -283,13 +310,16 @@ struct Planner {
 // The rows of all nodes of one kv head are at most kDepth times the call's.
 size_t tree_bytes(size_t rows, size_t heads) {
   const size_t parts = kDepth * heads * rows + static_cast<size_t>(num_sms()) * kUnitRows;
-  return parts * (kHeadDim * sizeof(float) + sizeof(float2)) + rows * sizeof(int) + heads * rows * (2 * kHeadDim + sizeof(float));
+  return parts * (kHeadDim * sizeof(float) + sizeof(float2)) + rows * sizeof(int2) +
+         heads * rows * (2 * kHeadDim + sizeof(float) + kDepth * sizeof(int4));
 }
 // Where pages are shared among slots of more rows, their own products fill the tensor cores already.
 bool tree_rows(const iq_paged* c, int q_heads, int n_queries, int n_slots) {
   const long long rows = static_cast<long long>(q_heads / c->kv_heads) * n_queries;
   return rows > 0 && rows <= kUnitRows && n_slots > 1 && kDepth * rows * n_slots * c->kv_heads < (1LL << 30);
 }
+
+thread_local bool share_next = false;
 
 int check_shared(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots,
                  int added, float scale, int causal, int window, int sinks, const void* out, int out_f32, const void* workspace,
@@ -309,6 +339,8 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   const int heads = c->kv_heads;
   Planner t;
   t.rep = q_heads / heads;
+  t.forced = share_next;
+  share_next = false;
   int longest = 0;
   for (int i = 0; i < n_slots; ++i) longest = std::max(longest, c->lens[slot_of(slots, i)]);
   if (window >= longest) window = sinks = 0;  // nothing is out of it, and positions less a window stay in 32 bits
@@ -328,8 +360,6 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   std::memset(&p, 0, sizeof(p));
   TreeCutParams cut;
   std::memset(&cut, 0, sizeof(cut));
-  JoinPlan join;
-  std::memset(&join, 0, sizeof(join));
   // leaves of at most 32 rows, as the split kernel's calls, behind the other nodes
   const int leaf_rows = t.rep * n_queries;
   const bool apart = leaf_rows <= 32;
@@ -341,10 +371,9 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
       p.leaves += wanted == 0;
     }
   for (int i = 0; i < t.n; ++i) {
-    cut.entry[i] = join.entry[i] = static_cast<short>(t.e[i].place);
-    join.lowest[i] = static_cast<short>(t.e[i].lowest < 0 ? -1 : number[t.e[i].lowest]);
+    cut.entry[i] = static_cast<short>(t.e[i].place);
+    cut.lowest[i] = static_cast<short>(t.e[i].lowest < 0 ? -1 : number[t.e[i].lowest]);
     cut.pos0[i] = t.e[i].p_lo;
-    join.row0[i] = cut.row0[i];
     cut.row0[i + 1] = cut.row0[i] + t.e[i].count * t.rep;
   }
   p.rows = cut.row0[t.n];
@@ -373,14 +402,32 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   }
   p.narrow_rows = leaf_rows <= 8 ? 8 : leaf_rows <= 16 ? 16 : 32;
   // the SMs go to the two kinds by what each has to do
-  const double wide = static_cast<double>(tiles[0] + units[0] * kWideCost), narrow = narrow_tile(p.narrow_rows) * (tiles[1] + units[1] * kNarrowCost);
+  const double many = static_cast<double>(tiles[0] + units[0] * kUnitCost), few = kFewTile[narrow_kind(leaf_rows)] / kTile * (tiles[1] + units[1] * kUnitCost);
   const int sms = num_sms();
-  p.narrow = tiles[1] == 0 ? 0 : std::min(std::max(static_cast<int>(sms * narrow / (wide + narrow) + 0.5), 1), sms - 1);
-  p.wide = static_cast<int>(std::min<long long>(sms - p.narrow, tiles[0]));
+  p.narrow = tiles[1] == 0 ? 0 : std::min(std::max(static_cast<int>(sms * few / (many + few) + 0.5), 1), sms - 1);
+  const int room = sms - p.narrow;
   p.narrow = static_cast<int>(std::min<long long>(p.narrow, tiles[1]));
+  // Units of one length are cut into as many ranges each, so that none is of two units.  Ranges
+  // of so many tiles that what the CTAs' number costs is not above what it saves.
+  bool alike = units[0] <= room && static_cast<int>(room % units[0]) * 16 <= room;
+  for (int k = 1; k < p.leaves; ++k) alike &= p.tiles[k] == p.tiles[0];
+  const long long length = alike ? tiles[0] / units[0] : tiles[0], most = alike ? room / units[0] : room;  // cut into `most` at most
+  long long each = (length + most - 1) / most;
+  const long long sets = alike ? units[0] : 1;
+  while (each < length && kFetch * sets * ((length + each - 1) / each - (length + each) / (each + 1)) > kTile) ++each;
+  p.wide = static_cast<int>(sets * ((length + each - 1) / each));
+  if (!t.forced) {  // whether that is faster than every slot's pages apart
+    const int kind = narrow_kind(leaf_rows);
+    long long apart_tiles = 0;
+    for (int i = 0; i < t.n; ++i) apart_tiles += t.seen(i, i + 1, 0, (t.e[i].pages + 1) / 2).n * heads;
+    const double shared = kLaunches + kFetch * (p.wide + p.narrow) +
+                          std::max(kTile * each, p.narrow ? kFewTile[kind] * (tiles[1] + units[1] * kUnitCost) / p.narrow : 0.0);
+    const double ordinary = kOrdinary + (apart_tiles >= sms ? sms : apart_tiles) * kFetch / 2 + kOrdinaryTile[kind] * apart_tiles / sms;
+    if (ordinary <= shared) return IQ_OK;
+  }
   // where ranges are shorter than units, these are cut at a tile's grain
-  p.wide_cost = tiles[0] >= 8ll * p.wide || units[0] >= p.wide ? kWideCost : 0;
-  p.narrow_cost = tiles[1] >= 8ll * p.narrow || units[1] >= p.narrow ? kNarrowCost : 0;
+  p.wide_cost = tiles[0] >= 8ll * p.wide || units[0] >= p.wide ? kUnitCost : 0;
+  p.narrow_cost = tiles[1] >= 8ll * p.narrow || units[1] >= p.narrow ? kUnitCost : 0;
   long long total[2] = {};
   for (int k = 0; k < p.nodes; ++k) {
     const int kind = k >= p.leaves;
@@ -398,10 +445,11 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   const long long pool_rows = static_cast<long long>(c->pages) * heads * kPage, cut_rows = static_cast<long long>(heads) * p.rows;
   p.part_o = static_cast<float*>(workspace);
   p.cut = reinterpret_cast<uint8_t*>(p.part_o + parts * kHeadDim);
-  p.part_ml = reinterpret_cast<float2*>(p.cut + cut_rows * 2 * kHeadDim);
-  p.factors = reinterpret_cast<float*>(p.part_ml + parts);
-  cut.pos = reinterpret_cast<int*>(p.factors + cut_rows);
-  p.pos = cut.pos;
+  cut.results = reinterpret_cast<int4*>(p.cut + cut_rows * 2 * kHeadDim);
+  p.part_ml = reinterpret_cast<float2*>(cut.results + cut_rows * kDepth);
+  cut.place = reinterpret_cast<int2*>(p.part_ml + parts);
+  p.factors = reinterpret_cast<float*>(cut.place + p.rows);
+  p.place = cut.place;
   if (!code_map(&p.k_map, c->k_codes, pool_rows) || !code_map(&p.v_map, c->v_codes, pool_rows) ||
       !code_map(&p.q_map, p.cut, 2 * cut_rows, kUnitRows))
     return fail(IQ_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -414,9 +462,9 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   p.out_f32 = out_f32;
   p.causal = causal;
   p.scale = scale;
-  p.heads = cut.heads = heads;
-  p.rep = cut.rep = t.rep;
-  p.nq = cut.nq = n_queries;
+  p.heads = heads;
+  p.rep = t.rep;
+  p.nq = n_queries;
   while ((2 << p.rep_shift) <= t.rep) ++p.rep_shift;
   if (t.rep & (t.rep - 1)) p.rep_mul = static_cast<unsigned>(((1ull << (32 + p.rep_shift)) + t.rep - 1) / t.rep);
   p.pages = c->pages;
@@ -435,17 +483,25 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int st = store_zeros(c, q_heads, n_queries, slots, counts, n_slots, out, out_f32, stream);
   if (st != IQ_OK) return st;
-  void* cut_args[] = {&cut};
+  void* cut_args[] = {&cut, &p};
   cudaError_t err = launch_after(reinterpret_cast<const void*>(&paged_tree_cut_kernel), dim3((p.rows + 31) / 32, heads), 256, 0, cs, cut_args);
   if (err == cudaSuccess) err = p.narrow_rows == 8 ? launch_tree<8>(p, cs) : p.narrow_rows == 16 ? launch_tree<16>(p, cs) : launch_tree<32>(p, cs);
   if (err == cudaSuccess) {
-    join.entries = t.n;
-    // warps to a row, so that each has some six partial results
+    TreeJoinParams j;
+    j.part_o = p.part_o;
+    j.part_ml = p.part_ml;
+    j.place = p.place;
+    j.results = cut.results;
+    j.out = out;
+    j.out_f32 = out_f32;
+    j.rows = p.rows;
+    j.stride = t.rep * n_queries;
+    // warps to a row, so that each has some six partial results, but all CTAs at once
     const long long of_row = parts / cut_rows;
-    join.shift = of_row <= 6 ? 0 : of_row <= 12 ? 1 : of_row <= 24 ? 2 : 3;
-    while (join.shift > 0 && (cut_rows << join.shift) / 8 > 4ll * sms) --join.shift;  // all CTAs at once
-    const int each = 8 >> join.shift;
-    void* args[] = {&p, &join};
+    j.shift = of_row <= 6 ? 0 : of_row <= 12 ? 1 : of_row <= 24 ? 2 : 3;
+    while (j.shift > 0 && (cut_rows << j.shift) / 8 > 4ll * sms) --j.shift;
+    const int each = 8 >> j.shift;
+    void* args[] = {&j};
     err = launch_after(reinterpret_cast<const void*>(&paged_tree_join_kernel), dim3((p.rows + each - 1) / each, heads), 256, 0, cs, args);
   }
   if (err != cudaSuccess) return cuda_fail(err, "paged attention of shared pages");
@@ -462,6 +518,12 @@ using namespace iq;
 using namespace iq::paged;
 
 extern "C" {
+
+int iq_paged_debug_share(void) {
+  clear_error();
+  share_next = true;
+  return IQ_OK;
+}
 
 int iq_paged_attend_shared_workspace(const iq_paged* c, int q_heads, int n_queries, int n_slots, size_t* bytes) {
   const int st = iq_paged_attend_workspace(c, q_heads, n_queries, n_slots, bytes);

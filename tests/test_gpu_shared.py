@@ -10,8 +10,15 @@ from test_gpu_paged import bounds, f64, pair, put, rows
 pytestmark = pytest.mark.gpu
 
 
+def shared(c, q, **kw):
+    """Shared wherever there are pages to share, however little is gained."""
+    from rotated_bit_quantized_gb300 import _abi
+    assert _abi.lib().iq_paged_debug_share() == 0
+    return c.attend(q, shared=True, **kw)
+
+
 def check(c, o, q, out_dtype=torch.float32, slots=None, counts=None, scale=1 / 16, **kw):
-    out = c.attend(q.cuda(), scale=scale, slots=slots, counts=counts, out_dtype=out_dtype, shared=True, **kw)
+    out = shared(c, q.cuda(), scale=scale, slots=slots, counts=counts, out_dtype=out_dtype, **kw)
     assert out.dtype == out_dtype and out.shape == q.shape
     res = paged.attend(o, f64(q), scale, slots, counts, **kw)
     got, live = f64(out), ~np.isnan(res[0])
@@ -102,7 +109,7 @@ def test_lists_of_slots_counts_and_empty_slots():
     counts = [5, 5, 0, 4, 1, 5, 0, 2, 3, 5, 1]
     check(c, o, q, slots=slots, counts=counts)
     out = torch.full((len(slots), 8, 5, 256), 7.0, device="cuda")
-    c.attend(q.cuda(), slots=slots, counts=counts, out=out, shared=True)
+    shared(c, q.cuda(), slots=slots, counts=counts, out=out)
     for i, n in enumerate(counts):
         assert (out[i, :, n:] == 7).all() and not (out[i, :, :n] == 7).any()
 
@@ -161,15 +168,27 @@ def test_one_heavy_key_among_many():
 def test_same_results_every_time_and_on_every_path():
     c, _ = tree(2, 3000, 700, [1 + (53 * b) % 200 for b in range(20)], 4)
     q = rows(9, 20, 16, 1).cuda()
-    first = c.attend(q, shared=True)
+    first = shared(c, q)
     for _ in range(10):
-        assert torch.equal(c.attend(q, shared=True), first)
+        assert torch.equal(shared(c, q), first)
     many = rows(9, 20, 16, 17).cuda()  # 136 rows of a slot: the ordinary kernels
     assert torch.equal(c.attend(many, shared=True), c.attend(many))
     alone = rows(9, 1, 16, 1).cuda()
     assert torch.equal(c.attend(alone, slots=[3], shared=True), c.attend(alone, slots=[3]))
     small = c.compact()
-    assert torch.equal(small.attend(q, shared=True), first)
+    assert torch.equal(shared(small, q), first)
+    little, _ = tree(2, 70, 0, [1, 2])  # nothing to gain: as without
+    q = rows(9, 2, 16, 1).cuda()
+    assert torch.equal(little.attend(q, shared=True), little.attend(q))
+
+
+@pytest.mark.parametrize("paths,common,n", [(2, 512, 1), (8, 2048, 1), (32, 4096, 1), (32, 1024, 4), (5, 3000, 13)])
+def test_whichever_way_is_taken(paths, common, n):
+    c, o = tree(2, common, 0, [n + (37 * b) % 90 for b in range(paths)])
+    q = rows(9, paths, 16, n)
+    way = c.attend(q.cuda(), shared=True, out_dtype=torch.float32)
+    either = [c.attend(q.cuda(), out_dtype=torch.float32), check(c, o, q)]
+    assert any(torch.equal(way, e) for e in either)
 
 
 def test_append_attend_as_two_calls():
@@ -178,9 +197,10 @@ def test_append_attend_as_two_calls():
     b, _ = tree(2, 900, 0, [5 + b for b in range(7)])
     k, v, q = rows(5, 7, 2, 3).cuda(), rows(6, 7, 2, 3).cuda(), rows(9, 7, 8, 3).cuda()
     counts = [3, 0, 1, 2, 3, 3, 1]
+    assert _abi.lib().iq_paged_debug_share() == 0
     x = a.append_attend(k, v, q, counts=counts, shared=True, window=600, sinks=2)
     b.append(k, v, counts=counts)
-    assert torch.equal(x, b.attend(q, counts=counts, shared=True, window=600, sinks=2))
+    assert torch.equal(x, shared(b, q, counts=counts, window=600, sinks=2))
     before = a.lens.tolist()
     with pytest.raises(_abi.IQError):
         a.append_attend(k, v, q, shared=True, sinks=1)
@@ -190,22 +210,22 @@ def test_append_attend_as_two_calls():
 def test_streams_and_graphs():
     c, o = tree(2, 1500, 0, [9 + b for b in range(9)])
     q = rows(9, 9, 8, 1).cuda()
-    want = c.attend(q, shared=True)
+    want = shared(c, q)
     streams = [torch.cuda.Stream() for _ in range(3)]
     outs = []
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
-            outs += [c.attend(q, shared=True) for _ in range(4)]
+            outs += [shared(c, q) for _ in range(4)]
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in outs)
     graphs = []
     for s in streams[:2]:
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
-            graphs.append((g, c.attend(q, shared=True)))
+            graphs.append((g, shared(c, q)))
     q2 = rows(19, 9, 8, 1).cuda()
-    want2 = c.attend(q2, shared=True)
+    want2 = shared(c, q2)
     torch.cuda.synchronize()
     q.copy_(q2)
     torch.cuda.synchronize()
@@ -222,7 +242,7 @@ def test_waits_run_out():
     c, o = tree(1, 1000, 0, [5] * 4)
     q = rows(9, 4, 4, 1)
     assert _abi.lib().iq_paged_debug_stall() == 0
-    c.attend(q.cuda(), shared=True)
+    shared(c, q.cuda())
     assert c.device_status() & 0xB
     check(c, o, q)
 
@@ -231,11 +251,11 @@ def test_a_bad_page_is_told_and_read_as_another():
     from rotated_bit_quantized_gb300 import _abi
     c, o = tree(1, 1000, 0, [5] * 4)
     q = rows(9, 4, 4, 1).cuda()
-    c.attend(q, shared=True)
+    shared(c, q)
     torch.cuda.synchronize()
     keep = c.table.clone()
     c.table[:, 3] = 10**6
-    c.attend(q, shared=True)
+    shared(c, q)
     assert c.device_status() == _abi.IQ_STATUS_BAD_PAGE
     c.table.copy_(keep)
     check(c, o, rows(9, 4, 4, 1))
@@ -254,7 +274,7 @@ def test_a_decode_step_of_all_of_it():
     for step in range(4):
         x = rows(10 + step, 1, 1, 8 * 12).view(8, 1, 12, 256).transpose(1, 2).cuda()
         q = a.append_rotary(x[:, :8], x[:, 8:10], x[:, 10:], rot, slots=range(1, 9))
-        one = a.attend(q, slots=range(1, 9), shared=True, out_dtype=torch.float32)
+        one = shared(a, q, slots=range(1, 9), out_dtype=torch.float32)
         q2, k2 = rot.apply(x[:, :8], x[:, 8:10], positions=700 + step)
         assert torch.equal(q, q2)
         b.append(k2, x[:, 10:].contiguous(), slots=range(1, 9))
