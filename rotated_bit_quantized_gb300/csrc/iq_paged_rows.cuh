@@ -226,10 +226,9 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
       if constexpr (P::kTree) next_pos = __ldcg(&p.place[p.row0[u.e] + u.z * kRows + r].x);
       return __ldcg(p.factors + cut_row(p, u) + r);
     };
-    if constexpr (P::kTree) wait_only();
     bool at_first = true;
     Place w = start;
-    float next_factor = first < last ? factor_of(w) : 0.0f;
+    float next_factor = !P::kTree && first < last ? factor_of(w) : 0.0f;
     for (int at = first;; next_unit(p, w)) {
       Tiles tiles{};
       Part part{0, 0};
@@ -242,10 +241,9 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
       if (n == 0) w = start;  // no unit follows: one turn more, for the last one's results alone
       const int k0 = part.begin;
       const bool whole = !P::kTree && n == tiles.n, exists = r < rows_at(p, w);
-      int row, pos, len = 0;
+      int row, pos = 0, len = 0;
       if constexpr (P::kTree) {
         row = k0 == 0 ? p.part0[w.e] + w.h * p.n[w.e] + w.z * kRows : p.wide_cont + work.block * kRows;
-        pos = next_pos;
       } else {
         const int slot = 2 * work.block + (at == first ? 0 : 1);
         if (n > 0 && n < tiles.n && k0 == 0 && threadIdx.x == 0) tell_cut(p, work, w, at, tiles.n, slot);
@@ -255,23 +253,28 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
       }
       at += tiles.n + work.cost - w.j;
       const bool causal = P::kTree || p.causal;  // (in a tree a query that sees all has the last position)
-      const int stop = !exists ? 0 : causal ? pos + 1 : len;
-      const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
       // a row that has seen no key yet has no reference (its weights are all 0)
       bool unset = exists;
       float ref = exists ? 0.0f : 0.5f * kFar, l = 0.0f;  // (rows that do not exist weigh next to nothing)
 
-      const float fq = next_factor;
-      if (n > 0 && at < last) {
-        Place after = w;
-        next_unit(p, after);
-        next_factor = factor_of(after);
-      }
-      // A tree's units are short, and its first tile's instructions, some 40 KB, come from a
-      // cache level that all of the GPU's first loads keep busy: one turn without
-      // effect, while those are under way, fetches them.
+      int stop = 0, low = 0;  // this row's keys
+      float fq = 0.0f;
+      auto begin_unit = [&]() {
+        if constexpr (P::kTree) pos = next_pos;
+        stop = !exists ? 0 : causal ? pos + 1 : len;
+        low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+        fq = next_factor;
+        if (n > 0 && at < last) {
+          Place after = w;
+          next_unit(p, after);
+          next_factor = factor_of(after);
+        }
+      };
+      // A tree's units are short, and all SMs fetch the instructions of their first tile, some
+      // 40 KB, at once: several microseconds, which one turn without effect spends while the
+      // queries are being cut and the first pages come.
       bool rehearsal = P::kTree && at_first;
-      at_first = false;
+      if (!rehearsal) begin_unit();
       int j = 0;
       do {
         const int b = it & 1;
@@ -384,7 +387,10 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
             l = fmaf(s0 + s1, ex2_approx((x ? above1 : above0) - ev - kPlace), l);
           }
           if (P::kTree && rehearsal) {
-            rehearsal = false;
+            rehearsal = at_first = false;
+            wait_only();  // for the cut queries' factors and positions
+            next_factor = factor_of(w);
+            begin_unit();
             unset = exists;
             ref = exists ? 0.0f : 0.5f * kFar;
             l = 0.0f;
