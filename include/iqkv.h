@@ -677,13 +677,14 @@ int iq_rotary_turns(const double* frequencies, int pairs, uint64_t* turns, iq_st
  * iq_rotary_apply — queries and keys normed and turned.
  * q, k: rows [entries][q_heads or k_heads][n] of dtype; q_out, k_out: the same, contiguous,
  *   16-byte aligned, apart from the inputs and each other.  q_heads or k_heads may be 0.
- * Row j of entry i is at position start[i] + j (start: host int32 [entries], NULL: zeros),
- *   or at positions[i][j] (device int32 [entries][n]); not both.
+ * Row j of entry i is at position start[i] + j (start: host int32 [n_start], one for each
+ *   entry or one for all; n_start 0: zeros), or at positions[i][j] (device int32
+ *   [entries][n]); not both.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_heads, const iq_rows* k, int k_heads,
-                    int entries, int n, const int32_t* start, const int32_t* positions, void* q_out, void* k_out,
-                    iq_stream_t stream);
+                    int entries, int n, const int32_t* start, int n_start, const int32_t* positions, void* q_out,
+                    void* k_out, iq_stream_t stream);
 
 /*
  * iq_paged_append_rotary — iq_paged_append of a projection's rows in one launch: queries and

@@ -129,7 +129,7 @@ def lib() -> ctypes.CDLL:
         ROTARY, ROWS, D = ctypes.POINTER(IQRotaryDesc), ctypes.POINTER(IQRows), ctypes.c_double
         L.iq_rotary_frequencies.argtypes = [I, D, I, D, D, D, D, P, ctypes.POINTER(D)]
         L.iq_rotary_turns.argtypes = [P, I, P, P]
-        L.iq_rotary_apply.argtypes = [ROTARY, I, ROWS, I, ROWS, I, I, I, P, P, P, P, P]
+        L.iq_rotary_apply.argtypes = [ROTARY, I, ROWS, I, ROWS, I, I, I, P, I, P, P, P, P]
         L.iq_paged_append_rotary.argtypes = [PAGED, ROTARY, ROWS, I, ROWS, ROWS, I, P, P, I, P, P, P]
         L.iq_paged_attend_shared_workspace.argtypes = L.iq_paged_attend_workspace.argtypes
         L.iq_paged_attend_shared.argtypes = L.iq_paged_attend.argtypes

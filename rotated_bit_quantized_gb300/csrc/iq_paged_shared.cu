@@ -215,13 +215,14 @@ __global__ void __launch_bounds__(256, 4) paged_tree_join_kernel(const __grid_co
 
 // ------------------------------------------------------------------ what is shared
 
-// Microseconds, measured over 2 to 40 paths of 256 to 32768 common tokens, 2 and 8 kv heads, 1
-// to 8 queries.  A launch's CTAs all fetch the same code at once, some 50 KB each, which the
-// GPU hands out at a rate: kFetch for each.  A tile of 128 rows (near the tensor cores' rate); of at most 8,
-// 16, 32 (HBM's, or the row threads' chain); a unit's beginning and end take as long as kUnitCost tiles.
-// The three launches of this file, without these; the attention of every slot apart: two launches
-// (more rows: three), a tile of at most 8, 16, 32 rows, and of more, over the SMs, part of them from L2.
-// 2 x 8 kv heads' paths of 2048: 14 us here, 11 apart; 32: 25 and 45; 8 paths of 8192, 2 kv heads: 16 and 20.
+// Microseconds, fitted to calls of 2 to 32 paths of 256 to 32768 common tokens, 2 and 8 kv
+// heads, 1 to 8 queries.  kFetch: all CTAs of a launch fetch the same code at once, some 50 KB,
+// which the GPU hands out at a rate, so each more delays them all.  kTile: a tile of 128
+// rows; kFewTile: one of at most 8, 16, 32; a unit's beginning and end take as long as
+// kUnitCost tiles.  kLaunches: the three launches without these.  kOrdinary, kOrdinaryTile: the
+// launches of the attention of every slot apart, its tile of at most 8, 16, 32 and of
+// more rows.  Shared and apart, 2 kv heads: 2 paths of 2048 tokens 13 and 10.5 us,
+// 8 of 4096 14 and 17, 32 of 8192 22 and 43.
 constexpr double kFetch = 0.05, kTile = 1.45, kFewTile[4] = {1.0, 1.45, 1.75, 0.0}, kLaunches = 9.25;
 constexpr double kOrdinary = 8.5, kOrdinaryTile[4] = {1.2, 1.8, 3.2, 2.2};
 constexpr int kUnitCost = 3;
@@ -263,9 +264,9 @@ struct Planner {
     return t;
   }
   int row_units(int a, int b) const {
-    long long rows = 0;
-    for (int i = a; i < b; ++i) rows += static_cast<long long>(e[i].count) * rep;
-    return static_cast<int>((rows + kUnitRows - 1) / kUnitRows);
+    int rows = 0;
+    for (int i = a; i < b; ++i) rows += e[i].count * rep;
+    return (rows + kUnitRows - 1) / kUnitRows;
   }
   int add(int a, int b, int parent, bool leaf, const Tiles& t) {
     node[nodes] = {a, b, parent, leaf, t};
@@ -305,6 +306,44 @@ struct Planner {
       split(x, y, common, once ? stop : start, under, depth + (once ? 1 : 0));
     }
   }
+
+  // How the nodes' units are shared out among the SMs; false: every slot's pages apart are faster.
+  // (tiles, units: of nodes of many rows, and of leaves of few, where these are apart)
+  long long tiles[2] = {}, units[2] = {};
+  int wide = 0, narrow = 0;
+  bool share_out(int heads, int leaf_rows, int sms) {
+    const int kind = narrow_kind(leaf_rows);
+    bool alike = true;  // all units of many rows have one length
+    int length = -1;
+    for (int k = 0; k < nodes; ++k) {
+      const Node& a = node[k];
+      const int few = a.leaf && kind < 3;
+      const long long u = static_cast<long long>(heads) * row_units(a.first, a.last);
+      units[few] += u;
+      tiles[few] += u * a.tiles.n;
+      if (few) continue;
+      alike &= length < 0 || length == a.tiles.n;
+      length = a.tiles.n;
+    }
+    // the SMs go to the two kinds by what each has to do
+    const double many = kTile * (tiles[0] + units[0] * kUnitCost), few = kFewTile[kind] * (tiles[1] + units[1] * kUnitCost);
+    narrow = tiles[1] == 0 ? 0 : std::min(std::max(static_cast<int>(sms * few / (many + few) + 0.5), 1), sms - 1);
+    const int room = sms - narrow;
+    narrow = static_cast<int>(std::min<long long>(narrow, tiles[1]));
+    // Units of one length are cut into as many ranges each, so that none is of two units.
+    alike &= units[0] <= room && static_cast<int>(room % units[0]) * 16 <= room;
+    const long long sets = alike ? units[0] : 1, whole = alike ? length : tiles[0], most = room / sets;
+    // tiles of a range: so many that one CTA less saves no more than a tile costs
+    long long each = (whole + most - 1) / most;
+    auto ranges = [&](long long x) { return (whole + x - 1) / x; };
+    while (each < whole && kFetch * sets * (ranges(each) - ranges(each + 1)) > kTile) ++each;
+    wide = static_cast<int>(sets * ranges(each));
+    if (forced) return true;
+    long long apart = 0;
+    for (int i = 0; i < n; ++i) apart += static_cast<long long>(seen(i, i + 1, 0, (e[i].pages + 1) / 2).n) * heads;
+    const double shared = kLaunches + kFetch * (wide + narrow) + std::max(kTile * each, narrow ? few / narrow : 0.0);
+    return shared < kOrdinary + kFetch / 2 * std::min<long long>(apart, sms) + kOrdinaryTile[kind] * apart / sms;
+  }
 };
 
 // The rows of all nodes of one kv head are at most kDepth times the call's.
@@ -334,13 +373,13 @@ int check_shared(const iq_paged* c, const void* q, int q_heads, int n_queries, c
 
 // The attention by the tree of shared pages, where there is one; *done says whether.
 int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots,
-                float scale, int causal, int window, int sinks, void* out, int out_f32, void* workspace, iq_stream_t stream, bool* done) {
+                float scale, int causal, int window, int sinks, void* out, int out_f32, void* workspace, iq_stream_t stream, bool forced,
+                bool* done) {
   *done = false;
   const int heads = c->kv_heads;
   Planner t;
   t.rep = q_heads / heads;
-  t.forced = share_next;
-  share_next = false;
+  t.forced = forced;
   int longest = 0;
   for (int i = 0; i < n_slots; ++i) longest = std::max(longest, c->lens[slot_of(slots, i)]);
   if (window >= longest) window = sinks = 0;  // nothing is out of it, and positions less a window stay in 32 bits
@@ -354,21 +393,20 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   }
   if (t.n < 2) return IQ_OK;
   t.split(0, t.n, 0, 0, -1, 0);
-  if (t.inner == 0) return IQ_OK;
+  const int leaf_rows = t.rep * n_queries, sms = num_sms();
+  if (t.inner == 0 || !t.share_out(heads, leaf_rows, sms)) return IQ_OK;
 
   TreeParams p;
   std::memset(&p, 0, sizeof(p));
   TreeCutParams cut;
   std::memset(&cut, 0, sizeof(cut));
   // leaves of at most 32 rows, as the split kernel's calls, behind the other nodes
-  const int leaf_rows = t.rep * n_queries;
-  const bool apart = leaf_rows <= 32;
   short number[kNodes];
-  for (int wanted = 0; wanted < 2; ++wanted)
+  for (int few = 0; few < 2; ++few)
     for (int k = 0; k < t.nodes; ++k) {
-      if ((t.node[k].leaf && apart) != (wanted == 1)) continue;
+      if ((t.node[k].leaf && leaf_rows <= 32) != (few == 1)) continue;
       number[k] = static_cast<short>(p.nodes++);
-      p.leaves += wanted == 0;
+      p.leaves += few == 0;
     }
   for (int i = 0; i < t.n; ++i) {
     cut.entry[i] = static_cast<short>(t.e[i].place);
@@ -377,11 +415,11 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
     cut.row0[i + 1] = cut.row0[i] + t.e[i].count * t.rep;
   }
   p.rows = cut.row0[t.n];
-  long long tiles[2] = {}, units[2] = {}, parts = 0;  // of many rows, of few
+  long long parts = 0;
   for (int i = 0; i < t.nodes; ++i) {
     const Planner::Node& a = t.node[i];
     const Planner::Entry& holder = t.e[a.first];
-    const int k = number[i], kind = k >= p.leaves;
+    const int k = number[i];
     p.slot[k] = static_cast<short>(holder.slot);
     p.entry[k] = static_cast<short>(holder.place);
     p.parent[k] = static_cast<short>(a.parent < 0 ? -1 : number[a.parent]);
@@ -396,38 +434,13 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
     p.p_lo[k] = a.tiles.p_lo;
     p.p_hi[k] = a.tiles.p_hi;
     parts += static_cast<long long>(heads) * p.n[k];
-    const long long u = static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows);
-    units[kind] += u;
-    tiles[kind] += u * a.tiles.n;
   }
+  p.wide = t.wide;
+  p.narrow = t.narrow;
   p.narrow_rows = leaf_rows <= 8 ? 8 : leaf_rows <= 16 ? 16 : 32;
-  // the SMs go to the two kinds by what each has to do
-  const double many = static_cast<double>(tiles[0] + units[0] * kUnitCost), few = kFewTile[narrow_kind(leaf_rows)] / kTile * (tiles[1] + units[1] * kUnitCost);
-  const int sms = num_sms();
-  p.narrow = tiles[1] == 0 ? 0 : std::min(std::max(static_cast<int>(sms * few / (many + few) + 0.5), 1), sms - 1);
-  const int room = sms - p.narrow;
-  p.narrow = static_cast<int>(std::min<long long>(p.narrow, tiles[1]));
-  // Units of one length are cut into as many ranges each, so that none is of two units.  Ranges
-  // of so many tiles that what the CTAs' number costs is not above what it saves.
-  bool alike = units[0] <= room && static_cast<int>(room % units[0]) * 16 <= room;
-  for (int k = 1; k < p.leaves; ++k) alike &= p.tiles[k] == p.tiles[0];
-  const long long length = alike ? tiles[0] / units[0] : tiles[0], most = alike ? room / units[0] : room;  // cut into `most` at most
-  long long each = (length + most - 1) / most;
-  const long long sets = alike ? units[0] : 1;
-  while (each < length && kFetch * sets * ((length + each - 1) / each - (length + each) / (each + 1)) > kTile) ++each;
-  p.wide = static_cast<int>(sets * ((length + each - 1) / each));
-  if (!t.forced) {  // whether that is faster than every slot's pages apart
-    const int kind = narrow_kind(leaf_rows);
-    long long apart_tiles = 0;
-    for (int i = 0; i < t.n; ++i) apart_tiles += t.seen(i, i + 1, 0, (t.e[i].pages + 1) / 2).n * heads;
-    const double shared = kLaunches + kFetch * (p.wide + p.narrow) +
-                          std::max(kTile * each, p.narrow ? kFewTile[kind] * (tiles[1] + units[1] * kUnitCost) / p.narrow : 0.0);
-    const double ordinary = kOrdinary + (apart_tiles >= sms ? sms : apart_tiles) * kFetch / 2 + kOrdinaryTile[kind] * apart_tiles / sms;
-    if (ordinary <= shared) return IQ_OK;
-  }
   // where ranges are shorter than units, these are cut at a tile's grain
-  p.wide_cost = tiles[0] >= 8ll * p.wide || units[0] >= p.wide ? kUnitCost : 0;
-  p.narrow_cost = tiles[1] >= 8ll * p.narrow || units[1] >= p.narrow ? kUnitCost : 0;
+  p.wide_cost = t.tiles[0] >= 8ll * p.wide || t.units[0] >= p.wide ? kUnitCost : 0;
+  p.narrow_cost = t.tiles[1] >= 8ll * p.narrow || t.units[1] >= p.narrow ? kUnitCost : 0;
   long long total[2] = {};
   for (int k = 0; k < p.nodes; ++k) {
     const int kind = k >= p.leaves;
@@ -537,11 +550,13 @@ int iq_paged_attend_shared(const iq_paged* c, const void* q, int q_heads, int n_
                            size_t workspace_bytes, iq_stream_t stream) {
   const int st = check_shared(c, q, q_heads, n_queries, slots, counts, n_slots, 0, scale, causal, window, sinks, out, out_f32, workspace,
                               workspace_bytes);
+  const bool forced = share_next;
+  share_next = false;
   if (st != IQ_OK || n_slots == 0 || n_queries == 0) return st;
   if (tree_rows(c, q_heads, n_queries, n_slots)) {
     bool done = false;
     const int tree = attend_tree(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32, workspace,
-                                 stream, &done);
+                                 stream, forced, &done);
     if (tree != IQ_OK || done) return tree;
   }
   return iq_paged_attend(c, q, q_heads, n_queries, slots, counts, n_slots, scale, causal, window, sinks, out, out_f32, workspace,

@@ -733,13 +733,15 @@ int iq_rotary_turns(const double* frequencies, int pairs, uint64_t* turns, iq_st
 }
 
 int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_heads, const iq_rows* k, int k_heads, int entries,
-                    int n, const int32_t* start, const int32_t* positions, void* q_out, void* k_out, iq_stream_t stream) {
+                    int n, const int32_t* start, int n_start, const int32_t* positions, void* q_out, void* k_out, iq_stream_t stream) {
   int st = check_rotary(rotary);
   if (st != IQ_OK) return st;
   if (dtype != IQ_DTYPE_BF16 && dtype != IQ_DTYPE_F32) return fail(IQ_ERR_INVALID_ARG, "unknown dtype");
   if (q_heads < 0 || k_heads < 0 || entries < 0 || n < 0) return fail(IQ_ERR_INVALID_ARG, "negative size");
   if (entries > IQ_MAX_BATCH) return fail(IQ_ERR_INVALID_ARG, "entries above IQ_MAX_BATCH");
-  if (start && positions) return fail(IQ_ERR_INVALID_ARG, "give either start or positions");
+  if (n_start != 0 && n_start != 1 && n_start != entries) return fail(IQ_ERR_INVALID_ARG, "n_start must be 0, 1 or entries");
+  if (n_start > 0 && !start) return fail(IQ_ERR_INVALID_ARG, "null start");
+  if (n_start > 0 && positions) return fail(IQ_ERR_INVALID_ARG, "give either start or positions");
   if (misaligned(positions, 4)) return fail(IQ_ERR_INVALID_ARG, "positions not 4-byte aligned");
   if (static_cast<long long>(entries) * n >= (1LL << 30)) return fail(IQ_ERR_UNSUPPORTED, "entries * n exceeds 2^30");
   if (q_heads > (1 << 16) || k_heads > (1 << 16)) return fail(IQ_ERR_UNSUPPORTED, "too many heads");
@@ -771,7 +773,7 @@ int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_
   const Quotient by_n(n);
   p.n_mul = by_n.mul;
   p.n_shift = by_n.shift;
-  for (int i = 0; i < entries; ++i) p.start[i] = start ? start[i] : 0;
+  for (int i = 0; i < entries; ++i) p.start[i] = n_start > 0 ? start[n_start == 1 ? 0 : i] : 0;
   // A CTA holds all heads of its rows (24 at most), so that angles are worked out once, and as many rows as make
   // whole waves of CTAs, three to an SM; where there are fewer rows than that, fewer heads, down to 8.
   const int heads = q_heads + k_heads, room = 3 * num_sms();

@@ -134,10 +134,9 @@ class IQRotary:
             k_out = torch.empty((E, Hk, n, D), dtype=dtype, device=self.device)
         if E > IQ_MAX_BATCH:
             raise ValueError(f"at most {IQ_MAX_BATCH} entries")
-        start = at = None
+        start, starts, at = None, 0, None
         if type(positions) is int and -1 << 31 <= positions < 1 << 31:
-            if positions:
-                start = np.full(E, positions, dtype=np.int32)
+            start, starts = ctypes.byref(ctypes.c_int32(positions)), 1
         elif isinstance(positions, torch.Tensor):
             positions = _positions(positions, E, n, self._index)
             at = positions.data_ptr()
@@ -147,10 +146,11 @@ class IQRotary:
                 raise ValueError("positions must be one whole number, one for each entry, or an int32 CUDA tensor")
             if start.size and (start.min() < -1 << 31 or start.max() >= 1 << 31):
                 raise ValueError("positions must fit in 32 bits")
-            start = np.ascontiguousarray(np.broadcast_to(start, (E,)), dtype=np.int32)
+            each = np.ascontiguousarray(start.reshape(-1), dtype=np.int32)
+            start, starts = each.ctypes.data, each.shape[0]
         q_out = torch.empty((E, Hq, n, D), dtype=dtype, device=self.device)
         args = (self._d, code, ctypes.byref(q_rows), Hq, None if k is None else ctypes.byref(k_rows), Hk, E, n,
-                None if start is None else start.__array_interface__["data"][0], at, q_out.data_ptr(), None if k is None else k_out.data_ptr())
+                start, starts, at, q_out.data_ptr(), None if k is None else k_out.data_ptr())
         if _device() == self._index:
             st = self._lib.iq_rotary_apply(*args, self._queue())
         else:

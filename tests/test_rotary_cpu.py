@@ -63,7 +63,7 @@ OUT_Q, OUT_K = 1 << 40, 1 << 41  # far from the inputs
 
 
 def apply(L, d=None, dtype=0, q=None, qh=4, k=None, kh=2, entries=3, n=5, start=None, positions=None, q_out=OUT_Q, k_out=OUT_K):
-    return L.iq_rotary_apply(d or desc(), dtype, q or rows(), qh, k or rows(), kh, entries, n, ints(start), positions, q_out, k_out, None)
+    return L.iq_rotary_apply(d or desc(), dtype, q or rows(), qh, k or rows(), kh, entries, n, ints(start), 0 if start is None else len(start), positions, q_out, k_out, None)
 
 
 BAD_PLANS = [(dict(rd=8), UNSUPPORTED), (dict(rd=-16), UNSUPPORTED), (dict(rd=272), UNSUPPORTED), (dict(interleaved=2), INVALID), (dict(turns=0), INVALID),
@@ -74,15 +74,16 @@ BAD_PLANS = [(dict(rd=8), UNSUPPORTED), (dict(rd=-16), UNSUPPORTED), (dict(rd=27
 def test_apply_refusals(L):  # noqa: F811
     for kw, want in BAD_PLANS:
         assert apply(L, desc(**kw)) == want, kw
-    assert L.iq_rotary_apply(None, 0, rows(), 1, rows(), 1, 1, 1, None, None, OUT_Q, OUT_K, None) == INVALID
-    for kw in (dict(dtype=2), dict(qh=-1), dict(kh=-1), dict(entries=-1), dict(n=-1), dict(entries=257), dict(start=[0, 1, 2], positions=A),
+    assert L.iq_rotary_apply(None, 0, rows(), 1, rows(), 1, 1, 1, None, 0, None, OUT_Q, OUT_K, None) == INVALID
+    for kw in (dict(dtype=2), dict(qh=-1), dict(kh=-1), dict(entries=-1), dict(n=-1), dict(entries=257), dict(start=[0, 1, 2], positions=A), dict(start=[0, 1]), dict(start=[0] * 4),
                dict(positions=A + 2), dict(q=rows(at=A + 8)), dict(q=rows(row=4100)), dict(k=rows(head=252)), dict(k=rows(entry=-4096)), dict(q=rows(row=1 << 41)),
                dict(q=rows(at=0)), dict(q_out=0), dict(k_out=0), dict(q_out=OUT_Q + 8), dict(q_out=A), dict(k_out=A + 4096),
                dict(q_out=OUT_K - 16), dict(k_out=OUT_Q + 4 * 3 * 5 * 512 - 16)):
         assert apply(L, **kw) == INVALID, kw
     assert apply(L, entries=256, n=1 << 22) == UNSUPPORTED
     assert apply(L, qh=(1 << 16) + 1) == UNSUPPORTED
-    assert L.iq_rotary_apply(desc(), 0, None, 4, rows(), 2, 3, 5, None, None, OUT_Q, OUT_K, None) == INVALID
+    assert L.iq_rotary_apply(desc(), 0, None, 4, rows(), 2, 3, 5, None, 0, None, OUT_Q, OUT_K, None) == INVALID
+    assert L.iq_rotary_apply(desc(), 0, rows(), 4, rows(), 2, 3, 5, None, 1, None, OUT_Q, OUT_K, None) == INVALID
     # nothing to do, whatever the pointers are
     assert apply(L, entries=0) == 0 and apply(L, n=0, q_out=0) == 0 and apply(L, qh=0, kh=0, q_out=0, k_out=0) == 0
 
