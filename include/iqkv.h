@@ -676,7 +676,8 @@ int iq_rotary_turns(const double* frequencies, int pairs, uint64_t* turns, iq_st
 /*
  * iq_rotary_apply — queries and keys normed and turned.
  * q, k: rows [entries][q_heads or k_heads][n] of dtype; q_out, k_out: the same, contiguous,
- *   16-byte aligned, apart from the inputs and each other.  q_heads or k_heads may be 0.
+ *   16-byte aligned, apart from the inputs and each other.  q_heads or k_heads may be 0, and
+ *   2^16 at most; entries * n below 2^30.
  * Row j of entry i is at position start[i] + j (start: host int32 [n_start], one for each
  *   entry or one for all; n_start 0: zeros), or at positions[i][j] (device int32
  *   [entries][n]); not both.
@@ -690,7 +691,7 @@ int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_
  * iq_paged_append_rotary — iq_paged_append of a projection's rows in one launch: queries and
  * keys normed and turned at the positions where the rows come to stand in their slots (or at
  * positions[i][j], device int32 [n_slots][n]), keys and values quantised into the pages.
- * q, k, v: bf16 rows [n_slots][q_heads or kv_heads][n]; q_heads may be 0.
+ * q, k, v: bf16 rows [n_slots][q_heads or kv_heads][n]; q_heads may be 0, and 2^14 at most.
  * q_out: device bf16 [n_slots][q_heads][n][256], apart from the inputs; rows behind counts[i]
  *   are not read, and left as they were.
  * Codes are rounded once, from the turned keys in float32: iq_rotary_apply and then

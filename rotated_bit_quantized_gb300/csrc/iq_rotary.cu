@@ -799,7 +799,8 @@ int iq_paged_append_rotary(iq_paged* c, const iq_rotary* rotary, const iq_rows* 
   if (st != IQ_OK) return st;
   st = check_append(c, k ? k->at : nullptr, v ? v->at : nullptr, n, slots, counts, n_slots);
   if (st != IQ_OK) return st;
-  if (q_heads < 0 || q_heads > (1 << 16)) return fail(IQ_ERR_INVALID_ARG, "bad q_heads");
+  if (q_heads < 0) return fail(IQ_ERR_INVALID_ARG, "bad q_heads");
+  if (q_heads > (1 << 14)) return fail(IQ_ERR_UNSUPPORTED, "q_heads above 2^14");
   if (misaligned(positions, 4)) return fail(IQ_ERR_INVALID_ARG, "positions not 4-byte aligned");
   if (n_slots == 0 || n == 0) return IQ_OK;
   RotaryAppend m;

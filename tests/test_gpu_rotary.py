@@ -135,6 +135,35 @@ def test_extreme_rows():
         assert torch.isinf(y[4, 200]) and torch.isfinite(y[4, :200]).all()
 
 
+def test_outputs_past_32_bits():
+    """4.6 GB of results, from one row's strides of zero; and a cache's rows far apart in a large tensor."""
+    rot, ref = plan(64)
+    one = rows(1, 1, 1, 1).cuda()
+    out = rot.apply(one.expand(3, 75, 20000, 256))
+    want = rot.apply(one.expand(1, 1, 20000, 256))[0, 0]
+    for e, h in ((0, 0), (1, 40), (2, 74)):
+        assert torch.equal(out[e, h], want)
+    del out
+    from rotated_bit_quantized_gb300 import IQPagedCache
+    x = torch.zeros(2, 2 * 10**9 // 2, dtype=torch.bfloat16, device="cuda")  # entries 2 GB apart
+    q, k, v = rows(2, 2, 4, 70).cuda(), rows(3, 2, 2, 70).cuda(), rows(4, 2, 2, 70).cuda()
+    views = []
+    for at, t in ((0, q), (5 * 10**8, k), (9 * 10**8, v)):
+        views.append(x[:, at:at + t[0].numel()].view(2, *t.shape[1:]))
+        views[-1].copy_(t)
+    a, b = IQPagedCache(2, 2, 8), IQPagedCache(2, 2, 8)
+    assert torch.equal(a.append_rotary(*views, rot), b.append_rotary(q, k, v, rot))
+    assert all(torch.equal(i, j) for i, j in zip(a.read(0, 70), b.read(0, 70)))
+
+
+def test_many_heads():
+    rot, ref = plan(128, True)
+    q = rows(1, 1, 300, 9).cuda()
+    check(rot.apply(q, q[:, :7], positions=4)[0], *exact(q, 4 + np.arange(9)[None], ref, 0))
+    c, o = pair(1, 1, 4)
+    check_append(c, o, rot, ref, rows(2, 1, 300, 70), rows(3, 1, 1, 70), rows(4, 1, 1, 70))
+
+
 def test_nothing_to_turn_and_no_rows():
     rot, _ = plan(0, norm=False)
     q = rows(8, 2, 3, 9).cuda()

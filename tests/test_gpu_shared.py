@@ -147,6 +147,17 @@ def test_scales(scale):
     check(c, o, rows(9, 8, 8, 1), scale=scale)
 
 
+def test_queries_that_are_not_finite_keep_to_themselves():
+    c, o = tree(2, 700, 0, [1 + (53 * b) % 200 for b in range(8)])
+    q = rows(9, 8, 8, 2)
+    bad = q.clone()
+    bad[2, 3, 1, 17], bad[5, 0, 0, 200], bad[7, 7, 1, 0] = float("nan"), float("inf"), -float("inf")
+    good, got, apart = shared(c, q.cuda()), shared(c, bad.cuda()), c.attend(bad.cuda())
+    touched = ~torch.isfinite(bad).all(-1).cuda()
+    assert torch.equal(got[~touched], good[~touched])
+    assert torch.isnan(apart[touched]).all() and torch.isnan(got[touched]).all()
+
+
 def test_one_heavy_key_among_many():
     """What many small weights leave next to a heavy key of the shared part, and of a path's own."""
     for heavy in (5, 1290):

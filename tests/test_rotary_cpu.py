@@ -106,6 +106,7 @@ def test_append_refusals_change_nothing(L):  # noqa: F811
                dict(q_out=0), dict(q_out=OUT_Q + 2), dict(q_out=A)):
         assert append(L, f, **kw) == INVALID, kw
     assert append(L, f, n=1000) == CAPACITY
+    assert append(L, f, qh=(1 << 14) + 1) == UNSUPPORTED
     assert f.state() == before
 
 
