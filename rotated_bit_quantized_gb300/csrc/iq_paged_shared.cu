@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(rows::kThreads, 1) paged_tree_kernel(const __g
 }
 template <int NR>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
-  constexpr int kSmem = rows::kTreeSmem > split::Shape<NR>::kSmem ? rows::kTreeSmem : split::Shape<NR>::kSmem;
-  static_assert(split::Shape<NR>::kThreads <= rows::kThreads, "threads of one CTA");
+  using Few = split::TreeShape<NR>;
+  constexpr int kSmem = rows::kTreeSmem > Few::kSmem ? rows::kTreeSmem : Few::kSmem;
+  static_assert(Few::kThreads <= rows::kThreads, "threads of one CTA");
   static std::atomic<uint64_t> seen{0};
   const void* kernel = reinterpret_cast<const void*>(&paged_tree_kernel<NR>);
   const cudaError_t e = allow_smem(kernel, kSmem, seen);
@@ -218,12 +219,14 @@ __global__ void __launch_bounds__(256, 4) paged_tree_join_kernel(const __grid_co
 // Microseconds, fitted to calls of 2 to 32 paths of 256 to 32768 common tokens, 2 and 8 kv
 // heads, 1 to 8 queries.  kFetch: all CTAs of a launch fetch the same code at once, some 50 KB,
 // which the GPU hands out at a rate, so each more delays them all.  kTile: a tile of 128
-// rows; kFewTile: one of at most 8, 16, 32; a unit's beginning and end take as long as
-// kUnitCost tiles.  kLaunches: the three launches without these.  kOrdinary, kOrdinaryTile: the
+// rows; kFewTile: one of at most 8, 16, 32, beside which the first take a quarter longer (so
+// these are below what a tile of few rows takes; fitted to the best split of the SMs on 14 trees
+// of 32 to 250 paths, 500 to 2048 tokens each of their own: a third more or less of them costs 3 to
+// 8%); a unit's beginning and end take as long as kUnitCost tiles.  kLaunches: the three launches without these.  kOrdinary, kOrdinaryTile: the
 // launches of the attention of every slot apart, its tile of at most 8, 16, 32 and of
 // more rows.  Shared and apart, 2 kv heads: 2 paths of 2048 tokens 13 and 10.5 us,
 // 8 of 4096 14 and 17, 32 of 8192 22 and 43.
-constexpr double kFetch = 0.05, kTile = 1.45, kFewTile[4] = {1.0, 1.45, 1.75, 0.0}, kLaunches = 9.25;
+constexpr double kFetch = 0.05, kTile = 1.45, kFewTile[4] = {0.8, 1.0, 1.5, 0.0}, kLaunches = 9.25;
 constexpr double kOrdinary = 8.5, kOrdinaryTile[4] = {1.2, 1.8, 3.2, 2.2};
 constexpr int kUnitCost = 3;
 constexpr int narrow_kind(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3; }

@@ -20,6 +20,8 @@
 // exchange between warps but a vote.
 #pragma once
 
+#include <type_traits>
+
 #include "iq_paged_mma.cuh"
 
 namespace iq {
@@ -30,10 +32,12 @@ constexpr int kMu = 4, kHu = 1;  // products unrolled in a tree
 constexpr float kPlace = 6.0f;  // the place of a block's largest weight
 constexpr float kPLo = 128.0f;  // the low parts' scale: half a step at 2^6 is 2, times 128 below 448
 
-template <int NR>
+template <int NR, int TURNS = 1>
 struct Shape {
-  static constexpr int kGroups = NR >= 32 ? 2 : 1;    // warpgroups on the softmax, NR / kGroups rows each
+  static constexpr int kTurns = TURNS;                // tiles of the sequence on the softmax at once
+  static constexpr int kGroups = NR >= 32 ? 2 : 1;    // warpgroups on a tile, NR / kGroups rows each
   static constexpr int kRows = NR / kGroups;
+  static constexpr int kWarps = 4 * kGroups * TURNS;  // on the softmax
   static constexpr int kCols = 2 * NR;                // high and low parts
   static constexpr int kSlots = 6;                    // tiles of keys or values in flight
   static constexpr int kQ = kSlots * kSlotBytes;      // [2 halves of the dims][kCols rows][128 bytes]
@@ -41,13 +45,21 @@ struct Shape {
   static constexpr int kScales = kP + 2 * kCols * 128;  // [2] the weights'
   static constexpr int kMisc = kScales + 2 * kScaleBytes;
   static constexpr int kRing = Loader<kSlots, false>::kRing;
-  static constexpr int kFloats = 2 * NR + 4 * NR;     // factors, references; reductions
+  static constexpr int kFloats = NR + TURNS * (NR + 4 * NR);  // factors; references, reductions
   static constexpr int kBars = 2 * kSlots + kRing + 10;
   static constexpr int kSmem = kMisc + kFloats * 4 + kRing * 16 + kBars * 8 + 8;
-  static constexpr int kThreads = kGroups * 128 + 64;
-  static constexpr int kTmem = 4 * kCols;             // S twice, O of both halves of the dims
+  static constexpr int kThreads = kWarps * 32 + 64;
+  static constexpr int kTmem = (TURNS == 2 ? 8 : 4) * kCols;  // S twice, O of both halves of the dims (of every turn)
+  static_assert(TURNS == 1 || kGroups == 1, "eight warps at most");
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
+// In a tree only some of the SMs stream leaves, each at more than its share of HBM, so the
+// row threads' chain (1.1 us a tile) would set the pace: up to 16 rows, two warpgroups take the
+// tiles in turn, each with references, sums and results of its own.  Mean of 14 trees of 32 to
+// 250 paths with leaves of 500 to 2048 tokens: 48.9 us with one warpgroup, 48.2 with two at
+// 8 rows, 74.3 and 70.8 at 16.  (32 rows take two warpgroups for a tile as it is.)
+template <int NR>
+using TreeShape = Shape<NR, NR <= 16 ? 2 : 1>;
 
 // One persistent CTA per SM: warps 0 .. 4 kGroups - 1 hold a key per thread
 // (warp w reaches tensor-memory lanes 32 (w % 4) ..), then one warp streams the
@@ -70,7 +82,8 @@ struct Shape {
 // for the others.
 template <int NR, class P>
 __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem) {
-  using C = Shape<NR>;
+  using C = std::conditional_t<P::kTree, TreeShape<NR>, Shape<NR>>;
+  constexpr int kTurns = C::kTurns;
   constexpr int RT = C::kRows;
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // (the kernel has no other shared memory in front)
@@ -79,9 +92,9 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
     return;
   }
   float* factor = reinterpret_cast<float*>(smem + C::kMisc);  // [NR] 2^eq * scale * log2 e
-  float* ref = factor + NR;                                   // [NR]
-  float* red = ref + NR;                                      // [4 warps][NR]
-  float4* scales = reinterpret_cast<float4*>(red + 4 * NR);   // [kRing] of a tile's two pages: keys', values'
+  float* ref0 = factor + NR;                                  // [kTurns][NR]
+  float* red0 = ref0 + kTurns * NR;                           // [kTurns][4 warps][NR]
+  float4* scales = reinterpret_cast<float4*>(red0 + kTurns * 4 * NR);  // [kRing] of a tile's two pages: keys', values'
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kRing);  // [kSlots]
   uint64_t* empty = full + C::kSlots;                         // [kSlots]
   uint64_t* scales_in = empty + C::kSlots;                    // [kRing]
@@ -96,7 +109,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
   static_assert(NR % 8 == 0 && C::kMisc % 16 == 0, "scales and barriers are aligned");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kLoader = 4 * C::kGroups, kIssuer = kLoader + 1;
+  constexpr int kLoader = C::kWarps, kIssuer = kLoader + 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&full[s], 1);
@@ -109,7 +122,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
       mbar_init(&p_ready[s], 4 * C::kGroups);
       mbar_init(&o_done[s], 1);
     }
-    mbar_init(q_ready, 4 * C::kGroups);
+    mbar_init(q_ready, C::kWarps);
     mbar_init(drained, 1);
     *abort = 0;
     mbar_fence_init();
@@ -126,7 +139,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
   tc_after();
   release_dependents();
   const uint32_t tmem = *tslot;
-  const uint32_t t_o = tmem + 2 * C::kCols;  // O: [half of the dims][kCols]
+  const uint32_t t_o = tmem + 2 * C::kCols;  // O: [turn][half of the dims][kCols]
   const Waits wait{abort, p.status};
 
   const int first = range_begin(work.block, work.grid, work.total), last = range_begin(work.block + 1, work.grid, work.total);
@@ -174,9 +187,9 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
             for (int half = 0; half < 2; ++half)
 #pragma unroll P::kTree ? kMu : 4
               for (int k = 0; k < 4; ++k)
-                mma_scaled(t_o + half * C::kCols, at_slot + ((s * kSlotBytes + half * kHalfBytes + k * 32 * 128) >> 4),
+                mma_scaled(t_o + ((kTurns == 2 ? 2 * b : 0) + half) * C::kCols, at_slot + ((s * kSlotBytes + half * kHalfBytes + k * 32 * 128) >> 4),
                            weights + ((b * C::kCols * 128 + k * 32) >> 4), shape_scaled(128, C::kCols, true, false, 0, k), place + 4, place,
-                           j > 1 || k > 0);
+                           j > kTurns || k > 0);
             mma_commit(&o_done[b]);
             mma_commit(&empty[s]);
             ++used;
@@ -191,13 +204,16 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
     }
   } else if (warp < kLoader) {
     // ---------------------------------------------------------------- softmax: a key per thread
-    const int group = warp >> 2, key = threadIdx.x & 127, r0 = group * RT;
+    // tiles of both parities, or this warpgroup's; all rows, or its half; its barrier
+    const int turn = kTurns == 2 ? warp >> 2 : 0, group = kTurns == 2 ? 0 : warp >> 2, own_bar = 1 + (warp >> 2);
+    const int key = threadIdx.x & 127, r0 = group * RT;
+    float *ref = ref0 + turn * NR, *red = red0 + turn * 4 * NR;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     if constexpr (!P::kTree) {
       if (threadIdx.x == 0) p.cuts[work.block].last = -1;
     }
     float l[RT];
-    int it = 0;
+    int it0 = 0;
     bool ok = true;
     auto await = [&](uint64_t* bar, uint32_t phase) {  // a lost wait changes no path: every barrier below is still reached
       if (ok) ok = wait(bar, phase, kLostRows);
@@ -205,6 +221,20 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
     };
     bool at_first = true;
     Place at_unit = start;
+    // the query rows, a warp each; with turns, which leave the registers, those of the next unit
+    // are fetched before this one's tiles
+    constexpr int kEach = NR / C::kWarps;
+    uint4 raw[kEach];
+    auto fetch = [&](const Place& unit) {
+      const int rows = rows_at(p, unit);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = warp + i * C::kWarps;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows) raw[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, unit, r) * kHeadDim) + lane);
+      }
+    };
+    if (kTurns == 2 && first < last) fetch(start);
     for (int at = first; at < last; next_unit(p, at_unit)) {
       const Tiles tiles = tiles_at(p, at_unit);
       const Part part = part_of(work, at_unit, tiles.n, last - at);
@@ -222,18 +252,10 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
       }
       at += tiles.n + work.cost - at_unit.j;
       if (n == 0) break;
-      // the query rows, a warp each
-      constexpr int kEach = NR / (4 * C::kGroups);
-      uint4 raw[kEach];
+      if (kTurns == 1) fetch(at_unit);
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int r = warp + i * 4 * C::kGroups;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows) raw[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + row_index(p, at_unit, r) * kHeadDim) + lane);
-      }
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int r = warp + i * 4 * C::kGroups;
+        const int r = warp + i * C::kWarps;
         uint2 hi, lo;
         const float f = clamp_finite(split_query<16>(raw[i], hi, lo) * (p.scale * kLog2e));
         uint8_t* to = smem + C::kQ + (lane >> 4) * C::kCols * 128;
@@ -241,22 +263,30 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         *reinterpret_cast<uint2*>(to + swizzled(NR + r, (lane & 15) * 8)) = lo;
         if (lane == 0) {
           factor[r] = f;
-          ref[r] = r < rows ? kUnset : kDead;
+#pragma unroll
+          for (int x = 0; x < kTurns; ++x) ref0[x * NR + r] = r < rows ? kUnset : kDead;
         }
       }
       proxy_fence();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
-      named_bar(3, 128 * C::kGroups);
+      if (kTurns == 2 && at < last) {
+        Place next = at_unit;
+        next_unit(p, next);
+        fetch(next);
+      }
+      named_bar(3, C::kWarps * 32);
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = 0.0f;
 
       // (a tree's first turn is a rehearsal: it fetches the instructions, see the rows' kernel)
-      for (int j = P::kTree && at_first ? -1 : 0; j < n; ++j) {
-        const int b = it & 1;
+      const int j0 = kTurns == 2 ? (turn - it0) & 1 : 0;  // the first tile of this turn
+      for (int j = P::kTree && at_first ? j0 - kTurns : j0; j < n; j += kTurns) {
+        const int it = it0 + j, b = it & 1;
         const bool rehearsal = P::kTree && j < 0;
         if (!rehearsal) await(&scales_in[it % C::kRing], it / C::kRing);
-        const float* sc = reinterpret_cast<const float*>(&scales[it % C::kRing]) + (key >> 6);  // this key's page
+        static_assert((C::kRing & (C::kRing - 1)) == 0, "tile -1 has a place");
+        const float* sc = reinterpret_cast<const float*>(&scales[it & (C::kRing - 1)]) + (key >> 6);  // this key's page
         const float ks = sc[0];
         const float ev = static_cast<float>(exponent_of(sc[2]));
         const int t0 = tiles.tile(k0 + j) * kTile;
@@ -293,14 +323,15 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         int far = (lane < RT && top + ev - ref[own] > kAhead) || rehearsal;
         asm volatile("{\n.reg .pred a, b;\nsetp.ne.s32 a, %0, 0;\nbarrier.cta.red.or.pred b, %1, 128, a;\nselp.s32 %0, 1, 0, b;\n}"
                      : "+r"(far)
-                     : "r"(1 + group)
+                     : "r"(own_bar)
                      : "memory");
         if (far) {
           // some row's scores passed its reference by 2^kAhead, or are its first: move
           // the references of such rows to their maxima, and what was summed with them
           if (lane < RT) red[(warp & 3) * NR + own] = top + ev;
-          named_bar(1 + group, 128);
-          if (j > 0) await(&o_done[b ^ 1], (it - 1) / 2);
+          named_bar(own_bar, 128);
+          const bool had = j >= kTurns;  // a tile before this one, in the same sums
+          if (had) await(&o_done[(it - kTurns) & 1], (it - kTurns) / 2);
           tc_after();
 #pragma unroll
           for (int r = 0; r < RT; r += 8) {
@@ -312,10 +343,10 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
               change[y] = m - old > kAhead ? ex2_approx(old - m) : 1.0f;
               l[r + y] *= change[y];
             }
-            if (j > 0) {
+            if (had) {
 #pragma unroll
               for (int part = 0; part < 4; ++part) {  // both halves of the dims, high and low parts
-                const uint32_t c = t_o + lanes + (part >> 1) * C::kCols + (part & 1) * NR + r0 + r;
+                const uint32_t c = t_o + lanes + (2 * turn + (part >> 1)) * C::kCols + (part & 1) * NR + r0 + r;
                 float o[8];
                 tmem_ld<8>(c, o);
                 ld_wait();
@@ -325,14 +356,14 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
               }
             }
           }
-          if (j > 0) st_wait();
-          named_bar(1 + group, 128);
+          if (had) st_wait();
+          named_bar(own_bar, 128);
           if (key < RT) {
             const int x = r0 + key;
             const float m = fmaxf(fmaxf(red[x], red[NR + x]), fmaxf(red[2 * NR + x], red[3 * NR + x]));
             if (m - ref[x] > kAhead) ref[x] = m;
           }
-          named_bar(1 + group, 128);
+          named_bar(own_bar, 128);
         }
         // weights, their sums, their two parts (the buffer is free once tile it - 2 is multiplied)
         if (it >= 2) await(&o_done[b], it / 2 - 1);
@@ -364,11 +395,11 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
           to[scale_at(NR + r0 + lane, warp & 3)] = x;
         }
         if (P::kTree && rehearsal) {
-          named_bar(1 + group, 128);
+          named_bar(own_bar, 128);
           if (key < RT) ref[r0 + key] = r0 + key < rows ? kUnset : kDead;
 #pragma unroll
           for (int r = 0; r < RT; ++r) l[r] = 0.0f;
-          named_bar(1 + group, 128);
+          named_bar(own_bar, 128);
           continue;
         }
         if (group == 0) {  // the values' scales, 1; the scores' place is free until this tile is multiplied
@@ -380,9 +411,9 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[b]);
-        ++it;
       }
       at_first = false;
+      it0 += n;
       // ---- the segment's end: sums over the keys, then the results
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -391,38 +422,73 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
         if (lane == 0) red[(warp & 3) * NR + r0 + r] = x;
       }
-      await(&o_done[(it - 1) & 1], (it - 1) / 2);
+      await(&o_done[(it0 - 1) & 1], (it0 - 1) / 2);  // (the last; products end in order)
       tc_after();
-      named_bar(3, 128 * C::kGroups);
+      named_bar(3, C::kWarps * 32);
+      if constexpr (kTurns == 2) {
+        // half of the dims each: both turns' results, under the larger of their references
+        const bool had0 = n > 1 || (it0 & 1), had1 = n > 1 || !(it0 & 1);
 #pragma unroll 1
-      for (int x = 0; x < rows; x += 8) {
-        float o[2][16];  // both halves of the dims, or this group's: high parts, low parts
+        for (int x = 0; x < rows; x += 8) {
+          float o[2][16];  // of each turn: high parts, low parts
 #pragma unroll
-        for (int i = 0; i < 2 / C::kGroups; ++i) {
-          const uint32_t c = t_o + lanes + (C::kGroups == 2 ? group : i) * C::kCols + x;
-          tmem_ld<8>(c, o[i]);
-          tmem_ld<8>(c + NR, o[i] + 8);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t c = t_o + lanes + (2 * i + turn) * C::kCols + x;
+            tmem_ld<8>(c, o[i]);
+            tmem_ld<8>(c + NR, o[i] + 8);
+          }
+          ld_wait();
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = x + y;
+            if (r >= rows) break;
+            float sums[2], f[2];
+            const float top = fmaxf(ref0[r], ref0[NR + r]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float* of = red0 + i * 4 * NR + r;
+              sums[i] = of[0] + of[NR] + of[2 * NR] + of[3 * NR];
+              f[i] = ex2_approx(ref0[i * NR + r] - top);
+            }
+            // (a turn that had no tile: its sums are 0, its results another unit's)
+            const float v0 = had0 ? fmaf(o[0][8 + y], 1.0f / kPLo, o[0][y]) : 0.0f;
+            const float v1 = had1 ? fmaf(o[1][8 + y], 1.0f / kPLo, o[1][y]) : 0.0f;
+            p.part_o[static_cast<long long>(row0 + r) * kHeadDim + turn * 128 + key] = fmaf(f[0], v0, f[1] * v1);
+            if (threadIdx.x == 0)
+              p.part_ml[row0 + r] = make_float2(top, fmaf(f[0], sums[0], f[1] * sums[1]));
+          }
         }
-        ld_wait();
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const int r = x + y;
-          if (r >= rows) break;
-          const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const long long to = (whole ? row_index(p, at_unit, r) : row0 + r) * kHeadDim;
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < rows; x += 8) {
+          float o[2][16];  // both halves of the dims, or this group's: high parts, low parts
 #pragma unroll
           for (int i = 0; i < 2 / C::kGroups; ++i) {
-            const int d = (C::kGroups == 2 ? group : i) * 128 + key;
-            const float v = fmaf(o[i][8 + y], 1.0f / kPLo, o[i][y]);
-            if (whole) store_out(p.out, p.out_f32, to + d, v * inv);
-            else p.part_o[to + d] = v;
+            const uint32_t c = t_o + lanes + (C::kGroups == 2 ? group : i) * C::kCols + x;
+            tmem_ld<8>(c, o[i]);
+            tmem_ld<8>(c + NR, o[i] + 8);
           }
-          if (!whole && threadIdx.x == 0) p.part_ml[row0 + r] = make_float2(ref[r], sum);
+          ld_wait();
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = x + y;
+            if (r >= rows) break;
+            const float sum = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const long long to = (whole ? row_index(p, at_unit, r) : row0 + r) * kHeadDim;
+#pragma unroll
+            for (int i = 0; i < 2 / C::kGroups; ++i) {
+              const int d = (C::kGroups == 2 ? group : i) * 128 + key;
+              const float v = fmaf(o[i][8 + y], 1.0f / kPLo, o[i][y]);
+              if (whole) store_out(p.out, p.out_f32, to + d, v * inv);
+              else p.part_o[to + d] = v;
+            }
+            if (!whole && threadIdx.x == 0) p.part_ml[row0 + r] = make_float2(ref[r], sum);
+          }
         }
       }
       tc_before();
-      named_bar(3, 128 * C::kGroups);  // red, ref and the query buffer are free again
+      named_bar(3, C::kWarps * 32);  // red, ref and the query buffer are free again
     }
   }
   __syncthreads();

@@ -141,6 +141,19 @@ def test_many_slots_and_rows():
     check(c, o, rows(9, 256, 2, 3), torch.bfloat16)
 
 
+@pytest.mark.parametrize("Hq,n", [(8, 1), (16, 2), (32, 2)])  # of 4, 16 and 32 rows a head
+@pytest.mark.parametrize("shift", [0, 1])
+def test_leaves_of_few_tiles_in_turn(Hq, n, shift):
+    """Several leaves a CTA, of one to six tiles, odd and even numbers after one another; heavy keys in one tile of some."""
+    H, tails = 2, [1 + n + 128 * ((5 * b + b // 7 + shift) % 6) + (37 * b) % 120 for b in range(170)]
+    c, o = tree(H, 256, 0, tails, outliers=False)
+    heavy = list(range(0, 170, 3))
+    for x in (c, o):
+        x.trim([int(256 + max(1, t - 100)) for t in tails], list(range(170)))
+    put(c, o, 60 * rows(7, len(heavy), H, n), rows(8, len(heavy), H, n), heavy)
+    check(c, o, rows(9, 170, Hq, n))
+
+
 @pytest.mark.parametrize("scale", [-1 / 16, 0.0, 2.0, 1e-6])
 def test_scales(scale):
     c, o = tree(2, 700, 0, [1 + (53 * b) % 200 for b in range(8)])
