@@ -681,6 +681,7 @@ int iq_rotary_turns(const double* frequencies, int pairs, uint64_t* turns, iq_st
  * Row j of entry i is at position start[i] + j (start: host int32 [n_start], one for each
  *   entry or one for all; n_start 0: zeros), or at positions[i][j] (device int32
  *   [entries][n]); not both.
+ * An infinity makes its pair's results (with a norm, its row's) infinite or NaN.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_heads, const iq_rows* k, int k_heads,
@@ -693,7 +694,7 @@ int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_
  * positions[i][j], device int32 [n_slots][n]), keys and values quantised into the pages.
  * q, k, v: bf16 rows [n_slots][q_heads or kv_heads][n]; q_heads may be 0, and 2^14 at most.
  * q_out: device bf16 [n_slots][q_heads][n][256], apart from the inputs; rows behind counts[i]
- *   are not read, and left as they were.
+ *   are not read, and their queries come back as zeros.
  * Codes are rounded once, from the turned keys in float32: iq_rotary_apply and then
  * iq_paged_append round twice, to bfloat16 in between.
  * Everything else as iq_paged_append.

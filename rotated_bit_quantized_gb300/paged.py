@@ -270,7 +270,7 @@ class IQPagedCache:
             positions = _positions(positions, E, n, self._index)
             at = positions.data_ptr()
         if q is not None:
-            out = (torch.empty if counts is None else torch.zeros)((E, Hq, n, D), dtype=torch.bfloat16, device=self.device)
+            out = torch.empty((E, Hq, n, D), dtype=torch.bfloat16, device=self.device)
         self._run(self._lib.iq_paged_append_rotary, self._d, rotary._d, None if q is None else ctypes.byref(q_rows), Hq, ctypes.byref(k_rows),
                   ctypes.byref(v_rows), n, _at(slots), _at(counts), E, at, None if q is None else out.data_ptr(), self._queue())
         return out

@@ -16,6 +16,7 @@ from ._abi import IQ_MAX_BATCH, IQRotaryDesc, IQRows, check, lib
 from .cache import _DTYPE_CODES, _device_of, _OnDevice, _raw_stream, _stream
 
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 _SCALINGS = {"none": _abi.IQ_SCALING_NONE, "linear": _abi.IQ_SCALING_LINEAR, "ntk": _abi.IQ_SCALING_NTK,
              "yarn": _abi.IQ_SCALING_YARN, "banded": _abi.IQ_SCALING_BANDED}
 _TURNS = {"yarn": (1.0, 32.0), "banded": (1.0, 4.0)}
@@ -74,7 +75,8 @@ class IQRotary:
     (2i, 2i+1), else (i, i + rotary_dim/2).  base, scaling, factor, original, low, high: see `rotary_frequencies`;
     `frequencies` (radians per position, one for each pair) takes their place, `amplitude` overrides theirs.
     q_norm, k_norm: [256] weights of the root-mean-square norm of each head's vector before it turns (None: no norm);
-    they are taken as norm_offset + weight, in float32.
+    they are taken as norm_offset + weight, in float32, as they are now.  Once made, a plan may be used on any stream of its
+    device, and must outlive the work that uses it.
     """
 
     def __init__(self, rotary_dim: int = 256, base: float = 10000.0, interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
@@ -107,6 +109,8 @@ class IQRotary:
             self.turns = torch.empty(rotary_dim // 2, dtype=torch.int64, device=self.device)
             with _OnDevice(self._index):
                 check(self._lib.iq_rotary_turns(f.ctypes.data, rotary_dim // 2, self.turns.data_ptr(), _stream(self._index)), "iq_rotary_turns")
+        if not _capturing():  # (a captured plan is made when the graph is replayed)
+            torch.cuda.current_stream(self.device).synchronize()
         at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self._desc = IQRotaryDesc(rotary_dim, 1 if interleaved else 0, self.amplitude, eps, at(self.turns), at(self.q_norm), at(self.k_norm))
         self._d = ctypes.byref(self._desc)
@@ -117,7 +121,8 @@ class IQRotary:
 
         bf16 or float32, views with any strides (a slice of a projection's output needs no copy where its
         rows lie at multiples of 16 bytes).  positions: of the entries' first rows, the others follow (one whole number, or
-        one for each entry), or an int32 CUDA tensor [entries, n] of every row's own.
+        one for each entry), or an int32 CUDA tensor [entries, n] of every row's own.  An infinity makes the elements
+        that it turns into infinite or NaN, and with a norm the row.
         """
         dtype = q.dtype
         code = _DTYPE_CODES.get(dtype)

@@ -133,6 +133,10 @@ def test_extreme_rows():
         y = plain.apply(x.to(dtype).cuda())[0, 0]
         assert torch.isnan(y[3, 5]) and torch.isnan(y[3, 21]) and torch.isfinite(torch.cat([y[3, :5], y[3, 6:21], y[3, 22:]])).all()
         assert torch.isinf(y[4, 200]) and torch.isfinite(y[4, :200]).all()
+        x[0, 0, 2, 20] = float("inf")  # one that turns: its pair's two, and no others
+        y = plain.apply(x.to(dtype).cuda())[0, 0, 2]
+        x[0, 0, 2, 20] = 1e-25
+        assert (torch.isfinite(y) == torch.tensor([j not in (4, 20) for j in range(256)], device="cuda")).all()
 
 
 def test_outputs_past_32_bits():
@@ -329,6 +333,20 @@ def test_replays_in_a_graph_on_another_stream():
     assert torch.equal(out, want) and torch.equal(turned[0], x) and torch.equal(turned[1], y)
     assert torch.equal(att, b.attend(want))
     assert a.device_status() == 0 and b.device_status() == 0
+
+
+def test_a_plan_made_on_a_busy_stream_is_ready_for_others():
+    x, (w, *_) = rows(1, 2, 4, 30).cuda(), plan(128)[1]
+    want = plan(128)[0].apply(x, x, positions=7)
+    w = [t.cuda() for t in w]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+        from rotated_bit_quantized_gb300 import IQRotary
+        rot = IQRotary(128, scaling="none", q_norm=w[0], k_norm=w[1], norm_offset=1.0)
+    got = rot.apply(x, x, positions=7)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_chains_of_calls_without_waits():
