@@ -367,11 +367,12 @@ struct RotaryAppendParams {
   Rows q, k, v;
   uint8_t* q_out;
   const int* positions;
+  int keys_first;  // in the order of CTAs: those of all segments' keys before others
   int q_heads, group, groups, part_rows;  // queries: of `groups` groups of heads, so many rows of a page
 };
 
-// CTA (page of a segment, y, segment): the keys of kv head y, the values of kv head y -
-// heads, or the queries of a group of heads at the page's new rows.  A page's rows
+// CTA (page of a segment, y, segment; y last where keys come first): the keys of kv head y, the values of
+// kv head y - heads, or the queries of a group of heads at the page's new rows.  A page's rows
 // stay in registers as they came, two to eight lanes; keys are turned twice, for the
 // page's largest element and for the codes, which takes fewer registers than keeping
 // them in fp32.  Codes are rounded from fp32, once.
@@ -381,8 +382,8 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
   __shared__ __align__(16) float weights[kHeadDim];
   __shared__ uint32_t tops[8];
   wait_for_last_kernel();
-  const Segment sg = p.a.seg[blockIdx.z];
-  const int k = blockIdx.x, heads = p.a.heads, y = blockIdx.y;
+  const Segment sg = p.a.seg[p.keys_first ? blockIdx.y : blockIdx.z];
+  const int k = blockIdx.x, heads = p.a.heads, y = p.keys_first ? blockIdx.z : blockIdx.y;
   const int off = sg.pos % kPage;                 // rows of the segment's first page before it
   const int begin = k == 0 ? off : 0;             // this page's new rows: [begin, end)
   const int end = min(kPage, off + sg.rows - k * kPage);
@@ -697,8 +698,14 @@ cudaError_t launch_append_rotary(const AppendParams& a, int widest, int segs, cu
   const void* kernel = append_kernel_of(m.kind);
   static std::atomic<uint64_t> seen[kShift + 1][3] = {};
   const cudaError_t e = smem > 48 * 1024 ? allow_smem(kernel, 64 * 1024, seen[m.kind.layout][m.kind.k]) : cudaSuccess;
+  const int parts = 2 * a.heads + p.groups * (kPage / p.part_rows);
+  // Keys' CTAs take longest.  In a few waves of CTAs they come first, so that none of them is the
+  // last (8 x 512 rows of 8 / 4 heads: 27 us, by segments 33); in more, CTAs that follow one another
+  // read the same segment's rows, which lie side by side (16 x 2048: 101 us, keys first 109).
+  p.keys_first = static_cast<long long>(widest) * segs * parts <= 4 * 3ll * num_sms();
+  const dim3 grid = p.keys_first ? dim3(widest, segs, parts) : dim3(widest, parts, segs);
   void* args[] = {&p};
-  return e == cudaSuccess ? launch_after(kernel, dim3(widest, 2 * a.heads + p.groups * (kPage / p.part_rows), segs), 256, smem, stream, args) : e;
+  return e == cudaSuccess ? launch_after(kernel, grid, 256, smem, stream, args) : e;
 }
 
 }  // namespace

@@ -207,6 +207,8 @@ def check_append(c, o, rot, ref, q, k, v, slots=None, counts=None, positions=Non
     before = [o.lens[s] for s in ids]
     at = np.array(before)[:, None] + np.arange(n) if positions is None else positions.numpy().astype(np.int64)
     y, tol = exact(k, at, ref, 1)
+    junk = None if q is None else torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+    del junk  # what the next allocation of that size finds
     out = c.append_rotary(None if q is None else q.cuda(), k.cuda(), v.cuda(), rot, slots=slots, counts=counts,
                           positions=None if positions is None else positions.cuda())
     o.append(y, f64(v), slots, counts)
