@@ -1,6 +1,6 @@
 // Attention of many query rows per kv head over the paged 8-bit cache: what a CTA does.
 //
-// The same mathematics as the split kernel (iq_paged_attend.cu) with the query
+// The same mathematics as the split kernel (iq_paged_split.cuh) with the query
 // rows as the products' M dimension: S = Q.K^T with Q as two e4m3 parts summed
 // into one accumulator, S (128 rows x 128 keys) twice in tensor memory, and
 // O += W.V with the weights W as two e4m3 parts that the row threads write over
@@ -63,13 +63,15 @@ static_assert(kTreeSmem <= 232448, "shared memory of one CTA");
 // over 32768 keys: 736 us, 1450 TFLOP/s, 76% of a measured bf16 matrix product
 // (710 with weights that are not block-scaled, whose second product reads no
 // scales); a unit's beginning and end cost 4 to 5 tiles' time, which shows where
-// units are short: 4 x 1531 tokens 116 us, 8191 under a window of 1023 182 us
-// (118 and 188 without: references had to follow the maxima).  What counted
+// units are short: 4 x 1531 tokens 116 us, 8191 under a window of 1023 171 us.  What counted
 // on the way: the queries cut beforehand (260 to 214 us on the last), products
 // issued by a whole warp (745 to 673 us on the first), the references' rescaling
 // behind the weights, scores issued over a unit's end.
 // P: AttendParams, or TreeParams: units of slots that share pages, all of whose results
 // are partial.  smem: the whole of the CTA's, 1024-byte aligned.
+// In a tree a CTA has ten tiles or so, and its beginning counts: 32 paths of 32768 common
+// tokens, 16 / 2 heads, take 6 us until the first scores (instructions are fetched by all
+// CTAs at once, 0.14 us a kilobyte), 1.45 us a tile and 3 us for the results.
 template <class P>
 __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem) {
   const uint32_t sbase = smem_u32(smem);

@@ -61,6 +61,8 @@ __device__ inline Results results_of(const TreeParams& p, int e, int h, int row)
   return {p.part0[e] + h * p.n[e] + x, (narrow ? p.narrow_cont : p.wide_cont) + (g0 + 1) * step + x - z * kUnitRows, step, 1 + g1 - g0};
 }
 
+// 3 us for 256 rows of 2 heads, latency that the next kernel's start hides (it fetches its first
+// pages meanwhile).
 // Every row of (entry, kv head): two e4m3 parts, the factor of its scores, where it
 // stands, and where its partial results will be (a lane for each node that it is under: the
 // joining kernel, of eight warps to a row, spent most of its time on that); a warp takes
@@ -112,7 +114,12 @@ __global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_consta
 
 // ------------------------------------------------------------------ products
 
-// CTAs of both kinds, so that neither waits for the other's end.
+// CTAs of both kinds, so that neither waits for the other's end.  16 / 2 heads, with the other two
+// launches: 32 paths of 32768 common tokens 30 us (550 TFLOP/s; every path's pages apart 132),
+// bound by a tile's row threads next to its products and by a launch of short CTAs, tensor
+// pipe 35%; 128 paths of 8192 common tokens and 16 tiles each of their own 66 us (apart
+// 167), 284 MB from HBM at 4.6 TB/s under a profiler, bound by its beginning, HBM and the
+// tiles of many rows, which take a quarter longer beside it.
 template <int NR>
 __global__ void __launch_bounds__(rows::kThreads, 1) paged_tree_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled operands need it; no room to align by hand
@@ -137,7 +144,8 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
 // CTA (x, h) joins rows of kv head h, 2^shift warps a row, a lane per 8 dims, in the
 // order of nodes and ranges.  A warp asks for four partial results at a time, references
 // and sums with them, so that it takes a trip to memory or two.  Bound by these, and by
-// L2, which the results of all CTAs pass at once (20 MB for 152 ranges of 128 rows).
+// L2, which the results of all CTAs pass at once (17 MB for 32 paths of 32768 common
+// tokens: 5 us).
 struct TreeJoinParams {
   const float* part_o;
   const float2* part_ml;

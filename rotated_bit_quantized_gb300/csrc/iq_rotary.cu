@@ -312,7 +312,11 @@ struct Split {
 };
 
 // A CTA takes a block of token rows of (entries x rows) and a group of heads: their
-// items, 32 at a time.
+// items, 32 at a time, the next ones' loads in front of these ones' arithmetic.
+// Bound by HBM.  16 x 2048 rows of 16 / 2 heads, norms, 64 dims turning: 98 us, 604 MB at 6.2
+// TB/s (91% of a measured copy), DRAM traffic that of the rows, 106 instructions of a warp per
+// row, half of the issue slots.  2047 rows of 12 / 4 heads in float32, all dims, 10.6 us; a
+// single token of 32 entries 2.3 us, a launch's latency.
 template <int LAYOUT, int K, bool F32>
 __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(const __grid_constant__ RotateParams p) {
   extern __shared__ __align__(16) float table[];
@@ -376,6 +380,9 @@ struct RotaryAppendParams {
 // stay in registers as they came, two to eight lanes; keys are turned twice, for the
 // page's largest element and for the codes, which takes fewer registers than keeping
 // them in fp32.  Codes are rounded from fp32, once.
+// Bound by HBM: 32 x 4096 rows of 16 / 2 heads, 64 dims turning, take 415 us, 2.52 GB at 6.1 TB/s
+// (90% of a measured copy), 55% of the issue slots.  With all dims turning and few rows by a
+// page's 8192 cosines in front of its keys: 7 x 513 rows of 8 / 4 heads 25 us, read back with them.
 template <int LAYOUT, int K>
 __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
   extern __shared__ __align__(16) float table[];  // of the page's new rows
