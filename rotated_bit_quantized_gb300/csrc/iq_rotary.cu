@@ -703,8 +703,8 @@ cudaError_t launch_append_rotary(const AppendParams& a, int widest, int segs, cu
   if (rows == 1) p.part_rows = kPage;
   const int smem = rows * 2 * m.turn.pairs * static_cast<int>(sizeof(float));
   const void* kernel = append_kernel_of(m.kind);
-  static std::atomic<uint64_t> seen[kShift + 1][3] = {};
-  const cudaError_t e = smem > 48 * 1024 ? allow_smem(kernel, 64 * 1024, seen[m.kind.layout][m.kind.k]) : cudaSuccess;
+  static std::atomic<uint64_t> seen[kShift + 1][3] = {};  // (48 KB need no leave, the kernel's own shared memory included)
+  const cudaError_t e = smem > 32 * 1024 ? allow_smem(kernel, 64 * 1024, seen[m.kind.layout][m.kind.k]) : cudaSuccess;
   const int parts = 2 * a.heads + p.groups * (kPage / p.part_rows);
   // Keys' CTAs take longest.  In a few waves of CTAs they come first, so that none of them is the
   // last (8 x 512 rows of 8 / 4 heads: 27 us, by segments 33); in more, CTAs that follow one another

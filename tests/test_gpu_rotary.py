@@ -250,6 +250,17 @@ def test_append_layouts(rd, interleaved, norm):
     assert c.device_status() == 0
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_of_full_pages_at_every_dim(interleaved):
+    """The table of a page's cosines is up to 64 KB of shared memory, 48 at 192 dims."""
+    for rd in range(16, 257, 16):
+        rot, ref = plan(rd, interleaved)
+        for n in (62, 63, 130):
+            c, o = pair(2, 1, 9)
+            check_append(c, o, rot, ref, rows(1, 2, 1, n), rows(2, 2, 1, n), rows(3, 2, 1, n))
+            assert c.device_status() == 0
+
+
 @pytest.mark.parametrize("H,Hq", [(1, 1), (1, 8), (3, 33), (8, 8)])
 def test_append_heads_and_padded_batches(H, Hq):
     rot, ref = plan(64)
