@@ -637,7 +637,7 @@ int iq_paged_append_attend_shared(iq_paged* cache, const void* keys, const void*
 typedef struct {
   int32_t rotary_dim;     /* 0 (nothing turns) or a multiple of 16 up to 256 */
   int32_t interleaved;    /* 1: pairs are elements (2i, 2i+1); 0: (i, i + rotary_dim/2) */
-  float amplitude, eps;   /* eps: 1e-30 or more, where a weight is given */
+  double amplitude, eps;  /* in float32's range; eps 1e-30 or more, where a weight is given */
   const uint64_t* turns;  /* device [rotary_dim/2], from iq_rotary_turns (NULL where rotary_dim is 0) */
   const float* q_weight;  /* device float32 [256], 16-byte aligned; NULL: queries are not normed */
   const float* k_weight;  /* the same for keys */
@@ -695,8 +695,8 @@ int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_
  * q, k, v: bf16 rows [n_slots][q_heads or kv_heads][n]; q_heads may be 0, and 2^14 at most.
  * q_out: device bf16 [n_slots][q_heads][n][256], apart from the inputs; rows behind counts[i]
  *   are not read, and their queries come back as zeros.
- * Codes are rounded once, from the turned keys in float32: iq_rotary_apply and then
- * iq_paged_append round twice, to bfloat16 in between.
+ * Codes are those nearest to the exact turned keys (float32 where it leaves no doubt, else
+ * float64): iq_rotary_apply and then iq_paged_append round twice, to bfloat16 in between.
  * Everything else as iq_paged_append.
  */
 int iq_paged_append_rotary(iq_paged* cache, const iq_rotary* rotary, const iq_rows* q, int q_heads, const iq_rows* k,

@@ -65,8 +65,8 @@ class IQPagedDesc(ctypes.Structure):
 
 
 class IQRotaryDesc(ctypes.Structure):
-    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
-                ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_double),
+                ("eps", ctypes.c_double), ("turns", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
                 ("k_weight", ctypes.c_void_p)]
 
 

@@ -31,7 +31,7 @@ struct Turn {
   const unsigned long long* turns;
   const float* q_weight;
   const float* k_weight;
-  float amplitude, eps;
+  double amplitude, eps;
   int pairs;
 };
 struct Rows {
@@ -128,11 +128,12 @@ __device__ __forceinline__ int table_place(int j, int pairs) {
 }
 template <int V, typename Position>
 __device__ __forceinline__ void fill_table(const Turn& t, float* table, int rows, Position position) {
+  const float amplitude = static_cast<float>(t.amplitude);
   int r = threadIdx.x / t.pairs, j = threadIdx.x - r * t.pairs;
   const int down = blockDim.x / t.pairs, across = blockDim.x - down * t.pairs;
   while (r < rows) {
     const long long p = position(r);
-    const float2 u = unit_at(static_cast<unsigned>((static_cast<unsigned long long>(p) * __ldg(t.turns + j)) >> 32), t.amplitude);
+    const float2 u = unit_at(static_cast<unsigned>((static_cast<unsigned long long>(p) * __ldg(t.turns + j)) >> 32), amplitude);
     const int to = 2 * r * t.pairs + table_place<V>(j, t.pairs);
     table[to] = u.x;
     table[to + t.pairs] = u.y;
@@ -147,8 +148,8 @@ __device__ __forceinline__ void fill_table(const Turn& t, float* table, int rows
 template <int LAYOUT, bool F32>
 constexpr int kTableOrder = LAYOUT == kPairs ? 1 : Raw<F32>::V;
 
-// a c - b s, or a c + b s.  EXACT: off by its own rounding alone, the first product's
-// is made good (for float32 results and codes, see unit_at).
+// a c - b s, or a c + b s.  EXACT: off by the roundings of its sum and of what makes the
+// first product's good (for float32 results and codes, see unit_at).
 template <bool EXACT>
 __device__ __forceinline__ float less(float a, float c, float b, float s) {
   const float t = b * s, x = fmaf(a, c, -t);
@@ -156,15 +157,32 @@ __device__ __forceinline__ float less(float a, float c, float b, float s) {
   return x;
 }
 
+// What looks at the results of turn_row: of elements e0 and e1, which were turned from elements
+// whose magnitudes' sums are m0 and m1, and of e and e + 1, which do not turn.
+struct NoLook {
+  __device__ __forceinline__ void turned(int, float, float, int, float, float) {}
+  __device__ __forceinline__ void rest(int, float, float) {}
+};
+
 // A row's vector, turned (a whole warp, four rows).  row: its cosines, then its sines.
-template <int LAYOUT, int K, bool F32, bool EXACT>
-__device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int pairs, int l) {
+template <int LAYOUT, int K, bool F32, bool EXACT, class Look>
+__device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int pairs, int l, Look& look) {
   constexpr int V = Raw<F32>::V, C = Raw<F32>::C;
-  if constexpr (LAYOUT == kPairs) {
+  auto rest = [&](int c) {  // a piece that does not turn
+#pragma unroll
+    for (int i = 0; i < V; i += 2) look.rest(V * c + i, x[V * c + i], x[V * c + i + 1]);
+  };
+  if constexpr (LAYOUT == kNone) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) rest(c);
+  } else if constexpr (LAYOUT == kPairs) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = (c * 8 * V + V * l) / 2;
-      if (j >= pairs) continue;
+      if (j >= pairs) {
+        rest(c);
+        continue;
+      }
       float co[4], si[4];
       if constexpr (F32) {
         const float2 a = *reinterpret_cast<const float2*>(row + j), b = *reinterpret_cast<const float2*>(row + pairs + j);
@@ -178,6 +196,8 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
         const float a = x[V * c + 2 * i], b = x[V * c + 2 * i + 1];
         x[V * c + 2 * i] = less<EXACT>(a, co[i], b, si[i]);
         x[V * c + 2 * i + 1] = less<EXACT>(a, si[i], -b, co[i]);
+        const float m = fabsf(a) + fabsf(b);
+        look.turned(V * c + 2 * i, x[V * c + 2 * i], m, V * c + 2 * i + 1, x[V * c + 2 * i + 1], m);
       }
     }
   } else if constexpr (LAYOUT == kHere) {
@@ -193,9 +213,13 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
           const float a = x[V * c + i + k], b = x[V * (c + K) + i + k];
           x[V * c + i + k] = less<EXACT>(a, cs[k], b, ss[k]);
           x[V * (c + K) + i + k] = less<EXACT>(a, ss[k], -b, cs[k]);
+          const float m = fabsf(a) + fabsf(b);
+          look.turned(V * c + i + k, x[V * c + i + k], m, V * (c + K) + i + k, x[V * (c + K) + i + k], m);
         }
       }
     }
+#pragma unroll
+    for (int c = 2 * K; c < C; ++c) rest(c);
   } else if constexpr (LAYOUT == kSwap || LAYOUT == kShift) {
     const int shift = pairs / V - 8 * K, lane = threadIdx.x & 31;
     const int up = (lane & 24) + ((l + shift) & 7), down = (lane & 24) + ((l - shift) & 7);
@@ -210,13 +234,17 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
       const int unit = c * 8 + l, half = pairs / V;
-      if (unit >= 2 * half) continue;
+      if (unit >= 2 * half) {
+        rest(c);
+        continue;
+      }
       const bool upper = unit >= half;
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
         const float* at = row + i * half + (upper ? unit - half : unit) * 4;
         const float4 co = *reinterpret_cast<const float4*>(at), si = *reinterpret_cast<const float4*>(at + pairs);
         const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+        float m[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float b;
@@ -230,10 +258,16 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
             const float back = borrow ? from_down[V * (c - K - 1 > 0 ? c - K - 1 : 0) + e] : from_down[V * (c - K > 0 ? c - K : 0) + e];
             b = upper ? back : on;
           }
+          m[k] = fabsf(x[V * c + i + k]) + fabsf(b);
           x[V * c + i + k] = less<EXACT>(x[V * c + i + k], cs[k], upper ? -b : b, ss[k]);
         }
+        const int e = V * c + i;
+        look.turned(e, x[e], m[0], e + 1, x[e + 1], m[1]);
+        look.turned(e + 2, x[e + 2], m[2], e + 3, x[e + 3], m[3]);
       }
     }
+#pragma unroll
+    for (int c = kPieces; c < C; ++c) rest(c);
   }
 }
 
@@ -352,10 +386,11 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(c
     raw.get(x);
     load(item + 32);
     if (p.turn.q_weight || p.turn.k_weight) {
-      const float inv = inverse_norm(x, p.turn.eps);
+      const float inv = inverse_norm(x, static_cast<float>(p.turn.eps));
       if (is_k ? p.turn.k_weight : p.turn.q_weight) weigh<F32>(x, inv, weights[is_k], l);
     }
-    turn_row<LAYOUT, K, F32, F32>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
+    NoLook look;
+    turn_row<LAYOUT, K, F32, F32>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l, look);
     if (item >= items) continue;
     const int e = divided(r0 + r, p.n_mul, p.n_shift), all = is_k ? p.k_heads : p.q_heads;
     const long long to = (static_cast<long long>(e) * all + (is_k ? head - p.q_heads : head)) * p.n + (r0 + r - e * p.n);
@@ -364,6 +399,127 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(c
 }
 
 // ------------------------------------------------------------------ rows into pages
+
+// The elements (bits, of a lane's 32) whose codes fp32 leaves open: what it may be off by
+// reaches over a border of two codes.  With u = 2^-24, y the result and m the sum of the
+// magnitudes that it is turned from: the norm's sum 12 u at most (chains of 8, 5 levels of a tree), its
+// factor then 7.5, of y; the product's rounding and its correction's 2, of y; the weight's products 2 and
+// the cosines' 1.6, of m.  Elements that do not turn: 9.5 u, or nothing without a norm.
+// About one element in 60,000.  32 x 4096 rows: 493 us where 481 left each such code to fp32.
+struct NearBorder {
+  float unit, of_y, of_m, of_rest;
+  uint32_t elements = 0;
+  __device__ __forceinline__ NearBorder(float unit, float amplitude, bool norm)
+      : unit(unit), of_y((norm ? 9.6f : 2.1f) * 0x1p-24f * unit), of_m((norm ? 3.7f : 1.7f) * 0x1p-24f * unit * amplitude), of_rest(norm ? of_y : 0.0f) {}
+  __device__ __forceinline__ void ends(int e0, float y0, float off0, int e1, float y1, float off1) {
+    const uint32_t apart = e4m3x2(fmaf(y0, unit, off0), fmaf(y1, unit, off1)) ^ e4m3x2(fmaf(y0, unit, -off0), fmaf(y1, unit, -off1));
+    if (apart) elements |= (apart & 0xFF ? 1u << e0 : 0u) | (apart >> 8 ? 1u << e1 : 0u);
+  }
+  __device__ __forceinline__ void turned(int e0, float y0, float m0, int e1, float y1, float m1) {
+    ends(e0, y0, fmaf(fabsf(y0), of_y, m0 * of_m), e1, y1, fmaf(fabsf(y1), of_y, m1 * of_m));
+  }
+  __device__ __forceinline__ void rest(int e, float y0, float y1) { ends(e, y0, fabsf(y0) * of_rest, e + 1, y1, fabsf(y1) * of_rest); }
+};
+// Cosine and sine of a / 2^64 turns in fp64: the nearest quarter taken off, Taylor's series.
+__device__ __forceinline__ double2 exact_unit_at(unsigned long long a) {
+  const unsigned quarter = static_cast<unsigned>((a + (1ull << 61)) >> 62);
+  const double t = static_cast<double>(static_cast<long long>(a - (static_cast<unsigned long long>(quarter) << 62))) * (6.283185307179586476925 * 0x1p-64);
+  const double t2 = t * t;
+  double s = -1.0 / 1307674368000, c = 1.0 / 20922789888000;
+  s = fma(s, t2, 1.0 / 6227020800);
+  s = fma(s, t2, -1.0 / 39916800);
+  s = fma(s, t2, 1.0 / 362880);
+  s = fma(s, t2, -1.0 / 5040);
+  s = fma(s, t2, 1.0 / 120);
+  s = fma(s, t2, -1.0 / 6);
+  s = fma(s * t2, t, t);
+  c = fma(c, t2, -1.0 / 87178291200);
+  c = fma(c, t2, 1.0 / 479001600);
+  c = fma(c, t2, -1.0 / 3628800);
+  c = fma(c, t2, 1.0 / 40320);
+  c = fma(c, t2, -1.0 / 720);
+  c = fma(c, t2, 1.0 / 24);
+  c = fma(c, t2, -0.5);
+  c = fma(c, t2, 1.0);
+  if (quarter & 1) {
+    const double x = c;
+    c = -s;
+    s = x;
+  }
+  return quarter & 2 ? make_double2(-c, -s) : make_double2(c, s);
+}
+__device__ __forceinline__ float bf16_at(const uint8_t* row, int d) {
+  return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row) + d)) << 16);
+}
+// Such elements again, in fp64, a warp's rows octet and octet + 32 of a page (`first`, `second`: the
+// lane's elements of each; rows: where the page's row 0 would be).  fp64 runs at a sixtieth of
+// fp32's rate, so squares, which fp32 holds, are summed there with what is rounded off; where they
+// leave its range, in fp64.
+template <bool PAIRS>
+__device__ __noinline__ void exact_codes(const Turn& t, const uint8_t* rows, long long stride, const int* positions, int position, float unit,
+                                         uint32_t first, uint32_t second, uint8_t* codes) {
+  const int l = threadIdx.x & 7;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    uint32_t elements = i ? second : first;
+    const uint32_t wanted = __ballot_sync(0xFFFFFFFFu, elements != 0);
+    if (wanted == 0) continue;
+    const bool here = (wanted >> (threadIdx.x & 24) & 0xFF) != 0;  // some lane of the row's eight
+    const int r = (threadIdx.x >> 3) + 32 * i;
+    const uint8_t* row = rows + r * stride;
+    double norm = 1.0;
+    if (t.k_weight) {
+      Raw<false> raw;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) raw.x[c] = make_uint4(0, 0, 0, 0);
+      if (here) raw.load(row, l);
+      float x[32], s[4] = {}, off[4] = {};
+      raw.get(x);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const float q = x[e] * x[e], before = s[e & 3], sum = before + q, back = sum - before;
+        off[e & 3] += (before - (sum - back)) + (q - back);
+        s[e & 3] = sum;
+      }
+      double sum = (static_cast<double>(s[0]) + s[1]) + (static_cast<double>(s[2]) + s[3]) + ((off[0] + off[1]) + (off[2] + off[3]));
+      const bool far = here && !(sum < 1e30 && sum > 1e-20);
+      if (__any_sync(0xFFFFFFFFu, far)) {
+        sum = 0.0;
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) {
+          const double y = here ? bf16_at(row, (e >> 3) * 64 + l * 8 + (e & 7)) : 0.0f;
+          sum = fma(y, y, sum);
+        }
+      }
+#pragma unroll
+      for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      sum = fma(sum, 1.0 / kHeadDim, t.eps);
+      norm = __frsqrt_rn(static_cast<float>(sum));  // off by 2^-23, and after a step of Newton's 2^-45
+      norm = sum < 1e30 && sum > 1e-30 ? norm * fma(-0.5 * sum * norm, norm, 1.5) : 1.0 / sqrt(sum);
+    }
+    const int at = !positions ? position + r : here ? __ldg(positions + r) : 0;
+    auto element = [&](int d) {
+      const double x = bf16_at(row, d);
+      return t.k_weight ? x * norm * static_cast<double>(__ldg(t.k_weight + d)) : x;
+    };
+#pragma unroll 1
+    for (; elements; elements &= elements - 1) {
+      const int e = __ffs(elements) - 1, d = (e >> 3) * 64 + l * 8 + (e & 7);
+      double y = element(d);
+      if (d < 2 * t.pairs) {
+        const bool upper = PAIRS ? d & 1 : d >= t.pairs;
+        const int j = PAIRS ? d >> 1 : upper ? d - t.pairs : d;
+        const double other = element(PAIRS ? d ^ 1 : upper ? d - t.pairs : d + t.pairs);
+        const double2 u = exact_unit_at(__ldg(t.turns + j) * static_cast<unsigned long long>(static_cast<long long>(at)));
+        y = t.amplitude * fma(y, u.x, upper ? other * u.y : -other * u.y);
+      }
+      y *= unit;
+      float z = __double2float_rz(y);  // to odd, so that the code's rounding is the only one
+      if (static_cast<double>(z) != y) z = __uint_as_float(__float_as_uint(z) | 1u);
+      codes[r * kHeadDim + d] = static_cast<uint8_t>(e4m3x2(z, 0.0f));
+    }
+  }
+}
 
 struct RotaryAppendParams {
   AppendParams a;  // (keys and values: unused)
@@ -379,10 +535,10 @@ struct RotaryAppendParams {
 // kv head y - heads, or the queries of a group of heads at the page's new rows.  A page's rows
 // stay in registers as they came, two to eight lanes; keys are turned twice, for the
 // page's largest element and for the codes, which takes fewer registers than keeping
-// them in fp32.  Codes are rounded from fp32, once.
-// Bound by HBM: 32 x 4096 rows of 16 / 2 heads, 64 dims turning, take 415 us, 2.52 GB at 6.1 TB/s
-// (90% of a measured copy), 55% of the issue slots.  With all dims turning and few rows by a
-// page's 8192 cosines in front of its keys: 7 x 513 rows of 8 / 4 heads 25 us, read back with them.
+// them in fp32.  Codes are those nearest to the exact keys (see NearBorder).
+// Bound by HBM: 32 x 4096 rows of 16 / 2 heads, 64 dims turning, take 427 us, 2.52 GB at 5.9 TB/s
+// (87% of a measured copy), 57% of the issue slots.  With all dims turning and few rows by a
+// page's 8192 cosines in front of its keys: 7 x 513 rows of 8 / 4 heads 29 us, read back with them.
 template <int LAYOUT, int K>
 __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
   extern __shared__ __align__(16) float table[];  // of the page's new rows
@@ -429,8 +585,9 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
       float x[32];
       raw[0].get(x);
       load(item + 32);
-      if (p.turn.q_weight) weigh<false>(x, inverse_norm(x, p.turn.eps), weights, l);
-      turn_row<LAYOUT, K, false, false>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
+      if (p.turn.q_weight) weigh<false>(x, inverse_norm(x, static_cast<float>(p.turn.eps)), weights, l);
+      NoLook look;
+      turn_row<LAYOUT, K, false, false>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l, look);
       if (item >= items) continue;
       const long long to = (static_cast<long long>(sg.entry) * p.q_heads + head0 + h) * p.a.n + row0 + first + r;
       Raw<false>::store(p.q_out + to * Raw<false>::kRowBytes, l, x);
@@ -457,11 +614,11 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
   const int octet0 = octet & ~3;
   auto idle = [&](int i) { return octet0 + 32 * i + 4 <= begin || octet0 + 32 * i >= end; };  // no new row in this warp
   float inv[2] = {};
-  auto turned = [&](int i, float (&x)[32]) {  // (rows that are not new are all zeros)
+  auto turned = [&](int i, float (&x)[32], auto& look) {  // (rows that are not new are all zeros)
     raw[i].get(x);
     if (weight) weigh<false>(x, inv[i], weights, l);
     const int r = min(max(octet + 32 * i, begin), end - 1) - begin;
-    turn_row<LAYOUT, K, false, true>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l);
+    turn_row<LAYOUT, K, false, true>(x, table + 2 * r * p.turn.pairs, p.turn.pairs, l, look);
   };
   uint32_t top = 0;
   bool odd;  // not a number, held as 0, or infinite, held as the largest value
@@ -492,9 +649,10 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
       float x[32];
       if (weight) {
         raw[i].get(x);
-        inv[i] = inverse_norm(x, p.turn.eps);
+        inv[i] = inverse_norm(x, static_cast<float>(p.turn.eps));
       }
-      turned(i, x);
+      NoLook look;
+      turned(i, x, look);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         most = fmaxf(most, fabsf(x[j]));
@@ -515,13 +673,19 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
   const int old = begin > 0 ? exponent_of(scales[at_from]) : e;
   e = max(e, old);
   const float unit = power2(-e);
+  uint32_t again[2] = {};  // elements whose codes fp32 leaves open
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (idle(i)) continue;
     const int r = octet + 32 * i;
     float x[32];
-    if (is_v) raw[i].get(x);
-    else turned(i, x);
+    if (is_v) {
+      raw[i].get(x);
+    } else {
+      NearBorder near(unit, fabsf(static_cast<float>(p.turn.amplitude)), weight != nullptr);
+      turned(i, x, near);
+      again[i] = odd || r < begin || r >= end ? 0 : near.elements;
+    }
     if (r < begin || r >= end) continue;
     if (odd)
 #pragma unroll
@@ -534,6 +698,10 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
                      e4m3x2(z[4] * unit, z[5] * unit) | e4m3x2(z[6] * unit, z[7] * unit) << 16);
     }
   }
+  if (__any_sync(0xFFFFFFFFu, (again[0] | again[1]) != 0))
+    exact_codes<LAYOUT == kPairs>(p.turn, p.k.at + sg.entry * p.k.entry + h * p.k.head + row0 * p.k.row, p.k.row,
+                                  p.positions ? p.positions + static_cast<long long>(sg.entry) * p.a.n + row0 : nullptr, sg.pos - off + k * kPage, unit,
+                                  again[0], again[1], codes);
   upkeep((is_v ? p.a.v_codes : p.a.k_codes) + at_from * kPageBytes, codes, begin, end, from != page, old, e);
   if (odd || beyond) atomicOr(p.a.status, IQ_STATUS_RANGE);
   __syncthreads();  // the old scale has been read by every thread
@@ -609,11 +777,11 @@ int check_rotary(const iq_rotary* r) {
   if (r->rotary_dim > 0) {
     if (!r->turns) return fail(IQ_ERR_INVALID_ARG, "null turns");
     if (misaligned(r->turns, 8)) return fail(IQ_ERR_INVALID_ARG, "turns not 8-byte aligned");
-    if (!(r->amplitude - r->amplitude == 0.0f)) return fail(IQ_ERR_INVALID_ARG, "amplitude is not finite");
+    if (!std::isfinite(static_cast<float>(r->amplitude))) return fail(IQ_ERR_INVALID_ARG, "amplitude is not finite");
   }
   if (r->q_weight || r->k_weight) {
     if (misaligned(r->q_weight) || misaligned(r->k_weight)) return fail(IQ_ERR_INVALID_ARG, "weights not 16-byte aligned");
-    if (!(r->eps >= 1e-30f && r->eps < __builtin_huge_valf())) return fail(IQ_ERR_INVALID_ARG, "eps must be 1e-30 or more, and finite");
+    if (!(r->eps >= 1e-30 && std::isfinite(static_cast<float>(r->eps)))) return fail(IQ_ERR_INVALID_ARG, "eps must be 1e-30 or more, and finite");
   }
   return IQ_OK;
 }

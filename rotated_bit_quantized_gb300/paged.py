@@ -250,7 +250,7 @@ class IQPagedCache:
 
         q [entries, Hq, n, D], keys, values [entries, Hkv, n, D]: bf16 CUDA tensors, views with any strides (see
         `IQRotary.apply`).  Rows behind counts[i] are not read; their queries come back as zeros.  Keys
-        are rounded to their codes once, from float32.
+        are held as the codes nearest to what the formula gives without any rounding.
         """
         if rotary._index != self._index:
             raise ValueError("the rotary plan must be on the cache's device")

@@ -94,9 +94,9 @@ class IQRotary:
         else:
             f, own = rotary_frequencies(rotary_dim, base, scaling, factor, original, low, high) if rotary_dim else (np.zeros(0), 1.0)
         self.frequencies, self.amplitude = f, float(own if amplitude is None else amplitude)
-        if not np.isfinite(self.amplitude):
+        if not np.isfinite(self.amplitude) or abs(self.amplitude) > 3e38:
             raise ValueError("amplitude must be finite")
-        if (q_norm is not None or k_norm is not None) and not 1e-30 <= eps < float("inf"):
+        if (q_norm is not None or k_norm is not None) and not 1e-30 <= eps <= 3e38:
             raise ValueError("eps must be 1e-30 or more, and finite")
         for w in (q_norm, k_norm):
             if w is not None and (w.shape != (256,) or not w.is_floating_point()):

@@ -273,6 +273,38 @@ def test_append_heads_and_padded_batches(H, Hq):
     assert c.device_status() == 0
 
 
+@pytest.mark.parametrize("rd,interleaved,norm,scaling", [(64, False, True, "none"), (256, False, True, "none"), (96, False, True, "yarn"), (160, False, False, "none"),
+                                                         (128, True, True, "yarn"), (64, True, False, "none"), (128, False, True, "none"), (0, False, True, "none")])
+def test_codes_are_the_nearest_to_the_exact_keys(rd, interleaved, norm, scaling):
+    """Four million codes, of which fp32 alone would put some on the wrong side of a border; in fp64 a border is
+    missed where a key lies within 2^-45 or so of it, once in 10^11."""
+    from rotated_bit_quantized_gb300 import IQPagedCache, IQRotary
+    E, H, n = 8, 2, 1024
+    g = torch.Generator().manual_seed(5)
+    w = (0.3 * torch.randn(256, generator=g) * 1024).round() / 1024 if norm else None  # 1 + w is exact
+    rot = IQRotary(rd, interleaved=interleaved, scaling=scaling, factor=8.0, original=4096, k_norm=w, norm_offset=1.0)
+    c = IQPagedCache(E, H, E * n // 64)
+    k, v = rows(6, E, H, n, True).cuda(), rows(7, E, H, n).cuda()
+    k[:, :, ::7] *= 0.01
+    at = torch.randint(0, 1 << 17, (E, n), generator=g, dtype=torch.int32).cuda()
+    at[0, :100] = 0
+    c.append_rotary(None, k, v, rot, positions=at)
+    y = k.double()
+    if norm:
+        y = y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt() * (1.0 + w.double().cuda())
+    if rd:
+        angle = (at.double()[..., None] * torch.from_numpy(rot.frequencies).cuda())[:, None]
+        a, b = (y[..., :rd:2], y[..., 1:rd:2]) if interleaved else (y[..., : rd // 2], y[..., rd // 2: rd])
+        x, z = rot.amplitude * (a * angle.cos() - b * angle.sin()), rot.amplitude * (a * angle.sin() + b * angle.cos())
+        y = torch.cat([torch.stack([x, z], -1).flatten(-2) if interleaved else torch.cat([x, z], -1), y[..., rd:]], -1)
+    scale = c.k_scales[c.table[:, : n // 64].long()].double().transpose(1, 2).repeat_interleave(64, 2)[..., None]
+    z = y / scale
+    step = torch.exp2(torch.floor(torch.log2(z.abs().clamp_min(2.0**-6))) - 3)
+    held = c.read(0, n)[0].double() / scale
+    assert (held == (torch.round(z / step) * step)).all()
+    assert c.device_status() == 0
+
+
 def test_append_copies_shared_pages():
     rot, ref = plan(64)
     c, o = pair(4, 2, 30, 400)
