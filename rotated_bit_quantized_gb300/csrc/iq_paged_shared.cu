@@ -283,12 +283,21 @@ struct Planner {
     node[nodes] = {a, b, parent, leaf, t};
     return nodes++;
   }
+  // Where [from, to) of two rows begins to differ, 64 ids at a time as long as it does not (one
+  // at a time, 32 paths of 512 pages took the host 6 us).
+  static int alike(const int32_t* u, const int32_t* v, int from, int to) {
+    constexpr int kAtOnce = 64;
+    while (from + kAtOnce <= to && std::memcmp(u + from, v + from, kAtOnce * sizeof(int32_t)) == 0) from += kAtOnce;
+    while (from < to && u[from] == v[from]) ++from;
+    return from;
+  }
   // Entries [a, b) hold the same first `page` pages; tiles before `start` are those of `parent` and above.
   void split(int a, int b, int page, int start, int parent, int depth) {
-    std::sort(e + a, e + b, [&](const Entry& x, const Entry& y) {
+    const auto before = [&](const Entry& x, const Entry& y) {
       const int i = x.pages > page ? x.row[page] : -1, j = y.pages > page ? y.row[page] : -1;
       return i != j ? i < j : x.place < y.place;
-    });
+    };
+    if (!std::is_sorted(e + a, e + b, before)) std::sort(e + a, e + b, before);  // (mostly they are)
     for (int x = a, y; x < b; x = y) {
       y = x + 1;
       if (e[x].pages > page)
@@ -300,9 +309,7 @@ struct Planner {
       }
       int common = e[x].pages, most = e[x].pages;
       for (int i = x + 1; i < y; ++i) {
-        const int32_t *u = e[x].row, *v = e[i].row;
-        const int32_t* end = std::mismatch(u + page, u + std::min(common, e[i].pages), v + page).first;
-        common = static_cast<int>(end - u);
+        common = alike(e[x].row, e[i].row, page, std::min(common, e[i].pages));
         most = std::max(most, e[i].pages);
       }
       const int stop = common == most ? (common + 1) / 2 : common / 2;
