@@ -157,10 +157,10 @@ __device__ __forceinline__ float less(float a, float c, float b, float s) {
   return x;
 }
 
-// What looks at the results of turn_row: of elements e0 and e1, which were turned from elements
-// whose magnitudes' sums are m0 and m1, and of e and e + 1, which do not turn.
+// What looks at the results of turn_row: y0 and y1 of elements e and e + 1, which were turned from
+// elements whose magnitudes' sums are m0 and m1, or do not turn.
 struct NoLook {
-  __device__ __forceinline__ void turned(int, float, float, int, float, float) {}
+  __device__ __forceinline__ void turned(int, float, float, float, float) {}
   __device__ __forceinline__ void rest(int, float, float) {}
 };
 
@@ -197,7 +197,7 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
         x[V * c + 2 * i] = less<EXACT>(a, co[i], b, si[i]);
         x[V * c + 2 * i + 1] = less<EXACT>(a, si[i], -b, co[i]);
         const float m = fabsf(a) + fabsf(b);
-        look.turned(V * c + 2 * i, x[V * c + 2 * i], m, V * c + 2 * i + 1, x[V * c + 2 * i + 1], m);
+        look.turned(V * c + 2 * i, x[V * c + 2 * i], m, x[V * c + 2 * i + 1], m);
       }
     }
   } else if constexpr (LAYOUT == kHere) {
@@ -208,13 +208,19 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
         const float* at = row + i * (pairs / V) + (c * 8 + l) * 4;
         const float4 co = *reinterpret_cast<const float4*>(at), si = *reinterpret_cast<const float4*>(at + pairs);
         const float cs[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+        float m[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float a = x[V * c + i + k], b = x[V * (c + K) + i + k];
           x[V * c + i + k] = less<EXACT>(a, cs[k], b, ss[k]);
           x[V * (c + K) + i + k] = less<EXACT>(a, ss[k], -b, cs[k]);
-          const float m = fabsf(a) + fabsf(b);
-          look.turned(V * c + i + k, x[V * c + i + k], m, V * (c + K) + i + k, x[V * (c + K) + i + k], m);
+          m[k] = fabsf(a) + fabsf(b);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const int e = V * c + i + k, f = e + V * K;
+          look.turned(e, x[e], m[k], x[e + 1], m[k + 1]);
+          look.turned(f, x[f], m[k], x[f + 1], m[k + 1]);
         }
       }
     }
@@ -262,8 +268,8 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
           x[V * c + i + k] = less<EXACT>(x[V * c + i + k], cs[k], upper ? -b : b, ss[k]);
         }
         const int e = V * c + i;
-        look.turned(e, x[e], m[0], e + 1, x[e + 1], m[1]);
-        look.turned(e + 2, x[e + 2], m[2], e + 3, x[e + 3], m[3]);
+        look.turned(e, x[e], m[0], x[e + 1], m[1]);
+        look.turned(e + 2, x[e + 2], m[2], x[e + 3], m[3]);
       }
     }
 #pragma unroll
@@ -272,12 +278,12 @@ __device__ __forceinline__ void turn_row(float (&x)[32], const float* row, int p
 }
 
 __device__ __forceinline__ float square_sum(const float (&x)[32], float unit) {
-  float a[4];
+  float a[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = (x[i] * unit) * (x[i] * unit);
+  for (int i = 0; i < 8; ++i) a[i] = (x[i] * unit) * (x[i] * unit);
 #pragma unroll
-  for (int i = 4; i < 32; ++i) a[i & 3] = fmaf(x[i] * unit, x[i] * unit, a[i & 3]);
-  float sum = (a[0] + a[1]) + (a[2] + a[3]);
+  for (int i = 8; i < 32; ++i) a[i & 7] = fmaf(x[i] * unit, x[i] * unit, a[i & 7]);
+  float sum = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
 #pragma unroll
   for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
   return sum;
@@ -400,47 +406,40 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(c
 
 // ------------------------------------------------------------------ rows into pages
 
-// The elements (bits, of a lane's 32) whose codes fp32 leaves open: what it may be off by
-// reaches over a border of two codes.  With u = 2^-24, y the result and m the sum of the
-// magnitudes that it is turned from: the norm's sum 12 u at most (chains of 8, 5 levels of a tree), its
-// factor then 7.5, of y; the product's rounding and its correction's 2, of y; the weight's products 2 and
-// the cosines' 1.6, of m.  Elements that do not turn: 9.5 u, or nothing without a norm.
-// About one element in 60,000.  32 x 4096 rows: 493 us where 481 left each such code to fp32.
+// A lane's codes, and the pairs of elements (bit e: e and e + 1) whose codes fp32 leaves open:
+// the ends of what it may be off by have other codes, their signs apart (of zeros).  With u = 2^-24, y the result and m the sum of the
+// magnitudes that it is turned from: the norm's sum 9 u at most (chains of 4, 6 levels of a tree), its
+// factor then 6, of y; the product's rounding and its correction's 2, of y; the weight's products 2 and
+// the cosines' 1.6, of m.  Elements that do not turn: 8 u, or nothing without a norm.
+// About one element in 60,000.  32 x 4096 rows of 16 / 2 heads and their read-back take 487 us, 481 where
+// each such code is left to fp32; 16 x 2048 rows of 8 / 8 heads 171 and 158.
 struct NearBorder {
   float unit, of_y, of_m, of_rest;
-  uint32_t elements = 0;
+  uint32_t elements = 0, words[8];
   __device__ __forceinline__ NearBorder(float unit, float amplitude, bool norm)
-      : unit(unit), of_y((norm ? 9.6f : 2.1f) * 0x1p-24f * unit), of_m((norm ? 3.7f : 1.7f) * 0x1p-24f * unit * amplitude), of_rest(norm ? of_y : 0.0f) {}
-  __device__ __forceinline__ void ends(int e0, float y0, float off0, int e1, float y1, float off1) {
-    const uint32_t apart = e4m3x2(fmaf(y0, unit, off0), fmaf(y1, unit, off1)) ^ e4m3x2(fmaf(y0, unit, -off0), fmaf(y1, unit, -off1));
-    if (apart) elements |= (apart & 0xFF ? 1u << e0 : 0u) | (apart >> 8 ? 1u << e1 : 0u);
+      : unit(unit), of_y((norm ? 8.1f : 2.1f) * 0x1p-24f * unit), of_m((norm ? 3.7f : 1.7f) * 0x1p-24f * unit * amplitude), of_rest(norm ? of_y : 0.0f) {}
+  __device__ __forceinline__ void ends(int e, float y0, float off0, float y1, float off1) {
+    const uint32_t code = e4m3x2(fmaf(y0, unit, off0), fmaf(y1, unit, off1)), other = e4m3x2(fmaf(y0, unit, -off0), fmaf(y1, unit, -off1));
+    if ((code ^ other) & 0x7F7Fu) elements |= 1u << e;
+    words[e / 4] = e % 4 ? words[e / 4] | code << 16 : code;
   }
-  __device__ __forceinline__ void turned(int e0, float y0, float m0, int e1, float y1, float m1) {
-    ends(e0, y0, fmaf(fabsf(y0), of_y, m0 * of_m), e1, y1, fmaf(fabsf(y1), of_y, m1 * of_m));
+  __device__ __forceinline__ void turned(int e, float y0, float m0, float y1, float m1) {
+    ends(e, y0, fmaf(fabsf(y0), of_y, m0 * of_m), y1, fmaf(fabsf(y1), of_y, m1 * of_m));
   }
-  __device__ __forceinline__ void rest(int e, float y0, float y1) { ends(e, y0, fabsf(y0) * of_rest, e + 1, y1, fabsf(y1) * of_rest); }
+  __device__ __forceinline__ void rest(int e, float y0, float y1) { ends(e, y0, fabsf(y0) * of_rest, y1, fabsf(y1) * of_rest); }
 };
 // Cosine and sine of a / 2^64 turns in fp64: the nearest quarter taken off, Taylor's series.
 __device__ __forceinline__ double2 exact_unit_at(unsigned long long a) {
   const unsigned quarter = static_cast<unsigned>((a + (1ull << 61)) >> 62);
   const double t = static_cast<double>(static_cast<long long>(a - (static_cast<unsigned long long>(quarter) << 62))) * (6.283185307179586476925 * 0x1p-64);
   const double t2 = t * t;
-  double s = -1.0 / 1307674368000, c = 1.0 / 20922789888000;
-  s = fma(s, t2, 1.0 / 6227020800);
-  s = fma(s, t2, -1.0 / 39916800);
-  s = fma(s, t2, 1.0 / 362880);
-  s = fma(s, t2, -1.0 / 5040);
-  s = fma(s, t2, 1.0 / 120);
-  s = fma(s, t2, -1.0 / 6);
-  s = fma(s * t2, t, t);
-  c = fma(c, t2, -1.0 / 87178291200);
-  c = fma(c, t2, 1.0 / 479001600);
-  c = fma(c, t2, -1.0 / 3628800);
-  c = fma(c, t2, 1.0 / 40320);
-  c = fma(c, t2, -1.0 / 720);
-  c = fma(c, t2, 1.0 / 24);
-  c = fma(c, t2, -0.5);
-  c = fma(c, t2, 1.0);
+  const double t4 = t2 * t2, t8 = t4 * t4;  // (in a tree: a step takes 60 cycles)
+  double s = fma(fma(t2, -1.0 / 1307674368000, 1.0 / 6227020800), t8,
+                 fma(fma(t2, -1.0 / 39916800, 1.0 / 362880), t4, fma(t2, -1.0 / 5040, 1.0 / 120)));
+  s = fma(fma(s, t2, -1.0 / 6) * t2, t, t);
+  double c = fma(fma(t4, 1.0 / 20922789888000, fma(t2, -1.0 / 87178291200, 1.0 / 479001600)), t8,
+                 fma(fma(t2, -1.0 / 3628800, 1.0 / 40320), t4, fma(t2, -1.0 / 720, 1.0 / 24)));
+  c = fma(c, t4, fma(t2, -0.5, 1.0));
   if (quarter & 1) {
     const double x = c;
     c = -s;
@@ -451,72 +450,78 @@ __device__ __forceinline__ double2 exact_unit_at(unsigned long long a) {
 __device__ __forceinline__ float bf16_at(const uint8_t* row, int d) {
   return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row) + d)) << 16);
 }
-// Such elements again, in fp64, a warp's rows octet and octet + 32 of a page (`first`, `second`: the
-// lane's elements of each; rows: where the page's row 0 would be).  fp64 runs at a sixtieth of
-// fp32's rate, so squares, which fp32 holds, are summed there with what is rounded off; where they
-// leave its range, in fp64.
+// Such elements again, in fp64, and those of lanes that hold what is not finite (NaN: 0), a warp's rows
+// octet and octet + 32 of a page (`first`, `second`: the lane's pairs of each; rows: where the
+// page's row 0 would be).  fp64 runs at a sixtieth of fp32's rate, so squares, which fp32 holds,
+// are summed there with what is rounded off, a row by the whole warp; where they leave its range, in
+// fp64.  Loops are not unrolled: what a warp waits for here is mostly instructions.
 template <bool PAIRS>
 __device__ __noinline__ void exact_codes(const Turn& t, const uint8_t* rows, long long stride, const int* positions, int position, float unit,
                                          uint32_t first, uint32_t second, uint8_t* codes) {
-  const int l = threadIdx.x & 7;
+  const int lane = threadIdx.x & 31, l = lane & 7;
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
-    uint32_t elements = i ? second : first;
-    const uint32_t wanted = __ballot_sync(0xFFFFFFFFu, elements != 0);
-    if (wanted == 0) continue;
-    const bool here = (wanted >> (threadIdx.x & 24) & 0xFF) != 0;  // some lane of the row's eight
+    uint32_t elements = i ? second : first, wanted = __ballot_sync(0xFFFFFFFFu, elements != 0);
+    const bool here = (wanted >> (lane & 24) & 0xFF) != 0;  // some lane of the row's eight
     const int r = (threadIdx.x >> 3) + 32 * i;
     const uint8_t* row = rows + r * stride;
     double norm = 1.0;
-    if (t.k_weight) {
-      Raw<false> raw;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) raw.x[c] = make_uint4(0, 0, 0, 0);
-      if (here) raw.load(row, l);
-      float x[32], s[4] = {}, off[4] = {};
-      raw.get(x);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float q = x[e] * x[e], before = s[e & 3], sum = before + q, back = sum - before;
-        off[e & 3] += (before - (sum - back)) + (q - back);
-        s[e & 3] = sum;
-      }
-      double sum = (static_cast<double>(s[0]) + s[1]) + (static_cast<double>(s[2]) + s[3]) + ((off[0] + off[1]) + (off[2] + off[3]));
-      const bool far = here && !(sum < 1e30 && sum > 1e-20);
-      if (__any_sync(0xFFFFFFFFu, far)) {
-        sum = 0.0;
+    if (t.k_weight)
 #pragma unroll 1
-        for (int e = 0; e < 32; ++e) {
-          const double y = here ? bf16_at(row, (e >> 3) * 64 + l * 8 + (e & 7)) : 0.0f;
-          sum = fma(y, y, sum);
-        }
-      }
+      while (wanted) {
+        const int of = (__ffs(wanted) - 1) & 24;
+        wanted &= ~(0xFFu << of);
+        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(rows + ((threadIdx.x >> 5) * 4 + of / 8 + 32 * i) * stride) + lane);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        float s = 0.0f, off = 0.0f;
 #pragma unroll
-      for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      sum = fma(sum, 1.0 / kHeadDim, t.eps);
-      norm = __frsqrt_rn(static_cast<float>(sum));  // off by 2^-23, and after a step of Newton's 2^-45
-      norm = sum < 1e30 && sum > 1e-30 ? norm * fma(-0.5 * sum * norm, norm, 1.5) : 1.0 / sqrt(sum);
-    }
+        for (int e = 0; e < 8; ++e) {
+          const float x = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16), q = x * x, sum = s + q, back = sum - s;
+          off += (s - (sum - back)) + (q - back);
+          s = sum;
+        }
+        double sum = static_cast<double>(s) + off;
+        if (__any_sync(0xFFFFFFFFu, !(s < 1e30f && (s > 1e-20f || s == 0.0f)))) {
+          sum = 0.0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const double x = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+            sum = fma(x, x, sum);
+          }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        sum = fma(sum, 1.0 / kHeadDim, t.eps);
+        double inv = __frsqrt_rn(static_cast<float>(sum));  // off by 2^-23, and after a step of Newton's 2^-45
+        inv = sum < 1e30 && sum > 1e-30 ? inv * fma(-0.5 * sum * inv, inv, 1.5) : 1.0 / sqrt(sum);
+        if ((lane & 24) == of) norm = inv;
+      }
     const int at = !positions ? position + r : here ? __ldg(positions + r) : 0;
     auto element = [&](int d) {
       const double x = bf16_at(row, d);
       return t.k_weight ? x * norm * static_cast<double>(__ldg(t.k_weight + d)) : x;
     };
+    __syncwarp();  // the codes of other lanes' elements are stored
 #pragma unroll 1
-    for (; elements; elements &= elements - 1) {
-      const int e = __ffs(elements) - 1, d = (e >> 3) * 64 + l * 8 + (e & 7);
-      double y = element(d);
-      if (d < 2 * t.pairs) {
-        const bool upper = PAIRS ? d & 1 : d >= t.pairs;
-        const int j = PAIRS ? d >> 1 : upper ? d - t.pairs : d;
-        const double other = element(PAIRS ? d ^ 1 : upper ? d - t.pairs : d + t.pairs);
-        const double2 u = exact_unit_at(__ldg(t.turns + j) * static_cast<unsigned long long>(static_cast<long long>(at)));
-        y = t.amplitude * fma(y, u.x, upper ? other * u.y : -other * u.y);
+    for (int half = 0; __any_sync(0xFFFFFFFFu, elements != 0); half ^= 1) {
+      // the first pairs of the even lanes, of the odd ones: an element by either of two lanes
+      const uint32_t pairs = __shfl_sync(0xFFFFFFFFu, elements, (lane & ~1) | half);
+      if (pairs) {
+        const int e = __ffs(pairs) - 1, d = (e >> 3) * 64 + ((l & ~1) | half) * 8 + (e & 7) + (lane & 1);
+        double y = element(d);
+        if (d < 2 * t.pairs) {
+          const bool upper = PAIRS ? lane & 1 : d >= t.pairs;
+          const int j = PAIRS ? d >> 1 : upper ? d - t.pairs : d;
+          const double other = element(PAIRS ? d ^ 1 : upper ? d - t.pairs : d + t.pairs);
+          const double2 u = exact_unit_at(__ldg(t.turns + j) * static_cast<unsigned long long>(static_cast<long long>(at)));
+          y = t.amplitude * fma(y, u.x, upper ? other * u.y : -other * u.y);
+        }
+        y = y == y ? y * unit : 0.0;
+        float z = __double2float_rz(y);  // to odd, so that the code's rounding is the only one
+        if (static_cast<double>(z) != y) z = __uint_as_float(__float_as_uint(z) | 1u);
+        codes[r * kHeadDim + d] = static_cast<uint8_t>(e4m3x2(z, 0.0f));
       }
-      y *= unit;
-      float z = __double2float_rz(y);  // to odd, so that the code's rounding is the only one
-      if (static_cast<double>(z) != y) z = __uint_as_float(__float_as_uint(z) | 1u);
-      codes[r * kHeadDim + d] = static_cast<uint8_t>(e4m3x2(z, 0.0f));
+      if ((lane & 1) == half) elements &= elements - 1;
     }
   }
 }
@@ -536,9 +541,9 @@ struct RotaryAppendParams {
 // stay in registers as they came, two to eight lanes; keys are turned twice, for the
 // page's largest element and for the codes, which takes fewer registers than keeping
 // them in fp32.  Codes are those nearest to the exact keys (see NearBorder).
-// Bound by HBM: 32 x 4096 rows of 16 / 2 heads, 64 dims turning, take 427 us, 2.52 GB at 5.9 TB/s
-// (87% of a measured copy), 57% of the issue slots.  With all dims turning and few rows by a
-// page's 8192 cosines in front of its keys: 7 x 513 rows of 8 / 4 heads 29 us, read back with them.
+// Bound by HBM: 32 x 4096 rows of 16 / 2 heads, 64 dims turning, take 421 us, 2.52 GB at 6.0 TB/s
+// (88% of a measured copy).  With all dims turning and few rows by a
+// page's 8192 cosines in front of its keys: 7 x 513 rows of 8 / 4 heads 28 us, read back with them.
 template <int LAYOUT, int K>
 __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
   extern __shared__ __align__(16) float table[];  // of the page's new rows
@@ -679,24 +684,24 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
     if (idle(i)) continue;
     const int r = octet + 32 * i;
     float x[32];
+    uint32_t words[8];
     if (is_v) {
       raw[i].get(x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float* z = x + 4 * j;
+        words[j] = e4m3x2(z[0] * unit, z[1] * unit) | e4m3x2(z[2] * unit, z[3] * unit) << 16;
+      }
     } else {
       NearBorder near(unit, fabsf(static_cast<float>(p.turn.amplitude)), weight != nullptr);
       turned(i, x, near);
-      again[i] = odd || r < begin || r >= end ? 0 : near.elements;
+      again[i] = r < begin || r >= end ? 0 : odd ? 0x55555555u : near.elements;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) words[j] = near.words[j];
     }
     if (r < begin || r >= end) continue;
-    if (odd)
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = x[j] != x[j] ? 0.0f : x[j];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float* z = x + 8 * c;
-      *reinterpret_cast<uint2*>(codes + r * kHeadDim + 64 * c + 8 * l) =
-          make_uint2(e4m3x2(z[0] * unit, z[1] * unit) | e4m3x2(z[2] * unit, z[3] * unit) << 16,
-                     e4m3x2(z[4] * unit, z[5] * unit) | e4m3x2(z[6] * unit, z[7] * unit) << 16);
-    }
+    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint2*>(codes + r * kHeadDim + 64 * c + 8 * l) = make_uint2(words[2 * c], words[2 * c + 1]);
   }
   if (__any_sync(0xFFFFFFFFu, (again[0] | again[1]) != 0))
     exact_codes<LAYOUT == kPairs>(p.turn, p.k.at + sg.entry * p.k.entry + h * p.k.head + row0 * p.k.row, p.k.row,
