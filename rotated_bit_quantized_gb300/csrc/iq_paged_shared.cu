@@ -359,7 +359,9 @@ struct Planner {
     if (forced) return true;
     long long apart = 0;
     for (int i = 0; i < n; ++i) apart += static_cast<long long>(seen(i, i + 1, 0, (e[i].pages + 1) / 2).n) * heads;
-    const double shared = kLaunches + kFetch * (wide + narrow) + std::max(kTile * each, narrow ? few / narrow : 0.0);
+    // (kLaunches has a unit's beginning and end for every CTA; many short units have more)
+    const double longest = std::max({kTile * each, many / wide - kTile * kUnitCost, narrow ? few / narrow : 0.0});
+    const double shared = kLaunches + kFetch * (wide + narrow) + longest;
     return shared < kOrdinary + kFetch / 2 * std::min<long long>(apart, sms) + kOrdinaryTile[kind] * apart / sms;
   }
 };
