@@ -598,8 +598,9 @@ int iq_paged_append_attend(iq_paged* cache, const void* keys, const void* values
 /*
  * iq_paged_attend_shared — iq_paged_attend where slots share pages (forked paths, a common
  * prompt): pages that several of the call's slots hold are read and multiplied once for all
- * of them.  The same arguments, results (other sums' orders: within the same bounds) and errors,
- * and its own size of workspace.  What is shared is taken from table_host, up to four levels of
+ * of them.  The same arguments and errors, its own size of workspace; results within the same
+ * bounds (sums in other orders, and small elements of a query beside a large one held to 2^-19
+ * of that one, not 2^-23, where rows of several slots are multiplied together).  What is shared is taken from table_host, up to four levels of
  * sharing; a call with nothing to gain (more than 128 query rows per kv head and slot, or little
  * in common) runs as iq_paged_attend.  A captured call replays with the sharing that it was captured with: the
  * slots that shared pages then still have to.

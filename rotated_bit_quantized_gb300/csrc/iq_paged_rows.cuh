@@ -22,7 +22,13 @@
 // In norm, on random rows with outliers, the weights leave 0.0006 to 0.0007 of the
 // result (bfloat16 weights 0.0016); with references that move at 2^6, so that the
 // heaviest key is exact more often, 0.0005, but 5 to 8% slower where units are
-// short; with sums of the weights as they are held, 0.0004, but 4% slower.
+// short; with sums of the weights as they are held, 0.0004, but 4% slower.  In a tree
+// the sums are those: its rows would run in the split kernel, whose sums are, if their pages
+// were not shared.  32 paths of 32768 common tokens: 0.00037 off in norm, apart 0.00037, for
+// 2% of the time (5% where the held weights were converted before they were added).  A
+// query's second part has the first one's scale here and 16 times it there: elements 2^10
+// (there 2^14) below the row's largest are held to 2^-19 of that one (2^-23), far below the
+// weights' own roundings.
 #pragma once
 
 #include "iq_paged_mma.cuh"
@@ -371,16 +377,24 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
                 const int c = 32 * x + 4 * i;
                 const float w0 = ex2_approx(fmaf(s[c], f, shift)), w1 = ex2_approx(fmaf(s[c + 1], f, shift));
                 const float w2 = ex2_approx(fmaf(s[c + 2], f, shift)), w3 = ex2_approx(fmaf(s[c + 3], f, shift));
-                s0 += w0;
-                s1 += w1;
-                s0 += w2;
-                s1 += w3;
+                if constexpr (!P::kTree) {
+                  s0 += w0;
+                  s1 += w1;
+                  s0 += w2;
+                  s1 += w3;
+                }
                 ha = f16x2(w0, w1);
                 hb = f16x2(w2, w3);
               }
               const uint32_t a = e4m3x2_of_f16x2(ha), d = e4m3x2_of_f16x2(hb);
+              const uint32_t a16 = e4m3x2_to_f16x2(a), d16 = e4m3x2_to_f16x2(d);
+              const uint32_t a_lo = e4m3x2_of_f16x2(sub_f16x2(ha, a16)), d_lo = e4m3x2_of_f16x2(sub_f16x2(hb, d16));
               hi[i] = a | d << 16;
-              lo[i] = e4m3x2_of_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a))) | e4m3x2_of_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d))) << 16;
+              lo[i] = a_lo | d_lo << 16;
+              if constexpr (P::kTree) {  // as they are held: multiples of the last place of their fp16 form, so exact there
+                add_to(s0, s1, add_f16x2(a16, e4m3x2_to_f16x2(a_lo)));
+                add_to(s0, s1, add_f16x2(d16, e4m3x2_to_f16x2(d_lo)));
+              }
             }
             if (!rehearsal) {
               tmem_st<8>(t_s + 8 * x, reinterpret_cast<const float*>(hi));

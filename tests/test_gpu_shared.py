@@ -308,3 +308,21 @@ def test_a_decode_step_of_all_of_it():
         for i, p in enumerate(a.page_ids(1)[: 700 // 64]):
             assert (b.page_ids(1)[i] == p)
     assert a.device_status() == 0 and b.device_status() == 0
+
+
+@pytest.mark.parametrize("paths,common,tail,Hq,n", [(6, 640, 90, 4, 1), (12, 1000, 300, 16, 2), (3, 513, 200, 32, 2), (40, 300, 20, 8, 5)])
+def test_values_that_are_all_alike_come_back(paths, common, tail, Hq, n):
+    """Weights are divided by the sum of the weights as they are held, so their own rounding cancels; what is left are the
+    roundings of float32 sums of positive numbers, 2^-23 of the sum each: 16 a tile in the products (8 of them, cut inside and
+    added), 34 and one a tile in the sums of weights, under 12 tiles: 240, and 16 for the joins and the division."""
+    H = 2
+    c, o = pair(paths, H, (common + 63) // 64 + paths * (2 + tail // 64), common + tail + 1)
+    alike = torch.tensor([1.0, -1.5, 0.75, 2.0, -0.25, 0.875, -1.125, 1.75]).repeat(32).to(torch.bfloat16)
+    put(c, o, rows(1, 1, H, common), alike.expand(1, H, common, 256), [0])
+    for x in (c, o):
+        x.fork([0] * (paths - 1), list(range(1, paths)))
+    put(c, o, rows(2, paths, H, tail), alike.expand(paths, H, tail, 256))
+    q = 3 * rows(9, paths, Hq, n).cuda()
+    for out in (c.attend(q, out_dtype=torch.float32), shared(c, q, out_dtype=torch.float32)):
+        assert (f64(out) / f64(alike) - 1).__abs__().max() <= 256 * 2.0**-23
+    assert c.device_status() == 0
