@@ -413,11 +413,15 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(c
 // the cosines' 1.6, of m.  Elements that do not turn: 8 u, or nothing without a norm.
 // About one element in 60,000.  32 x 4096 rows of 16 / 2 heads and their read-back take 487 us, 481 where
 // each such code is left to fp32; 16 x 2048 rows of 8 / 8 heads 171 and 158.
-struct NearBorder {
-  float unit, of_y, of_m, of_rest;
+struct Bound {
+  float of_y, of_m, of_rest;  // of elements times unit
+  __device__ __forceinline__ Bound(float unit, float amplitude, bool norm)
+      : of_y((norm ? 8.1f : 2.1f) * 0x1p-24f * unit), of_m((norm ? 3.7f : 1.7f) * 0x1p-24f * unit * amplitude), of_rest(norm ? of_y : 0.0f) {}
+};
+struct NearBorder : Bound {
+  float unit;
   uint32_t elements = 0, words[8];
-  __device__ __forceinline__ NearBorder(float unit, float amplitude, bool norm)
-      : unit(unit), of_y((norm ? 8.1f : 2.1f) * 0x1p-24f * unit), of_m((norm ? 3.7f : 1.7f) * 0x1p-24f * unit * amplitude), of_rest(norm ? of_y : 0.0f) {}
+  __device__ __forceinline__ NearBorder(float unit, float amplitude, bool norm) : Bound(unit, amplitude, norm), unit(unit) {}
   __device__ __forceinline__ void ends(int e, float y0, float off0, float y1, float off1) {
     const uint32_t code = e4m3x2(fmaf(y0, unit, off0), fmaf(y1, unit, off1)), other = e4m3x2(fmaf(y0, unit, -off0), fmaf(y1, unit, -off1));
     if ((code ^ other) & 0x7F7Fu) elements |= 1u << e;
@@ -427,6 +431,26 @@ struct NearBorder {
     ends(e, y0, fmaf(fabsf(y0), of_y, m0 * of_m), y1, fmaf(fabsf(y1), of_y, m1 * of_m));
   }
   __device__ __forceinline__ void rest(int e, float y0, float y1) { ends(e, y0, fabsf(y0) * of_rest, y1, fabsf(y1) * of_rest); }
+};
+// Whether a lane's elements are above a limit, and those (bit e: e and e + 1) that fp32 leaves open.
+struct AboveLimit : Bound {
+  float limit;
+  uint32_t elements = 0;
+  bool above = false;
+  __device__ __forceinline__ AboveLimit(float limit, float amplitude, bool norm) : Bound(1.0f, amplitude, norm), limit(limit) {}
+  __device__ __forceinline__ void look(int e, float y, float off) {
+    const float d = fabsf(y) - limit;  // (exact where it is small)
+    if (d > off) above = true;
+    else if (d > -off) elements |= 1u << e;
+  }
+  __device__ __forceinline__ void turned(int e, float y0, float m0, float y1, float m1) {
+    look(e, y0, fmaf(fabsf(y0), of_y, m0 * of_m));
+    look(e, y1, fmaf(fabsf(y1), of_y, m1 * of_m));
+  }
+  __device__ __forceinline__ void rest(int e, float y0, float y1) {
+    look(e, y0, fabsf(y0) * of_rest);
+    look(e, y1, fabsf(y1) * of_rest);
+  }
 };
 // Cosine and sine of a / 2^64 turns in fp64: the nearest quarter taken off, Taylor's series.
 __device__ __forceinline__ double2 exact_unit_at(unsigned long long a) {
@@ -455,10 +479,12 @@ __device__ __forceinline__ float bf16_at(const uint8_t* row, int d) {
 // page's row 0 would be).  fp64 runs at a sixtieth of fp32's rate, so squares, which fp32 holds,
 // are summed there with what is rounded off, a row by the whole warp; where they leave its range, in
 // fp64.  Loops are not unrolled: what a warp waits for here is mostly instructions.
+// Without codes to store: whether some element of the lane's is above 448 / unit.
 template <bool PAIRS>
-__device__ __noinline__ void exact_codes(const Turn& t, const uint8_t* rows, long long stride, const int* positions, int position, float unit,
+__device__ __noinline__ bool exact_codes(const Turn& t, const uint8_t* rows, long long stride, const int* positions, int position, float unit,
                                          uint32_t first, uint32_t second, uint8_t* codes) {
   const int lane = threadIdx.x & 31, l = lane & 7;
+  bool above = false;
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     uint32_t elements = i ? second : first, wanted = __ballot_sync(0xFFFFFFFFu, elements != 0);
@@ -517,13 +543,15 @@ __device__ __noinline__ void exact_codes(const Turn& t, const uint8_t* rows, lon
           y = t.amplitude * fma(y, u.x, upper ? other * u.y : -other * u.y);
         }
         y = y == y ? y * unit : 0.0;
+        above |= fabs(y) > 448.0;
         float z = __double2float_rz(y);  // to odd, so that the code's rounding is the only one
         if (static_cast<double>(z) != y) z = __uint_as_float(__float_as_uint(z) | 1u);
-        codes[r * kHeadDim + d] = static_cast<uint8_t>(e4m3x2(z, 0.0f));
+        if (codes) codes[r * kHeadDim + d] = static_cast<uint8_t>(e4m3x2(z, 0.0f));
       }
       if ((lane & 1) == half) elements &= elements - 1;
     }
   }
+  return above;
 }
 
 struct RotaryAppendParams {
@@ -535,6 +563,38 @@ struct RotaryAppendParams {
   int keys_first;  // in the order of CTAs: those of all segments' keys before others
   int q_heads, group, groups, part_rows;  // queries: of `groups` groups of heads, so many rows of a page
 };
+
+// Whether one of the lane's new elements of a page's rows [begin, end) is above 448 * 2^e.  The page's
+// exponent hangs on it where the largest element, in fp32, is as near to that as it may be off
+// (three pages in a million; where elements that are exact are the largest, one in 200, which need no fp64).
+template <int LAYOUT, int K>
+__device__ __noinline__ bool key_above(const Turn& t, const uint8_t* rows, long long stride, const int* positions, int position, int begin,
+                                       int end, const float* weights, const float* table, int e) {
+  const int octet = threadIdx.x >> 3, l = threadIdx.x & 7, octet0 = octet & ~3;
+  uint32_t open[2] = {};
+  bool above = false;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (octet0 + 32 * i + 4 <= begin || octet0 + 32 * i >= end) continue;  // no new row in this warp
+    const int r = octet + 32 * i;
+    const bool is_new = r >= begin && r < end;
+    Raw<false> raw;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) raw.x[c] = make_uint4(0, 0, 0, 0);
+    if (is_new) raw.load(rows + r * stride, l);
+    float x[32];
+    raw.get(x);
+    if (t.k_weight) weigh<false>(x, inverse_norm(x, static_cast<float>(t.eps)), weights, l);
+    AboveLimit look(448.0f * power2(e), fabsf(static_cast<float>(t.amplitude)), t.k_weight != nullptr);
+    turn_row<LAYOUT, K, false, true>(x, table + 2 * (min(max(r, begin), end - 1) - begin) * t.pairs, t.pairs, l, look);
+    if (!is_new) continue;
+    (i ? open[1] : open[0]) = look.elements;
+    above |= look.above;
+  }
+  if (__any_sync(0xFFFFFFFFu, (open[0] | open[1]) != 0))
+    above |= exact_codes<LAYOUT == kPairs>(t, rows, stride, positions, position, power2(-e), open[0], open[1], nullptr);
+  return above;
+}
 
 // CTA (page of a segment, y, segment; y last where keys come first): the keys of kv head y, the values of
 // kv head y - heads, or the queries of a group of heads at the page's new rows.  A page's rows
@@ -569,8 +629,11 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
     __syncthreads();
   };
   Raw<false> raw[2];
+  auto clear = [&]() {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) raw[0].x[c] = raw[1].x[c] = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < 4; ++c) raw[0].x[c] = raw[1].x[c] = make_uint4(0, 0, 0, 0);
+  };
+  clear();
 
   if (y >= 2 * heads) {
     // ---------------------------------------------------------------- queries
@@ -607,7 +670,7 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
   uint8_t* codes = (is_v ? p.a.v_codes : p.a.k_codes) + at * kPageBytes;
   float* scales = is_v ? p.a.v_scales : p.a.k_scales;
   const float* weight = p.turn.k_weight;
-  {
+  auto load_rows = [&]() {
     const Rows& in = is_v ? p.v : p.k;
     const uint8_t* rows = in.at + sg.entry * in.entry + h * in.head;
 #pragma unroll
@@ -615,7 +678,8 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
       const int r = octet + 32 * i;
       if (r >= begin && r < end) raw[i].load(rows + (row0 + r) * in.row, l);
     }
-  }
+  };
+  load_rows();
   const int octet0 = octet & ~3;
   auto idle = [&](int i) { return octet0 + 32 * i + 4 <= begin || octet0 + 32 * i >= end; };  // no new row in this warp
   float inv[2] = {};
@@ -672,7 +736,21 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, tops[i]);
+  const uint8_t* key_rows = p.k.at + sg.entry * p.k.entry + h * p.k.head + row0 * p.k.row;
+  const int* key_positions = p.positions ? p.positions + static_cast<long long>(sg.entry) * p.a.n + row0 : nullptr;
+  const int key_position = sg.pos - off + k * kPage;
   int e = least_exponent(top);
+  if (!is_v) {
+    // The largest key is off by 2^-24 * (8.1 + 2 * 3.7) of it at most: of the pair that it is turned from, the magnitudes' sum
+    // times the amplitude is at most twice the larger of the pair's results.
+    const float most = __uint_as_float(top);
+    const int least = least_exponent(__float_as_uint(most * (1.0f - 0x1p-20f)));
+    if (least != least_exponent(__float_as_uint(most * (1.0f + 0x1p-20f)))) {
+      e = least + __syncthreads_or(key_above<LAYOUT, K>(p.turn, key_rows, p.k.row, key_positions, key_position, begin, end, weights, table, least));
+      clear();  // (the rows again, rather than in registers over the call)
+      load_rows();
+    }
+  }
   const bool beyond = e > kEMax;
   e = min(e, kEMax);
   const int old = begin > 0 ? exponent_of(scales[at_from]) : e;
@@ -704,9 +782,7 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
     for (int c = 0; c < 4; ++c) *reinterpret_cast<uint2*>(codes + r * kHeadDim + 64 * c + 8 * l) = make_uint2(words[2 * c], words[2 * c + 1]);
   }
   if (__any_sync(0xFFFFFFFFu, (again[0] | again[1]) != 0))
-    exact_codes<LAYOUT == kPairs>(p.turn, p.k.at + sg.entry * p.k.entry + h * p.k.head + row0 * p.k.row, p.k.row,
-                                  p.positions ? p.positions + static_cast<long long>(sg.entry) * p.a.n + row0 : nullptr, sg.pos - off + k * kPage, unit,
-                                  again[0], again[1], codes);
+    exact_codes<LAYOUT == kPairs>(p.turn, key_rows, p.k.row, key_positions, key_position, unit, again[0], again[1], codes);
   upkeep((is_v ? p.a.v_codes : p.a.k_codes) + at_from * kPageBytes, codes, begin, end, from != page, old, e);
   if (odd || beyond) atomicOr(p.a.status, IQ_STATUS_RANGE);
   __syncthreads();  // the old scale has been read by every thread

@@ -444,3 +444,63 @@ def test_float32_cache_takes_turned_rows():
     # 8 bits of groups whose elements span some 8: half a step of 8 / 255 in a value; a score of 256 such products
     # of keys off by as much at random moves by 0.02 * |q| / 16, some 0.03 of the weights
     assert np.abs(out[:, :, 0] - want).max() < 0.1
+
+
+def keys_at_a_border(want):
+    """Pairs (a, b) of bf16 numbers, positions and a frequency whose first turned element is 448 but for 2^-26 of it, from 64 bits."""
+    w, got = 0.7310585786300049, []
+    p = np.arange(1, 40000, dtype=np.float64)[:, None]
+    a = 256 + 2.0 * np.arange(128)
+    c, s = np.cos(p * w), np.sin(p * w)
+    b = torch.from_numpy((a * c - 448) / s).to(torch.bfloat16).double().numpy()
+    y, z = a * c - b * s, a * s + b * c
+    off = np.abs(y / 448 - 1)
+    at = np.argwhere((off < 2.0**-26) & (off > 2.0**-40) & (np.abs(z) < 440))  # (angles in 64 bits are off by 2^-38 of this at most)
+    for i, j in at[:want]:
+        got.append((a[j], b[i, j], int(p[i, 0]), y[i, j]))
+    return w, got
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_page_exponents_are_those_of_the_exact_keys(interleaved):
+    """The least e with the page's largest exact key at most 448 * 2^e: where float32 cannot tell, it is not asked."""
+    from rotated_bit_quantized_gb300 import IQPagedCache, IQRotary
+    w, found = keys_at_a_border(256)
+    n = len(found)
+    assert n >= 64 and {y > 448 for *_, y in found} == {True, False}
+    for rd in (16, 64, 96, 256):
+        rot = IQRotary(rd, interleaved=interleaved, frequencies=[w] * (rd // 2))
+        c = IQPagedCache(n, 1, n)
+        k = torch.zeros(n, 1, 3, 256)
+        at = torch.zeros(n, 3, dtype=torch.int32)
+        first, second = (4, 5) if interleaved else (2, 2 + rd // 2)
+        for i, (a, b, p, _) in enumerate(found):
+            r = i % 3
+            k[i, 0, r, first], k[i, 0, r, second], at[i, r] = a, b, p
+            k[i, 0, (r + 1) % 3, 200] = 7.0
+        k = k.to(torch.bfloat16).cuda()
+        c.append_rotary(None, k, torch.zeros_like(k), rot, positions=at.cuda())
+        want = [2.0 if y > 448 else 1.0 for *_, y in found]
+        assert c.k_scales[:, 0].tolist() == want
+        assert c.device_status() == 0
+
+
+def test_page_exponents_of_normed_keys():
+    from rotated_bit_quantized_gb300 import IQPagedCache, IQRotary
+    g = np.random.default_rng(1)
+    seen = set()
+    for i in range(40):
+        x = torch.from_numpy(g.standard_normal(256)).to(torch.bfloat16)
+        x[i] = 9.0
+        unit = 9.0 / np.sqrt((x.double().numpy() ** 2).mean() + 1e-6)
+        weight = np.float32(448.0 / unit)
+        y = float(weight) * unit
+        if abs(y / 448 - 1) < 2.0**-45:
+            continue
+        rot = IQRotary(64 if i % 2 else 0, k_norm=torch.full((256,), float(weight)))
+        c = IQPagedCache(1, 1, 1)
+        k = x.view(1, 1, 1, 256).cuda()
+        c.append_rotary(None, k, k, rot)
+        assert c.k_scales.item() == (2.0 if y > 448 else 1.0), i
+        seen.add(y > 448)
+    assert seen == {True, False}
