@@ -9,7 +9,8 @@
 // tell (at 2^20, 2^-4 of a radian is lost), so a frequency is held as its turns per
 // position modulo 1 in 64 bits of fixed point: the product with a position, modulo
 // 2^64, is the angle modulo a turn, off by at most position * 2^-64 and what the
-// frequency itself was off.  One integer product; no table in memory, no fp64.
+// frequency itself was off.  One integer product and no table in memory; fp64 only for
+// what fp32 leaves open of codes (see exact_codes).
 //
 // Rows.  Eight lanes hold a row, 32 elements each in pieces of 16 bytes, 128 bytes apart:
 // what a row costs besides its elements (its address, the norm's sum over lanes and root)
@@ -86,16 +87,19 @@ enum Layout {
   kShift   // halves, any other: K pieces on, or one more, of the lane `shift` on
 };
 
-// Cosine and sine, times the amplitude, of an angle of a / 2^32 turns.  The nearest
-// quarter is taken off, and of what is left, t = h + l with |t| <= pi / 4 and l below half
-// a step of h, Taylor's series: what follows their first terms is below 2^-3 of them,
-// so the results are a half and some hundredths of a step off at most (codes are rounded
-// from what they turn: the nearer, the fewer land on the wrong side of a border).
-__device__ __forceinline__ float2 unit_at(unsigned a, float amplitude) {
-  const unsigned quarter = (a + 0x20000000u) >> 30;
+// Cosine and sine, times the amplitude, of an angle of a / 2^64 turns.  The nearest
+// quarter is taken off, and of what is left, t = h + l with |t| <= pi / 4 and l of half a step
+// of h or 2^-32 of a turn, Taylor's series: what follows their first terms is below 2^-3 of
+// them, so the results are a half and some hundredths of a step off at most (codes are rounded
+// from what they turn: the nearer, the fewer land on the wrong side of a border).  Of the
+// angle's lower half 23 bits count, so that it is held to 2^-55 of a turn (without them the sine of
+// 10^-4 radians was off by 10^-5 of it).
+__device__ __forceinline__ float2 unit_at(unsigned long long angle, float amplitude) {
+  const unsigned a = static_cast<unsigned>(angle >> 32), quarter = (a + 0x20000000u) >> 30;
   const int rest = static_cast<int>(a - (quarter << 30));
   constexpr float kHi = 0x1.921fb6p-30f, kLo = -0x1.777a5cp-55f;  // 2 pi / 2^32
-  const float u = static_cast<float>(rest), v = static_cast<float>(rest - static_cast<int>(u));
+  const float lower = __uint_as_float(0x3F800000u | static_cast<unsigned>(angle) >> 9) - 1.0f;
+  const float u = static_cast<float>(rest), v = static_cast<float>(rest - static_cast<int>(u)) + lower;
   const float h = u * kHi, l = fmaf(u, kHi, -h) + fmaf(u, kLo, v * kHi);
   const float h2 = h * h, rounded = fmaf(h, h, -h2);  // h^2 = h2 + rounded
   float p = fmaf(h2, 1.0f / 362880, -1.0f / 5040);
@@ -133,7 +137,7 @@ __device__ __forceinline__ void fill_table(const Turn& t, float* table, int rows
   const int down = blockDim.x / t.pairs, across = blockDim.x - down * t.pairs;
   while (r < rows) {
     const long long p = position(r);
-    const float2 u = unit_at(static_cast<unsigned>((static_cast<unsigned long long>(p) * __ldg(t.turns + j)) >> 32), amplitude);
+    const float2 u = unit_at(static_cast<unsigned long long>(p) * __ldg(t.turns + j), amplitude);
     const int to = 2 * r * t.pairs + table_place<V>(j, t.pairs);
     table[to] = u.x;
     table[to + t.pairs] = u.y;

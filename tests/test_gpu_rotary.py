@@ -504,3 +504,25 @@ def test_page_exponents_of_normed_keys():
         assert c.k_scales.item() == (2.0 if y > 448 else 1.0), i
         seen.add(y > 448)
     assert seen == {True, False}
+
+
+@pytest.mark.parametrize("base", [1e4, 1e7])
+def test_float32_sines_of_small_angles(base):
+    """Each product of a result is off by a few roundings of its own, also where the angle is a small part of a turn: a
+    cosine or sine by 2, its product by 1, their sum by 2 and its correction: 6 U, and 2 for the angle's own
+    reduction (held to 2^-24 of it and to 2^-54 of a turn); the frequency's 2^-52 times the position besides."""
+    from rotated_bit_quantized_gb300 import IQRotary
+    rot = IQRotary(256, base=base)
+    x = torch.zeros(4, 1, 300, 256)
+    g = torch.Generator().manual_seed(1)
+    x[0, :, :, 128:] = torch.randn(1, 300, 128, generator=g)
+    x[1, :, :, :128] = torch.randn(1, 300, 128, generator=g)
+    x[2, :, :, 128:], x[2, :, :, :128] = torch.randn(1, 300, 128, generator=g), 1e-6 * torch.randn(1, 300, 128, generator=g)
+    x[3] = x[0]
+    at = np.stack([np.arange(300), np.arange(300), np.arange(300), 100000 - np.arange(300)])
+    out = f64(rot.apply(x.cuda(), positions=torch.from_numpy(at).int().cuda()))
+    a, b = f64(x)[..., :128], f64(x)[..., 128:]
+    angle = (at[..., None] * rot.frequencies)[:, None]
+    c, s, slip = np.cos(angle), np.sin(angle), 2.0**-51 * angle + 2.0**-52
+    for got, want, tol in ((out[..., :128], a * c - b * s, np.abs(a * c) + np.abs(b * s)), (out[..., 128:], a * s + b * c, np.abs(a * s) + np.abs(b * c))):
+        assert (np.abs(got - want) <= 8 * U * tol + slip * (np.abs(a) + np.abs(b))).all()
