@@ -298,7 +298,7 @@ __device__ __forceinline__ float inverse_norm(const float (&x)[32], float eps) {
   float inv = __frsqrt_rn(fmaf(sum, 1.0f / kHeadDim, eps));
   if (__any_sync(0xFFFFFFFFu, sum == __int_as_float(0x7F800000))) {  // above 2^63 or so the squares pass fp32's range, not their root
     const float small = square_sum(x, 0x1p-80f);
-    if (sum == __int_as_float(0x7F800000)) inv = __frsqrt_rn(small * (1.0f / kHeadDim)) * 0x1p-80f;
+    if (sum == __int_as_float(0x7F800000)) inv = __frsqrt_rn(fmaf(small, 1.0f / kHeadDim, eps * 0x1p-80f * 0x1p-80f)) * 0x1p-80f;
   }
   return inv;
 }

@@ -526,3 +526,16 @@ def test_float32_sines_of_small_angles(base):
     c, s, slip = np.cos(angle), np.sin(angle), 2.0**-51 * angle + 2.0**-52
     for got, want, tol in ((out[..., :128], a * c - b * s, np.abs(a * c) + np.abs(b * s)), (out[..., 128:], a * s + b * c, np.abs(a * s) + np.abs(b * c))):
         assert (np.abs(got - want) <= 8 * U * tol + slip * (np.abs(a) + np.abs(b))).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_large_eps_beside_squares_past_32_bits(dtype):
+    """Sums of squares that pass float32 still have eps added to their mean."""
+    from rotated_bit_quantized_gb300 import IQRotary
+    x = torch.full((1, 1, 3, 256), 2.0**60, dtype=dtype)
+    x[0, 0, 1] = 2.0**62
+    x[0, 0, 2] = 2.0**100
+    for eps in (1e-6, 1e30, 1e37, 3e38):
+        rot = IQRotary(0, q_norm=torch.ones(256), k_norm=torch.ones(256), eps=eps)
+        y = f64(x) / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True) + eps)
+        check(rot.apply(x.cuda()), y, 10 * U * np.abs(y))
