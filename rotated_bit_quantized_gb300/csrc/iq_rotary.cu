@@ -887,6 +887,7 @@ int check_rows(const iq_rows* r, int entries, int heads, int n, int size, const 
     if (strides[i] < 0 || strides[i] > (1LL << 40)) return fail(IQ_ERR_INVALID_ARG, std::string(name) + ": stride outside [0, 2^40]");
     in_bytes[i] = strides[i] * size;
     bad |= in_bytes[i] % 16 != 0;
+    if (in_bytes[i] > (1LL << 56) / (counts[i] - 1)) return fail(IQ_ERR_INVALID_ARG, std::string(name) + ": rows past any address");
     last += in_bytes[i] * (counts[i] - 1);
   }
   if (bad) return fail(IQ_ERR_INVALID_ARG, std::string(name) + ": rows not 16-byte aligned");

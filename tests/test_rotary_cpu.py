@@ -131,3 +131,17 @@ def test_binding_refusals():
                dict(amplitude=float("inf")), dict(q_norm=torch.ones(256), eps=0.0), dict(k_norm=torch.ones(255)), dict(q_norm=torch.ones(256, dtype=torch.int32))):
         with pytest.raises(ValueError):
             IQRotary(**kw)
+
+
+def test_rows_whose_span_passes_64_bits(L):  # noqa: F811
+    """Strides within their limit whose product with the rows is not an address: refused, not wrapped round."""
+    wide = (1 << 23) + 1  # 2^40 elements of 2 bytes, times 2^23: 2^64
+    for kw in (dict(q=rows(row=1 << 40)), dict(k=rows(row=1 << 40))):
+        assert apply(L, n=wide, **kw) == INVALID, kw
+    assert apply(L, dtype=1, n=(1 << 22) + 1, q=rows(row=1 << 40)) == INVALID
+    assert apply(L, n=(1 << 22) + 1, entries=3, q=rows(entry=1 << 40, row=1 << 40)) == INVALID
+    f = Fake(L, pages=1 << 20, max_pages=1 << 18)
+    before = f.state()
+    for kw in (dict(q=rows(row=1 << 40)), dict(k=rows(row=1 << 40)), dict(v=rows(row=1 << 40))):
+        assert append(L, f, n=wide, entries=1, **kw) == INVALID, kw
+    assert f.state() == before
