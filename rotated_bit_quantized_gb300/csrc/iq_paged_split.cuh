@@ -422,9 +422,13 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
         if (lane == 0) red[(warp & 3) * NR + r0 + r] = x;
       }
-      await(&o_done[(it0 - 1) & 1], (it0 - 1) / 2);  // (the last; products end in order)
+      // The last tile's product (products end in order).  With turns the other warps' barrier comes first: a
+      // warp that had no part in that tile cannot tell the end of its phase from that of the one
+      // before, two tiles earlier, which the warps that had waited for.
+      if constexpr (kTurns == 2) named_bar(3, C::kWarps * 32);
+      await(&o_done[(it0 - 1) & 1], (it0 - 1) / 2);
       tc_after();
-      named_bar(3, C::kWarps * 32);
+      if constexpr (kTurns == 1) named_bar(3, C::kWarps * 32);
       if constexpr (kTurns == 2) {
         // half of the dims each: both turns' results, under the larger of their references
         const bool had0 = n > 1 || (it0 & 1), had1 = n > 1 || !(it0 & 1);

@@ -326,3 +326,22 @@ def test_values_that_are_all_alike_come_back(paths, common, tail, Hq, n):
     for out in (c.attend(q, out_dtype=torch.float32), shared(c, q, out_dtype=torch.float32)):
         assert (f64(out) / f64(alike) - 1).__abs__().max() <= 256 * 2.0**-23
     assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("Hq", [2, 8])  # of 4 and 16 rows a head
+def test_turns_that_end_apart(Hq):
+    """Two warpgroups take a leaf's tiles in turn and join their results: leaves of one to ten tiles, of which one
+    warpgroup's keys hold references that move in every tile; the same from call to call."""
+    H, n, paths = 1, 2, 60
+    c, o = pair(paths, H, 2 + paths * 22, 256 + 1400)
+    put(c, o, rows(1, 1, H, 256), rows(2, 1, H, 256), [0])
+    for x in (c, o):
+        x.fork([0] * (paths - 1), list(range(1, paths)))
+    k = rows(3, paths, H, 1290)
+    for t in range(1290):  # growing, in every other tile
+        k[:, :, t] *= 1 + 10 * (t // 128) if (t // 128) % 2 else 1
+    put(c, o, k, rows(4, paths, H, 1290), None, [n + (149 * b) % 1280 for b in range(paths)])
+    q = rows(9, paths, Hq, n)
+    first = check(c, o, q)
+    for _ in range(30):
+        assert torch.equal(shared(c, q.cuda(), out_dtype=torch.float32), first)
