@@ -101,6 +101,8 @@ class IQRotary:
         for w in (q_norm, k_norm):
             if w is not None and (w.shape != (256,) or not w.is_floating_point()):
                 raise ValueError("q_norm and k_norm must be 256 floating-point weights")
+        if device is not None and not isinstance(device, int) and torch.device(device).type != "cuda":
+            raise ValueError("device must be a CUDA device")
         self.device = _device_of(device)
         self._index, self._lib = self.device.index, lib()
         self.q_norm, self.k_norm = (None if w is None else (norm_offset + w.detach().to(self.device, torch.float32)).contiguous() for w in (q_norm, k_norm))

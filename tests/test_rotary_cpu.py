@@ -145,3 +145,13 @@ def test_rows_whose_span_passes_64_bits(L):  # noqa: F811
     for kw in (dict(q=rows(row=1 << 40)), dict(k=rows(row=1 << 40)), dict(v=rows(row=1 << 40))):
         assert append(L, f, n=wide, entries=1, **kw) == INVALID, kw
     assert f.state() == before
+
+
+def test_a_plan_is_for_a_cuda_device():
+    """A name of another kind of device is refused, not taken for the current CUDA device."""
+    import torch
+
+    from rotated_bit_quantized_gb300 import IQRotary
+    for device in ("cpu", torch.device("cpu"), "meta"):
+        with pytest.raises(ValueError):
+            IQRotary(rotary_dim=0, device=device)
