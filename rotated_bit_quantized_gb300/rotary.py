@@ -111,8 +111,9 @@ class IQRotary:
             self.turns = torch.empty(rotary_dim // 2, dtype=torch.int64, device=self.device)
             with _OnDevice(self._index):
                 check(self._lib.iq_rotary_turns(f.ctypes.data, rotary_dim // 2, self.turns.data_ptr(), _stream(self._index)), "iq_rotary_turns")
-        if not _capturing():  # (a captured plan is made when the graph is replayed)
-            torch.cuda.current_stream(self.device).synchronize()
+        with _OnDevice(self._index):
+            if not _capturing():  # (a captured plan is made when the graph is replayed)
+                torch.cuda.current_stream(self.device).synchronize()
         at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self._desc = IQRotaryDesc(rotary_dim, 1 if interleaved else 0, self.amplitude, eps, at(self.turns), at(self.q_norm), at(self.k_norm))
         self._d = ctypes.byref(self._desc)

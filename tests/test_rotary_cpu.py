@@ -155,3 +155,31 @@ def test_a_plan_is_for_a_cuda_device():
     for device in ("cpu", torch.device("cpu"), "meta"):
         with pytest.raises(ValueError):
             IQRotary(rotary_dim=0, device=device)
+
+
+@pytest.mark.parametrize("captured", [0, 1])
+def test_a_plan_waits_where_its_own_device_captures_nothing(captured, monkeypatch):
+    """Whether the plan's device is capturing is asked of that device, whichever is current."""
+    import torch
+
+    from rotated_bit_quantized_gb300 import rotary as r
+    current, waited = [0], []
+
+    class On:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.prev, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.prev
+
+    class Stream:
+        def synchronize(self):
+            waited.append(True)
+    monkeypatch.setattr(r, "_OnDevice", On)
+    monkeypatch.setattr(r, "_capturing", lambda: current[0] == captured)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    r.IQRotary(rotary_dim=0, device="cuda:1")
+    assert bool(waited) == (captured != 1) and current == [0]
