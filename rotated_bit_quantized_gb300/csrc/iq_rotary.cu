@@ -33,6 +33,7 @@ struct Turn {
   const float* q_weight;
   const float* k_weight;
   double amplitude, eps;
+  float unit_off;  // what cosines and sines may be off by, in 2^-24 of the amplitude
   int pairs;
 };
 struct Rows {
@@ -414,18 +415,21 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(c
 // the ends of what it may be off by have other codes, their signs apart (of zeros).  With u = 2^-24, y the result and m the sum of the
 // magnitudes that it is turned from: the norm's sum 9 u at most (chains of 4, 6 levels of a tree), its
 // factor then 6, of y; the product's rounding and its correction's 2, of y; the weight's products 2 and
-// the cosines' 1.6, of m.  Elements that do not turn: 8 u, or nothing without a norm.
+// the cosines' 1.7, of m, or 2.7 where the amplitude is rounded to fp32 too.  Elements that do not
+// turn: 8 u, or nothing without a norm.
 // About one element in 60,000.  32 x 4096 rows of 16 / 2 heads and their read-back take 487 us, 481 where
 // each such code is left to fp32; 16 x 2048 rows of 8 / 8 heads 171 and 158.
 struct Bound {
   float of_y, of_m, of_rest;  // of elements times unit
-  __device__ __forceinline__ Bound(float unit, float amplitude, bool norm)
-      : of_y((norm ? 8.1f : 2.1f) * 0x1p-24f * unit), of_m((norm ? 3.7f : 1.7f) * 0x1p-24f * unit * amplitude), of_rest(norm ? of_y : 0.0f) {}
+  __device__ __forceinline__ Bound(float unit, const Turn& t)
+      : of_y((t.k_weight ? 8.1f : 2.1f) * 0x1p-24f * unit),
+        of_m((t.k_weight ? 2.0f + t.unit_off : t.unit_off) * 0x1p-24f * unit * fabsf(static_cast<float>(t.amplitude))),
+        of_rest(t.k_weight ? of_y : 0.0f) {}
 };
 struct NearBorder : Bound {
   float unit;
   uint32_t elements = 0, words[8];
-  __device__ __forceinline__ NearBorder(float unit, float amplitude, bool norm) : Bound(unit, amplitude, norm), unit(unit) {}
+  __device__ __forceinline__ NearBorder(float unit, const Turn& t) : Bound(unit, t), unit(unit) {}
   __device__ __forceinline__ void ends(int e, float y0, float off0, float y1, float off1) {
     const uint32_t code = e4m3x2(fmaf(y0, unit, off0), fmaf(y1, unit, off1)), other = e4m3x2(fmaf(y0, unit, -off0), fmaf(y1, unit, -off1));
     if ((code ^ other) & 0x7F7Fu) elements |= 1u << e;
@@ -441,7 +445,7 @@ struct AboveLimit : Bound {
   float limit;
   uint32_t elements = 0;
   bool above = false;
-  __device__ __forceinline__ AboveLimit(float limit, float amplitude, bool norm) : Bound(1.0f, amplitude, norm), limit(limit) {}
+  __device__ __forceinline__ AboveLimit(float limit, const Turn& t) : Bound(1.0f, t), limit(limit) {}
   __device__ __forceinline__ void look(int e, float y, float off) {
     const float d = fabsf(y) - limit;  // (exact where it is small)
     if (d > off) above = true;
@@ -570,7 +574,7 @@ struct RotaryAppendParams {
 
 // Whether one of the lane's new elements of a page's rows [begin, end) is above 448 * 2^e.  The page's
 // exponent hangs on it where the largest element, in fp32, is as near to that as it may be off
-// (three pages in a million; where elements that are exact are the largest, one in 200, which need no fp64).
+// (four pages in a million; where elements that are exact are the largest, one in 200, which need no fp64).
 template <int LAYOUT, int K>
 __device__ __noinline__ bool key_above(const Turn& t, const uint8_t* rows, long long stride, const int* positions, int position, int begin,
                                        int end, const float* weights, const float* table, int e) {
@@ -589,7 +593,7 @@ __device__ __noinline__ bool key_above(const Turn& t, const uint8_t* rows, long 
     float x[32];
     raw.get(x);
     if (t.k_weight) weigh<false>(x, inverse_norm(x, static_cast<float>(t.eps)), weights, l);
-    AboveLimit look(448.0f * power2(e), fabsf(static_cast<float>(t.amplitude)), t.k_weight != nullptr);
+    AboveLimit look(448.0f * power2(e), t);
     turn_row<LAYOUT, K, false, true>(x, table + 2 * (min(max(r, begin), end - 1) - begin) * t.pairs, t.pairs, l, look);
     if (!is_new) continue;
     (i ? open[1] : open[0]) = look.elements;
@@ -745,11 +749,11 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
   const int key_position = sg.pos - off + k * kPage;
   int e = least_exponent(top);
   if (!is_v) {
-    // The largest key is off by 2^-24 * (8.1 + 2 * 3.7) of it at most: of the pair that it is turned from, the magnitudes' sum
+    // The largest key is off by 2^-24 * (8.1 + 2 * 4.7) of it at most: of the pair that it is turned from, the magnitudes' sum
     // times the amplitude is at most twice the larger of the pair's results.
     const float most = __uint_as_float(top);
-    const int least = least_exponent(__float_as_uint(most * (1.0f - 0x1p-20f)));
-    if (least != least_exponent(__float_as_uint(most * (1.0f + 0x1p-20f)))) {
+    const int least = least_exponent(__float_as_uint(most * (1.0f - 0x1.4p-20f)));
+    if (least != least_exponent(__float_as_uint(most * (1.0f + 0x1.4p-20f)))) {
       e = least + __syncthreads_or(key_above<LAYOUT, K>(p.turn, key_rows, p.k.row, key_positions, key_position, begin, end, weights, table, least));
       clear();  // (the rows again, rather than in registers over the call)
       load_rows();
@@ -775,7 +779,7 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_ro
         words[j] = e4m3x2(z[0] * unit, z[1] * unit) | e4m3x2(z[2] * unit, z[3] * unit) << 16;
       }
     } else {
-      NearBorder near(unit, fabsf(static_cast<float>(p.turn.amplitude)), weight != nullptr);
+      NearBorder near(unit, p.turn);
       turned(i, x, near);
       again[i] = r < begin || r >= end ? 0 : odd ? 0x55555555u : near.elements;
 #pragma unroll
@@ -850,7 +854,8 @@ Kind kind_of(const iq_rotary* r, bool f32) {
   return {!f32 && pairs == 32 ? kSwap : kShift, pairs / piece};
 }
 Turn turn_of(const iq_rotary* r) {
-  return {reinterpret_cast<const unsigned long long*>(r->turns), r->q_weight, r->k_weight, r->amplitude, r->eps, r->rotary_dim / 2};
+  const bool rounded = static_cast<double>(static_cast<float>(r->amplitude)) != r->amplitude;
+  return {reinterpret_cast<const unsigned long long*>(r->turns), r->q_weight, r->k_weight, r->amplitude, r->eps, rounded ? 2.7f : 1.7f, r->rotary_dim / 2};
 }
 
 int check_rotary(const iq_rotary* r) {

@@ -539,3 +539,32 @@ def test_a_large_eps_beside_squares_past_32_bits(dtype):
         rot = IQRotary(0, q_norm=torch.ones(256), k_norm=torch.ones(256), eps=eps)
         y = f64(x) / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True) + eps)
         check(rot.apply(x.cuda()), y, 10 * U * np.abs(y))
+
+
+@pytest.mark.parametrize("rd,interleaved,norm", [(64, False, True), (128, True, False), (96, False, True)])
+def test_codes_where_the_amplitude_is_rounded_to_float32(rd, interleaved, norm):
+    """An amplitude as far from float32's numbers as it may be: the codes are the nearest to the keys of that one."""
+    from rotated_bit_quantized_gb300 import IQPagedCache, IQRotary
+    E, H, n = 8, 2, 1024
+    g = torch.Generator().manual_seed(5)
+    w = (0.3 * torch.randn(256, generator=g) * 1024).round() / 1024 if norm else None  # 1 + w is exact
+    rot = IQRotary(rd, interleaved=interleaved, k_norm=w, norm_offset=1.0, amplitude=1 + 2.0**-23 * 3 + 2.0**-24 * 0.99)
+    c = IQPagedCache(E, H, E * n // 64)
+    k = rows(6, E, H, n, True).cuda()
+    at = torch.randint(0, 1 << 17, (E, n), generator=g, dtype=torch.int32).cuda()
+    c.append_rotary(None, k, k, rot, positions=at)
+    y = k.double()
+    if norm:
+        y = y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt() * (1.0 + w.double().cuda())
+    angle = (at.double()[..., None] * torch.from_numpy(rot.frequencies).cuda())[:, None]
+    a, b = (y[..., :rd:2], y[..., 1:rd:2]) if interleaved else (y[..., : rd // 2], y[..., rd // 2: rd])
+    x, z = rot.amplitude * (a * angle.cos() - b * angle.sin()), rot.amplitude * (a * angle.sin() + b * angle.cos())
+    y = torch.cat([torch.stack([x, z], -1).flatten(-2) if interleaved else torch.cat([x, z], -1), y[..., rd:]], -1)
+    scale = c.k_scales[c.table[:, : n // 64].long()].double().transpose(1, 2).repeat_interleave(64, 2)[..., None]
+    z = y / scale
+    step = torch.exp2(torch.floor(torch.log2(z.abs().clamp_min(2.0**-6))) - 3)
+    held = c.read(0, n)[0].double() / scale
+    assert (held == (torch.round(z / step) * step)).all()
+    top = z.abs().unflatten(2, (-1, 64)).amax((-1, -2))
+    assert (top <= 448).all() and (top > 224).all()  # the least exponent
+    assert c.device_status() == 0
