@@ -617,6 +617,20 @@ int iq_paged_attend_shared(const iq_paged* cache, const void* q, int q_heads, in
  */
 int iq_paged_debug_share(void);
 
+/*
+ * iq_paged_debug_plan — a hook for tests (host only): what iq_paged_attend_shared of these arguments multiplies
+ * once (forced: as after iq_paged_debug_share), in plan [IQ_PLAN_WORDS]: twelve words (nodes; those before
+ * the leaves of few rows; entries; rows of a kv head; ranges of either kind; a unit's extra slots, of
+ * either kind; all slots, of either kind; rows of a narrow range; rows of partial results), thirteen for each node
+ * (slot, parent, the slot's last page, first row, rows, first partial result, slots before it, tiles, first tile,
+ * tiles of the sinks, tiles skipped behind these, the least and the largest position of a row), four for each entry
+ * that has queries and keys (place in the call, lowest node, first row, first position).  No nodes: it
+ * runs as iq_paged_attend.  Errors: those of iq_paged_attend_shared.
+ */
+#define IQ_PLAN_WORDS (12 + 13 * 320 + 4 * IQ_MAX_BATCH)
+int iq_paged_debug_plan(const iq_paged* cache, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts,
+                        int n_slots, int causal, int window, int sinks, int forced, int32_t* plan);
+
 /* iq_paged_append_attend_shared — iq_paged_append_attend with iq_paged_attend_shared in the second place. */
 int iq_paged_append_attend_shared(iq_paged* cache, const void* keys, const void* values, int n, const void* q,
                                   int q_heads, int n_queries, const int32_t* slots, const int32_t* counts,

@@ -25,6 +25,7 @@ IQ_MASK_NONE, IQ_MASK_CAUSAL, IQ_MASK_ADD_F32, IQ_MASK_BOOL_U8 = 0, 1, 2, 3
 IQ_INJECT_COMBINE_WAIT, IQ_INJECT_STAGE_NEVER_FILLED = 1, 2
 IQ_DTYPE_BF16, IQ_DTYPE_F32 = 0, 1
 IQ_PAGE = 64
+IQ_PLAN_WORDS = 12 + 13 * 320 + 4 * IQ_MAX_BATCH
 IQ_WORKSPACE_HEAD_BYTES = 8448
 IQ_STATUS_RANGE, IQ_STATUS_BAD_PAGE = 0x40000, 0x80000
 IQ_SCALING_NONE, IQ_SCALING_LINEAR, IQ_SCALING_NTK, IQ_SCALING_YARN, IQ_SCALING_BANDED = range(5)
@@ -38,7 +39,8 @@ EXPORTS = ("iq_status_string", "iq_last_error", "iq_build_rotation", "iq_cache_b
            "iq_paged_fork", "iq_paged_compact", "iq_paged_attend_workspace", "iq_paged_attend",
            "iq_paged_append_attend", "iq_paged_debug_fail", "iq_paged_debug_stall", "iq_rotary_frequencies",
            "iq_rotary_turns", "iq_rotary_apply", "iq_paged_append_rotary", "iq_paged_attend_shared_workspace",
-           "iq_paged_attend_shared", "iq_paged_append_attend_shared", "iq_paged_debug_share")
+           "iq_paged_attend_shared", "iq_paged_append_attend_shared", "iq_paged_debug_share",
+           "iq_paged_debug_plan")
 
 
 class IQCacheDesc(ctypes.Structure):
@@ -137,6 +139,7 @@ def lib() -> ctypes.CDLL:
         L.iq_paged_debug_fail.argtypes = [I]
         L.iq_paged_debug_stall.argtypes = []
         L.iq_paged_debug_share.argtypes = []
+        L.iq_paged_debug_plan.argtypes = [PAGED, I, I, P, P, I, I, I, I, I, P]
         for name in EXPORTS:
             if name not in ("iq_status_string", "iq_last_error", "iq_cache_nbytes"):
                 getattr(L, name).restype = I

@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include <cstring>
 
 #include "iq_paged_rows.cuh"
@@ -391,11 +392,10 @@ int check_shared(const iq_paged* c, const void* q, int q_heads, int n_queries, c
   return IQ_OK;
 }
 
-// The attention by the tree of shared pages, where there is one; *done says whether.
-int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots,
-                float scale, int causal, int window, int sinks, void* out, int out_f32, void* workspace, iq_stream_t stream, bool forced,
-                bool* done) {
-  *done = false;
+// The tree of shared pages of a call, where there is one and it is the faster way (or `forced`): everything of
+// the launches' parameters but addresses, and how many rows of partial results there are.
+bool plan_tree(const iq_paged* c, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots, int causal, int window,
+               int sinks, bool forced, TreeParams* tree, TreeCutParams* cutting, long long* results) {
   const int heads = c->kv_heads;
   Planner t;
   t.rep = q_heads / heads;
@@ -411,14 +411,14 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
     const int first = causal ? len - count : len - 1;
     t.e[t.n++] = {c->table_host + static_cast<long long>(s) * c->max_pages, pages_for(len), len, count, first, len - 1, i, s, -1};
   }
-  if (t.n < 2) return IQ_OK;
+  if (t.n < 2) return false;
   t.split(0, t.n, 0, 0, -1, 0);
   const int leaf_rows = t.rep * n_queries, sms = num_sms();
-  if (t.inner == 0 || !t.share_out(heads, leaf_rows, sms)) return IQ_OK;
+  if (t.inner == 0 || !t.share_out(heads, leaf_rows, sms)) return false;
 
-  TreeParams p;
+  TreeParams& p = *tree;
   std::memset(&p, 0, sizeof(p));
-  TreeCutParams cut;
+  TreeCutParams& cut = *cutting;
   std::memset(&cut, 0, sizeof(cut));
   // leaves of at most 32 rows, as the split kernel's calls, behind the other nodes
   short number[kNodes];
@@ -466,7 +466,7 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
     const int kind = k >= p.leaves;
     p.cum[k] = static_cast<int>(total[kind]);
     total[kind] += static_cast<long long>(heads) * ((p.n[k] + kUnitRows - 1) / kUnitRows) * (p.tiles[k] + (kind ? p.narrow_cost : p.wide_cost));
-    if (total[kind] >= (1LL << 31)) return IQ_OK;
+    if (total[kind] >= (1LL << 31)) return false;
   }
   p.wide_total = static_cast<int>(total[0]);
   p.narrow_total = static_cast<int>(total[1]);
@@ -474,7 +474,31 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   parts += static_cast<long long>(p.wide) * kUnitRows;
   p.narrow_cont = static_cast<int>(parts);
   parts += static_cast<long long>(p.narrow) * p.narrow_rows;
+  p.heads = heads;
+  p.rep = t.rep;
+  p.nq = n_queries;
+  while ((2 << p.rep_shift) <= t.rep) ++p.rep_shift;
+  if (t.rep & (t.rep - 1)) p.rep_mul = static_cast<unsigned>(((1ull << (32 + p.rep_shift)) + t.rep - 1) / t.rep);
+  p.causal = causal;
+  p.window = window;
+  p.sinks = sinks;
+  cut.rows = p.rows;
+  cut.entries = t.n;
+  cut.causal = causal;
+  *results = parts;
+  return true;
+}
 
+// The attention by the tree of shared pages, where there is one; *done says whether.
+int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots,
+                float scale, int causal, int window, int sinks, void* out, int out_f32, void* workspace, iq_stream_t stream, bool forced,
+                bool* done) {
+  *done = false;
+  TreeParams p;
+  TreeCutParams cut;
+  long long parts = 0;
+  if (!plan_tree(c, q_heads, n_queries, slots, counts, n_slots, causal, window, sinks, forced, &p, &cut, &parts)) return IQ_OK;
+  const int heads = c->kv_heads;
   const long long pool_rows = static_cast<long long>(c->pages) * heads * kPage, cut_rows = static_cast<long long>(heads) * p.rows;
   p.part_o = static_cast<float*>(workspace);
   p.cut = reinterpret_cast<uint8_t*>(p.part_o + parts * kHeadDim);
@@ -493,25 +517,14 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
   p.q = static_cast<const uint16_t*>(q);
   p.out = out;
   p.out_f32 = out_f32;
-  p.causal = causal;
   p.scale = scale;
-  p.heads = heads;
-  p.rep = t.rep;
-  p.nq = n_queries;
-  while ((2 << p.rep_shift) <= t.rep) ++p.rep_shift;
-  if (t.rep & (t.rep - 1)) p.rep_mul = static_cast<unsigned>(((1ull << (32 + p.rep_shift)) + t.rep - 1) / t.rep);
   p.pages = c->pages;
   p.max_pages = c->max_pages;
-  p.window = window;
-  p.sinks = sinks;
   p.stall = stall_next ? 1 : 0;
   stall_next = false;
   cut.q = static_cast<const uint16_t*>(q);
   cut.cut = p.cut;
   cut.factors = p.factors;
-  cut.rows = p.rows;
-  cut.entries = t.n;
-  cut.causal = causal;
   cut.scale = scale;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int st = store_zeros(c, q_heads, n_queries, slots, counts, n_slots, out, out_f32, stream);
@@ -528,11 +541,11 @@ int attend_tree(const iq_paged* c, const void* q, int q_heads, int n_queries, co
     j.out = out;
     j.out_f32 = out_f32;
     j.rows = p.rows;
-    j.stride = t.rep * n_queries;
+    j.stride = p.rep * n_queries;
     // warps to a row, so that each has some six partial results, but all CTAs at once
     const long long of_row = parts / cut_rows;
     j.shift = of_row <= 6 ? 0 : of_row <= 12 ? 1 : of_row <= 24 ? 2 : 3;
-    while (j.shift > 0 && (cut_rows << j.shift) / 8 > 4ll * sms) --j.shift;
+    while (j.shift > 0 && (cut_rows << j.shift) / 8 > 4ll * num_sms()) --j.shift;
     const int each = 8 >> j.shift;
     void* args[] = {&j};
     err = launch_after(reinterpret_cast<const void*>(&paged_tree_join_kernel), dim3((p.rows + each - 1) / each, heads), 256, 0, cs, args);
@@ -555,6 +568,36 @@ extern "C" {
 int iq_paged_debug_share(void) {
   clear_error();
   share_next = true;
+  return IQ_OK;
+}
+
+int iq_paged_debug_plan(const iq_paged* c, int q_heads, int n_queries, const int32_t* slots, const int32_t* counts, int n_slots, int causal,
+                        int window, int sinks, int forced, int32_t* plan) {
+  size_t need = 0;
+  int st = iq_paged_attend_shared_workspace(c, q_heads, n_queries, n_slots, &need);
+  if (st != IQ_OK) return st;
+  if (!plan) return fail(IQ_ERR_INVALID_ARG, "null plan");
+  st = check_attend(c, c->k_codes, q_heads, n_queries, slots, counts, n_slots, 0, 1.0f, causal, window, sinks, c->k_codes, 0, c->k_codes,
+                    SIZE_MAX);
+  if (st != IQ_OK) return st;
+  std::fill(plan, plan + IQ_PLAN_WORDS, 0);
+  TreeParams p;
+  TreeCutParams cut;
+  long long parts = 0;
+  if (!tree_rows(c, q_heads, n_queries, n_slots) ||
+      !plan_tree(c, q_heads, n_queries, slots, counts, n_slots, causal, window, sinks, forced != 0, &p, &cut, &parts))
+    return IQ_OK;
+  static_assert(IQ_PLAN_WORDS == 12 + 13 * kNodes + 4 * IQ_MAX_BATCH, "the largest plan fits");
+  int32_t* to = plan;
+  for (int x : {p.nodes, p.leaves, cut.entries, p.rows, p.wide, p.narrow, p.wide_cost, p.narrow_cost, p.wide_total, p.narrow_total,
+                p.narrow_rows, static_cast<int>(parts)})
+    *to++ = x;
+  for (int k = 0; k < p.nodes; ++k)
+    for (int x : {static_cast<int>(p.slot[k]), static_cast<int>(p.parent[k]), p.end_page[k], p.row0[k], p.n[k], p.part0[k], p.cum[k], p.tiles[k],
+                  p.base[k], p.sink_tiles[k], p.skip[k], p.p_lo[k], p.p_hi[k]})
+      *to++ = x;
+  for (int i = 0; i < cut.entries; ++i)
+    for (int x : {static_cast<int>(cut.entry[i]), static_cast<int>(cut.lowest[i]), cut.row0[i], cut.pos0[i]}) *to++ = x;
   return IQ_OK;
 }
 
