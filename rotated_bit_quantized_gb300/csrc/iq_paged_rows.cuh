@@ -122,7 +122,11 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
   if (threadIdx.x < kScaleBytes / 4) reinterpret_cast<uint32_t*>(smem + kScales + 2 * kScaleBytes)[threadIdx.x] = 0x7F7F7F7Fu;
   proxy_fence();
   // In a tree the kernel in front is the one that cuts the queries, which takes no tensor
-  // memory and lets this one begin when all before it is done: only what it writes is waited for.
+  // memory and lets this one begin when all before it is done: only what it writes is waited for,
+  // by the threads that read it, and by every CTA before it stores a result.  Pages, scales and the table
+  // are read in front of that wait.  This rests on the cutting kernel: each of its threads has waited for
+  // the kernels that wrote them, whose writes are then in L2, before it lets this kernel begin, and
+  // all of these reads go to L2 (bulk copies, ld.cg), none to what an L1 may have kept.
   if constexpr (!P::kTree) wait_only();
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512));

@@ -128,7 +128,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
     mbar_fence_init();
   }
   // In a tree what the kernel in front writes is not read here, and that one began when
-  // all before it was done (see the rows' kernel).
+  // all before it was done (see the rows' kernel); it is waited for before the first results.
   if constexpr (!P::kTree) wait_only();
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(C::kTmem));
@@ -412,6 +412,7 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[b]);
       }
+      if (P::kTree && at_first) wait_only();
       at_first = false;
       it0 += n;
       // ---- the segment's end: sums over the keys, then the results
