@@ -600,9 +600,11 @@ int iq_paged_append_attend(iq_paged* cache, const void* keys, const void* values
  * prompt): pages that several of the call's slots hold are read and multiplied once for all
  * of them.  The same arguments and errors, its own size of workspace; results within the same
  * bounds (sums in other orders, and small elements of a query beside a large one held to 2^-19
- * of that one, not 2^-23, where rows of several slots are multiplied together).  What is shared is taken from table_host, up to four levels of
- * sharing; a call with nothing to gain (more than 128 query rows per kv head and slot, or little
- * in common) runs as iq_paged_attend.  A captured call replays with the sharing that it was captured with: the
+ * of that one, not 2^-23, where rows of several slots are multiplied together).  What is shared is taken from table_host, up to
+ * three levels of sharing and 64 shared runs of pages (where there are more, those of the larger page ids are
+ * read for each slot).  A call with nothing to gain runs as iq_paged_attend: more than 128 query rows per kv head
+ * and slot, or little in common, which is told by an estimate of both ways' times (of 20000 random
+ * calls 0.4% took 8% longer than apart, or more, the worst 1.4 times as long).  A captured call replays with the sharing that it was captured with: the
  * slots that shared pages then still have to.
  */
 int iq_paged_attend_shared_workspace(const iq_paged* cache, int q_heads, int n_queries, int n_slots, size_t* bytes);
@@ -697,7 +699,8 @@ int iq_rotary_turns(const double* frequencies, int pairs, uint64_t* turns, iq_st
  * Row j of entry i is at position start[i] + j (start: host int32 [n_start], one for each
  *   entry or one for all; n_start 0: zeros), or at positions[i][j] (device int32
  *   [entries][n]); not both.
- * An infinity makes its pair's results (with a norm, its row's) infinite or NaN.
+ * An infinity makes its pair's results infinite or NaN; with a norm, whose factor is then 0, its pair's
+ * are NaN and the row's others 0.  A NaN makes its pair's NaN, with a norm the row's.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_heads, const iq_rows* k, int k_heads,
@@ -711,8 +714,10 @@ int iq_rotary_apply(const iq_rotary* rotary, int dtype, const iq_rows* q, int q_
  * q, k, v: bf16 rows [n_slots][q_heads or kv_heads][n]; q_heads may be 0, and 2^14 at most.
  * q_out: device bf16 [n_slots][q_heads][n][256], apart from the inputs; rows behind counts[i]
  *   are not read, and their queries come back as zeros.
- * Codes are those nearest to the exact turned keys (float32 where it leaves no doubt, else
- * float64): iq_rotary_apply and then iq_paged_append round twice, to bfloat16 in between.
+ * Codes are those nearest to the exact turned keys, and a page's exponent the least that takes them, as the
+ * plan's weights, turns and amplitude give them (float32 where it leaves no doubt, else float64; a key within
+ * 2^-40 or so of the border between two codes may go either way): iq_rotary_apply and then
+ * iq_paged_append round twice, to bfloat16 in between.
  * Everything else as iq_paged_append.
  */
 int iq_paged_append_rotary(iq_paged* cache, const iq_rotary* rotary, const iq_rows* q, int q_heads, const iq_rows* k,

@@ -37,7 +37,7 @@ namespace iq {
 namespace paged {
 namespace rows {
 
-constexpr int kMu = 4;  // products unrolled in a tree (fully: 9 KB more to fetch; rolled: 2.2 us a tile instead of 1.45)
+constexpr int kMu = 4;  // products unrolled in a tree (fully: 9 KB more to fetch; rolled: 2.2 us a tile instead of 1.45 then)
 constexpr int kRows = 128;
 constexpr int kSlots = 4;                         // tiles of keys or values in flight, from L2 mostly (3: no slower, 5: 1.5% slower)
 constexpr int kQ = kSlots * kSlotBytes;           // [high, low][2 halves of the dims][128 rows][128 bytes]
@@ -77,7 +77,7 @@ static_assert(kTreeSmem <= 232448, "shared memory of one CTA");
 // are partial.  smem: the whole of the CTA's, 1024-byte aligned.
 // In a tree a CTA has ten tiles or so, and its beginning counts: 32 paths of 32768 common
 // tokens, 16 / 2 heads, take 6 us until the first scores (instructions are fetched by all
-// CTAs at once, 0.14 us a kilobyte), 1.45 us a tile and 3 us for the results.
+// CTAs at once, 0.14 us a kilobyte), 1.5 us a tile and 3 us for the results.
 template <class P>
 __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem) {
   const uint32_t sbase = smem_u32(smem);

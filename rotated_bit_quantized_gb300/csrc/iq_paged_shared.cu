@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) paged_tree_cut_kernel(const __grid_consta
 // ------------------------------------------------------------------ products
 
 // CTAs of both kinds, so that neither waits for the other's end.  16 / 2 heads, with the other two
-// launches: 32 paths of 32768 common tokens 30 us (550 TFLOP/s; every path's pages apart 132),
+// launches: 32 paths of 32768 common tokens 31 us (540 TFLOP/s; every path's pages apart 132),
 // bound by a tile's row threads next to its products and by a launch of short CTAs, tensor
 // pipe 35%; 128 paths of 8192 common tokens and 16 tiles each of their own 66 us (apart
 // 167), 284 MB from HBM at 4.6 TB/s under a profiler, bound by its beginning, HBM and the

@@ -3,14 +3,14 @@
 //
 // Mathematics.  y = x * (mean(x^2) + eps)^-1/2 * weight (where a weight is given), then
 // the pairs (a, b) of the leading rotary dims become (a c - b s, a s + b c) * amplitude
-// with c, s the cosine and sine of position * frequency.  fp32 throughout, rounded once.
+// with c, s the cosine and sine of position * frequency.  fp32 throughout, rounded once;
+// the codes and page exponents that this leaves open come from fp64 (see Bound, exact_codes).
 //
 // Angles.  A far position times a frequency has a fraction of a turn that fp32 cannot
 // tell (at 2^20, 2^-4 of a radian is lost), so a frequency is held as its turns per
 // position modulo 1 in 64 bits of fixed point: the product with a position, modulo
 // 2^64, is the angle modulo a turn, off by at most position * 2^-64 and what the
-// frequency itself was off.  One integer product and no table in memory; fp64 only for
-// what fp32 leaves open of codes (see exact_codes).
+// frequency itself was off.  One integer product; no table in memory.
 //
 // Rows.  Eight lanes hold a row, 32 elements each in pieces of 16 bytes, 128 bytes apart:
 // what a row costs besides its elements (its address, the norm's sum over lanes and root)
@@ -361,7 +361,10 @@ struct Split {
 // Bound by HBM.  16 x 2048 rows of 16 / 2 heads, norms, 64 dims turning: 98 us, 604 MB at 6.2
 // TB/s (91% of a measured copy), DRAM traffic that of the rows, 106 instructions of a warp per
 // row, half of the issue slots.  2047 rows of 12 / 4 heads in float32, all dims, 10.6 us; a
-// single token of 32 entries 2.3 us, a launch's latency.
+// single token of 32 entries 2.3 us, a launch's latency.  Halves of dims that are no
+// multiple of 128 nor 64 (kShift: pairs in other lanes, two CTAs to an SM instead of three), the first's
+// sizes: 109 us at 16 or 32 dims, 112 at 96, 129 at 192, 142 at 240; in float32, where a lane's
+// pieces are 4 elements, 182 at 16 or 32, 186 at 96 and 196 at 192 (64: 189; the rows take 178).
 template <int LAYOUT, int K, bool F32>
 __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(const __grid_constant__ RotateParams p) {
   extern __shared__ __align__(16) float table[];
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(c
 // factor then 6, of y; the product's rounding and its correction's 2, of y; the weight's products 2 and
 // the cosines' 1.7, of m, or 2.7 where the amplitude is rounded to fp32 too.  Elements that do not
 // turn: 8 u, or nothing without a norm.
-// About one element in 60,000.  32 x 4096 rows of 16 / 2 heads and their read-back take 487 us, 481 where
+// About one element in 60,000.  32 x 4096 rows of 16 / 2 heads and their read-back take 488 us, 481 where
 // each such code is left to fp32; 16 x 2048 rows of 8 / 8 heads 171 and 158.
 struct Bound {
   float of_y, of_m, of_rest;  // of elements times unit
@@ -611,7 +614,10 @@ __device__ __noinline__ bool key_above(const Turn& t, const uint8_t* rows, long 
 // them in fp32.  Codes are those nearest to the exact keys (see NearBorder).
 // Bound by HBM: 32 x 4096 rows of 16 / 2 heads, 64 dims turning, take 421 us, 2.52 GB at 6.0 TB/s
 // (88% of a measured copy).  With all dims turning and few rows by a
-// page's 8192 cosines in front of its keys: 7 x 513 rows of 8 / 4 heads 28 us, read back with them.
+// page's 8192 cosines in front of its keys: 7 x 513 rows of 8 / 4 heads 29 us, read back with them.
+// Three CTAs to an SM leave 80 registers, of which two rows as they came take 32: instances that
+// turn keep 40 to 140 bytes in local memory (none at kNone; the 128 of kShift<1> 52).  kShift: the large append
+// and its read-back take 536 us at 32 dims, 584 at 96, 736 at 192 (64: 488).
 template <int LAYOUT, int K>
 __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) paged_append_rotary_kernel(const __grid_constant__ RotaryAppendParams p) {
   extern __shared__ __align__(16) float table[];  // of the page's new rows

@@ -250,7 +250,8 @@ class IQPagedCache:
 
         q [entries, Hq, n, D], keys, values [entries, Hkv, n, D]: bf16 CUDA tensors, views with any strides (see
         `IQRotary.apply`).  Rows behind counts[i] are not read; their queries come back as zeros.  Keys
-        are held as the codes nearest to what the formula gives without any rounding.
+        are held as the codes nearest to what the formula gives without any rounding, from the plan's
+        weights (norm_offset + weight in float32), frequencies and amplitude.
         """
         if rotary._index != self._index:
             raise ValueError("the rotary plan must be on the cache's device")
@@ -340,7 +341,8 @@ class IQPagedCache:
         the slot's first `sinks` tokens.  A query that sees nothing gets 0.
         Softmax weights are held to 2^-8 of each, sums in float32, whatever out_dtype is.
         shared: read pages that several of the slots hold (forked paths, a common prompt) once for all of
-        them; a call captured so replays with the sharing it was captured with.
+        them, where an estimate says that this is faster (of 20000 random calls 0.4% took 8% longer, or more, the worst 1.4 times as long); a
+        call captured so replays with the sharing it was captured with.
         """
         q = self._tensor(q, "q")
         E, Hq, L, D = q.shape

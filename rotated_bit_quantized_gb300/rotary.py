@@ -124,8 +124,8 @@ class IQRotary:
 
         bf16 or float32, views with any strides (a slice of a projection's output needs no copy where its
         rows lie at multiples of 16 bytes).  positions: of the entries' first rows, the others follow (one whole number, or
-        one for each entry), or an int32 CUDA tensor [entries, n] of every row's own.  An infinity makes the elements
-        that it turns into infinite or NaN, and with a norm the row.
+        one for each entry), or an int32 CUDA tensor [entries, n] of every row's own.  An infinity makes the
+        elements that it turns into infinite or NaN; with a norm NaN, and the row's others 0.
         """
         dtype = q.dtype
         code = _DTYPE_CODES.get(dtype)
