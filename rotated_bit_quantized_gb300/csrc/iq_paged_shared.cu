@@ -577,8 +577,8 @@ int iq_paged_debug_plan(const iq_paged* c, int q_heads, int n_queries, const int
   int st = iq_paged_attend_shared_workspace(c, q_heads, n_queries, n_slots, &need);
   if (st != IQ_OK) return st;
   if (!plan) return fail(IQ_ERR_INVALID_ARG, "null plan");
-  st = check_attend(c, c->k_codes, q_heads, n_queries, slots, counts, n_slots, 0, 1.0f, causal, window, sinks, c->k_codes, 0, c->k_codes,
-                    SIZE_MAX);
+  const void* any = reinterpret_cast<const void*>(uintptr_t{256});  // (never followed)
+  st = check_attend(c, any, q_heads, n_queries, slots, counts, n_slots, 0, 1.0f, causal, window, sinks, any, 0, any, SIZE_MAX);
   if (st != IQ_OK) return st;
   std::fill(plan, plan + IQ_PLAN_WORDS, 0);
   TreeParams p;

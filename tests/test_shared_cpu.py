@@ -208,3 +208,10 @@ def test_plan_refusals(L):  # noqa: F811
         assert call(**kw) == want, kw
     assert call() == 0 and call(n=0) == 0 and call(k=0) == 0 and w[0] == 0
     assert L.iq_paged_debug_plan(None, 4, 1, None, None, 4, 1, 0, 0, 1, w.ctypes.data) == INVALID
+
+
+def test_plans_of_a_pool_that_is_16_byte_aligned(L):  # noqa: F811
+    f = Fake(L, base=0x10000010)
+    for s in range(4):
+        f.hold(s, [0, 1, 2 + s], 150)
+    assert check_plan(f, 8, 1, None, None, 4, 1, 0, 0, 1)
