@@ -649,8 +649,8 @@ int iq_paged_append_attend_shared(iq_paged* cache, const void* keys, const void*
  * the leading rotary_dim elements becomes amplitude * (a cos - b sin, a sin + b cos) of
  * the angle t * frequency.  In float32, rounded once to the output's type.  Angles are
  * reduced in 64-bit fixed point: a position is any 32-bit integer, and however far it
- * is, the angle is off by no more than the frequency itself times it (2^-53 of the frequency's
- * radians, 2^-53 of its turns) and 2^-54 of a turn, before float32's roundings of its sine and cosine.
+ * is, the angle is off by no more than the frequency itself times it (2^-53 of its
+ * turns, and 2^-64 of a turn) and 2^-55 of a turn, before float32's roundings of its sine and cosine.
  */
 typedef struct {
   int32_t rotary_dim;     /* 0 (nothing turns) or a multiple of 16 up to 256 */
