@@ -345,3 +345,71 @@ def test_turns_that_end_apart(Hq):
     first = check(c, o, q)
     for _ in range(30):
         assert torch.equal(shared(c, q.cuda(), out_dtype=torch.float32), first)
+
+
+def forked(k, v, k2, v2, H=1):
+    """Paths of one prompt (k, v) with rows of their own (k2, v2)."""
+    paths, common, tail = k2.shape[0], k.shape[2], k2.shape[2]
+    c, o = pair(paths, H, (common + 63) // 64 + paths * (2 + tail // 64), common + tail)
+    put(c, o, k, v, [0])
+    for x in (c, o):
+        x.fork([0] * (paths - 1), list(range(1, paths)))
+    put(c, o, k2, v2)
+    return c, o
+
+
+@pytest.mark.parametrize("n", [1, 5, 12])  # of 4, 20 and 48 rows: leaves of both kinds
+@pytest.mark.parametrize("signs", [(1, -1), (-1, -2), (2, 1)])
+@pytest.mark.parametrize("heavy", [700, 1100])
+def test_scores_of_any_size(n, signs, heavy):
+    """Scores of 1e34 and their like, of either sign, in the common pages and in a path's own: the largest takes all the weight."""
+    u = torch.randn(256, generator=torch.Generator().manual_seed(4)).sign()
+    k = (signs[1] * 1e14 * u).expand(1, 1, 1300, 256).clone()
+    k[0, 0, heavy] = signs[0] * 1e14 * u
+    k, v, v2 = k.bfloat16(), rows(2, 1, 1, 1000), rows(3, 5, 1, 300)
+    c, o = forked(k[:, :, :1000], v, k[:, :, 1000:].expand(5, -1, -1, -1), v2)
+    out = shared(c, (1e18 * u).expand(5, 4, n, 256).bfloat16().cuda(), causal=False, out_dtype=torch.float32)
+    for s in range(5):
+        want = o.values(s)[1][0, heavy]  # held exactly: one key, one weight
+        assert np.allclose(f64(out[s]), want, rtol=2.0**-8, atol=0)
+    assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 5, 12])
+def test_masked_rows_cannot_leak(n):
+    k, v, k2, v2 = rows(1, 1, 1, 1000), rows(2, 1, 1, 1000), rows(3, 5, 1, 200), rows(4, 5, 1, 200)
+    for x, y in ((k, v), (k2, v2)):
+        x[:, :, 4: x.shape[2] - 70], y[:, :, 4: x.shape[2] - 70] = -3e20, 3e20
+    k2[:, :, :130], v2[:, :, :130] = rows(5, 5, 1, 130), rows(6, 5, 1, 130)
+    c, o = forked(k, v, k2, v2)
+    check(c, o, rows(9, 5, 4, n), window=120, sinks=4)
+
+
+@pytest.mark.parametrize("n", [1, 5, 12])
+def test_value_pages_of_very_different_sizes(n):
+    v, v2 = rows(2, 1, 1, 960), rows(4, 5, 1, 320)
+    sizes = [1, 1e-9, 1e6, 1e3, 1e-3, 0, 1e9, 1e-12, 1, 1e4]
+    for x in (v, v2):
+        for j in range(x.shape[2] // 64):
+            x[:, :, 64 * j: 64 * j + 64] *= sizes[(j + x.shape[0]) % 10]
+    c, o = forked(rows(1, 1, 1, 960) * 4, v, rows(3, 5, 1, 320) * 4, v2)
+    check(c, o, rows(9, 5, 8, n))
+
+
+@pytest.mark.parametrize("n", [1, 5, 12])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rising_scores_move_the_reference(n, sign):
+    u = torch.randn(256, generator=torch.Generator().manual_seed(4))
+    k = rows(1, 1, 1, 1500, dtype=torch.float32) * 0.2 + sign * u * torch.linspace(-6, 6, 1500)[None, None, :, None]
+    k = k.bfloat16()
+    c, o = forked(k[:, :, :1000], rows(2, 1, 1, 1000), k[:, :, 1000:].expand(6, -1, -1, -1), rows(3, 6, 1, 500))
+    q = (u + 0.1 * rows(9, 6, 4, n).float()).bfloat16()
+    check(c, o, q)
+    check(c, o, q, causal=False)
+
+
+@pytest.mark.parametrize("qs,ks,vs", [(1e-20, 1, 1), (1, 1e-9, 1e-9), (1e4, 1e-4, 1e10), (30, 1, 1), (1e15, 1e-15, 1e-20), (0, 1, 1), (1, 0, 1)])
+@pytest.mark.parametrize("n", [1, 12])
+def test_ranges(qs, ks, vs, n):
+    c, o = forked(rows(1, 1, 1, 700) * ks, rows(2, 1, 1, 700) * vs, rows(3, 5, 1, 200) * ks, rows(4, 5, 1, 200) * vs)
+    check(c, o, rows(9, 5, 4, n) * qs)
