@@ -599,8 +599,8 @@ int iq_paged_append_attend(iq_paged* cache, const void* keys, const void* values
  * iq_paged_attend_shared — iq_paged_attend where slots share pages (forked paths, a common
  * prompt): pages that several of the call's slots hold are read and multiplied once for all
  * of them.  The same arguments and errors, its own size of workspace; results within the same
- * bounds (sums in other orders, and small elements of a query beside a large one held to 2^-19
- * of that one, not 2^-23, where rows of several slots are multiplied together).  What is shared is taken from table_host, up to
+ * bounds (sums in other orders, and small elements of a query beside a large one held to 2^-17
+ * of that one, not 2^-21, where rows of several slots are multiplied together).  What is shared is taken from table_host, up to
  * three levels of sharing and 64 shared runs of pages (where there are more, those of the larger page ids are
  * read for each slot).  A call with nothing to gain runs as iq_paged_attend: more than 128 query rows per kv head
  * and slot, or little in common, which is told by an estimate of both ways' times (of 20000 random

@@ -27,8 +27,8 @@
 // were not shared.  32 paths of 32768 common tokens: 0.00037 off in norm, apart 0.00037, for
 // 2% of the time (5% where the held weights were converted before they were added).  A
 // query's second part has the first one's scale here and 16 times it there: elements 2^10
-// (there 2^14) below the row's largest are held to 2^-19 of that one (2^-23), far below the
-// weights' own roundings.
+// (there 2^14) below the row's largest are held to 2^-17 of that one (2^-21), half a step of
+// the least code, far below the weights' own roundings.
 #pragma once
 
 #include "iq_paged_mma.cuh"
