@@ -421,7 +421,9 @@ __global__ void __launch_bounds__(256, LAYOUT == kShift ? 2 : 3) rotate_kernel(c
 // the cosines' 1.7, of m, or 2.7 where the amplitude is rounded to fp32 too.  Elements that do not
 // turn: 8 u, or nothing without a norm.
 // About one element in 60,000.  32 x 4096 rows of 16 / 2 heads and their read-back take 488 us, 481 where
-// each such code is left to fp32; 16 x 2048 rows of 8 / 8 heads 171 and 158.
+// each such code is left to fp32; 16 x 2048 rows of 8 / 8 heads 171 and 158.  At worst, 32 x 4096 rows of two
+// heads without queries (149 us): 1.5 ms where every key is one number on a border, 3 ms with a NaN in
+// every row.
 struct Bound {
   float of_y, of_m, of_rest;  // of elements times unit
   __device__ __forceinline__ Bound(float unit, const Turn& t)
