@@ -391,13 +391,16 @@ __device__ __forceinline__ void run(const P& p, const Work& work, uint8_t* smem)
                 hb = f16x2(w2, w3);
               }
               const uint32_t a = e4m3x2_of_f16x2(ha), d = e4m3x2_of_f16x2(hb);
-              const uint32_t a16 = e4m3x2_to_f16x2(a), d16 = e4m3x2_to_f16x2(d);
-              const uint32_t a_lo = e4m3x2_of_f16x2(sub_f16x2(ha, a16)), d_lo = e4m3x2_of_f16x2(sub_f16x2(hb, d16));
               hi[i] = a | d << 16;
-              lo[i] = a_lo | d_lo << 16;
-              if constexpr (P::kTree) {  // as they are held: multiples of the last place of their fp16 form, so exact there
+              if constexpr (P::kTree) {
+                const uint32_t a16 = e4m3x2_to_f16x2(a), d16 = e4m3x2_to_f16x2(d);
+                const uint32_t a_lo = e4m3x2_of_f16x2(sub_f16x2(ha, a16)), d_lo = e4m3x2_of_f16x2(sub_f16x2(hb, d16));
+                lo[i] = a_lo | d_lo << 16;
+                // summed as they are held: multiples of the last place of their fp16 form, so exact there
                 add_to(s0, s1, add_f16x2(a16, e4m3x2_to_f16x2(a_lo)));
                 add_to(s0, s1, add_f16x2(d16, e4m3x2_to_f16x2(d_lo)));
+              } else {
+                lo[i] = e4m3x2_of_f16x2(sub_f16x2(ha, e4m3x2_to_f16x2(a))) | e4m3x2_of_f16x2(sub_f16x2(hb, e4m3x2_to_f16x2(d))) << 16;
               }
             }
             if (!rehearsal) {
